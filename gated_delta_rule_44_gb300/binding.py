@@ -140,13 +140,56 @@ class gdn_mixed_meta(ctypes.Structure):
                 ("prefill_has_initial_state_host", _vp)]
 
 
+class gdn_attn_rows(ctypes.Structure):
+    _fields_ = [("data", _vp), ("len", _i64), ("token_stride", _i64), ("head_stride", _i64)]
+
+
+class gdn_attn_cache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("k_len", _i64), ("k_page_stride", _i64), ("k_head_stride", _i64),
+                ("k_token_stride", _i64), ("v", _vp), ("v_len", _i64), ("v_page_stride", _i64),
+                ("v_head_stride", _i64), ("v_token_stride", _i64), ("num_pages", _i64),
+                ("page_size", _i64), ("block_table", _vp), ("max_pages", _i64),
+                ("table_stride", _i64), ("block_table_host", _vp)]
+
+
+class gdn_attn_prepare_args(ctypes.Structure):
+    _fields_ = [("T", _i64), ("N", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64),
+                ("rot_dim", _i64), ("act_dtype", _i32), ("norm_eps", _f32),
+                ("q", gdn_attn_rows), ("k", gdn_attn_rows), ("v", gdn_attn_rows),
+                ("q_norm_weight", _vp), ("q_norm_weight_len", _i64),
+                ("k_norm_weight", _vp), ("k_norm_weight_len", _i64),
+                ("cos_sin", _vp), ("cos_sin_len", _i64), ("positions", _vp),
+                ("cu_seqlens", _vp), ("kv_lens", _vp), ("cu_seqlens_host", _vp),
+                ("kv_lens_host", _vp), ("cache", ctypes.POINTER(gdn_attn_cache)),
+                ("q_out", _vp), ("q_out_len", _i64), ("k_out", _vp), ("k_out_len", _i64)]
+
+
+class gdn_attn_varlen_args(ctypes.Structure):
+    _fields_ = [("T", _i64), ("N", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64),
+                ("act_dtype", _i32), ("scale", _f32), ("q", gdn_attn_rows), ("k", gdn_attn_rows),
+                ("v", gdn_attn_rows), ("gate", gdn_attn_rows), ("cu_seqlens", _vp),
+                ("cu_seqlens_host", _vp), ("out", _vp), ("out_len", _i64), ("lse", _vp),
+                ("lse_len", _i64)]
+
+
+class gdn_attn_paged_args(ctypes.Structure):
+    _fields_ = [("T", _i64), ("N", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64),
+                ("max_q_len", _i64), ("act_dtype", _i32), ("scale", _f32), ("q", gdn_attn_rows),
+                ("gate", gdn_attn_rows), ("cu_seqlens", _vp), ("kv_lens", _vp),
+                ("cu_seqlens_host", _vp), ("kv_lens_host", _vp),
+                ("cache", ctypes.POINTER(gdn_attn_cache)), ("out", _vp), ("out_len", _i64),
+                ("lse", _vp), ("lse_len", _i64), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 EXPORTED = ("gdn_prepare", "gdn_decode", "gdn_prefill_varlen", "gdn_kda_varlen",
             "gdn_spec_prepare", "gdn_spec_decode", "gdn_packed_decode", "gdn_gated_rmsnorm",
             "gdn_prefill_workspace_bytes",
             "gdn_prefill_resolve_algo", "gdn_kda_resolve_algo", "gdn_kda_workspace_bytes",
             "gdn_status_string", "gdn_last_error_message",
             "gdn_read_device_status", "gdn_version", "gdn_launch_count", "gdn_validate_mixed",
-            "gdn_check_wait_timeout")
+            "gdn_check_wait_timeout", "gdn_attn_prepare", "gdn_attn_varlen", "gdn_attn_paged",
+            "gdn_attn_paged_workspace_bytes")
 
 
 class GdnError(RuntimeError):
@@ -191,6 +234,13 @@ def lib() -> ctypes.CDLL:
             L.gdn_kda_resolve_algo.argtypes = [_i64, _i64, _i64, _i64, _i32, _i32]
             L.gdn_kda_workspace_bytes.restype = ctypes.c_size_t
             L.gdn_kda_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i64, _i32, _i32]
+            for name, args in (("gdn_attn_prepare", gdn_attn_prepare_args),
+                               ("gdn_attn_varlen", gdn_attn_varlen_args),
+                               ("gdn_attn_paged", gdn_attn_paged_args)):
+                getattr(L, name).restype = ctypes.c_int
+                getattr(L, name).argtypes = [ctypes.POINTER(args), _vp]
+            L.gdn_attn_paged_workspace_bytes.restype = ctypes.c_size_t
+            L.gdn_attn_paged_workspace_bytes.argtypes = [_i64] * 6 + [_i32]
             L.gdn_status_string.restype = ctypes.c_char_p
             L.gdn_status_string.argtypes = [ctypes.c_int]
             L.gdn_last_error_message.restype = ctypes.c_char_p
@@ -462,6 +512,210 @@ def gdn_prefill_varlen(q, k, v, g, beta, state, cu_seqlens, out, *, scale=-1.0,
         workspace_bytes=0 if workspace is None else workspace.numel() * workspace.element_size(),
         out_norm=nrm_p)
     _check(lib().gdn_prefill_varlen(ctypes.byref(a), _stream(stream)))
+
+
+def _bad(msg: str):
+    return GdnError(GDN_ERR_INVALID_ARGUMENT, "GDN_ERR_INVALID_ARGUMENT", msg)
+
+
+def _attn_shape(name, t, shape, like, dtype=None):
+    """The C entries see sizes, not tensors: shape, type and device are checked here."""
+    want = like.dtype if dtype is None else dtype
+    if tuple(t.shape) != tuple(shape):
+        raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE",
+                       f"attention {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype != want:
+        raise GdnError(GDN_ERR_DTYPE, "GDN_ERR_DTYPE",
+                       f"attention {name} is {t.dtype}, not {want}")
+    if t.device != like.device:
+        raise _bad(f"attention {name} is on {t.device}, not {like.device}")
+
+
+def _attn_rows(name, t, shape, like):
+    """gdn_attn_rows of a [tokens, heads, D] view (any token and head stride)."""
+    if t is None:
+        return gdn_attn_rows()
+    _attn_shape(name, t, shape, like)
+    if t.stride(2) != 1:
+        raise _bad(f"attention {name}'s last dimension must be contiguous")
+    # A dimension of one entry has no step of its own: its stride is free.
+    ts = t.stride(0) if t.shape[0] > 1 else 0
+    hs = t.stride(1) if t.shape[1] > 1 else 0
+    if (t.shape[0] > 1 and ts == 0) or (t.shape[1] > 1 and hs == 0):
+        raise _bad(f"attention {name} is a broadcast view; pass real rows")
+    return gdn_attn_rows(data=_p(t), len=_n(t), token_stride=ts, head_stride=hs)
+
+
+def _attn_contig(name, t, shape, like, dtype=None):
+    if t is None:
+        return
+    _attn_shape(name, t, shape, like, dtype)
+    if not t.is_contiguous():
+        raise _bad(f"attention {name} must be contiguous")
+
+
+def _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, like, block_table_host):
+    """gdn_attn_cache of k_cache, v_cache [pages, Hkv, page_size, D] (any strides
+    but the last) and block_table [N, max_pages] int32; and the host mirror."""
+    P, _, page = k_cache.shape[:3] if k_cache.dim() == 4 else (0, 0, 0)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _attn_shape(name, t, (P, Hkv, page, D), like)
+        if t.stride(3) != 1:
+            raise _bad(f"attention {name}'s last dimension must be contiguous")
+        if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+            raise _bad(f"attention {name} is a broadcast view; pass a real cache")
+    if block_table.dim() != 2:
+        raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE", "attention block_table must be [N, max_pages]")
+    _attn_shape("block_table", block_table, (N, block_table.shape[1]), like, torch.int32)
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise _bad("attention block_table's last dimension must be contiguous")
+
+    def strides(t):
+        return [st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3])]
+
+    kp, kh, kt = strides(k_cache)
+    vp, vh, vt = strides(v_cache)
+    host, host_p = _host_i32(block_table_host)
+    ts = block_table.stride(0) if N > 1 else 0
+    if host is not None:
+        if tuple(host.shape) != tuple(block_table.shape):
+            raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE",
+                           "attention block_table_host must have block_table's shape")
+        if N > 1 and ts != block_table.shape[1]:  # the mirror shares the row stride
+            wide = torch.zeros((N, ts), dtype=torch.int32)
+            wide[:, :host.shape[1]] = host
+            host, host_p = wide, wide.data_ptr()
+    c = gdn_attn_cache(k=_p(k_cache), k_len=_n(k_cache), k_page_stride=kp, k_head_stride=kh,
+                       k_token_stride=kt, v=_p(v_cache), v_len=_n(v_cache), v_page_stride=vp,
+                       v_head_stride=vh, v_token_stride=vt, num_pages=P, page_size=page,
+                       block_table=_p(block_table), max_pages=block_table.shape[1],
+                       table_stride=ts, block_table_host=host_p)
+    return c, host
+
+
+def _attn_meta(N, T, cu_seqlens, kv_lens, like, cu_seqlens_host, kv_lens_host):
+    """Checks the metadata tensors' shapes; returns the host mirrors to keep."""
+    for name, t, n in (("cu_seqlens", cu_seqlens, N + 1), ("kv_lens", kv_lens, N)):
+        _attn_contig(name, t, (n,), like, torch.int32)
+    out = []
+    for name, t, n in (("cu_seqlens_host", cu_seqlens_host, N + 1),
+                       ("kv_lens_host", kv_lens_host, N)):
+        h, p = _host_i32(t)
+        if h is not None and h.numel() != n:
+            raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE",
+                           f"attention {name} holds {h.numel()} entries, not {n}")
+        out.append((h, p))
+    return out
+
+
+def _attn_call(fn, a, q, stream) -> None:
+    if not q.is_cuda:
+        raise _bad(f"attention tensors must be on a CUDA device, got {q.device}")
+    _check(fn(ctypes.byref(a), _stream(stream)))
+
+
+def _attn_dims(q, kv_heads, cu_seqlens):
+    if q.dim() != 3:
+        raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE", "attention query must be [tokens, heads, D]")
+    T, Hq, D = q.shape
+    return T, (T if cu_seqlens is None else cu_seqlens.numel() - 1), Hq, kv_heads, D
+
+
+def gdn_attn_prepare(q, k, v, cu_seqlens, q_out, *, kv_lens=None, block_table=None, k_cache=None,
+                     v_cache=None, k_out=None, q_norm_weight=None, k_norm_weight=None,
+                     norm_eps=1e-6, cos_sin=None, positions=None, cu_seqlens_host=None,
+                     kv_lens_host=None, block_table_host=None, stream=None) -> None:
+    """include/gdn.h gdn_attn_prepare.  q [T, Hq, D], k, v [T, Hkv, D] views of
+    the projection rows; q_out [T, Hq, D] and k_out [T, Hkv, D] are written, and
+    the new rows of k_cache, v_cache [pages, Hkv, page_size, D] in place.
+    cos_sin [positions, rot_dim] f32; cu_seqlens None: one token per sequence."""
+    T, N, Hq, Hkv, D = _attn_dims(q, k.shape[1], cu_seqlens)
+    (cuh, cuh_p), (kvh, kvh_p) = _attn_meta(N, T, cu_seqlens, kv_lens, q, cu_seqlens_host,
+                                            kv_lens_host)
+    _attn_contig("q_out", q_out, (T, Hq, D), q)
+    _attn_contig("k_out", k_out, (T, Hkv, D), q)
+    _attn_contig("q_norm_weight", q_norm_weight, (D,), q)
+    _attn_contig("k_norm_weight", k_norm_weight, (D,), q)
+    _attn_contig("positions", positions, (T,), q, torch.int32)
+    rot = 0
+    if cos_sin is not None:
+        rot = cos_sin.shape[-1]
+        _attn_contig("cos_sin", cos_sin, (cos_sin.shape[0], rot), q, torch.float32)
+    cache = host = None
+    if k_cache is not None or v_cache is not None or block_table is not None:
+        if k_cache is None or v_cache is None or block_table is None:
+            raise _bad("attention cache needs k_cache, v_cache and block_table")
+        cache, host = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, q, block_table_host)
+    a = gdn_attn_prepare_args(
+        T=T, N=N, Hq=Hq, Hkv=Hkv, D=D, rot_dim=rot, act_dtype=_dt(q), norm_eps=float(norm_eps),
+        q=_attn_rows("query", q, (T, Hq, D), q), k=_attn_rows("key", k, (T, Hkv, D), q),
+        v=_attn_rows("value", v, (T, Hkv, D), q), q_norm_weight=_p(q_norm_weight),
+        q_norm_weight_len=_n(q_norm_weight), k_norm_weight=_p(k_norm_weight),
+        k_norm_weight_len=_n(k_norm_weight), cos_sin=_p(cos_sin), cos_sin_len=_n(cos_sin),
+        positions=_p(positions), cu_seqlens=_p(cu_seqlens), kv_lens=_p(kv_lens),
+        cu_seqlens_host=cuh_p, kv_lens_host=kvh_p,
+        cache=None if cache is None else ctypes.pointer(cache), q_out=_p(q_out),
+        q_out_len=_n(q_out), k_out=_p(k_out), k_out_len=_n(k_out))
+    _attn_call(lib().gdn_attn_prepare, a, q, stream)
+
+
+def gdn_attn_varlen(q, k, v, cu_seqlens, out, *, scale=-1.0, gate=None, lse=None,
+                    cu_seqlens_host=None, stream=None) -> None:
+    """include/gdn.h gdn_attn_varlen.  q, gate [T, Hq, D], k, v [T, Hkv, D] (any
+    token and head strides); out [T, Hq, D] and lse [T, Hq] f32 are written."""
+    T, N, Hq, Hkv, D = _attn_dims(q, k.shape[1], cu_seqlens)
+    (cuh, cuh_p), _ = _attn_meta(N, T, cu_seqlens, None, q, cu_seqlens_host, None)
+    _attn_contig("out", out, (T, Hq, D), q)
+    _attn_contig("lse", lse, (T, Hq), q, torch.float32)
+    a = gdn_attn_varlen_args(
+        T=T, N=N, Hq=Hq, Hkv=Hkv, D=D, act_dtype=_dt(q), scale=float(scale),
+        q=_attn_rows("query", q, (T, Hq, D), q), k=_attn_rows("key", k, (T, Hkv, D), q),
+        v=_attn_rows("value", v, (T, Hkv, D), q), gate=_attn_rows("gate", gate, (T, Hq, D), q),
+        cu_seqlens=_p(cu_seqlens), cu_seqlens_host=cuh_p, out=_p(out), out_len=_n(out),
+        lse=_p(lse), lse_len=_n(lse))
+    _attn_call(lib().gdn_attn_varlen, a, q, stream)
+
+
+def gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len=0,
+                                   act_dtype=GDN_DTYPE_BF16) -> int:
+    return int(lib().gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len, act_dtype))
+
+
+def gdn_attn_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, *, max_q_len=0,
+                   scale=-1.0, gate=None, lse=None, workspace=None, cu_seqlens_host=None,
+                   kv_lens_host=None, block_table_host=None, stream=None) -> None:
+    """include/gdn.h gdn_attn_paged.  q, gate [T, Hq, D]; k_cache, v_cache
+    [pages, Hkv, page_size, D]; block_table [N, max_pages], kv_lens [N],
+    cu_seqlens [N + 1] (None: one token per sequence) int32; out [T, Hq, D] and
+    lse [T, Hq] f32 are written.  `workspace`: a uint8 device tensor of at least
+    gdn_attn_paged_workspace_bytes() bytes; when None and one is needed, it is
+    allocated here for the call."""
+    if k_cache.dim() != 4:
+        raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE",
+                       "attention k_cache must be [pages, Hkv, page_size, D]")
+    T, N, Hq, Hkv, D = _attn_dims(q, k_cache.shape[1], cu_seqlens)
+    if kv_lens is None:
+        raise _bad("kv_lens is NULL")
+    (cuh, cuh_p), (kvh, kvh_p) = _attn_meta(N, T, cu_seqlens, kv_lens, q, cu_seqlens_host,
+                                            kv_lens_host)
+    _attn_contig("out", out, (T, Hq, D), q)
+    _attn_contig("lse", lse, (T, Hq), q, torch.float32)
+    cache, host = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, q, block_table_host)
+    if workspace is None:
+        nbytes = gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len, _dt(q))
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            if stream is not None:  # freed for reuse only after the call's stream has run it
+                workspace.record_stream(stream)
+    a = gdn_attn_paged_args(
+        T=T, N=N, Hq=Hq, Hkv=Hkv, D=D, max_q_len=int(max_q_len), act_dtype=_dt(q),
+        scale=float(scale), q=_attn_rows("query", q, (T, Hq, D), q),
+        gate=_attn_rows("gate", gate, (T, Hq, D), q), cu_seqlens=_p(cu_seqlens),
+        kv_lens=_p(kv_lens), cu_seqlens_host=cuh_p, kv_lens_host=kvh_p,
+        cache=ctypes.pointer(cache), out=_p(out), out_len=_n(out), lse=_p(lse), lse_len=_n(lse),
+        workspace=_p(workspace),
+        workspace_bytes=0 if workspace is None else workspace.numel() * workspace.element_size())
+    _attn_call(lib().gdn_attn_paged, a, q, stream)
 
 
 def _host_u8(t: Optional[torch.Tensor]):

@@ -1031,3 +1031,356 @@ int gdn_prefill_varlen(const gdn_prefill_args* a, void* stream) {
 }
 
 }  // extern "C"
+
+// ---- full attention --------------------------------------------------------------
+
+namespace {
+
+int check_attn_dims(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D) {
+  if (T <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0)
+    return fail(GDN_ERR_SHAPE, "attention shape must be positive, got tokens=" + S(T) +
+                                   " batch=" + S(N) + " query_heads=" + S(Hq) + " kv_heads=" +
+                                   S(Hkv) + " head_dim=" + S(D));
+  if (Hq % Hkv != 0)
+    return fail(GDN_ERR_SHAPE, "attention query_heads " + S(Hq) +
+                                   " must be divisible by kv_heads " + S(Hkv));
+  if ((D != 32 && D != 64 && D != 128 && D != 256) || Hq / Hkv > 64)
+    return fail(GDN_ERR_UNSUPPORTED,
+                "attention supports D in {32, 64, 128, 256} and at most 64 query heads per kv head");
+  // The kernels number tokens, tiles and (tile, kv head) pairs in 32 bits.
+  if (T > (int64_t)1 << 26 || N > (int64_t)1 << 24 || Hq > 65535 || (T + N) * Hq >= INT32_MAX)
+    return fail(GDN_ERR_UNSUPPORTED, "attention sizes exceed 32-bit tile indexing");
+  return GDN_OK;
+}
+
+// Strides and length of a [T, H, D] tensor; 0 strides are the contiguous ones.
+int check_attn_rows(const gdn_attn_rows& r, const char* label, int64_t T, int64_t H, int64_t D,
+                    int32_t dt, gdn::AttnRows* out) {
+  const int64_t ts = r.token_stride != 0 ? r.token_stride : H * D;
+  const int64_t hs = r.head_stride != 0 ? r.head_stride : D;
+  if (ts < 0 || hs < 0 || ts > INT64_MAX / 4 / T || hs > INT64_MAX / 4 / H)
+    return fail(GDN_ERR_SHAPE, std::string("attention ") + label + " strides out of range");
+  const LenRule rules[] = {{label, r.len, (T - 1) * ts + (H - 1) * hs + D}};
+  if (int rc = check_lengths("attention", rules)) return rc;
+  if (int rc = require_ptr(r.data, label)) return rc;
+  if (int rc = require_aligned(r.data, label)) return rc;
+  if ((ts * elem_size(dt)) % 16 != 0 || (hs * elem_size(dt)) % 16 != 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT,
+                std::string("attention ") + label + " strides must be multiples of 16 bytes");
+  *out = gdn::AttnRows{r.data, ts, hs};
+  return GDN_OK;
+}
+
+struct AttnCacheView {
+  gdn::AttnPages k, v;
+  int64_t table_stride;
+};
+
+int check_attn_pages(const char* label, void* p, int64_t len, int64_t ps, int64_t hs, int64_t ts,
+                     const gdn_attn_cache& c, int64_t Hkv, int64_t D, int32_t dt,
+                     gdn::AttnPages* out) {
+  if (ts == 0) ts = D;
+  if (hs == 0) hs = c.page_size * D;
+  if (ps == 0) ps = Hkv * c.page_size * D;
+  const int64_t big = INT64_MAX / 8;
+  if (ts < 0 || hs < 0 || ps < 0 || ts > big / c.page_size || hs > big / Hkv ||
+      ps > big / c.num_pages)
+    return fail(GDN_ERR_SHAPE, std::string("attention ") + label + " strides out of range");
+  const LenRule rules[] = {{label, len, (c.num_pages - 1) * ps + (Hkv - 1) * hs +
+                                            (c.page_size - 1) * ts + D}};
+  if (int rc = check_lengths("attention", rules)) return rc;
+  if (int rc = require_ptr(p, label)) return rc;
+  if (int rc = require_aligned(p, label)) return rc;
+  const int64_t es = elem_size(dt);
+  if ((ts * es) % 16 != 0 || (hs * es) % 16 != 0 || (ps * es) % 16 != 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT,
+                std::string("attention ") + label + " strides must be multiples of 16 bytes");
+  *out = gdn::AttnPages{p, ps, hs, ts};
+  return GDN_OK;
+}
+
+int check_attn_cache(const gdn_attn_cache* c, int64_t N, int64_t Hkv, int64_t D, int32_t dt,
+                     AttnCacheView* out) {
+  if (c->num_pages <= 0 || c->page_size <= 0 || c->max_pages <= 0)
+    return fail(GDN_ERR_SHAPE, "attention cache shape must be positive, got num_pages=" +
+                                   S(c->num_pages) + " page_size=" + S(c->page_size) +
+                                   " max_pages=" + S(c->max_pages));
+  if (c->num_pages > INT32_MAX || c->page_size > (1 << 20) || c->max_pages > INT32_MAX / c->page_size)
+    return fail(GDN_ERR_UNSUPPORTED, "attention cache positions exceed 32 bits");
+  out->table_stride = c->table_stride != 0 ? c->table_stride : c->max_pages;
+  if (out->table_stride < c->max_pages || out->table_stride > INT64_MAX / 8 / N)
+    return fail(GDN_ERR_SHAPE, "attention block_table stride shorter than the row or out of range");
+  if (int rc = require_ptr(c->block_table, "block_table")) return rc;
+  if (int rc = check_attn_pages("k_cache", c->k, c->k_len, c->k_page_stride, c->k_head_stride,
+                                c->k_token_stride, *c, Hkv, D, dt, &out->k))
+    return rc;
+  return check_attn_pages("v_cache", c->v, c->v_len, c->v_page_stride, c->v_head_stride,
+                          c->v_token_stride, *c, Hkv, D, dt, &out->v);
+}
+
+// Host copies of the metadata (mirrors, or device copies under
+// GDN_DEBUG_CHECKS); empty sequences are allowed.
+int check_attn_meta(const char* who, int64_t T, int64_t N, int64_t max_q, const int32_t* cu_dev,
+                    const int32_t* cu_host, const int32_t* kv_dev, const int32_t* kv_host,
+                    const gdn_attn_cache* c, int64_t table_stride, cudaStream_t st) {
+  std::vector<int32_t> cu_buf, kv_buf, tb_buf;
+  const int32_t *cu = nullptr, *kv = nullptr, *tb = nullptr;
+  if (int rc = host_view(cu_host, cu_dev, N + 1, st, cu_buf, cu)) return rc;
+  if (int rc = host_view(kv_host, kv_dev, N, st, kv_buf, kv)) return rc;
+  if (cu != nullptr) {
+    if (cu[0] != 0 || cu[N] != T)
+      return fail(GDN_ERR_INVALID_ARGUMENT,
+                  std::string(who) + " cu_seqlens must start at 0 and end at total_tokens " + S(T) +
+                      ", got first=" + S(cu[0]) + " last=" + S(cu[N]));
+    for (int64_t s = 0; s < N; ++s)
+      if (cu[s + 1] < cu[s] || cu[s + 1] > T || cu[s + 1] - cu[s] > max_q)
+        return fail(GDN_ERR_INVALID_ARGUMENT, std::string(who) + " sequence " + S(s) +
+                                                  " has range " + S(cu[s]) + ".." + S(cu[s + 1]) +
+                                                  ", not 0.." + S(max_q) + " tokens");
+  }
+  if (kv != nullptr) {
+    const int64_t cap = c != nullptr ? c->max_pages * c->page_size : INT32_MAX;
+    for (int64_t s = 0; s < N; ++s)
+      if (kv[s] < 0 || kv[s] > cap)
+        return fail(GDN_ERR_INVALID_ARGUMENT, std::string(who) + " sequence " + S(s) +
+                                                  " has kv_len " + S(kv[s]) + ", not 0.." + S(cap));
+  }
+  if (c == nullptr || kv == nullptr) return GDN_OK;
+  if (int rc = host_view(c->block_table_host, c->block_table, (N - 1) * table_stride + c->max_pages,
+                         st, tb_buf, tb))
+    return rc;
+  if (tb != nullptr)
+    for (int64_t s = 0; s < N; ++s)
+      for (int64_t i = 0; i < (kv[s] + c->page_size - 1) / c->page_size; ++i) {
+        const int32_t pg = tb[s * table_stride + i];
+        if (pg < 0 || pg >= c->num_pages)
+          return fail(GDN_ERR_INVALID_ARGUMENT, std::string(who) + " sequence " + S(s) + " names page " +
+                                                    S(pg) + " of " + S(c->num_pages));
+      }
+  return GDN_OK;
+}
+
+int check_attn_out(const void* out, int64_t out_len, const float* lse, int64_t lse_len, int64_t T,
+                   int64_t Hq, int64_t D) {
+  const LenRule rules[] = {{"output", out_len, T * Hq * D},
+                           {"lse", lse != nullptr ? lse_len : T * Hq, T * Hq}};
+  if (int rc = check_lengths("attention", rules)) return rc;
+  if (int rc = require_ptr(out, "out")) return rc;
+  return require_aligned(out, "out");
+}
+
+// The vectors and messages above allocate: nothing may be thrown through the C
+// entry.  The text fits std::string's own buffer.
+template <typename F>
+int no_throw(F f) {
+  try {
+    return f();
+  } catch (...) {
+    t_msg = "host memory";
+    return GDN_ERR_CUDA;
+  }
+}
+
+int one_token_each(const int32_t* cu, int64_t T, int64_t N) {
+  if (cu == nullptr && T != N)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "attention without cu_seqlens takes one token per sequence, got " +
+                                              S(T) + " tokens of " + S(N) + " sequences");
+  return GDN_OK;
+}
+
+int attn_prepare(const gdn_attn_prepare_args* a, void* stream) {
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+  if (int rc = check_act_dtype(a->act_dtype)) return rc;
+  if (int rc = check_attn_dims(a->T, a->N, a->Hq, a->Hkv, a->D)) return rc;
+  if (int rc = one_token_each(a->cu_seqlens, a->T, a->N)) return rc;
+  const int64_t R = a->rot_dim;
+  if (R < 0 || R > a->D || R % 16 != 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT,
+                "attention rot_dim must be 0 or a multiple of 16 up to D, got " + S(R));
+  if (!(a->norm_eps >= 0.0f)) return fail(GDN_ERR_INVALID_ARGUMENT, "attention norm_eps must be >= 0");
+  gdn::AttnPrepareLaunch p{};
+  if (int rc = check_attn_rows(a->q, "query", a->T, a->Hq, a->D, a->act_dtype, &p.q)) return rc;
+  if (int rc = check_attn_rows(a->k, "key", a->T, a->Hkv, a->D, a->act_dtype, &p.k)) return rc;
+  if (a->cache == nullptr && a->k_out == nullptr)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "attention prepare needs a cache or k_out");
+  AttnCacheView cv{};
+  if (a->cache != nullptr) {
+    if (int rc = check_attn_rows(a->v, "value", a->T, a->Hkv, a->D, a->act_dtype, &p.v)) return rc;
+    if (int rc = check_attn_cache(a->cache, a->N, a->Hkv, a->D, a->act_dtype, &cv)) return rc;
+  }
+  const LenRule rules[] = {
+      {"query output", a->q_out_len, a->T * a->Hq * a->D},
+      {"key output", a->k_out ? a->k_out_len : a->T * a->Hkv * a->D, a->T * a->Hkv * a->D},
+      {"q_norm_weight", a->q_norm_weight ? a->q_norm_weight_len : a->D, a->D},
+      {"k_norm_weight", a->k_norm_weight ? a->k_norm_weight_len : a->D, a->D},
+      {"cos_sin", R > 0 ? a->cos_sin_len : 1, R > 0 ? R : 1},
+  };
+  if (int rc = check_lengths("attention", rules)) return rc;
+  if (int rc = require_ptr(a->q_out, "q_out")) return rc;
+  if (R > 0)
+    if (int rc = require_ptr(a->cos_sin, "cos_sin")) return rc;
+  for (auto pr : {std::make_pair((const void*)a->q_out, "q_out"),
+                  std::make_pair((const void*)a->k_out, "k_out"),
+                  std::make_pair(a->q_norm_weight, "q_norm_weight"),
+                  std::make_pair(a->k_norm_weight, "k_norm_weight"),
+                  std::make_pair((const void*)a->cos_sin, "cos_sin")})
+    if (int rc = require_aligned(pr.first, pr.second)) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (int rc = check_attn_meta("attention_prepare", a->T, a->N, a->T, a->cu_seqlens,
+                               a->cu_seqlens_host, a->kv_lens, a->kv_lens_host, a->cache,
+                               cv.table_stride, st))
+    return rc;
+  p.T = (int)a->T;
+  p.N = (int)a->N;
+  p.Hq = (int)a->Hq;
+  p.Hkv = (int)a->Hkv;
+  p.D = (int)a->D;
+  p.rot = (int)R;
+  p.bf16 = a->act_dtype == GDN_DTYPE_BF16;
+  p.eps = a->norm_eps;
+  p.q_w = a->q_norm_weight;
+  p.k_w = a->k_norm_weight;
+  p.cos_sin = a->cos_sin;
+  p.max_pos = R > 0 ? a->cos_sin_len / R : 0;
+  p.positions = a->positions;
+  p.cu = a->cu_seqlens;
+  p.kv_lens = a->kv_lens;
+  if (a->cache != nullptr) {
+    p.table = a->cache->block_table;
+    p.table_stride = cv.table_stride;
+    p.max_pages = (int)a->cache->max_pages;
+    p.page_size = (int)a->cache->page_size;
+    p.num_pages = a->cache->num_pages;
+    p.kc = cv.k;
+    p.vc = cv.v;
+  }
+  p.q_out = a->q_out;
+  p.k_out = a->k_out;
+  p.status = gdn::status_word();
+  if (p.status == nullptr) return fail(GDN_ERR_CUDA, "device status word unavailable");
+  return launch_result(gdn::launch_attn_prepare(p, st), "gdn_attn_prepare");
+}
+
+int attn_varlen(const gdn_attn_varlen_args* a, void* stream) {
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+  if (int rc = check_act_dtype(a->act_dtype)) return rc;
+  if (int rc = check_attn_dims(a->T, a->N, a->Hq, a->Hkv, a->D)) return rc;
+  gdn::AttnLaunch p{};
+  if (int rc = check_attn_rows(a->q, "query", a->T, a->Hq, a->D, a->act_dtype, &p.q)) return rc;
+  if (int rc = check_attn_rows(a->k, "key", a->T, a->Hkv, a->D, a->act_dtype, &p.k)) return rc;
+  if (int rc = check_attn_rows(a->v, "value", a->T, a->Hkv, a->D, a->act_dtype, &p.v)) return rc;
+  if (a->gate.data != nullptr)
+    if (int rc = check_attn_rows(a->gate, "gate", a->T, a->Hq, a->D, a->act_dtype, &p.gate)) return rc;
+  if (int rc = check_attn_out(a->out, a->out_len, a->lse, a->lse_len, a->T, a->Hq, a->D)) return rc;
+  if (int rc = require_ptr(a->cu_seqlens, "cu_seqlens")) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (int rc = check_attn_meta("attention_varlen", a->T, a->N, a->T, a->cu_seqlens,
+                               a->cu_seqlens_host, nullptr, nullptr, nullptr, 0, st))
+    return rc;
+  p.T = (int)a->T;
+  p.N = (int)a->N;
+  p.Hq = (int)a->Hq;
+  p.Hkv = (int)a->Hkv;
+  p.D = (int)a->D;
+  p.max_q = (int)a->T;
+  p.bf16 = a->act_dtype == GDN_DTYPE_BF16;
+  p.scale = resolve_scale(a->scale, a->D);
+  p.cu = a->cu_seqlens;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.status = gdn::status_word();
+  if (p.status == nullptr) return fail(GDN_ERR_CUDA, "device status word unavailable");
+  return launch_result(gdn::launch_attn_simt(p, st), "gdn_attn_varlen");
+}
+
+size_t attn_paged_workspace(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
+                            int64_t max_q_len, int32_t act_dtype) {
+  if (check_act_dtype(act_dtype) || check_attn_dims(T, N, Hq, Hkv, D) || max_q_len < 0) return 0;
+  return gdn::attn_simt_workspace_bytes(T, N, Hq, Hkv, D);
+}
+
+int attn_paged(const gdn_attn_paged_args* a, void* stream) {
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+  if (int rc = check_act_dtype(a->act_dtype)) return rc;
+  if (int rc = check_attn_dims(a->T, a->N, a->Hq, a->Hkv, a->D)) return rc;
+  if (int rc = one_token_each(a->cu_seqlens, a->T, a->N)) return rc;
+  if (a->max_q_len < 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "attention max_q_len must be >= 0, got " + S(a->max_q_len));
+  const int64_t max_q = a->cu_seqlens == nullptr ? 1
+                        : a->max_q_len == 0 || a->max_q_len > a->T ? a->T : a->max_q_len;
+  gdn::AttnLaunch p{};
+  if (int rc = check_attn_rows(a->q, "query", a->T, a->Hq, a->D, a->act_dtype, &p.q)) return rc;
+  if (a->gate.data != nullptr)
+    if (int rc = check_attn_rows(a->gate, "gate", a->T, a->Hq, a->D, a->act_dtype, &p.gate)) return rc;
+  if (int rc = check_attn_out(a->out, a->out_len, a->lse, a->lse_len, a->T, a->Hq, a->D)) return rc;
+  if (int rc = require_ptr(a->kv_lens, "kv_lens")) return rc;
+  if (int rc = require_ptr(a->cache, "cache")) return rc;
+  AttnCacheView cv{};
+  if (int rc = check_attn_cache(a->cache, a->N, a->Hkv, a->D, a->act_dtype, &cv)) return rc;
+  const size_t need =
+      attn_paged_workspace(a->T, a->N, a->Hq, a->Hkv, a->D, a->max_q_len, a->act_dtype);
+  if (need > 0) {
+    if (a->workspace == nullptr || a->workspace_bytes < need)
+      return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_attn_paged workspace needs " + S((int64_t)need) +
+                                                " bytes, got " + S((int64_t)a->workspace_bytes));
+    if ((reinterpret_cast<uintptr_t>(a->workspace) & 255u) != 0)
+      return fail(GDN_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (int rc = check_attn_meta("attention_paged", a->T, a->N, max_q, a->cu_seqlens,
+                               a->cu_seqlens_host, a->kv_lens, a->kv_lens_host, a->cache,
+                               cv.table_stride, st))
+    return rc;
+  p.T = (int)a->T;
+  p.N = (int)a->N;
+  p.Hq = (int)a->Hq;
+  p.Hkv = (int)a->Hkv;
+  p.D = (int)a->D;
+  p.max_q = (int)max_q;
+  p.bf16 = a->act_dtype == GDN_DTYPE_BF16;
+  p.scale = resolve_scale(a->scale, a->D);
+  p.cu = a->cu_seqlens;
+  p.kv_lens = a->kv_lens;
+  p.table = a->cache->block_table;
+  p.table_stride = cv.table_stride;
+  p.max_pages = (int)a->cache->max_pages;
+  p.page_size = (int)a->cache->page_size;
+  p.num_pages = a->cache->num_pages;
+  p.kc = cv.k;
+  p.vc = cv.v;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.ws = a->workspace;
+  p.ws_bytes = a->workspace_bytes;
+  p.status = gdn::status_word();
+  if (p.status == nullptr) return fail(GDN_ERR_CUDA, "device status word unavailable");
+  return launch_result(gdn::launch_attn_simt(p, st), "gdn_attn_paged");
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_attn_prepare(const gdn_attn_prepare_args* a, void* stream) {
+  return no_throw([&] { return attn_prepare(a, stream); });
+}
+
+int gdn_attn_varlen(const gdn_attn_varlen_args* a, void* stream) {
+  return no_throw([&] { return attn_varlen(a, stream); });
+}
+
+int gdn_attn_paged(const gdn_attn_paged_args* a, void* stream) {
+  return no_throw([&] { return attn_paged(a, stream); });
+}
+
+size_t gdn_attn_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
+                                      int64_t max_q_len, int32_t act_dtype) {
+  size_t n = 0;
+  no_throw([&] {
+    n = attn_paged_workspace(T, N, Hq, Hkv, D, max_q_len, act_dtype);
+    return succeed();
+  });
+  return n;
+}
+
+}  // extern "C"

@@ -1,0 +1,228 @@
+// gdn_attn_common.cuh -- what the full-attention kernels share: the tile map
+// of packed new tokens, key addresses in packed rows and in paged caches, the
+// scalar tail of an output row, and the exact form of one row.
+//
+// New tokens.  Sequence s owns tokens cu[s] .. cu[s+1]-1 (q_len of them) and a
+// context of L = kv_lens[s] keys that ends with them: token i sits at position
+// L - q_len + i and sees the keys at positions 0 .. L - q_len + i.  A token at
+// a negative position (q_len > L) sees nothing: its output is 0, its lse -inf.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdn_internal.h"
+#include "gdn_math.cuh"
+
+namespace gdn {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ int cu_at(const int32_t* cu, int s) { return cu ? cu[s] : s; }
+
+// Tiles of TT tokens, each inside one sequence, numbered without a prefix sum:
+// sequence s owns the numbers from floor(cu[s] / TT) + s on.  Its ceil(q_len /
+// TT) tiles fit below the next sequence's first number because
+// floor((a + n) / TT) - floor(a / TT) >= floor(n / TT) >= ceil(n / TT) - 1.
+// The numbers in use are below floor(T / TT) + N; the rest are empty.
+__host__ __device__ inline int64_t tile_bound(int64_t T, int64_t N, int64_t TT) {
+  return T / TT + N;
+}
+
+struct SeqTile {
+  int s;       // sequence
+  int t0;      // first token of the tile
+  int nt;      // its tokens (0: an empty number)
+  int pos0;    // position of the first token (may be negative)
+  int kv_len;  // keys of the sequence
+  int bad;     // 1: cu_seqlens or kv_lens cannot be right here
+};
+
+__device__ inline SeqTile find_tile(const AttnLaunch& p, int id, int TT) {
+  int lo = 0, hi = p.N - 1;  // the last s whose first number is <= id
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu_at(p.cu, mid) / TT + mid <= id) lo = mid;
+    else hi = mid - 1;
+  }
+  SeqTile r;
+  r.s = lo;
+  r.nt = 0;
+  r.t0 = r.pos0 = r.kv_len = 0;
+  const int a = cu_at(p.cu, lo), b = cu_at(p.cu, lo + 1);
+  r.bad = (a < 0 || b < a || b > p.T || (lo == 0 && a != 0) || (lo == p.N - 1 && b != p.T));
+  if (a < 0 || b < a || b > p.T) return r;
+  int kv = b - a;
+  if (p.kv_lens != nullptr) {
+    kv = p.kv_lens[lo];
+    const int64_t cap = (int64_t)p.max_pages * p.page_size;
+    if (kv < 0 || kv > cap) {
+      r.bad = 1;
+      kv = kv < 0 ? 0 : (int)cap;
+    }
+  }
+  if (p.table != nullptr && p.max_q > 0 && b - a > p.max_q) r.bad = 1;
+  const int64_t off = (int64_t)(id - (a / TT + lo)) * TT;
+  if (off < 0 || off >= b - a) return r;
+  r.t0 = a + (int)off;
+  r.nt = min(TT, b - r.t0);
+  r.pos0 = kv - (b - r.t0);
+  r.kv_len = kv;
+  return r;
+}
+
+// Element offset of key row j of sequence s: of its page's row j % page_size,
+// or of packed token base + j.  -1 when the page number is outside the cache
+// (the row then reads as zeros and the status word is raised).
+__device__ __forceinline__ int64_t page_of(const AttnLaunch& p, int s, int page_idx) {
+  const int pg = p.table[(int64_t)s * p.table_stride + page_idx];
+  return (pg >= 0 && pg < p.num_pages) ? pg : -1;
+}
+__device__ __forceinline__ int64_t key_offset(const AttnLaunch& p, bool of_v, int s, int base,
+                                              int hkv, int j) {
+  if (p.table == nullptr) {
+    const AttnRows& r = of_v ? p.v : p.k;
+    return (int64_t)(base + j) * r.ts + (int64_t)hkv * r.hs;
+  }
+  const AttnPages& c = of_v ? p.vc : p.kc;
+  const int64_t pg = page_of(p, s, j / p.page_size);
+  if (pg < 0) return -1;
+  return pg * c.ps + (int64_t)hkv * c.hs + (int64_t)(j % p.page_size) * c.ts;
+}
+__device__ __forceinline__ const void* key_base(const AttnLaunch& p, bool of_v) {
+  return p.table == nullptr ? (of_v ? p.v.p : p.k.p) : (of_v ? p.vc.p : p.kc.p);
+}
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+__device__ __forceinline__ float sigmoid_gate(float z) { return math::norm_gate(z, true); }
+
+// The sums of a row over a range of its keys, kept in a workspace until the
+// ranges are joined: O [slots][rows][D], then (m, l) [slots][rows] pairs, f32.
+struct Partials {
+  float* o;
+  float2* ml;
+  int rows, D;
+  __host__ __device__ Partials(void* ws, int64_t slots, int rows_, int D_)
+      : o(static_cast<float*>(ws)),
+        ml(reinterpret_cast<float2*>(static_cast<float*>(ws) + slots * rows_ * D_)),
+        rows(rows_),
+        D(D_) {}
+  static size_t bytes(int64_t slots, int rows, int64_t D) {
+    return (size_t)(slots * rows * (D + 2)) * sizeof(float);
+  }
+#ifdef __CUDACC__
+  // One warp, E = D / 32 dims per lane.
+  template <int E>
+  __device__ void put(int64_t slot, int r, int lane, const float (&acc)[E], float m, float l) const {
+    float* d = o + (slot * rows + r) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) d[e] = acc[e];
+    if (lane == 0) ml[slot * rows + r] = make_float2(m, l);
+  }
+  // acc, m, l <- the sums over both key ranges.  A range without keys (m = -inf)
+  // adds nothing.
+  template <int E>
+  __device__ void add(int64_t slot, int r, int lane, float (&acc)[E], float& m, float& l) const {
+    const float2 x = ml[slot * rows + r];
+    if (x.x == -INFINITY) return;
+    const float mn = fmaxf(m, x.x);
+    const float f = m == -INFINITY ? 0.0f : exp2f(m - mn), g = exp2f(x.x - mn);
+    const float* s = o + (slot * rows + r) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, g * s[e]);
+    l = fmaf(l, f, g * x.y);
+    m = mn;
+  }
+#endif
+};
+
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+// The tail of a row by one warp: normalise, gate, round once, store; the lse
+// of the scaled scores from their base-2 form.  A row without a key: 0, -inf.
+template <typename T, int D>
+__device__ __forceinline__ void finish_row(const AttnLaunch& p, int t, int h, int lane,
+                                           const float (&acc)[D / 32], float m, float l) {
+  constexpr int E = D / 32;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  T* out = static_cast<T*>(p.out) + ((int64_t)t * p.Hq + h) * D + lane * E;
+  const T* gate = p.gate.p == nullptr ? nullptr
+                                      : static_cast<const T*>(p.gate.p) + (int64_t)t * p.gate.ts +
+                                            (int64_t)h * p.gate.hs + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    float x = acc[e] * inv;
+    if (gate != nullptr) x *= sigmoid_gate(to_f(gate[e]));
+    out[e] = from_f<T>(x);
+  }
+  if (p.lse != nullptr && lane == 0)
+    p.lse[(int64_t)t * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// One row (token t, query head h) over the keys [k0, k1) of its sequence, by
+// one warp, key after key in f32 with a running maximum: D / 32 dims per lane.
+// m is the maximum of the scaled scores times log2(e), acc and l the sums at
+// that reference.  The tiled kernels multiply a masked key's weight 0 into its
+// v row, which is not 0 when that v is infinite or NaN; a row whose tiled
+// result is not finite is therefore evaluated here, where a masked key is not
+// touched at all.  bad pages read as zeros, as in the tiled kernels.
+template <typename T, int D>
+__device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int t, int h, int k0,
+                                       int k1, float (&acc)[D / 32], float& m, float& l) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int hkv = h / (p.Hq / p.Hkv);
+  const T* q = static_cast<const T*>(p.q.p) + (int64_t)t * p.q.ts + (int64_t)h * p.q.hs + lane * E;
+  float qv[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    qv[e] = to_f(q[e]);
+    acc[e] = 0.0f;
+  }
+  m = -INFINITY;
+  l = 0.0f;
+  bool nan = false;
+  const float c = p.scale * kLog2e;
+  for (int j = k0; j < k1; ++j) {
+    const int64_t ko = key_offset(p, false, s, base, hkv, j);
+    const int64_t vo = key_offset(p, true, s, base, hkv, j);
+    float dot = 0.0f;
+    if (ko >= 0) {
+      const T* kr = static_cast<const T*>(key_base(p, false)) + ko + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) dot = fmaf(qv[e], to_f(kr[e]), dot);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    const float x = dot * c;
+    if (x != x) nan = true;
+    if (x == -INFINITY && m == -INFINITY) continue;  // weight 0 beside any finite score
+    const float mn = fmaxf(m, x);
+    const float f = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
+    const float w = exp2f(x - mn);
+    m = mn;
+    l = fmaf(l, f, w);
+    const T* vr = static_cast<const T*>(key_base(p, true)) + (vo < 0 ? 0 : vo) + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * (vo < 0 ? 0.0f : to_f(vr[e])));
+  }
+  if (nan) {
+    m = 0.0f;
+    l = __int_as_float(0x7fc00000);
+  }
+}
+
+}  // namespace attn
+}  // namespace gdn

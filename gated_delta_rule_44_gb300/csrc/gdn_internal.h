@@ -168,4 +168,67 @@ cudaError_t launch_gated_rmsnorm(const NormLaunch& p, cudaStream_t s);
 size_t chunked_workspace_bytes(int64_t T, int64_t N, int64_t Hv, int64_t Dk, int64_t Dv);
 cudaError_t launch_chunked(const ChunkedLaunch& p, cudaStream_t s);
 
+// ---- full (softmax) attention layer ------------------------------------------
+
+// One strided [tokens, heads, D] tensor (D contiguous; strides in elements).
+struct AttnRows {
+  const void* p;
+  int64_t ts, hs;  // token, head stride
+};
+
+// One paged cache tensor [pages, heads, page_size, D] by strides (elements).
+struct AttnPages {
+  void* p;
+  int64_t ps, hs, ts;  // page, head, token stride
+};
+
+struct AttnPrepareLaunch {
+  int T, N, Hq, Hkv, D, rot;
+  bool bf16;
+  float eps;
+  AttnRows q, k, v;
+  const void* q_w;  // null: no norm
+  const void* k_w;
+  const float* cos_sin;  // [max_pos, rot]; null when rot == 0
+  int64_t max_pos;
+  const int32_t* positions;  // null: the token's place in its sequence
+  const int32_t* cu;         // null: one token per sequence
+  const int32_t* kv_lens;    // null: the number of new tokens
+  const int32_t* table;      // null: no cache
+  int64_t table_stride;
+  int max_pages, page_size;
+  int64_t num_pages;
+  AttnPages kc, vc;
+  void* q_out;  // [T, Hq, D]
+  void* k_out;  // [T, Hkv, D] or null
+  unsigned* status;
+};
+cudaError_t launch_attn_prepare(const AttnPrepareLaunch& p, cudaStream_t s);
+
+// Causal attention of packed new tokens over packed keys (table == null: k, v
+// are [T, Hkv, D] rows) or over a paged cache.
+struct AttnLaunch {
+  int T, N, Hq, Hkv, D, max_q;
+  bool bf16;
+  float scale;
+  AttnRows q;
+  AttnRows k, v;         // packed form
+  const int32_t* cu;     // null: one token per sequence
+  const int32_t* kv_lens;  // paged form
+  const int32_t* table;
+  int64_t table_stride;
+  int max_pages, page_size;
+  int64_t num_pages;
+  AttnPages kc, vc;
+  AttnRows gate;  // p null: none
+  void* out;      // [T, Hq, D]
+  float* lse;     // [T, Hq] or null
+  void* ws;
+  size_t ws_bytes;
+  unsigned* status;
+};
+// CUDA-core form: any supported size (D in {32, 64, 128, 256}, Hq / Hkv <= 64).
+cudaError_t launch_attn_simt(const AttnLaunch& p, cudaStream_t s);
+size_t attn_simt_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D);
+
 }  // namespace gdn

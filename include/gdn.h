@@ -18,6 +18,13 @@
  *   gdn_spec_decode     multi-token decode step (per-draft state snapshots)
  *   gdn_kda_varlen      the recurrence with one decay per key channel (KDA)
  *   gdn_gated_rmsnorm   the gated RMSNorm applied to the recurrence output
+ * and the full (softmax) attention layer that stands between such layers in a
+ * hybrid model, over packed prompts or a paged key/value cache:
+ *   gdn_attn_prepare    per-head RMS norm of q and k, rotary positions, new k
+ *                       and v rows into the paged cache
+ *   gdn_attn_varlen     causal attention over packed prompts
+ *   gdn_attn_paged      attention of new tokens (one, a few drafts, a chunk of
+ *                       a prompt) over the paged cache
  * and a host-only check of a mixed step's metadata:
  *   gdn_validate_mixed  decode rows first, prefill cu_seqlens rebased
  *
@@ -641,6 +648,142 @@ typedef struct gdn_mixed_meta {
 } gdn_mixed_meta;
 
 int gdn_validate_mixed(const gdn_mixed_meta* meta);
+
+/* ---------------------------------------------------------------------------
+ * Full attention: the layer of a hybrid model that keeps every key and value.
+ *
+ * Sequence s has q_len = cu_seqlens[s+1] - cu_seqlens[s] new tokens and a
+ * context of L = kv_lens[s] tokens that ends with them: new token i sits at
+ * position L - q_len + i and attends to the keys at positions 0 .. L - q_len +
+ * i of its own sequence.  A token at a negative position (L < q_len; L = 0
+ * makes a whole sequence padding) sees no key: its output is 0, its lse -inf,
+ * and nothing of it is written to a cache.  q_len = 0 is allowed.  Query head
+ * h reads kv head h / (Hq / Hkv).
+ *
+ * Common rules: D in {32, 64, 128, 256}; Hq a multiple of Hkv, Hq / Hkv <= 64;
+ * f32 or bf16 rows of D contiguous values; every pointer 16-byte aligned and
+ * every stride a multiple of 16 bytes.  Sums, softmax statistics and norms are
+ * f32; results are rounded once, where they are stored.
+ * What only the device can see is checked there: cu_seqlens that decrease or
+ * do not span the T tokens, kv_lens outside [0, max_pages * page_size], pages
+ * outside [0, num_pages), positions outside the rotary table.  Nothing is then
+ * read or written out of bounds (a bad page reads as zeros and is not written;
+ * a sequence with bad offsets is skipped) and gdn_read_device_status() returns
+ * GDN_ERR_DEVICE_CHECK.  Host mirrors, where given, are checked before launch.
+ * ------------------------------------------------------------------------- */
+
+/* A [tokens, heads, D] tensor with its strides in elements (0: contiguous). */
+typedef struct gdn_attn_rows {
+  const void* data;
+  int64_t len;           /* elements reachable from data */
+  int64_t token_stride;  /* 0 = heads * D */
+  int64_t head_stride;   /* 0 = D */
+} gdn_attn_rows;
+
+/* A paged cache: keys and values of position p of sequence s are row
+ * p % page_size of page block_table[s * table_stride + p / page_size].
+ * Each of k and v is [num_pages, Hkv, page_size, D] by strides in elements
+ * (0: contiguous in that order), so [num_pages, page_size, Hkv, D] or one
+ * tensor for both are strides, too. */
+typedef struct gdn_attn_cache {
+  void* k;
+  int64_t k_len, k_page_stride, k_head_stride, k_token_stride;
+  void* v;
+  int64_t v_len, v_page_stride, v_head_stride, v_token_stride;
+  int64_t num_pages, page_size;
+  const int32_t* block_table;      /* [N, max_pages] */
+  int64_t max_pages, table_stride; /* table_stride 0 = max_pages */
+  const int32_t* block_table_host; /* optional host copy (needs kv_lens_host): the pages
+                                      of live positions are checked */
+} gdn_attn_cache;
+
+/* gdn_attn_prepare -- per token and head, over the head's D values:
+ *   x^ = x / sqrt(mean_d x^2 + eps) * weight    (q, k; where a weight is given)
+ *   rotary on the first rot_dim values: with (c, s) the [cos | sin] halves of
+ *   the table row of the token's rotary position,
+ *     y[j] = x^[j] c[j] - x^[j + R/2] s[j],  y[j + R/2] = x^[j + R/2] c[j] + x^[j] s[j]
+ * q goes to q_out; k to the cache and / or k_out; v to the cache.  A token
+ * without a position, or with one outside the rotary table, gives a zero q_out
+ * and k_out row and is not written to the cache.  Two tokens of one call must
+ * not share a cache row. */
+typedef struct gdn_attn_prepare_args {
+  int64_t T, N, Hq, Hkv, D;
+  int64_t rot_dim;           /* rotated values per head: 0, or a multiple of 16, <= D */
+  int32_t act_dtype;         /* gdn_dtype of q, k, v, weights, caches, q_out, k_out */
+  float norm_eps;
+  gdn_attn_rows q, k, v;     /* v may be NULL without a cache */
+  const void* q_norm_weight; /* [D] or NULL (no norm) */
+  int64_t q_norm_weight_len;
+  const void* k_norm_weight; /* [D] or NULL */
+  int64_t k_norm_weight_len;
+  const float* cos_sin;      /* [max_positions, rot_dim]: cos then sin; NULL if rot_dim = 0 */
+  int64_t cos_sin_len;       /* max_positions = cos_sin_len / rot_dim */
+  const int32_t* positions;  /* [T] rotary positions, or NULL (position in the sequence) */
+  const int32_t* cu_seqlens; /* [N+1], or NULL: one new token per sequence (T == N) */
+  const int32_t* kv_lens;    /* [N], or NULL: the q_len of each sequence */
+  const int32_t* cu_seqlens_host; /* optional host copies */
+  const int32_t* kv_lens_host;
+  const gdn_attn_cache* cache; /* NULL: no cache write (k_out is then required) */
+  void* q_out;               /* [T, Hq, D] */
+  int64_t q_out_len;
+  void* k_out;               /* [T, Hkv, D] or NULL */
+  int64_t k_out_len;
+} gdn_attn_prepare_args;
+
+int gdn_attn_prepare(const gdn_attn_prepare_args* args, void* stream);
+
+/* gdn_attn_varlen -- causal attention over packed prompts (L = q_len):
+ *   out[t, h] = sum_j softmax_j(scale q[t, h] . k[j, h']) v[j, h']  over the
+ *   keys j <= t of the token's sequence; times sigmoid(gate[t, h]) when a gate
+ *   is given.  lse[t, h] = ln sum_j exp(scale q . k).
+ * scale < 0 selects 1/sqrt(D). */
+typedef struct gdn_attn_varlen_args {
+  int64_t T, N, Hq, Hkv, D;
+  int32_t act_dtype;         /* gdn_dtype of q, k, v, gate, out */
+  float scale;
+  gdn_attn_rows q, k, v;
+  gdn_attn_rows gate;        /* [T, Hq, D]; data NULL: no gate */
+  const int32_t* cu_seqlens; /* [N+1] */
+  const int32_t* cu_seqlens_host;
+  void* out;                 /* [T, Hq, D] */
+  int64_t out_len;
+  float* lse;                /* [T, Hq] or NULL */
+  int64_t lse_len;
+} gdn_attn_varlen_args;
+
+int gdn_attn_varlen(const gdn_attn_varlen_args* args, void* stream);
+
+/* gdn_attn_paged -- the same attention of new tokens whose keys and values,
+ * their own included, are in the paged cache.  max_q_len bounds every
+ * sequence's q_len (0: T); a sequence with more raises the device status and
+ * its outputs are unspecified.  The workspace (256-byte aligned, any contents)
+ * holds the sums of key ranges that are handled apart. */
+typedef struct gdn_attn_paged_args {
+  int64_t T, N, Hq, Hkv, D;
+  int64_t max_q_len;
+  int32_t act_dtype;         /* gdn_dtype of q, cache, gate, out */
+  float scale;
+  gdn_attn_rows q;
+  gdn_attn_rows gate;        /* [T, Hq, D]; data NULL: no gate */
+  const int32_t* cu_seqlens; /* [N+1], or NULL: one token per sequence (T == N) */
+  const int32_t* kv_lens;    /* [N] */
+  const int32_t* cu_seqlens_host;
+  const int32_t* kv_lens_host;
+  const gdn_attn_cache* cache;
+  void* out;                 /* [T, Hq, D] */
+  int64_t out_len;
+  float* lse;                /* [T, Hq] or NULL */
+  int64_t lse_len;
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_attn_paged_args;
+
+int gdn_attn_paged(const gdn_attn_paged_args* args, void* stream);
+
+/* Workspace bytes gdn_attn_paged needs for these sizes (0 for sizes the call
+ * would refuse). */
+size_t gdn_attn_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
+                                      int64_t max_q_len, int32_t act_dtype);
 
 /* Scratch bytes gdn_prefill_varlen needs for these sizes and algorithm (0 for
  * the recurrent algorithm; for the fused one the bytes of its optional
