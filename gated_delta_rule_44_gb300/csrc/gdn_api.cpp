@@ -8,6 +8,7 @@
 // qwen3_5.cpp) ValidateGdnStateIndices.  On any error nothing is launched.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -1169,6 +1170,12 @@ int check_attn_out(const void* out, int64_t out_len, const float* lse, int64_t l
   return require_aligned(out, "out");
 }
 
+cudaError_t launch_attn(const gdn::AttnLaunch& p, cudaStream_t st) {
+  return gdn::attn_tc_supported(p) ? gdn::launch_attn_tc(p, st) : gdn::launch_attn_simt(p, st);
+}
+
+int64_t resolve_max_q(int64_t max_q, int64_t T) { return max_q == 0 || max_q > T ? T : max_q; }
+
 // The vectors and messages above allocate: nothing may be thrown through the C
 // entry.  The text fits std::string's own buffer.
 template <typename F>
@@ -1290,13 +1297,19 @@ int attn_varlen(const gdn_attn_varlen_args* a, void* stream) {
   p.lse = a->lse;
   p.status = gdn::status_word();
   if (p.status == nullptr) return fail(GDN_ERR_CUDA, "device status word unavailable");
-  return launch_result(gdn::launch_attn_simt(p, st), "gdn_attn_varlen");
+  return launch_result(launch_attn(p, st), "gdn_attn_varlen");
 }
 
 size_t attn_paged_workspace(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
                             int64_t max_q_len, int32_t act_dtype) {
   if (check_act_dtype(act_dtype) || check_attn_dims(T, N, Hq, Hkv, D) || max_q_len < 0) return 0;
-  return gdn::attn_simt_workspace_bytes(T, N, Hq, Hkv, D);
+  // The larger of the two forms' (the page size, which decides, is not known here).
+  size_t n = gdn::attn_simt_workspace_bytes(T, N, Hq, Hkv, D);
+  if (act_dtype != GDN_DTYPE_BF16) return n;
+  n = std::max(n, gdn::attn_tc_workspace_bytes(T, N, Hq, Hkv, D, resolve_max_q(max_q_len, T)));
+  // As many tokens as sequences may mean one token each, without cu_seqlens.
+  if (T == N) n = std::max(n, gdn::attn_tc_workspace_bytes(T, N, Hq, Hkv, D, 1));
+  return n;
 }
 
 int attn_paged(const gdn_attn_paged_args* a, void* stream) {
@@ -1306,8 +1319,7 @@ int attn_paged(const gdn_attn_paged_args* a, void* stream) {
   if (int rc = one_token_each(a->cu_seqlens, a->T, a->N)) return rc;
   if (a->max_q_len < 0)
     return fail(GDN_ERR_INVALID_ARGUMENT, "attention max_q_len must be >= 0, got " + S(a->max_q_len));
-  const int64_t max_q = a->cu_seqlens == nullptr ? 1
-                        : a->max_q_len == 0 || a->max_q_len > a->T ? a->T : a->max_q_len;
+  const int64_t max_q = a->cu_seqlens == nullptr ? 1 : resolve_max_q(a->max_q_len, a->T);
   gdn::AttnLaunch p{};
   if (int rc = check_attn_rows(a->q, "query", a->T, a->Hq, a->D, a->act_dtype, &p.q)) return rc;
   if (a->gate.data != nullptr)
@@ -1354,7 +1366,7 @@ int attn_paged(const gdn_attn_paged_args* a, void* stream) {
   p.ws_bytes = a->workspace_bytes;
   p.status = gdn::status_word();
   if (p.status == nullptr) return fail(GDN_ERR_CUDA, "device status word unavailable");
-  return launch_result(gdn::launch_attn_simt(p, st), "gdn_attn_paged");
+  return launch_result(launch_attn(p, st), "gdn_attn_paged");
 }
 
 }  // namespace

@@ -32,13 +32,41 @@ __host__ __device__ inline int64_t tile_bound(int64_t T, int64_t N, int64_t TT) 
   return T / TT + N;
 }
 
+// Sequence s as the device sees it: tokens a .. b-1 and its context length,
+// clamped to what the tables hold.  bad: cu_seqlens or kv_lens cannot be right
+// (with offsets outside 0 .. T the sequence is taken as empty).
+struct SeqRange {
+  int a, b, kv;
+  int bad;
+};
+__device__ inline SeqRange seq_range(const AttnLaunch& p, int s) {
+  SeqRange r;
+  r.a = cu_at(p.cu, s);
+  r.b = cu_at(p.cu, s + 1);
+  r.bad = r.a < 0 || r.b < r.a || r.b > p.T || (s == 0 && r.a != 0) || (s == p.N - 1 && r.b != p.T);
+  if (r.a < 0 || r.b < r.a || r.b > p.T) {
+    r.a = r.b = r.kv = 0;
+    return r;
+  }
+  r.kv = r.b - r.a;
+  if (p.kv_lens != nullptr) {
+    r.kv = p.kv_lens[s];
+    const int64_t cap = (int64_t)p.max_pages * p.page_size;
+    if (r.kv < 0 || r.kv > cap) {
+      r.bad = 1;
+      r.kv = r.kv < 0 ? 0 : (int)cap;
+    }
+  }
+  if (p.table != nullptr && r.b - r.a > p.max_q) r.bad = 1;
+  return r;
+}
+
 struct SeqTile {
   int s;       // sequence
   int t0;      // first token of the tile
   int nt;      // its tokens (0: an empty number)
   int pos0;    // position of the first token (may be negative)
-  int kv_len;  // keys of the sequence
-  int bad;     // 1: cu_seqlens or kv_lens cannot be right here
+  int bad;
 };
 
 __device__ inline SeqTile find_tile(const AttnLaunch& p, int id, int TT) {
@@ -48,29 +76,13 @@ __device__ inline SeqTile find_tile(const AttnLaunch& p, int id, int TT) {
     if (cu_at(p.cu, mid) / TT + mid <= id) lo = mid;
     else hi = mid - 1;
   }
-  SeqTile r;
-  r.s = lo;
-  r.nt = 0;
-  r.t0 = r.pos0 = r.kv_len = 0;
-  const int a = cu_at(p.cu, lo), b = cu_at(p.cu, lo + 1);
-  r.bad = (a < 0 || b < a || b > p.T || (lo == 0 && a != 0) || (lo == p.N - 1 && b != p.T));
-  if (a < 0 || b < a || b > p.T) return r;
-  int kv = b - a;
-  if (p.kv_lens != nullptr) {
-    kv = p.kv_lens[lo];
-    const int64_t cap = (int64_t)p.max_pages * p.page_size;
-    if (kv < 0 || kv > cap) {
-      r.bad = 1;
-      kv = kv < 0 ? 0 : (int)cap;
-    }
-  }
-  if (p.table != nullptr && p.max_q > 0 && b - a > p.max_q) r.bad = 1;
-  const int64_t off = (int64_t)(id - (a / TT + lo)) * TT;
-  if (off < 0 || off >= b - a) return r;
-  r.t0 = a + (int)off;
-  r.nt = min(TT, b - r.t0);
-  r.pos0 = kv - (b - r.t0);
-  r.kv_len = kv;
+  const SeqRange q = seq_range(p, lo);
+  SeqTile r{lo, 0, 0, 0, q.bad};
+  const int64_t off = (int64_t)(id - (q.a / TT + lo)) * TT;
+  if (off < 0 || off >= q.b - q.a) return r;
+  r.t0 = q.a + (int)off;
+  r.nt = min(TT, q.b - r.t0);
+  r.pos0 = q.kv - (q.b - r.t0);
   return r;
 }
 

@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
 // Joins the key ranges of a row: out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_constant__ AttnLaunch p,
-                                                             int splits, int bm) {
-  const int G = p.Hq / p.Hkv, TT = bm / G;
+                                                             int splits, int bm, int TT) {
+  const int G = p.Hq / p.Hkv;
   const int id = (int)(blockIdx.x / p.Hkv), hkv = blockIdx.x % p.Hkv;
   const SeqTile tile = find_tile(p, id, TT);
   const int lane = threadIdx.x & 31;
@@ -258,9 +258,7 @@ cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
   note_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
-  attn_join_kernel<T, D><<<dim3((unsigned)ctas, BM / (kThreads / 32)), kThreads, 0, st>>>(p, splits, BM);
-  note_launch();
-  return cudaGetLastError();
+  return launch_attn_join(p, splits, BM, TT, st);
 }
 
 template <typename T>
@@ -279,6 +277,23 @@ size_t attn_simt_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, 
   const int64_t ctas = tile_bound(T, N, BM / (Hq / Hkv)) * Hkv;
   const int splits = pick_splits(ctas, INT64_MAX);
   return splits > 1 ? Partials::bytes(ctas * splits, BM, D) : 0;
+}
+
+cudaError_t launch_attn_join(const AttnLaunch& p, int splits, int bm, int TT, cudaStream_t st) {
+  const dim3 grid((unsigned)(tile_bound(p.T, p.N, TT) * p.Hkv), (bm + kThreads / 32 - 1) / (kThreads / 32));
+  if (p.bf16) {
+    if (p.D == 32) attn_join_kernel<__nv_bfloat16, 32><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
+    else if (p.D == 64) attn_join_kernel<__nv_bfloat16, 64><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
+    else if (p.D == 128) attn_join_kernel<__nv_bfloat16, 128><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
+    else attn_join_kernel<__nv_bfloat16, 256><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
+  } else {
+    if (p.D == 32) attn_join_kernel<float, 32><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
+    else if (p.D == 64) attn_join_kernel<float, 64><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
+    else if (p.D == 128) attn_join_kernel<float, 128><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
+    else attn_join_kernel<float, 256><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
+  }
+  note_launch();
+  return cudaGetLastError();
 }
 
 cudaError_t launch_attn_simt(const AttnLaunch& p, cudaStream_t st) {
