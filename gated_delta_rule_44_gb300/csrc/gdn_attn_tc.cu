@@ -15,13 +15,16 @@
 // after the first tiles is rare; P's values stay below 2^8 and its rounding
 // (2^-9 relative) is the same for any reference.  l sums P before the rounding.
 //
-// Warps:  0       TMA loads of Q and of K / V units (128 keys x up to 128 dims)
+// Warps:  0, 3    TMA loads of Q and K, of V, in units of 128 keys x up to 128 dims
+//                 (two warps, because a page of 16 rows makes 16 loads a unit)
 //         1       every MMA
 //         2       zeroes the rows of V past the last visible key (a stale or
-//                 foreign NaN there would survive a weight of 0)
-//         3       bookkeeping of the stream form
-//         4-7     softmax and output of row tile 0, one thread per row
-//         8-11    the same for row tile 1 (two-tile form)
+//                 foreign NaN there would survive a weight of 0); the stream
+//                 form's bookkeeping
+//         4-11    softmax and output of row tile 0: two threads per row, each with
+//                 half the keys (one warp per row would be as many instructions,
+//                 but its dependent chain would outlast the other tile's MMAs)
+//         12-19   the same for row tile 1 (two-tile form)
 // Two-tile form (D <= 128, 256 rows): while one tile's softmax runs on the CUDA
 // cores the other's MMAs run.  One-tile form (D = 256, whose O fills half the
 // TMEM, and few rows): two S buffers, so that the next key tile's scores are
@@ -64,6 +67,24 @@ constexpr int BK = 128;                          // keys per tile
 constexpr float kRaise = 8.0f;                   // log2 headroom of the reference m
 constexpr int kMaxSplits = 64;
 
+constexpr uint32_t kSmemMax = 232448;  // per CTA
+
+struct Shared {
+  uint64_t full[12], empty[12];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv, o_full[2], o_empty, v_landed, v_fixed, end, pair[2][4];
+  uint32_t tmem;
+  int abort;
+  uint32_t loads[12], q_loads;  // issued so far into each place, and of Q
+  uint32_t v_at[2];  // places of the V units to clear
+  int start_s, start_hkv, start_u;
+  long long left;
+  long long scan[20];
+  union {  // what the two warps of 32 rows exchange
+    uint16_t top[2][2][2][128];  // [tile & 1][row tile][half][row]: maxima, as bf16
+    float val[2][2][128];        // [row tile][half][row]
+  } swap;
+};
+
 template <int D, int NQ>
 struct Cfg {
   static constexpr int DU = D < 128 ? D : 128;          // dims of a K / V unit
@@ -71,15 +92,13 @@ struct Cfg {
   static constexpr uint32_t kUnit = BK * DU * 2;        // bytes
   static constexpr uint32_t kQTile = 128 * D * 2;
   static constexpr uint32_t kQ = NQ * kQTile;
-  static constexpr int kStages =
-      (int)((229376u - kQ) / kUnit) > 12 ? 12 : (int)((229376u - kQ) / kUnit);
+  static constexpr int kFit = (int)((kSmemMax - sizeof(Shared) - kQ) / kUnit);
+  static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static constexpr uint32_t kBars = kQ + kStages * kUnit;
-  static constexpr uint32_t kBytes = kBars + 512 + 1024;  // barriers; 1024-byte alignment
-  static constexpr int kThreads = NQ == 2 ? 384 : 256;
+  static constexpr uint32_t kBytes = kBars + sizeof(Shared);
+  static constexpr int kThreads = 128 + 256 * NQ;
 };
-static_assert(Cfg<128, 2>::kBytes <= 232448 && Cfg<256, 1>::kBytes <= 232448 &&
-                  Cfg<64, 2>::kBytes <= 232448 && Cfg<128, 1>::kBytes <= 232448,
-              "shared memory per CTA");
+static_assert(Cfg<128, 2>::kStages >= 5 && Cfg<256, 1>::kStages >= 5, "units in flight");
 
 // TMEM columns (512 allocated): S buffers of 128, then O.
 constexpr uint32_t kTO = 256;
@@ -143,18 +162,6 @@ struct SegIter {
   }
 };
 
-struct Shared {
-  uint64_t full[12], empty[12];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv[2], o_full[2], o_empty[2], v_landed, v_fixed, end;
-  uint32_t tmem;
-  int abort;
-  uint32_t v_at;  // ring position of the V units to clear
-  int start_s, start_hkv, start_u;
-  long long left;
-  long long scan[12];
-};
-static_assert(sizeof(Shared) <= 512, "barrier space");
-
 // The bounded wait of every role; false: leave.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Shared* sh,
                                               unsigned* status) {
@@ -170,6 +177,29 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Sh
     }
   }
   return true;
+}
+// The same by a whole warp, with one answer for it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared* sh,
+                                          unsigned* status) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, sh, status));
+}
+// One lane of a converged warp.  The issuing roles run with all 32 lanes on
+// values the compiler can see are the warp's (from lane 0 by a shuffle), and
+// only the tcgen05 / TMA instruction itself is under this: operands then stay
+// in uniform registers.  Issued by a lone lane of a diverged warp, each MMA
+// cost some 100 cycles of register moves, more than its own 64.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e != 0;
+}
+template <typename T>
+__device__ __forceinline__ T uni(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
 }
 // Inside a role: the bounded wait, or leave the role.
 #define WAIT(bar, parity) \
@@ -217,8 +247,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
                    const __grid_constant__ TcArgs a) {
   using C = Cfg<D, NQ>;
   constexpr int DU = C::DU, NU = C::NU, ST = C::kStages;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char smem[];  // the swizzle atoms' alignment
   Shared* sh = reinterpret_cast<Shared*>(smem + C::kBars);
   const uint32_t sq = smem_u32(smem), skv = sq + C::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -263,15 +292,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       mbar_init(smem_u32(&sh->q_empty), 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&sh->s_full[i]), 1);
-        mbar_init(smem_u32(&sh->p_full[i]), 128);
-        mbar_init(smem_u32(&sh->pv[i]), 1);
+        mbar_init(smem_u32(&sh->p_full[i]), 8);
         mbar_init(smem_u32(&sh->o_full[i]), 1);
-        mbar_init(smem_u32(&sh->o_empty[i]), 128);
+        for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sh->pair[i][w]), 2);
       }
+      mbar_init(smem_u32(&sh->pv), 1);
+      mbar_init(smem_u32(&sh->o_empty), 8);
       mbar_init(smem_u32(&sh->v_landed), 1);
       mbar_init(smem_u32(&sh->v_fixed), 1);
       mbar_init(smem_u32(&sh->end), 1);
       sh->abort = 0;
+      sh->q_loads = 0;
+      for (int i = 0; i < ST; ++i) sh->loads[i] = 0;
       fence_mbar_init();
     }
   } else if (warp == 2) {
@@ -324,7 +356,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = sh->tmem;
+  // All 512 columns: their base is 0, which the addresses below use as such.
+  if (sh->tmem != 0 && tid == 0) atomicOr(p.status, kStatusTimeout);
+  constexpr uint32_t tmem = 0;
   SegIter iter{};
   if constexpr (STREAM)
     iter = SegIter{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
@@ -342,238 +376,236 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     }
   };
 
-  if (warp == 0) {
-    // ---- loads ----
-    uint32_t it = 0;  // units issued
+  if (warp == 0 || warp == 3) {
+    // ---- loads: Q and K by warp 0, V by warp 3 ----
+    // Units go round the ring in the order of their use: K 0 .. A-1, then V j and
+    // K j+A in turn (A = key tiles whose scores run ahead of P V).  Each warp
+    // waits for its own units' places; a place it waits for was freed after every
+    // place it has filled before, so a phase cannot be mistaken for the one two
+    // before it.
+    constexpr int A = NQ == 1 ? 2 : 1;
+    const bool is_k = warp == 0;
+    uint32_t base = 0;           // units of the ranges before
     int seg_n = 0;
     auto role = [&] {
-    Seg g;
-    while (next_seg(g)) {
-      const int n = g.kt1 - g.kt0;
-      const int nq = (NQ == 2 && g.nt > a.TQ) ? 2 : 1;
-      if (seg_n > 0) WAIT(sh->q_empty, (seg_n - 1) & 1);
-      if (lane == 0) {
-        mbar_expect_tx(smem_u32(&sh->q_full), nq * (D / 64) * 128u * G * a.q_box);
-        for (int q = 0; q < nq; ++q)
-          for (int b = 0; b < D / 64; ++b)
-            tma_load_4d(sq + q * C::kQTile + b * 16384, &mq, smem_u32(&sh->q_full), b * 64, 0, g.hkv,
-                        g.t0 + q * a.TQ);
-      }
-      __syncwarp();
-      ++seg_n;
-      // Loads of one key tile's K or V units.  A lane issues one box of 64 dims
-      // x pb keys; boxes past the last visible key are left out.
-      auto load = [&](const CUtensorMap* m, int kt) -> bool {
-        const int j0 = kt * BK;
-        constexpr int NB = DU / 64;
-        int page = 0, row = 0;
-        bool mine = lane < NB * (BK / a.pb);
-        const int jb = j0 + (lane / NB) * a.pb;
-        mine = mine && jb < g.hi;
-        if constexpr (PAGED) {
-          if (mine) {
-            const int64_t pg = page_of(p, g.s, jb / p.page_size);
-            row = jb % p.page_size;
-            if (pg < 0) atomicOr(p.status, kStatusBadIndex);
-            page = pg < 0 ? (int)p.num_pages : (int)pg;  // past the end: reads as zeros
-          }
-        }
-        const int boxes = min(BK, (g.hi - j0 + a.pb - 1) / a.pb * a.pb) / a.pb * NB;
+      Seg g;
+      while (next_seg(g)) {
+        const int kt0 = uni(g.kt0), n = uni(g.kt1) - kt0, hi = uni(g.hi), hkv = uni(g.hkv);
+        if (is_k) {
+          const int nq = uni((NQ == 2 && g.nt > a.TQ) ? 2 : 1), t0 = uni(g.t0);
+          if (seg_n > 0)
+            if (!warp_wait(&sh->q_empty, (seg_n - 1) & 1, sh, p.status)) return;
+          if (elect_one()) {
+            sh->q_loads = seg_n + 1;
+            mbar_expect_tx(smem_u32(&sh->q_full), nq * (D / 64) * 128u * G * a.q_box);
+            for (int q = 0; q < nq; ++q)
 #pragma unroll
-        for (int u = 0; u < NU; ++u, ++it) {
-          const int st = it % ST;
-          if (it >= (uint32_t)ST)
-            if (!wait_or_abort(&sh->empty[st], (it / ST - 1) & 1, sh, p.status)) return false;
-          const uint32_t full = smem_u32(&sh->full[st]);
-          if (lane == 0) mbar_expect_tx(full, boxes * a.pb * 128u);
-          __syncwarp();
-          if (mine) {
-            const uint32_t dst =
-                skv + st * C::kUnit + (lane % NB) * 16384 + (lane / NB) * a.pb * 128;
-            const int d = u * DU + (lane % NB) * 64;
-            if constexpr (PAGED) tma_load_4d(dst, m, full, d, row, g.hkv, page);
-            else tma_load_3d(dst, m, full, d, cu_at(p.cu, g.s) + jb, g.hkv);
+              for (int b = 0; b < D / 64; ++b)
+                tma_load_4d(sq + q * C::kQTile + b * 16384, &mq, smem_u32(&sh->q_full), b * 64, 0, hkv,
+                            t0 + q * a.TQ);
           }
-          __syncwarp();
+          ++seg_n;
         }
-        return true;
-      };
-      constexpr int kAhead = NQ == 1 ? 2 : 1;  // key tiles whose scores run ahead of P V
-      for (int j = 0; j < min(n, kAhead); ++j)
-        if (!load(&mk, g.kt0 + j)) return;
-      for (int j = 0; j < n; ++j) {
-        // The order of use: K j+1 follows V j in the two-tile form, K j+2 in the other.
-        if (!load(&mv, g.kt0 + j)) return;
-        if (j + kAhead < n)
-          if (!load(&mk, g.kt0 + j + kAhead)) return;
+        // Loads of 64 dims x pb keys; those past the last visible key are left out.
+        constexpr int NB = DU / 64;
+        const CUtensorMap* map = is_k ? &mk : &mv;
+        const int per_tile = BK / a.pb;
+        const int row0 = PAGED ? 0 : uni(cu_at(p.cu, g.s));
+        // Lane i looks up the page of, and issues, the tile's i-th load: 64 dims of a
+        // group of pb keys.  (A loop over the loads with one elected lane was slower:
+        // 461 against 380 us for drafts over pages of 16 rows.)
+        const int grp = lane / NB, blk = lane % NB;
+        auto find_page = [&](int kt) -> int {
+          const int jb = kt * BK + grp * a.pb;
+          if (!PAGED || grp >= per_tile || kt >= kt0 + n || jb >= hi) return 0;
+          const int64_t pg = page_of(p, g.s, jb / p.page_size);
+          if (pg < 0 && is_k) atomicOr(p.status, kStatusBadIndex);
+          return pg < 0 ? (int)p.num_pages : (int)pg;  // past the end: reads as zeros
+        };
+        int next_page = find_page(kt0);
+        for (int j = 0; j < n; ++j) {
+          const int j0 = (kt0 + j) * BK;
+          const int page = next_page;
+          next_page = find_page(kt0 + j + 1);  // its latency passes during this tile's waits
+          const int groups = min(per_tile, (hi - j0 + a.pb - 1) / a.pb);
+          const uint32_t at = base + NU * (j + (is_k ? max(0, j - A + 1) : min(n, j + A)));
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            const uint32_t it = at + u, st = it % ST;
+            if (it >= (uint32_t)ST)
+              if (!warp_wait(&sh->empty[st], (it / ST - 1) & 1, sh, p.status)) return;
+            const uint32_t full = smem_u32(&sh->full[st]);
+            const uint32_t dst = skv + st * C::kUnit;
+            if (elect_one()) {
+              sh->loads[st] = it / ST + 1;
+              mbar_expect_tx(full, groups * NB * a.pb * 128u);
+            }
+            if constexpr (PAGED) {
+              __syncwarp();
+              if (grp < groups)
+                tma_load_4d(dst + blk * 16384 + grp * a.pb * 128, map, full, u * DU + blk * 64,
+                            (j0 + grp * a.pb) % p.page_size, hkv, page);
+              __syncwarp();
+            } else {
+              if (elect_one()) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                  tma_load_3d(dst + b * 16384, map, full, u * DU + b * 64, row0 + j0, hkv);
+              }
+            }
+          }
+        }
+        base += 2 * n * NU;
       }
-    }
     };
     role();
-    // Every copy issued has landed before the CTA's memory is given up.
-    for (int st = 0; st < ST; ++st) {
-      if (it <= (uint32_t)st) break;
-      const uint32_t uses = (it - st + ST - 1) / ST;
-      mbar_wait(smem_u32(&sh->full[st]), (uses - 1) & 1, kWaitBudget);
-    }
-    if (seg_n > 0) mbar_wait(smem_u32(&sh->q_full), (seg_n - 1) & 1, kWaitBudget);
   } else if (warp == 1) {
     // ---- MMAs ----
-    if (lane == 0) {
-      constexpr uint32_t kIdQK = idesc_bf16_f32(128, BK, false, false);
-      constexpr uint32_t kIdPV = idesc_bf16_f32(128, DU, false, true);
-      uint32_t it = 0;   // units used
-      uint32_t nk = 0;   // key tiles done (one-tile form: S buffer and its phases)
-      int seg_n = 0;
-      int fixes = 0;
-      auto role = [&] {
+    constexpr uint32_t kIdQK = idesc_bf16_f32(128, BK, false, false);
+    constexpr uint32_t kIdPV = idesc_bf16_f32(128, DU, false, true);
+    auto role = [&] {
+      uint32_t nk = 0;  // key tiles done (one-tile form: S buffer and its phases)
+      uint32_t st = 0, round = 0;  // place of the next unit, parity of its round
+      int seg_n = 0, fixes = 0;
       Seg g;
-      while (next_seg(g)) {
-        const int n = g.kt1 - g.kt0;
-        const int nq = (NQ == 2 && g.nt > a.TQ) ? 2 : 1;
-        const bool partial = g.kt1 * BK > g.hi;  // the last tile ends inside
-        WAIT(sh->q_full, seg_n & 1);
+      auto wait = [&](uint64_t& bar, uint32_t parity) { return warp_wait(&bar, parity, sh, p.status); };
+      // The next unit has landed; its place in at.
+      auto take1 = [&](uint32_t& at) -> bool {
+        at = st;
+        if (!wait(sh->full[st], round)) return false;
+        if (++st == ST) {
+          st = 0;
+          round ^= 1;
+        }
         fence_after_sync();
-        // S[buf] = Q[q] K^T over the K units at ring position `at`.
-        auto qk = [&](int q, int buf, uint32_t at) {
+        return true;
+      };
+      // One unit's MMAs, 8 at most: the pipe has about 280 cycles of work queued
+      // when they have been issued, so that one wait between two such blocks is
+      // hidden, and the waits below are spread accordingly.  `done`, if any, is
+      // arrived on when all MMAs so far are complete, and so is the unit's place
+      // if it is not needed again.
+      // S[buf] (+)= Q[q] K^T over the dims of unit u.
+      auto qk = [&](int q, uint32_t buf, int u, uint32_t at, bool last_use, uint64_t* done) {
+        if (elect_one()) {
+          const uint64_t kd = desc_sw128(skv + at * C::kUnit, 16, 1024);
+          const uint64_t qd = desc_sw128(sq + q * C::kQTile + u * (DU / 64) * 16384, 16, 1024);
 #pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            const uint32_t kb = skv + ((at + u) % ST) * C::kUnit;
-            const uint32_t qb = sq + q * C::kQTile + u * (DU / 64) * 16384;
-#pragma unroll
-            for (int k = 0; k < DU / 16; ++k) {
-              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-              mma_bf16(tmem + buf * 128, desc_sw128(qb + off, 16, 1024),
-                       desc_sw128(kb + off, 16, 1024), kIdQK, u + k > 0);
-            }
+          for (int k = 0; k < DU / 16; ++k) {
+            const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+            mma_bf16(buf * 128, qd + off, kd + off, kIdQK, u + k > 0);
           }
-          mma_commit(smem_u32(&sh->s_full[buf]));
-        };
-        // O[q] (+)= P[buf] V over the V units at `at`.
-        auto pv = [&](int q, int buf, uint32_t at, bool acc) {
+          if (last_use) mma_commit(smem_u32(&sh->empty[at]));
+          if (done) mma_commit(smem_u32(done));
+        }
+      };
+      // O[q] (+)= P[buf] V over the dims of unit u.
+      auto pv = [&](int q, uint32_t buf, int u, uint32_t at, bool acc, bool last_use, uint64_t* done) {
+        if (elect_one()) {
+          const uint64_t vd = desc_sw128(skv + at * C::kUnit, 16384, 1024);
 #pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            const uint32_t vb = skv + ((at + u) % ST) * C::kUnit;
+          for (int k = 0; k < BK / 16; ++k)
+            mma_bf16_ta(kTO + q * 128 + u * DU, buf * 128 + (k >> 2) * 64 + (k & 3) * 8, vd + ((k * 2048) >> 4), kIdPV,
+                        acc || k > 0);
+          if (last_use) mma_commit(smem_u32(&sh->empty[at]));
+          if (done) mma_commit(smem_u32(done));
+        }
+      };
+      auto ask_fix = [&](const uint32_t(&at)[NU]) {  // V's units have landed: clear their tail
+        if (lane == 0) {
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              mma_bf16_ta(tmem + kTO + q * 128 + u * DU, tmem + buf * 128 + k * 8,
-                          desc_sw128(vb + k * 2048, 16384, 1024), kIdPV, acc || k > 0);
-          }
-        };
-        auto take = [&]() -> bool {  // the next NU units have landed
-          for (int u = 0; u < NU; ++u, ++it)
-            if (!wait_or_abort(&sh->full[it % ST], (it / ST) & 1, sh, p.status)) return false;
-          fence_after_sync();
-          return true;
-        };
-        auto give = [&](uint32_t at) {  // free NU units once the MMAs so far are done
-          for (int u = 0; u < NU; ++u) mma_commit(smem_u32(&sh->empty[(at + u) % ST]));
-        };
-        auto ask_fix = [&](uint32_t at) {  // V's units have landed: clear their tail
-          sh->v_at = at;
+          for (int u = 0; u < NU; ++u) sh->v_at[u] = at[u];
           mbar_arrive(smem_u32(&sh->v_landed));
-        };
+        }
+        __syncwarp();
+      };
+      while (next_seg(g)) {
+        const int n = uni(g.kt1 - g.kt0);
+        const int nq = uni((NQ == 2 && g.nt > a.TQ) ? 2 : 1);
+        const bool partial = uni((int)(g.kt1 * BK > g.hi));  // the last tile ends inside
+        if (!wait(sh->q_full, seg_n & 1)) return;
+        fence_after_sync();
+        uint32_t ak[NU], av[NU];
         if constexpr (NQ == 2) {
-          uint32_t at = it;
-          if (!take()) return;
-          for (int q = 0; q < nq; ++q) qk(q, q, at);
-          give(at);
+          // NU = 1.  PV 0 | QK 0 | PV 1 | QK 1, a wait before each.
+          if (!take1(ak[0])) return;
+          for (int q = 0; q < nq; ++q) qk(q, q, 0, ak[0], q == nq - 1, &sh->s_full[q]);
+          if (!take1(av[0])) return;
           for (int j = 0; j < n; ++j) {
-            const uint32_t av = it;
-            if (!take()) return;
-            if (j == n - 1 && partial) ask_fix(av);
-            const uint32_t ak = it;
-            if (j + 1 < n)
-              if (!take()) return;
+            const bool more = j + 1 < n;
+            if (!more && partial) ask_fix(av);
+            uint32_t next_v = 0;
             for (int q = 0; q < nq; ++q) {
-              if (!wait_or_abort(&sh->p_full[q], j & 1, sh, p.status)) return;
-              if (j == n - 1 && partial && q == 0)
-                if (!wait_or_abort(&sh->v_fixed, fixes++ & 1, sh, p.status)) return;
+              if (!wait(sh->p_full[q], j & 1)) return;
+              if (!more && partial && q == 0)
+                if (!wait(sh->v_fixed, fixes++ & 1)) return;
               fence_after_sync();
-              pv(q, q, av, j > 0);
-              if (j + 1 < n) qk(q, q, ak);
-              else mma_commit(smem_u32(&sh->o_full[q]));
+              pv(q, q, 0, av[0], j > 0, q == nq - 1, more ? nullptr : &sh->o_full[q]);
+              if (more) {
+                if (q == 0)
+                  if (!take1(ak[0])) return;
+                if (q == nq - 1)
+                  if (!take1(next_v)) return;
+                qk(q, q, 0, ak[0], q == nq - 1, &sh->s_full[q]);
+              }
             }
-            give(av);
-            if (j + 1 < n) give(ak);
+            av[0] = next_v;
           }
         } else {
-          for (int j = 0; j < min(n, 2); ++j) {
-            const uint32_t at = it;
-            if (!take()) return;
-            qk(0, (nk + j) & 1, at);
-            give(at);
-          }
-          for (int j = 0; j < n; ++j, ++nk) {
-            const uint32_t av = it;
-            if (!take()) return;
-            if (j == n - 1 && partial) ask_fix(av);
-            if (j == 0 && seg_n > 0)  // the last range's O has been read
-              if (!wait_or_abort(&sh->o_empty[0], (seg_n - 1) & 1, sh, p.status)) return;
-            if (!wait_or_abort(&sh->p_full[nk & 1], (nk >> 1) & 1, sh, p.status)) return;
-            if (j == n - 1 && partial)
-              if (!wait_or_abort(&sh->v_fixed, fixes++ & 1, sh, p.status)) return;
-            fence_after_sync();
-            pv(0, nk & 1, av, j > 0);
-            mma_commit(smem_u32(&sh->pv[0]));
-            give(av);
-            if (j + 2 < n) {
-              const uint32_t ak = it;
-              if (!take()) return;
-              qk(0, nk & 1, ak);
-              give(ak);
+          // PV j | QK j+2, unit by unit; K j+2 and V j+1 are waited for on the way.
+          for (int j = 0; j < min(n, 2); ++j)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+              if (!take1(ak[u])) return;
+              qk(0, (nk + j) & 1, u, ak[u], true, u == NU - 1 ? &sh->s_full[(nk + j) & 1] : nullptr);
             }
-            if (j == n - 1) mma_commit(smem_u32(&sh->o_full[0]));
+#pragma unroll
+          for (int u = 0; u < NU; ++u)
+            if (!take1(av[u])) return;
+          for (int j = 0; j < n; ++j, ++nk) {
+            const uint32_t buf = nk & 1;
+            const bool more_v = j + 1 < n, more_k = j + 2 < n;
+            if (!more_v && partial) ask_fix(av);
+            if (j == 0 && seg_n > 0)  // the last range's O has been read
+              if (!wait(sh->o_empty, (seg_n - 1) & 1)) return;
+            if (!wait(sh->p_full[buf], (nk >> 1) & 1)) return;
+            if (!more_v && partial)
+              if (!wait(sh->v_fixed, fixes++ & 1)) return;
+            fence_after_sync();
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+              pv(0, buf, u, av[u], j > 0, true, u == NU - 1 ? &sh->pv : nullptr);
+              if (more_k)
+                if (!take1(ak[u])) return;
+            }
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+              if (more_k) qk(0, buf, u, ak[u], true, u == NU - 1 ? &sh->s_full[buf] : nullptr);
+              if (more_v)
+                if (!take1(av[u])) return;
+            }
           }
+          if (elect_one()) mma_commit(smem_u32(&sh->o_full[0]));
         }
-        mma_commit(smem_u32(&sh->q_empty));
+        if (elect_one()) mma_commit(smem_u32(&sh->q_empty));
         ++seg_n;
-      }
-      };
-      role();
-      mma_commit(smem_u32(&sh->end));
-      mbar_wait(smem_u32(&sh->end), 0, kWaitBudget);
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ---- V's rows past the last visible key ----
-    auto role = [&] {
-      int fixes = 0;
-      Seg g;
-      while (next_seg(g)) {
-        if (g.kt1 * BK <= g.hi) continue;
-        WAIT(sh->v_landed, fixes & 1);
-        ++fixes;
-        const uint32_t at = sh->v_at;
-        const int r0 = g.hi - (g.kt1 - 1) * BK;  // first row to clear
-        for (int u = 0; u < NU; ++u) {
-          unsigned char* v = smem + C::kQ + ((at + u) % ST) * C::kUnit;
-          // Whole 128-byte rows: the swizzle permutes inside a row only.
-          for (int i = lane; i < (BK - r0) * (DU / 8); i += 32) {
-            const int r = r0 + i / (DU / 8), ch = i % (DU / 8);
-            *reinterpret_cast<uint4*>(v + (ch >> 3) * 16384 + r * 128 + (ch & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh->v_fixed));
       }
     };
     role();
-  } else if (warp == 3) {
+    if (elect_one()) mma_commit(smem_u32(&sh->end));
+    warp_wait(&sh->end, 0, sh, p.status);
+  } else if (warp == 2) {
     if constexpr (STREAM) {
       // What the joining kernel needs of this CTA's ranges; the outputs of
       // sequences without a key.
       if (lane == 0) {
         int4 r = make_int4(-1, 0, 2, 0);
-        bool first = true;
+        SegIter every = iter;
         Seg g;
-        while (next_seg(g)) {
-          const SeqRange q = seq_range(p, g.s);
-          if (first) r.z = g.kt1 == key_tiles(q) ? 1 : 0;
-          first = false;
-          if (g.kt0 == 0 && g.kt1 < key_tiles(q)) {
+        for (bool first = true; every.next(p, g); first = false) {
+          const int n = key_tiles(seq_range(p, g.s));
+          if (first) r.z = g.kt1 == n ? 1 : 0;
+          if (g.kt0 == 0 && g.kt1 < n) {
             r.x = g.s;
             r.y = g.hkv;
           }
@@ -588,15 +620,57 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           for (int h = 0; h < p.Hq; ++h) finish_row<bf16, D>(p, t, h, lane, zero, -INFINITY, 0.0f);
       }
     }
+    // ---- V's rows past the last visible key ----
+    auto role = [&] {
+      int fixes = 0;
+      Seg g;
+      while (next_seg(g)) {
+        if (g.kt1 * BK <= g.hi) continue;
+        WAIT(sh->v_landed, fixes & 1);
+        ++fixes;
+        const int r0 = g.hi - (g.kt1 - 1) * BK;  // first row to clear
+        for (int u = 0; u < NU; ++u) {
+          unsigned char* v = smem + C::kQ + sh->v_at[u] * C::kUnit;
+          // Whole 128-byte rows: the swizzle permutes inside a row only.
+          for (int i = lane; i < (BK - r0) * (DU / 8); i += 32) {
+            const int r = r0 + i / (DU / 8), ch = i % (DU / 8);
+            *reinterpret_cast<uint4*>(v + (ch >> 3) * 16384 + r * 128 + (ch & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->v_fixed));
+      }
+    };
+    role();
   } else {
     // ---- softmax, output ----
-    const int qt = NQ == 2 ? (warp - 4) >> 2 : 0;
-    const int r = tid & 127;                           // row of the tile, lane of TMEM
+    // Two warps share 32 rows: `half` is the half of the keys of a tile, and of
+    // the dims of O, that this one handles.
+    const int sw = warp - 4, half = (sw >> 2) & 1, qt = NQ == 2 ? sw >> 3 : 0;
+    const int r = tid & 127;                            // row of the tile, lane of TMEM
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // (32 * (warp % 4)) << 16
     const float c = p.scale * kLog2e;
-    const int tok = qt * a.TQ + r / G;                 // token of the tile
+    const int tok = qt * a.TQ + r / G;                  // token of the tile
     auto role = [&] {
-    uint32_t nk = 0;
+    uint32_t nk = 0, np = 0;
+    // Meeting the pair's other warp (bounded; false: leave).
+    uint64_t& pair = sh->pair[qt][warp & 3];
+    auto pair_arrive = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&pair));
+    };
+    auto pair_wait = [&]() -> bool { return wait_or_abort(&pair, np++ & 1, sh, p.status); };
+    // x becomes the row's value of it from the other warp (between two meetings
+    // that keep `val` from being written early).
+    auto swap = [&](float& x) -> bool {
+      sh->swap.val[qt][half][r] = x;
+      pair_arrive();
+      const bool ok = pair_wait();
+      x = sh->swap.val[qt][half ^ 1][r];
+      return ok;
+    };
     int seg_n = 0;
     Seg g;
     while (next_seg(g)) {
@@ -606,145 +680,205 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       // values are not used) so that they cost no masking.
       const int last = valid ? g.pos0 + tok : INT32_MAX;
       const bool idle = __all_sync(0xffffffffu, !valid);
+      // m, the reference of P, is the same in both warps.  It follows the scores
+      // one tile behind: the first tile's maximum is exchanged before its P, later
+      // ones while the next tile's scores are computed, so that neither the
+      // exchange nor the maximum itself delays a P.  P may thus exceed 2^8 (one
+      // rounding relative to its size all the same); should it overflow, the row
+      // is not finite and is evaluated again.
       float m = -INFINITY, l = 0.0f;
-      const uint32_t to = tmem + lanes + kTO + qt * 128;
+      uint32_t top_bits = 0;  // this warp's last published maximum
+      const uint32_t to = tmem + lanes + kTO + qt * 128 + half * (D / 2);
       for (int kt = g.kt0; kt < g.kt1; ++kt, ++nk) {
         const int buf = NQ == 2 ? qt : (int)(nk & 1);
         const uint32_t ph = NQ == 2 ? (uint32_t)(kt - g.kt0) & 1 : (nk >> 1) & 1;
+        const int jj = kt - g.kt0;
         WAIT(sh->s_full[buf], ph);
         fence_after_sync();
         if (!idle) {
           const uint32_t ts = tmem + lanes + buf * 128;
-          float s[4][32];
+          float s[2][32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(ts + i * 32, s[i]);
+          for (int i = 0; i < 2; ++i) tmem_ld32(ts + half * 64 + i * 32, s[i]);
           tmem_ld_wait();
-          const int j0 = kt * BK;
-          if (__any_sync(0xffffffffu, j0 + BK - 1 > last)) {
+          const int j0 = kt * BK + half * 64;
+          if (__any_sync(0xffffffffu, j0 + 63 > last)) {
             const int lim = last - j0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int e = 0; e < 32; ++e) s[i][e] = i * 32 + e <= lim ? s[i][e] : -INFINITY;
           }
-          float mx[4];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto publish = [&] {
+            const float t = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            top_bits = __float_as_uint(t) >> 16;  // cut to bf16: only the agreement matters
+            sh->swap.top[jj & 1][qt][half][r] = (uint16_t)top_bits;
+            pair_arrive();
+          };
+          if (jj == 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            mx[i] = fmaxf(s[i][0], s[i][1]);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 2; e < 32; e += 2) mx[i] = fmaxf(mx[i], fmaxf(s[i][e], s[i][e + 1]));
+              for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mx[k] = fmaxf(mx[k], fmaxf(s[i][e + 2 * k], s[i][e + 2 * k + 1]));
+            publish();
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // c may be 0 (scale 0): 0 * -inf must stay "no key".
-          const float tm = top == -INFINITY ? -INFINITY : top * c;
-          float f = 1.0f;
-          bool raise = false;
-          if (tm > m + kRaise || (m == -INFINITY && tm > m)) {
-            raise = valid && m != -INFINITY;
-            f = m == -INFINITY ? 0.0f : ex2(m - tm);
-            m = tm;
-          }
-          if (__any_sync(0xffffffffu, raise)) {
-            // O is at rest: in the two-tile form S j follows P V j-1, in the
-            // other that product is waited for.
-            if constexpr (NQ == 1) {
-              WAIT(sh->pv[0], (nk - 1) & 1);
-              fence_after_sync();
+          if (jj != 1) {
+            if (!pair_wait()) return;
+            const int slot = jj == 0 ? 0 : (jj - 1) & 1;
+            const float top = fmaxf(__uint_as_float(top_bits << 16),
+                                    __uint_as_float((uint32_t)sh->swap.top[slot][qt][half ^ 1][r] << 16));
+            // Without a score above -inf so far the reference is 0.  (c may be 0,
+            // and 0 * -inf must not count as a score.)
+            const float tm = top == -INFINITY ? -INFINITY : top * c;
+            float f = 1.0f;
+            bool raise = false;
+            if (tm > m + kRaise || (m == -INFINITY && tm > m)) {
+              raise = valid && jj > 0;
+              f = ex2(m - tm);
+              m = tm;
             }
-            l *= f;
+            if (m == -INFINITY) m = 0.0f;
+            if (__any_sync(0xffffffffu, raise)) {
+              // O is at rest: in the two-tile form S j follows P V j-1, in the
+              // other that product is waited for.
+              if constexpr (NQ == 1) {
+                WAIT(sh->pv, (nk - 1) & 1);
+                fence_after_sync();
+              }
+              l *= f;
 #pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
-              float o[32];
-              tmem_ld32(to + i * 32, o);
-              tmem_ld_wait();
+              for (int i = 0; i < D / 32; ++i) {
+                float o[16];
+                tmem_ld16(to + i * 16, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= f;
-              tmem_st32(to + i * 32, o);
+                for (int e = 0; e < 16; ++e) o[e] *= f;
+                tmem_st16(to + i * 16, o);
+              }
+              tmem_st_wait();
             }
-            tmem_st_wait();
           }
-          const float ref = m == -INFINITY ? 0.0f : -m;
+          const float ref = -m;
           float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float pk[32];
+          for (int i = 0; i < 2; ++i) {
+            float(&x)[32] = s[i];
+            float pk[16];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float(&x)[32] = s[h * 2 + i];
+            for (int e = 0; e < 32; e += 4) {
+              mx[(e >> 1) & 2] = fmaxf(mx[(e >> 1) & 2], fmaxf(x[e], x[e + 1]));
+              mx[((e >> 1) & 2) + 1] = fmaxf(mx[((e >> 1) & 2) + 1], fmaxf(x[e + 2], x[e + 3]));
+              fma2(x[e], x[e + 1], c, ref);
+              fma2(x[e + 2], x[e + 3], c, ref);
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                fma2(x[e], x[e + 1], c, ref);
-                fma2(x[e + 2], x[e + 3], c, ref);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[e + k] = ex2(x[e + k]);
-                add2(l0, l1, x[e], x[e + 1]);
-                add2(l2, l3, x[e + 2], x[e + 3]);
-                pk[i * 16 + e / 2] = __uint_as_float(pack_bf16(x[e], x[e + 1]));
-                pk[i * 16 + e / 2 + 1] = __uint_as_float(pack_bf16(x[e + 2], x[e + 3]));
-              }
+              for (int k = 0; k < 4; ++k) x[e + k] = ex2(x[e + k]);
+              add2(l0, l1, x[e], x[e + 1]);
+              add2(l2, l3, x[e + 2], x[e + 3]);
+              pk[e / 2] = __uint_as_float(pack_bf16(x[e], x[e + 1]));
+              pk[e / 2 + 1] = __uint_as_float(pack_bf16(x[e + 2], x[e + 3]));
             }
-            tmem_st32(ts + h * 32, pk);
+            tmem_st16(ts + half * 64 + i * 16, pk);
           }
-          l += (l0 + l1) + (l2 + l3);
           tmem_st_wait();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
+          l += (l0 + l1) + (l2 + l3);
+          if (jj > 0 && kt + 1 < g.kt1) publish();
+        } else if (lane == 0) {
+          mbar_arrive(smem_u32(&sh->p_full[buf]));
         }
-        fence_before_sync();
-        mbar_arrive(smem_u32(&sh->p_full[buf]));
       }
       // ---- the row's sums out ----
+      const int t = g.t0 + tok, h = g.hkv * G + r % G;
+      const bool gated = p.gate.p != nullptr && g.slot < 0 && valid;
+      const uint4* gate = reinterpret_cast<const uint4*>(
+          static_cast<const bf16*>(p.gate.p) + (int64_t)t * p.gate.ts + (int64_t)h * p.gate.hs +
+          half * (D / 2));
+      // The gate's loads go out before the wait and a chunk of 32 dims ahead: one
+      // at a time, just before use, they were half the time of a short row.
+      uint4 gw[4];
+      if (gated) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gw[e] = gate[e];
+      }
       WAIT(sh->o_full[qt], seg_n & 1);
       fence_after_sync();
       if (!idle) {
-        const int t = g.t0 + tok, h = g.hkv * G + r % G;
+        float theirs = l;
+        if (!swap(theirs)) return;
+        l = half == 0 ? l + theirs : theirs + l;  // the same sum on both sides
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const Partials part(a.ws, STREAM ? 2 * (int64_t)a.ctas : (int64_t)gridDim.x * a.splits, a.rows, D);
         const int pr = tok * G + r % G;
-        bool finite = isfinite(l);
-        bf16* out = static_cast<bf16*>(p.out) + ((int64_t)t * p.Hq + h) * D;
-        const bf16* gate = static_cast<const bf16*>(p.gate.p) + (int64_t)t * p.gate.ts +
-                           (int64_t)h * p.gate.hs;
+        // A sum of 0 with a key in sight: every weight was lost beside a reference
+        // of 0 that no score gave.
+        bool finite = isfinite(l) && !(l == 0.0f && last >= g.kt0 * BK);
+        bf16* out = static_cast<bf16*>(p.out) + ((int64_t)t * p.Hq + h) * D + half * (D / 2);
 #pragma unroll 1
-        for (int i = 0; i < D / 32; ++i) {
+        for (int i = 0; i < D / 64; ++i) {
           float o[32];
           tmem_ld32(to + i * 32, o);
           tmem_ld_wait();
+          float big = 0.0f;  // NaN and infinities survive a sum of x - x
 #pragma unroll
-          for (int e = 0; e < 32; ++e) finite = finite && isfinite(o[e]);
-          if (valid) {
-            if (g.slot >= 0) {
-              float4* d = reinterpret_cast<float4*>(part.o + (g.slot * a.rows + pr) * D + i * 32);
+          for (int e = 0; e < 32; ++e) big += o[e] - o[e];
+          finite = finite && big == 0.0f;
+          if (g.slot >= 0) {
+            if (valid) {
+              float4* d = reinterpret_cast<float4*>(part.o + (g.slot * a.rows + pr) * D +
+                                                    half * (D / 2) + i * 32);
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            } else {
+            }
+            continue;
+          }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint4 w;
-                uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
-                uint4 gw = make_uint4(0u, 0u, 0u, 0u);
-                if (p.gate.p != nullptr) gw = *reinterpret_cast<const uint4*>(gate + i * 32 + e * 8);
-                const uint32_t* gp = reinterpret_cast<const uint32_t*>(&gw);
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          if (gated) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  float x0 = o[e * 8 + 2 * k] * inv, x1 = o[e * 8 + 2 * k + 1] * inv;
-                  if (p.gate.p != nullptr) {
-                    x0 *= sigmoid_gate(__uint_as_float(gp[k] << 16));
-                    x1 *= sigmoid_gate(__uint_as_float(gp[k] & 0xffff0000u));
-                  }
-                  wp[k] = pack_bf16(x0, x1);
-                }
-                *reinterpret_cast<uint4*>(out + i * 32 + e * 8) = w;
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t gp[4] = {gw[e].x, gw[e].y, gw[e].z, gw[e].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                o[e * 8 + 2 * k] *= sigmoid_gate(__uint_as_float(gp[k] << 16));
+                o[e * 8 + 2 * k + 1] *= sigmoid_gate(__uint_as_float(gp[k] & 0xffff0000u));
               }
+            }
+            if (i + 1 < D / 64) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) gw[e] = gate[(i + 1) * 4 + e];
+            }
+          }
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = pack_bf16(o[e * 8 + 2 * k], o[e * 8 + 2 * k + 1]);
+              *reinterpret_cast<uint4*>(out + i * 32 + e * 8) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
-        if (valid) {
-          if (g.slot >= 0) part.ml[g.slot * a.rows + pr] = make_float2(m, l);
+        if (valid && half == 0) {
+          if (g.slot >= 0) part.ml[g.slot * a.rows + pr] = make_float2(l == 0.0f ? -INFINITY : m, l);
           else if (p.lse != nullptr)
             p.lse[(int64_t)t * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
-        unsigned redo = __ballot_sync(0xffffffffu, valid && !finite);
-        __syncwarp();
+        // Rows to evaluate again, by the pair's first warp once both have stored.
+        pair_arrive();
+        if (!pair_wait()) return;
+        theirs = finite ? 1.0f : 0.0f;
+        if (!swap(theirs)) return;
+        unsigned redo = __ballot_sync(0xffffffffu, valid && !(finite && theirs == 1.0f));
+        pair_arrive();  // `theirs` has been read: the next range may publish
+        if (!pair_wait()) return;
+        if (half == 1) redo = 0;
         while (redo) {
           const int src = __ffs(redo) - 1;
           redo &= redo - 1;
@@ -760,7 +894,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       ++seg_n;
       if constexpr (STREAM) {
         fence_before_sync();
-        mbar_arrive(smem_u32(&sh->o_empty[0]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->o_empty));
       }
     }
     };
@@ -769,12 +904,24 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   __syncwarp();
   fence_before_sync();
   __syncthreads();
-  if (warp == 2) tmem_dealloc(tmem, 512);
+  if (sh->abort) {
+    // A wait gave up: copies may still be in flight (otherwise the MMA role has
+    // waited for each).  They land before the CTA's memory is given up.
+    if (tid == 0) {
+      for (int i = 0; i < ST; ++i)
+        if (sh->loads[i]) mbar_wait(smem_u32(&sh->full[i]), (sh->loads[i] - 1) & 1, kWaitBudget);
+      if (sh->q_loads) mbar_wait(smem_u32(&sh->q_full), (sh->q_loads - 1) & 1, kWaitBudget);
+    }
+    __syncthreads();
+  }
+  if (warp == 2) tmem_dealloc(sh->tmem, 512);
 }
 
 // Joins the ranges of the pairs that the stream form cut: CTA c serves the pair
 // that range c began and left open; its further sums are in the blocks of the
-// CTAs after it, in the order of their keys.
+// CTAs after it, in the order of their keys.  A block takes 8 rows, a warp one
+// row at a time: the ranges' (m, l) first, a lane each, then the weighted sum of
+// their O, whose loads do not wait for one another.
 template <int D>
 __global__ void __launch_bounds__(256) attn_stream_join_kernel(const __grid_constant__ AttnLaunch p,
                                                                const __grid_constant__ TcArgs a) {
@@ -784,15 +931,61 @@ __global__ void __launch_bounds__(256) attn_stream_join_kernel(const __grid_cons
   const int G = p.Hq / p.Hkv;
   const SeqRange q = seq_range(p, mine.x);
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  // The last range: the first after c0 that ends the pair.
+  int c1 = c0;
+  for (int c = c0 + 1; c1 == c0 && c < a.ctas; c += 32) {
+    const unsigned ends = __ballot_sync(0xffffffffu, c + lane < a.ctas && a.info[c + lane].z == 1);
+    c1 = ends ? c + __ffs(ends) - 1 : (c + 32 >= a.ctas ? a.ctas - 1 : c0);
+  }
   if (r >= min(q.b - q.a, p.max_q) * G) return;
   const Partials part(a.ws, 2 * (int64_t)a.ctas, a.rows, D);
-  float acc[D / 32] = {}, m = -INFINITY, l = 0.0f;
-  part.add<D / 32>(2 * (int64_t)c0 + 1, r, lane, acc, m, l);
-  for (int c = c0 + 1; c < a.ctas; ++c) {
-    const int ends = a.info[c].z;
-    if (ends == 2) continue;
-    part.add<D / 32>(2 * (int64_t)c, r, lane, acc, m, l);
-    if (ends == 1) break;
+  constexpr int E = D / 32;
+  float acc[E] = {}, m = -INFINITY, l = 0.0f;
+  for (int c = c0; c <= c1; c += 32) {
+    // Range c + lane: block 2 c0 + 1 for the first, 2 c' for the rest; CTAs
+    // without a range (z = 2) hold nothing.
+    const int cl = c + lane;
+    const int64_t slot = 2 * (int64_t)cl + (cl == c0 ? 1 : 0);
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (cl <= c1 && (cl == c0 || a.info[cl].z != 2)) ml = part.ml[slot * a.rows + r];
+    float mn = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mn = fmaxf(mn, m);
+    if (mn == -INFINITY) continue;
+    const float f = exp2f(m - mn);  // 0 for m = -inf
+    const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mn);
+    float lw = ml.x == -INFINITY ? 0.0f : w * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    l = fmaf(l, f, lw);
+    m = mn;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= f;
+    unsigned live = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
+    while (live) {  // four ranges' loads in flight
+      float x[4][E], wk[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        wk[k] = 0.0f;
+        if (live) {
+          const int src = __ffs(live) - 1;
+          live &= live - 1;
+          wk[k] = __shfl_sync(0xffffffffu, w, src);
+          const int ck = c + src;
+          const float* o = part.o + ((2 * (int64_t)ck + (ck == c0 ? 1 : 0)) * a.rows + r) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[k][e] = o[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[k][e] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wk[k], x[k][e], acc[e]);
+    }
   }
   finish_row<bf16, D>(p, q.a + r / G, mine.y * G + r % G, lane, acc, m, l);
 }
