@@ -15,24 +15,29 @@
 // after the first tiles is rare; P's values stay below 2^8 and its rounding
 // (2^-9 relative) is the same for any reference.  l sums P before the rounding.
 //
-// Warps:  0, 3    TMA loads of Q and K, of V, in units of 128 keys x up to 128 dims
-//                 (two warps, because a page of 16 rows makes 16 loads a unit)
-//         1       every MMA
-//         2       zeroes the rows of V past the last visible key (a stale or
-//                 foreign NaN there would survive a weight of 0); the stream
-//                 form's bookkeeping
-//         4-11    softmax and output of row tile 0: two threads per row, each with
-//                 half the keys (one warp per row would be as many instructions,
-//                 but its dependent chain would outlast the other tile's MMAs)
+// Warps:  0       hands out the work; TMA loads of Q and K
+//         1, 2    the MMAs: two-tile form, a row tile each; one-tile form, Q K^T and
+//                 P V.  Issuing an MMA takes its warp as long as the pipe works on
+//                 it (64 cycles), so a wait by a lone issuer is a hole in the pipe
+//                 (3000 cycles for each 2048 of MMAs); here the other warp fills it
+//         3       TMA loads of V; clears the rows of V past the last visible key (a
+//                 stale or foreign NaN there would survive a weight of 0); the
+//                 stream form's bookkeeping
+//         4-11    softmax and output of row tile 0, two threads per row, each with
+//                 half the keys and half the dims of O
 //         12-19   the same for row tile 1 (two-tile form)
+// K and V each go through their own ring of 16 KB units (K: 128 keys x 64 dims;
+// V: 64 keys x 128 dims, or 128 x 64 for D = 64).
 // Two-tile form (D <= 128, 256 rows): while one tile's softmax runs on the CUDA
 // cores the other's MMAs run.  One-tile form (D = 256, whose O fills half the
 // TMEM, and few rows): two S buffers, so that the next key tile's scores are
 // computed during a softmax.
 //
-// Work.  The tile form has one CTA per (tile, kv head), the longest first, and
-// with few of them cuts each into key ranges whose sums a second kernel joins.
-// The stream form serves sequences whose new rows fit one tile (decode,
+// Work.  The tile form has a grid of (tile, kv head) items, the longest first,
+// and with few of them cuts each into key ranges whose sums a second kernel
+// joins.  A CTA that nears the end of its item takes the next one off the grid
+// (cluster launch control) and loads for it while the last one's rows are
+// stored.  The stream form serves sequences whose new rows fit one tile (decode,
 // drafts): the key tiles of all (sequence, kv head) pairs, in order, are cut
 // into equal consecutive ranges, one per SM, whatever the lengths; a pair cut
 // between SMs leaves its sums in the workspace, and a second kernel joins them
@@ -69,13 +74,24 @@ constexpr int kMaxSplits = 64;
 
 constexpr uint32_t kSmemMax = 232448;  // per CTA
 
+constexpr int kMaxRing = 6;
+
+// A range of key tiles of one (tile, kv head).
+struct Seg {
+  int s, hkv, t0, nt, pos0, hi, kt0, kt1;  // s < 0: no more
+  int64_t slot;  // workspace block of its sums; -1: it has every key of its rows
+};
+
 struct Shared {
-  uint64_t full[12], empty[12];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv, o_full[2], o_empty, v_landed, v_fixed, end, pair[2][4];
+  uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv[2], o_full[2], o_empty[2], v_land, end[2];
+  uint64_t pair[2][4];
+  uint64_t seg_full[2], seg_empty[2], clc_full;
+  alignas(16) uint4 clc;  // the next item's answer
+  Seg seg[2];
   uint32_t tmem;
   int abort;
-  uint32_t loads[12], q_loads;  // issued so far into each place, and of Q
-  uint32_t v_at[2];  // places of the V units to clear
+  uint32_t k_loads[kMaxRing], v_loads[kMaxRing], q_loads, clc_asked, land_asked;  // issued so far
   int start_s, start_hkv, start_u;
   long long left;
   long long scan[20];
@@ -87,18 +103,20 @@ struct Shared {
 
 template <int D, int NQ>
 struct Cfg {
-  static constexpr int DU = D < 128 ? D : 128;          // dims of a K / V unit
-  static constexpr int NU = D / DU;                     // units per key tile
-  static constexpr uint32_t kUnit = BK * DU * 2;        // bytes
+  static constexpr uint32_t kUnit = 16384;
+  static constexpr int NU = D / 64;                       // units of a key tile, of K and of V
+  static constexpr int VK = D == 64 ? 128 : 64;           // keys of a V unit
+  static constexpr int VD = D == 64 ? 64 : 128;           // its dims
   static constexpr uint32_t kQTile = 128 * D * 2;
   static constexpr uint32_t kQ = NQ * kQTile;
-  static constexpr int kFit = (int)((kSmemMax - sizeof(Shared) - kQ) / kUnit);
-  static constexpr int kStages = kFit > 12 ? 12 : kFit;
-  static constexpr uint32_t kBars = kQ + kStages * kUnit;
+  static constexpr int kFit = (int)((kSmemMax - sizeof(Shared) - kQ) / kUnit) / 2;
+  static constexpr int ST = kFit > kMaxRing ? kMaxRing : kFit;  // units of either ring
+  static constexpr uint32_t kBars = kQ + 2 * ST * kUnit;
   static constexpr uint32_t kBytes = kBars + sizeof(Shared);
   static constexpr int kThreads = 128 + 256 * NQ;
+  static constexpr int kReaders = 3 + 8 * NQ;  // warps that read the handed-out work
 };
-static_assert(Cfg<128, 2>::kStages >= 5 && Cfg<256, 1>::kStages >= 5, "units in flight");
+static_assert(Cfg<128, 2>::ST >= 5 && Cfg<256, 1>::ST >= 5, "units in flight");
 
 // TMEM columns (512 allocated): S buffers of 128, then O.
 constexpr uint32_t kTO = 256;
@@ -107,18 +125,12 @@ struct TcArgs {
   int splits;   // key ranges per tile (tile form)
   int TQ;       // tokens per row tile: 128 / G
   int q_box;    // tokens of a Q load
-  int pb;       // rows of a K / V load: 128 (packed), or a divisor of the page
+  int pbk, pbv; // rows of a load of K, of V: a unit's keys, or a divisor of the page
   int ctas;     // stream form: the grid
   int rows;     // rows of a workspace block
   int4* info;   // stream form, per CTA: {s, kv head of the pair it began and left open (s = -1:
                 // none), how its first range ends: 0 open, 1 the pair's end, 2 no range at all}
   float* ws;    // the sums
-};
-
-// A range of key tiles of one (tile, kv head).
-struct Seg {
-  int s, hkv, t0, nt, pos0, hi, kt0, kt1;
-  int64_t slot;  // workspace block of its sums; -1: it has every key of its rows
 };
 
 __device__ __forceinline__ int key_tiles(const SeqRange& q) {
@@ -240,70 +252,72 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Asks for a further CTA of the grid in place of its launch.
+__device__ __forceinline__ void clc_ask(Shared* sh) {
+  const uint32_t mb = smem_u32(&sh->clc_full);
+  mbar_expect_tx(mb, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];\n" ::"r"(smem_u32(&sh->clc)),
+      "r"(mb)
+      : "memory");
+}
+// The answer: false when no CTA was left.
+__device__ __forceinline__ bool clc_answer(Shared* sh, uint32_t& x, uint32_t& y) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%3];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, _, _}, r;\n\t}\n"
+      : "=r"(ok), "=&r"(x), "=&r"(y)
+      : "r"(smem_u32(&sh->clc))
+      : "memory");
+  return ok != 0;
+}
+
 template <int D, int NQ, bool PAGED, bool STREAM>
 __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnLaunch p, const __grid_constant__ CUtensorMap mq,
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                    const __grid_constant__ TcArgs a) {
   using C = Cfg<D, NQ>;
-  constexpr int DU = C::DU, NU = C::NU, ST = C::kStages;
+  constexpr int NU = C::NU, ST = C::ST, VK = C::VK, VD = C::VD;
   extern __shared__ __align__(1024) unsigned char smem[];  // the swizzle atoms' alignment
   Shared* sh = reinterpret_cast<Shared*>(smem + C::kBars);
-  const uint32_t sq = smem_u32(smem), skv = sq + C::kQ;
+  const uint32_t sq = smem_u32(smem), sk = sq + C::kQ, sv = sk + ST * C::kUnit;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.Hq / p.Hkv;
 
-  // ---- which work ----
-  Seg seg0;
-  if constexpr (!STREAM) {
-    const int TT = NQ * a.TQ;
-    const int id = (int)(gridDim.x / p.Hkv) - 1 - (int)(blockIdx.x / p.Hkv);
-    const SeqTile t = find_tile(p, id, TT);
-    if (t.bad && tid == 0) atomicOr(p.status, kStatusBadSeqlens);
-    if (t.nt == 0) return;
-    seg0.s = t.s;
-    seg0.hkv = blockIdx.x % p.Hkv;
-    seg0.t0 = t.t0;
-    seg0.nt = t.nt;
-    seg0.pos0 = t.pos0;
-    seg0.hi = max(0, t.pos0 + t.nt);
-    const int n = (seg0.hi + BK - 1) / BK;
-    seg0.kt0 = (int)((int64_t)n * blockIdx.y / a.splits);
-    seg0.kt1 = (int)((int64_t)n * (blockIdx.y + 1) / a.splits);
-    seg0.slot = a.splits > 1 ? ((int64_t)id * p.Hkv + seg0.hkv) * a.splits + blockIdx.y : -1;
-    if (seg0.kt0 == seg0.kt1) {  // no key here
-      const Partials part(a.ws, (int64_t)gridDim.x * a.splits, a.rows, D);
-      for (int r = warp; r < seg0.nt * G; r += C::kThreads / 32) {
-        const float zero[D / 32] = {};
-        if (seg0.slot >= 0) part.put<D / 32>(seg0.slot, r, lane, zero, -INFINITY, 0.0f);
-        else finish_row<bf16, D>(p, seg0.t0 + r / G, seg0.hkv * G + r % G, lane, zero, -INFINITY, 0.0f);
-      }
-      return;
-    }
-  }
-
   if (warp == 0) {
     if (lane == 0) {
+      constexpr int kReleases = NQ == 2 ? 2 : 1;  // MMA warps that use a unit
       for (int i = 0; i < ST; ++i) {
-        mbar_init(smem_u32(&sh->full[i]), 1);
-        mbar_init(smem_u32(&sh->empty[i]), 1);
+        mbar_init(smem_u32(&sh->k_full[i]), 1);
+        mbar_init(smem_u32(&sh->k_empty[i]), kReleases);
+        mbar_init(smem_u32(&sh->v_full[i]), 1);
+        mbar_init(smem_u32(&sh->v_empty[i]), kReleases);
+        sh->k_loads[i] = sh->v_loads[i] = 0;
       }
       mbar_init(smem_u32(&sh->q_full), 1);
-      mbar_init(smem_u32(&sh->q_empty), 1);
+      mbar_init(smem_u32(&sh->q_empty), kReleases);
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&sh->s_full[i]), 1);
         mbar_init(smem_u32(&sh->p_full[i]), 8);
+        mbar_init(smem_u32(&sh->pv[i]), 1);
         mbar_init(smem_u32(&sh->o_full[i]), 1);
+        mbar_init(smem_u32(&sh->o_empty[i]), 8);
+        mbar_init(smem_u32(&sh->end[i]), 1);
+        mbar_init(smem_u32(&sh->seg_full[i]), 1);
+        mbar_init(smem_u32(&sh->seg_empty[i]), C::kReaders);
         for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sh->pair[i][w]), 2);
       }
-      mbar_init(smem_u32(&sh->pv), 1);
-      mbar_init(smem_u32(&sh->o_empty), 8);
-      mbar_init(smem_u32(&sh->v_landed), 1);
-      mbar_init(smem_u32(&sh->v_fixed), 1);
-      mbar_init(smem_u32(&sh->end), 1);
+      mbar_init(smem_u32(&sh->v_land), NU);
+      mbar_init(smem_u32(&sh->clc_full), 1);
       sh->abort = 0;
-      sh->q_loads = 0;
-      for (int i = 0; i < ST; ++i) sh->loads[i] = 0;
+      sh->q_loads = sh->clc_asked = sh->land_asked = 0;
       fence_mbar_init();
     }
   } else if (warp == 2) {
@@ -359,67 +373,100 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   // All 512 columns: their base is 0, which the addresses below use as such.
   if (sh->tmem != 0 && tid == 0) atomicOr(p.status, kStatusTimeout);
   constexpr uint32_t tmem = 0;
-  SegIter iter{};
-  if constexpr (STREAM)
-    iter = SegIter{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
 
-  // The next range into g; one of them in the tile form.
-  bool once = true;
+  // The ranges handed out by warp 0, through two places, to every other role.
+  int seg_in = 0;
   auto next_seg = [&](Seg& g) -> bool {
-    if constexpr (STREAM) {
-      return iter.next(p, g);
-    } else {
-      g = seg0;
-      const bool r = once;
-      once = false;
-      return r;
+    const int i = seg_in & 1;
+    if (!warp_wait(&sh->seg_full[i], (seg_in >> 1) & 1, sh, p.status)) return false;
+    g = sh->seg[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh->seg_empty[i]));
+    ++seg_in;
+    return g.s >= 0;
+  };
+  // A ring's position: place and parity of its round.
+  struct Ring {
+    uint32_t st = 0, round = 0;
+    __device__ void step() {
+      if (++st == ST) {
+        st = 0;
+        round ^= 1;
+      }
     }
   };
 
-  if (warp == 0 || warp == 3) {
-    // ---- loads: Q and K by warp 0, V by warp 3 ----
-    // Units go round the ring in the order of their use: K 0 .. A-1, then V j and
-    // K j+A in turn (A = key tiles whose scores run ahead of P V).  Each warp
-    // waits for its own units' places; a place it waits for was freed after every
-    // place it has filled before, so a phase cannot be mistaken for the one two
-    // before it.
-    constexpr int A = NQ == 1 ? 2 : 1;
-    const bool is_k = warp == 0;
-    uint32_t base = 0;           // units of the ranges before
-    int seg_n = 0;
+  if (warp == 0) {
+    // ---- work; loads of Q and K ----
+    SegIter iter{};
+    if constexpr (STREAM)
+      iter = SegIter{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
     auto role = [&] {
-      Seg g;
-      while (next_seg(g)) {
-        const int kt0 = uni(g.kt0), n = uni(g.kt1) - kt0, hi = uni(g.hi), hkv = uni(g.hkv);
-        if (is_k) {
-          const int nq = uni((NQ == 2 && g.nt > a.TQ) ? 2 : 1), t0 = uni(g.t0);
-          if (seg_n > 0)
-            if (!warp_wait(&sh->q_empty, (seg_n - 1) & 1, sh, p.status)) return;
-          if (elect_one()) {
-            sh->q_loads = seg_n + 1;
-            mbar_expect_tx(smem_u32(&sh->q_full), nq * (D / 64) * 128u * G * a.q_box);
-            for (int q = 0; q < nq; ++q)
-#pragma unroll
-              for (int b = 0; b < D / 64; ++b)
-                tma_load_4d(sq + q * C::kQTile + b * 16384, &mq, smem_u32(&sh->q_full), b * 64, 0, hkv,
-                            t0 + q * a.TQ);
+      Ring ring;
+      uint32_t filled = 0;  // units so far
+      int nseg = 0, loads = 0, asked = 0;
+      bool more = true;     // the tile form's grid may have an item left
+      uint32_t bx = blockIdx.x, by = blockIdx.y;
+      for (;;) {
+        // The next range, into g.
+        Seg g;
+        g.s = -1;
+        if constexpr (STREAM) {
+          if (!iter.next(p, g)) g.s = -1;
+        } else {
+          while (more) {
+            const int id = (int)(gridDim.x / p.Hkv) - 1 - (int)(bx / p.Hkv);
+            const SeqTile t = find_tile(p, id, NQ * a.TQ);
+            if (t.bad && lane == 0) atomicOr(p.status, kStatusBadSeqlens);
+            if (t.nt > 0) {
+              g.s = t.s;
+              g.hkv = bx % p.Hkv;
+              g.t0 = t.t0;
+              g.nt = t.nt;
+              g.pos0 = t.pos0;
+              g.hi = max(0, t.pos0 + t.nt);
+              const int n = (g.hi + BK - 1) / BK;
+              g.kt0 = (int)((int64_t)n * by / a.splits);
+              g.kt1 = (int)((int64_t)n * (by + 1) / a.splits);
+              g.slot = a.splits > 1 ? ((int64_t)id * p.Hkv + g.hkv) * a.splits + by : -1;
+            }
+            // The item after this one is asked for now and taken when this one's
+            // loads have been issued.
+            if (asked > 0) fence_proxy_async();
+            __syncwarp();
+            if (elect_one()) {
+              sh->clc_asked = asked + 1;
+              clc_ask(sh);
+            }
+            ++asked;
+            if (g.s >= 0) break;
+            if (!warp_wait(&sh->clc_full, (asked - 1) & 1, sh, p.status)) return;
+            more = uni((int)clc_answer(sh, bx, by));
           }
-          ++seg_n;
         }
-        // Loads of 64 dims x pb keys; those past the last visible key are left out.
-        constexpr int NB = DU / 64;
-        const CUtensorMap* map = is_k ? &mk : &mv;
-        const int per_tile = BK / a.pb;
+        {
+          const int i = nseg & 1;
+          if (nseg >= 2)
+            if (!warp_wait(&sh->seg_empty[i], ((nseg >> 1) - 1) & 1, sh, p.status)) return;
+          if (lane == 0) {
+            sh->seg[i] = g;
+            mbar_arrive(smem_u32(&sh->seg_full[i]));
+          }
+          __syncwarp();
+          ++nseg;
+        }
+        if (g.s < 0) return;
+        const int kt0 = uni(g.kt0), n = uni(g.kt1) - kt0, hi = uni(g.hi), hkv = uni(g.hkv);
+        const int per_tile = BK / a.pbk;
         const int row0 = PAGED ? 0 : uni(cu_at(p.cu, g.s));
-        // Lane i looks up the page of, and issues, the tile's i-th load: 64 dims of a
-        // group of pb keys.  (A loop over the loads with one elected lane was slower:
-        // 461 against 380 us for drafts over pages of 16 rows.)
-        const int grp = lane / NB, blk = lane % NB;
+        // Lane i looks up the page of, and issues, the i-th group of pbk keys.  (A
+        // loop over the groups with one elected lane was slower: 461 against
+        // 380 us for drafts over pages of 16 rows.)
         auto find_page = [&](int kt) -> int {
-          const int jb = kt * BK + grp * a.pb;
-          if (!PAGED || grp >= per_tile || kt >= kt0 + n || jb >= hi) return 0;
+          const int jb = kt * BK + lane * a.pbk;
+          if (!PAGED || lane >= per_tile || kt >= kt0 + n || jb >= hi) return 0;
           const int64_t pg = page_of(p, g.s, jb / p.page_size);
-          if (pg < 0 && is_k) atomicOr(p.status, kStatusBadIndex);
+          if (pg < 0) atomicOr(p.status, kStatusBadIndex);
           return pg < 0 ? (int)p.num_pages : (int)pg;  // past the end: reads as zeros
         };
         int next_page = find_page(kt0);
@@ -427,180 +474,240 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           const int j0 = (kt0 + j) * BK;
           const int page = next_page;
           next_page = find_page(kt0 + j + 1);  // its latency passes during this tile's waits
-          const int groups = min(per_tile, (hi - j0 + a.pb - 1) / a.pb);
-          const uint32_t at = base + NU * (j + (is_k ? max(0, j - A + 1) : min(n, j + A)));
+          const int groups = min(per_tile, (hi - j0 + a.pbk - 1) / a.pbk);
 #pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            const uint32_t it = at + u, st = it % ST;
-            if (it >= (uint32_t)ST)
-              if (!warp_wait(&sh->empty[st], (it / ST - 1) & 1, sh, p.status)) return;
-            const uint32_t full = smem_u32(&sh->full[st]);
-            const uint32_t dst = skv + st * C::kUnit;
+          for (int u = 0; u < NU; ++u, ring.step(), ++filled) {
+            if (filled >= ST)
+              if (!warp_wait(&sh->k_empty[ring.st], ring.round ^ 1, sh, p.status)) return;
+            const uint32_t full = smem_u32(&sh->k_full[ring.st]), dst = sk + ring.st * C::kUnit;
             if (elect_one()) {
-              sh->loads[st] = it / ST + 1;
-              mbar_expect_tx(full, groups * NB * a.pb * 128u);
+              ++sh->k_loads[ring.st];
+              mbar_expect_tx(full, groups * a.pbk * 128u);
+              if constexpr (!PAGED) tma_load_3d(dst, &mk, full, u * 64, row0 + j0, hkv);
             }
             if constexpr (PAGED) {
               __syncwarp();
-              if (grp < groups)
-                tma_load_4d(dst + blk * 16384 + grp * a.pb * 128, map, full, u * DU + blk * 64,
-                            (j0 + grp * a.pb) % p.page_size, hkv, page);
+              if (lane < groups)
+                tma_load_4d(dst + lane * a.pbk * 128, &mk, full, u * 64,
+                            (j0 + lane * a.pbk) % p.page_size, hkv, page);
               __syncwarp();
-            } else {
-              if (elect_one()) {
+            }
+          }
+          if (j == 0) {  // Q, once the last range's scores are done
+            const int nq = uni((NQ == 2 && g.nt > a.TQ) ? 2 : 1), t0 = uni(g.t0);
+            if (loads > 0)
+              if (!warp_wait(&sh->q_empty, (loads - 1) & 1, sh, p.status)) return;
+            ++loads;
+            if (elect_one()) {
+              sh->q_loads = loads;
+              mbar_expect_tx(smem_u32(&sh->q_full), nq * NU * 128u * G * a.q_box);
+              for (int q = 0; q < nq; ++q)
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                  tma_load_3d(dst + b * 16384, map, full, u * DU + b * 64, row0 + j0, hkv);
-              }
+                for (int b = 0; b < NU; ++b)
+                  tma_load_4d(sq + q * C::kQTile + b * 16384, &mq, smem_u32(&sh->q_full), b * 64, 0, hkv,
+                              t0 + q * a.TQ);
             }
           }
         }
-        base += 2 * n * NU;
+        if constexpr (!STREAM) {
+          if (!warp_wait(&sh->clc_full, (asked - 1) & 1, sh, p.status)) return;
+          more = uni((int)clc_answer(sh, bx, by));
+        }
       }
     };
     role();
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 2) {
     // ---- MMAs ----
     constexpr uint32_t kIdQK = idesc_bf16_f32(128, BK, false, false);
-    constexpr uint32_t kIdPV = idesc_bf16_f32(128, DU, false, true);
-    auto role = [&] {
-      uint32_t nk = 0;  // key tiles done (one-tile form: S buffer and its phases)
-      uint32_t st = 0, round = 0;  // place of the next unit, parity of its round
-      int seg_n = 0, fixes = 0;
-      Seg g;
-      auto wait = [&](uint64_t& bar, uint32_t parity) { return warp_wait(&bar, parity, sh, p.status); };
-      // The next unit has landed; its place in at.
-      auto take1 = [&](uint32_t& at) -> bool {
-        at = st;
-        if (!wait(sh->full[st], round)) return false;
-        if (++st == ST) {
-          st = 0;
-          round ^= 1;
-        }
+    constexpr uint32_t kIdPV = idesc_bf16_f32(128, VD, false, true);
+    const int q = NQ == 2 ? warp - 1 : 0;  // row tile
+    Ring kr, vr;
+    auto wait = [&](uint64_t& bar, uint32_t parity) { return warp_wait(&bar, parity, sh, p.status); };
+    // S[buf] = Q[q] K^T, unit by unit; idle: only pass the units on.
+    auto qk = [&](uint32_t buf, bool idle) -> bool {
+#pragma unroll
+      for (int u = 0; u < NU; ++u, kr.step()) {
+        if (!wait(sh->k_full[kr.st], kr.round)) return false;
         fence_after_sync();
-        return true;
-      };
-      // One unit's MMAs, 8 at most: the pipe has about 280 cycles of work queued
-      // when they have been issued, so that one wait between two such blocks is
-      // hidden, and the waits below are spread accordingly.  `done`, if any, is
-      // arrived on when all MMAs so far are complete, and so is the unit's place
-      // if it is not needed again.
-      // S[buf] (+)= Q[q] K^T over the dims of unit u.
-      auto qk = [&](int q, uint32_t buf, int u, uint32_t at, bool last_use, uint64_t* done) {
         if (elect_one()) {
-          const uint64_t kd = desc_sw128(skv + at * C::kUnit, 16, 1024);
-          const uint64_t qd = desc_sw128(sq + q * C::kQTile + u * (DU / 64) * 16384, 16, 1024);
+          if (!idle) {
+            const uint64_t kd = desc_sw128(sk + kr.st * C::kUnit, 16, 1024);
+            const uint64_t qd = desc_sw128(sq + q * C::kQTile + u * 16384, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < DU / 16; ++k) {
-            const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-            mma_bf16(buf * 128, qd + off, kd + off, kIdQK, u + k > 0);
+            for (int k = 0; k < 4; ++k) mma_bf16(buf * 128, qd + k * 2, kd + k * 2, kIdQK, u + k > 0);
           }
-          if (last_use) mma_commit(smem_u32(&sh->empty[at]));
-          if (done) mma_commit(smem_u32(done));
+          mma_commit(smem_u32(&sh->k_empty[kr.st]));
+          if (u == NU - 1 && !idle) mma_commit(smem_u32(&sh->s_full[buf]));
         }
-      };
-      // O[q] (+)= P[buf] V over the dims of unit u.
-      auto pv = [&](int q, uint32_t buf, int u, uint32_t at, bool acc, bool last_use, uint64_t* done) {
+      }
+      return true;
+    };
+    // O[q] (+)= P[buf] V, unit by unit (keys outermost); then `done` arrives.
+    auto pv = [&](uint32_t buf, bool acc, bool idle, uint64_t* done) -> bool {
+#pragma unroll
+      for (int u = 0; u < NU; ++u, vr.step()) {
+        constexpr int ND = D / VD;       // units side by side in the dims
+        const int kh = u / ND, db = u % ND;
+        if (!wait(sh->v_full[vr.st], vr.round)) return false;
+        fence_after_sync();
         if (elect_one()) {
-          const uint64_t vd = desc_sw128(skv + at * C::kUnit, 16384, 1024);
+          if (!idle) {
+            const uint64_t vd = desc_sw128(sv + vr.st * C::kUnit, VK * 128, 1024);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            mma_bf16_ta(kTO + q * 128 + u * DU, buf * 128 + (k >> 2) * 64 + (k & 3) * 8, vd + ((k * 2048) >> 4), kIdPV,
-                        acc || k > 0);
-          if (last_use) mma_commit(smem_u32(&sh->empty[at]));
-          if (done) mma_commit(smem_u32(done));
+            for (int k = 0; k < VK / 16; ++k) {
+              const int ks = kh * (VK / 16) + k;  // step of 16 keys in the tile
+              mma_bf16_ta(kTO + q * 128 + db * VD, buf * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
+                          vd + ((k * 2048) >> 4), kIdPV, acc || ks > 0);
+            }
+          }
+          mma_commit(smem_u32(&sh->v_empty[vr.st]));
+          if (u == NU - 1 && !idle) mma_commit(smem_u32(done));
         }
-      };
-      auto ask_fix = [&](const uint32_t(&at)[NU]) {  // V's units have landed: clear their tail
-        if (lane == 0) {
-#pragma unroll
-          for (int u = 0; u < NU; ++u) sh->v_at[u] = at[u];
-          mbar_arrive(smem_u32(&sh->v_landed));
-        }
-        __syncwarp();
-      };
+      }
+      return true;
+    };
+    auto role = [&] {
+      uint32_t nk = 0;  // key tiles before this range
+      int nseg = 0, nact = 0;  // ranges, of them with rows of tile q
+      Seg g;
       while (next_seg(g)) {
         const int n = uni(g.kt1 - g.kt0);
-        const int nq = uni((NQ == 2 && g.nt > a.TQ) ? 2 : 1);
-        const bool partial = uni((int)(g.kt1 * BK > g.hi));  // the last tile ends inside
-        if (!wait(sh->q_full, seg_n & 1)) return;
-        fence_after_sync();
-        uint32_t ak[NU], av[NU];
+        if (n == 0) continue;
         if constexpr (NQ == 2) {
-          // NU = 1.  PV 0 | QK 0 | PV 1 | QK 1, a wait before each.
-          if (!take1(ak[0])) return;
-          for (int q = 0; q < nq; ++q) qk(q, q, 0, ak[0], q == nq - 1, &sh->s_full[q]);
-          if (!take1(av[0])) return;
-          for (int j = 0; j < n; ++j) {
-            const bool more = j + 1 < n;
-            if (!more && partial) ask_fix(av);
-            uint32_t next_v = 0;
-            for (int q = 0; q < nq; ++q) {
-              if (!wait(sh->p_full[q], j & 1)) return;
-              if (!more && partial && q == 0)
-                if (!wait(sh->v_fixed, fixes++ & 1)) return;
-              fence_after_sync();
-              pv(q, q, 0, av[0], j > 0, q == nq - 1, more ? nullptr : &sh->o_full[q]);
-              if (more) {
-                if (q == 0)
-                  if (!take1(ak[0])) return;
-                if (q == nq - 1)
-                  if (!take1(next_v)) return;
-                qk(q, q, 0, ak[0], q == nq - 1, &sh->s_full[q]);
-              }
-            }
-            av[0] = next_v;
-          }
-        } else {
-          // PV j | QK j+2, unit by unit; K j+2 and V j+1 are waited for on the way.
-          for (int j = 0; j < min(n, 2); ++j)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-              if (!take1(ak[u])) return;
-              qk(0, (nk + j) & 1, u, ak[u], true, u == NU - 1 ? &sh->s_full[(nk + j) & 1] : nullptr);
-            }
-#pragma unroll
-          for (int u = 0; u < NU; ++u)
-            if (!take1(av[u])) return;
-          for (int j = 0; j < n; ++j, ++nk) {
-            const uint32_t buf = nk & 1;
-            const bool more_v = j + 1 < n, more_k = j + 2 < n;
-            if (!more_v && partial) ask_fix(av);
-            if (j == 0 && seg_n > 0)  // the last range's O has been read
-              if (!wait(sh->o_empty, (seg_n - 1) & 1)) return;
-            if (!wait(sh->p_full[buf], (nk >> 1) & 1)) return;
-            if (!more_v && partial)
-              if (!wait(sh->v_fixed, fixes++ & 1)) return;
+          const bool idle = uni((int)(q == 1 && g.nt <= a.TQ));
+          if (!wait(sh->q_full, nseg & 1)) return;
+          fence_after_sync();
+          if (!qk(q, idle)) return;
+          for (int j = 0; j < n; ++j, nk += idle ? 0 : 1) {
+            if (!idle)
+              if (!wait(sh->p_full[q], nk & 1)) return;
+            if (j == 0 && nact > 0 && !idle)  // the last range's O has been read
+              if (!wait(sh->o_empty[q], (nact - 1) & 1)) return;
             fence_after_sync();
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-              pv(0, buf, u, av[u], j > 0, true, u == NU - 1 ? &sh->pv : nullptr);
-              if (more_k)
-                if (!take1(ak[u])) return;
-            }
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-              if (more_k) qk(0, buf, u, ak[u], true, u == NU - 1 ? &sh->s_full[buf] : nullptr);
-              if (more_v)
-                if (!take1(av[u])) return;
-            }
+            if (!pv(q, j > 0, idle, j == n - 1 ? &sh->o_full[q] : &sh->pv[q])) return;
+            if (j + 1 < n)
+              if (!qk(q, idle)) return;
           }
-          if (elect_one()) mma_commit(smem_u32(&sh->o_full[0]));
+          if (elect_one()) mma_commit(smem_u32(&sh->q_empty));
+          nact += idle ? 0 : 1;
+        } else if (warp == 1) {
+          if (!wait(sh->q_full, nseg & 1)) return;
+          fence_after_sync();
+          for (int j = 0; j < n; ++j, ++nk) {
+            if (nk >= 2)  // P V has read the buffer's last P
+              if (!wait(sh->pv[nk & 1], ((nk >> 1) - 1) & 1)) return;
+            fence_after_sync();
+            if (!qk(nk & 1, false)) return;
+          }
+          if (elect_one()) mma_commit(smem_u32(&sh->q_empty));
+        } else {
+          for (int j = 0; j < n; ++j, ++nk) {
+            if (!wait(sh->p_full[nk & 1], (nk >> 1) & 1)) return;
+            if (j == 0 && nseg > 0)
+              if (!wait(sh->o_empty[0], (nseg - 1) & 1)) return;
+            fence_after_sync();
+            if (!pv(nk & 1, j > 0, false, &sh->pv[nk & 1])) return;
+            if (j == n - 1 && elect_one()) mma_commit(smem_u32(&sh->o_full[0]));
+          }
         }
-        if (elect_one()) mma_commit(smem_u32(&sh->q_empty));
-        ++seg_n;
+        ++nseg;
       }
     };
     role();
-    if (elect_one()) mma_commit(smem_u32(&sh->end));
-    warp_wait(&sh->end, 0, sh, p.status);
-  } else if (warp == 2) {
+    __syncwarp();
+    if (elect_one()) mma_commit(smem_u32(&sh->end[warp - 1]));
+    mbar_wait(smem_u32(&sh->end[warp - 1]), 0, kWaitBudget);
+  } else if (warp == 3) {
+    // ---- loads of V ----
+    auto role = [&] {
+      Ring ring;
+      uint32_t filled = 0, tails = 0;
+      Seg g;
+      while (next_seg(g)) {
+        const int kt0 = uni(g.kt0), n = uni(g.kt1) - kt0, hi = uni(g.hi), hkv = uni(g.hkv);
+        const int row0 = PAGED ? 0 : uni(cu_at(p.cu, g.s));
+        constexpr int NB = VD / 64;
+        const int per_unit = VK / a.pbv, per_tile = BK / a.pbv;
+        const int grp = lane / NB, blk = lane % NB;  // this lane's load of a unit
+        auto find_page = [&](int kt) -> int {  // lane i: of the tile's i-th group of pbv keys
+          const int jb = kt * BK + lane * a.pbv;
+          if (!PAGED || lane >= per_tile || kt >= kt0 + n || jb >= hi) return 0;
+          const int64_t pg = page_of(p, g.s, jb / p.page_size);
+          return pg < 0 ? (int)p.num_pages : (int)pg;
+        };
+        int next_page = find_page(kt0);
+        for (int j = 0; j < n; ++j) {
+          const int j0 = (kt0 + j) * BK;
+          const int pages = next_page;
+          next_page = find_page(kt0 + j + 1);
+          const int r0 = hi - j0;  // the first row past the last visible key, if below 128
+          const bool tail = r0 < BK;
+          Ring first = ring;
+#pragma unroll
+          for (int u = 0; u < NU; ++u, ring.step(), ++filled) {
+            constexpr int ND = D / VD;
+            const int kh = u / ND, db = u % ND;
+            if (filled >= ST)
+              if (!warp_wait(&sh->v_empty[ring.st], ring.round ^ 1, sh, p.status)) return;
+            // A tile with a tail lands on a barrier of its own and is passed on below.
+            const uint32_t full = smem_u32(tail ? &sh->v_land : &sh->v_full[ring.st]);
+            const uint32_t dst = sv + ring.st * C::kUnit;
+            // Loads of groups with a visible key; none for a unit past the last one.
+            const int groups = max(0, min(per_unit, (r0 - kh * VK + a.pbv - 1) / a.pbv));
+            if (elect_one()) {
+              if (!tail) ++sh->v_loads[ring.st];
+              else if (u == NU - 1) sh->land_asked = tails + 1;
+              mbar_expect_tx(full, groups * NB * a.pbv * 128u);
+              if constexpr (!PAGED) {
+                if (groups > 0)
+#pragma unroll
+                  for (int b = 0; b < NB; ++b)
+                    tma_load_3d(dst + b * VK * 128, &mv, full, db * VD + b * 64, row0 + j0 + kh * VK,
+                                hkv);
+              }
+            }
+            if constexpr (PAGED) {
+              const int page = __shfl_sync(0xffffffffu, pages, (kh * per_unit + grp) & 31);
+              if (grp < groups)
+                tma_load_4d(dst + blk * VK * 128 + grp * a.pbv * 128, &mv, full, db * VD + blk * 64,
+                            (j0 + kh * VK + grp * a.pbv) % p.page_size, hkv, page);
+              __syncwarp();
+            }
+          }
+          if (tail) {
+            if (!warp_wait(&sh->v_land, tails++ & 1, sh, p.status)) return;
+            // Whole 128-byte rows: the swizzle permutes inside a row only.
+            Ring at = first;
+#pragma unroll
+            for (int u = 0; u < NU; ++u, at.step()) {
+              constexpr int ND = D / VD;
+              const int c0 = max(0, r0 - (u / ND) * VK);  // first row of the unit to clear
+              unsigned char* v = smem + C::kQ + (ST + at.st) * C::kUnit;
+              for (int i = lane; i < (VK - c0) * (VD / 8); i += 32) {
+                const int r = c0 + i / (VD / 8), ch = i % (VD / 8);
+                *reinterpret_cast<uint4*>(v + (ch >> 3) * (VK * 128) + r * 128 + (ch & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+            fence_proxy_async();
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < NU; ++u, first.step())
+              if (elect_one()) {
+                ++sh->v_loads[first.st];
+                mbar_arrive(smem_u32(&sh->v_full[first.st]));
+              }
+          }
+        }
+      }
+    };
+    role();
     if constexpr (STREAM) {
       // What the joining kernel needs of this CTA's ranges; the outputs of
       // sequences without a key.
       if (lane == 0) {
         int4 r = make_int4(-1, 0, 2, 0);
-        SegIter every = iter;
+        SegIter every{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
         Seg g;
         for (bool first = true; every.next(p, g); first = false) {
           const int n = key_tiles(seq_range(p, g.s));
@@ -620,30 +727,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           for (int h = 0; h < p.Hq; ++h) finish_row<bf16, D>(p, t, h, lane, zero, -INFINITY, 0.0f);
       }
     }
-    // ---- V's rows past the last visible key ----
-    auto role = [&] {
-      int fixes = 0;
-      Seg g;
-      while (next_seg(g)) {
-        if (g.kt1 * BK <= g.hi) continue;
-        WAIT(sh->v_landed, fixes & 1);
-        ++fixes;
-        const int r0 = g.hi - (g.kt1 - 1) * BK;  // first row to clear
-        for (int u = 0; u < NU; ++u) {
-          unsigned char* v = smem + C::kQ + sh->v_at[u] * C::kUnit;
-          // Whole 128-byte rows: the swizzle permutes inside a row only.
-          for (int i = lane; i < (BK - r0) * (DU / 8); i += 32) {
-            const int r = r0 + i / (DU / 8), ch = i % (DU / 8);
-            *reinterpret_cast<uint4*>(v + (ch >> 3) * 16384 + r * 128 + (ch & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh->v_fixed));
-      }
-    };
-    role();
   } else {
     // ---- softmax, output ----
     // Two warps share 32 rows: `half` is the half of the keys of a tile, and of
@@ -674,7 +757,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     int seg_n = 0;
     Seg g;
     while (next_seg(g)) {
-      if (NQ == 2 && qt == 1 && g.nt <= a.TQ) break;   // no second row tile
+      if (NQ == 2 && qt == 1 && g.nt <= a.TQ) continue;   // no second row tile
+      if (g.kt0 == g.kt1) {  // no key for any row
+        const Partials part(a.ws, (int64_t)gridDim.x * a.splits, a.rows, D);
+        const float zero[D / 32] = {};
+        const int rows = (min(g.nt, (qt + 1) * a.TQ) - qt * a.TQ) * G;
+        for (int i = (warp - 4) & 7; i < rows; i += 8) {
+          const int pr = qt * a.TQ * G + i, t = g.t0 + pr / G, h = g.hkv * G + pr % G;
+          if (g.slot >= 0) part.put<D / 32>(g.slot, pr, lane, zero, -INFINITY, 0.0f);
+          else finish_row<bf16, D>(p, t, h, lane, zero, -INFINITY, 0.0f);
+        }
+        continue;
+      }
       const bool valid = r < a.TQ * G && tok < g.nt;
       // The row's last visible key; rows that do not exist see all (their
       // values are not used) so that they cost no masking.
@@ -691,41 +785,46 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       const uint32_t to = tmem + lanes + kTO + qt * 128 + half * (D / 2);
       for (int kt = g.kt0; kt < g.kt1; ++kt, ++nk) {
         const int buf = NQ == 2 ? qt : (int)(nk & 1);
-        const uint32_t ph = NQ == 2 ? (uint32_t)(kt - g.kt0) & 1 : (nk >> 1) & 1;
+        const uint32_t ph = NQ == 2 ? nk & 1 : (nk >> 1) & 1;
         const int jj = kt - g.kt0;
         WAIT(sh->s_full[buf], ph);
         fence_after_sync();
         if (!idle) {
           const uint32_t ts = tmem + lanes + buf * 128;
-          float s[2][32];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) tmem_ld32(ts + half * 64 + i * 32, s[i]);
-          tmem_ld_wait();
-          const int j0 = kt * BK + half * 64;
-          if (__any_sync(0xffffffffu, j0 + 63 > last)) {
-            const int lim = last - j0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) s[i][e] = i * 32 + e <= lim ? s[i][e] : -INFINITY;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const int lim = last - kt * BK - half * 64;  // the row's last visible column
+          const bool masked = __any_sync(0xffffffffu, lim < 63);
+          float mx[2] = {-INFINITY, -INFINITY};
           auto publish = [&] {
-            const float t = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float t = fmaxf(mx[0], mx[1]);
             top_bits = __float_as_uint(t) >> 16;  // cut to bf16: only the agreement matters
             sh->swap.top[jj & 1][qt][half][r] = (uint16_t)top_bits;
             pair_arrive();
           };
+          // Columns 16 c .. 16 c + 15 of this half, masked, into the maximum.
+          auto column_max = [&](float(&x)[16], int c16) {
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = c16 * 16 + e <= lim ? x[e] : -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              mx[0] = fmaxf(mx[0], fmaxf(x[e], x[e + 1]));
+              mx[1] = fmaxf(mx[1], fmaxf(x[e + 2], x[e + 3]));
+            }
+          };
           if (jj == 0) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mx[k] = fmaxf(mx[k], fmaxf(s[i][e + 2 * k], s[i][e + 2 * k + 1]));
+            for (int i = 0; i < 4; ++i) {
+              float x[16];
+              tmem_ld16(ts + half * 64 + i * 16, x);
+              tmem_ld_wait();
+              column_max(x, i);
+            }
             publish();
           }
+          // In flight during the exchange.
+          float x[2][16];
+          tmem_ld16(ts + half * 64, x[0]);
           if (jj != 1) {
             if (!pair_wait()) return;
             const int slot = jj == 0 ? 0 : (jj - 1) & 1;
@@ -746,7 +845,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               // O is at rest: in the two-tile form S j follows P V j-1, in the
               // other that product is waited for.
               if constexpr (NQ == 1) {
-                WAIT(sh->pv, (nk - 1) & 1);
+                WAIT(sh->pv[(nk - 1) & 1], ((nk - 1) >> 1) & 1);
                 fence_after_sync();
               }
               l *= f;
@@ -764,24 +863,27 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           }
           const float ref = -m;
           float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
+          // 16 columns at a time, the next 16 on their way; P's 8 columns go where
+          // this half's scores were read before.
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float(&x)[32] = s[i];
-            float pk[16];
+          for (int i = 0; i < 4; ++i) {
+            tmem_ld_wait();
+            if (i + 1 < 4) tmem_ld16(ts + half * 64 + (i + 1) * 16, x[(i + 1) & 1]);
+            float(&y)[16] = x[i & 1];
+            column_max(y, i);
+            uint32_t pk[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              mx[(e >> 1) & 2] = fmaxf(mx[(e >> 1) & 2], fmaxf(x[e], x[e + 1]));
-              mx[((e >> 1) & 2) + 1] = fmaxf(mx[((e >> 1) & 2) + 1], fmaxf(x[e + 2], x[e + 3]));
-              fma2(x[e], x[e + 1], c, ref);
-              fma2(x[e + 2], x[e + 3], c, ref);
+            for (int e = 0; e < 16; e += 4) {
+              fma2(y[e], y[e + 1], c, ref);
+              fma2(y[e + 2], y[e + 3], c, ref);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) x[e + k] = ex2(x[e + k]);
-              add2(l0, l1, x[e], x[e + 1]);
-              add2(l2, l3, x[e + 2], x[e + 3]);
-              pk[e / 2] = __uint_as_float(pack_bf16(x[e], x[e + 1]));
-              pk[e / 2 + 1] = __uint_as_float(pack_bf16(x[e + 2], x[e + 3]));
+              for (int k = 0; k < 4; ++k) y[e + k] = ex2(y[e + k]);
+              add2(l0, l1, y[e], y[e + 1]);
+              add2(l2, l3, y[e + 2], y[e + 3]);
+              pk[e / 2] = pack_bf16(y[e], y[e + 1]);
+              pk[e / 2 + 1] = pack_bf16(y[e + 2], y[e + 3]);
             }
-            tmem_st16(ts + half * 64 + i * 16, pk);
+            tmem_st8u(ts + half * 64 + i * 8, pk);
           }
           tmem_st_wait();
           fence_before_sync();
@@ -892,11 +994,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         }
       }
       ++seg_n;
-      if constexpr (STREAM) {
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh->o_empty));
-      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh->o_empty[qt]));
     }
     };
     role();
@@ -908,9 +1008,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     // A wait gave up: copies may still be in flight (otherwise the MMA role has
     // waited for each).  They land before the CTA's memory is given up.
     if (tid == 0) {
-      for (int i = 0; i < ST; ++i)
-        if (sh->loads[i]) mbar_wait(smem_u32(&sh->full[i]), (sh->loads[i] - 1) & 1, kWaitBudget);
+      for (int i = 0; i < ST; ++i) {
+        if (sh->k_loads[i]) mbar_wait(smem_u32(&sh->k_full[i]), (sh->k_loads[i] - 1) & 1, kWaitBudget);
+        if (sh->v_loads[i]) mbar_wait(smem_u32(&sh->v_full[i]), (sh->v_loads[i] - 1) & 1, kWaitBudget);
+      }
+      if (sh->land_asked) mbar_wait(smem_u32(&sh->v_land), (sh->land_asked - 1) & 1, kWaitBudget);
       if (sh->q_loads) mbar_wait(smem_u32(&sh->q_full), (sh->q_loads - 1) & 1, kWaitBudget);
+      if (sh->clc_asked) mbar_wait(smem_u32(&sh->clc_full), (sh->clc_asked - 1) & 1, kWaitBudget);
     }
     __syncthreads();
   }
@@ -1011,10 +1115,10 @@ bool q_map(CUtensorMap* m, const AttnLaunch& p, int q_box) {
   const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)q_box};
   return encode(m, p.q.p, 4, dims, st, box);
 }
-bool rows_map(CUtensorMap* m, const AttnRows& r, const AttnLaunch& p) {
+bool rows_map(CUtensorMap* m, const AttnRows& r, const AttnLaunch& p, int rows) {
   const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.T, (cuuint64_t)p.Hkv};
   const int64_t st[2] = {r.ts, r.hs};
-  const cuuint32_t box[3] = {64, (cuuint32_t)BK, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
   return encode(m, r.p, 3, dims, st, box);
 }
 bool pages_map(CUtensorMap* m, const AttnPages& c, const AttnLaunch& p, int pb) {
@@ -1043,8 +1147,8 @@ template <int D, int NQ, bool PAGED, bool STREAM>
 cudaError_t run(const AttnLaunch& p, TcArgs a, dim3 grid, cudaStream_t st) {
   using C = Cfg<D, NQ>;
   CUtensorMap mq, mk, mv;
-  if (!q_map(&mq, p, a.q_box) || !(PAGED ? pages_map(&mk, p.kc, p, a.pb) : rows_map(&mk, p.k, p)) ||
-      !(PAGED ? pages_map(&mv, p.vc, p, a.pb) : rows_map(&mv, p.v, p)))
+  if (!q_map(&mq, p, a.q_box) || !(PAGED ? pages_map(&mk, p.kc, p, a.pbk) : rows_map(&mk, p.k, p, a.pbk)) ||
+      !(PAGED ? pages_map(&mv, p.vc, p, a.pbv) : rows_map(&mv, p.v, p, a.pbv)))
     return cudaErrorInvalidValue;
   static const cudaError_t attr =
       cudaFuncSetAttribute(attn_tc_kernel<D, NQ, PAGED, STREAM>,
@@ -1062,9 +1166,10 @@ cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
   TcArgs a{};
   a.TQ = 128 / G;
   a.splits = 1;
-  a.pb = BK;
+  a.pbk = BK;
   if (p.table != nullptr)
-    while (p.page_size % a.pb != 0) a.pb >>= 1;
+    while (p.page_size % a.pbk != 0) a.pbk >>= 1;
+  a.pbv = std::min(a.pbk, Cfg<D, NQ>::VK);
   if (p.table != nullptr && use_stream(p.max_q, G)) {
     a.q_box = std::min(a.TQ, p.max_q);
     a.ctas = sms;
