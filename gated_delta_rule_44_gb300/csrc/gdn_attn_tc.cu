@@ -16,10 +16,11 @@
 // (2^-9 relative) is the same for any reference.  l sums P before the rounding.
 //
 // Warps:  0       hands out the work; TMA loads of Q and K
-//         1, 2    the MMAs: two-tile form, a row tile each; one-tile form, Q K^T and
-//                 P V.  Issuing an MMA takes its warp as long as the pipe works on
-//                 it (64 cycles), so a wait by a lone issuer is a hole in the pipe
-//                 (3000 cycles for each 2048 of MMAs); here the other warp fills it
+//         1, 2    the MMAs: two-tile form, a row tile each, in turns; one-tile form,
+//                 Q K^T and P V.  Issuing an MMA takes its warp as long as the pipe
+//                 works on it (64 cycles), so that whatever a lone issuer does between
+//                 two is a hole in the pipe; here the other warp fills it.  Without
+//                 turns two row tiles fall into step and wait for their P together
 //         3       TMA loads of V; clears the rows of V past the last visible key (a
 //                 stale or foreign NaN there would survive a weight of 0); the
 //                 stream form's bookkeeping
@@ -84,7 +85,7 @@ struct Seg {
 
 struct Shared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv[2], o_full[2], o_empty[2], v_land, end[2];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], p_rest[2], turn[2], pv[2], o_full[2], o_empty[2], v_land, end[2];
   uint64_t pair[2][4];
   uint64_t seg_full[2], seg_empty[2], clc_full;
   alignas(16) uint4 clc;  // the next item's answer
@@ -96,9 +97,9 @@ struct Shared {
   long long left;
   long long scan[20];
   union {  // what the two warps of 32 rows exchange
-    uint16_t top[2][2][2][128];  // [tile & 1][row tile][half][row]: maxima, as bf16
-    float val[2][2][128];        // [row tile][half][row]
-  } swap;
+    uint16_t top[2][2][128];  // [key tile & 1][half][row]: maxima, as bf16
+    float val[2][128];        // [half][row]
+  } swap[2];                  // of a row tile
 };
 
 template <int D, int NQ>
@@ -306,6 +307,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&sh->s_full[i]), 1);
         mbar_init(smem_u32(&sh->p_full[i]), 8);
+        mbar_init(smem_u32(&sh->p_rest[i]), 8);
+        mbar_init(smem_u32(&sh->turn[i]), 1);
         mbar_init(smem_u32(&sh->pv[i]), 1);
         mbar_init(smem_u32(&sh->o_full[i]), 1);
         mbar_init(smem_u32(&sh->o_empty[i]), 8);
@@ -520,94 +523,144 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     // ---- MMAs ----
     constexpr uint32_t kIdQK = idesc_bf16_f32(128, BK, false, false);
     constexpr uint32_t kIdPV = idesc_bf16_f32(128, VD, false, true);
-    const int q = NQ == 2 ? warp - 1 : 0;  // row tile
+    // Two-tile form: this warp's row tile; the warps take turns, and wait for what
+    // a turn needs before it.  One-tile form: warp 1 has the scores, warp 2 P V.
+    const int me = warp - 1, q = NQ == 2 ? me : 0;
     Ring kr, vr;
+    int turns = 0;
     auto wait = [&](uint64_t& bar, uint32_t parity) { return warp_wait(&bar, parity, sh, p.status); };
-    // S[buf] = Q[q] K^T, unit by unit; idle: only pass the units on.
-    auto qk = [&](uint32_t buf, bool idle) -> bool {
+    auto take_turn = [&]() -> bool {
+      const int k = turns++ - (me == 0 ? 1 : 0);  // warp 1 begins
+      return k < 0 || wait(sh->turn[me], k & 1);
+    };
+    auto pass_turn = [&] {
+      if (elect_one()) mbar_arrive(smem_u32(&sh->turn[me ^ 1]));
+    };
+    // The next key tile's units of a ring have landed; their places.
+    auto land = [&](Ring& ring, uint64_t* full, uint32_t(&at)[NU]) -> bool {
 #pragma unroll
-      for (int u = 0; u < NU; ++u, kr.step()) {
-        if (!wait(sh->k_full[kr.st], kr.round)) return false;
-        fence_after_sync();
-        if (elect_one()) {
-          if (!idle) {
-            const uint64_t kd = desc_sw128(sk + kr.st * C::kUnit, 16, 1024);
-            const uint64_t qd = desc_sw128(sq + q * C::kQTile + u * 16384, 16, 1024);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_bf16(buf * 128, qd + k * 2, kd + k * 2, kIdQK, u + k > 0);
-          }
-          mma_commit(smem_u32(&sh->k_empty[kr.st]));
-          if (u == NU - 1 && !idle) mma_commit(smem_u32(&sh->s_full[buf]));
-        }
+      for (int u = 0; u < NU; ++u, ring.step()) {
+        at[u] = ring.st;
+        if (!wait(full[ring.st], ring.round)) return false;
       }
       return true;
     };
-    // O[q] (+)= P[buf] V, unit by unit (keys outermost); then `done` arrives.
-    auto pv = [&](uint32_t buf, bool acc, bool idle, uint64_t* done) -> bool {
+    // S[buf] = Q[q] K^T of unit u.
+    auto qk_unit = [&](uint32_t buf, int u, uint32_t at) {
+      if (elect_one()) {
+        const uint64_t kd = desc_sw128(sk + at * C::kUnit, 16, 1024);
+        const uint64_t qd = desc_sw128(sq + q * C::kQTile + u * 16384, 16, 1024);
 #pragma unroll
-      for (int u = 0; u < NU; ++u, vr.step()) {
-        constexpr int ND = D / VD;       // units side by side in the dims
-        const int kh = u / ND, db = u % ND;
-        if (!wait(sh->v_full[vr.st], vr.round)) return false;
+        for (int k = 0; k < 4; ++k) mma_bf16(buf * 128, qd + k * 2, kd + k * 2, kIdQK, u + k > 0);
+        mma_commit(smem_u32(&sh->k_empty[at]));
+        if (u == NU - 1) mma_commit(smem_u32(&sh->s_full[buf]));
+      }
+    };
+    // O[q] (+)= P[buf] V: first the keys whose P comes first (columns 0 .. 31 of
+    // either half of the tile), then the rest; then `done` and `done2` arrive.
+    auto pv = [&](uint32_t buf, uint32_t phase, bool acc, const uint32_t(&at)[NU], uint64_t* done,
+                  uint64_t* done2) -> bool {
+      constexpr int ND = D / VD;  // units side by side in the dims
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        if (part == 1)
+          if (!wait(sh->p_rest[buf], phase)) return false;
         fence_after_sync();
         if (elect_one()) {
-          if (!idle) {
-            const uint64_t vd = desc_sw128(sv + vr.st * C::kUnit, VK * 128, 1024);
 #pragma unroll
-            for (int k = 0; k < VK / 16; ++k) {
-              const int ks = kh * (VK / 16) + k;  // step of 16 keys in the tile
+          for (int db = 0; db < ND; ++db)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int ks = (i >> 1) * 4 + part * 2 + (i & 1);  // step of 16 keys in the tile
+              const int u = (ks / (VK / 16)) * ND + db, k = ks % (VK / 16);
+              const uint64_t vd = desc_sw128(sv + at[u] * C::kUnit, VK * 128, 1024);
               mma_bf16_ta(kTO + q * 128 + db * VD, buf * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
-                          vd + ((k * 2048) >> 4), kIdPV, acc || ks > 0);
+                          vd + ((k * 2048) >> 4), kIdPV, acc || part + i > 0);
             }
+          if (part == 1) {
+#pragma unroll
+            for (int u = 0; u < NU; ++u) mma_commit(smem_u32(&sh->v_empty[at[u]]));
+            if (done) mma_commit(smem_u32(done));
+            if (done2) mma_commit(smem_u32(done2));
           }
-          mma_commit(smem_u32(&sh->v_empty[vr.st]));
-          if (u == NU - 1 && !idle) mma_commit(smem_u32(done));
         }
       }
       return true;
     };
     auto role = [&] {
-      uint32_t nk = 0;  // key tiles before this range
+      uint32_t nk = 0;  // key tiles before this range (of this row tile)
       int nseg = 0, nact = 0;  // ranges, of them with rows of tile q
+      uint32_t ak[NU], av[NU];
       Seg g;
       while (next_seg(g)) {
         const int n = uni(g.kt1 - g.kt0);
         if (n == 0) continue;
         if constexpr (NQ == 2) {
-          const bool idle = uni((int)(q == 1 && g.nt <= a.TQ));
+          const bool idle = uni((int)(q == 1 && g.nt <= a.TQ));  // no row of this tile
           if (!wait(sh->q_full, nseg & 1)) return;
-          fence_after_sync();
-          if (!qk(q, idle)) return;
-          for (int j = 0; j < n; ++j, nk += idle ? 0 : 1) {
-            if (!idle)
-              if (!wait(sh->p_full[q], nk & 1)) return;
-            if (j == 0 && nact > 0 && !idle)  // the last range's O has been read
-              if (!wait(sh->o_empty[q], (nact - 1) & 1)) return;
-            fence_after_sync();
-            if (!pv(q, j > 0, idle, j == n - 1 ? &sh->o_full[q] : &sh->pv[q])) return;
+          // Turn 0: the scores of key tile 0; turn j + 1: P V of tile j and the scores
+          // of tile j + 1.
+          for (int j = -1; j < n; ++j) {
+            if (j >= 0) {
+              if (!idle)
+                if (!wait(sh->p_full[q], nk & 1)) return;
+              if (j == 0 && nact > 0 && !idle)  // the last range's O has been read
+                if (!wait(sh->o_empty[q], (nact - 1) & 1)) return;
+              if (!land(vr, sh->v_full, av)) return;
+            }
             if (j + 1 < n)
-              if (!qk(q, idle)) return;
+              if (!land(kr, sh->k_full, ak)) return;
+            fence_after_sync();
+            if (!take_turn()) return;
+            if (idle) {
+              pass_turn();
+              if (elect_one()) {
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                  if (j >= 0) mbar_arrive(smem_u32(&sh->v_empty[av[u]]));
+                  if (j + 1 < n) mbar_arrive(smem_u32(&sh->k_empty[ak[u]]));
+                }
+              }
+              continue;
+            }
+            if (j >= 0) {
+              if (!pv(q, nk & 1, j > 0, av, j == n - 1 ? &sh->o_full[q] : nullptr, nullptr)) return;
+              ++nk;
+            }
+            if (j + 1 < n) {
+#pragma unroll
+              for (int u = 0; u < NU; ++u) {
+                if (u == NU - 1) pass_turn();
+                qk_unit(q, u, ak[u]);
+              }
+            } else {
+              pass_turn();
+            }
           }
-          if (elect_one()) mma_commit(smem_u32(&sh->q_empty));
           nact += idle ? 0 : 1;
+          if (elect_one()) mma_commit(smem_u32(&sh->q_empty));
         } else if (warp == 1) {
           if (!wait(sh->q_full, nseg & 1)) return;
-          fence_after_sync();
           for (int j = 0; j < n; ++j, ++nk) {
             if (nk >= 2)  // P V has read the buffer's last P
               if (!wait(sh->pv[nk & 1], ((nk >> 1) - 1) & 1)) return;
-            fence_after_sync();
-            if (!qk(nk & 1, false)) return;
+#pragma unroll
+            for (int u = 0; u < NU; ++u, kr.step()) {
+              if (!wait(sh->k_full[kr.st], kr.round)) return;
+              fence_after_sync();
+              qk_unit(nk & 1, u, kr.st);
+            }
           }
           if (elect_one()) mma_commit(smem_u32(&sh->q_empty));
         } else {
           for (int j = 0; j < n; ++j, ++nk) {
-            if (!wait(sh->p_full[nk & 1], (nk >> 1) & 1)) return;
+            if (!land(vr, sh->v_full, av)) return;
             if (j == 0 && nseg > 0)
               if (!wait(sh->o_empty[0], (nseg - 1) & 1)) return;
-            fence_after_sync();
-            if (!pv(nk & 1, j > 0, false, &sh->pv[nk & 1])) return;
-            if (j == n - 1 && elect_one()) mma_commit(smem_u32(&sh->o_full[0]));
+            if (!wait(sh->p_full[nk & 1], (nk >> 1) & 1)) return;
+            if (!pv(nk & 1, (nk >> 1) & 1, j > 0, av, &sh->pv[nk & 1],
+                    j == n - 1 ? &sh->o_full[0] : nullptr))
+              return;
           }
         }
         ++nseg;
@@ -748,10 +801,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     // x becomes the row's value of it from the other warp (between two meetings
     // that keep `val` from being written early).
     auto swap = [&](float& x) -> bool {
-      sh->swap.val[qt][half][r] = x;
+      sh->swap[qt].val[half][r] = x;
       pair_arrive();
       const bool ok = pair_wait();
-      x = sh->swap.val[qt][half ^ 1][r];
+      x = sh->swap[qt].val[half ^ 1][r];
       return ok;
     };
     int seg_n = 0;
@@ -797,7 +850,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           auto publish = [&] {
             const float t = fmaxf(mx[0], mx[1]);
             top_bits = __float_as_uint(t) >> 16;  // cut to bf16: only the agreement matters
-            sh->swap.top[jj & 1][qt][half][r] = (uint16_t)top_bits;
+            sh->swap[qt].top[jj & 1][half][r] = (uint16_t)top_bits;
             pair_arrive();
           };
           // Columns 16 c .. 16 c + 15 of this half, masked, into the maximum.
@@ -829,7 +882,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             if (!pair_wait()) return;
             const int slot = jj == 0 ? 0 : (jj - 1) & 1;
             const float top = fmaxf(__uint_as_float(top_bits << 16),
-                                    __uint_as_float((uint32_t)sh->swap.top[slot][qt][half ^ 1][r] << 16));
+                                    __uint_as_float((uint32_t)sh->swap[qt].top[slot][half ^ 1][r] << 16));
             // Without a score above -inf so far the reference is 0.  (c may be 0,
             // and 0 * -inf must not count as a score.)
             const float tm = top == -INFINITY ? -INFINITY : top * c;
@@ -884,15 +937,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               pk[e / 2 + 1] = pack_bf16(y[e + 2], y[e + 3]);
             }
             tmem_st8u(ts + half * 64 + i * 8, pk);
+            if (i & 1) {  // the product with V may begin on the first half
+              tmem_st_wait();
+              fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(i == 1 ? &sh->p_full[buf] : &sh->p_rest[buf]));
+            }
           }
-          tmem_st_wait();
-          fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
           l += (l0 + l1) + (l2 + l3);
           if (jj > 0 && kt + 1 < g.kt1) publish();
         } else if (lane == 0) {
           mbar_arrive(smem_u32(&sh->p_full[buf]));
+          mbar_arrive(smem_u32(&sh->p_rest[buf]));
         }
       }
       // ---- the row's sums out ----
