@@ -85,7 +85,7 @@ struct Seg {
 
 struct Shared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], p_rest[2], turn[2], pv[2], o_full[2], o_empty[2], v_land, end[2];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], turn[2], pv[2], o_full[2], o_empty[2], v_land, end[2];
   uint64_t pair[2][4];
   uint64_t seg_full[2], seg_empty[2], clc_full;
   alignas(16) uint4 clc;  // the next item's answer
@@ -97,9 +97,9 @@ struct Shared {
   long long left;
   long long scan[20];
   union {  // what the two warps of 32 rows exchange
-    uint16_t top[2][2][128];  // [key tile & 1][half][row]: maxima, as bf16
-    float val[2][128];        // [half][row]
-  } swap[2];                  // of a row tile
+    uint16_t top[2][2][32];  // [key tile & 1][half][row]: maxima, as bf16
+    float val[2][32];        // [half][row]
+  } swap[2][4];              // of their own: other pairs may be in another range
 };
 
 template <int D, int NQ>
@@ -175,13 +175,26 @@ struct SegIter {
   }
 };
 
-// The bounded wait of every role; false: leave.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Shared* sh,
-                                              unsigned* status) {
-  const uint32_t mb = smem_u32(bar);
-  if (mbar_try_wait(mb, parity)) return true;
+// A wait that parks the warp until the phase completes or about 20 us have gone
+// by.  Without a time limit of its own a try returns after a short one, and some
+// ten waiting warps' retries then slow every other shared-memory access of the SM
+// (a wait for a completed phase took 200 cycles instead of 30).
+__device__ __forceinline__ bool parked_wait(uint32_t mb, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(mb), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+// The bounded wait of every role; false: leave.  The rare part is kept out of
+// line: the roles' hot loops share the instruction cache.
+__device__ __noinline__ bool long_wait(uint32_t mb, uint32_t parity, Shared* sh, unsigned* status) {
   const long long t0 = clock64();
-  while (!mbar_try_wait(mb, parity)) {
+  while (!parked_wait(mb, parity)) {
     if (*(volatile int*)&sh->abort) return false;
     if (clock64() - t0 > kWaitBudget) {
       *(volatile int*)&sh->abort = 1;
@@ -190,6 +203,11 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Sh
     }
   }
   return true;
+}
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Shared* sh,
+                                              unsigned* status) {
+  const uint32_t mb = smem_u32(bar);
+  return parked_wait(mb, parity) || long_wait(mb, parity, sh, status);
 }
 // The same by a whole warp, with one answer for it.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared* sh,
@@ -307,7 +325,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&sh->s_full[i]), 1);
         mbar_init(smem_u32(&sh->p_full[i]), 8);
-        mbar_init(smem_u32(&sh->p_rest[i]), 8);
         mbar_init(smem_u32(&sh->turn[i]), 1);
         mbar_init(smem_u32(&sh->pv[i]), 1);
         mbar_init(smem_u32(&sh->o_full[i]), 1);
@@ -556,36 +573,26 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         if (u == NU - 1) mma_commit(smem_u32(&sh->s_full[buf]));
       }
     };
-    // O[q] (+)= P[buf] V: first the keys whose P comes first (columns 0 .. 31 of
-    // either half of the tile), then the rest; then `done` and `done2` arrive.
-    auto pv = [&](uint32_t buf, uint32_t phase, bool acc, const uint32_t(&at)[NU], uint64_t* done,
-                  uint64_t* done2) -> bool {
+    // O[q] (+)= P[buf] V over the key tile's units (keys outermost); then `done`
+    // and `done2` arrive.
+    auto pv = [&](uint32_t buf, bool acc, const uint32_t(&at)[NU], uint64_t* done, uint64_t* done2) {
       constexpr int ND = D / VD;  // units side by side in the dims
+      fence_after_sync();
+      if (elect_one()) {
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        if (part == 1)
-          if (!wait(sh->p_rest[buf], phase)) return false;
-        fence_after_sync();
-        if (elect_one()) {
+        for (int u = 0; u < NU; ++u) {
+          const uint64_t vd = desc_sw128(sv + at[u] * C::kUnit, VK * 128, 1024);
 #pragma unroll
-          for (int db = 0; db < ND; ++db)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int ks = (i >> 1) * 4 + part * 2 + (i & 1);  // step of 16 keys in the tile
-              const int u = (ks / (VK / 16)) * ND + db, k = ks % (VK / 16);
-              const uint64_t vd = desc_sw128(sv + at[u] * C::kUnit, VK * 128, 1024);
-              mma_bf16_ta(kTO + q * 128 + db * VD, buf * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
-                          vd + ((k * 2048) >> 4), kIdPV, acc || part + i > 0);
-            }
-          if (part == 1) {
-#pragma unroll
-            for (int u = 0; u < NU; ++u) mma_commit(smem_u32(&sh->v_empty[at[u]]));
-            if (done) mma_commit(smem_u32(done));
-            if (done2) mma_commit(smem_u32(done2));
+          for (int k = 0; k < VK / 16; ++k) {
+            const int ks = (u / ND) * (VK / 16) + k;  // step of 16 keys in the tile
+            mma_bf16_ta(kTO + q * 128 + (u % ND) * VD, buf * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
+                        vd + ((k * 2048) >> 4), kIdPV, acc || ks > 0);
           }
+          mma_commit(smem_u32(&sh->v_empty[at[u]]));
         }
+        if (done) mma_commit(smem_u32(done));
+        if (done2) mma_commit(smem_u32(done2));
       }
-      return true;
     };
     auto role = [&] {
       uint32_t nk = 0;  // key tiles before this range (of this row tile)
@@ -624,7 +631,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               continue;
             }
             if (j >= 0) {
-              if (!pv(q, nk & 1, j > 0, av, j == n - 1 ? &sh->o_full[q] : nullptr, nullptr)) return;
+              pv(q, j > 0, av, j == n - 1 ? &sh->o_full[q] : nullptr, nullptr);
               ++nk;
             }
             if (j + 1 < n) {
@@ -658,9 +665,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             if (j == 0 && nseg > 0)
               if (!wait(sh->o_empty[0], (nseg - 1) & 1)) return;
             if (!wait(sh->p_full[nk & 1], (nk >> 1) & 1)) return;
-            if (!pv(nk & 1, (nk >> 1) & 1, j > 0, av, &sh->pv[nk & 1],
-                    j == n - 1 ? &sh->o_full[0] : nullptr))
-              return;
+            pv(nk & 1, j > 0, av, &sh->pv[nk & 1], j == n - 1 ? &sh->o_full[0] : nullptr);
           }
         }
         ++nseg;
@@ -793,6 +798,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     uint32_t nk = 0, np = 0;
     // Meeting the pair's other warp (bounded; false: leave).
     uint64_t& pair = sh->pair[qt][warp & 3];
+    auto& mine = sh->swap[qt][warp & 3];
     auto pair_arrive = [&] {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&pair));
@@ -801,10 +807,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     // x becomes the row's value of it from the other warp (between two meetings
     // that keep `val` from being written early).
     auto swap = [&](float& x) -> bool {
-      sh->swap[qt].val[half][r] = x;
+      mine.val[half][lane] = x;
       pair_arrive();
       const bool ok = pair_wait();
-      x = sh->swap[qt].val[half ^ 1][r];
+      x = mine.val[half ^ 1][lane];
       return ok;
     };
     int seg_n = 0;
@@ -846,43 +852,42 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           const uint32_t ts = tmem + lanes + buf * 128;
           const int lim = last - kt * BK - half * 64;  // the row's last visible column
           const bool masked = __any_sync(0xffffffffu, lim < 63);
-          float mx[2] = {-INFINITY, -INFINITY};
-          auto publish = [&] {
-            const float t = fmaxf(mx[0], mx[1]);
-            top_bits = __float_as_uint(t) >> 16;  // cut to bf16: only the agreement matters
-            sh->swap[qt].top[jj & 1][half][r] = (uint16_t)top_bits;
-            pair_arrive();
-          };
-          // Columns 16 c .. 16 c + 15 of this half, masked, into the maximum.
-          auto column_max = [&](float(&x)[16], int c16) {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // Scores 32 i .. 32 i + 31 of this half, masked, into the maxima.  Loops
+          // over i stay rolled: unrolled, the roles' loops together overflowed the
+          // instruction cache (95 % hits) and the registers, and an iteration took
+          // 4800 cycles, most of them waiting for instructions and spills.
+          auto scores = [&](float(&y)[32], int i) {
+            tmem_ld32(ts + half * 64 + i * 32, y);
+            tmem_ld_wait();
             if (masked) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) x[e] = c16 * 16 + e <= lim ? x[e] : -INFINITY;
+              for (int e = 0; e < 32; ++e) y[e] = i * 32 + e <= lim ? y[e] : -INFINITY;
             }
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              mx[0] = fmaxf(mx[0], fmaxf(x[e], x[e + 1]));
-              mx[1] = fmaxf(mx[1], fmaxf(x[e + 2], x[e + 3]));
-            }
+            for (int e = 0; e < 32; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(y[e + k], y[e + k + 4]));
+          };
+          auto publish = [&] {
+            const float t = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            top_bits = __float_as_uint(t) >> 16;  // cut to bf16: only the agreement matters
+            mine.top[jj & 1][half][lane] = (uint16_t)top_bits;
+            pair_arrive();
           };
           if (jj == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float x[16];
-              tmem_ld16(ts + half * 64 + i * 16, x);
-              tmem_ld_wait();
-              column_max(x, i);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              float y[32];
+              scores(y, i);
             }
             publish();
           }
-          // In flight during the exchange.
-          float x[2][16];
-          tmem_ld16(ts + half * 64, x[0]);
           if (jj != 1) {
             if (!pair_wait()) return;
             const int slot = jj == 0 ? 0 : (jj - 1) & 1;
             const float top = fmaxf(__uint_as_float(top_bits << 16),
-                                    __uint_as_float((uint32_t)sh->swap[qt].top[slot][half ^ 1][r] << 16));
+                                    __uint_as_float((uint32_t)mine.top[slot][half ^ 1][lane] << 16));
             // Without a score above -inf so far the reference is 0.  (c may be 0,
             // and 0 * -inf must not count as a score.)
             const float tm = top == -INFINITY ? -INFINITY : top * c;
@@ -916,39 +921,32 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           }
           const float ref = -m;
           float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
-          // 16 columns at a time, the next 16 on their way; P's 8 columns go where
-          // this half's scores were read before.
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            float y[32];
+            scores(y, i);
+            float pk[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            tmem_ld_wait();
-            if (i + 1 < 4) tmem_ld16(ts + half * 64 + (i + 1) * 16, x[(i + 1) & 1]);
-            float(&y)[16] = x[i & 1];
-            column_max(y, i);
-            uint32_t pk[8];
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
+            for (int e = 0; e < 32; e += 4) {
               fma2(y[e], y[e + 1], c, ref);
               fma2(y[e + 2], y[e + 3], c, ref);
 #pragma unroll
               for (int k = 0; k < 4; ++k) y[e + k] = ex2(y[e + k]);
               add2(l0, l1, y[e], y[e + 1]);
               add2(l2, l3, y[e + 2], y[e + 3]);
-              pk[e / 2] = pack_bf16(y[e], y[e + 1]);
-              pk[e / 2 + 1] = pack_bf16(y[e + 2], y[e + 3]);
+              pk[e / 2] = __uint_as_float(pack_bf16(y[e], y[e + 1]));
+              pk[e / 2 + 1] = __uint_as_float(pack_bf16(y[e + 2], y[e + 3]));
             }
-            tmem_st8u(ts + half * 64 + i * 8, pk);
-            if (i & 1) {  // the product with V may begin on the first half
-              tmem_st_wait();
-              fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(i == 1 ? &sh->p_full[buf] : &sh->p_rest[buf]));
-            }
+            tmem_st16(ts + half * 64 + i * 16, pk);
           }
+          tmem_st_wait();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
           l += (l0 + l1) + (l2 + l3);
           if (jj > 0 && kt + 1 < g.kt1) publish();
         } else if (lane == 0) {
           mbar_arrive(smem_u32(&sh->p_full[buf]));
-          mbar_arrive(smem_u32(&sh->p_rest[buf]));
         }
       }
       // ---- the row's sums out ----
