@@ -194,7 +194,10 @@ __device__ __forceinline__ bool parked_wait(uint32_t mb, uint32_t parity) {
 // line: the roles' hot loops share the instruction cache.
 __device__ __noinline__ bool long_wait(uint32_t mb, uint32_t parity, Shared* sh, unsigned* status) {
   const long long t0 = clock64();
-  while (!parked_wait(mb, parity)) {
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (parked_wait(mb, parity)) return true;
     if (*(volatile int*)&sh->abort) return false;
     if (clock64() - t0 > kWaitBudget) {
       *(volatile int*)&sh->abort = 1;
@@ -202,7 +205,6 @@ __device__ __noinline__ bool long_wait(uint32_t mb, uint32_t parity, Shared* sh,
       return false;
     }
   }
-  return true;
 }
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Shared* sh,
                                               unsigned* status) {
@@ -249,22 +251,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-// (a0, a1) * (c, c) + (b, b), two f32 lanes in one instruction.
-__device__ __forceinline__ void fma2(float& x0, float& x1, float c, float b) {
-  uint64_t x, cc, bb;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(bb) : "f"(b));
-  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(cc), "l"(bb));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
-}
-__device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
-  uint64_t s, x;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(s) : "f"(s0), "f"(s1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s) : "l"(x));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(s));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -608,15 +594,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           // Turn 0: the scores of key tile 0; turn j + 1: P V of tile j and the scores
           // of tile j + 1.
           for (int j = -1; j < n; ++j) {
-            if (j >= 0) {
-              if (!idle)
-                if (!wait(sh->p_full[q], nk & 1)) return;
-              if (j == 0 && nact > 0 && !idle)  // the last range's O has been read
-                if (!wait(sh->o_empty[q], (nact - 1) & 1)) return;
+            if (j >= 0)
               if (!land(vr, sh->v_full, av)) return;
-            }
             if (j + 1 < n)
               if (!land(kr, sh->k_full, ak)) return;
+            if (j == 0 && nact > 0 && !idle)  // the last range's O has been read
+              if (!wait(sh->o_empty[q], (nact - 1) & 1)) return;
+            if (j >= 0 && !idle)
+              if (!wait(sh->p_full[q], nk & 1)) return;
             fence_after_sync();
             if (!take_turn()) return;
             if (idle) {
@@ -793,6 +778,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     const int r = tid & 127;                            // row of the tile, lane of TMEM
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // (32 * (warp % 4)) << 16
     const float c = p.scale * kLog2e;
+    const float2 c2 = make_float2(c, c);
     const int tok = qt * a.TQ + r / G;                  // token of the tile
     auto role = [&] {
     uint32_t nk = 0, np = 0;
@@ -846,96 +832,101 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const int buf = NQ == 2 ? qt : (int)(nk & 1);
         const uint32_t ph = NQ == 2 ? nk & 1 : (nk >> 1) & 1;
         const int jj = kt - g.kt0;
+        // Takes the other half's last published maximum and raises m where needed.
+        auto raise_reference = [&]() -> bool {
+          if (!pair_wait()) return false;
+          const int slot = jj == 0 ? 0 : (jj - 1) & 1;
+          const float top = fmaxf(__uint_as_float(top_bits << 16),
+                                  __uint_as_float((uint32_t)mine.top[slot][half ^ 1][lane] << 16));
+          // Without a score above -inf so far the reference is 0.
+          const float tm = top;
+          float f = 1.0f;
+          bool raise = false;
+          if (tm > m + kRaise || (m == -INFINITY && tm > m)) {
+            raise = valid && jj > 0;
+            f = ex2(m - tm);
+            m = tm;
+          }
+          if (m == -INFINITY) m = 0.0f;
+          if (__any_sync(0xffffffffu, raise)) {
+            // O is at rest: in the two-tile form S j follows P V j-1, in the other
+            // that product is waited for.
+            if constexpr (NQ == 1) {
+              if (!wait_or_abort(&sh->pv[(nk - 1) & 1], ((nk - 1) >> 1) & 1, sh, p.status)) return false;
+              fence_after_sync();
+            }
+            l *= f;
+            tmem_ld_wait();  // the scores on their way
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              float o[16];
+              tmem_ld16(to + i * 16, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tmem_st16(to + i * 16, o);
+            }
+            tmem_st_wait();
+          }
+          return true;
+        };
         WAIT(sh->s_full[buf], ph);
         fence_after_sync();
         if (!idle) {
           const uint32_t ts = tmem + lanes + buf * 128;
           const int lim = last - kt * BK - half * 64;  // the row's last visible column
           const bool masked = __any_sync(0xffffffffu, lim < 63);
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          // Scores 32 i .. 32 i + 31 of this half, masked, into the maxima.  Loops
-          // over i stay rolled: unrolled, the roles' loops together overflowed the
-          // instruction cache (95 % hits) and the registers, and an iteration took
-          // 4800 cycles, most of them waiting for instructions and spills.
+          // Publishes a maximum, cut to bf16: only the agreement matters.
+          auto publish = [&](float t) {
+            top_bits = __float_as_uint(t) >> 16;
+            mine.top[jj & 1][half][lane] = (uint16_t)top_bits;
+            pair_arrive();
+          };
           auto scores = [&](float(&y)[32], int i) {
             tmem_ld32(ts + half * 64 + i * 32, y);
             tmem_ld_wait();
             if (masked) {
+              const int li = lim - i * 32;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = i * 32 + e <= lim ? y[e] : -INFINITY;
+              for (int e = 0; e < 32; ++e) y[e] = e <= li ? y[e] : -INFINITY;
             }
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(y[e + k], y[e + k + 4]));
-          };
-          auto publish = [&] {
-            const float t = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            top_bits = __float_as_uint(t) >> 16;  // cut to bf16: only the agreement matters
-            mine.top[jj & 1][half][lane] = (uint16_t)top_bits;
-            pair_arrive();
           };
           if (jj == 0) {
+            float t = -INFINITY;
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
               float y[32];
               scores(y, i);
-            }
-            publish();
-          }
-          if (jj != 1) {
-            if (!pair_wait()) return;
-            const int slot = jj == 0 ? 0 : (jj - 1) & 1;
-            const float top = fmaxf(__uint_as_float(top_bits << 16),
-                                    __uint_as_float((uint32_t)mine.top[slot][half ^ 1][lane] << 16));
-            // Without a score above -inf so far the reference is 0.  (c may be 0,
-            // and 0 * -inf must not count as a score.)
-            const float tm = top == -INFINITY ? -INFINITY : top * c;
-            float f = 1.0f;
-            bool raise = false;
-            if (tm > m + kRaise || (m == -INFINITY && tm > m)) {
-              raise = valid && jj > 0;
-              f = ex2(m - tm);
-              m = tm;
-            }
-            if (m == -INFINITY) m = 0.0f;
-            if (__any_sync(0xffffffffu, raise)) {
-              // O is at rest: in the two-tile form S j follows P V j-1, in the
-              // other that product is waited for.
-              if constexpr (NQ == 1) {
-                WAIT(sh->pv[(nk - 1) & 1], ((nk - 1) >> 1) & 1);
-                fence_after_sync();
-              }
-              l *= f;
-#pragma unroll 1
-              for (int i = 0; i < D / 32; ++i) {
-                float o[16];
-                tmem_ld16(to + i * 16, o);
-                tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] *= f;
-                tmem_st16(to + i * 16, o);
-              }
-              tmem_st_wait();
+              for (int e = 0; e < 32; e += 2) t = fmaxf(t, fmaxf(y[e], y[e + 1]));
             }
+            publish(t == -INFINITY ? t : t * c);  // (0 * -inf must not count as a score)
           }
-          const float ref = -m;
-          float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
+          if (jj != 1)
+            if (!raise_reference()) return;
+          float2 sum01 = make_float2(0.0f, 0.0f), sum23 = sum01;
+          __nv_bfloat162 big = __float2bfloat162_rn(0.0f);
+          const float2 nm2 = make_float2(-m, -m);
+          // 32 columns at a time in a rolled loop: unrolled, the roles' loops together
+          // overflowed the instruction cache (95 % hits) and the registers, and an
+          // iteration took 4800 cycles, most of them waiting for instructions and
+          // spills.  P's 16 columns of a step go where scores have been read.  The
+          // next reference comes from the largest P, two at a time in bf16.
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
             float y[32];
             scores(y, i);
             float pk[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              fma2(y[e], y[e + 1], c, ref);
-              fma2(y[e + 2], y[e + 3], c, ref);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) y[e + k] = ex2(y[e + k]);
-              add2(l0, l1, y[e], y[e + 1]);
-              add2(l2, l3, y[e + 2], y[e + 3]);
-              pk[e / 2] = __uint_as_float(pack_bf16(y[e], y[e + 1]));
-              pk[e / 2 + 1] = __uint_as_float(pack_bf16(y[e + 2], y[e + 3]));
+            for (int e = 0; e < 32; e += 2) {
+              float2 w = __ffma2_rn(make_float2(y[e], y[e + 1]), c2, nm2);
+              w.x = ex2(w.x);
+              w.y = ex2(w.y);
+              float2& sum = e & 2 ? sum23 : sum01;
+              sum = __fadd2_rn(sum, w);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(w.x, w.y);
+              big = __hmax2(big, h);
+              pk[e / 2] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
             }
             tmem_st16(ts + half * 64 + i * 16, pk);
           }
@@ -943,8 +934,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
-          l += (l0 + l1) + (l2 + l3);
-          if (jj > 0 && kt + 1 < g.kt1) publish();
+          sum01 = __fadd2_rn(sum01, sum23);
+          l += sum01.x + sum01.y;
+          if (jj > 0 && kt + 1 < g.kt1)
+            publish(m + log2f(fmaxf(__low2float(big), __high2float(big))));
         } else if (lane == 0) {
           mbar_arrive(smem_u32(&sh->p_full[buf]));
         }
@@ -955,12 +948,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       const uint4* gate = reinterpret_cast<const uint4*>(
           static_cast<const bf16*>(p.gate.p) + (int64_t)t * p.gate.ts + (int64_t)h * p.gate.hs +
           half * (D / 2));
-      // The gate's loads go out before the wait and a chunk of 32 dims ahead: one
+      // The gate's loads go out before the wait and a chunk of 16 dims ahead: one
       // at a time, just before use, they were half the time of a short row.
-      uint4 gw[4];
+      uint4 gw[2];
       if (gated) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) gw[e] = gate[e];
+        for (int e = 0; e < 2; ++e) gw[e] = gate[e];
       }
       WAIT(sh->o_full[qt], seg_n & 1);
       fence_after_sync();
@@ -976,29 +969,29 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         bool finite = isfinite(l) && !(l == 0.0f && last >= g.kt0 * BK);
         bf16* out = static_cast<bf16*>(p.out) + ((int64_t)t * p.Hq + h) * D + half * (D / 2);
 #pragma unroll 1
-        for (int i = 0; i < D / 64; ++i) {
-          float o[32];
-          tmem_ld32(to + i * 32, o);
+        for (int i = 0; i < D / 32; ++i) {
+          float o[16];
+          tmem_ld16(to + i * 16, o);
           tmem_ld_wait();
           float big = 0.0f;  // NaN and infinities survive a sum of x - x
 #pragma unroll
-          for (int e = 0; e < 32; ++e) big += o[e] - o[e];
+          for (int e = 0; e < 16; ++e) big += o[e] - o[e];
           finite = finite && big == 0.0f;
           if (g.slot >= 0) {
             if (valid) {
               float4* d = reinterpret_cast<float4*>(part.o + (g.slot * a.rows + pr) * D +
-                                                    half * (D / 2) + i * 32);
+                                                    half * (D / 2) + i * 16);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
+              for (int e = 0; e < 4; ++e)
                 d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
             continue;
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          for (int e = 0; e < 16; ++e) o[e] *= inv;
           if (gated) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               const uint32_t gp[4] = {gw[e].x, gw[e].y, gw[e].z, gw[e].w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -1006,18 +999,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
                 o[e * 8 + 2 * k + 1] *= sigmoid_gate(__uint_as_float(gp[k] & 0xffff0000u));
               }
             }
-            if (i + 1 < D / 64) {
+            if (i + 1 < D / 32) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) gw[e] = gate[(i + 1) * 4 + e];
+              for (int e = 0; e < 2; ++e) gw[e] = gate[(i + 1) * 2 + e];
             }
           }
           if (valid) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) w[k] = pack_bf16(o[e * 8 + 2 * k], o[e * 8 + 2 * k + 1]);
-              *reinterpret_cast<uint4*>(out + i * 32 + e * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(out + i * 16 + e * 8) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
