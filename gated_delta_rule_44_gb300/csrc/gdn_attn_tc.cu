@@ -600,10 +600,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               if (!land(kr, sh->k_full, ak)) return;
             if (j == 0 && nact > 0 && !idle)  // the last range's O has been read
               if (!wait(sh->o_empty[q], (nact - 1) & 1)) return;
+            if (!take_turn()) return;
             if (j >= 0 && !idle)
               if (!wait(sh->p_full[q], nk & 1)) return;
             fence_after_sync();
-            if (!take_turn()) return;
             if (idle) {
               pass_turn();
               if (elect_one()) {
@@ -832,44 +832,24 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const int buf = NQ == 2 ? qt : (int)(nk & 1);
         const uint32_t ph = NQ == 2 ? nk & 1 : (nk >> 1) & 1;
         const int jj = kt - g.kt0;
-        // Takes the other half's last published maximum and raises m where needed.
-        auto raise_reference = [&]() -> bool {
+        // Takes the other half's last published maximum; true in raise: m grew.
+        float f = 1.0f;
+        bool raise = false;
+        auto new_reference = [&]() -> bool {
           if (!pair_wait()) return false;
           const int slot = jj == 0 ? 0 : (jj - 1) & 1;
           const float top = fmaxf(__uint_as_float(top_bits << 16),
                                   __uint_as_float((uint32_t)mine.top[slot][half ^ 1][lane] << 16));
-          // Without a score above -inf so far the reference is 0.
-          const float tm = top;
-          float f = 1.0f;
-          bool raise = false;
-          if (tm > m + kRaise || (m == -INFINITY && tm > m)) {
+          if (top > m + kRaise || (m == -INFINITY && top > m)) {
             raise = valid && jj > 0;
-            f = ex2(m - tm);
-            m = tm;
+            f = ex2(m - top);
+            m = top;
           }
-          if (m == -INFINITY) m = 0.0f;
-          if (__any_sync(0xffffffffu, raise)) {
-            // O is at rest: in the two-tile form S j follows P V j-1, in the other
-            // that product is waited for.
-            if constexpr (NQ == 1) {
-              if (!wait_or_abort(&sh->pv[(nk - 1) & 1], ((nk - 1) >> 1) & 1, sh, p.status)) return false;
-              fence_after_sync();
-            }
-            l *= f;
-            tmem_ld_wait();  // the scores on their way
-#pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
-              float o[16];
-              tmem_ld16(to + i * 16, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= f;
-              tmem_st16(to + i * 16, o);
-            }
-            tmem_st_wait();
-          }
+          if (m == -INFINITY) m = 0.0f;  // no score above -inf so far
           return true;
         };
+        if (jj > 1 && !idle)
+          if (!new_reference()) return;
         WAIT(sh->s_full[buf], ph);
         fence_after_sync();
         if (!idle) {
@@ -901,9 +881,27 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               for (int e = 0; e < 32; e += 2) t = fmaxf(t, fmaxf(y[e], y[e + 1]));
             }
             publish(t == -INFINITY ? t : t * c);  // (0 * -inf must not count as a score)
+            if (!new_reference()) return;
           }
-          if (jj != 1)
-            if (!raise_reference()) return;
+          if (__any_sync(0xffffffffu, raise)) {
+            // O is at rest: in the two-tile form S j follows P V j-1, in the other
+            // that product is waited for.
+            if constexpr (NQ == 1) {
+              WAIT(sh->pv[(nk - 1) & 1], ((nk - 1) >> 1) & 1);
+              fence_after_sync();
+            }
+            l *= f;
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              float o[16];
+              tmem_ld16(to + i * 16, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tmem_st16(to + i * 16, o);
+            }
+            tmem_st_wait();
+          }
           float2 sum01 = make_float2(0.0f, 0.0f), sum23 = sum01;
           __nv_bfloat162 big = __float2bfloat162_rn(0.0f);
           const float2 nm2 = make_float2(-m, -m);
