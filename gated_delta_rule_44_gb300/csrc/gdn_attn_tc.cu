@@ -905,18 +905,24 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           float2 sum01 = make_float2(0.0f, 0.0f), sum23 = sum01;
           __nv_bfloat162 big = __float2bfloat162_rn(0.0f);
           const float2 nm2 = make_float2(-m, -m);
-          // 32 columns at a time in a rolled loop: unrolled, the roles' loops together
+          // 16 columns at a time in a rolled loop: unrolled, the roles' loops together
           // overflowed the instruction cache (95 % hits) and the registers, and an
           // iteration took 4800 cycles, most of them waiting for instructions and
-          // spills.  P's 16 columns of a step go where scores have been read.  The
+          // spills.  P's 8 columns of a step go where scores have been read.  The
           // next reference comes from the largest P, two at a time in bf16.
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            float y[32];
-            scores(y, i);
-            float pk[16];
+          for (int i = 0; i < 4; ++i) {
+            float y[16];
+            tmem_ld16(ts + half * 64 + i * 16, y);
+            tmem_ld_wait();
+            if (masked) {
+              const int li = lim - i * 16;
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
+              for (int e = 0; e < 16; ++e) y[e] = e <= li ? y[e] : -INFINITY;
+            }
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
               float2 w = __ffma2_rn(make_float2(y[e], y[e + 1]), c2, nm2);
               w.x = ex2(w.x);
               w.y = ex2(w.y);
@@ -924,9 +930,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               sum = __fadd2_rn(sum, w);
               const __nv_bfloat162 h = __floats2bfloat162_rn(w.x, w.y);
               big = __hmax2(big, h);
-              pk[e / 2] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+              pk[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            tmem_st16(ts + half * 64 + i * 16, pk);
+            tmem_st8u(ts + half * 64 + i * 8, pk);
           }
           tmem_st_wait();
           fence_before_sync();
