@@ -8,6 +8,7 @@ if the library cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 from typing import Optional
 
@@ -234,11 +235,9 @@ def lib() -> ctypes.CDLL:
             L.gdn_kda_resolve_algo.argtypes = [_i64, _i64, _i64, _i64, _i32, _i32]
             L.gdn_kda_workspace_bytes.restype = ctypes.c_size_t
             L.gdn_kda_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i64, _i32, _i32]
-            for name, args in (("gdn_attn_prepare", gdn_attn_prepare_args),
-                               ("gdn_attn_varlen", gdn_attn_varlen_args),
-                               ("gdn_attn_paged", gdn_attn_paged_args)):
+            for name in ("gdn_attn_prepare", "gdn_attn_varlen", "gdn_attn_paged"):
                 getattr(L, name).restype = ctypes.c_int
-                getattr(L, name).argtypes = [ctypes.POINTER(args), _vp]
+                getattr(L, name).argtypes = [_vp, _vp]  # an address of, or a reference to, args
             L.gdn_attn_paged_workspace_bytes.restype = ctypes.c_size_t
             L.gdn_attn_paged_workspace_bytes.argtypes = [_i64] * 6 + [_i32]
             L.gdn_status_string.restype = ctypes.c_char_p
@@ -514,111 +513,162 @@ def gdn_prefill_varlen(q, k, v, g, beta, state, cu_seqlens, out, *, scale=-1.0,
     _check(lib().gdn_prefill_varlen(ctypes.byref(a), _stream(stream)))
 
 
+# ---- full attention ----------------------------------------------------------------
+#
+# A decode step calls these once per layer, so their host side is kept short:
+# each tensor is looked at once, and the argument structures are packed into one
+# buffer per thread with struct (building them field by field through ctypes
+# took 40 us for gdn_attn_prepare).
+
+_MAX_BYTES = 1024
+
+
+def _packer(cls):
+    """struct.Struct of a ctypes structure's fields, nested ones in line."""
+    def codes(c):
+        out = ""
+        for _, t in c._fields_:
+            if issubclass(t, ctypes.Structure):
+                out += codes(t)
+            else:
+                out += {_i64: "q", _i32: "i", _f32: "f", ctypes.c_size_t: "N"}.get(t, "P")
+        return out
+    s = struct.Struct("@" + codes(cls) + "0q")
+    assert s.size == ctypes.sizeof(cls) <= _MAX_BYTES
+    return s
+
+
+_PREPARE = _packer(gdn_attn_prepare_args)
+_VARLEN = _packer(gdn_attn_varlen_args)
+_PAGED = _packer(gdn_attn_paged_args)
+_CACHE = _packer(gdn_attn_cache)
+_NO_ROWS = (0, 0, 0, 0)
+
+
+class _Args(threading.local):
+    """A thread's argument buffer and its address; the same for a cache."""
+
+    def __init__(self):
+        self.buf = ctypes.create_string_buffer(_MAX_BYTES)
+        self.cache = ctypes.create_string_buffer(_MAX_BYTES)
+        self.at, self.cache_at = ctypes.addressof(self.buf), ctypes.addressof(self.cache)
+
+
+_args = _Args()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _bad(msg: str):
     return GdnError(GDN_ERR_INVALID_ARGUMENT, "GDN_ERR_INVALID_ARGUMENT", msg)
 
 
-def _attn_shape(name, t, shape, like, dtype=None):
+def _bad_shape(msg: str):
+    return GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE", msg)
+
+
+def _attn_check(name, t, shape, dtype, dev):
     """The C entries see sizes, not tensors: shape, type and device are checked here."""
-    want = like.dtype if dtype is None else dtype
-    if tuple(t.shape) != tuple(shape):
-        raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE",
-                       f"attention {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.dtype != want:
-        raise GdnError(GDN_ERR_DTYPE, "GDN_ERR_DTYPE",
-                       f"attention {name} is {t.dtype}, not {want}")
-    if t.device != like.device:
-        raise _bad(f"attention {name} is on {t.device}, not {like.device}")
+    if t.shape != shape:
+        raise _bad_shape(f"attention {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise GdnError(GDN_ERR_DTYPE, "GDN_ERR_DTYPE", f"attention {name} is {t.dtype}, not {dtype}")
+    if t.device != dev:
+        raise _bad(f"attention {name} is on {t.device}, not {dev}")
 
 
-def _attn_rows(name, t, shape, like):
-    """gdn_attn_rows of a [tokens, heads, D] view (any token and head stride)."""
+def _attn_rows(name, t, shape, dtype, dev):
+    """The gdn_attn_rows of a [tokens, heads, D] view (any token and head stride)."""
     if t is None:
-        return gdn_attn_rows()
-    _attn_shape(name, t, shape, like)
-    if t.stride(2) != 1:
+        return _NO_ROWS
+    _attn_check(name, t, shape, dtype, dev)
+    n, h, d = shape
+    ts, hs, ds = t.stride()
+    if ds != 1:
         raise _bad(f"attention {name}'s last dimension must be contiguous")
     # A dimension of one entry has no step of its own: its stride is free.
-    ts = t.stride(0) if t.shape[0] > 1 else 0
-    hs = t.stride(1) if t.shape[1] > 1 else 0
-    if (t.shape[0] > 1 and ts == 0) or (t.shape[1] > 1 and hs == 0):
+    if n == 1:
+        ts = 0
+    elif ts == 0:
         raise _bad(f"attention {name} is a broadcast view; pass real rows")
-    return gdn_attn_rows(data=_p(t), len=_n(t), token_stride=ts, head_stride=hs)
+    if h == 1:
+        hs = 0
+    elif hs == 0:
+        raise _bad(f"attention {name} is a broadcast view; pass real rows")
+    return t.data_ptr(), (n - 1) * ts + (h - 1) * hs + d, ts, hs
 
 
-def _attn_contig(name, t, shape, like, dtype=None):
+def _attn_flat(name, t, shape, dtype, dev):
+    """Address and length of a contiguous tensor (0, 0 for None)."""
     if t is None:
-        return
-    _attn_shape(name, t, shape, like, dtype)
+        return 0, 0
+    _attn_check(name, t, shape, dtype, dev)
     if not t.is_contiguous():
         raise _bad(f"attention {name} must be contiguous")
+    return t.data_ptr(), t.numel()
 
 
-def _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, like, block_table_host):
-    """gdn_attn_cache of k_cache, v_cache [pages, Hkv, page_size, D] (any strides
-    but the last) and block_table [N, max_pages] int32; and the host mirror."""
-    P, _, page = k_cache.shape[:3] if k_cache.dim() == 4 else (0, 0, 0)
+def _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dtype, dev, block_table_host):
+    """Packs the gdn_attn_cache of k_cache, v_cache [pages, Hkv, page_size, D]
+    (any strides but the last) and block_table [N, max_pages] int32 into the
+    thread's buffer; returns its address and the host mirror to keep."""
+    P, _, page, _ = k_cache.shape if k_cache.dim() == 4 else (0, 0, 0, 0)
+    shape = (P, Hkv, page, D)
+    parts = []
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _attn_shape(name, t, (P, Hkv, page, D), like)
-        if t.stride(3) != 1:
+        _attn_check(name, t, shape, dtype, dev)
+        ps, hs, ts, ds = t.stride()
+        if ds != 1:
             raise _bad(f"attention {name}'s last dimension must be contiguous")
-        if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+        if (P > 1 and ps == 0) or (Hkv > 1 and hs == 0) or (page > 1 and ts == 0):
             raise _bad(f"attention {name} is a broadcast view; pass a real cache")
+        parts += [t.data_ptr(), (P - 1) * ps + (Hkv - 1) * hs + (page - 1) * ts + D,
+                  ps if P > 1 else 0, hs if Hkv > 1 else 0, ts if page > 1 else 0]
     if block_table.dim() != 2:
-        raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE", "attention block_table must be [N, max_pages]")
-    _attn_shape("block_table", block_table, (N, block_table.shape[1]), like, torch.int32)
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise _bad_shape("attention block_table must be [N, max_pages]")
+    width = block_table.shape[1]
+    _attn_check("block_table", block_table, (N, width), torch.int32, dev)
+    if width > 1 and block_table.stride(1) != 1:
         raise _bad("attention block_table's last dimension must be contiguous")
-
-    def strides(t):
-        return [st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3])]
-
-    kp, kh, kt = strides(k_cache)
-    vp, vh, vt = strides(v_cache)
+    row = block_table.stride(0) if N > 1 else 0
     host, host_p = _host_i32(block_table_host)
-    ts = block_table.stride(0) if N > 1 else 0
     if host is not None:
-        if tuple(host.shape) != tuple(block_table.shape):
-            raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE",
-                           "attention block_table_host must have block_table's shape")
-        if N > 1 and ts != block_table.shape[1]:  # the mirror shares the row stride
-            wide = torch.zeros((N, ts), dtype=torch.int32)
-            wide[:, :host.shape[1]] = host
+        if host.shape != block_table.shape:
+            raise _bad_shape("attention block_table_host must have block_table's shape")
+        if N > 1 and row != width:  # the mirror shares the row stride
+            wide = torch.zeros((N, row), dtype=torch.int32)
+            wide[:, :width] = host
             host, host_p = wide, wide.data_ptr()
-    c = gdn_attn_cache(k=_p(k_cache), k_len=_n(k_cache), k_page_stride=kp, k_head_stride=kh,
-                       k_token_stride=kt, v=_p(v_cache), v_len=_n(v_cache), v_page_stride=vp,
-                       v_head_stride=vh, v_token_stride=vt, num_pages=P, page_size=page,
-                       block_table=_p(block_table), max_pages=block_table.shape[1],
-                       table_stride=ts, block_table_host=host_p)
-    return c, host
+    _CACHE.pack_into(_args.cache, 0, *parts, P, page, block_table.data_ptr(), width, row,
+                     host_p or 0)
+    return _args.cache_at, host
 
 
-def _attn_meta(N, T, cu_seqlens, kv_lens, like, cu_seqlens_host, kv_lens_host):
-    """Checks the metadata tensors' shapes; returns the host mirrors to keep."""
-    for name, t, n in (("cu_seqlens", cu_seqlens, N + 1), ("kv_lens", kv_lens, N)):
-        _attn_contig(name, t, (n,), like, torch.int32)
-    out = []
-    for name, t, n in (("cu_seqlens_host", cu_seqlens_host, N + 1),
-                       ("kv_lens_host", kv_lens_host, N)):
-        h, p = _host_i32(t)
-        if h is not None and h.numel() != n:
-            raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE",
-                           f"attention {name} holds {h.numel()} entries, not {n}")
-        out.append((h, p))
-    return out
+def _attn_mirror(name, t, n):
+    if t is None:
+        return None, 0
+    h, p = _host_i32(t)
+    if h.numel() != n:
+        raise _bad_shape(f"attention {name} holds {h.numel()} entries, not {n}")
+    return h, p
 
 
-def _attn_call(fn, a, q, stream) -> None:
+def _attn_dims(q, kv, cu_seqlens):
+    if q.dim() != 3 or kv.dim() < 2:
+        raise _bad_shape("attention query must be [tokens, heads, D]")
+    T, Hq, D = q.shape
+    return T, (T if cu_seqlens is None else cu_seqlens.numel() - 1), Hq, kv.shape[1], D
+
+
+def _attn_call(fn, q, stream) -> None:
     if not q.is_cuda:
         raise _bad(f"attention tensors must be on a CUDA device, got {q.device}")
-    _check(fn(ctypes.byref(a), _stream(stream)))
-
-
-def _attn_dims(q, kv_heads, cu_seqlens):
-    if q.dim() != 3:
-        raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE", "attention query must be [tokens, heads, D]")
-    T, Hq, D = q.shape
-    return T, (T if cu_seqlens is None else cu_seqlens.numel() - 1), Hq, kv_heads, D
+    if stream is not None:
+        s = stream.cuda_stream
+    elif _raw_stream is not None:
+        s = _raw_stream(q.device.index)
+    else:
+        s = torch.cuda.current_stream(q.device).cuda_stream
+    _check(fn(_args.at, s))
 
 
 def gdn_attn_prepare(q, k, v, cu_seqlens, q_out, *, kv_lens=None, block_table=None, k_cache=None,
@@ -629,51 +679,50 @@ def gdn_attn_prepare(q, k, v, cu_seqlens, q_out, *, kv_lens=None, block_table=No
     the projection rows; q_out [T, Hq, D] and k_out [T, Hkv, D] are written, and
     the new rows of k_cache, v_cache [pages, Hkv, page_size, D] in place.
     cos_sin [positions, rot_dim] f32; cu_seqlens None: one token per sequence."""
-    T, N, Hq, Hkv, D = _attn_dims(q, k.shape[1], cu_seqlens)
-    (cuh, cuh_p), (kvh, kvh_p) = _attn_meta(N, T, cu_seqlens, kv_lens, q, cu_seqlens_host,
-                                            kv_lens_host)
-    _attn_contig("q_out", q_out, (T, Hq, D), q)
-    _attn_contig("k_out", k_out, (T, Hkv, D), q)
-    _attn_contig("q_norm_weight", q_norm_weight, (D,), q)
-    _attn_contig("k_norm_weight", k_norm_weight, (D,), q)
-    _attn_contig("positions", positions, (T,), q, torch.int32)
-    rot = 0
-    if cos_sin is not None:
-        rot = cos_sin.shape[-1]
-        _attn_contig("cos_sin", cos_sin, (cos_sin.shape[0], rot), q, torch.float32)
-    cache = host = None
+    T, N, Hq, Hkv, D = _attn_dims(q, k, cu_seqlens)
+    dt, dev, i32 = q.dtype, q.device, torch.int32
+    keep_cu, cu_host = _attn_mirror("cu_seqlens_host", cu_seqlens_host, N + 1)
+    keep_kv, kv_host = _attn_mirror("kv_lens_host", kv_lens_host, N)
+    keep_table, cache = None, 0
     if k_cache is not None or v_cache is not None or block_table is not None:
         if k_cache is None or v_cache is None or block_table is None:
             raise _bad("attention cache needs k_cache, v_cache and block_table")
-        cache, host = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, q, block_table_host)
-    a = gdn_attn_prepare_args(
-        T=T, N=N, Hq=Hq, Hkv=Hkv, D=D, rot_dim=rot, act_dtype=_dt(q), norm_eps=float(norm_eps),
-        q=_attn_rows("query", q, (T, Hq, D), q), k=_attn_rows("key", k, (T, Hkv, D), q),
-        v=_attn_rows("value", v, (T, Hkv, D), q), q_norm_weight=_p(q_norm_weight),
-        q_norm_weight_len=_n(q_norm_weight), k_norm_weight=_p(k_norm_weight),
-        k_norm_weight_len=_n(k_norm_weight), cos_sin=_p(cos_sin), cos_sin_len=_n(cos_sin),
-        positions=_p(positions), cu_seqlens=_p(cu_seqlens), kv_lens=_p(kv_lens),
-        cu_seqlens_host=cuh_p, kv_lens_host=kvh_p,
-        cache=None if cache is None else ctypes.pointer(cache), q_out=_p(q_out),
-        q_out_len=_n(q_out), k_out=_p(k_out), k_out_len=_n(k_out))
-    _attn_call(lib().gdn_attn_prepare, a, q, stream)
+        cache, keep_table = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dt, dev,
+                                        block_table_host)
+    rot, cs = 0, (0, 0)
+    if cos_sin is not None:
+        rot = cos_sin.shape[-1]
+        cs = _attn_flat("cos_sin", cos_sin, (cos_sin.shape[0], rot), torch.float32, dev)
+    _PREPARE.pack_into(
+        _args.buf, 0, T, N, Hq, Hkv, D, rot, _dt(q), norm_eps,
+        *_attn_rows("query", q, (T, Hq, D), dt, dev), *_attn_rows("key", k, (T, Hkv, D), dt, dev),
+        *_attn_rows("value", v, (T, Hkv, D), dt, dev),
+        *_attn_flat("q_norm_weight", q_norm_weight, (D,), dt, dev),
+        *_attn_flat("k_norm_weight", k_norm_weight, (D,), dt, dev), *cs,
+        _attn_flat("positions", positions, (T,), i32, dev)[0],
+        _attn_flat("cu_seqlens", cu_seqlens, (N + 1,), i32, dev)[0],
+        _attn_flat("kv_lens", kv_lens, (N,), i32, dev)[0], cu_host, kv_host, cache,
+        *_attn_flat("q_out", q_out, (T, Hq, D), dt, dev),
+        *_attn_flat("k_out", k_out, (T, Hkv, D), dt, dev))
+    _attn_call(lib().gdn_attn_prepare, q, stream)
 
 
 def gdn_attn_varlen(q, k, v, cu_seqlens, out, *, scale=-1.0, gate=None, lse=None,
                     cu_seqlens_host=None, stream=None) -> None:
     """include/gdn.h gdn_attn_varlen.  q, gate [T, Hq, D], k, v [T, Hkv, D] (any
     token and head strides); out [T, Hq, D] and lse [T, Hq] f32 are written."""
-    T, N, Hq, Hkv, D = _attn_dims(q, k.shape[1], cu_seqlens)
-    (cuh, cuh_p), _ = _attn_meta(N, T, cu_seqlens, None, q, cu_seqlens_host, None)
-    _attn_contig("out", out, (T, Hq, D), q)
-    _attn_contig("lse", lse, (T, Hq), q, torch.float32)
-    a = gdn_attn_varlen_args(
-        T=T, N=N, Hq=Hq, Hkv=Hkv, D=D, act_dtype=_dt(q), scale=float(scale),
-        q=_attn_rows("query", q, (T, Hq, D), q), k=_attn_rows("key", k, (T, Hkv, D), q),
-        v=_attn_rows("value", v, (T, Hkv, D), q), gate=_attn_rows("gate", gate, (T, Hq, D), q),
-        cu_seqlens=_p(cu_seqlens), cu_seqlens_host=cuh_p, out=_p(out), out_len=_n(out),
-        lse=_p(lse), lse_len=_n(lse))
-    _attn_call(lib().gdn_attn_varlen, a, q, stream)
+    T, N, Hq, Hkv, D = _attn_dims(q, k, cu_seqlens)
+    dt, dev = q.dtype, q.device
+    keep, cu_host = _attn_mirror("cu_seqlens_host", cu_seqlens_host, N + 1)
+    _VARLEN.pack_into(
+        _args.buf, 0, T, N, Hq, Hkv, D, _dt(q), scale,
+        *_attn_rows("query", q, (T, Hq, D), dt, dev), *_attn_rows("key", k, (T, Hkv, D), dt, dev),
+        *_attn_rows("value", v, (T, Hkv, D), dt, dev),
+        *_attn_rows("gate", gate, (T, Hq, D), dt, dev),
+        _attn_flat("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)[0], cu_host,
+        *_attn_flat("out", out, (T, Hq, D), dt, dev),
+        *_attn_flat("lse", lse, (T, Hq), torch.float32, dev))
+    _attn_call(lib().gdn_attn_varlen, q, stream)
 
 
 def gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len=0,
@@ -691,31 +740,33 @@ def gdn_attn_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, *
     gdn_attn_paged_workspace_bytes() bytes; when None and one is needed, it is
     allocated here for the call."""
     if k_cache.dim() != 4:
-        raise GdnError(GDN_ERR_SHAPE, "GDN_ERR_SHAPE",
-                       "attention k_cache must be [pages, Hkv, page_size, D]")
-    T, N, Hq, Hkv, D = _attn_dims(q, k_cache.shape[1], cu_seqlens)
+        raise _bad_shape("attention k_cache must be [pages, Hkv, page_size, D]")
+    T, N, Hq, Hkv, D = _attn_dims(q, k_cache, cu_seqlens)
     if kv_lens is None:
         raise _bad("kv_lens is NULL")
-    (cuh, cuh_p), (kvh, kvh_p) = _attn_meta(N, T, cu_seqlens, kv_lens, q, cu_seqlens_host,
-                                            kv_lens_host)
-    _attn_contig("out", out, (T, Hq, D), q)
-    _attn_contig("lse", lse, (T, Hq), q, torch.float32)
-    cache, host = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, q, block_table_host)
+    dt, dev, i32 = q.dtype, q.device, torch.int32
+    keep_cu, cu_host = _attn_mirror("cu_seqlens_host", cu_seqlens_host, N + 1)
+    keep_kv, kv_host = _attn_mirror("kv_lens_host", kv_lens_host, N)
+    cache, keep_table = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dt, dev,
+                                    block_table_host)
     if workspace is None:
         nbytes = gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len, _dt(q))
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             if stream is not None:  # freed for reuse only after the call's stream has run it
                 workspace.record_stream(stream)
-    a = gdn_attn_paged_args(
-        T=T, N=N, Hq=Hq, Hkv=Hkv, D=D, max_q_len=int(max_q_len), act_dtype=_dt(q),
-        scale=float(scale), q=_attn_rows("query", q, (T, Hq, D), q),
-        gate=_attn_rows("gate", gate, (T, Hq, D), q), cu_seqlens=_p(cu_seqlens),
-        kv_lens=_p(kv_lens), cu_seqlens_host=cuh_p, kv_lens_host=kvh_p,
-        cache=ctypes.pointer(cache), out=_p(out), out_len=_n(out), lse=_p(lse), lse_len=_n(lse),
-        workspace=_p(workspace),
-        workspace_bytes=0 if workspace is None else workspace.numel() * workspace.element_size())
-    _attn_call(lib().gdn_attn_paged, a, q, stream)
+    elif workspace.device != dev:
+        raise _bad(f"attention workspace is on {workspace.device}, not {dev}")
+    ws = (0, 0) if workspace is None else (workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size())
+    _PAGED.pack_into(
+        _args.buf, 0, T, N, Hq, Hkv, D, max_q_len, _dt(q), scale,
+        *_attn_rows("query", q, (T, Hq, D), dt, dev), *_attn_rows("gate", gate, (T, Hq, D), dt, dev),
+        _attn_flat("cu_seqlens", cu_seqlens, (N + 1,), i32, dev)[0],
+        _attn_flat("kv_lens", kv_lens, (N,), i32, dev)[0], cu_host, kv_host, cache,
+        *_attn_flat("out", out, (T, Hq, D), dt, dev),
+        *_attn_flat("lse", lse, (T, Hq), torch.float32, dev), *ws)
+    _attn_call(lib().gdn_attn_paged, q, stream)
 
 
 def _host_u8(t: Optional[torch.Tensor]):
