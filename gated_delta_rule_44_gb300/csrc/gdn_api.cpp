@@ -1300,16 +1300,22 @@ int attn_varlen(const gdn_attn_varlen_args* a, void* stream) {
   return launch_result(launch_attn(p, st), "gdn_attn_varlen");
 }
 
+// The larger of the two forms' workspaces (the page size, which decides, is not
+// known before the call).
+size_t paged_need(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q,
+                  int32_t act_dtype) {
+  const size_t n = gdn::attn_simt_workspace_bytes(T, N, Hq, Hkv, D, max_q);
+  if (act_dtype != GDN_DTYPE_BF16) return n;
+  return std::max(n, gdn::attn_tc_workspace_bytes(T, N, Hq, Hkv, D, max_q));
+}
+
 size_t attn_paged_workspace(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
                             int64_t max_q_len, int32_t act_dtype) {
   if (check_act_dtype(act_dtype) || check_attn_dims(T, N, Hq, Hkv, D) || max_q_len < 0) return 0;
-  // The larger of the two forms' (the page size, which decides, is not known here).
-  size_t n = gdn::attn_simt_workspace_bytes(T, N, Hq, Hkv, D);
-  if (act_dtype != GDN_DTYPE_BF16) return n;
-  n = std::max(n, gdn::attn_tc_workspace_bytes(T, N, Hq, Hkv, D, resolve_max_q(max_q_len, T)));
   // As many tokens as sequences may mean one token each, without cu_seqlens.
-  if (T == N) n = std::max(n, gdn::attn_tc_workspace_bytes(T, N, Hq, Hkv, D, 1));
-  return n;
+  const int64_t mq = resolve_max_q(max_q_len, T);
+  const size_t n = paged_need(T, N, Hq, Hkv, D, mq, act_dtype);
+  return T == N ? std::max(n, paged_need(T, N, Hq, Hkv, D, 1, act_dtype)) : n;
 }
 
 int attn_paged(const gdn_attn_paged_args* a, void* stream) {
@@ -1329,8 +1335,7 @@ int attn_paged(const gdn_attn_paged_args* a, void* stream) {
   if (int rc = require_ptr(a->cache, "cache")) return rc;
   AttnCacheView cv{};
   if (int rc = check_attn_cache(a->cache, a->N, a->Hkv, a->D, a->act_dtype, &cv)) return rc;
-  const size_t need =
-      attn_paged_workspace(a->T, a->N, a->Hq, a->Hkv, a->D, a->max_q_len, a->act_dtype);
+  const size_t need = paged_need(a->T, a->N, a->Hq, a->Hkv, a->D, max_q, a->act_dtype);
   if (need > 0) {
     if (a->workspace == nullptr || a->workspace_bytes < need)
       return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_attn_paged workspace needs " + S((int64_t)need) +

@@ -2,15 +2,24 @@
 // supported size, type, page size and stride.  It serves f32 activations and
 // what the tensor-core kernel does not take.
 //
-// A CTA owns 64 rows (tokens x the query heads of one kv head, so that a key
-// read once serves the whole group) and walks its keys 64 at a time with a
+// Tile kernel.  A tile is 64 rows (tokens x the query heads of one kv head, so
+// that a key read once serves the whole group); its keys come 64 at a time with a
 // running maximum m and sum l per row:
 //   S = scale log2(e) Q K^T;  m' = max(m, max S);  P = 2^(S - m')
 //   l = l 2^(m - m') + sum P;  O = O 2^(m - m') + P V;   out = O / l
-// 256 threads hold a 4 x 4 piece of S and 4 x D/16 of O in registers; Q, K, V
-// and P tiles are in shared memory.  Bound by f32 FMA issue (about 12
-// shared-memory wavefronts to 64 FMAs).  With few CTAs a sequence's keys are
-// cut into ranges over blockIdx.y, whose sums a second kernel joins.
+// 256 threads hold a 4 x 4 piece of S and 4 x D/16 of O in registers; Q, P and one
+// of K and V at a time are in shared memory, the other on its way in registers
+// (D <= 128), so that two CTAs fit an SM.  Bound by f32 FMA issue.  A cluster of
+// CTAs shares a tile: each takes every so many key blocks, and the sums are joined
+// through distributed shared memory, so that few or unequal tiles still fill the
+// SMs.
+//
+// Row kernel, for a few rows per kv head (decode, drafts): a warp takes 8 keys at
+// a time with the dims over its lanes, each key and value read once and straight
+// from global memory; the 8 x rows partial dot products of the lanes are summed
+// by one transposing butterfly.  Bound by HBM.  Key ranges over the warps of a CTA
+// are joined in shared memory, over CTAs by a second kernel.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,16 +32,17 @@ namespace gdn {
 namespace {
 
 using namespace attn;
+namespace cg = cooperative_groups;
 
 constexpr int BM = 64, BN = 64, kThreads = 256;
-constexpr int kMaxSplits = 64;
+constexpr int kMaxCluster = 8;
 
 template <int D>
 struct Smem {
   static constexpr int kLd = D + 4;   // padded rows: float4 columns fall on distinct banks
   static constexpr int kLdP = BN + 4;
-  float q[BM][kLd], k[BN][kLd], v[BN][D], p[BM][kLdP];
-  float m[BM], l[BM], f[BM];
+  float q[BM][kLd], kv[BN][kLd], p[BM][kLdP];
+  float m[BM], l[BM];
 };
 
 template <typename T>
@@ -49,28 +59,30 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_constant__ AttnLaunch p,
-                                                             int splits) {
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1)
+    attn_simt_kernel(const __grid_constant__ AttnLaunch p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
   constexpr int NC = D / 16;              // O columns per thread
   constexpr int VW = NC < 4 ? NC : 4;     // in vectors of VW
   constexpr int NJ = NC / VW;
+  constexpr int NL = BN * (D / 4) / kThreads;  // float4 of a K or V block per thread
+  constexpr bool kAhead = D <= 128;       // the next block waits in registers
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int G = p.Hq / p.Hkv, TT = BM / G;
   // The longest rows first: the last tiles of a sequence see the most keys.
-  const int id = (int)(gridDim.x / p.Hkv) - 1 - (int)(blockIdx.x / p.Hkv);
-  const int hkv = blockIdx.x % p.Hkv;
+  const int item = blockIdx.x / ranks;
+  const int id = (int)(gridDim.x / ranks / p.Hkv) - 1 - item / p.Hkv;
+  const int hkv = item % p.Hkv;
   const SeqTile tile = find_tile(p, id, TT);
   if (tile.bad && tid == 0) atomicOr(p.status, kStatusBadSeqlens);
-  if (tile.nt == 0) return;
+  if (tile.nt == 0) return;  // the whole cluster
   const int base = cu_at(p.cu, tile.s);
   const int rows = tile.nt * G;
-  // Keys any row of the tile sees, and this CTA's range of them.
-  const int hi = max(0, tile.pos0 + tile.nt);
+  const int hi = max(0, tile.pos0 + tile.nt);  // keys any row of the tile sees
   const int blocks = (hi + BN - 1) / BN;
-  const int kb0 = (int)((int64_t)blocks * blockIdx.y / splits);
-  const int kb1 = (int)((int64_t)blocks * (blockIdx.y + 1) / splits);
   const float c = p.scale * kLog2e;
 
   for (int i = tid; i < BM * (D / 4); i += kThreads) {
@@ -91,23 +103,40 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
 #pragma unroll
     for (int j = 0; j < NC; ++j) o[i][j] = 0.0f;
 
-  for (int kb = kb0; kb < kb1; ++kb) {
-    const int j0 = kb * BN, nk = min(BN, hi - j0);
-    __syncthreads();
-    for (int i = tid; i < BN * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (r < nk) {
-        const int64_t ko = key_offset(p, false, tile.s, base, hkv, j0 + r);
-        const int64_t vo = key_offset(p, true, tile.s, base, hkv, j0 + r);
-        if (ko >= 0) x = load4(static_cast<const T*>(key_base(p, false)) + ko + d);
-        if (vo >= 0) y = load4(static_cast<const T*>(key_base(p, true)) + vo + d);
-        if (ko < 0 && d == 0) atomicOr(p.status, kStatusBadIndex);
-      }
-      *reinterpret_cast<float4*>(&sm.k[r][d]) = x;
-      *reinterpret_cast<float4*>(&sm.v[r][d]) = y;
+  // This thread's vectors of block kb of K or V; rows past the last visible key
+  // and bad pages are zeros.
+  float4 next[kAhead ? NL : 1];
+  auto fetch1 = [&](bool of_v, int kb, int n) -> float4 {
+    const int i = tid + n * kThreads, r = i / (D / 4), d = i % (D / 4) * 4, j = kb * BN + r;
+    if (j >= hi) return make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t at = key_offset(p, of_v, tile.s, base, hkv, j);
+    if (at < 0) {
+      if (d == 0) atomicOr(p.status, kStatusBadIndex);
+      return make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    return load4(static_cast<const T*>(key_base(p, of_v)) + at + d);
+  };
+  auto fetch = [&](bool of_v, int kb) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int n = 0; n < NL; ++n) next[n] = fetch1(of_v, kb, n);
+    }
+  };
+  auto place = [&](bool of_v, int kb) {
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int i = tid + n * kThreads;
+      const float4 x = kAhead ? next[kAhead ? n : 0] : fetch1(of_v, kb, n);
+      *reinterpret_cast<float4*>(&sm.kv[i / (D / 4)][i % (D / 4) * 4]) = x;
+    }
+  };
+  if (rank < blocks) fetch(false, rank);
+  for (int kb = rank; kb < blocks; kb += ranks) {
+    const int j0 = kb * BN;
     __syncthreads();
+    place(false, kb);
+    __syncthreads();
+    fetch(true, kb);
     float s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -119,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(&sm.q[ty * 4 + i][d]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][d]);
+      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(&sm.kv[tx + 16 * j][d]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -163,7 +192,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
 #pragma unroll
       for (int j = 0; j < NC; ++j) o[i][j] *= f;
     }
-    __syncwarp();  // a warp's own 8 rows of P are all it reads below
+    __syncthreads();  // K has been read
+    place(true, kb);
+    __syncthreads();
+    if (kb + ranks < blocks) fetch(false, kb + ranks);
 #pragma unroll 2
     for (int j = 0; j < BN; j += 4) {
       float4 pr[4];
@@ -174,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
 #pragma unroll
         for (int n = 0; n < NJ; ++n) {
           float v[VW];
-          const float* vp = &sm.v[j + jj][n * 16 * VW + tx * VW];
+          const float* vp = &sm.kv[j + jj][n * 16 * VW + tx * VW];
           if constexpr (VW == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(vp);
           else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(vp);
 #pragma unroll
@@ -188,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
     }
   }
 
-  // The rows' sums into shared memory (over Q), a warp's 8 rows by that warp.
+  // The rows' sums into shared memory, over Q, for the whole cluster to see.
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -196,27 +228,188 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
     for (int n = 0; n < NJ; ++n)
 #pragma unroll
       for (int e = 0; e < VW; ++e) sm.q[ty * 4 + i][n * 16 * VW + tx * VW + e] = o[i][n * VW + e];
-  __syncwarp();
+  cluster.sync();
   const int lane = tid & 31;
   constexpr int E = D / 32;
-  for (int r = (tid >> 5) * 8; r < (tid >> 5) * 8 + 8 && r < rows; ++r) {
+  for (int r = rank * (kThreads / 32) + (tid >> 5); r < rows; r += ranks * (kThreads / 32)) {
     const int t = tile.t0 + r / G, h = hkv * G + r % G;
-    float acc[E], m = sm.m[r], l = sm.l[r];
+    float acc[E] = {}, m = -INFINITY, l = 0.0f;
+    for (int z = 0; z < ranks; ++z) {  // the same order in every call
+      const Smem<D>& other = *cluster.map_shared_rank(&sm, z);
+      const float mz = other.m[r];
+      const float mn = fmaxf(m, mz);
+      // A share without a key (m = -inf) adds its l = 0, or the NaN of a row all of
+      // whose scores are NaN.
+      const float f = m == -INFINITY ? 0.0f : exp2f(m - mn);
+      const float g = mz == -INFINITY ? 1.0f : exp2f(mz - mn);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, g * other.q[r][lane * E + e]);
+      l = fmaf(l, f, g * other.l[r]);
+      m = mn;
+    }
     bool finite = isfinite(l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      acc[e] = sm.q[r][lane * E + e];
-      finite = finite && isfinite(acc[e]);
-    }
+    for (int e = 0; e < E; ++e) finite = finite && isfinite(acc[e]);
     if (!__all_sync(0xffffffffu, finite))
-      exact_row<T, D>(p, tile.s, base, t, h, kb0 * BN, min(kb1 * BN, tile.pos0 + r / G + 1), acc, m,
-                      l);
-    if (splits > 1) {
-      const Partials part(p.ws, (int64_t)gridDim.x * splits, BM, D);
-      const int64_t slot = ((int64_t)id * p.Hkv + hkv) * splits + blockIdx.y;
-      part.put<E>(slot, r, lane, acc, m, l);
+      exact_row<T, D>(p, tile.s, base, t, h, 0, min(hi, tile.pos0 + r / G + 1), acc, m, l);
+    finish_row<T, D>(p, t, h, lane, acc, m, l);
+  }
+  cluster.sync();  // no CTA leaves while its sums may be read
+}
+
+// Sums v[0 .. 31] of every lane over the warp: lane i is left with the sum of
+// v[i].  Each step halves the values: a lane keeps the half its bit names and
+// sends the other.
+__device__ __forceinline__ float butterfly(float (&v)[32], int lane) {
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float send = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+    }
+  }
+  return v[0];
+}
+
+constexpr int kKeys = 8;   // keys of a warp's step
+
+// RB rows at most: RB * kKeys / 32 butterflies per step.
+template <typename T, int D, int RB>
+__global__ void __launch_bounds__(kThreads) attn_rows_kernel(const __grid_constant__ AttnLaunch p,
+                                                             int splits) {
+  constexpr int E = D / 32, W = kThreads / 32, NB = RB * kKeys / 32;
+  __shared__ float so[W][RB][D];
+  __shared__ float2 sml[W][RB];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = p.Hq / p.Hkv, TT = RB / G;
+  const int id = blockIdx.x / p.Hkv, hkv = blockIdx.x % p.Hkv;
+  const SeqTile tile = find_tile(p, id, TT);
+  if (tile.bad && threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
+  if (tile.nt == 0) return;
+  const int base = cu_at(p.cu, tile.s), rows = tile.nt * G;
+  const int hi = max(0, tile.pos0 + tile.nt);
+  const int steps = (hi + kKeys - 1) / kKeys;
+  const int k0 = (int)((int64_t)steps * blockIdx.y / splits) * kKeys;
+  const int k1 = min(hi, (int)((int64_t)steps * (blockIdx.y + 1) / splits) * kKeys);
+  const float c = p.scale * kLog2e;
+
+  auto loadE = [&](const T* x, float (&v)[E]) {
+    if constexpr (E == 1) {
+      v[0] = to_f(x[lane]);
+    } else if constexpr (E % 4 == 0) {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 f = load4(x + lane * E + e);
+        v[e] = f.x; v[e + 1] = f.y; v[e + 2] = f.z; v[e + 3] = f.w;
+      }
     } else {
-      finish_row<T, D>(p, t, h, lane, acc, m, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = to_f(x[lane * E + e]);
+    }
+  };
+  float q[RB][E], acc[RB][E], m[RB], l[RB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) q[r][e] = acc[r][e] = 0.0f;
+    if (r < rows)
+      loadE(static_cast<const T*>(p.q.p) + (int64_t)(tile.t0 + r / G) * p.q.ts +
+                (int64_t)(hkv * G + r % G) * p.q.hs, q[r]);
+  }
+  for (int j0 = k0 + warp * kKeys; j0 < k1; j0 += W * kKeys) {
+    float k[kKeys][E], v[kKeys][E];
+    // Lane i < kKeys finds key i.
+    int64_t ko = -1, vo = -1;
+    if (lane < kKeys && j0 + lane < k1) {
+      ko = key_offset(p, false, tile.s, base, hkv, j0 + lane);
+      vo = key_offset(p, true, tile.s, base, hkv, j0 + lane);
+      if (ko < 0) atomicOr(p.status, kStatusBadIndex);
+    }
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const int64_t a = __shfl_sync(0xffffffffu, ko, i), b = __shfl_sync(0xffffffffu, vo, i);
+#pragma unroll
+      for (int e = 0; e < E; ++e) k[i][e] = v[i][e] = 0.0f;
+      if (a >= 0) loadE(static_cast<const T*>(key_base(p, false)) + a, k[i]);
+      if (b >= 0) loadE(static_cast<const T*>(key_base(p, true)) + b, v[i]);
+    }
+    // Dot products: value rr * kKeys + i of a butterfly is row rr, key i.
+    float s[NB];  // this lane's row and key of each butterfly
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      float x[32];
+#pragma unroll
+      for (int z = 0; z < 32; ++z) {
+        const int r = n * (32 / kKeys) + z / kKeys, i = z % kKeys;
+        float d = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) d = fmaf(q[r][e], k[i][e], d);
+        x[z] = d;
+      }
+      s[n] = butterfly(x, lane);
+      const int r = n * (32 / kKeys) + lane / kKeys, j = j0 + lane % kKeys;
+      s[n] = (j < k1 && j <= tile.pos0 + r / G) ? s[n] * c : -INFINITY;
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      float mx = s[n];  // over the row's 8 lanes
+#pragma unroll
+      for (int w = kKeys / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+#pragma unroll
+      for (int rr = 0; rr < 32 / kKeys; ++rr) {
+        const int r = n * (32 / kKeys) + rr;
+        const float mn = fmaxf(m[r], __shfl_sync(0xffffffffu, mx, rr * kKeys));
+        const float ref = mn == -INFINITY ? 0.0f : mn;
+        const float f = exp2f(m[r] - ref);
+        m[r] = mn;
+        l[r] *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[r][e] *= f;
+        const float w = exp2f(s[n] - ref);  // of this lane's key, if it is of row r
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, rr * kKeys + i);
+          l[r] += wi;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[r][e] = fmaf(wi, v[i][e], acc[r][e]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][r][lane * E + e] = acc[r][e];
+    if (lane == 0) sml[warp][r] = make_float2(m[r], l[r]);
+  }
+  __syncthreads();
+  for (int r = warp; r < rows; r += W) {
+    float a[E] = {}, mm = -INFINITY, ll = 0.0f;
+    for (int w = 0; w < W; ++w) {
+      const float2 x = sml[w][r];
+      const float mn = fmaxf(mm, x.x);
+      const float f = mm == -INFINITY ? 0.0f : exp2f(mm - mn);
+      const float g = x.x == -INFINITY ? 1.0f : exp2f(x.x - mn);  // (0, or a NaN: kept)
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] = fmaf(a[e], f, g * so[w][r][lane * E + e]);
+      ll = fmaf(ll, f, g * x.y);
+      mm = mn;
+    }
+    const int t = tile.t0 + r / G, h = hkv * G + r % G;
+    bool finite = isfinite(ll);
+#pragma unroll
+    for (int e = 0; e < E; ++e) finite = finite && isfinite(a[e]);
+    if (!__all_sync(0xffffffffu, finite))
+      exact_row<T, D>(p, tile.s, base, t, h, k0, min(k1, tile.pos0 + r / G + 1), a, mm, ll);
+    if (splits > 1) {
+      const Partials part(p.ws, (int64_t)gridDim.x * splits, RB, D);
+      part.put<E>(((int64_t)id * p.Hkv + hkv) * splits + blockIdx.y, r, lane, a, mm, ll);
+    } else {
+      finish_row<T, D>(p, t, h, lane, a, mm, ll);
     }
   }
 }
@@ -239,26 +432,68 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
   finish_row<T, D>(p, tile.t0 + r / G, hkv * G + r % G, lane, acc, m, l);
 }
 
-int pick_splits(int64_t ctas, int64_t max_kv) {
-  // Twice the SMs in flight, ranges of at least 4 key blocks.
-  const int64_t want = (2 * 152 + ctas - 1) / ctas, most = max_kv / (4 * BN);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, kMaxSplits}));
+// Rows of the row kernel's CTA that hold `need` of them; 0: too many (its warps'
+// sums, 8 x rows x D, take 32 KB of shared memory at most, and the registers).
+int row_block(int64_t need, int64_t D) {
+  for (int rb = 4; rb <= 16 && rb * D <= 1024; rb <<= 1)
+    if (need <= rb) return rb;
+  return 0;
+}
+
+int row_splits(int64_t ctas, int64_t max_kv) {
+  // Four CTAs per SM, ranges of at least 16 keys a warp.
+  const int64_t want = (4 * 152 + ctas - 1) / ctas, most = max_kv / 128;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 64}));
+}
+
+template <typename T, int D, int RB>
+cudaError_t launch_rows(const AttnLaunch& p, cudaStream_t st) {
+  const int TT = RB / (p.Hq / p.Hkv);
+  const int64_t ctas = tile_bound(p.T, p.N, TT) * p.Hkv;
+  const int splits = row_splits(ctas, (int64_t)p.max_pages * p.page_size);
+  attn_rows_kernel<T, D, RB><<<dim3((unsigned)ctas, splits), kThreads, 0, st>>>(p, splits);
+  note_launch();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || splits == 1) return e;
+  return launch_attn_join(p, splits, RB, TT, st);
 }
 
 template <typename T, int D>
 cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
   const int G = p.Hq / p.Hkv, TT = BM / G;
-  const int64_t ctas = tile_bound(p.T, p.N, TT) * p.Hkv;
-  const int64_t max_kv = p.table ? (int64_t)p.max_pages * p.page_size : 0;
-  const int splits = pick_splits(ctas, max_kv);
+  if (p.table != nullptr) {
+    switch (row_block((int64_t)p.max_q * G, D)) {
+      case 4: return launch_rows<T, D, 4>(p, st);
+      case 8:
+        if constexpr (D <= 128) return launch_rows<T, D, 8>(p, st);
+        break;
+      case 16:
+        if constexpr (D <= 64) return launch_rows<T, D, 16>(p, st);
+        break;
+    }
+  }
+  const int64_t items = tile_bound(p.T, p.N, TT) * p.Hkv;
+  // A cluster per tile, large enough for about four CTAs per SM: two are resident,
+  // and shares of unequal tiles even out over the rest.
+  int ranks = 1;
+  while (ranks < kMaxCluster && items * ranks < 4 * 152) ranks <<= 1;
   static const cudaError_t attr = cudaFuncSetAttribute(
       attn_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
   if (attr != cudaSuccess) return attr;
-  attn_simt_kernel<T, D><<<dim3((unsigned)ctas, splits), kThreads, sizeof(Smem<D>), st>>>(p, splits);
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ranks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(items * ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Smem<D>);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_simt_kernel<T, D>, p);
   note_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || splits == 1) return e;
-  return launch_attn_join(p, splits, BM, TT, st);
+  return e;
 }
 
 template <typename T>
@@ -273,10 +508,14 @@ cudaError_t by_dim(const AttnLaunch& p, cudaStream_t st) {
 
 }  // namespace
 
-size_t attn_simt_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D) {
-  const int64_t ctas = tile_bound(T, N, BM / (Hq / Hkv)) * Hkv;
-  const int splits = pick_splits(ctas, INT64_MAX);
-  return splits > 1 ? Partials::bytes(ctas * splits, BM, D) : 0;
+size_t attn_simt_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
+                                 int64_t max_q) {
+  const int64_t G = Hq / Hkv;
+  const int rb = row_block(max_q * G, D);
+  if (rb == 0) return 0;
+  const int64_t ctas = tile_bound(T, N, rb / G) * Hkv;
+  const int splits = row_splits(ctas, INT64_MAX);
+  return splits > 1 ? Partials::bytes(ctas * splits, rb, D) : 0;
 }
 
 cudaError_t launch_attn_join(const AttnLaunch& p, int splits, int bm, int TT, cudaStream_t st) {

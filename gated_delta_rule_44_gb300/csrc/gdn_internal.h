@@ -232,7 +232,8 @@ cudaError_t launch_attn_simt(const AttnLaunch& p, cudaStream_t s);
 // Joins the sums of `splits` key ranges per tile of TT tokens, left in p.ws in
 // blocks of bm rows.
 cudaError_t launch_attn_join(const AttnLaunch& p, int splits, int bm, int TT, cudaStream_t s);
-size_t attn_simt_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D);
+size_t attn_simt_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
+                                 int64_t max_q);
 // Tensor-core form: bf16, D in {64, 128, 256}, pages of a multiple of 16 rows.
 bool attn_tc_supported(const AttnLaunch& p);
 cudaError_t launch_attn_tc(const AttnLaunch& p, cudaStream_t s);

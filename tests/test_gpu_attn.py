@@ -509,3 +509,39 @@ def test_side_stream_and_graph_replay(cuda_device):
         assert torch.equal(x, y) and torch.equal(x, z)
     assert torch.equal(e[0], c[0]) and torch.equal(e[1], c[1])
     B.gdn_read_device_status()
+
+
+# ---- f32 and other sizes: few rows, clusters of key shares -------------------------
+
+@pytest.mark.parametrize("case", [
+    (None, [700, 5, 0, 64], 16, 1, 64, 16, F32, True, "head"),     # 16 rows at D = 64
+    (None, [300, 129], 8, 1, 128, 64, F32, False, "token"),        # 8 rows
+    ([2, 1, 2], [900, 1, 2], 4, 2, 128, 7, F32, True, "joint"),    # 2 tokens x 2 heads
+    ([1, 4], [33, 600], 1, 1, 256, 16, F32, False, "head"),        # 4 rows at D = 256
+    ([3, 2], [40, 500], 6, 2, 32, 3, BF, False, "head"),           # 9 rows at D = 32
+    ([9, 30], [9, 1500], 8, 2, 256, 16, F32, True, "head"),        # tiles in clusters
+    ([200], [900], 12, 4, 64, 9, BF, False, "head"),               # bf16, pages of 9
+])
+def test_paged_cuda_cores(case, cuda_device):
+    out, lse, ro, rl, pieces, dtype = run_paged(case, cuda_device)
+    B.gdn_read_device_status()
+    R.check(R.f64(out), ro, R.bound(ro, pieces, dtype, dtype == BF), "out")
+    R.check(R.f64(lse), rl, R.lse_bound(rl, pieces), "lse")
+
+
+def test_paged_poisoned_rows_cuda_cores(cuda_device):
+    """A later token's infinite value, in f32: earlier rows of the same call keep
+    their results (few rows, and tiles in clusters)."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(12)
+    for q_len, D in ((2, 128), (40, 64)):
+        kc, vc, table = make_paged(g, [400], 1, D, 16, F32, dev, poison=False)
+        q = torch.randn(q_len, 2, D, generator=g).to(dev)
+        kv = torch.tensor([400], dtype=torch.int32, device=dev)
+        cu = cu_of([q_len], dev)
+        clean, out = torch.empty_like(q), torch.empty_like(q)
+        B.gdn_attn_paged(q, kc, vc, table, kv, cu, clean, max_q_len=q_len)
+        vc[table[0, 24], 0, 15] = float("inf")  # position 399, the last token's own
+        B.gdn_attn_paged(q, kc, vc, table, kv, cu, out, max_q_len=q_len)
+        torch.testing.assert_close(out[:-1], clean[:-1], rtol=1e-5, atol=1e-6)
+        assert not torch.isfinite(out[-1]).any()
