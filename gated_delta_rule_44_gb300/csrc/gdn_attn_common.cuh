@@ -136,20 +136,6 @@ struct Partials {
     for (int e = 0; e < E; ++e) d[e] = acc[e];
     if (lane == 0) ml[slot * rows + r] = make_float2(m, l);
   }
-  // acc, m, l <- the sums over both key ranges.  A range without keys (m = -inf)
-  // adds nothing.
-  template <int E>
-  __device__ void add(int64_t slot, int r, int lane, float (&acc)[E], float& m, float& l) const {
-    const float2 x = ml[slot * rows + r];
-    if (x.x == -INFINITY) return;
-    const float mn = fmaxf(m, x.x);
-    const float f = m == -INFINITY ? 0.0f : exp2f(m - mn), g = exp2f(x.x - mn);
-    const float* s = o + (slot * rows + r) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, g * s[e]);
-    l = fmaf(l, f, g * x.y);
-    m = mn;
-  }
 #endif
 };
 
@@ -181,6 +167,107 @@ __device__ __forceinline__ void finish_row(const AttnLaunch& p, int t, int h, in
   }
   if (p.lse != nullptr && lane == 0)
     p.lse[(int64_t)t * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// A joining kernel is launched with programmatic dependence on the kernel whose
+// sums it joins: its launch is prepared while that one runs.
+__device__ __forceinline__ void start_next_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+template <typename... K, typename... A>
+cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, cudaStream_t st, const A&... a) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
+  note_launch();
+  return e;
+}
+
+// Joins the n ranges of a row,
+//   out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z,
+// whose sums are in the blocks slot_of(z) (negative: none), by RW warps of a CTA
+// of 8: warp w takes z = w, w + RW, ...: the (m, l) of 32 ranges first, a lane
+// each, then their weighted O, four loads in flight.  The order of the sums
+// depends on n alone.
+template <typename T, int D, int RW, typename SlotOf>
+__device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& part, int n,
+                                         SlotOf slot_of, int r, bool live, int t, int h) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % RW;
+  float acc[E] = {}, m = -INFINITY, l = 0.0f;
+  for (int z0 = 0; live && w + z0 * RW < n; z0 += 32) {
+    const int z = w + (z0 + lane) * RW;
+    const int64_t slot = z < n ? slot_of(z) : -1;
+    const float2 ml = slot >= 0 ? part.ml[slot * part.rows + r] : make_float2(-INFINITY, 0.0f);
+    float mn = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mn = fmaxf(mn, m);
+    if (mn == -INFINITY) continue;
+    const float f = exp2f(m - mn);  // 0 for m = -inf
+    const float wt = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mn);
+    float lw = ml.x == -INFINITY ? 0.0f : wt * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    l = fmaf(l, f, lw);
+    m = mn;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= f;
+    unsigned todo = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
+    while (todo) {
+      float x[4][E], wk[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        wk[k] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[k][e] = 0.0f;
+        if (todo) {
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          wk[k] = __shfl_sync(0xffffffffu, wt, src);
+          const int64_t sk = __shfl_sync(0xffffffffu, slot, src);
+          const float* o = part.o + (sk * part.rows + r) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[k][e] = o[e];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wk[k], x[k][e], acc[e]);
+    }
+  }
+  if constexpr (RW > 1) {
+    __shared__ float so[8][D];
+    __shared__ float2 sml[8];
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (w != 0) return;
+    for (int k = 1; k < RW; ++k) {
+      const float2 x = sml[warp + k];
+      if (x.x == -INFINITY) continue;
+      const float mn = fmaxf(m, x.x);
+      const float f = m == -INFINITY ? 0.0f : exp2f(m - mn), g = exp2f(x.x - mn);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, g * so[warp + k][lane * E + e]);
+      l = fmaf(l, f, g * x.y);
+      m = mn;
+    }
+  }
+  if (live) finish_row<T, D>(p, t, h, lane, acc, m, l);
 }
 
 // One row (token t, query head h) over the keys [k0, k1) of its sequence, by

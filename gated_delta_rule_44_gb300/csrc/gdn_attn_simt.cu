@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const __grid_consta
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = p.Hq / p.Hkv, TT = RB / G;
   const int id = blockIdx.x / p.Hkv, hkv = blockIdx.x % p.Hkv;
+  start_next_kernel();
   const SeqTile tile = find_tile(p, id, TT);
   if (tile.bad && threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
   if (tile.nt == 0) return;
@@ -414,22 +415,19 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const __grid_consta
   }
 }
 
-// Joins the key ranges of a row: out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z.
-template <typename T, int D>
+// Joins the key ranges of the rows of each tile, RW warps to a row.
+template <typename T, int D, int RW>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_constant__ AttnLaunch p,
                                                              int splits, int bm, int TT) {
+  wait_for_previous_kernel();
   const int G = p.Hq / p.Hkv;
   const int id = (int)(blockIdx.x / p.Hkv), hkv = blockIdx.x % p.Hkv;
   const SeqTile tile = find_tile(p, id, TT);
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5);
-  if (r >= tile.nt * G) return;
+  const int r = (blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5)) / RW;
   const Partials part(p.ws, (int64_t)gridDim.x * splits, bm, D);
-  constexpr int E = D / 32;
-  float acc[E] = {}, m = -INFINITY, l = 0.0f;
   const int64_t slot = ((int64_t)id * p.Hkv + hkv) * splits;
-  for (int z = 0; z < splits; ++z) part.add<E>(slot + z, r, lane, acc, m, l);
-  finish_row<T, D>(p, tile.t0 + r / G, hkv * G + r % G, lane, acc, m, l);
+  join_row<T, D, RW>(p, part, splits, [&](int z) { return slot + z; }, r, r < tile.nt * G,
+                     tile.t0 + r / G, hkv * G + r % G);
 }
 
 // Rows of the row kernel's CTA that hold `need` of them; 0: too many (its warps'
@@ -473,10 +471,10 @@ cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
     }
   }
   const int64_t items = tile_bound(p.T, p.N, TT) * p.Hkv;
-  // A cluster per tile, large enough for about four CTAs per SM: two are resident,
-  // and shares of unequal tiles even out over the rest.
+  // A cluster per tile, large enough for two CTAs per SM.  (1024 tokens, 8 heads,
+  // D = 128: 187, 122, 103 and 154 us with 1, 2, 4 and 8; the rule takes 4.)
   int ranks = 1;
-  while (ranks < kMaxCluster && items * ranks < 4 * 152) ranks <<= 1;
+  while (ranks < kMaxCluster && items * ranks < 2 * 152) ranks <<= 1;
   static const cudaError_t attr = cudaFuncSetAttribute(
       attn_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
   if (attr != cudaSuccess) return attr;
@@ -518,21 +516,36 @@ size_t attn_simt_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, 
   return splits > 1 ? Partials::bytes(ctas * splits, rb, D) : 0;
 }
 
-cudaError_t launch_attn_join(const AttnLaunch& p, int splits, int bm, int TT, cudaStream_t st) {
-  const dim3 grid((unsigned)(tile_bound(p.T, p.N, TT) * p.Hkv), (bm + kThreads / 32 - 1) / (kThreads / 32));
-  if (p.bf16) {
-    if (p.D == 32) attn_join_kernel<__nv_bfloat16, 32><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
-    else if (p.D == 64) attn_join_kernel<__nv_bfloat16, 64><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
-    else if (p.D == 128) attn_join_kernel<__nv_bfloat16, 128><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
-    else attn_join_kernel<__nv_bfloat16, 256><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
-  } else {
-    if (p.D == 32) attn_join_kernel<float, 32><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
-    else if (p.D == 64) attn_join_kernel<float, 64><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
-    else if (p.D == 128) attn_join_kernel<float, 128><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
-    else attn_join_kernel<float, 256><<<grid, kThreads, 0, st>>>(p, splits, bm, TT);
+namespace {
+
+template <typename T, int D>
+cudaError_t join(const AttnLaunch& p, int splits, int bm, int TT, cudaStream_t st) {
+  const int64_t ctas = tile_bound(p.T, p.N, TT) * p.Hkv;
+  const int rows = TT * (p.Hq / p.Hkv);
+  // Eight warps to a row when there is a range for each (5 instead of 16 us for 16
+  // ranges of 8 rows), else a warp.
+  if (splits >= 8)
+    return launch_after(attn_join_kernel<T, D, 8>, dim3((unsigned)ctas, rows), kThreads, st, p, splits,
+                        bm, TT);
+  return launch_after(attn_join_kernel<T, D, 1>, dim3((unsigned)ctas, (rows + 7) / 8), kThreads, st, p,
+                      splits, bm, TT);
+}
+
+template <typename T>
+cudaError_t join_by_dim(const AttnLaunch& p, int splits, int bm, int TT, cudaStream_t st) {
+  switch (p.D) {
+    case 32: return join<T, 32>(p, splits, bm, TT, st);
+    case 64: return join<T, 64>(p, splits, bm, TT, st);
+    case 128: return join<T, 128>(p, splits, bm, TT, st);
+    default: return join<T, 256>(p, splits, bm, TT, st);
   }
-  note_launch();
-  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_join(const AttnLaunch& p, int splits, int bm, int TT, cudaStream_t st) {
+  return p.bf16 ? join_by_dim<__nv_bfloat16>(p, splits, bm, TT, st)
+                : join_by_dim<float>(p, splits, bm, TT, st);
 }
 
 cudaError_t launch_attn_simt(const AttnLaunch& p, cudaStream_t st) {

@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.Hq / p.Hkv;
 
+  start_next_kernel();
   if (warp == 0) {
     if (lane == 0) {
       constexpr int kReleases = NQ == 2 ? 2 : 1;  // MMA warps that use a unit
@@ -1073,76 +1074,35 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 }
 
 // Joins the ranges of the pairs that the stream form cut: CTA c serves the pair
-// that range c began and left open; its further sums are in the blocks of the
-// CTAs after it, in the order of their keys.  A block takes 8 rows, a warp one
-// row at a time: the ranges' (m, l) first, a lane each, then the weighted sum of
-// their O, whose loads do not wait for one another.
+// that range c began and left open, a row of it per blockIdx.y and its multiples;
+// its further sums are in the blocks of the CTAs after it, in the order of their
+// keys.
 template <int D>
 __global__ void __launch_bounds__(256) attn_stream_join_kernel(const __grid_constant__ AttnLaunch p,
                                                                const __grid_constant__ TcArgs a) {
+  wait_for_previous_kernel();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const int4 mine = a.info[c0];
   if (mine.x < 0) return;
   const int G = p.Hq / p.Hkv;
   const SeqRange q = seq_range(p, mine.x);
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int rows = min(q.b - q.a, p.max_q) * G;
+  if ((int)blockIdx.y >= rows) return;
   // The last range: the first after c0 that ends the pair.
   int c1 = c0;
   for (int c = c0 + 1; c1 == c0 && c < a.ctas; c += 32) {
     const unsigned ends = __ballot_sync(0xffffffffu, c + lane < a.ctas && a.info[c + lane].z == 1);
     c1 = ends ? c + __ffs(ends) - 1 : (c + 32 >= a.ctas ? a.ctas - 1 : c0);
   }
-  if (r >= min(q.b - q.a, p.max_q) * G) return;
   const Partials part(a.ws, 2 * (int64_t)a.ctas, a.rows, D);
-  constexpr int E = D / 32;
-  float acc[E] = {}, m = -INFINITY, l = 0.0f;
-  for (int c = c0; c <= c1; c += 32) {
-    // Range c + lane: block 2 c0 + 1 for the first, 2 c' for the rest; CTAs
-    // without a range (z = 2) hold nothing.
-    const int cl = c + lane;
-    const int64_t slot = 2 * (int64_t)cl + (cl == c0 ? 1 : 0);
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (cl <= c1 && (cl == c0 || a.info[cl].z != 2)) ml = part.ml[slot * a.rows + r];
-    float mn = ml.x;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mn = fmaxf(mn, m);
-    if (mn == -INFINITY) continue;
-    const float f = exp2f(m - mn);  // 0 for m = -inf
-    const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mn);
-    float lw = ml.x == -INFINITY ? 0.0f : w * ml.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-    l = fmaf(l, f, lw);
-    m = mn;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= f;
-    unsigned live = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
-    while (live) {  // four ranges' loads in flight
-      float x[4][E], wk[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        wk[k] = 0.0f;
-        if (live) {
-          const int src = __ffs(live) - 1;
-          live &= live - 1;
-          wk[k] = __shfl_sync(0xffffffffu, w, src);
-          const int ck = c + src;
-          const float* o = part.o + ((2 * (int64_t)ck + (ck == c0 ? 1 : 0)) * a.rows + r) * D + lane * E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[k][e] = o[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[k][e] = 0.0f;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(wk[k], x[k][e], acc[e]);
-    }
+  // Block 2 c0 + 1 for the first range, 2 c for the rest; none for a CTA without one.
+  auto slot_of = [&](int z) -> int64_t {
+    return z == 0 ? 2 * (int64_t)c0 + 1 : a.info[c0 + z].z == 2 ? -1 : 2 * (int64_t)(c0 + z);
+  };
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    join_row<bf16, D, 8>(p, part, c1 - c0 + 1, slot_of, r, true, q.a + r / G, mine.y * G + r % G);
+    __syncthreads();
   }
-  finish_row<bf16, D>(p, q.a + r / G, mine.y * G + r % G, lane, acc, m, l);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -1229,9 +1189,7 @@ cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
     a.ws = reinterpret_cast<float*>(static_cast<char*>(p.ws) + info_bytes(sms));
     cudaError_t e = run<D, 1, true, true>(p, a, dim3(sms), st);
     if (e != cudaSuccess) return e;
-    attn_stream_join_kernel<D><<<dim3(sms, (a.rows + 7) / 8), 256, 0, st>>>(p, a);
-    note_launch();
-    return cudaGetLastError();
+    return launch_after(attn_stream_join_kernel<D>, dim3(sms, std::min(a.rows, 16)), 256, st, p, a);
   }
   a.q_box = a.TQ;
   const int TT = NQ * a.TQ;
