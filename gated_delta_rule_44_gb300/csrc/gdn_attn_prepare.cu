@@ -10,11 +10,14 @@
 // row p % page of page table[s, p / page]; v to the cache.  All arithmetic in
 // f32, one rounding at the store.
 //
-// HBM-bound: every row is read and written once in 16-byte vectors.  D / 8
-// lanes own one token and 8 dims each, so the norm is a shuffle reduction, the
-// rotary partner (R / 2 dims away, a whole number of lanes) is one shuffle,
-// and the table row and the norm weights stay in registers while the lanes
-// walk a range of the token's heads.
+// HBM-bound: every row is read and written once.  D / 8 lanes own one token and
+// 8 dims each: of the rotated ones 4 and their 4 partners R / 2 further on, so that
+// a rotation stays inside a lane; of the others 8 in a row.  The table row and the
+// norm weights stay in registers while the lanes walk a range of the token's
+// heads.  What binds before HBM is the number of instructions of a row: with
+// partners fetched by shuffles and addresses multiplied out per head, 222 of them
+// took 44 us where HBM takes 25 (four 2048-token prompts of 16 + 2 + 2 heads of
+// 256); now about 100 take 39, 64 % of the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,96 +28,100 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // heads whose loads are in flight before the first is used
+constexpr int kDepth = 2;  // heads on their way while as many are worked on (4: 43 for 39 us)
 
+// 8 values of a row: 4 at lo, 4 at hi.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
-  uint4 r;
-  __device__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
+  uint2 a, b;
+  __device__ void load(const __nv_bfloat16* p, int lo, int hi) {
+    a = *reinterpret_cast<const uint2*>(p + lo);
+    b = *reinterpret_cast<const uint2*>(p + hi);
+  }
   __device__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  __device__ static void store(__nv_bfloat16* p, const float (&x)[8]) {
+  __device__ static Vec8 of(const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return {make_uint2(w[0], w[1]), make_uint2(w[2], w[3])};
   }
-  __device__ void copy(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = r; }
+  __device__ void store(__nv_bfloat16* p, int lo, int hi) const {
+    *reinterpret_cast<uint2*>(p + lo) = a;
+    *reinterpret_cast<uint2*>(p + hi) = b;
+  }
 };
 template <>
 struct Vec8<float> {
   float4 a, b;
-  __device__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+  __device__ void load(const float* p, int lo, int hi) {
+    a = *reinterpret_cast<const float4*>(p + lo);
+    b = *reinterpret_cast<const float4*>(p + hi);
   }
   __device__ void get(float (&x)[8]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
-  __device__ static void store(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  __device__ static Vec8 of(const float (&x)[8]) {
+    return {make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7])};
   }
-  __device__ void copy(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
+  __device__ void store(float* p, int lo, int hi) const {
+    *reinterpret_cast<float4*>(p + lo) = a;
+    *reinterpret_cast<float4*>(p + hi) = b;
   }
 };
 
-// The last sequence s with cu[s] <= t.  A decode batch (t = s) and a single
-// sequence are tried first: a binary search is a chain of dependent loads.
+// The last sequence s with cu[s] <= t, for the warp's first token t: 32 probes at
+// a time, a lane each, so that the chain of dependent loads is log32 N long.  A
+// decode batch's answer, s = t, is tried beside the first probes.
 __device__ __forceinline__ int find_seq(const int32_t* cu, int N, int t) {
-  if (cu == nullptr) return t;
-  if (t < N && cu[t] == t && cu[t + 1] == t + 1) return t;
-  int lo = 0, hi = N - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu[mid] <= t) lo = mid;
-    else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = N;  // the answer is in lo .. lo + n - 1
+  const bool guess = t < N && cu[t] == t && cu[t + 1] == t + 1;
+  for (;;) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const unsigned below = __ballot_sync(0xffffffffu, at < lo + n && cu[at] <= t);
+    if (guess) return t;
+    // cu rises, so the lanes below are the first ones (of malformed offsets any
+    // answer will do: the caller checks it).
+    lo += max(0, __popc(below) - 1) * step;
+    n = min(step, N - lo);
+    if (step == 1) return lo;
   }
-  return lo;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) attn_prepare_kernel(
+__global__ void __launch_bounds__(kThreads, 4) attn_prepare_kernel(
     const __grid_constant__ AttnPrepareLaunch p, int heads, int heads_per_group) {
   constexpr int LG = D / 8;               // lanes of a token
   constexpr int GROUPS = kThreads / LG;   // tokens of a CTA
-  const int lane = threadIdx.x % LG, d0 = lane * 8;
+  const int lane = threadIdx.x % LG;
   const int t = blockIdx.x * GROUPS + threadIdx.x / LG;
-  const bool live = t < p.T;
+  const int t_first = blockIdx.x * GROUPS + (threadIdx.x & ~31) / LG;  // the warp's first token
+  if (t_first >= p.T) return;
   const int h0 = blockIdx.y * heads_per_group, h1 = min(heads, h0 + heads_per_group);
   const unsigned grp = (LG == 32) ? 0xffffffffu
                                   : ((1u << (LG & 31)) - 1u) << ((threadIdx.x & 31) / LG * LG);
-
-  auto src = [&](int h) -> const T* {
-    if (h < p.Hq) return static_cast<const T*>(p.q.p) + (int64_t)t * p.q.ts + (int64_t)h * p.q.hs;
-    h -= p.Hq;
-    if (h < p.Hkv) return static_cast<const T*>(p.k.p) + (int64_t)t * p.k.ts + (int64_t)h * p.k.hs;
-    h -= p.Hkv;
-    return static_cast<const T*>(p.v.p) + (int64_t)t * p.v.ts + (int64_t)h * p.v.hs;
-  };
-  if (!live) return;  // whole groups leave: the shuffles below stay inside a group
-
-  Vec8<T> raw[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (h0 + i < h1) raw[i].load(src(h0 + i) + d0);
+  // This lane's dims.
+  const bool rotates = lane < p.rot / 8;
+  const int lo = rotates ? lane * 4 : lane * 8, hi = rotates ? p.rot / 2 + lane * 4 : lane * 8 + 4;
 
   // The token's sequence, position, table row and cache row.
-  const int s = find_seq(p.cu, p.N, t);
+  int s = p.cu == nullptr ? t : find_seq(p.cu, p.N, t_first);
+  if (t >= p.T) return;  // whole groups leave: the shuffles below stay inside a group
+  if (p.cu != nullptr)   // the warp's later tokens may be in later sequences
+    while (s + 1 < p.N && p.cu[s + 1] <= t) ++s;
   const int a = attn::cu_at(p.cu, s), b = attn::cu_at(p.cu, s + 1);
   unsigned bad = 0;
   if (s >= p.N || a > t || b <= t || b > p.T || (s == 0 && a != 0) || (s == p.N - 1 && b != p.T))
@@ -140,9 +147,7 @@ __global__ void __launch_bounds__(kThreads) attn_prepare_kernel(
       }
     }
   }
-  float c8[8], s8[8];
-  const int half = p.rot >> 1;
-  const bool rotates = d0 < p.rot;
+  float c4[4], s4[4];
   bool shown = pos >= 0;  // a token without a position gives a zero q and k
   if (p.rot > 0 && shown) {
     const int rp = p.positions ? p.positions[t] : pos;
@@ -151,85 +156,91 @@ __global__ void __launch_bounds__(kThreads) attn_prepare_kernel(
       shown = false;
       page = -1;
     } else if (rotates) {
-      const float* cs = p.cos_sin + (int64_t)rp * p.rot + (d0 < half ? d0 : d0 - half);
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        *reinterpret_cast<float4*>(&c8[i]) = *reinterpret_cast<const float4*>(cs + i);
-        *reinterpret_cast<float4*>(&s8[i]) = *reinterpret_cast<const float4*>(cs + half + i);
-      }
-      // The lower half of a pair subtracts its partner's sine term.
-      if (d0 < half) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s8[i] = -s8[i];
-      }
+      const float* cs = p.cos_sin + (int64_t)rp * p.rot + lo;
+      *reinterpret_cast<float4*>(c4) = *reinterpret_cast<const float4*>(cs);
+      *reinterpret_cast<float4*>(s4) = *reinterpret_cast<const float4*>(cs + p.rot / 2);
     }
   }
   if (bad && lane == 0) atomicOr(p.status, bad);
-  // The lane (of the whole warp) that holds the partner dims, R / 2 away.
-  const int wl = threadIdx.x & 31;
-  const int partner = !rotates ? wl : (d0 < half ? wl + half / 8 : wl - half / 8);
 
-  float qw[8], kw[8];
-  if (p.q_w && h0 < p.Hq) {
-    Vec8<T> w;
-    w.load(static_cast<const T*>(p.q_w) + d0);
-    w.get(qw);
-  }
-  if (p.k_w && h1 > p.Hq) {
-    Vec8<T> w;
-    w.load(static_cast<const T*>(p.k_w) + d0);
-    w.get(kw);
-  }
-
-  for (int hb = h0; hb < h1; hb += kAhead) {
+  // Heads first .. last - 1 of q or k: norm, rotation, store to one or two places.
+  auto rows = [&](const AttnRows& r, const void* weight, int first, int last, T* out, T* cache,
+                  int64_t cache_hs) {
+    if (first >= last) return;
+    const T* in = static_cast<const T*>(r.p) + (int64_t)t * r.ts + (int64_t)first * r.hs;
+    if (out != nullptr) out += (int64_t)first * D;
+    if (cache != nullptr) cache += (int64_t)first * cache_hs;
+    Vec8<T> next[kDepth];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int h = hb + i;
-      if (h >= h1) break;
-      if (h >= p.Hq + p.Hkv) {  // v: copied
-        if (page >= 0)
-          raw[i].copy(static_cast<T*>(p.vc.p) + page * p.vc.ps +
-                      (int64_t)(h - p.Hq - p.Hkv) * p.vc.hs + (int64_t)row * p.vc.ts + d0);
-        continue;
+    for (int i = 0; i < kDepth; ++i)
+      if (first + i < last) next[i].load(in + i * r.hs, lo, hi);
+    float w[8];
+    if (weight != nullptr) {
+      Vec8<T> v;
+      v.load(static_cast<const T*>(weight), lo, hi);
+      v.get(w);
+    }
+#pragma unroll 1
+    for (int hb = first; hb < last; hb += kDepth) {
+      Vec8<T> cur[kDepth];
+      in += kDepth * r.hs;
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {
+        cur[i] = next[i];
+        if (hb + kDepth + i < last) next[i].load(in + i * r.hs, lo, hi);
       }
-      const bool is_q = h < p.Hq;
-      float x[8];
-      raw[i].get(x);
-      if (is_q ? p.q_w != nullptr : p.k_w != nullptr) {
-        float ss = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int i = 0; i < kDepth; ++i) {
+        if (hb + i >= last) break;
+        float x[8];
+        cur[i].get(x);
+        if (weight != nullptr) {
+          float ss = 0.0f;
 #pragma unroll
-        for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(grp, ss, o);
-        const float inv = math::rms_inv(ss, 1.0f / D, p.eps);
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv * (is_q ? qw[e] : kw[e]);
-      }
-      if (p.rot > 0) {
+          for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(grp, ss, o);
+          const float inv = math::rms_inv(ss, 1.0f / D, p.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = __shfl_sync(grp, x[e], partner);
-          if (rotates) x[e] = fmaf(x[e], c8[e], y * s8[e]);
+          for (int e = 0; e < 8; ++e) x[e] *= inv * w[e];
+        }
+        if (rotates) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float u = x[e], v = x[e + 4];
+            x[e] = fmaf(u, c4[e], -v * s4[e]);
+            x[e + 4] = fmaf(v, c4[e], u * s4[e]);
+          }
+        }
+        if (!shown) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+        }
+        const Vec8<T> y = Vec8<T>::of(x);
+        if (out != nullptr) {
+          y.store(out, lo, hi);
+          out += D;
+        }
+        if (cache != nullptr) {
+          y.store(cache, lo, hi);
+          cache += cache_hs;
         }
       }
-      if (!shown) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-      }
-      if (is_q) {
-        Vec8<T>::store(static_cast<T*>(p.q_out) + ((int64_t)t * p.Hq + h) * D + d0, x);
-      } else {
-        const int hk = h - p.Hq;
-        if (p.k_out)
-          Vec8<T>::store(static_cast<T*>(p.k_out) + ((int64_t)t * p.Hkv + hk) * D + d0, x);
-        if (page >= 0)
-          Vec8<T>::store(static_cast<T*>(p.kc.p) + page * p.kc.ps + (int64_t)hk * p.kc.hs +
-                             (int64_t)row * p.kc.ts + d0, x);
-      }
     }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (hb + kAhead + i < h1) raw[i].load(src(hb + kAhead + i) + d0);
+  };
+  rows(p.q, p.q_w, h0, min(h1, p.Hq), static_cast<T*>(p.q_out) + (int64_t)t * p.Hq * D, nullptr, 0);
+  const int k0 = max(h0 - p.Hq, 0), k1 = min(h1 - p.Hq, p.Hkv);
+  rows(p.k, p.k_w, k0, k1, p.k_out ? static_cast<T*>(p.k_out) + (int64_t)t * p.Hkv * D : nullptr,
+       page >= 0 ? static_cast<T*>(p.kc.p) + page * p.kc.ps + (int64_t)row * p.kc.ts : nullptr,
+       p.kc.hs);
+  if (page >= 0) {
+    const T* in = static_cast<const T*>(p.v.p) + (int64_t)t * p.v.ts;
+    T* out = static_cast<T*>(p.vc.p) + page * p.vc.ps + (int64_t)row * p.vc.ts;
+    for (int h = max(h0 - p.Hq - p.Hkv, 0); h < h1 - p.Hq - p.Hkv; ++h) {
+      Vec8<T> v;
+      v.load(in + (int64_t)h * p.v.hs, lane * 8, lane * 8 + 4);
+      v.store(out + (int64_t)h * p.vc.hs, lane * 8, lane * 8 + 4);
+    }
   }
 }
 
@@ -239,9 +250,13 @@ cudaError_t launch(const AttnPrepareLaunch& p, cudaStream_t st) {
   // Without a cache the v heads have nowhere to go.
   const int used = p.Hq + (p.table ? 2 : 1) * p.Hkv;
   const unsigned gx = (unsigned)((p.T + GROUPS - 1) / GROUPS);
-  // Heads per group: 8 once that still leaves a few CTAs per SM, fewer before.
-  int per = 8;
-  while (per > 1 && (int64_t)gx * ((used + per - 1) / per) < 4 * 152) per >>= 1;
+  // Heads per group: all of them once that leaves two CTAs per SM, fewer before:
+  // what a group does before its first head (sequence, position, table rows) is a
+  // chain of loads and as many instructions as four heads.  (Four 2048-token
+  // prompts: 39, 42, 47 and 50 us with 20, 10, 5 and 4 heads; 512 single tokens
+  // of 40 heads: 13, 12, 13 and 15 us with 8, 4, 2 and 1; the rule takes 20 and 3.)
+  int per = used;
+  while (per > 1 && (int64_t)gx * ((used + per - 1) / per) < 2 * 152) per = (per + 1) / 2;
   const dim3 grid(gx, (unsigned)((used + per - 1) / per));
   attn_prepare_kernel<T, D><<<grid, kThreads, 0, st>>>(p, used, per);
   note_launch();
