@@ -277,7 +277,7 @@ constexpr int kKeys = 8;   // keys of a warp's step
 
 // RB rows at most: RB * kKeys / 32 butterflies per step.
 template <typename T, int D, int RB>
-__global__ void __launch_bounds__(kThreads) attn_rows_kernel(const __grid_constant__ AttnLaunch p,
+__global__ void __launch_bounds__(kThreads, RB * D <= 512 ? 2 : 1) attn_rows_kernel(const __grid_constant__ AttnLaunch p,
                                                              int splits) {
   constexpr int E = D / 32, W = kThreads / 32, NB = RB * kKeys / 32;
   __shared__ float so[W][RB][D];
@@ -321,15 +321,21 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const __grid_consta
       loadE(static_cast<const T*>(p.q.p) + (int64_t)(tile.t0 + r / G) * p.q.ts +
                 (int64_t)(hkv * G + r % G) * p.q.hs, q[r]);
   }
+  // Lane i < kKeys finds key i of a step, one step ahead.
+  int64_t next_k = -1, next_v = -1;
+  auto find = [&](int j) {
+    next_k = next_v = -1;
+    if (lane < kKeys && j < k1) {
+      next_k = key_offset(p, false, tile.s, base, hkv, j);
+      next_v = key_offset(p, true, tile.s, base, hkv, j);
+      if (next_k < 0) atomicOr(p.status, kStatusBadIndex);
+    }
+  };
+  find(k0 + warp * kKeys + lane);
+#pragma unroll 1
   for (int j0 = k0 + warp * kKeys; j0 < k1; j0 += W * kKeys) {
     float k[kKeys][E], v[kKeys][E];
-    // Lane i < kKeys finds key i.
-    int64_t ko = -1, vo = -1;
-    if (lane < kKeys && j0 + lane < k1) {
-      ko = key_offset(p, false, tile.s, base, hkv, j0 + lane);
-      vo = key_offset(p, true, tile.s, base, hkv, j0 + lane);
-      if (ko < 0) atomicOr(p.status, kStatusBadIndex);
-    }
+    const int64_t ko = next_k, vo = next_v;
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
       const int64_t a = __shfl_sync(0xffffffffu, ko, i), b = __shfl_sync(0xffffffffu, vo, i);
@@ -338,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const __grid_consta
       if (a >= 0) loadE(static_cast<const T*>(key_base(p, false)) + a, k[i]);
       if (b >= 0) loadE(static_cast<const T*>(key_base(p, true)) + b, v[i]);
     }
+    find(j0 + W * kKeys + lane);
     // Dot products: value rr * kKeys + i of a butterfly is row rr, key i.
     float s[NB];  // this lane's row and key of each butterfly
 #pragma unroll
@@ -439,7 +446,8 @@ int row_block(int64_t need, int64_t D) {
 }
 
 int row_splits(int64_t ctas, int64_t max_kv) {
-  // Four CTAs per SM, ranges of at least 16 keys a warp.
+  // Two CTAs per SM (about half the tile numbers are empty), ranges of at least 16
+  // keys a warp.
   const int64_t want = (4 * 152 + ctas - 1) / ctas, most = max_kv / 128;
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 64}));
 }
