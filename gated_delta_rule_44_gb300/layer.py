@@ -9,6 +9,11 @@ over every token; ``gdn_decode`` then takes rows [0, n_decode) and
 All buffers are torch tensors on one device; everything is asynchronous on the
 given stream.
 
+``AttnStep`` is the same for a full-attention layer of the stack: one
+``gdn_attn_prepare`` over every token, then attention over the paged cache for
+the decode rows and over the cache or, for new prompts, over the packed keys for
+the rest.
+
 ``GdnHostPipeline`` serves callers whose per-step inputs and outputs live in
 pinned host memory: it copies a step's inputs in and its output out on their
 own streams, so that they overlap the neighbouring steps' compute; the steps'
@@ -110,6 +115,70 @@ class GdnStep:
                                  cu_seqlens_host=cu_seqlens_prefill_host if host else None,
                                  state_indices_host=state_indices_host[nd:] if host else None,
                                  algo=self.algo, workspace=self.workspace, stream=stream)
+        return out
+
+
+class AttnStep:
+    """Preallocated intermediates (q, the prompts' keys, out, workspaces) for
+    batches of a fixed token count, and the calls of one full-attention step.
+
+    The batch is laid out like GdnStep's: n_decode single-token sequences first,
+    then sequences of up to max_q_len tokens.  ``new_prompts``: those later
+    sequences have no context before their tokens, so that their attention reads
+    the packed keys instead of the cache (which is filled all the same)."""
+
+    def __init__(self, T: int, N: int, n_decode: int, Hq: int, Hkv: int, D: int,
+                 act_dtype: torch.dtype, device, max_q_len: int = 0, new_prompts: bool = False,
+                 scale: float = -1.0):
+        self.T, self.N, self.n_decode = T, N, n_decode
+        self.Hq, self.Hkv, self.D = Hq, Hkv, D
+        self.new_prompts, self.scale = new_prompts, scale
+        dev = torch.device(device)
+        Tp, Np = T - n_decode, N - n_decode
+        self.max_q_len = min(max_q_len, Tp) if max_q_len > 0 else Tp
+        self.q = torch.empty((T, Hq, D), dtype=act_dtype, device=dev)
+        self.out = torch.empty((T, Hq, D), dtype=act_dtype, device=dev)
+        self.k = (torch.empty((T, Hkv, D), dtype=act_dtype, device=dev)
+                  if new_prompts and Np > 0 else None)
+        dt = B.GDN_DTYPE_BF16 if act_dtype == torch.bfloat16 else B.GDN_DTYPE_F32
+        ws = 0
+        if n_decode > 0:
+            ws = B.gdn_attn_paged_workspace_bytes(n_decode, n_decode, Hq, Hkv, D, 1, dt)
+        if Np > 0 and not new_prompts:
+            ws = max(ws, B.gdn_attn_paged_workspace_bytes(Tp, Np, Hq, Hkv, D, self.max_q_len, dt))
+        # One after the other on one stream: the two calls share it.
+        self.workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
+
+    def run(self, q, k, v, cu_seqlens, kv_lens, block_table, k_cache, v_cache, *,
+            cu_seqlens_prefill=None, gate=None, q_norm_weight=None, k_norm_weight=None,
+            norm_eps=1e-6, cos_sin=None, positions=None,
+            stream: Optional[torch.cuda.Stream] = None,
+            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """One step over the raw projections q, gate [T, Hq, D], k, v [T, Hkv, D]
+        (views of any row stride).  Writes the new keys and values into the cache
+        pages of block_table [N, max_pages], and the output to ``out`` (default:
+        this object's own buffer), which it returns.  cu_seqlens_prefill: the
+        offsets of the sequences after the decode rows, rebased to 0."""
+        nd = self.n_decode
+        out = self.out if out is None else out
+        B.gdn_attn_prepare(q, k, v, cu_seqlens, self.q, kv_lens=kv_lens, block_table=block_table,
+                           k_cache=k_cache, v_cache=v_cache, k_out=self.k,
+                           q_norm_weight=q_norm_weight, k_norm_weight=k_norm_weight,
+                           norm_eps=norm_eps, cos_sin=cos_sin, positions=positions, stream=stream)
+        if nd > 0:
+            B.gdn_attn_paged(self.q[:nd], k_cache, v_cache, block_table[:nd], kv_lens[:nd], None,
+                             out[:nd], max_q_len=1, scale=self.scale,
+                             gate=None if gate is None else gate[:nd], workspace=self.workspace,
+                             stream=stream)
+        if self.N > nd:
+            g = None if gate is None else gate[nd:]
+            if self.new_prompts:
+                B.gdn_attn_varlen(self.q[nd:], self.k[nd:], v[nd:], cu_seqlens_prefill, out[nd:],
+                                  scale=self.scale, gate=g, stream=stream)
+            else:
+                B.gdn_attn_paged(self.q[nd:], k_cache, v_cache, block_table[nd:], kv_lens[nd:],
+                                 cu_seqlens_prefill, out[nd:], max_q_len=self.max_q_len,
+                                 scale=self.scale, gate=g, workspace=self.workspace, stream=stream)
         return out
 
 
