@@ -851,12 +851,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         };
         if (jj > 1 && !idle)
           if (!new_reference()) return;
+        const bool raising = __any_sync(0xffffffffu, raise);
+        const int lim = last - kt * BK - half * 64;  // the row's last visible column
+        const bool masked = __any_sync(0xffffffffu, lim < 63);
         WAIT(sh->s_full[buf], ph);
         fence_after_sync();
         if (!idle) {
           const uint32_t ts = tmem + lanes + buf * 128;
-          const int lim = last - kt * BK - half * 64;  // the row's last visible column
-          const bool masked = __any_sync(0xffffffffu, lim < 63);
           // Publishes a maximum, cut to bf16: only the agreement matters.
           auto publish = [&](float t) {
             top_bits = __float_as_uint(t) >> 16;
@@ -884,7 +885,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             publish(t == -INFINITY ? t : t * c);  // (0 * -inf must not count as a score)
             if (!new_reference()) return;
           }
-          if (__any_sync(0xffffffffu, raise)) {
+          if (raising) {
             // O is at rest: in the two-tile form S j follows P V j-1, in the other
             // that product is waited for.
             if constexpr (NQ == 1) {
