@@ -292,7 +292,6 @@ __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int
   }
   m = -INFINITY;
   l = 0.0f;
-  bool nan = false;
   const float c = p.scale * kLog2e;
   for (int j = k0; j < k1; ++j) {
     const int64_t ko = key_offset(p, false, s, base, hkv, j);
@@ -306,7 +305,11 @@ __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     const float x = dot * c;
-    if (x != x) nan = true;
+    if (x != x) {  // no weight of the row is a number
+      m = 0.0f;
+      l = x;
+      return;
+    }
     if (x == -INFINITY && m == -INFINITY) continue;  // weight 0 beside any finite score
     const float mn = fmaxf(m, x);
     const float f = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
@@ -316,10 +319,6 @@ __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int
     const T* vr = static_cast<const T*>(key_base(p, true)) + (vo < 0 ? 0 : vo) + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * (vo < 0 ? 0.0f : to_f(vr[e])));
-  }
-  if (nan) {
-    m = 0.0f;
-    l = __int_as_float(0x7fc00000);
   }
 }
 

@@ -545,3 +545,105 @@ def test_paged_poisoned_rows_cuda_cores(cuda_device):
         B.gdn_attn_paged(q, kc, vc, table, kv, cu, out, max_q_len=q_len)
         torch.testing.assert_close(out[:-1], clean[:-1], rtol=1e-5, atol=1e-6)
         assert not torch.isfinite(out[-1]).any()
+
+
+# ---- what is written ------------------------------------------------------------------
+
+class Guarded:
+    """Buffers with 4 KB of a NaN bit pattern on either side."""
+
+    def __init__(self, dev):
+        self.dev, self.all = dev, []
+
+    def new(self, shape, dtype, fill=0.0):
+        n = int(np.prod(shape))
+        pad = 4096 // torch.empty(0, dtype=dtype).element_size()
+        raw = torch.empty(n + 2 * pad, dtype=dtype, device=self.dev)
+        raw.view(torch.uint8).fill_(0x7F)
+        raw.view(torch.uint8).add_(0x80)  # 0xff bytes
+        body = raw[pad:pad + n]
+        body.fill_(fill)
+        self.all.append((raw, pad, n))
+        return body.view(shape)
+
+    def check(self):
+        torch.cuda.synchronize()
+        for raw, pad, n in self.all:
+            for side in (raw[:pad], raw[pad + n:]):
+                assert (side.view(torch.uint8) == 0xFF).all()
+
+
+@pytest.mark.parametrize("dtype,D,page", [(BF, 128, 16), (BF, 256, 64), (BF, 64, 5), (F32, 128, 16),
+                                          (F32, 32, 16)])
+def test_nothing_is_written_outside(dtype, D, page, cuda_device):
+    dev = cuda_device
+    gd = Guarded(dev)
+    g = torch.Generator().manual_seed(D)
+    Hq, Hkv = 6, 2
+    for ql, kl in (([1, 1, 1], [3, 700, 0]), ([3, 1, 2], [40, 1, 500]), ([130, 5], [130, 900])):
+        T, N = sum(ql), len(ql)
+        width = -(-max(kl) // page)
+        kc = gd.new((N * width, Hkv, page, D), dtype)
+        vc = gd.new((N * width, Hkv, page, D), dtype)
+        table = torch.randperm(N * width, generator=g).to(torch.int32).view(N, width).to(dev)
+        kv = torch.tensor(kl, dtype=torch.int32, device=dev)
+        q, k, v = (randn(g, T, h, D, dtype=dtype).to(dev) for h in (Hq, Hkv, Hkv))
+        q_out, k_out = gd.new((T, Hq, D), dtype), gd.new((T, Hkv, D), dtype)
+        out, lse = gd.new((T, Hq, D), dtype), gd.new((T, Hq), F32)
+        need = B.gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max(ql), B._dt(q))
+        ws = gd.new((need,), torch.uint8, 0)
+        cs = torch.randn(max(kl) + 1, 32, generator=g).to(dev)
+        cu = cu_of(ql, dev)
+        B.gdn_attn_prepare(q, k, v, cu, q_out, kv_lens=kv, block_table=table, k_cache=kc, v_cache=vc,
+                           k_out=k_out, cos_sin=cs)
+        B.gdn_attn_paged(q_out, kc, vc, table, kv, cu, out, max_q_len=max(ql), lse=lse, workspace=ws)
+        B.gdn_attn_varlen(q_out, k_out, v, cu, out, lse=lse)
+        gd.check()
+    B.gdn_read_device_status()
+
+
+def test_results_repeat_bit_for_bit(cuda_device):
+    """No sum's order depends on timing: key ranges over SMs and clusters included."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(2)
+    for dtype, D, ql, kl in ((BF, 128, [1] * 5, [900, 31, 4000, 0, 77]), (BF, 256, [2, 3], [3000, 50]),
+                             (F32, 64, [1, 1], [2000, 300]), (F32, 128, [70], [300]),
+                             (BF, 128, [300, 200], [300, 2000])):
+        kc, vc, table = make_paged(g, kl, 2, D, 16, dtype, dev, poison=False)
+        q = randn(g, sum(ql), 8, D, dtype=dtype).to(dev)
+        kv = torch.tensor(kl, dtype=torch.int32, device=dev)
+        outs = []
+        for _ in range(20):
+            out = torch.empty_like(q)
+            B.gdn_attn_paged(q, kc, vc, table, kv, cu_of(ql, dev), out, max_q_len=max(ql))
+            outs.append(out)
+        assert all(torch.equal(outs[0], o) for o in outs[1:])
+    q, k = randn(g, 3000, 8, 128).to(dev), randn(g, 3000, 2, 128).to(dev)
+    cu = cu_of([1700, 300, 1000], dev)
+    outs = []
+    for _ in range(20):
+        out = torch.empty_like(q)
+        B.gdn_attn_varlen(q, k, k, cu, out)
+        outs.append(out)
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_varlen_long_against_key_blocks(D, cuda_device):
+    """A prompt of many key tiles and items per SM, against the f64 form of some of
+    its rows (the whole would take too long)."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(D)
+    lens, Hq, Hkv = [2999, 1500, 700], 16, 2
+    T = sum(lens)
+    q, k, v = (randn(g, T, h, D, std=s) for h, s in ((Hq, 1.5), (Hkv, 1), (Hkv, 1)))
+    out = torch.empty(T, Hq, D, dtype=BF, device=dev)
+    for _ in range(3):  # back to back: the later calls find the SMs' memory used
+        B.gdn_attn_varlen(q.to(dev), k.to(dev), v.to(dev), cu_of(lens, dev), out)
+    B.gdn_read_device_status()
+    starts = np.concatenate([[0], np.cumsum(lens)[:-1]])
+    for a, n in zip(starts, lens):
+        for i in sorted({0, 1, 127, 128, n // 2, n - 129, n - 2, n - 1}):
+            ro, rl, pieces = R.attention_rows(R.f64(q[a + i:a + i + 1]), R.f64(k[a:a + n]),
+                                              R.f64(v[a:a + n]), i, D ** -0.5)
+            R.check(R.f64(out[a + i:a + i + 1]), ro, R.bound(ro, pieces, BF, True), f"row {i} of {n}")
