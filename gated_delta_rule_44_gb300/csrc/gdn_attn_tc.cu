@@ -96,10 +96,9 @@ struct Shared {
   int start_s, start_hkv, start_u;
   long long left;
   long long scan[20];
-  union {  // what the two warps of 32 rows exchange
-    uint16_t top[2][2][32];  // [key tile & 1][half][row]: maxima, as bf16
-    float val[2][32];        // [half][row]
-  } swap[2][4];              // of their own: other pairs may be in another range
+  // What the two warps of 32 rows exchange, 256 bytes twice for each of the four
+  // pairs of the one-tile form, once for each of the eight of the other.
+  alignas(16) unsigned char swap[2048];
 };
 
 template <int D, int NQ>
@@ -785,7 +784,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     uint32_t nk = 0, np = 0;
     // Meeting the pair's other warp (bounded; false: leave).
     uint64_t& pair = sh->pair[qt][warp & 3];
-    auto& mine = sh->swap[qt][warp & 3];
+    // Values in f32 [half][row], and maxima in bf16 [key tile & 1][half][row].  In the
+    // two-tile form they share their place: the scores of a tile wait for the P of
+    // the one before of both warps, so that neither can write one kind while the
+    // other warp still reads the other.
+    unsigned char* mine = sh->swap + (NQ == 2 ? (qt * 4 + (warp & 3)) * 256 : (warp & 3) * 512);
+    float* val = reinterpret_cast<float*>(mine) + lane;
+    uint16_t* tops = reinterpret_cast<uint16_t*>(mine + (NQ == 2 ? 0 : 256)) + lane;
     auto pair_arrive = [&] {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&pair));
@@ -794,10 +799,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     // x becomes the row's value of it from the other warp (between two meetings
     // that keep `val` from being written early).
     auto swap = [&](float& x) -> bool {
-      mine.val[half][lane] = x;
+      val[half * 32] = x;
       pair_arrive();
       const bool ok = pair_wait();
-      x = mine.val[half ^ 1][lane];
+      x = val[(half ^ 1) * 32];
       return ok;
     };
     int seg_n = 0;
@@ -833,24 +838,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const int buf = NQ == 2 ? qt : (int)(nk & 1);
         const uint32_t ph = NQ == 2 ? nk & 1 : (nk >> 1) & 1;
         const int jj = kt - g.kt0;
-        // Takes the other half's last published maximum; true in raise: m grew.
+        // Takes a maximum of both halves (m of the first tile becomes it); raise: m grew.
         float f = 1.0f;
         bool raise = false;
-        auto new_reference = [&]() -> bool {
-          if (!pair_wait()) return false;
-          const int slot = jj == 0 ? 0 : (jj - 1) & 1;
-          const float top = fmaxf(__uint_as_float(top_bits << 16),
-                                  __uint_as_float((uint32_t)mine.top[slot][half ^ 1][lane] << 16));
+        auto raise_to = [&](float top) {
           if (top > m + kRaise || (m == -INFINITY && top > m)) {
             raise = valid && jj > 0;
             f = ex2(m - top);
             m = top;
           }
           if (m == -INFINITY) m = 0.0f;  // no score above -inf so far
-          return true;
         };
-        if (jj > 1 && !idle)
-          if (!new_reference()) return;
+        if (jj > 1 && !idle) {
+          if (!pair_wait()) return;
+          const uint32_t their_bits = tops[(((jj - 1) & 1) * 2 + (half ^ 1)) * 32];
+          raise_to(fmaxf(__uint_as_float(top_bits << 16), __uint_as_float(their_bits << 16)));
+        }
         const bool raising = __any_sync(0xffffffffu, raise);
         const int lim = last - kt * BK - half * 64;  // the row's last visible column
         const bool masked = __any_sync(0xffffffffu, lim < 63);
@@ -858,12 +861,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         fence_after_sync();
         if (!idle) {
           const uint32_t ts = tmem + lanes + buf * 128;
-          // Publishes a maximum, cut to bf16: only the agreement matters.
-          auto publish = [&](float t) {
-            top_bits = __float_as_uint(t) >> 16;
-            mine.top[jj & 1][half][lane] = (uint16_t)top_bits;
-            pair_arrive();
-          };
           auto scores = [&](float(&y)[32], int i) {
             tmem_ld32(ts + half * 64 + i * 32, y);
             tmem_ld_wait();
@@ -882,8 +879,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) t = fmaxf(t, fmaxf(y[e], y[e + 1]));
             }
-            publish(t == -INFINITY ? t : t * c);  // (0 * -inf must not count as a score)
-            if (!new_reference()) return;
+            // In full f32: a row whose largest weight is then exactly 1 loses nothing
+            // of it to P's rounding.  (0 * -inf must not count as a score.)
+            t = t == -INFINITY ? t : t * c;
+            float theirs = t;
+            if (!swap(theirs)) return;
+            raise_to(fmaxf(t, theirs));
           }
           if (raising) {
             // O is at rest: in the two-tile form S j follows P V j-1, in the other
@@ -942,8 +943,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
           sum01 = __fadd2_rn(sum01, sum23);
           l += sum01.x + sum01.y;
-          if (jj > 0 && kt + 1 < g.kt1)
-            publish(m + log2f(fmaxf(__low2float(big), __high2float(big))));
+          if (jj > 0 && kt + 1 < g.kt1) {
+            // Published cut to bf16: only the agreement of the two warps matters.
+            const float t = m + log2f(fmaxf(__low2float(big), __high2float(big)));
+            top_bits = __float_as_uint(t) >> 16;
+            tops[((jj & 1) * 2 + half) * 32] = (uint16_t)top_bits;
+            pair_arrive();
+          }
         } else if (lane == 0) {
           mbar_arrive(smem_u32(&sh->p_full[buf]));
         }
