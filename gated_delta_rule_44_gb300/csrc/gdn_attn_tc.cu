@@ -34,6 +34,15 @@
 // cores the other's MMAs run.  One-tile form (D = 256, whose O fills half the
 // TMEM, and few rows): two S buffers, so that the next key tile's scores are
 // computed during a softmax.
+// Pair (D = 256 over prompts and chunks): two CTAs of a cluster have a row tile each of
+// one 256-row item and share its keys.  Every load goes to both (multicast), issued
+// by the two in turns, unit for unit; a unit is free when the MMAs of both are done
+// with it.  Alone a CTA took 128 KB per key tile from L2, 10 TB/s in all, and waited
+// for it: 1190 us for the eight prompts below, against 1153.  The rest of the way to
+// 1090 are the waits: a wait costs 150 cycles even for what is there, so that Q K^T
+// has its four units' before that for the S buffer; P V has each unit's in front of
+// it, as V comes late (5 units of 16 KB fit, 4 are a tile: the next tile's come as
+// this one's are freed, 1200 cycles behind).  4 + 6 units: 1195; 6 + 4: 1096.
 //
 // Work.  The tile form has a grid of (tile, kv head) items, the longest first,
 // and with few of them cuts each into key ranges whose sums a second kernel
@@ -56,13 +65,13 @@
 //     burst rate of a library product.  An iteration takes 3070 cycles: a tile's
 //     chain of scores, softmax (1300), P V and Q K^T (1150) and their latencies is
 //     longer than the two tiles' MMAs.
-//   2048 tokens over 32768, the same heads, pages of 128: 740-780 us, 1.4 PFLOP/s,
+//   2048 tokens over 32768, the same heads, pages of 128: 720-780 us, 1.4 PFLOP/s,
 //     82-86 % of the sustained rate.
-//   eight prompts of 512 .. 8192, 16 + 2 heads of 256: 1190-1250 us, 1.25 PFLOP/s.
-//     One row tile per SM needs 128 KB of K and V per 128 keys from L2: 10 TB/s,
-//     which is what binds.
+//   eight prompts of 512 .. 8192, 16 + 2 heads of 256: 1090 us, 1.41 PFLOP/s, 82 % of
+//     the sustained rate.  A key tile takes 2650 cycles for 2048 of MMA: K and V wait
+//     for room.
 //   256 single tokens over 1 .. 16384 keys, 32 + 4 heads of 128, pages of 64: 650 us,
-//     6.9 TB/s, the copy rate.  128 x 1 .. 4 drafts, pages of 16: 370 us, 84 %.
+//     6.9 TB/s, the copy rate.  128 x 1 .. 4 drafts, pages of 16: 357 us, 87 %.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -99,14 +108,15 @@ struct Seg {
 
 struct Shared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], turn[2], pv[2], o_full[2], o_empty[2], v_land, end[2];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], turn[2], pv[2], o_full[2], o_empty[2], end[2];
+  uint64_t v_land[kMaxRing];
   uint64_t pair[2][4];
-  uint64_t seg_full[2], seg_empty[2], clc_full;
+  uint64_t seg_full[2], seg_empty[2], clc_full, clc_read;
   alignas(16) uint4 clc;  // the next item's answer
   Seg seg[2];
   uint32_t tmem;
   int abort;
-  uint32_t k_loads[kMaxRing], v_loads[kMaxRing], q_loads, clc_asked, land_asked;  // issued so far
+  uint32_t k_loads[kMaxRing], v_loads[kMaxRing], v_lands[kMaxRing], q_loads, clc_asked;  // issued so far
   int start_s, start_hkv, start_u;
   long long left;
   long long scan[20];
@@ -260,6 +270,45 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 
+// The same into both CTAs of a pair, at the same place and barrier of each.
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void* tmap, uint32_t mbar, int c0,
+                                                 int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(mbar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, uint32_t mbar, int c0,
+                                                 int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(mbar), "h"((uint16_t)3)
+      : "memory");
+}
+// Arrives on the barrier of both CTAs once the MMAs so far are complete.
+__device__ __forceinline__ void mma_commit_pair(uint32_t mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+      "%1;\n" ::"r"(mbar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// Arrives on the barrier at this place of CTA `rank` of the pair.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t mbar, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}\n" ::"r"(mbar),
+      "r"(rank)
+      : "memory");
+}
+__device__ __forceinline__ void pair_barrier() {  // all threads of both CTAs
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -271,14 +320,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Asks for a further CTA of the grid in place of its launch.
+template <bool PAIR>
 __device__ __forceinline__ void clc_ask(Shared* sh) {
   const uint32_t mb = smem_u32(&sh->clc_full);
-  mbar_expect_tx(mb, 16);
-  asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
-      "[%1];\n" ::"r"(smem_u32(&sh->clc)),
-      "r"(mb)
-      : "memory");
+  if constexpr (PAIR) {  // the answer goes to both CTAs
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];\n" ::"r"(smem_u32(&sh->clc)),
+        "r"(mb)
+        : "memory");
+  } else {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+        "[%1];\n" ::"r"(smem_u32(&sh->clc)),
+        "r"(mb)
+        : "memory");
+  }
 }
 // The answer: false when no CTA was left.
 __device__ __forceinline__ bool clc_answer(Shared* sh, uint32_t& x, uint32_t& y) {
@@ -296,7 +353,7 @@ __device__ __forceinline__ bool clc_answer(Shared* sh, uint32_t& x, uint32_t& y)
   return ok != 0;
 }
 
-template <int D, int NQ, bool PAGED, bool STREAM>
+template <int D, int NQ, bool PAGED, bool STREAM, bool PAIR>
 __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnLaunch p, const __grid_constant__ CUtensorMap mq,
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -308,20 +365,25 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   const uint32_t sq = smem_u32(smem), sk = sq + C::kQ, sv = sk + ST * C::kUnit;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.Hq / p.Hkv;
+  constexpr int CL = PAIR ? 2 : 1;
+  // Of a pair, the CTA's row tile.
+  uint32_t rank = 0;
+  if constexpr (PAIR) asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
 
   start_next_kernel();
   if (warp == 0) {
     if (lane == 0) {
-      constexpr int kReleases = NQ == 2 ? 2 : 1;  // MMA warps that use a unit
+      constexpr int kReleases = NQ == 2 || PAIR ? 2 : 1;  // MMA warps that use a unit, of a pair in both CTAs
       for (int i = 0; i < ST; ++i) {
         mbar_init(smem_u32(&sh->k_full[i]), 1);
         mbar_init(smem_u32(&sh->k_empty[i]), kReleases);
         mbar_init(smem_u32(&sh->v_full[i]), 1);
         mbar_init(smem_u32(&sh->v_empty[i]), kReleases);
-        sh->k_loads[i] = sh->v_loads[i] = 0;
+        mbar_init(smem_u32(&sh->v_land[i]), 1);
+        sh->k_loads[i] = sh->v_loads[i] = sh->v_lands[i] = 0;
       }
       mbar_init(smem_u32(&sh->q_full), 1);
-      mbar_init(smem_u32(&sh->q_empty), kReleases);
+      mbar_init(smem_u32(&sh->q_empty), NQ);
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&sh->s_full[i]), 1);
         mbar_init(smem_u32(&sh->p_full[i]), 8);
@@ -334,10 +396,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         mbar_init(smem_u32(&sh->seg_empty[i]), C::kReaders);
         for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sh->pair[i][w]), 2);
       }
-      mbar_init(smem_u32(&sh->v_land), NU);
       mbar_init(smem_u32(&sh->clc_full), 1);
+      mbar_init(smem_u32(&sh->clc_read), 1);
       sh->abort = 0;
-      sh->q_loads = sh->clc_asked = sh->land_asked = 0;
+      sh->q_loads = sh->clc_asked = 0;
       fence_mbar_init();
     }
   } else if (warp == 2) {
@@ -389,6 +451,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   }
   fence_before_sync();
   __syncthreads();
+  if constexpr (PAIR) pair_barrier();  // the other CTA's barriers stand
   fence_after_sync();
   // All 512 columns: their base is 0, which the addresses below use as such.
   if (sh->tmem != 0 && tid == 0) atomicOr(p.status, kStatusTimeout);
@@ -415,6 +478,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
     }
   };
+  // Every unit of a ring has been released: of a pair, the other CTA's last arrivals
+  // are in, and this one may end.
+  auto drain = [&](Ring ring, uint32_t filled, uint64_t* empty) {
+    for (int i = 0; i < ST; ++i, ring.step(), ++filled)
+      if (filled >= ST)
+        if (!warp_wait(&empty[ring.st], ring.round ^ 1, sh, p.status)) return;
+  };
 
   if (warp == 0) {
     // ---- work; loads of Q and K ----
@@ -426,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       uint32_t filled = 0;  // units so far
       int nseg = 0, loads = 0, asked = 0;
       bool more = true;     // the tile form's grid may have an item left
-      uint32_t bx = blockIdx.x, by = blockIdx.y;
+      uint32_t bx = blockIdx.x - rank, by = blockIdx.y;  // (of a pair, its first CTA's)
       for (;;) {
         // The next range, into g.
         Seg g;
@@ -435,15 +505,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           if (!iter.next(p, g)) g.s = -1;
         } else {
           while (more) {
-            const int id = (int)(gridDim.x / p.Hkv) - 1 - (int)(bx / p.Hkv);
-            const SeqTile t = find_tile(p, id, NQ * a.TQ);
+            const int item = (int)bx / CL;
+            const int id = (int)(gridDim.x / CL / p.Hkv) - 1 - item / p.Hkv;
+            const SeqTile t = find_tile(p, id, NQ * CL * a.TQ);
             if (t.bad && lane == 0) atomicOr(p.status, kStatusBadSeqlens);
             if (t.nt > 0) {
               g.s = t.s;
-              g.hkv = bx % p.Hkv;
-              g.t0 = t.t0;
-              g.nt = t.nt;
-              g.pos0 = t.pos0;
+              g.hkv = item % p.Hkv;
+              g.t0 = t.t0 + (int)rank * a.TQ;
+              g.nt = t.nt - (int)rank * a.TQ;  // <= 0: no row for the pair's second CTA
+              g.pos0 = t.pos0 + (int)rank * a.TQ;
               g.hi = max(0, t.pos0 + t.nt);
               const int n = (g.hi + BK - 1) / BK;
               g.kt0 = (int)((int64_t)n * by / a.splits);
@@ -452,11 +523,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             }
             // The item after this one is asked for now and taken when this one's
             // loads have been issued.
-            if (asked > 0) fence_proxy_async();
+            if (asked > 0) {
+              fence_proxy_async();  // the last answer has been read
+              __syncwarp();
+              if constexpr (PAIR) {
+                if (rank == 0) {  // by the other CTA, too
+                  if (!warp_wait(&sh->clc_read, (asked - 1) & 1, sh, p.status)) return;
+                } else if (elect_one()) {
+                  mbar_arrive_at(smem_u32(&sh->clc_read), 0);
+                }
+              }
+            }
             __syncwarp();
             if (elect_one()) {
               sh->clc_asked = asked + 1;
-              clc_ask(sh);
+              mbar_expect_tx(smem_u32(&sh->clc_full), 16);
+              if (rank == 0) clc_ask<PAIR>(sh);
             }
             ++asked;
             if (g.s >= 0) break;
@@ -475,7 +557,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           __syncwarp();
           ++nseg;
         }
-        if (g.s < 0) return;
+        if (g.s < 0) {
+          if constexpr (PAIR) drain(ring, filled, sh->k_empty);
+          return;
+        }
         const int kt0 = uni(g.kt0), n = uni(g.kt1) - kt0, hi = uni(g.hi), hkv = uni(g.hkv);
         const int per_tile = BK / a.pbk;
         const int row0 = PAGED ? 0 : uni(cu_at(p.cu, g.s));
@@ -503,13 +588,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             if (elect_one()) {
               ++sh->k_loads[ring.st];
               mbar_expect_tx(full, groups * a.pbk * 128u);
-              if constexpr (!PAGED) tma_load_3d(dst, &mk, full, u * 64, row0 + j0, hkv);
+              if constexpr (!PAGED && !PAIR) tma_load_3d(dst, &mk, full, u * 64, row0 + j0, hkv);
+              if constexpr (!PAGED && PAIR)  // units in turn by either CTA
+                if ((filled & 1) == rank) tma_load_3d_pair(dst, &mk, full, u * 64, row0 + j0, hkv);
             }
             if constexpr (PAGED) {
               __syncwarp();
-              if (lane < groups)
-                tma_load_4d(dst + lane * a.pbk * 128, &mk, full, u * 64,
-                            (j0 + lane * a.pbk) % p.page_size, hkv, page);
+              const int row = (j0 + lane * a.pbk) % p.page_size;
+              if constexpr (PAIR) {
+                if (lane < groups && (filled & 1) == rank)
+                  tma_load_4d_pair(dst + lane * a.pbk * 128, &mk, full, u * 64, row, hkv, page);
+              } else {
+                if (lane < groups)
+                  tma_load_4d(dst + lane * a.pbk * 128, &mk, full, u * 64, row, hkv, page);
+              }
               __syncwarp();
             }
           }
@@ -562,6 +654,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
       return true;
     };
+    // The MMAs so far have read the unit.
+    auto release = [&](uint64_t* empty) {
+      if constexpr (PAIR) mma_commit_pair(smem_u32(empty));
+      else mma_commit(smem_u32(empty));
+    };
     // S[buf] = Q[q] K^T of unit u.
     auto qk_unit = [&](uint32_t buf, int u, uint32_t at) {
       if (elect_one()) {
@@ -569,29 +666,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const uint64_t qd = desc_sw128(sq + q * C::kQTile + u * 16384, 16, 1024);
 #pragma unroll
         for (int k = 0; k < 4; ++k) mma_bf16(buf * 128, qd + k * 2, kd + k * 2, kIdQK, u + k > 0);
-        mma_commit(smem_u32(&sh->k_empty[at]));
+        release(&sh->k_empty[at]);
         if (u == NU - 1) mma_commit(smem_u32(&sh->s_full[buf]));
       }
     };
-    // O[q] (+)= P[buf] V over the key tile's units (keys outermost); then `done`
-    // and `done2` arrive.
-    auto pv = [&](uint32_t buf, bool acc, const uint32_t(&at)[NU], uint64_t* done, uint64_t* done2) {
+    // O[q] (+)= P[buf] V of the key tile's unit u (keys outermost).
+    auto pv_unit = [&](uint32_t buf, bool acc, int u, uint32_t at) {
       constexpr int ND = D / VD;  // units side by side in the dims
-      fence_after_sync();
       if (elect_one()) {
+        const uint64_t vd = desc_sw128(sv + at * C::kUnit, VK * 128, 1024);
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-          const uint64_t vd = desc_sw128(sv + at[u] * C::kUnit, VK * 128, 1024);
-#pragma unroll
-          for (int k = 0; k < VK / 16; ++k) {
-            const int ks = (u / ND) * (VK / 16) + k;  // step of 16 keys in the tile
-            mma_bf16_ta(kTO + q * 128 + (u % ND) * VD, buf * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
-                        vd + ((k * 2048) >> 4), kIdPV, acc || ks > 0);
-          }
-          mma_commit(smem_u32(&sh->v_empty[at[u]]));
+        for (int k = 0; k < VK / 16; ++k) {
+          const int ks = (u / ND) * (VK / 16) + k;  // step of 16 keys in the tile
+          mma_bf16_ta(kTO + q * 128 + (u % ND) * VD, buf * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
+                      vd + ((k * 2048) >> 4), kIdPV, acc || ks > 0);
         }
-        if (done) mma_commit(smem_u32(done));
-        if (done2) mma_commit(smem_u32(done2));
+        release(&sh->v_empty[at]);
       }
     };
     auto role = [&] {
@@ -630,7 +720,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               continue;
             }
             if (j >= 0) {
-              pv(q, j > 0, av, j == n - 1 ? &sh->o_full[q] : nullptr, nullptr);
+#pragma unroll
+              for (int u = 0; u < NU; ++u) pv_unit(q, j > 0, u, av[u]);
+              if (j == n - 1 && elect_one()) mma_commit(smem_u32(&sh->o_full[q]));
               ++nk;
             }
             if (j + 1 < n) {
@@ -648,23 +740,47 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         } else if (warp == 1) {
           if (!wait(sh->q_full, nseg & 1)) return;
           for (int j = 0; j < n; ++j, ++nk) {
+            if constexpr (PAIR)  // (for single tokens, bound by the reads of K, 1 % slower)
+              if (!land(kr, sh->k_full, ak)) return;
             if (nk >= 2)  // P V has read the buffer's last P
               if (!wait(sh->pv[nk & 1], ((nk >> 1) - 1) & 1)) return;
+            fence_after_sync();
+            if constexpr (PAIR) {
 #pragma unroll
-            for (int u = 0; u < NU; ++u, kr.step()) {
-              if (!wait(sh->k_full[kr.st], kr.round)) return;
-              fence_after_sync();
-              qk_unit(nk & 1, u, kr.st);
+              for (int u = 0; u < NU; ++u) qk_unit(nk & 1, u, ak[u]);
+            } else {
+#pragma unroll
+              for (int u = 0; u < NU; ++u, kr.step()) {
+                if (!wait(sh->k_full[kr.st], kr.round)) return;
+                fence_after_sync();
+                qk_unit(nk & 1, u, kr.st);
+              }
             }
           }
           if (elect_one()) mma_commit(smem_u32(&sh->q_empty));
         } else {
           for (int j = 0; j < n; ++j, ++nk) {
-            if (!land(vr, sh->v_full, av)) return;
+            if constexpr (!PAIR)
+              if (!land(vr, sh->v_full, av)) return;
             if (j == 0 && nseg > 0)
               if (!wait(sh->o_empty[0], (nseg - 1) & 1)) return;
             if (!wait(sh->p_full[nk & 1], (nk >> 1) & 1)) return;
-            pv(nk & 1, j > 0, av, &sh->pv[nk & 1], j == n - 1 ? &sh->o_full[0] : nullptr);
+            fence_after_sync();
+            if constexpr (PAIR) {
+#pragma unroll
+              for (int u = 0; u < NU; ++u, vr.step()) {
+                if (!wait(sh->v_full[vr.st], vr.round)) return;
+                fence_after_sync();
+                pv_unit(nk & 1, j > 0, u, vr.st);
+              }
+            } else {
+#pragma unroll
+              for (int u = 0; u < NU; ++u) pv_unit(nk & 1, j > 0, u, av[u]);
+            }
+            if (elect_one()) {
+              mma_commit(smem_u32(&sh->pv[nk & 1]));
+              if (j == n - 1) mma_commit(smem_u32(&sh->o_full[0]));
+            }
           }
         }
         ++nseg;
@@ -678,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     // ---- loads of V ----
     auto role = [&] {
       Ring ring;
-      uint32_t filled = 0, tails = 0;
+      uint32_t filled = 0, landed = 0;  // bit i: phase of v_land[i]
       Seg g;
       while (next_seg(g)) {
         const int kt0 = uni(g.kt0), n = uni(g.kt1) - kt0, hi = uni(g.hi), hkv = uni(g.hkv);
@@ -706,37 +822,47 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             const int kh = u / ND, db = u % ND;
             if (filled >= ST)
               if (!warp_wait(&sh->v_empty[ring.st], ring.round ^ 1, sh, p.status)) return;
-            // A tile with a tail lands on a barrier of its own and is passed on below.
-            const uint32_t full = smem_u32(tail ? &sh->v_land : &sh->v_full[ring.st]);
+            // Units of a tile with a tail land on barriers of their own and are passed on
+            // below.
+            const uint32_t full = smem_u32(tail ? &sh->v_land[ring.st] : &sh->v_full[ring.st]);
             const uint32_t dst = sv + ring.st * C::kUnit;
             // Loads of groups with a visible key; none for a unit past the last one.
             const int groups = max(0, min(per_unit, (r0 - kh * VK + a.pbv - 1) / a.pbv));
             if (elect_one()) {
-              if (!tail) ++sh->v_loads[ring.st];
-              else if (u == NU - 1) sh->land_asked = tails + 1;
+              ++(tail ? sh->v_lands : sh->v_loads)[ring.st];
               mbar_expect_tx(full, groups * NB * a.pbv * 128u);
               if constexpr (!PAGED) {
                 if (groups > 0)
 #pragma unroll
-                  for (int b = 0; b < NB; ++b)
-                    tma_load_3d(dst + b * VK * 128, &mv, full, db * VD + b * 64, row0 + j0 + kh * VK,
-                                hkv);
+                  for (int b = 0; b < NB; ++b) {
+                    const int d = db * VD + b * 64, row = row0 + j0 + kh * VK;
+                    if constexpr (PAIR) {
+                      if ((filled & 1) == rank) tma_load_3d_pair(dst + b * VK * 128, &mv, full, d, row, hkv);
+                    } else {
+                      tma_load_3d(dst + b * VK * 128, &mv, full, d, row, hkv);
+                    }
+                  }
               }
             }
             if constexpr (PAGED) {
               const int page = __shfl_sync(0xffffffffu, pages, (kh * per_unit + grp) & 31);
-              if (grp < groups)
-                tma_load_4d(dst + blk * VK * 128 + grp * a.pbv * 128, &mv, full, db * VD + blk * 64,
-                            (j0 + kh * VK + grp * a.pbv) % p.page_size, hkv, page);
+              const uint32_t to = dst + blk * VK * 128 + grp * a.pbv * 128;
+              const int d = db * VD + blk * 64, row = (j0 + kh * VK + grp * a.pbv) % p.page_size;
+              if constexpr (PAIR) {
+                if (grp < groups && (filled & 1) == rank) tma_load_4d_pair(to, &mv, full, d, row, hkv, page);
+              } else {
+                if (grp < groups) tma_load_4d(to, &mv, full, d, row, hkv, page);
+              }
               __syncwarp();
             }
           }
           if (tail) {
-            if (!warp_wait(&sh->v_land, tails++ & 1, sh, p.status)) return;
             // Whole 128-byte rows: the swizzle permutes inside a row only.
             Ring at = first;
 #pragma unroll
             for (int u = 0; u < NU; ++u, at.step()) {
+              if (!warp_wait(&sh->v_land[at.st], (landed >> at.st) & 1, sh, p.status)) return;
+              landed ^= 1u << at.st;
               constexpr int ND = D / VD;
               const int c0 = max(0, r0 - (u / ND) * VK);  // first row of the unit to clear
               unsigned char* v = smem + C::kQ + (ST + at.st) * C::kUnit;
@@ -757,6 +883,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           }
         }
       }
+      if constexpr (PAIR) drain(ring, filled, sh->v_empty);
     };
     role();
     if constexpr (STREAM) {
@@ -794,6 +921,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     const float c = p.scale * kLog2e;
     const float2 c2 = make_float2(c, c);
     const int tok = qt * a.TQ + r / G;                  // token of the tile
+    const int row0 = (int)rank * a.TQ * G;              // first row in a workspace block
     auto role = [&] {
     uint32_t nk = 0, np = 0;
     // Meeting the pair's other warp (bounded; false: leave).
@@ -824,12 +952,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     while (next_seg(g)) {
       if (NQ == 2 && qt == 1 && g.nt <= a.TQ) continue;   // no second row tile
       if (g.kt0 == g.kt1) {  // no key for any row
-        const Partials part(a.ws, (int64_t)gridDim.x * a.splits, a.rows, D);
+        const Partials part(a.ws, (int64_t)gridDim.x / CL * a.splits, a.rows, D);
         const float zero[D / 32] = {};
         const int rows = (min(g.nt, (qt + 1) * a.TQ) - qt * a.TQ) * G;
         for (int i = (warp - 4) & 7; i < rows; i += 8) {
-          const int pr = qt * a.TQ * G + i, t = g.t0 + pr / G, h = g.hkv * G + pr % G;
-          if (g.slot >= 0) part.put<D / 32>(g.slot, pr, lane, zero, -INFINITY, 0.0f);
+          const int in_tile = qt * a.TQ * G + i, t = g.t0 + in_tile / G, h = g.hkv * G + in_tile % G;
+          if (g.slot >= 0) part.put<D / 32>(g.slot, row0 + in_tile, lane, zero, -INFINITY, 0.0f);
           else finish_row<bf16, D>(p, t, h, lane, zero, -INFINITY, 0.0f);
         }
         continue;
@@ -988,8 +1116,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         if (!swap(theirs)) return;
         l = half == 0 ? l + theirs : theirs + l;  // the same sum on both sides
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const Partials part(a.ws, STREAM ? 2 * (int64_t)a.ctas : (int64_t)gridDim.x * a.splits, a.rows, D);
-        const int pr = tok * G + r % G;
+        const Partials part(a.ws, STREAM ? 2 * (int64_t)a.ctas : (int64_t)gridDim.x / CL * a.splits, a.rows, D);
+        const int pr = row0 + tok * G + r % G;
         // A sum of 0 with a key in sight: every weight was lost beside a reference
         // of 0 that no score gave.
         bool finite = isfinite(l) && !(l == 0.0f && last >= g.kt0 * BK);
@@ -1083,15 +1211,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     if (tid == 0) {
       for (int i = 0; i < ST; ++i) {
         if (sh->k_loads[i]) mbar_wait(smem_u32(&sh->k_full[i]), (sh->k_loads[i] - 1) & 1, kWaitBudget);
+        if (sh->v_lands[i]) mbar_wait(smem_u32(&sh->v_land[i]), (sh->v_lands[i] - 1) & 1, kWaitBudget);
         if (sh->v_loads[i]) mbar_wait(smem_u32(&sh->v_full[i]), (sh->v_loads[i] - 1) & 1, kWaitBudget);
       }
-      if (sh->land_asked) mbar_wait(smem_u32(&sh->v_land), (sh->land_asked - 1) & 1, kWaitBudget);
       if (sh->q_loads) mbar_wait(smem_u32(&sh->q_full), (sh->q_loads - 1) & 1, kWaitBudget);
       if (sh->clc_asked) mbar_wait(smem_u32(&sh->clc_full), (sh->clc_asked - 1) & 1, kWaitBudget);
     }
     __syncthreads();
   }
   if (warp == 2) tmem_dealloc(sh->tmem, 512);
+  if constexpr (PAIR) {  // until here the other CTA writes to this one's memory
+    __syncthreads();
+    pair_barrier();
+  }
 }
 
 // Joins the ranges of the pairs that the stream form cut: CTA c serves the pair
@@ -1175,7 +1307,7 @@ constexpr int tiles_of() {
 
 size_t info_bytes(int ctas) { return ((size_t)ctas * sizeof(int4) + 255) & ~(size_t)255; }
 
-template <int D, int NQ, bool PAGED, bool STREAM>
+template <int D, int NQ, bool PAGED, bool STREAM, bool PAIR = false>
 cudaError_t run(const AttnLaunch& p, TcArgs a, dim3 grid, cudaStream_t st) {
   using C = Cfg<D, NQ>;
   CUtensorMap mq, mk, mv;
@@ -1183,12 +1315,30 @@ cudaError_t run(const AttnLaunch& p, TcArgs a, dim3 grid, cudaStream_t st) {
       !(PAGED ? pages_map(&mv, p.vc, p, a.pbv) : rows_map(&mv, p.v, p, a.pbv)))
     return cudaErrorInvalidValue;
   static const cudaError_t attr =
-      cudaFuncSetAttribute(attn_tc_kernel<D, NQ, PAGED, STREAM>,
+      cudaFuncSetAttribute(attn_tc_kernel<D, NQ, PAGED, STREAM, PAIR>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
   if (attr != cudaSuccess) return attr;
-  attn_tc_kernel<D, NQ, PAGED, STREAM><<<grid, C::kThreads, C::kBytes, st>>>(p, mq, mk, mv, a);
-  note_launch();
-  return cudaGetLastError();
+  if constexpr (PAIR) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, NQ, PAGED, STREAM, PAIR>, p, mq, mk, mv, a);
+    note_launch();
+    return e;
+  } else {
+    attn_tc_kernel<D, NQ, PAGED, STREAM, PAIR><<<grid, C::kThreads, C::kBytes, st>>>(p, mq, mk, mv, a);
+    note_launch();
+    return cudaGetLastError();
+  }
 }
 
 template <int D>
@@ -1213,13 +1363,16 @@ cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
     return launch_after(attn_stream_join_kernel<D>, dim3(sms, std::min(a.rows, 16)), 256, st, p, a);
   }
   a.q_box = a.TQ;
-  const int TT = NQ * a.TQ;
+  // D = 256: two CTAs share an item, a row tile each.
+  constexpr int CL = NQ == 1 ? 2 : 1;
+  const int TT = 2 * a.TQ;
   const int64_t items = tile_bound(p.T, p.N, TT) * p.Hkv;
-  a.rows = 128 * NQ;
-  if (p.table == nullptr) return run<D, NQ, false, false>(p, a, dim3((unsigned)items), st);
-  a.splits = tile_splits(items, (int64_t)p.max_pages * p.page_size, sms);
+  a.rows = 256;
+  if (p.table == nullptr)
+    return run<D, NQ, false, false, CL == 2>(p, a, dim3((unsigned)(items * CL)), st);
+  a.splits = tile_splits(items * CL, (int64_t)p.max_pages * p.page_size, sms);
   a.ws = static_cast<float*>(p.ws);
-  cudaError_t e = run<D, NQ, true, false>(p, a, dim3((unsigned)items, a.splits), st);
+  cudaError_t e = run<D, NQ, true, false, CL == 2>(p, a, dim3((unsigned)(items * CL), a.splits), st);
   if (e != cudaSuccess || a.splits == 1) return e;
   return launch_attn_join(p, a.splits, a.rows, TT, st);
 }
@@ -1245,9 +1398,9 @@ size_t attn_tc_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, in
   const int64_t G = Hq / Hkv;
   if (use_stream(max_q, G))
     return info_bytes(sms) + Partials::bytes(2 * (int64_t)sms, (int)(max_q * G), D);
-  const int64_t nq = D <= 128 ? 2 : 1, items = tile_bound(T, N, nq * (128 / G)) * Hkv;
-  const int splits = tile_splits(items, INT64_MAX, sms);
-  return splits > 1 ? Partials::bytes(items * splits, (int)(128 * nq), D) : 0;
+  const int64_t items = tile_bound(T, N, 2 * (128 / G)) * Hkv;
+  const int splits = tile_splits(D <= 128 ? items : 2 * items, INT64_MAX, sms);
+  return splits > 1 ? Partials::bytes(items * splits, 256, D) : 0;
 }
 
 cudaError_t launch_attn_tc(const AttnLaunch& p, cudaStream_t st) {

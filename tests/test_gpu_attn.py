@@ -647,3 +647,43 @@ def test_varlen_long_against_key_blocks(D, cuda_device):
             ro, rl, pieces = R.attention_rows(R.f64(q[a + i:a + i + 1]), R.f64(k[a:a + n]),
                                               R.f64(v[a:a + n]), i, D ** -0.5)
             R.check(R.f64(out[a + i:a + i + 1]), ro, R.bound(ro, pieces, BF, True), f"row {i} of {n}")
+
+
+# ---- heads of 256: two row tiles share their keys --------------------------------
+
+def test_varlen_256_short_items(cuda_device):
+    """Hundreds of items of one or two key tiles, each with a last key inside the
+    tile: tiles whose second half has no row, full ones, empty sequences."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(21)
+    lens = [(i * 29) % 67 if i % 7 else 0 for i in range(150)] + [130, 1, 257]
+    T, Hq, Hkv, D = sum(lens), 8, 2, 256
+    q, k, v = (randn(g, T, h, D, std=s) for h, s in ((Hq, 1.5), (Hkv, 1), (Hkv, 1)))
+    cu = cu_of(lens, dev)
+    outs = []
+    for _ in range(10):
+        out = torch.full((T, Hq, D), float("nan"), dtype=BF, device=dev)
+        lse = torch.full((T, Hq), float("nan"), device=dev)
+        B.gdn_attn_varlen(q.to(dev), k.to(dev), v.to(dev), cu, out, lse=lse)
+        outs.append(out)
+    B.gdn_read_device_status()
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    ro, rl, pieces = R.varlen(q, k, v, lens, D ** -0.5, None)
+    R.check(R.f64(outs[0]), ro, R.bound(ro, pieces, BF, True), "out")
+    R.check(R.f64(lse), rl, R.lse_bound(rl, pieces), "lse")
+
+
+@pytest.mark.parametrize("case", [
+    ([300, 20], [4000, 1021], 8, 1, 256, 16, BF, True, "head"),     # few items: key ranges
+    ([130, 33, 0, 64], [130, 2000, 7, 900], 16, 2, 256, 48, BF, False, "token"),
+    ([90] * 30, [90 + 31 * i for i in range(30)], 16, 4, 256, 128, BF, False, "joint"),  # many
+])
+def test_paged_256(case, cuda_device):
+    first = None
+    for _ in range(2):
+        out, lse, ro, rl, pieces, dtype = run_paged(case, cuda_device)
+        B.gdn_read_device_status()
+        R.check(R.f64(out), ro, R.bound(ro, pieces, dtype, True), "out")
+        R.check(R.f64(lse), rl, R.lse_bound(rl, pieces), "lse")
+        assert first is None or torch.equal(first, out)
+        first = out
