@@ -57,7 +57,7 @@
 // A row whose result is not finite is evaluated again key by key (exact_row):
 // the product above multiplies a masked key's weight 0 into its v.
 //
-// Every wait is bounded; once one gives up, every role leaves at its next
+// Every wait is bounded (rows evaluated again extend it); once one gives up, every role leaves at its next
 // wait, copies and MMAs in flight are waited for (bounded) and TMEM is freed.
 //
 // Measured on GB300 (1.93 GHz, hot loop of one key tile pair = 2048 cycles of MMA):
@@ -116,6 +116,7 @@ struct Shared {
   Seg seg[2];
   uint32_t tmem;
   int abort;
+  int redone;  // rows evaluated again so far, by either CTA of a pair
   uint32_t k_loads[kMaxRing], v_loads[kMaxRing], v_lands[kMaxRing], q_loads, clc_asked;  // issued so far
   int start_s, start_hkv, start_u;
   long long left;
@@ -216,12 +217,19 @@ __device__ __forceinline__ bool parked_wait(uint32_t mb, uint32_t parity) {
 // The bounded wait of every role; false: leave.  The rare part is kept out of
 // line: the roles' hot loops share the instruction cache.
 __device__ __noinline__ bool long_wait(uint32_t mb, uint32_t parity, Shared* sh, unsigned* status) {
-  const long long t0 = clock64();
+  long long t0 = clock64();
+  int redone = 0;
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (parked_wait(mb, parity)) return true;
     if (*(volatile int*)&sh->abort) return false;
+    // Rows evaluated again take about 1 us a key: the time counts from the last one.
+    const int now = *(volatile int*)&sh->redone;
+    if (now != redone) {
+      redone = now;
+      t0 = clock64();
+    }
     if (clock64() - t0 > kWaitBudget) {
       *(volatile int*)&sh->abort = 1;
       atomicOr(status, kStatusTimeout);
@@ -302,6 +310,15 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t mbar, uint32_t rank) {
       "{\n\t.reg .b32 a;\n\t"
       "mapa.shared::cluster.u32 a, %0, %1;\n\t"
       "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}\n" ::"r"(mbar),
+      "r"(rank)
+      : "memory");
+}
+// Adds 1 to the shared word at this place of CTA `rank` of the cluster.
+__device__ __forceinline__ void count_at(uint32_t word, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "red.relaxed.cluster.shared::cluster.add.u32 [a], 1;\n\t}\n" ::"r"(word),
       "r"(rank)
       : "memory");
 }
@@ -398,7 +415,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
       mbar_init(smem_u32(&sh->clc_full), 1);
       mbar_init(smem_u32(&sh->clc_read), 1);
-      sh->abort = 0;
+      sh->abort = sh->redone = 0;
       sh->q_loads = sh->clc_asked = 0;
       fence_mbar_init();
     }
@@ -1173,7 +1190,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           else if (p.lse != nullptr)
             p.lse[(int64_t)t * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
-        // Rows to evaluate again, by the pair's first warp once both have stored.
+        // Rows to evaluate again once both warps have stored, every other one by either.
         pair_arrive();
         if (!pair_wait()) return;
         theirs = finite ? 1.0f : 0.0f;
@@ -1181,7 +1198,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         unsigned redo = __ballot_sync(0xffffffffu, valid && !(finite && theirs == 1.0f));
         pair_arrive();  // `theirs` has been read: the next range may publish
         if (!pair_wait()) return;
-        if (half == 1) redo = 0;
+        redo &= half ? 0xaaaaaaaau : 0x55555555u;
         while (redo) {
           const int src = __ffs(redo) - 1;
           redo &= redo - 1;
@@ -1192,6 +1209,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
                              em, el);
           if (g.slot >= 0) part.put<D / 32>(g.slot, rp, lane, acc, em, el);
           else finish_row<bf16, D>(p, rt, rh, lane, acc, em, el);
+          if (lane < CL) count_at(smem_u32(&sh->redone), PAIR ? lane : 0);
         }
       }
       ++seg_n;

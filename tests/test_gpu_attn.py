@@ -687,3 +687,58 @@ def test_paged_256(case, cuda_device):
         R.check(R.f64(lse), rl, R.lse_bound(rl, pieces), "lse")
         assert first is None or torch.equal(first, out)
         first = out
+
+
+@pytest.mark.parametrize("D,dtype,q_len,kv", [(128, BF, 200, 9000), (256, BF, 100, 9001), (64, BF, 300, 3003),
+                                              (256, BF, 3, 20001), (128, F32, 70, 2000),
+                                              (32, F32, 2, 3001)])
+def test_paged_infinite_value_in_sight(D, dtype, q_len, kv, cuda_device):
+    """An infinite value that every row sees: its dim is infinite, the others are
+    what they are without it, and no wait runs out over the rows' evaluation."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(D + q_len)
+    Hq, Hkv, page = 8, 2, 16
+    kc, vc, table = make_paged(g, [kv], Hkv, D, page, dtype, dev, poison=False)
+    q = randn(g, q_len, Hq, D, dtype=dtype).to(dev)
+    lens = torch.tensor([kv], dtype=torch.int32, device=dev)
+    cu = cu_of([q_len], dev)
+    j = 1003
+    vc[table[0, j // page], 1, j % page, 5] = 0.0
+    clean, out = torch.empty_like(q), torch.empty_like(q)
+    lse, lse0 = (torch.empty(q_len, Hq, device=dev) for _ in range(2))
+    B.gdn_attn_paged(q, kc, vc, table, lens, cu, clean, max_q_len=q_len, lse=lse0)
+    vc[table[0, j // page], 1, j % page, 5] = float("inf")
+    B.gdn_attn_paged(q, kc, vc, table, lens, cu, out, max_q_len=q_len, lse=lse)
+    B.gdn_read_device_status()
+    assert (out[:, 4:, 5] == float("inf")).all()
+    out[:, 4:, 5] = clean[:, 4:, 5]
+    # Both sides carry the tiled form's error: P rounded to bf16 (2^-8 of each weight,
+    # of values of size 1), and a store's rounding; in f32 sums in two orders.
+    tol = dict(rtol=2.0 ** -7, atol=2.0 ** -7) if dtype == BF else dict(rtol=1e-4, atol=1e-5)
+    torch.testing.assert_close(out, clean, **tol)
+    torch.testing.assert_close(lse, lse0, rtol=1e-5, atol=1e-4)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,q_len", [(128, 32, 4, 1216), (256, 16, 2, 1216)])
+def test_paged_long_evaluation_is_not_a_timeout(D, Hq, Hkv, q_len, cuda_device):
+    """Rows evaluated key by key for longer than any wait of the kernel may last (about
+    a second): the waits of the other roles, and of a pair's other CTA, go on."""
+    dev = cuda_device
+    kv, page = 70000, 64
+    g = torch.Generator(device=dev).manual_seed(D)
+    pages = -(-kv // page)
+    kc, vc = (torch.randn(pages, Hkv, page, D, generator=g, device=dev).to(BF) for _ in range(2))
+    table = torch.randperm(pages, generator=g, device=dev).to(torch.int32).view(1, -1)
+    q = torch.randn(q_len, Hq, D, generator=g, device=dev).to(BF)
+    lens = torch.tensor([kv], dtype=torch.int32, device=dev)
+    cu = cu_of([q_len], dev)
+    vc[table[0, 0], :, 3, 5] = 0.0
+    clean, out = torch.empty_like(q), torch.empty_like(q)
+    B.gdn_attn_paged(q, kc, vc, table, lens, cu, clean, max_q_len=q_len)
+    for i in range(0, pages, 8):  # in every key range, should there be several
+        vc[table[0, i], :, 3, 5] = float("inf")
+    B.gdn_attn_paged(q, kc, vc, table, lens, cu, out, max_q_len=q_len)
+    B.gdn_read_device_status()
+    assert (out[:, :, 5] == float("inf")).all()
+    rest = [d for d in range(D) if d != 5]
+    torch.testing.assert_close(out[..., rest], clean[..., rest], rtol=2.0 ** -7, atol=2.0 ** -7)
