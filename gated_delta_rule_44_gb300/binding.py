@@ -580,7 +580,8 @@ def _attn_rows(name, t, shape, dtype, dev):
     """The gdn_attn_rows of a [tokens, heads, D] view (any token and head stride)."""
     if t is None:
         return _NO_ROWS
-    _attn_check(name, t, shape, dtype, dev)
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+        _attn_check(name, t, shape, dtype, dev)
     n, h, d = shape
     ts, hs, ds = t.stride()
     if ds != 1:
@@ -601,37 +602,56 @@ def _attn_flat(name, t, shape, dtype, dev):
     """Address and length of a contiguous tensor (0, 0 for None)."""
     if t is None:
         return 0, 0
-    _attn_check(name, t, shape, dtype, dev)
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+        _attn_check(name, t, shape, dtype, dev)
     if not t.is_contiguous():
         raise _bad(f"attention {name} must be contiguous")
     return t.data_ptr(), t.numel()
+
+
+def _attn_i32(name, t, n, dev):
+    """Address of a contiguous int32 [n] (0 for None)."""
+    if t is None:
+        return 0
+    if t.shape != (n,) or t.dtype is not torch.int32 or t.device != dev:
+        _attn_check(name, t, (n,), torch.int32, dev)
+    if not t.is_contiguous():
+        raise _bad(f"attention {name} must be contiguous")
+    return t.data_ptr()
 
 
 def _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dtype, dev, block_table_host):
     """Packs the gdn_attn_cache of k_cache, v_cache [pages, Hkv, page_size, D]
     (any strides but the last) and block_table [N, max_pages] int32 into the
     thread's buffer; returns its address and the host mirror to keep."""
-    P, _, page, _ = k_cache.shape if k_cache.dim() == 4 else (0, 0, 0, 0)
+    shape = k_cache.shape
+    P, _, page, _ = shape if len(shape) == 4 else (0, 0, 0, 0)
     shape = (P, Hkv, page, D)
     parts = []
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _attn_check(name, t, shape, dtype, dev)
+        if t.shape != shape or t.dtype is not dtype or t.device != dev:
+            _attn_check(name, t, shape, dtype, dev)
         ps, hs, ts, ds = t.stride()
         if ds != 1:
             raise _bad(f"attention {name}'s last dimension must be contiguous")
         if (P > 1 and ps == 0) or (Hkv > 1 and hs == 0) or (page > 1 and ts == 0):
             raise _bad(f"attention {name} is a broadcast view; pass a real cache")
-        parts += [t.data_ptr(), (P - 1) * ps + (Hkv - 1) * hs + (page - 1) * ts + D,
-                  ps if P > 1 else 0, hs if Hkv > 1 else 0, ts if page > 1 else 0]
-    if block_table.dim() != 2:
+        parts += (t.data_ptr(), (P - 1) * ps + (Hkv - 1) * hs + (page - 1) * ts + D,
+                  ps if P > 1 else 0, hs if Hkv > 1 else 0, ts if page > 1 else 0)
+    rows = block_table.shape
+    if len(rows) != 2:
         raise _bad_shape("attention block_table must be [N, max_pages]")
-    width = block_table.shape[1]
-    _attn_check("block_table", block_table, (N, width), torch.int32, dev)
-    if width > 1 and block_table.stride(1) != 1:
+    width = rows[1]
+    if rows[0] != N or block_table.dtype is not torch.int32 or block_table.device != dev:
+        _attn_check("block_table", block_table, (N, width), torch.int32, dev)
+    row, one = block_table.stride()
+    if width > 1 and one != 1:
         raise _bad("attention block_table's last dimension must be contiguous")
-    row = block_table.stride(0) if N > 1 else 0
-    host, host_p = _host_i32(block_table_host)
-    if host is not None:
+    if N <= 1:
+        row = 0
+    host, host_p = None, 0
+    if block_table_host is not None:
+        host, host_p = _host_i32(block_table_host)
         if host.shape != block_table.shape:
             raise _bad_shape("attention block_table_host must have block_table's shape")
         if N > 1 and row != width:  # the mirror shares the row stride
@@ -653,10 +673,11 @@ def _attn_mirror(name, t, n):
 
 
 def _attn_dims(q, kv, cu_seqlens):
-    if q.dim() != 3 or kv.dim() < 2:
+    shape, heads = q.shape, kv.shape
+    if len(shape) != 3 or len(heads) < 2:
         raise _bad_shape("attention query must be [tokens, heads, D]")
-    T, Hq, D = q.shape
-    return T, (T if cu_seqlens is None else cu_seqlens.numel() - 1), Hq, kv.shape[1], D
+    T, Hq, D = shape
+    return T, (T if cu_seqlens is None else cu_seqlens.numel() - 1), Hq, heads[1], D
 
 
 def _attn_call(fn, q, stream) -> None:
@@ -680,7 +701,7 @@ def gdn_attn_prepare(q, k, v, cu_seqlens, q_out, *, kv_lens=None, block_table=No
     the new rows of k_cache, v_cache [pages, Hkv, page_size, D] in place.
     cos_sin [positions, rot_dim] f32; cu_seqlens None: one token per sequence."""
     T, N, Hq, Hkv, D = _attn_dims(q, k, cu_seqlens)
-    dt, dev, i32 = q.dtype, q.device, torch.int32
+    dt, dev = q.dtype, q.device
     keep_cu, cu_host = _attn_mirror("cu_seqlens_host", cu_seqlens_host, N + 1)
     keep_kv, kv_host = _attn_mirror("kv_lens_host", kv_lens_host, N)
     keep_table, cache = None, 0
@@ -699,12 +720,12 @@ def gdn_attn_prepare(q, k, v, cu_seqlens, q_out, *, kv_lens=None, block_table=No
         *_attn_rows("value", v, (T, Hkv, D), dt, dev),
         *_attn_flat("q_norm_weight", q_norm_weight, (D,), dt, dev),
         *_attn_flat("k_norm_weight", k_norm_weight, (D,), dt, dev), *cs,
-        _attn_flat("positions", positions, (T,), i32, dev)[0],
-        _attn_flat("cu_seqlens", cu_seqlens, (N + 1,), i32, dev)[0],
-        _attn_flat("kv_lens", kv_lens, (N,), i32, dev)[0], cu_host, kv_host, cache,
+        _attn_i32("positions", positions, T, dev),
+        _attn_i32("cu_seqlens", cu_seqlens, N + 1, dev),
+        _attn_i32("kv_lens", kv_lens, N, dev), cu_host, kv_host, cache,
         *_attn_flat("q_out", q_out, (T, Hq, D), dt, dev),
         *_attn_flat("k_out", k_out, (T, Hkv, D), dt, dev))
-    _attn_call(lib().gdn_attn_prepare, q, stream)
+    _attn_call((_lib or lib()).gdn_attn_prepare, q, stream)
 
 
 def gdn_attn_varlen(q, k, v, cu_seqlens, out, *, scale=-1.0, gate=None, lse=None,
@@ -719,10 +740,10 @@ def gdn_attn_varlen(q, k, v, cu_seqlens, out, *, scale=-1.0, gate=None, lse=None
         *_attn_rows("query", q, (T, Hq, D), dt, dev), *_attn_rows("key", k, (T, Hkv, D), dt, dev),
         *_attn_rows("value", v, (T, Hkv, D), dt, dev),
         *_attn_rows("gate", gate, (T, Hq, D), dt, dev),
-        _attn_flat("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)[0], cu_host,
+        _attn_i32("cu_seqlens", cu_seqlens, N + 1, dev), cu_host,
         *_attn_flat("out", out, (T, Hq, D), dt, dev),
         *_attn_flat("lse", lse, (T, Hq), torch.float32, dev))
-    _attn_call(lib().gdn_attn_varlen, q, stream)
+    _attn_call((_lib or lib()).gdn_attn_varlen, q, stream)
 
 
 def gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len=0,
@@ -744,7 +765,7 @@ def gdn_attn_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, *
     T, N, Hq, Hkv, D = _attn_dims(q, k_cache, cu_seqlens)
     if kv_lens is None:
         raise _bad("kv_lens is NULL")
-    dt, dev, i32 = q.dtype, q.device, torch.int32
+    dt, dev = q.dtype, q.device
     keep_cu, cu_host = _attn_mirror("cu_seqlens_host", cu_seqlens_host, N + 1)
     keep_kv, kv_host = _attn_mirror("kv_lens_host", kv_lens_host, N)
     cache, keep_table = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dt, dev,
@@ -762,11 +783,11 @@ def gdn_attn_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, *
     _PAGED.pack_into(
         _args.buf, 0, T, N, Hq, Hkv, D, max_q_len, _dt(q), scale,
         *_attn_rows("query", q, (T, Hq, D), dt, dev), *_attn_rows("gate", gate, (T, Hq, D), dt, dev),
-        _attn_flat("cu_seqlens", cu_seqlens, (N + 1,), i32, dev)[0],
-        _attn_flat("kv_lens", kv_lens, (N,), i32, dev)[0], cu_host, kv_host, cache,
+        _attn_i32("cu_seqlens", cu_seqlens, N + 1, dev),
+        _attn_i32("kv_lens", kv_lens, N, dev), cu_host, kv_host, cache,
         *_attn_flat("out", out, (T, Hq, D), dt, dev),
         *_attn_flat("lse", lse, (T, Hq), torch.float32, dev), *ws)
-    _attn_call(lib().gdn_attn_paged, q, stream)
+    _attn_call((_lib or lib()).gdn_attn_paged, q, stream)
 
 
 def _host_u8(t: Optional[torch.Tensor]):
