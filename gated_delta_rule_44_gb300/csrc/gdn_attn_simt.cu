@@ -459,10 +459,13 @@ int row_block(int64_t need, int64_t D) {
 }
 
 int row_splits(int64_t ctas, int64_t max_kv) {
-  // Two CTAs per SM (about half the tile numbers are empty), ranges of at least 16
-  // keys a warp.
-  const int64_t want = (4 * 152 + ctas - 1) / ctas, most = max_kv / 128;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 64}));
+  // Four CTAs per SM (about half the tile numbers are empty), two at a time: unequal
+  // sequences even out.  Ranges of at least 32 keys a warp: each costs the join a step.
+  // (f32, 8 + 2 heads of 128; two per SM, 64 ranges at most, against this: one sequence of
+  // 100000 keys 99 and 72 us, 32 of 1 .. 8192 99 and 93, 128 of 1 .. 4096 181 and 165, 4
+  // of up to 7000 33 and 34; with ranges of 8 keys a warp the last takes 38.)
+  const int64_t want = (8 * 152 + ctas - 1) / ctas, most = max_kv / 256;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 256}));
 }
 
 template <typename T, int D, int RB>
