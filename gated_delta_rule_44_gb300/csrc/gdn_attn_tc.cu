@@ -57,8 +57,9 @@
 // A row whose result is not finite is evaluated again key by key (exact_row):
 // the product above multiplies a masked key's weight 0 into its v.
 //
-// Every wait is bounded (rows evaluated again extend it); once one gives up, every role leaves at its next
-// wait, copies and MMAs in flight are waited for (bounded) and TMEM is freed.
+// Every wait is bounded (rows evaluated again extend it); once one gives up, every
+// role leaves at its next wait, copies and MMAs in flight are waited for (bounded) and
+// TMEM is freed.
 //
 // Measured on GB300 (1.93 GHz, hot loop of one key tile pair = 2048 cycles of MMA):
 //   one 4096-token prompt, 32 + 4 heads of 128: 109 us, 1.26 PFLOP/s, 65 % of the
