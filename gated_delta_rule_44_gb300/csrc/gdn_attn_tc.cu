@@ -991,7 +991,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       // exchange nor the maximum itself delays a P.  P may thus exceed 2^8 (one
       // rounding relative to its size all the same); should it overflow, the row
       // is not finite and is evaluated again.
+      // A row with keys but no score in the first tile of the range (all of them -inf)
+      // has no reference for the others, which may lie where a weight relative to 0 is 0
+      // or infinite: it is evaluated again, too.
       float m = -INFINITY, l = 0.0f;
+      bool scoreless = false;
       uint32_t top_bits = 0;  // this warp's last published maximum
       const uint32_t to = tmem + lanes + kTO + qt * 128 + half * (D / 2);
       for (int kt = g.kt0; kt < g.kt1; ++kt, ++nk) {
@@ -1002,12 +1006,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         float f = 1.0f;
         bool raise = false;
         auto raise_to = [&](float top) {
-          if (top > m + kRaise || (m == -INFINITY && top > m)) {
+          if (top > m + kRaise) {
             raise = valid && jj > 0;
             f = ex2(m - top);
             m = top;
           }
-          if (m == -INFINITY) m = 0.0f;  // no score above -inf so far
         };
         if (jj > 1 && !idle) {
           if (!pair_wait()) return;
@@ -1045,6 +1048,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             float theirs = t;
             if (!swap(theirs)) return;
             raise_to(fmaxf(t, theirs));
+            if (m == -INFINITY) {  // no score above -inf: a reference that no score gave
+              m = 0.0f;
+              scoreless = last >= kt * BK;
+            }
           }
           if (raising) {
             // O is at rest: in the two-tile form S j follows P V j-1, in the other
@@ -1136,9 +1143,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const Partials part(a.ws, STREAM ? 2 * (int64_t)a.ctas : (int64_t)gridDim.x / CL * a.splits, a.rows, D);
         const int pr = row0 + tok * G + r % G;
-        // A sum of 0 with a key in sight: every weight was lost beside a reference
-        // of 0 that no score gave.
-        bool finite = isfinite(l) && !(l == 0.0f && last >= g.kt0 * BK);
+        // A sum of 0 with a key in sight: every weight was lost.
+        bool finite = isfinite(l) && !scoreless && !(l == 0.0f && last >= g.kt0 * BK);
         bf16* out = static_cast<bf16*>(p.out) + ((int64_t)t * p.Hq + h) * D + half * (D / 2);
 #pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
