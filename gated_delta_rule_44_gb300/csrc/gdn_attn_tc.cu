@@ -1111,9 +1111,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           sum01 = __fadd2_rn(sum01, sum23);
           l += sum01.x + sum01.y;
           if (jj > 0 && kt + 1 < g.kt1) {
-            // Published cut to bf16: only the agreement of the two warps matters.
+            // Published in bf16, rounded towards -inf: a reference above the scores by as
+            // much as a bf16 step of -20000 (128) would leave their weights out of f32's
+            // range, while one below them makes a weight that overflows, which is seen.
             const float t = m + log2f(fmaxf(__low2float(big), __high2float(big)));
-            top_bits = __float_as_uint(t) >> 16;
+            top_bits = (__float_as_uint(t) + (t < 0.0f ? 0xffffu : 0u)) >> 16;
             tops[((jj & 1) * 2 + half) * 32] = (uint16_t)top_bits;
             pair_arrive();
           }
@@ -1143,8 +1145,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const Partials part(a.ws, STREAM ? 2 * (int64_t)a.ctas : (int64_t)gridDim.x / CL * a.splits, a.rows, D);
         const int pr = row0 + tok * G + r % G;
-        // A sum of 0 with a key in sight: every weight was lost.
-        bool finite = isfinite(l) && !scoreless && !(l == 0.0f && last >= g.kt0 * BK);
+        bool finite = isfinite(l) && !scoreless;
         bf16* out = static_cast<bf16*>(p.out) + ((int64_t)t * p.Hq + h) * D + half * (D / 2);
 #pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {

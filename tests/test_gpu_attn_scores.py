@@ -119,3 +119,35 @@ def test_low_scores_beside_infinite_ones(q_lens, kv_lens, page, Hq, Hkv, D, dtyp
     ro, rl, pieces = reference(q, k, v, q_lens, kv_lens)
     R.check(R.f64(out), ro, R.bound(ro, pieces, dtype, dtype == BF), "out")
     R.check(R.f64(lse), rl, R.lse_bound(rl, pieces), "lse")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens,page,Hq,Hkv", [
+    ([1500], [1500], None, 2, 1),
+    ([1] * 64, [2048] * 64, 16, 1, 1),     # few rows: several key tiles per SM
+    ([1100], [2300], 64, 2, 1),
+])
+def test_scores_far_below_zero(q_lens, kv_lens, page, Hq, Hkv, D, cuda_device):
+    """Scores around -19966, blocks of 128 keys at -20028 between them: the running
+    reference moves up by 62 and has to stay within f32's range of the scores."""
+    g = torch.Generator().manual_seed(D + len(kv_lens))
+    L = sum(kv_lens)
+    score = torch.empty(L, Hkv, 2)
+    score[..., 0] = -19968.0
+    score[..., 1] = torch.randint(0, 129, (L, Hkv), generator=g).float() / 32
+    a = 0
+    for n in kv_lens:
+        score[a:a + n, :, 1][(torch.arange(n) // TILE) % 2 == 0] -= 64.0
+        a += n
+    score[..., 1] = score[..., 1].to(BF).float()
+    q = unit_q(sum(q_lens), Hq, D, BF, 2)
+    k, v = keys_with(score, Hkv, D, BF), torch.randn(L, Hkv, D, generator=g).to(BF)
+    out, lse = run(q, k, v, q_lens, kv_lens, page, cuda_device, g)
+    ro, rl, (A, ds, S, keys) = reference(q, k, v, q_lens, kv_lens)
+    # The scores are exact in f32.  What is left of their error in a weight is that of
+    # the factor to log2 units (two roundings) on a difference of at most 68 of them,
+    # and one rounding of the difference.
+    ds = np.full_like(ds, 68 * math.log(2.0) * 4 * R.U)
+    R.check(R.f64(out), ro, R.bound(ro, (A, ds, S, keys), BF, True), "out")
+    # lse: that factor, the one back and a sum, on a value of 13840.
+    R.check(R.f64(lse), rl, R.lse_bound(rl, (A, ds, S, keys)) + 8 * R.U * np.abs(rl), "lse")
