@@ -276,7 +276,8 @@ __device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& pa
 // that reference.  The tiled kernels multiply a masked key's weight 0 into its
 // v row, which is not 0 when that v is infinite or NaN; a row whose tiled
 // result is not finite is therefore evaluated here, where a masked key is not
-// touched at all.  bad pages read as zeros, as in the tiled kernels.
+// touched at all, and one that scores -inf adds nothing.  bad pages read as
+// zeros, as in the tiled kernels.
 template <typename T, int D>
 __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int t, int h, int k0,
                                        int k1, float (&acc)[D / 32], float& m, float& l) {
@@ -310,7 +311,7 @@ __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int
       l = x;
       return;
     }
-    if (x == -INFINITY && m == -INFINITY) continue;  // weight 0 beside any finite score
+    if (x == -INFINITY) continue;  // weight 0: no part, as of a masked key, whatever its v
     const float mn = fmaxf(m, x);
     const float f = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
     const float w = exp2f(x - mn);

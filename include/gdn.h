@@ -657,8 +657,10 @@ int gdn_validate_mixed(const gdn_mixed_meta* meta);
  * position L - q_len + i and attends to the keys at positions 0 .. L - q_len +
  * i of its own sequence.  A token at a negative position (L < q_len; L = 0
  * makes a whole sequence padding) sees no key: its output is 0, its lse -inf,
- * and nothing of it is written to a cache.  q_len = 0 is allowed.  Query head
- * h reads kv head h / (Hq / Hkv).
+ * and nothing of it is written to a cache.  A key that scores -inf has weight 0
+ * and takes no part, whatever its value; a token all of whose keys do is as one
+ * that sees none.  q_len = 0 is allowed.  Query head h reads kv head
+ * h / (Hq / Hkv).
  *
  * Common rules: D in {32, 64, 128, 256}; Hq a multiple of Hkv, Hq / Hkv <= 64;
  * f32 or bf16 rows of D contiguous values; every pointer 16-byte aligned and

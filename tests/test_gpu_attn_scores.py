@@ -151,3 +151,24 @@ def test_scores_far_below_zero(q_lens, kv_lens, page, Hq, Hkv, D, cuda_device):
     R.check(R.f64(out), ro, R.bound(ro, (A, ds, S, keys), BF, True), "out")
     # lse: that factor, the one back and a sum, on a value of 13840.
     R.check(R.f64(lse), rl, R.lse_bound(rl, (A, ds, S, keys)) + 8 * R.U * np.abs(rl), "lse")
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, BF), (256, BF), (128, F32), (32, BF)])
+@pytest.mark.parametrize("q_lens,kv_lens,page,Hq,Hkv", FORMS)
+def test_infinite_values_at_keys_without_weight(q_lens, kv_lens, page, Hq, Hkv, D, dtype, cuda_device):
+    """Keys that score -inf take no part, whatever their value is and wherever among
+    the others they stand."""
+    g = torch.Generator().manual_seed(D + 1 + sum(kv_lens))
+    L = sum(kv_lens)
+    score = torch.randint(-8, 9, (L, Hkv, 1), generator=g).float() / 4
+    out_of = torch.rand(L, generator=g) < 0.01
+    out_of[[0, L // 2, L - 1]] = True
+    score[out_of] = -math.inf
+    q = unit_q(sum(q_lens), Hq, D, dtype, 1)
+    k, v = keys_with(score, Hkv, D, dtype), torch.randn(L, Hkv, D, generator=g).to(dtype)
+    bad = v.clone()
+    bad[out_of] = math.inf
+    out, lse = run(q, k, bad, q_lens, kv_lens, page, cuda_device, g)
+    ro, rl, pieces = reference(q, k, v, q_lens, kv_lens)
+    R.check(R.f64(out), ro, R.bound(ro, pieces, dtype, dtype == BF), "out")
+    R.check(R.f64(lse), rl, R.lse_bound(rl, pieces), "lse")
