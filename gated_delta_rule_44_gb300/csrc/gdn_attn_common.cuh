@@ -61,6 +61,13 @@ __device__ inline SeqRange seq_range(const AttnLaunch& p, int s) {
   return r;
 }
 
+// The search of find_tile takes rising offsets as given, and of others may never land
+// on the sequence that falls. So sequence `id`, where there is one, is looked at with
+// tile number `id` as well: the numbers reach N and all are asked for.
+__device__ __forceinline__ bool own_range_bad(const AttnLaunch& p, int id) {
+  return id < p.N && seq_range(p, id).bad;
+}
+
 struct SeqTile {
   int s;       // sequence
   int t0;      // first token of the tile

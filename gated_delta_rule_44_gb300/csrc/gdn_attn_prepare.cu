@@ -101,11 +101,34 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int N, int t) {
   }
 }
 
+// The search takes rising offsets as given, and of others may never land on the
+// sequence that falls, so every sequence's are looked at once: by CTAs of their own,
+// which delay none of the others.
+constexpr int kCheckSeqs = 2048;  // sequences of such a CTA
+
+__device__ void check_offsets(const AttnPrepareLaunch& p, int cta) {
+  const int64_t cap = (int64_t)p.max_pages * p.page_size;
+  unsigned bad = 0;
+  const int s1 = min(p.N, (cta + 1) * kCheckSeqs);
+#pragma unroll 4
+  for (int s = cta * kCheckSeqs + threadIdx.x; s < s1; s += kThreads) {
+    const int a = p.cu[s], b = p.cu[s + 1], kv = p.kv_lens ? p.kv_lens[s] : 0;
+    if (a < 0 || b < a || b > p.T || (s == 0 && a != 0) || (s == p.N - 1 && b != p.T) || kv < 0 ||
+        (p.table != nullptr && kv > cap))
+      bad = kStatusBadSeqlens;
+  }
+  if (bad) atomicOr(p.status, bad);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 4) attn_prepare_kernel(
-    const __grid_constant__ AttnPrepareLaunch p, int heads, int heads_per_group) {
+    const __grid_constant__ AttnPrepareLaunch p, int heads, int heads_per_group, int token_ctas) {
   constexpr int LG = D / 8;               // lanes of a token
   constexpr int GROUPS = kThreads / LG;   // tokens of a CTA
+  if ((int)blockIdx.x >= token_ctas) {
+    if (blockIdx.y == 0) check_offsets(p, blockIdx.x - token_ctas);
+    return;
+  }
   const int lane = threadIdx.x % LG;
   const int t = blockIdx.x * GROUPS + threadIdx.x / LG;
   const int t_first = blockIdx.x * GROUPS + (threadIdx.x & ~31) / LG;  // the warp's first token
@@ -257,8 +280,9 @@ cudaError_t launch(const AttnPrepareLaunch& p, cudaStream_t st) {
   // of 40 heads: 13, 12, 13 and 15 us with 8, 4, 2 and 1; the rule takes 20 and 3.)
   int per = used;
   while (per > 1 && (int64_t)gx * ((used + per - 1) / per) < 2 * 152) per = (per + 1) / 2;
-  const dim3 grid(gx, (unsigned)((used + per - 1) / per));
-  attn_prepare_kernel<T, D><<<grid, kThreads, 0, st>>>(p, used, per);
+  const unsigned checks = p.cu == nullptr ? 0 : (unsigned)((p.N + kCheckSeqs - 1) / kCheckSeqs);
+  const dim3 grid(gx + checks, (unsigned)((used + per - 1) / per));
+  attn_prepare_kernel<T, D><<<grid, kThreads, 0, st>>>(p, used, per, (int)gx);
   note_launch();
   return cudaGetLastError();
 }

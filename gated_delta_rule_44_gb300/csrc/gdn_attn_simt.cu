@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1)
   const int id = (int)(gridDim.x / ranks / p.Hkv) - 1 - item / p.Hkv;
   const int hkv = item % p.Hkv;
   const SeqTile tile = find_tile(p, id, TT);
-  if (tile.bad && tid == 0) atomicOr(p.status, kStatusBadSeqlens);
+  if ((tid == 0 && tile.bad) || (tid == kThreads - 1 && rank == 0 && hkv == 0 && own_range_bad(p, id)))
+    atomicOr(p.status, kStatusBadSeqlens);
   if (tile.nt == 0) return;  // the whole cluster
   const int base = cu_at(p.cu, tile.s);
   const int rows = tile.nt * G;
@@ -300,7 +301,9 @@ __global__ void __launch_bounds__(kThreads, RB * D <= 512 ? 2 : 1) attn_rows_ker
   const int id = blockIdx.x / p.Hkv, hkv = blockIdx.x % p.Hkv;
   start_next_kernel();
   const SeqTile tile = find_tile(p, id, TT);
-  if (tile.bad && threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
+  if ((threadIdx.x == 0 && tile.bad) ||
+      (threadIdx.x == kThreads - 1 && blockIdx.y == 0 && hkv == 0 && own_range_bad(p, id)))
+    atomicOr(p.status, kStatusBadSeqlens);
   if (tile.nt == 0) return;
   const int base = cu_at(p.cu, tile.s), rows = tile.nt * G;
   const int hi = max(0, tile.pos0 + tile.nt);

@@ -526,7 +526,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             const int item = (int)bx / CL;
             const int id = (int)(gridDim.x / CL / p.Hkv) - 1 - item / p.Hkv;
             const SeqTile t = find_tile(p, id, NQ * CL * a.TQ);
-            if (t.bad && lane == 0) atomicOr(p.status, kStatusBadSeqlens);
+            if ((lane == 0 && t.bad) ||
+                (lane == 1 && by == 0 && item % p.Hkv == 0 && own_range_bad(p, id)))
+              atomicOr(p.status, kStatusBadSeqlens);
             if (t.nt > 0) {
               g.s = t.s;
               g.hkv = item % p.Hkv;
