@@ -283,6 +283,15 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _scratch(nbytes, device, stream):
+    """A call's own workspace, allocated on the stream that uses it: a block that the
+    allocator has for another one may have kernels of that one pending on it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _host_i32(t: Optional[torch.Tensor]):
     if t is None:
         return None, None
@@ -428,7 +437,7 @@ def gdn_kda_varlen(q, k, v, g, beta, state, cu_seqlens, out, *, scale=-1.0, stat
     if workspace is None:
         nbytes = gdn_kda_workspace_bytes(T, N, Hv, Dk, Dv, _dt(q), algo)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _scratch(nbytes, q.device, stream)
     a = gdn_kda_args(
         T=T, N=N, Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, act_dtype=_dt(q), scale=float(scale),
         q=_p(q), q_len=_n(q), k=_p(k), k_len=_n(k), v=_p(v), v_len=_n(v), g=_p(g), g_len=_n(g),
@@ -773,9 +782,7 @@ def gdn_attn_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, *
     if workspace is None:
         nbytes = gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len, _dt(q))
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            if stream is not None:  # freed for reuse only after the call's stream has run it
-                workspace.record_stream(stream)
+            workspace = _scratch(nbytes, dev, stream)
     elif workspace.device != dev:
         raise _bad(f"attention workspace is on {workspace.device}, not {dev}")
     ws = (0, 0) if workspace is None else (workspace.data_ptr(),
