@@ -34,15 +34,11 @@
 // cores the other's MMAs run.  One-tile form (D = 256, whose O fills half the
 // TMEM, and few rows): two S buffers, so that the next key tile's scores are
 // computed during a softmax.
-// Pair (D = 256 over prompts and chunks): two CTAs of a cluster have a row tile each of
-// one 256-row item and share its keys.  Every load goes to both (multicast), issued
-// by the two in turns, unit for unit; a unit is free when the MMAs of both are done
-// with it.  Alone a CTA took 128 KB per key tile from L2, 10 TB/s in all, and waited
-// for it: 1190 us for the eight prompts below, against 1153.  The rest of the way to
-// 1090 are the waits: a wait costs 150 cycles even for what is there, so that Q K^T
-// has its four units' before that for the S buffer; P V has each unit's in front of
-// it, as V comes late (5 units of 16 KB fit, 4 are a tile: the next tile's come as
-// this one's are freed, 1200 cycles behind).  4 + 6 units: 1195; 6 + 4: 1096.
+// At D = 256 a key tile's K and V are 128 KB for 128 rows, and the SMs together ask
+// 11 TB/s of L2 for them, which binds.  A wait costs 150 cycles even for what is there,
+// so over prompts and chunks Q K^T has its four units' before that for the S buffer
+// (1188 us with a wait in front of each unit, 1118 so, for the eight prompts below).
+// Few rows have the waits unit by unit.
 //
 // Work.  The tile form has a grid of (tile, kv head) items, the longest first,
 // and with few of them cuts each into key ranges whose sums a second kernel
@@ -68,9 +64,8 @@
 //     longer than the two tiles' MMAs.
 //   2048 tokens over 32768, the same heads, pages of 128: 720-780 us, 1.4 PFLOP/s,
 //     82-86 % of the sustained rate.
-//   eight prompts of 512 .. 8192, 16 + 2 heads of 256: 1090 us, 1.41 PFLOP/s, 82 % of
-//     the sustained rate.  A key tile takes 2650 cycles for 2048 of MMA: K and V wait
-//     for room.
+//   eight prompts of 512 .. 8192, 16 + 2 heads of 256: 1118 us, 1.38 PFLOP/s, 80 % of
+//     the sustained rate.
 //   256 single tokens over 1 .. 16384 keys, 32 + 4 heads of 128, pages of 64: 650 us,
 //     6.9 TB/s, the copy rate.  128 x 1 .. 4 drafts, pages of 16: 357 us, 87 %.
 #include <cuda.h>
@@ -112,12 +107,12 @@ struct Shared {
   uint64_t q_full, q_empty, s_full[2], p_full[2], turn[2], pv[2], o_full[2], o_empty[2], end[2];
   uint64_t v_land[kMaxRing];
   uint64_t pair[2][4];
-  uint64_t seg_full[2], seg_empty[2], clc_full, clc_read;
+  uint64_t seg_full[2], seg_empty[2], clc_full;
   alignas(16) uint4 clc;  // the next item's answer
   Seg seg[2];
   uint32_t tmem;
   int abort;
-  int redone;  // rows evaluated again so far, by either CTA of a pair
+  int redone;  // rows evaluated again so far
   uint32_t k_loads[kMaxRing], v_loads[kMaxRing], v_lands[kMaxRing], q_loads, clc_asked;  // issued so far
   int start_s, start_hkv, start_u;
   long long left;
@@ -279,54 +274,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 
-// The same into both CTAs of a pair, at the same place and barrier of each.
-__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void* tmap, uint32_t mbar, int c0,
-                                                 int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(mbar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, uint32_t mbar, int c0,
-                                                 int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(mbar), "h"((uint16_t)3)
-      : "memory");
-}
-// Arrives on the barrier of both CTAs once the MMAs so far are complete.
-__device__ __forceinline__ void mma_commit_pair(uint32_t mbar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
-      "%1;\n" ::"r"(mbar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-// Arrives on the barrier at this place of CTA `rank` of the pair.
-__device__ __forceinline__ void mbar_arrive_at(uint32_t mbar, uint32_t rank) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}\n" ::"r"(mbar),
-      "r"(rank)
-      : "memory");
-}
-// Adds 1 to the shared word at this place of CTA `rank` of the cluster.
-__device__ __forceinline__ void count_at(uint32_t word, uint32_t rank) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "red.relaxed.cluster.shared::cluster.add.u32 [a], 1;\n\t}\n" ::"r"(word),
-      "r"(rank)
-      : "memory");
-}
-__device__ __forceinline__ void pair_barrier() {  // all threads of both CTAs
-  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -338,22 +285,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Asks for a further CTA of the grid in place of its launch.
-template <bool PAIR>
 __device__ __forceinline__ void clc_ask(Shared* sh) {
-  const uint32_t mb = smem_u32(&sh->clc_full);
-  if constexpr (PAIR) {  // the answer goes to both CTAs
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
-        ".multicast::cluster::all.b128 [%0], [%1];\n" ::"r"(smem_u32(&sh->clc)),
-        "r"(mb)
-        : "memory");
-  } else {
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
-        "[%1];\n" ::"r"(smem_u32(&sh->clc)),
-        "r"(mb)
-        : "memory");
-  }
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];\n" ::"r"(smem_u32(&sh->clc)),
+      "r"(smem_u32(&sh->clc_full))
+      : "memory");
 }
 // The answer: false when no CTA was left.
 __device__ __forceinline__ bool clc_answer(Shared* sh, uint32_t& x, uint32_t& y) {
@@ -371,7 +308,7 @@ __device__ __forceinline__ bool clc_answer(Shared* sh, uint32_t& x, uint32_t& y)
   return ok != 0;
 }
 
-template <int D, int NQ, bool PAGED, bool STREAM, bool PAIR>
+template <int D, int NQ, bool PAGED, bool STREAM>
 __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnLaunch p, const __grid_constant__ CUtensorMap mq,
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -383,15 +320,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   const uint32_t sq = smem_u32(smem), sk = sq + C::kQ, sv = sk + ST * C::kUnit;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.Hq / p.Hkv;
-  constexpr int CL = PAIR ? 2 : 1;
-  // Of a pair, the CTA's row tile.
-  uint32_t rank = 0;
-  if constexpr (PAIR) asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
 
   start_next_kernel();
   if (warp == 0) {
     if (lane == 0) {
-      constexpr int kReleases = NQ == 2 || PAIR ? 2 : 1;  // MMA warps that use a unit, of a pair in both CTAs
+      constexpr int kReleases = NQ;  // MMA warps that use a unit
       for (int i = 0; i < ST; ++i) {
         mbar_init(smem_u32(&sh->k_full[i]), 1);
         mbar_init(smem_u32(&sh->k_empty[i]), kReleases);
@@ -415,7 +348,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sh->pair[i][w]), 2);
       }
       mbar_init(smem_u32(&sh->clc_full), 1);
-      mbar_init(smem_u32(&sh->clc_read), 1);
       sh->abort = sh->redone = 0;
       sh->q_loads = sh->clc_asked = 0;
       fence_mbar_init();
@@ -469,7 +401,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   }
   fence_before_sync();
   __syncthreads();
-  if constexpr (PAIR) pair_barrier();  // the other CTA's barriers stand
   fence_after_sync();
   // All 512 columns: their base is 0, which the addresses below use as such.
   if (sh->tmem != 0 && tid == 0) atomicOr(p.status, kStatusTimeout);
@@ -496,14 +427,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
     }
   };
-  // Every unit of a ring has been released: of a pair, the other CTA's last arrivals
-  // are in, and this one may end.
-  auto drain = [&](Ring ring, uint32_t filled, uint64_t* empty) {
-    for (int i = 0; i < ST; ++i, ring.step(), ++filled)
-      if (filled >= ST)
-        if (!warp_wait(&empty[ring.st], ring.round ^ 1, sh, p.status)) return;
-  };
-
   if (warp == 0) {
     // ---- work; loads of Q and K ----
     SegIter iter{};
@@ -514,7 +437,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       uint32_t filled = 0;  // units so far
       int nseg = 0, loads = 0, asked = 0;
       bool more = true;     // the tile form's grid may have an item left
-      uint32_t bx = blockIdx.x - rank, by = blockIdx.y;  // (of a pair, its first CTA's)
+      uint32_t bx = blockIdx.x, by = blockIdx.y;
       for (;;) {
         // The next range, into g.
         Seg g;
@@ -523,18 +446,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           if (!iter.next(p, g)) g.s = -1;
         } else {
           while (more) {
-            const int item = (int)bx / CL;
-            const int id = (int)(gridDim.x / CL / p.Hkv) - 1 - item / p.Hkv;
-            const SeqTile t = find_tile(p, id, NQ * CL * a.TQ);
+            const int item = (int)bx;
+            const int id = (int)(gridDim.x / p.Hkv) - 1 - item / p.Hkv;
+            const SeqTile t = find_tile(p, id, NQ * a.TQ);
             if ((lane == 0 && t.bad) ||
                 (lane == 1 && by == 0 && item % p.Hkv == 0 && own_range_bad(p, id)))
               atomicOr(p.status, kStatusBadSeqlens);
             if (t.nt > 0) {
               g.s = t.s;
               g.hkv = item % p.Hkv;
-              g.t0 = t.t0 + (int)rank * a.TQ;
-              g.nt = t.nt - (int)rank * a.TQ;  // <= 0: no row for the pair's second CTA
-              g.pos0 = t.pos0 + (int)rank * a.TQ;
+              g.t0 = t.t0;
+              g.nt = t.nt;
+              g.pos0 = t.pos0;
               g.hi = max(0, t.pos0 + t.nt);
               const int n = (g.hi + BK - 1) / BK;
               g.kt0 = (int)((int64_t)n * by / a.splits);
@@ -543,22 +466,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             }
             // The item after this one is asked for now and taken when this one's
             // loads have been issued.
-            if (asked > 0) {
-              fence_proxy_async();  // the last answer has been read
-              __syncwarp();
-              if constexpr (PAIR) {
-                if (rank == 0) {  // by the other CTA, too
-                  if (!warp_wait(&sh->clc_read, (asked - 1) & 1, sh, p.status)) return;
-                } else if (elect_one()) {
-                  mbar_arrive_at(smem_u32(&sh->clc_read), 0);
-                }
-              }
-            }
+            if (asked > 0) fence_proxy_async();  // the last answer has been read
             __syncwarp();
             if (elect_one()) {
               sh->clc_asked = asked + 1;
               mbar_expect_tx(smem_u32(&sh->clc_full), 16);
-              if (rank == 0) clc_ask<PAIR>(sh);
+              clc_ask(sh);
             }
             ++asked;
             if (g.s >= 0) break;
@@ -577,10 +490,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           __syncwarp();
           ++nseg;
         }
-        if (g.s < 0) {
-          if constexpr (PAIR) drain(ring, filled, sh->k_empty);
-          return;
-        }
+        if (g.s < 0) return;
         const int kt0 = uni(g.kt0), n = uni(g.kt1) - kt0, hi = uni(g.hi), hkv = uni(g.hkv);
         const int per_tile = BK / a.pbk;
         const int row0 = PAGED ? 0 : uni(cu_at(p.cu, g.s));
@@ -608,20 +518,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             if (elect_one()) {
               ++sh->k_loads[ring.st];
               mbar_expect_tx(full, groups * a.pbk * 128u);
-              if constexpr (!PAGED && !PAIR) tma_load_3d(dst, &mk, full, u * 64, row0 + j0, hkv);
-              if constexpr (!PAGED && PAIR)  // units in turn by either CTA
-                if ((filled & 1) == rank) tma_load_3d_pair(dst, &mk, full, u * 64, row0 + j0, hkv);
+              if constexpr (!PAGED) tma_load_3d(dst, &mk, full, u * 64, row0 + j0, hkv);
             }
             if constexpr (PAGED) {
               __syncwarp();
               const int row = (j0 + lane * a.pbk) % p.page_size;
-              if constexpr (PAIR) {
-                if (lane < groups && (filled & 1) == rank)
-                  tma_load_4d_pair(dst + lane * a.pbk * 128, &mk, full, u * 64, row, hkv, page);
-              } else {
-                if (lane < groups)
-                  tma_load_4d(dst + lane * a.pbk * 128, &mk, full, u * 64, row, hkv, page);
-              }
+              if (lane < groups) tma_load_4d(dst + lane * a.pbk * 128, &mk, full, u * 64, row, hkv, page);
               __syncwarp();
             }
           }
@@ -675,10 +577,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       return true;
     };
     // The MMAs so far have read the unit.
-    auto release = [&](uint64_t* empty) {
-      if constexpr (PAIR) mma_commit_pair(smem_u32(empty));
-      else mma_commit(smem_u32(empty));
-    };
+    auto release = [&](uint64_t* empty) { mma_commit(smem_u32(empty)); };
     // S[buf] = Q[q] K^T of unit u.
     auto qk_unit = [&](uint32_t buf, int u, uint32_t at) {
       if (elect_one()) {
@@ -760,12 +659,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         } else if (warp == 1) {
           if (!wait(sh->q_full, nseg & 1)) return;
           for (int j = 0; j < n; ++j, ++nk) {
-            if constexpr (PAIR)  // (for single tokens, bound by the reads of K, 1 % slower)
+            if constexpr (!STREAM)  // (for single tokens, bound by the reads of K, 1 % slower)
               if (!land(kr, sh->k_full, ak)) return;
             if (nk >= 2)  // P V has read the buffer's last P
               if (!wait(sh->pv[nk & 1], ((nk >> 1) - 1) & 1)) return;
             fence_after_sync();
-            if constexpr (PAIR) {
+            if constexpr (!STREAM) {
 #pragma unroll
               for (int u = 0; u < NU; ++u) qk_unit(nk & 1, u, ak[u]);
             } else {
@@ -780,23 +679,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           if (elect_one()) mma_commit(smem_u32(&sh->q_empty));
         } else {
           for (int j = 0; j < n; ++j, ++nk) {
-            if constexpr (!PAIR)
-              if (!land(vr, sh->v_full, av)) return;
+            if (!land(vr, sh->v_full, av)) return;
             if (j == 0 && nseg > 0)
               if (!wait(sh->o_empty[0], (nseg - 1) & 1)) return;
             if (!wait(sh->p_full[nk & 1], (nk >> 1) & 1)) return;
             fence_after_sync();
-            if constexpr (PAIR) {
 #pragma unroll
-              for (int u = 0; u < NU; ++u, vr.step()) {
-                if (!wait(sh->v_full[vr.st], vr.round)) return;
-                fence_after_sync();
-                pv_unit(nk & 1, j > 0, u, vr.st);
-              }
-            } else {
-#pragma unroll
-              for (int u = 0; u < NU; ++u) pv_unit(nk & 1, j > 0, u, av[u]);
-            }
+            for (int u = 0; u < NU; ++u) pv_unit(nk & 1, j > 0, u, av[u]);
             if (elect_one()) {
               mma_commit(smem_u32(&sh->pv[nk & 1]));
               if (j == n - 1) mma_commit(smem_u32(&sh->o_full[0]));
@@ -856,11 +745,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 #pragma unroll
                   for (int b = 0; b < NB; ++b) {
                     const int d = db * VD + b * 64, row = row0 + j0 + kh * VK;
-                    if constexpr (PAIR) {
-                      if ((filled & 1) == rank) tma_load_3d_pair(dst + b * VK * 128, &mv, full, d, row, hkv);
-                    } else {
-                      tma_load_3d(dst + b * VK * 128, &mv, full, d, row, hkv);
-                    }
+                    tma_load_3d(dst + b * VK * 128, &mv, full, d, row, hkv);
                   }
               }
             }
@@ -868,11 +753,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               const int page = __shfl_sync(0xffffffffu, pages, (kh * per_unit + grp) & 31);
               const uint32_t to = dst + blk * VK * 128 + grp * a.pbv * 128;
               const int d = db * VD + blk * 64, row = (j0 + kh * VK + grp * a.pbv) % p.page_size;
-              if constexpr (PAIR) {
-                if (grp < groups && (filled & 1) == rank) tma_load_4d_pair(to, &mv, full, d, row, hkv, page);
-              } else {
-                if (grp < groups) tma_load_4d(to, &mv, full, d, row, hkv, page);
-              }
+              if (grp < groups) tma_load_4d(to, &mv, full, d, row, hkv, page);
               __syncwarp();
             }
           }
@@ -903,7 +784,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           }
         }
       }
-      if constexpr (PAIR) drain(ring, filled, sh->v_empty);
     };
     role();
     if constexpr (STREAM) {
@@ -941,7 +821,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     const float c = p.scale * kLog2e;
     const float2 c2 = make_float2(c, c);
     const int tok = qt * a.TQ + r / G;                  // token of the tile
-    const int row0 = (int)rank * a.TQ * G;              // first row in a workspace block
     auto role = [&] {
     uint32_t nk = 0, np = 0;
     // Meeting the pair's other warp (bounded; false: leave).
@@ -972,12 +851,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     while (next_seg(g)) {
       if (NQ == 2 && qt == 1 && g.nt <= a.TQ) continue;   // no second row tile
       if (g.kt0 == g.kt1) {  // no key for any row
-        const Partials part(a.ws, (int64_t)gridDim.x / CL * a.splits, a.rows, D);
+        const Partials part(a.ws, (int64_t)gridDim.x * a.splits, a.rows, D);
         const float zero[D / 32] = {};
         const int rows = (min(g.nt, (qt + 1) * a.TQ) - qt * a.TQ) * G;
         for (int i = (warp - 4) & 7; i < rows; i += 8) {
           const int in_tile = qt * a.TQ * G + i, t = g.t0 + in_tile / G, h = g.hkv * G + in_tile % G;
-          if (g.slot >= 0) part.put<D / 32>(g.slot, row0 + in_tile, lane, zero, -INFINITY, 0.0f);
+          if (g.slot >= 0) part.put<D / 32>(g.slot, in_tile, lane, zero, -INFINITY, 0.0f);
           else finish_row<bf16, D>(p, t, h, lane, zero, -INFINITY, 0.0f);
         }
         continue;
@@ -1145,8 +1024,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         if (!swap(theirs)) return;
         l = half == 0 ? l + theirs : theirs + l;  // the same sum on both sides
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const Partials part(a.ws, STREAM ? 2 * (int64_t)a.ctas : (int64_t)gridDim.x / CL * a.splits, a.rows, D);
-        const int pr = row0 + tok * G + r % G;
+        const Partials part(a.ws, STREAM ? 2 * (int64_t)a.ctas : (int64_t)gridDim.x * a.splits, a.rows, D);
+        const int pr = tok * G + r % G;
         bool finite = isfinite(l) && !scoreless;
         bf16* out = static_cast<bf16*>(p.out) + ((int64_t)t * p.Hq + h) * D + half * (D / 2);
 #pragma unroll 1
@@ -1219,7 +1098,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
                              em, el);
           if (g.slot >= 0) part.put<D / 32>(g.slot, rp, lane, acc, em, el);
           else finish_row<bf16, D>(p, rt, rh, lane, acc, em, el);
-          if (lane < CL) count_at(smem_u32(&sh->redone), PAIR ? lane : 0);
+          if (lane == 0) atomicAdd(&sh->redone, 1);
         }
       }
       ++seg_n;
@@ -1248,10 +1127,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     __syncthreads();
   }
   if (warp == 2) tmem_dealloc(sh->tmem, 512);
-  if constexpr (PAIR) {  // until here the other CTA writes to this one's memory
-    __syncthreads();
-    pair_barrier();
-  }
 }
 
 // Joins the ranges of the pairs that the stream form cut: CTA c serves the pair
@@ -1335,7 +1210,7 @@ constexpr int tiles_of() {
 
 size_t info_bytes(int ctas) { return ((size_t)ctas * sizeof(int4) + 255) & ~(size_t)255; }
 
-template <int D, int NQ, bool PAGED, bool STREAM, bool PAIR = false>
+template <int D, int NQ, bool PAGED, bool STREAM>
 cudaError_t run(const AttnLaunch& p, TcArgs a, dim3 grid, cudaStream_t st) {
   using C = Cfg<D, NQ>;
   CUtensorMap mq, mk, mv;
@@ -1343,30 +1218,12 @@ cudaError_t run(const AttnLaunch& p, TcArgs a, dim3 grid, cudaStream_t st) {
       !(PAGED ? pages_map(&mv, p.vc, p, a.pbv) : rows_map(&mv, p.v, p, a.pbv)))
     return cudaErrorInvalidValue;
   static const cudaError_t attr =
-      cudaFuncSetAttribute(attn_tc_kernel<D, NQ, PAGED, STREAM, PAIR>,
+      cudaFuncSetAttribute(attn_tc_kernel<D, NQ, PAGED, STREAM>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
   if (attr != cudaSuccess) return attr;
-  if constexpr (PAIR) {
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 2;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kBytes;
-    cfg.stream = st;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, NQ, PAGED, STREAM, PAIR>, p, mq, mk, mv, a);
-    note_launch();
-    return e;
-  } else {
-    attn_tc_kernel<D, NQ, PAGED, STREAM, PAIR><<<grid, C::kThreads, C::kBytes, st>>>(p, mq, mk, mv, a);
-    note_launch();
-    return cudaGetLastError();
-  }
+  attn_tc_kernel<D, NQ, PAGED, STREAM><<<grid, C::kThreads, C::kBytes, st>>>(p, mq, mk, mv, a);
+  note_launch();
+  return cudaGetLastError();
 }
 
 template <int D>
@@ -1391,16 +1248,13 @@ cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
     return launch_after(attn_stream_join_kernel<D>, dim3(sms, std::min(a.rows, 16)), 256, st, p, a);
   }
   a.q_box = a.TQ;
-  // D = 256: two CTAs share an item, a row tile each.
-  constexpr int CL = NQ == 1 ? 2 : 1;
-  const int TT = 2 * a.TQ;
+  const int TT = NQ * a.TQ;
   const int64_t items = tile_bound(p.T, p.N, TT) * p.Hkv;
-  a.rows = 256;
-  if (p.table == nullptr)
-    return run<D, NQ, false, false, CL == 2>(p, a, dim3((unsigned)(items * CL)), st);
-  a.splits = tile_splits(items * CL, (int64_t)p.max_pages * p.page_size, sms);
+  a.rows = NQ * 128;
+  if (p.table == nullptr) return run<D, NQ, false, false>(p, a, dim3((unsigned)items), st);
+  a.splits = tile_splits(items, (int64_t)p.max_pages * p.page_size, sms);
   a.ws = static_cast<float*>(p.ws);
-  cudaError_t e = run<D, NQ, true, false, CL == 2>(p, a, dim3((unsigned)(items * CL), a.splits), st);
+  cudaError_t e = run<D, NQ, true, false>(p, a, dim3((unsigned)items, a.splits), st);
   if (e != cudaSuccess || a.splits == 1) return e;
   return launch_attn_join(p, a.splits, a.rows, TT, st);
 }
@@ -1426,9 +1280,10 @@ size_t attn_tc_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, in
   const int64_t G = Hq / Hkv;
   if (use_stream(max_q, G))
     return info_bytes(sms) + Partials::bytes(2 * (int64_t)sms, (int)(max_q * G), D);
-  const int64_t items = tile_bound(T, N, 2 * (128 / G)) * Hkv;
-  const int splits = tile_splits(D <= 128 ? items : 2 * items, INT64_MAX, sms);
-  return splits > 1 ? Partials::bytes(items * splits, 256, D) : 0;
+  const int NQ = D <= 128 ? tiles_of<128>() : tiles_of<256>();
+  const int64_t items = tile_bound(T, N, NQ * (128 / G)) * Hkv;
+  const int splits = tile_splits(items, INT64_MAX, sms);
+  return splits > 1 ? Partials::bytes(items * splits, NQ * 128, D) : 0;
 }
 
 cudaError_t launch_attn_tc(const AttnLaunch& p, cudaStream_t st) {
