@@ -210,7 +210,7 @@ __device__ __forceinline__ bool parked_wait(uint32_t mb, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// The bounded wait of every role; false: leave.  The rare part is kept out of
+// The long part of every role's bounded wait; false: leave.  It is kept out of
 // line: the roles' hot loops share the instruction cache.
 __device__ __noinline__ bool long_wait(uint32_t mb, uint32_t parity, Shared* sh, unsigned* status) {
   long long t0 = clock64();
@@ -233,15 +233,14 @@ __device__ __noinline__ bool long_wait(uint32_t mb, uint32_t parity, Shared* sh,
     }
   }
 }
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Shared* sh,
-                                              unsigned* status) {
-  const uint32_t mb = smem_u32(bar);
-  return parked_wait(mb, parity) || long_wait(mb, parity, sh, status);
-}
-// The same by a whole warp, with one answer for it.
+// By a whole warp, with one answer for it: near the limit the lanes' own answers may
+// differ, and a warp that some of them leave may not go on with the rest.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared* sh,
                                           unsigned* status) {
-  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, sh, status));
+  const uint32_t mb = smem_u32(bar);
+  const bool ok = parked_wait(mb, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return __all_sync(0xffffffffu, ok || long_wait(mb, parity, sh, status));
 }
 // One lane of a converged warp.  The issuing roles run with all 32 lanes on
 // values the compiler can see are the warp's (from lane 0 by a shuffle), and
@@ -263,7 +262,7 @@ __device__ __forceinline__ T uni(T x) {
 }
 // Inside a role: the bounded wait, or leave the role.
 #define WAIT(bar, parity) \
-  if (!wait_or_abort(&(bar), (parity), sh, p.status)) return
+  if (!warp_wait(&(bar), (parity), sh, p.status)) return
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t mbar, int c0,
                                             int c1, int c2, int c3) {
@@ -836,7 +835,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&pair));
     };
-    auto pair_wait = [&]() -> bool { return wait_or_abort(&pair, np++ & 1, sh, p.status); };
+    auto pair_wait = [&]() -> bool { return warp_wait(&pair, np++ & 1, sh, p.status); };
     // x becomes the row's value of it from the other warp (between two meetings
     // that keep `val` from being written early).
     auto swap = [&](float& x) -> bool {
