@@ -284,10 +284,12 @@ __device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& pa
 // v row, which is not 0 when that v is infinite or NaN; a row whose tiled
 // result is not finite is therefore evaluated here, where a masked key is not
 // touched at all, and one that scores -inf adds nothing.  bad pages read as
-// zeros, as in the tiled kernels.
+// zeros, as in the tiled kernels.  `progress` (may be null) counts on every 2^14
+// keys, for others that wait.
 template <typename T, int D>
 __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int t, int h, int k0,
-                                       int k1, float (&acc)[D / 32], float& m, float& l) {
+                                       int k1, float (&acc)[D / 32], float& m, float& l,
+                                       int* progress = nullptr) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int hkv = h / (p.Hq / p.Hkv);
@@ -302,6 +304,7 @@ __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int
   l = 0.0f;
   const float c = p.scale * kLog2e;
   for (int j = k0; j < k1; ++j) {
+    if (progress != nullptr && lane == 0 && (j & 0x3fff) == 0) atomicAdd(progress, 1);
     const int64_t ko = key_offset(p, false, s, base, hkv, j);
     const int64_t vo = key_offset(p, true, s, base, hkv, j);
     float dot = 0.0f;

@@ -53,9 +53,9 @@
 // A row whose result is not finite is evaluated again key by key (exact_row):
 // the product above multiplies a masked key's weight 0 into its v.
 //
-// Every wait is bounded (rows evaluated again extend it); once one gives up, every
-// role leaves at its next wait, copies and MMAs in flight are waited for (bounded) and
-// TMEM is freed.
+// Every wait is bounded (counted from the last sign of a row evaluated again); once one
+// gives up, every role leaves at its next wait, copies and MMAs in flight are waited for
+// (bounded) and TMEM is freed.
 //
 // Measured on GB300 (1.93 GHz, hot loop of one key tile pair = 2048 cycles of MMA):
 //   one 4096-token prompt, 32 + 4 heads of 128: 109 us, 1.26 PFLOP/s, 65 % of the
@@ -112,7 +112,7 @@ struct Shared {
   Seg seg[2];
   uint32_t tmem;
   int abort;
-  int redone;  // rows evaluated again so far
+  int redone;  // rows evaluated again so far, and parts of them
   uint32_t k_loads[kMaxRing], v_loads[kMaxRing], v_lands[kMaxRing], q_loads, clc_asked;  // issued so far
   int start_s, start_hkv, start_u;
   long long left;
@@ -220,7 +220,8 @@ __device__ __noinline__ bool long_wait(uint32_t mb, uint32_t parity, Shared* sh,
     for (int i = 0; i < 64; ++i)
       if (parked_wait(mb, parity)) return true;
     if (*(volatile int*)&sh->abort) return false;
-    // Rows evaluated again take about 1 us a key: the time counts from the last one.
+    // Rows evaluated again take about 1 us a key: the time counts from the last sign of
+    // one of them.
     const int now = *(volatile int*)&sh->redone;
     if (now != redone) {
       redone = now;
@@ -1094,7 +1095,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           const int rl = __shfl_sync(0xffffffffu, last, src), rp = __shfl_sync(0xffffffffu, pr, src);
           float acc[D / 32], em, el;
           exact_row<bf16, D>(p, g.s, cu_at(p.cu, g.s), rt, rh, g.kt0 * BK, min(g.kt1 * BK, rl + 1), acc,
-                             em, el);
+                             em, el, &sh->redone);
           if (g.slot >= 0) part.put<D / 32>(g.slot, rp, lane, acc, em, el);
           else finish_row<bf16, D>(p, rt, rh, lane, acc, em, el);
           if (lane == 0) atomicAdd(&sh->redone, 1);
