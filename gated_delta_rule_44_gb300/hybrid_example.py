@@ -88,7 +88,15 @@ class HybridStack:
 
 def generate(stack: HybridStack, x, prompt_lens: List[int], total_lens: List[int]):
     """Rows x (the sequences packed, total_lens each) through the stack: the first
-    prompt_lens of each as one batch of prompts, the others token by token."""
+    prompt_lens of each as one batch of prompts, the others token by token, one of
+    every sequence a step: each has as many of them as the others."""
+    steps = total_lens[0] - prompt_lens[0]
+    if any(t - n != steps for t, n in zip(total_lens, prompt_lens)) or steps < 0:
+        raise ValueError(f"sequences with unequal numbers of further tokens: prompts of {list(prompt_lens)} "
+                         f"tokens in sequences of {list(total_lens)}")
+    if len(total_lens) != len(prompt_lens) or sum(total_lens) != x.shape[0]:
+        raise ValueError(f"{len(prompt_lens)} prompts and sequences of {list(total_lens)} tokens do not "
+                         f"make {x.shape[0]} rows")
     starts = [sum(total_lens[:i]) for i in range(len(total_lens))]
     first = torch.cat([x[a:a + n] for a, n in zip(starts, prompt_lens)])
     y = stack.step(first, list(prompt_lens), list(prompt_lens), True)
@@ -96,8 +104,7 @@ def generate(stack: HybridStack, x, prompt_lens: List[int], total_lens: List[int
     for a, n in zip(starts, prompt_lens):
         out[a:a + n] = y[at:at + n]
         at += n
-    steps = max(t - n for t, n in zip(total_lens, prompt_lens))
-    for i in range(steps):     # equal numbers of further tokens, one of each a step
+    for i in range(steps):
         rows = torch.tensor([a + n + i for a, n in zip(starts, prompt_lens)], device=x.device)
         out[rows] = stack.step(x[rows], [1] * len(rows), [n + i + 1 for n in prompt_lens], False)
     return out
