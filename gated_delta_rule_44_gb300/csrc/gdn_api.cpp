@@ -1368,7 +1368,6 @@ int attn_paged(const gdn_attn_paged_args* a, void* stream) {
   p.out = a->out;
   p.lse = a->lse;
   p.ws = a->workspace;
-  p.ws_bytes = a->workspace_bytes;
   p.status = gdn::status_word();
   if (p.status == nullptr) return fail(GDN_ERR_CUDA, "device status word unavailable");
   return launch_result(launch_attn(p, st), "gdn_attn_paged");

@@ -224,7 +224,6 @@ struct AttnLaunch {
   void* out;      // [T, Hq, D]
   float* lse;     // [T, Hq] or null
   void* ws;
-  size_t ws_bytes;
   unsigned* status;
 };
 // CUDA-core form: any supported size (D in {32, 64, 128, 256}, Hq / Hkv <= 64).
