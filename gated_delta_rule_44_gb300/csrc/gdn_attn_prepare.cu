@@ -17,7 +17,7 @@
 // heads.  What binds before HBM is the number of instructions of a row: with
 // partners fetched by shuffles and addresses multiplied out per head, 222 of them
 // took 44 us where HBM takes 25 (four 2048-token prompts of 16 + 2 + 2 heads of
-// 256); now about 100 take 39, 64 % of the copy rate.
+// 256); now about 100 take 37, 67 % of the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

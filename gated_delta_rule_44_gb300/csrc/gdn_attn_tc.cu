@@ -12,7 +12,7 @@
 // in tensor memory), so nothing of a tile but K and V passes through shared
 // memory.  m is a reference near the running maximum: the first tile's, then raised,
 // and O and l scaled, only when the maximum of the tiles before has outgrown it by
-// 2^8, which is rare.  It does not matter to P's rounding (2^-9 relative at any
+// 2^8, which is rare.  It does not matter to P's rounding (2^-8 relative at any
 // size); P overflows only where one tile's scores exceed all before by 2^120, and
 // such a row is evaluated again (below).  l sums P before the rounding.
 //
@@ -37,8 +37,8 @@
 // At D = 256 a key tile's K and V are 128 KB for 128 rows, and the SMs together ask
 // 11 TB/s of L2 for them, which binds.  A wait costs 150 cycles even for what is there,
 // so over prompts and chunks Q K^T has its four units' before that for the S buffer
-// (1188 us with a wait in front of each unit, 1118 so, for the eight prompts below).
-// Few rows have the waits unit by unit.
+// (the eight prompts below: 6 % slower with a wait in front of each unit).  Few rows have
+// the waits unit by unit.
 //
 // Work.  The tile form has a grid of (tile, kv head) items, the longest first,
 // and with few of them cuts each into key ranges whose sums a second kernel
@@ -62,12 +62,12 @@
 //     burst rate of a library product.  An iteration takes 3070 cycles: a tile's
 //     chain of scores, softmax (1300), P V and Q K^T (1150) and their latencies is
 //     longer than the two tiles' MMAs.
-//   2048 tokens over 32768, the same heads, pages of 128: 720-780 us, 1.4 PFLOP/s,
-//     82-86 % of the sustained rate.
-//   eight prompts of 512 .. 8192, 16 + 2 heads of 256: 1118 us, 1.38 PFLOP/s, 80 % of
-//     the sustained rate.
-//   256 single tokens over 1 .. 16384 keys, 32 + 4 heads of 128, pages of 64: 650 us,
-//     6.9 TB/s, the copy rate.  128 x 1 .. 4 drafts, pages of 16: 357 us, 87 %.
+//   2048 tokens over 32768, the same heads, pages of 128: 720-760 us, 1.44-1.52 PFLOP/s,
+//     84-88 % of the sustained rate.
+//   eight prompts of 512 .. 8192, 16 + 2 heads of 256: 1100-1170 us (the latter call after
+//     call, at the power limit), 1.31-1.40 PFLOP/s, 77-82 % of the sustained rate.
+//   256 single tokens over 1 .. 16384 keys, 32 + 4 heads of 128, pages of 64: 660-670 us,
+//     6.7 TB/s, 99 % of the copy rate.  128 x 1 .. 4 drafts, pages of 16: 352 us, 88 %.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -235,7 +235,8 @@ __device__ __noinline__ bool long_wait(uint32_t mb, uint32_t parity, Shared* sh,
   }
 }
 // By a whole warp, with one answer for it: near the limit the lanes' own answers may
-// differ, and a warp that some of them leave may not go on with the rest.
+// differ, and a warp that some of them leave may not go on with the rest.  (A vote in
+// front of the branch: behind a branch per lane it cost the tile forms 1 %.)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared* sh,
                                           unsigned* status) {
   const uint32_t mb = smem_u32(bar);

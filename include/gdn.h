@@ -665,13 +665,21 @@ int gdn_validate_mixed(const gdn_mixed_meta* meta);
  * Common rules: D in {32, 64, 128, 256}; Hq a multiple of Hkv, Hq / Hkv <= 64;
  * f32 or bf16 rows of D contiguous values; every pointer 16-byte aligned and
  * every stride a multiple of 16 bytes.  Sums, softmax statistics and norms are
- * f32; results are rounded once, where they are stored.
+ * f32; results are rounded once, where they are stored.  One more rounding is in
+ * the tensor-core form of the attention (bf16, D >= 64, packed keys or pages of a
+ * multiple of 16 rows): each weight is rounded to bf16, 2^-8 relative at most, for
+ * its product with v; the sum of the weights is taken before that.
+ * A row whose tiled sums are not finite (an infinite or NaN value or score among
+ * its keys, or among the masked ones of the last tile) is evaluated again key by
+ * key, at about 1 us a key and some 2400 rows at a time: right, however long the
+ * context, but slow (2048 tokens of 32 heads over 32768 keys: 1.5 s).
  * What only the device can see is checked there: cu_seqlens that decrease or
  * do not span the T tokens, kv_lens outside [0, max_pages * page_size], pages
  * outside [0, num_pages), positions outside the rotary table.  Nothing is then
  * read or written out of bounds (a bad page reads as zeros and is not written;
- * a sequence with bad offsets is skipped) and gdn_read_device_status() returns
- * GDN_ERR_DEVICE_CHECK.  Host mirrors, where given, are checked before launch.
+ * a sequence with bad offsets is skipped, and what others overlap it is
+ * unspecified) and gdn_read_device_status() returns GDN_ERR_DEVICE_CHECK.
+ * Host mirrors, where given, are checked before launch.
  * ------------------------------------------------------------------------- */
 
 /* A [tokens, heads, D] tensor with its strides in elements (0: contiguous). */
