@@ -183,6 +183,19 @@ class gdn_attn_paged_args(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class gdn_attn_cache8(ctypes.Structure):
+    _fields_ = [("codes", gdn_attn_cache), ("k_scale", _vp), ("k_scale_len", _i64),
+                ("v_scale", _vp), ("v_scale_len", _i64), ("block", _i64)]
+
+
+class gdn_attn8_prepare_args(ctypes.Structure):
+    _fields_ = [("base", gdn_attn_prepare_args), ("cache", ctypes.POINTER(gdn_attn_cache8))]
+
+
+class gdn_attn8_paged_args(ctypes.Structure):
+    _fields_ = [("base", gdn_attn_paged_args), ("cache", ctypes.POINTER(gdn_attn_cache8))]
+
+
 EXPORTED = ("gdn_prepare", "gdn_decode", "gdn_prefill_varlen", "gdn_kda_varlen",
             "gdn_spec_prepare", "gdn_spec_decode", "gdn_packed_decode", "gdn_gated_rmsnorm",
             "gdn_prefill_workspace_bytes",
@@ -190,7 +203,8 @@ EXPORTED = ("gdn_prepare", "gdn_decode", "gdn_prefill_varlen", "gdn_kda_varlen",
             "gdn_status_string", "gdn_last_error_message",
             "gdn_read_device_status", "gdn_version", "gdn_launch_count", "gdn_validate_mixed",
             "gdn_check_wait_timeout", "gdn_attn_prepare", "gdn_attn_varlen", "gdn_attn_paged",
-            "gdn_attn_paged_workspace_bytes")
+            "gdn_attn_paged_workspace_bytes", "gdn_attn8_prepare", "gdn_attn8_paged",
+            "gdn_attn8_paged_workspace_bytes")
 
 
 class GdnError(RuntimeError):
@@ -235,11 +249,14 @@ def lib() -> ctypes.CDLL:
             L.gdn_kda_resolve_algo.argtypes = [_i64, _i64, _i64, _i64, _i32, _i32]
             L.gdn_kda_workspace_bytes.restype = ctypes.c_size_t
             L.gdn_kda_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i64, _i32, _i32]
-            for name in ("gdn_attn_prepare", "gdn_attn_varlen", "gdn_attn_paged"):
+            for name in ("gdn_attn_prepare", "gdn_attn_varlen", "gdn_attn_paged",
+                         "gdn_attn8_prepare", "gdn_attn8_paged"):
                 getattr(L, name).restype = ctypes.c_int
                 getattr(L, name).argtypes = [_vp, _vp]  # an address of, or a reference to, args
             L.gdn_attn_paged_workspace_bytes.restype = ctypes.c_size_t
             L.gdn_attn_paged_workspace_bytes.argtypes = [_i64] * 6 + [_i32]
+            L.gdn_attn8_paged_workspace_bytes.restype = ctypes.c_size_t
+            L.gdn_attn8_paged_workspace_bytes.argtypes = [_i64] * 6 + [_i32] + [_i64] * 2
             L.gdn_status_string.restype = ctypes.c_char_p
             L.gdn_status_string.argtypes = [ctypes.c_int]
             L.gdn_last_error_message.restype = ctypes.c_char_p
@@ -551,7 +568,11 @@ _PREPARE = _packer(gdn_attn_prepare_args)
 _VARLEN = _packer(gdn_attn_varlen_args)
 _PAGED = _packer(gdn_attn_paged_args)
 _CACHE = _packer(gdn_attn_cache)
+_PREPARE8 = _packer(gdn_attn8_prepare_args)
+_PAGED8 = _packer(gdn_attn8_paged_args)
+_CACHE8 = _packer(gdn_attn_cache8)
 _NO_ROWS = (0, 0, 0, 0)
+_E4M3 = torch.float8_e4m3fn
 
 
 class _Args(threading.local):
@@ -629,10 +650,11 @@ def _attn_i32(name, t, n, dev):
     return t.data_ptr()
 
 
-def _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dtype, dev, block_table_host):
+def _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dtype, dev, block_table_host, scales=None):
     """Packs the gdn_attn_cache of k_cache, v_cache [pages, Hkv, page_size, D]
     (any strides but the last) and block_table [N, max_pages] int32 into the
-    thread's buffer; returns its address and the host mirror to keep."""
+    thread's buffer, as a gdn_attn_cache8 with the scales (k_scale, v_scale) of
+    one in 8 bits; returns its address and the host mirror to keep."""
     shape = k_cache.shape
     P, _, page, _ = shape if len(shape) == 4 else (0, 0, 0, 0)
     shape = (P, Hkv, page, D)
@@ -667,8 +689,18 @@ def _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dtype, dev, block_tabl
             wide = torch.zeros((N, row), dtype=torch.int32)
             wide[:, :width] = host
             host, host_p = wide, wide.data_ptr()
-    _CACHE.pack_into(_args.cache, 0, *parts, P, page, block_table.data_ptr(), width, row,
-                     host_p or 0)
+    if scales is None:
+        _CACHE.pack_into(_args.cache, 0, *parts, P, page, block_table.data_ptr(), width, row,
+                         host_p or 0)
+        return _args.cache_at, host
+    blocks = scales[0].shape[-1] if scales[0].dim() == 3 else 0
+    if blocks == 0 or page % blocks != 0:
+        raise _bad_shape(f"attention k_scale has shape {tuple(scales[0].shape)}, not [{P}, {Hkv}, "
+                         f"blocks of a page of {page} rows]")
+    shape = (P, Hkv, blocks)
+    _CACHE8.pack_into(_args.cache, 0, *parts, P, page, block_table.data_ptr(), width, row,
+                      host_p or 0, *_attn_flat("k_scale", scales[0], shape, torch.float32, dev),
+                      *_attn_flat("v_scale", scales[1], shape, torch.float32, dev), page // blocks)
     return _args.cache_at, host
 
 
@@ -698,7 +730,44 @@ def _attn_call(fn, q, stream) -> None:
         s = _raw_stream(q.device.index)
     else:
         s = torch.cuda.current_stream(q.device).cuda_stream
-    _check(fn(_args.at, s))
+    if q.device.index != torch.cuda.current_device():  # the library launches on the current device
+        with torch.cuda.device(q.device):
+            _check(fn(_args.at, s))
+    else:
+        _check(fn(_args.at, s))
+
+
+def _attn_prepare(packer, fn, q, k, v, cu_seqlens, q_out, kv_lens, block_table, k_cache, v_cache,
+                  scales, k_out, q_norm_weight, k_norm_weight, norm_eps, cos_sin, positions,
+                  cu_seqlens_host, kv_lens_host, block_table_host, stream):
+    """The prepare calls; scales: of a cache in 8 bits, whose address then ends the arguments."""
+    T, N, Hq, Hkv, D = _attn_dims(q, k, cu_seqlens)
+    dt, dev = q.dtype, q.device
+    keep_cu, cu_host = _attn_mirror("cu_seqlens_host", cu_seqlens_host, N + 1)
+    keep_kv, kv_host = _attn_mirror("kv_lens_host", kv_lens_host, N)
+    keep_table, cache = None, 0
+    if k_cache is not None or v_cache is not None or block_table is not None:
+        if k_cache is None or v_cache is None or block_table is None:
+            raise _bad("attention cache needs k_cache, v_cache and block_table")
+        cache, keep_table = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D,
+                                        dt if scales is None else _E4M3, dev, block_table_host,
+                                        scales)
+    rot, cs = 0, (0, 0)
+    if cos_sin is not None:
+        rot = cos_sin.shape[-1]
+        cs = _attn_flat("cos_sin", cos_sin, (cos_sin.shape[0], rot), torch.float32, dev)
+    packer.pack_into(
+        _args.buf, 0, T, N, Hq, Hkv, D, rot, _dt(q), norm_eps,
+        *_attn_rows("query", q, (T, Hq, D), dt, dev), *_attn_rows("key", k, (T, Hkv, D), dt, dev),
+        *_attn_rows("value", v, (T, Hkv, D), dt, dev),
+        *_attn_flat("q_norm_weight", q_norm_weight, (D,), dt, dev),
+        *_attn_flat("k_norm_weight", k_norm_weight, (D,), dt, dev), *cs,
+        _attn_i32("positions", positions, T, dev),
+        _attn_i32("cu_seqlens", cu_seqlens, N + 1, dev),
+        _attn_i32("kv_lens", kv_lens, N, dev), cu_host, kv_host, cache if scales is None else 0,
+        *_attn_flat("q_out", q_out, (T, Hq, D), dt, dev),
+        *_attn_flat("k_out", k_out, (T, Hkv, D), dt, dev), *(() if scales is None else (cache,)))
+    _attn_call(fn, q, stream)
 
 
 def gdn_attn_prepare(q, k, v, cu_seqlens, q_out, *, kv_lens=None, block_table=None, k_cache=None,
@@ -709,32 +778,26 @@ def gdn_attn_prepare(q, k, v, cu_seqlens, q_out, *, kv_lens=None, block_table=No
     the projection rows; q_out [T, Hq, D] and k_out [T, Hkv, D] are written, and
     the new rows of k_cache, v_cache [pages, Hkv, page_size, D] in place.
     cos_sin [positions, rot_dim] f32; cu_seqlens None: one token per sequence."""
-    T, N, Hq, Hkv, D = _attn_dims(q, k, cu_seqlens)
-    dt, dev = q.dtype, q.device
-    keep_cu, cu_host = _attn_mirror("cu_seqlens_host", cu_seqlens_host, N + 1)
-    keep_kv, kv_host = _attn_mirror("kv_lens_host", kv_lens_host, N)
-    keep_table, cache = None, 0
-    if k_cache is not None or v_cache is not None or block_table is not None:
-        if k_cache is None or v_cache is None or block_table is None:
-            raise _bad("attention cache needs k_cache, v_cache and block_table")
-        cache, keep_table = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dt, dev,
-                                        block_table_host)
-    rot, cs = 0, (0, 0)
-    if cos_sin is not None:
-        rot = cos_sin.shape[-1]
-        cs = _attn_flat("cos_sin", cos_sin, (cos_sin.shape[0], rot), torch.float32, dev)
-    _PREPARE.pack_into(
-        _args.buf, 0, T, N, Hq, Hkv, D, rot, _dt(q), norm_eps,
-        *_attn_rows("query", q, (T, Hq, D), dt, dev), *_attn_rows("key", k, (T, Hkv, D), dt, dev),
-        *_attn_rows("value", v, (T, Hkv, D), dt, dev),
-        *_attn_flat("q_norm_weight", q_norm_weight, (D,), dt, dev),
-        *_attn_flat("k_norm_weight", k_norm_weight, (D,), dt, dev), *cs,
-        _attn_i32("positions", positions, T, dev),
-        _attn_i32("cu_seqlens", cu_seqlens, N + 1, dev),
-        _attn_i32("kv_lens", kv_lens, N, dev), cu_host, kv_host, cache,
-        *_attn_flat("q_out", q_out, (T, Hq, D), dt, dev),
-        *_attn_flat("k_out", k_out, (T, Hkv, D), dt, dev))
-    _attn_call((_lib or lib()).gdn_attn_prepare, q, stream)
+    _attn_prepare(_PREPARE, (_lib or lib()).gdn_attn_prepare, q, k, v, cu_seqlens, q_out, kv_lens,
+                  block_table, k_cache, v_cache, None, k_out, q_norm_weight, k_norm_weight, norm_eps,
+                  cos_sin, positions, cu_seqlens_host, kv_lens_host, block_table_host, stream)
+
+
+def gdn_attn8_prepare(q, k, v, cu_seqlens, q_out, *, kv_lens=None, block_table, k_cache, v_cache,
+                      k_scale, v_scale, k_out=None, q_norm_weight=None, k_norm_weight=None,
+                      norm_eps=1e-6, cos_sin=None, positions=None, cu_seqlens_host=None,
+                      kv_lens_host=None, block_table_host=None, stream=None) -> None:
+    """include/gdn.h gdn_attn8_prepare: gdn_attn_prepare into a cache in 8 bits.
+    k_cache, v_cache [pages, Hkv, page_size, D] float8_e4m3fn; k_scale, v_scale
+    [pages, Hkv, page_size / block] f32."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table),
+                    ("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is None:
+            raise _bad(f"{name} is NULL")
+    _attn_prepare(_PREPARE8, (_lib or lib()).gdn_attn8_prepare, q, k, v, cu_seqlens, q_out, kv_lens,
+                  block_table, k_cache, v_cache, (k_scale, v_scale), k_out, q_norm_weight,
+                  k_norm_weight, norm_eps, cos_sin, positions, cu_seqlens_host, kv_lens_host,
+                  block_table_host, stream)
 
 
 def gdn_attn_varlen(q, k, v, cu_seqlens, out, *, scale=-1.0, gate=None, lse=None,
@@ -760,6 +823,44 @@ def gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len=0,
     return int(lib().gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len, act_dtype))
 
 
+def _attn_paged(packer, fn, q, k_cache, v_cache, scales, block_table, kv_lens, cu_seqlens, out,
+                max_q_len, scale, gate, lse, workspace, cu_seqlens_host, kv_lens_host,
+                block_table_host, stream):
+    """The paged calls; scales: of a cache in 8 bits, whose address then ends the arguments."""
+    if k_cache.dim() != 4:
+        raise _bad_shape("attention k_cache must be [pages, Hkv, page_size, D]")
+    T, N, Hq, Hkv, D = _attn_dims(q, k_cache, cu_seqlens)
+    if kv_lens is None:
+        raise _bad("kv_lens is NULL")
+    dt, dev = q.dtype, q.device
+    keep_cu, cu_host = _attn_mirror("cu_seqlens_host", cu_seqlens_host, N + 1)
+    keep_kv, kv_host = _attn_mirror("kv_lens_host", kv_lens_host, N)
+    cache, keep_table = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D,
+                                    dt if scales is None else _E4M3, dev, block_table_host, scales)
+    if workspace is None:
+        # Without offsets a call has one token per sequence, whatever max_q_len says.
+        most = max_q_len if cu_seqlens is not None or scales is None else 1
+        nbytes = (gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, most, _dt(q)) if scales is None else
+                  gdn_attn8_paged_workspace_bytes(T, N, Hq, Hkv, D, most, _dt(q),
+                                                  block_table.shape[1], k_cache.shape[2]))
+        if nbytes:
+            workspace = _scratch(nbytes, dev, stream)
+    elif workspace.device != dev:
+        raise _bad(f"attention workspace is on {workspace.device}, not {dev}")
+    ws = (0, 0) if workspace is None else (workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size())
+    packer.pack_into(
+        _args.buf, 0, T, N, Hq, Hkv, D, max_q_len, _dt(q), scale,
+        *_attn_rows("query", q, (T, Hq, D), dt, dev), *_attn_rows("gate", gate, (T, Hq, D), dt, dev),
+        _attn_i32("cu_seqlens", cu_seqlens, N + 1, dev),
+        _attn_i32("kv_lens", kv_lens, N, dev), cu_host, kv_host,
+        cache if scales is None else 0,
+        *_attn_flat("out", out, (T, Hq, D), dt, dev),
+        *_attn_flat("lse", lse, (T, Hq), torch.float32, dev), *ws,
+        *(() if scales is None else (cache,)))
+    _attn_call(fn, q, stream)
+
+
 def gdn_attn_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, *, max_q_len=0,
                    scale=-1.0, gate=None, lse=None, workspace=None, cu_seqlens_host=None,
                    kv_lens_host=None, block_table_host=None, stream=None) -> None:
@@ -769,32 +870,28 @@ def gdn_attn_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, *
     lse [T, Hq] f32 are written.  `workspace`: a uint8 device tensor of at least
     gdn_attn_paged_workspace_bytes() bytes; when None and one is needed, it is
     allocated here for the call."""
-    if k_cache.dim() != 4:
-        raise _bad_shape("attention k_cache must be [pages, Hkv, page_size, D]")
-    T, N, Hq, Hkv, D = _attn_dims(q, k_cache, cu_seqlens)
-    if kv_lens is None:
-        raise _bad("kv_lens is NULL")
-    dt, dev = q.dtype, q.device
-    keep_cu, cu_host = _attn_mirror("cu_seqlens_host", cu_seqlens_host, N + 1)
-    keep_kv, kv_host = _attn_mirror("kv_lens_host", kv_lens_host, N)
-    cache, keep_table = _attn_cache(k_cache, v_cache, block_table, N, Hkv, D, dt, dev,
-                                    block_table_host)
-    if workspace is None:
-        nbytes = gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len, _dt(q))
-        if nbytes:
-            workspace = _scratch(nbytes, dev, stream)
-    elif workspace.device != dev:
-        raise _bad(f"attention workspace is on {workspace.device}, not {dev}")
-    ws = (0, 0) if workspace is None else (workspace.data_ptr(),
-                                           workspace.numel() * workspace.element_size())
-    _PAGED.pack_into(
-        _args.buf, 0, T, N, Hq, Hkv, D, max_q_len, _dt(q), scale,
-        *_attn_rows("query", q, (T, Hq, D), dt, dev), *_attn_rows("gate", gate, (T, Hq, D), dt, dev),
-        _attn_i32("cu_seqlens", cu_seqlens, N + 1, dev),
-        _attn_i32("kv_lens", kv_lens, N, dev), cu_host, kv_host, cache,
-        *_attn_flat("out", out, (T, Hq, D), dt, dev),
-        *_attn_flat("lse", lse, (T, Hq), torch.float32, dev), *ws)
-    _attn_call((_lib or lib()).gdn_attn_paged, q, stream)
+    _attn_paged(_PAGED, (_lib or lib()).gdn_attn_paged, q, k_cache, v_cache, None, block_table,
+                kv_lens, cu_seqlens, out, max_q_len, scale, gate, lse, workspace, cu_seqlens_host,
+                kv_lens_host, block_table_host, stream)
+
+
+def gdn_attn8_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len=0, act_dtype=GDN_DTYPE_BF16,
+                                    max_pages=1, page_size=128) -> int:
+    """max_pages, page_size: of the block table and cache that the call will have."""
+    return int(lib().gdn_attn8_paged_workspace_bytes(T, N, Hq, Hkv, D, max_q_len, act_dtype,
+                                                     max_pages, page_size))
+
+
+def gdn_attn8_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, out, *,
+                    max_q_len=0, scale=-1.0, gate=None, lse=None, workspace=None,
+                    cu_seqlens_host=None, kv_lens_host=None, block_table_host=None,
+                    stream=None) -> None:
+    """include/gdn.h gdn_attn8_paged: gdn_attn_paged over a cache in 8 bits.  k_cache,
+    v_cache [pages, Hkv, page_size, D] float8_e4m3fn; k_scale, v_scale [pages, Hkv,
+    page_size / block] f32."""
+    _attn_paged(_PAGED8, (_lib or lib()).gdn_attn8_paged, q, k_cache, v_cache, (k_scale, v_scale),
+                block_table, kv_lens, cu_seqlens, out, max_q_len, scale, gate, lse, workspace,
+                cu_seqlens_host, kv_lens_host, block_table_host, stream)
 
 
 def _host_u8(t: Optional[torch.Tensor]):

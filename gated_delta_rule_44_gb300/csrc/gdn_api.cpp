@@ -1078,7 +1078,7 @@ struct AttnCacheView {
 };
 
 int check_attn_pages(const char* label, void* p, int64_t len, int64_t ps, int64_t hs, int64_t ts,
-                     const gdn_attn_cache& c, int64_t Hkv, int64_t D, int32_t dt,
+                     const gdn_attn_cache& c, int64_t Hkv, int64_t D, int64_t es,
                      gdn::AttnPages* out) {
   if (ts == 0) ts = D;
   if (hs == 0) hs = c.page_size * D;
@@ -1092,7 +1092,6 @@ int check_attn_pages(const char* label, void* p, int64_t len, int64_t ps, int64_
   if (int rc = check_lengths("attention", rules)) return rc;
   if (int rc = require_ptr(p, label)) return rc;
   if (int rc = require_aligned(p, label)) return rc;
-  const int64_t es = elem_size(dt);
   if ((ts * es) % 16 != 0 || (hs * es) % 16 != 0 || (ps * es) % 16 != 0)
     return fail(GDN_ERR_INVALID_ARGUMENT,
                 std::string("attention ") + label + " strides must be multiples of 16 bytes");
@@ -1100,7 +1099,8 @@ int check_attn_pages(const char* label, void* p, int64_t len, int64_t ps, int64_
   return GDN_OK;
 }
 
-int check_attn_cache(const gdn_attn_cache* c, int64_t N, int64_t Hkv, int64_t D, int32_t dt,
+// es: bytes of a cache element.
+int check_attn_cache(const gdn_attn_cache* c, int64_t N, int64_t Hkv, int64_t D, int64_t es,
                      AttnCacheView* out) {
   if (c->num_pages <= 0 || c->page_size <= 0 || c->max_pages <= 0)
     return fail(GDN_ERR_SHAPE, "attention cache shape must be positive, got num_pages=" +
@@ -1113,10 +1113,10 @@ int check_attn_cache(const gdn_attn_cache* c, int64_t N, int64_t Hkv, int64_t D,
     return fail(GDN_ERR_SHAPE, "attention block_table stride shorter than the row or out of range");
   if (int rc = require_ptr(c->block_table, "block_table")) return rc;
   if (int rc = check_attn_pages("k_cache", c->k, c->k_len, c->k_page_stride, c->k_head_stride,
-                                c->k_token_stride, *c, Hkv, D, dt, &out->k))
+                                c->k_token_stride, *c, Hkv, D, es, &out->k))
     return rc;
   return check_attn_pages("v_cache", c->v, c->v_len, c->v_page_stride, c->v_head_stride,
-                          c->v_token_stride, *c, Hkv, D, dt, &out->v);
+                          c->v_token_stride, *c, Hkv, D, es, &out->v);
 }
 
 // Host copies of the metadata (mirrors, or device copies under
@@ -1195,8 +1195,32 @@ int one_token_each(const int32_t* cu, int64_t T, int64_t N) {
   return GDN_OK;
 }
 
-int attn_prepare(const gdn_attn_prepare_args* a, void* stream) {
-  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+// What a cache in 8 bits has beside its codes (whose view is v): scales, smaller strides.
+int check_attn_scales(const gdn_attn_cache8& c, const AttnCacheView& v, int64_t Hkv) {
+  const int64_t B = c.block, page = c.codes.page_size;
+  if (B != 16 && B != 32 && B != 64 && B != 128)
+    return fail(GDN_ERR_UNSUPPORTED, "attention scale blocks have 16, 32, 64 or 128 rows, got " + S(B));
+  if (page % B != 0)
+    return fail(GDN_ERR_SHAPE, "attention page_size " + S(page) + " must be a multiple of the scale block " + S(B));
+  const int64_t n = c.codes.num_pages * Hkv * (page / B);
+  const LenRule rules[] = {{"k_scale", c.k_scale_len, n}, {"v_scale", c.v_scale_len, n}};
+  if (int rc = check_lengths("attention", rules)) return rc;
+  for (auto pr : {std::make_pair((const void*)c.k_scale, "k_scale"),
+                  std::make_pair((const void*)c.v_scale, "v_scale")}) {
+    if (int rc = require_ptr(pr.first, pr.second)) return rc;
+    if (int rc = require_aligned(pr.first, pr.second)) return rc;
+  }
+  for (const gdn::AttnPages* t : {&v.k, &v.v})
+    if (std::max({t->ps, t->hs, t->ts}) >= (int64_t)1 << 40)
+      return fail(GDN_ERR_UNSUPPORTED, "attention cache strides must be below 2^40 bytes");
+  return GDN_OK;
+}
+
+// The checks of the prepare calls; fills p.  The cache is c8's where that is not NULL.
+int attn_prepare_checks(const gdn_attn_prepare_args* a, const gdn_attn_cache8* c8, cudaStream_t st,
+                        gdn::AttnPrepareLaunch& p) {
+  const gdn_attn_cache* cache = c8 != nullptr ? &c8->codes : a->cache;
+  const int64_t es = c8 != nullptr ? 1 : elem_size(a->act_dtype);
   if (int rc = check_act_dtype(a->act_dtype)) return rc;
   if (int rc = check_attn_dims(a->T, a->N, a->Hq, a->Hkv, a->D)) return rc;
   if (int rc = one_token_each(a->cu_seqlens, a->T, a->N)) return rc;
@@ -1205,15 +1229,20 @@ int attn_prepare(const gdn_attn_prepare_args* a, void* stream) {
     return fail(GDN_ERR_INVALID_ARGUMENT,
                 "attention rot_dim must be 0 or a multiple of 16 up to D, got " + S(R));
   if (!(a->norm_eps >= 0.0f)) return fail(GDN_ERR_INVALID_ARGUMENT, "attention norm_eps must be >= 0");
-  gdn::AttnPrepareLaunch p{};
   if (int rc = check_attn_rows(a->q, "query", a->T, a->Hq, a->D, a->act_dtype, &p.q)) return rc;
   if (int rc = check_attn_rows(a->k, "key", a->T, a->Hkv, a->D, a->act_dtype, &p.k)) return rc;
-  if (a->cache == nullptr && a->k_out == nullptr)
+  if (cache == nullptr && a->k_out == nullptr)
     return fail(GDN_ERR_INVALID_ARGUMENT, "attention prepare needs a cache or k_out");
   AttnCacheView cv{};
-  if (a->cache != nullptr) {
+  if (cache != nullptr) {
     if (int rc = check_attn_rows(a->v, "value", a->T, a->Hkv, a->D, a->act_dtype, &p.v)) return rc;
-    if (int rc = check_attn_cache(a->cache, a->N, a->Hkv, a->D, a->act_dtype, &cv)) return rc;
+    if (int rc = check_attn_cache(cache, a->N, a->Hkv, a->D, es, &cv)) return rc;
+    if (c8 != nullptr) {
+      if (int rc = check_attn_scales(*c8, cv, a->Hkv)) return rc;
+      p.ks = c8->k_scale;
+      p.vs = c8->v_scale;
+      p.block = (int)c8->block;
+    }
   }
   const LenRule rules[] = {
       {"query output", a->q_out_len, a->T * a->Hq * a->D},
@@ -1232,9 +1261,8 @@ int attn_prepare(const gdn_attn_prepare_args* a, void* stream) {
                   std::make_pair(a->k_norm_weight, "k_norm_weight"),
                   std::make_pair((const void*)a->cos_sin, "cos_sin")})
     if (int rc = require_aligned(pr.first, pr.second)) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (int rc = check_attn_meta("attention_prepare", a->T, a->N, a->T, a->cu_seqlens,
-                               a->cu_seqlens_host, a->kv_lens, a->kv_lens_host, a->cache,
+                               a->cu_seqlens_host, a->kv_lens, a->kv_lens_host, cache,
                                cv.table_stride, st))
     return rc;
   p.T = (int)a->T;
@@ -1252,12 +1280,12 @@ int attn_prepare(const gdn_attn_prepare_args* a, void* stream) {
   p.positions = a->positions;
   p.cu = a->cu_seqlens;
   p.kv_lens = a->kv_lens;
-  if (a->cache != nullptr) {
-    p.table = a->cache->block_table;
+  if (cache != nullptr) {
+    p.table = cache->block_table;
     p.table_stride = cv.table_stride;
-    p.max_pages = (int)a->cache->max_pages;
-    p.page_size = (int)a->cache->page_size;
-    p.num_pages = a->cache->num_pages;
+    p.max_pages = (int)cache->max_pages;
+    p.page_size = (int)cache->page_size;
+    p.num_pages = cache->num_pages;
     p.kc = cv.k;
     p.vc = cv.v;
   }
@@ -1265,8 +1293,28 @@ int attn_prepare(const gdn_attn_prepare_args* a, void* stream) {
   p.k_out = a->k_out;
   p.status = gdn::status_word();
   if (p.status == nullptr) return fail(GDN_ERR_CUDA, "device status word unavailable");
+  return GDN_OK;
+}
+
+int attn_prepare(const gdn_attn_prepare_args* a, void* stream) {
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+  gdn::AttnPrepareLaunch p{};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (int rc = attn_prepare_checks(a, nullptr, st, p)) return rc;
   return launch_result(gdn::launch_attn_prepare(p, st), "gdn_attn_prepare");
 }
+
+int attn8_prepare(const gdn_attn8_prepare_args* a, void* stream) {
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+  if (int rc = require_ptr(a->cache, "cache")) return rc;
+  if (a->base.cache != nullptr)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_attn8_prepare takes its cache in `cache`, not in base.cache");
+  gdn::AttnPrepareLaunch p{};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (int rc = attn_prepare_checks(&a->base, a->cache, st, p)) return rc;
+  return launch_result(gdn::launch_attn8_prepare(p, st), "gdn_attn8_prepare");
+}
+
 
 int attn_varlen(const gdn_attn_varlen_args* a, void* stream) {
   if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
@@ -1318,34 +1366,43 @@ size_t attn_paged_workspace(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64
   return T == N ? std::max(n, paged_need(T, N, Hq, Hkv, D, 1, act_dtype)) : n;
 }
 
-int attn_paged(const gdn_attn_paged_args* a, void* stream) {
-  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+// The checks of the paged calls; fills p.  The cache is c8's where that is not NULL;
+// need_of(max_q): the workspace bytes of the call.
+template <typename Need>
+int attn_paged_checks(const gdn_attn_paged_args* a, const gdn_attn_cache8* c8, const char* what,
+                      Need need_of, cudaStream_t st, gdn::AttnLaunch& p) {
+  const gdn_attn_cache* cache = c8 != nullptr ? &c8->codes : a->cache;
+  const int64_t es = c8 != nullptr ? 1 : elem_size(a->act_dtype);
   if (int rc = check_act_dtype(a->act_dtype)) return rc;
   if (int rc = check_attn_dims(a->T, a->N, a->Hq, a->Hkv, a->D)) return rc;
   if (int rc = one_token_each(a->cu_seqlens, a->T, a->N)) return rc;
   if (a->max_q_len < 0)
     return fail(GDN_ERR_INVALID_ARGUMENT, "attention max_q_len must be >= 0, got " + S(a->max_q_len));
   const int64_t max_q = a->cu_seqlens == nullptr ? 1 : resolve_max_q(a->max_q_len, a->T);
-  gdn::AttnLaunch p{};
   if (int rc = check_attn_rows(a->q, "query", a->T, a->Hq, a->D, a->act_dtype, &p.q)) return rc;
   if (a->gate.data != nullptr)
     if (int rc = check_attn_rows(a->gate, "gate", a->T, a->Hq, a->D, a->act_dtype, &p.gate)) return rc;
   if (int rc = check_attn_out(a->out, a->out_len, a->lse, a->lse_len, a->T, a->Hq, a->D)) return rc;
   if (int rc = require_ptr(a->kv_lens, "kv_lens")) return rc;
-  if (int rc = require_ptr(a->cache, "cache")) return rc;
+  if (int rc = require_ptr(cache, "cache")) return rc;
   AttnCacheView cv{};
-  if (int rc = check_attn_cache(a->cache, a->N, a->Hkv, a->D, a->act_dtype, &cv)) return rc;
-  const size_t need = paged_need(a->T, a->N, a->Hq, a->Hkv, a->D, max_q, a->act_dtype);
+  if (int rc = check_attn_cache(cache, a->N, a->Hkv, a->D, es, &cv)) return rc;
+  if (c8 != nullptr) {
+    if (int rc = check_attn_scales(*c8, cv, a->Hkv)) return rc;
+    p.ks = c8->k_scale;
+    p.vs = c8->v_scale;
+    p.block = (int)c8->block;
+  }
+  const size_t need = need_of(max_q);
   if (need > 0) {
     if (a->workspace == nullptr || a->workspace_bytes < need)
-      return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_attn_paged workspace needs " + S((int64_t)need) +
+      return fail(GDN_ERR_INVALID_ARGUMENT, std::string(what) + " workspace needs " + S((int64_t)need) +
                                                 " bytes, got " + S((int64_t)a->workspace_bytes));
     if ((reinterpret_cast<uintptr_t>(a->workspace) & 255u) != 0)
       return fail(GDN_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
   }
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (int rc = check_attn_meta("attention_paged", a->T, a->N, max_q, a->cu_seqlens,
-                               a->cu_seqlens_host, a->kv_lens, a->kv_lens_host, a->cache,
+                               a->cu_seqlens_host, a->kv_lens, a->kv_lens_host, cache,
                                cv.table_stride, st))
     return rc;
   p.T = (int)a->T;
@@ -1358,11 +1415,11 @@ int attn_paged(const gdn_attn_paged_args* a, void* stream) {
   p.scale = resolve_scale(a->scale, a->D);
   p.cu = a->cu_seqlens;
   p.kv_lens = a->kv_lens;
-  p.table = a->cache->block_table;
+  p.table = cache->block_table;
   p.table_stride = cv.table_stride;
-  p.max_pages = (int)a->cache->max_pages;
-  p.page_size = (int)a->cache->page_size;
-  p.num_pages = a->cache->num_pages;
+  p.max_pages = (int)cache->max_pages;
+  p.page_size = (int)cache->page_size;
+  p.num_pages = cache->num_pages;
   p.kc = cv.k;
   p.vc = cv.v;
   p.out = a->out;
@@ -1370,8 +1427,72 @@ int attn_paged(const gdn_attn_paged_args* a, void* stream) {
   p.ws = a->workspace;
   p.status = gdn::status_word();
   if (p.status == nullptr) return fail(GDN_ERR_CUDA, "device status word unavailable");
+  return GDN_OK;
+}
+
+int attn_paged(const gdn_attn_paged_args* a, void* stream) {
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+  gdn::AttnLaunch p{};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto need = [&](int64_t max_q) {
+    return paged_need(a->T, a->N, a->Hq, a->Hkv, a->D, max_q, a->act_dtype);
+  };
+  if (int rc = attn_paged_checks(a, nullptr, "gdn_attn_paged", need, st, p))
+    return rc;
   return launch_result(launch_attn(p, st), "gdn_attn_paged");
 }
+
+// Which form serves a cache in 8 bits: by the sizes and the type alone.
+enum class Attn8Form { rows, wide };
+Attn8Form attn8_form(int64_t rows, int64_t D, int32_t act_dtype) {
+  (void)act_dtype;
+  return gdn::attn8_rows_supported(rows, D) ? Attn8Form::rows : Attn8Form::wide;
+}
+
+size_t paged8_need(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q,
+                   int32_t act_dtype, int64_t max_pages, int64_t page_size) {
+  if (attn8_form(max_q * (Hq / Hkv), D, act_dtype) == Attn8Form::rows)
+    return gdn::attn_simt_workspace_bytes(T, N, Hq, Hkv, D, max_q);
+  return gdn::attn8_wide_workspace_bytes(T, N, Hq, Hkv, D, max_q, act_dtype == GDN_DTYPE_BF16,
+                                         max_pages, page_size);
+}
+
+bool attn8_cache_dims(int64_t max_pages, int64_t page_size) {
+  return max_pages > 0 && page_size > 0 && page_size <= (1 << 20) && max_pages <= INT32_MAX / page_size;
+}
+
+size_t attn8_paged_workspace(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q_len,
+                             int32_t act_dtype, int64_t max_pages, int64_t page_size) {
+  if (check_act_dtype(act_dtype) || check_attn_dims(T, N, Hq, Hkv, D) || max_q_len < 0 ||
+      !attn8_cache_dims(max_pages, page_size))
+    return 0;
+  // As many tokens as sequences may mean one token each, without cu_seqlens.
+  const int64_t mq = resolve_max_q(max_q_len, T);
+  const size_t n = paged8_need(T, N, Hq, Hkv, D, mq, act_dtype, max_pages, page_size);
+  return T == N ? std::max(n, paged8_need(T, N, Hq, Hkv, D, 1, act_dtype, max_pages, page_size)) : n;
+}
+
+int attn8_paged(const gdn_attn8_paged_args* a, void* stream) {
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+  if (int rc = require_ptr(a->cache, "cache")) return rc;
+  if (a->base.cache != nullptr)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_attn8_paged takes its cache in `cache`, not in base.cache");
+  gdn::AttnLaunch p{};
+  const gdn_attn_paged_args& b = a->base;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto need = [&](int64_t max_q) {
+    return paged8_need(b.T, b.N, b.Hq, b.Hkv, b.D, max_q, b.act_dtype, a->cache->codes.max_pages,
+                       a->cache->codes.page_size);
+  };
+  if (int rc = attn_paged_checks(&b, a->cache, "gdn_attn8_paged", need, st, p)) return rc;
+  cudaError_t e;
+  switch (attn8_form((int64_t)p.max_q * (p.Hq / p.Hkv), p.D, b.act_dtype)) {
+    case Attn8Form::rows: e = gdn::launch_attn8_rows(p, st); break;
+    default: e = gdn::launch_attn8_wide(p, st);
+  }
+  return launch_result(e, "gdn_attn8_paged");
+}
+
 
 }  // namespace
 
@@ -1387,6 +1508,25 @@ int gdn_attn_varlen(const gdn_attn_varlen_args* a, void* stream) {
 
 int gdn_attn_paged(const gdn_attn_paged_args* a, void* stream) {
   return no_throw([&] { return attn_paged(a, stream); });
+}
+
+int gdn_attn8_prepare(const gdn_attn8_prepare_args* a, void* stream) {
+  return no_throw([&] { return attn8_prepare(a, stream); });
+}
+
+int gdn_attn8_paged(const gdn_attn8_paged_args* a, void* stream) {
+  return no_throw([&] { return attn8_paged(a, stream); });
+}
+
+size_t gdn_attn8_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
+                                       int64_t max_q_len, int32_t act_dtype, int64_t max_pages,
+                                       int64_t page_size) {
+  size_t n = 0;
+  no_throw([&] {
+    n = attn8_paged_workspace(T, N, Hq, Hkv, D, max_q_len, act_dtype, max_pages, page_size);
+    return succeed();
+  });
+  return n;
 }
 
 size_t gdn_attn_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,

@@ -9,8 +9,11 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "gdn_internal.h"
 #include "gdn_math.cuh"
@@ -43,7 +46,8 @@ __device__ inline SeqRange seq_range(const AttnLaunch& p, int s) {
   SeqRange r;
   r.a = cu_at(p.cu, s);
   r.b = cu_at(p.cu, s + 1);
-  r.bad = r.a < 0 || r.b < r.a || r.b > p.T || (s == 0 && r.a != 0) || (s == p.N - 1 && r.b != p.T);
+  r.bad = r.a < 0 || r.b < r.a || r.b > p.T ||
+          (!p.part && ((s == 0 && r.a != 0) || (s == p.N - 1 && r.b != p.T)));
   if (r.a < 0 || r.b < r.a || r.b > p.T) {
     r.a = r.b = r.kv = 0;
     return r;
@@ -115,8 +119,39 @@ __device__ __forceinline__ const void* key_base(const AttnLaunch& p, bool of_v) 
   return p.table == nullptr ? (of_v ? p.v.p : p.k.p) : (of_v ? p.vc.p : p.kc.p);
 }
 
+// ---- caches in 8 bits ----
+// A value is its e4m3 code times the f32 scale of its block of rows and kv head.
+struct E4 {
+  unsigned char code;
+};
+// Two codes (the first in the low byte) as floats, exact; a NaN code gives NaN.
+__device__ __forceinline__ float2 e4x2_to_f(uint32_t codes) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}\n" : "=r"(h) : "r"(codes));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ float to_f(E4 x) { return e4x2_to_f(x.code).x; }
+// (a, b) rounded to the nearest codes, a in the low byte; NaN stays NaN, larger magnitudes
+// than 448 become 448.
+__device__ __forceinline__ uint32_t f_to_e4x2(float a, float b) {
+  unsigned short c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(b), "f"(a));
+  return c;
+}
+// The place of row `row` of page pg in the scales.
+__device__ __forceinline__ int64_t scale_at(int Hkv, int page_size, int block, int64_t pg, int hkv,
+                                            int row) {
+  return (pg * Hkv + hkv) * (page_size / block) + row / block;
+}
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// The scale of key row j of sequence s; 0 for a page outside the cache.
+__device__ __forceinline__ float key_scale(const AttnLaunch& p, bool of_v, int s, int hkv, int j) {
+  const int64_t pg = page_of(p, s, j / p.page_size);
+  if (pg < 0) return 0.0f;
+  return (of_v ? p.vs : p.ks)[scale_at(p.Hkv, p.page_size, p.block, pg, hkv, j % p.page_size)];
+}
 
 __device__ __forceinline__ float sigmoid_gate(float z) { return math::norm_gate(z, true); }
 
@@ -285,8 +320,8 @@ __device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& pa
 // result is not finite is therefore evaluated here, where a masked key is not
 // touched at all, and one that scores -inf adds nothing.  bad pages read as
 // zeros, as in the tiled kernels.  `progress` (may be null) counts on every 2^14
-// keys, for others that wait.
-template <typename T, int D>
+// keys, for others that wait.  C: the cache's type (T, or E4 with scales).
+template <typename T, int D, typename C = T>
 __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int t, int h, int k0,
                                        int k1, float (&acc)[D / 32], float& m, float& l,
                                        int* progress = nullptr) {
@@ -309,13 +344,18 @@ __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int
     const int64_t vo = key_offset(p, true, s, base, hkv, j);
     float dot = 0.0f;
     if (ko >= 0) {
-      const T* kr = static_cast<const T*>(key_base(p, false)) + ko + lane * E;
+      const C* kr = static_cast<const C*>(key_base(p, false)) + ko + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) dot = fmaf(qv[e], to_f(kr[e]), dot);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    const float x = dot * c;
+    float x = dot * c;
+    float vscale = 1.0f;
+    if constexpr (std::is_same<C, E4>::value) {
+      x *= key_scale(p, false, s, hkv, j);
+      vscale = key_scale(p, true, s, hkv, j);
+    }
     if (x != x) {  // no weight of the row is a number
       m = 0.0f;
       l = x;
@@ -327,9 +367,10 @@ __device__ __noinline__ void exact_row(const AttnLaunch& p, int s, int base, int
     const float w = exp2f(x - mn);
     m = mn;
     l = fmaf(l, f, w);
-    const T* vr = static_cast<const T*>(key_base(p, true)) + (vo < 0 ? 0 : vo) + lane * E;
+    const C* vr = static_cast<const C*>(key_base(p, true)) + (vo < 0 ? 0 : vo) + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * (vo < 0 ? 0.0f : to_f(vr[e])));
+    for (int e = 0; e < E; ++e)
+      acc[e] = fmaf(acc[e], f, w * (vo < 0 ? 0.0f : to_f(vr[e]) * vscale));
   }
 }
 

@@ -64,6 +64,14 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
                      __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
 }
 
+// Four codes of an 8-bit cache (without their scale).
+template <>
+__device__ __forceinline__ float4 load4<E4>(const E4* p) {
+  const uint32_t c = *reinterpret_cast<const uint32_t*>(p);
+  const float2 a = e4x2_to_f(c & 0xffffu), b = e4x2_to_f(c >> 16);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
 template <typename T, int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1)
     attn_simt_kernel(const __grid_constant__ AttnLaunch p) {
@@ -289,8 +297,27 @@ __device__ __forceinline__ float butterfly(float (&v)[32], int lane) {
 
 constexpr int kKeys = 8;   // keys of a warp's step
 
-// RB rows at most: RB * kKeys / 32 butterflies per step.
-template <typename T, int D, int RB>
+// Lane `lane`'s E of a row's 32 E values.
+template <typename X, int E>
+__device__ __forceinline__ void load_lane(int lane, const X* x, float (&v)[E]) {
+  if constexpr (E == 1) {
+    v[0] = to_f(x[lane]);
+  } else if constexpr (E % 4 == 0) {
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      const float4 f = load4(x + lane * E + e);
+      v[e] = f.x; v[e + 1] = f.y; v[e + 2] = f.z; v[e + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = to_f(x[lane * E + e]);
+  }
+}
+
+// RB rows at most: RB * kKeys / 32 butterflies per step.  C: the cache's type (T, or E4:
+// the scale of a key's block then joins its scores after the sums over the dims, and its
+// values as they are loaded).
+template <typename T, int D, int RB, typename C = T>
 __global__ void __launch_bounds__(kThreads, RB * D <= 512 ? 2 : 1) attn_rows_kernel(const __grid_constant__ AttnLaunch p,
                                                              int splits) {
   constexpr int E = D / 32, W = kThreads / 32, NB = RB * kKeys / 32;
@@ -312,20 +339,7 @@ __global__ void __launch_bounds__(kThreads, RB * D <= 512 ? 2 : 1) attn_rows_ker
   const int k1 = min(hi, (int)((int64_t)steps * (blockIdx.y + 1) / splits) * kKeys);
   const float c = p.scale * kLog2e;
 
-  auto loadE = [&](const T* x, float (&v)[E]) {
-    if constexpr (E == 1) {
-      v[0] = to_f(x[lane]);
-    } else if constexpr (E % 4 == 0) {
-#pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const float4 f = load4(x + lane * E + e);
-        v[e] = f.x; v[e + 1] = f.y; v[e + 2] = f.z; v[e + 3] = f.w;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = to_f(x[lane * E + e]);
-    }
-  };
+  constexpr bool kScaled = std::is_same<C, E4>::value;
   float q[RB][E], acc[RB][E], m[RB], l[RB];
 #pragma unroll
   for (int r = 0; r < RB; ++r) {
@@ -334,14 +348,19 @@ __global__ void __launch_bounds__(kThreads, RB * D <= 512 ? 2 : 1) attn_rows_ker
 #pragma unroll
     for (int e = 0; e < E; ++e) q[r][e] = acc[r][e] = 0.0f;
     if (r < rows)
-      loadE(static_cast<const T*>(p.q.p) + (int64_t)(tile.t0 + r / G) * p.q.ts +
+      load_lane(lane, static_cast<const T*>(p.q.p) + (int64_t)(tile.t0 + r / G) * p.q.ts +
                 (int64_t)(hkv * G + r % G) * p.q.hs, q[r]);
   }
   // Lane i < kKeys finds key i of a step, one step ahead.
   int64_t next_k = -1, next_v = -1;
+  float next_ks = 0.0f, next_vs = 0.0f;
   auto find = [&](int j) {
     next_k = next_v = -1;
     if (lane < kKeys && j < k1) {
+      if constexpr (kScaled) {
+        next_ks = key_scale(p, false, tile.s, hkv, j);
+        next_vs = key_scale(p, true, tile.s, hkv, j);
+      }
       next_k = key_offset(p, false, tile.s, base, hkv, j);
       next_v = key_offset(p, true, tile.s, base, hkv, j);
       if (next_k < 0) atomicOr(p.status, kStatusBadIndex);
@@ -352,13 +371,22 @@ __global__ void __launch_bounds__(kThreads, RB * D <= 512 ? 2 : 1) attn_rows_ker
   for (int j0 = k0 + warp * kKeys; j0 < k1; j0 += W * kKeys) {
     float k[kKeys][E], v[kKeys][E];
     const int64_t ko = next_k, vo = next_v;
+    const float ks = next_ks, vs = next_vs;
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
       const int64_t a = __shfl_sync(0xffffffffu, ko, i), b = __shfl_sync(0xffffffffu, vo, i);
 #pragma unroll
       for (int e = 0; e < E; ++e) k[i][e] = v[i][e] = 0.0f;
-      if (a >= 0) loadE(static_cast<const T*>(key_base(p, false)) + a, k[i]);
-      if (b >= 0) loadE(static_cast<const T*>(key_base(p, true)) + b, v[i]);
+      if (a >= 0) load_lane(lane, static_cast<const C*>(key_base(p, false)) + a, k[i]);
+      if (b >= 0) load_lane(lane, static_cast<const C*>(key_base(p, true)) + b, v[i]);
+    }
+    if constexpr (kScaled) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) {
+        const float f = __shfl_sync(0xffffffffu, vs, i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[i][e] *= f;
+      }
     }
     find(j0 + W * kKeys + lane);
     // Dot products: value rr * kKeys + i of a butterfly is row rr, key i.
@@ -375,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, RB * D <= 512 ? 2 : 1) attn_rows_ker
         x[z] = d;
       }
       s[n] = butterfly(x, lane);
+      if constexpr (kScaled) s[n] *= __shfl_sync(0xffffffffu, ks, lane % kKeys);
       const int r = n * (32 / kKeys) + lane / kKeys, j = j0 + lane % kKeys;
       s[n] = (j < k1 && j <= tile.pos0 + r / G) ? s[n] * c : -INFINITY;
     }
@@ -428,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, RB * D <= 512 ? 2 : 1) attn_rows_ker
 #pragma unroll
     for (int e = 0; e < E; ++e) finite = finite && isfinite(a[e]);
     if (!__all_sync(0xffffffffu, finite))
-      exact_row<T, D>(p, tile.s, base, t, h, k0, min(k1, tile.pos0 + r / G + 1), a, mm, ll);
+      exact_row<T, D, C>(p, tile.s, base, t, h, k0, min(k1, tile.pos0 + r / G + 1), a, mm, ll);
     if (splits > 1) {
       const Partials part(p.ws, (int64_t)gridDim.x * splits, RB, D);
       part.put<E>(((int64_t)id * p.Hkv + hkv) * splits + blockIdx.y, r, lane, a, mm, ll);
@@ -471,12 +500,12 @@ int row_splits(int64_t ctas, int64_t max_kv) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 256}));
 }
 
-template <typename T, int D, int RB>
+template <typename T, int D, int RB, typename C = T>
 cudaError_t launch_rows(const AttnLaunch& p, cudaStream_t st) {
   const int TT = RB / (p.Hq / p.Hkv);
   const int64_t ctas = tile_bound(p.T, p.N, TT) * p.Hkv;
   const int splits = row_splits(ctas, (int64_t)p.max_pages * p.page_size);
-  attn_rows_kernel<T, D, RB><<<dim3((unsigned)ctas, splits), kThreads, 0, st>>>(p, splits);
+  attn_rows_kernel<T, D, RB, C><<<dim3((unsigned)ctas, splits), kThreads, 0, st>>>(p, splits);
   note_launch();
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
@@ -505,20 +534,25 @@ cudaError_t launch_tiles(const AttnLaunch& p, int64_t items, int ranks, cudaStre
   return e;
 }
 
+// The row kernel for sizes that row_block() takes.
+template <typename T, int D, typename C>
+cudaError_t rows_by_block(const AttnLaunch& p, cudaStream_t st) {
+  switch (row_block((int64_t)p.max_q * (p.Hq / p.Hkv), D)) {
+    case 16:
+      if constexpr (D <= 64) return launch_rows<T, D, 16, C>(p, st);
+      break;
+    case 8:
+      if constexpr (D <= 128) return launch_rows<T, D, 8, C>(p, st);
+      break;
+    case 4: return launch_rows<T, D, 4, C>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
 template <typename T, int D>
 cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
   const int G = p.Hq / p.Hkv, TT = BM / G;
-  if (p.table != nullptr) {
-    switch (row_block((int64_t)p.max_q * G, D)) {
-      case 4: return launch_rows<T, D, 4>(p, st);
-      case 8:
-        if constexpr (D <= 128) return launch_rows<T, D, 8>(p, st);
-        break;
-      case 16:
-        if constexpr (D <= 64) return launch_rows<T, D, 16>(p, st);
-        break;
-    }
-  }
+  if (p.table != nullptr && row_block((int64_t)p.max_q * G, D) != 0) return rows_by_block<T, D, T>(p, st);
   const int64_t items = tile_bound(p.T, p.N, TT) * p.Hkv;
   // A cluster per tile, large enough for two CTAs per SM.  (1024 tokens, 8 heads,
   // D = 128: 187, 122, 103 and 154 us with 1, 2, 4 and 8; the rule takes 4.)
@@ -580,6 +614,26 @@ cudaError_t join_by_dim(const AttnLaunch& p, int splits, int bm, int TT, cudaStr
 cudaError_t launch_attn_join(const AttnLaunch& p, int splits, int bm, int TT, cudaStream_t st) {
   return p.bf16 ? join_by_dim<__nv_bfloat16>(p, splits, bm, TT, st)
                 : join_by_dim<float>(p, splits, bm, TT, st);
+}
+
+bool attn8_rows_supported(int64_t rows, int64_t D) { return row_block(rows, D) != 0; }
+
+namespace {
+
+template <typename T>
+cudaError_t rows8_by_dim(const AttnLaunch& p, cudaStream_t st) {
+  switch (p.D) {
+    case 32: return rows_by_block<T, 32, E4>(p, st);
+    case 64: return rows_by_block<T, 64, E4>(p, st);
+    case 128: return rows_by_block<T, 128, E4>(p, st);
+    default: return rows_by_block<T, 256, E4>(p, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn8_rows(const AttnLaunch& p, cudaStream_t st) {
+  return p.bf16 ? rows8_by_dim<__nv_bfloat16>(p, st) : rows8_by_dim<float>(p, st);
 }
 
 cudaError_t launch_attn_simt(const AttnLaunch& p, cudaStream_t st) {

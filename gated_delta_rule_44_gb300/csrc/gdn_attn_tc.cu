@@ -76,6 +76,7 @@
 #include <algorithm>
 
 #include "gdn_attn_common.cuh"
+#include "gdn_attn_stream.cuh"
 #include "gdn_chunk_common.cuh"
 #include "gdn_internal.h"
 #include "tcgen05.cuh"
@@ -87,20 +88,12 @@ using namespace attn;
 using namespace umma;
 using bf16 = __nv_bfloat16;
 
-constexpr long long kWaitBudget = 2000000000LL;  // ~1 s of SM clock per wait
-constexpr int BK = 128;                          // keys per tile
 constexpr float kRaise = 8.0f;                   // log2 headroom of the reference m
 constexpr int kMaxSplits = 64;
 
 constexpr uint32_t kSmemMax = 232448;  // per CTA
 
 constexpr int kMaxRing = 6;
-
-// A range of key tiles of one (tile, kv head).
-struct Seg {
-  int s, hkv, t0, nt, pos0, hi, kt0, kt1;  // s < 0: no more
-  int64_t slot;  // workspace block of its sums; -1: it has every key of its rows
-};
 
 struct Shared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
@@ -154,132 +147,10 @@ struct TcArgs {
   float* ws;    // the sums
 };
 
-__device__ __forceinline__ int key_tiles(const SeqRange& q) {
-  return q.b > q.a ? (q.kv + BK - 1) / BK : 0;
-}
-
-// The ranges of one CTA of the stream form.
-struct SegIter {
-  int s, hkv, u, cta;
-  int64_t left;
-  __device__ bool next(const AttnLaunch& p, Seg& g) {
-    if (left <= 0) return false;
-    SeqRange q;
-    int n;
-    for (;; ++s) {
-      if (s >= p.N) return false;
-      q = seq_range(p, s);
-      n = key_tiles(q);
-      if (n > 0) break;
-    }
-    const int take = (int)min((int64_t)(n - u), left);
-    g.s = s;
-    g.hkv = hkv;
-    g.t0 = q.a;
-    g.nt = min(q.b - q.a, p.max_q);
-    g.pos0 = q.kv - (q.b - q.a);
-    g.hi = q.kv;
-    g.kt0 = u;
-    g.kt1 = u + take;
-    g.slot = take == n ? -1 : 2 * (int64_t)cta + (u == 0 ? 1 : 0);
-    left -= take;
-    u += take;
-    if (u == n) {
-      u = 0;
-      if (++hkv == p.Hkv) {
-        hkv = 0;
-        ++s;
-      }
-    }
-    return true;
-  }
-};
-
-// A wait that parks the warp until the phase completes or about 20 us have gone
-// by.  Without a time limit of its own a try returns after a short one, and some
-// ten waiting warps' retries then slow every other shared-memory access of the SM
-// (a wait for a completed phase took 200 cycles instead of 30).
-__device__ __forceinline__ bool parked_wait(uint32_t mb, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(mb), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-// The long part of every role's bounded wait; false: leave.  It is kept out of
-// line: the roles' hot loops share the instruction cache.
-__device__ __noinline__ bool long_wait(uint32_t mb, uint32_t parity, Shared* sh, unsigned* status) {
-  long long t0 = clock64();
-  int redone = 0;
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (parked_wait(mb, parity)) return true;
-    if (*(volatile int*)&sh->abort) return false;
-    // Rows evaluated again take about 1 us a key: the time counts from the last sign of
-    // one of them.
-    const int now = *(volatile int*)&sh->redone;
-    if (now != redone) {
-      redone = now;
-      t0 = clock64();
-    }
-    if (clock64() - t0 > kWaitBudget) {
-      *(volatile int*)&sh->abort = 1;
-      atomicOr(status, kStatusTimeout);
-      return false;
-    }
-  }
-}
-// By a whole warp, with one answer for it: near the limit the lanes' own answers may
-// differ, and a warp that some of them leave may not go on with the rest.  (A vote in
-// front of the branch: behind a branch per lane it cost the tile forms 1 %.)
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared* sh,
-                                          unsigned* status) {
-  const uint32_t mb = smem_u32(bar);
-  const bool ok = parked_wait(mb, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  return __all_sync(0xffffffffu, ok || long_wait(mb, parity, sh, status));
-}
-// One lane of a converged warp.  The issuing roles run with all 32 lanes on
-// values the compiler can see are the warp's (from lane 0 by a shuffle), and
-// only the tcgen05 / TMA instruction itself is under this: operands then stay
-// in uniform registers.  Issued by a lone lane of a diverged warp, each MMA
-// cost some 100 cycles of register moves, more than its own 64.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(e));
-  return e != 0;
-}
-template <typename T>
-__device__ __forceinline__ T uni(T x) {
-  return __shfl_sync(0xffffffffu, x, 0);
-}
 // Inside a role: the bounded wait, or leave the role.
 #define WAIT(bar, parity) \
   if (!warp_wait(&(bar), (parity), sh, p.status)) return
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t mbar, int c0,
-                                            int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(mbar)
-      : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -356,50 +227,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   } else if (warp == 2) {
     tmem_alloc(smem_u32(&sh->tmem), 512);
   }
-  if constexpr (STREAM) {
-    // Prefix sum of the key tiles over the sequences, a run of them per thread.
-    const int per = (p.N + C::kThreads - 1) / C::kThreads;
-    const int s0 = min(p.N, tid * per), s1 = min(p.N, s0 + per);
-    long long mine = 0;
-    unsigned bad = 0;
-    for (int s = s0; s < s1; ++s) {
-      const SeqRange q = seq_range(p, s);
-      mine += key_tiles(q);
-      bad |= q.bad;
-    }
-    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) sh->scan[warp] = inc;
-    if (tid == 0) sh->start_s = p.N;
-    __syncthreads();
-    long long before = inc - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < C::kThreads / 32; ++w) {
-      if (w < warp) before += sh->scan[w];
-      total += sh->scan[w];
-    }
-    total *= p.Hkv;
-    const long long w0 = total * blockIdx.x / a.ctas, w1 = total * (blockIdx.x + 1) / a.ctas;
-    if (tid == 0) sh->left = w1 - w0;
-    if (w1 > w0 && before * p.Hkv <= w0 && w0 < (before + mine) * p.Hkv) {
-      long long at = before * p.Hkv;
-      for (int s = s0; s < s1; ++s) {
-        const int n = key_tiles(seq_range(p, s));
-        if (w0 < at + (long long)n * p.Hkv) {
-          sh->start_s = s;
-          sh->start_hkv = (int)((w0 - at) / n);
-          sh->start_u = (int)((w0 - at) % n);
-          break;
-        }
-        at += (long long)n * p.Hkv;
-      }
-    }
-  }
+  if constexpr (STREAM) stream_start<C::kThreads>(p, a.ctas, sh);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -791,18 +619,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       // What the joining kernel needs of this CTA's ranges; the outputs of
       // sequences without a key.
       if (lane == 0) {
-        int4 r = make_int4(-1, 0, 2, 0);
-        SegIter every{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
-        Seg g;
-        for (bool first = true; every.next(p, g); first = false) {
-          const int n = key_tiles(seq_range(p, g.s));
-          if (first) r.z = g.kt1 == n ? 1 : 0;
-          if (g.kt0 == 0 && g.kt1 < n) {
-            r.x = g.s;
-            r.y = g.hkv;
-          }
-        }
-        a.info[blockIdx.x] = r;
+        a.info[blockIdx.x] = stream_info(p, sh);
       }
       for (int s = blockIdx.x; s < p.N; s += a.ctas) {
         const SeqRange q = seq_range(p, s);
@@ -1130,36 +947,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   if (warp == 2) tmem_dealloc(sh->tmem, 512);
 }
 
-// Joins the ranges of the pairs that the stream form cut: CTA c serves the pair
-// that range c began and left open, a row of it per blockIdx.y and its multiples;
-// its further sums are in the blocks of the CTAs after it, in the order of their
-// keys.
 template <int D>
 __global__ void __launch_bounds__(256) attn_stream_join_kernel(const __grid_constant__ AttnLaunch p,
                                                                const __grid_constant__ TcArgs a) {
-  wait_for_previous_kernel();
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
-  const int4 mine = a.info[c0];
-  if (mine.x < 0) return;
-  const int G = p.Hq / p.Hkv;
-  const SeqRange q = seq_range(p, mine.x);
-  const int rows = min(q.b - q.a, p.max_q) * G;
-  if ((int)blockIdx.y >= rows) return;
-  // The last range: the first after c0 that ends the pair.
-  int c1 = c0;
-  for (int c = c0 + 1; c1 == c0 && c < a.ctas; c += 32) {
-    const unsigned ends = __ballot_sync(0xffffffffu, c + lane < a.ctas && a.info[c + lane].z == 1);
-    c1 = ends ? c + __ffs(ends) - 1 : (c + 32 >= a.ctas ? a.ctas - 1 : c0);
-  }
-  const Partials part(a.ws, 2 * (int64_t)a.ctas, a.rows, D);
-  // Block 2 c0 + 1 for the first range, 2 c for the rest; none for a CTA without one.
-  auto slot_of = [&](int z) -> int64_t {
-    return z == 0 ? 2 * (int64_t)c0 + 1 : a.info[c0 + z].z == 2 ? -1 : 2 * (int64_t)(c0 + z);
-  };
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    join_row<bf16, D, 8>(p, part, c1 - c0 + 1, slot_of, r, true, q.a + r / G, mine.y * G + r % G);
-    __syncthreads();
-  }
+  stream_join<bf16, D>(p, a);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -1208,8 +999,6 @@ template <int D>
 constexpr int tiles_of() {
   return D <= 128 ? 2 : 1;
 }
-
-size_t info_bytes(int ctas) { return ((size_t)ctas * sizeof(int4) + 255) & ~(size_t)255; }
 
 template <int D, int NQ, bool PAGED, bool STREAM>
 cudaError_t run(const AttnLaunch& p, TcArgs a, dim3 grid, cudaStream_t st) {

@@ -202,8 +202,13 @@ struct AttnPrepareLaunch {
   void* q_out;  // [T, Hq, D]
   void* k_out;  // [T, Hkv, D] or null
   unsigned* status;
+  // A cache in 8 bits: the scales of its blocks of `block` rows (see AttnLaunch).
+  float* ks;
+  float* vs;
+  int block;
 };
 cudaError_t launch_attn_prepare(const AttnPrepareLaunch& p, cudaStream_t s);
+cudaError_t launch_attn8_prepare(const AttnPrepareLaunch& p, cudaStream_t s);
 
 // Causal attention of packed new tokens over packed keys (table == null: k, v
 // are [T, Hkv, D] rows) or over a paged cache.
@@ -225,6 +230,12 @@ struct AttnLaunch {
   float* lse;     // [T, Hq] or null
   void* ws;
   unsigned* status;
+  bool part;      // the N sequences are some of a call's: their tokens need not span all T
+  // A cache in 8 bits (kc, vc: e4m3 codes, strides in bytes): the scales of its blocks of
+  // `block` rows, [num_pages, Hkv, page_size / block]; null otherwise.
+  const float* ks;
+  const float* vs;
+  int block;
 };
 // CUDA-core form: any supported size (D in {32, 64, 128, 256}, Hq / Hkv <= 64).
 cudaError_t launch_attn_simt(const AttnLaunch& p, cudaStream_t s);
@@ -238,5 +249,15 @@ bool attn_tc_supported(const AttnLaunch& p);
 cudaError_t launch_attn_tc(const AttnLaunch& p, cudaStream_t s);
 size_t attn_tc_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
                                int64_t max_q);
+
+// The same attention over a cache in 8 bits (p.ks, p.vs, p.block).
+// Few rows per kv head on CUDA cores: attn8_rows_supported() sizes.
+bool attn8_rows_supported(int64_t rows, int64_t D);
+cudaError_t launch_attn8_rows(const AttnLaunch& p, cudaStream_t s);
+// Any sizes: the contexts of some sequences at a time are widened into the workspace, and
+// the kernels above run on them.
+cudaError_t launch_attn8_wide(const AttnLaunch& p, cudaStream_t s);
+size_t attn8_wide_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
+                                  int64_t max_q, bool bf16, int64_t max_pages, int64_t page_size);
 
 }  // namespace gdn

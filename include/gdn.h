@@ -795,6 +795,67 @@ int gdn_attn_paged(const gdn_attn_paged_args* args, void* stream);
 size_t gdn_attn_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
                                       int64_t max_q_len, int32_t act_dtype);
 
+/* ---------------------------------------------------------------------------
+ * Full attention over a cache in 8 bits: half the bytes of a bf16 cache, for the same
+ * layer and by the same rules as above.
+ *
+ * A cached value is an e4m3 code (4 exponent, 3 mantissa bits, up to 448; no infinity)
+ * times the f32 scale of its block of `block` rows of a page, per kv head, for keys and
+ * values apart.
+ * ------------------------------------------------------------------------- */
+
+/* codes: k and v hold e4m3 codes, their lengths and strides count codes (bytes), strides
+ * are multiples of 16 and below 2^40.  The scales are contiguous, [num_pages, Hkv,
+ * page_size / block]. */
+typedef struct gdn_attn_cache8 {
+  gdn_attn_cache codes;
+  float* k_scale;
+  int64_t k_scale_len;
+  float* v_scale;
+  int64_t v_scale_len;
+  int64_t block;         /* 16, 32, 64 or 128; page_size a multiple of it */
+} gdn_attn_cache8;
+
+/* gdn_attn8_prepare -- gdn_attn_prepare into a cache in 8 bits.  q_out and k_out are as
+ * there.  For each block that receives rows, kv head, and k or v:
+ *   need = the smallest 2^e, e >= -64, with max |x| <= 448 2^e over the block's finite new
+ *          values (of k after norm and rotary, in f32)
+ *   S = need, when no earlier row of the sequence is in the block; else the larger of need
+ *       and the block's scale
+ *   code = x / S rounded to the nearest code, ties to even; NaN for what is not finite
+ * and where S grew, the codes of the earlier rows are rounded again: c S_old / S.  Rows of
+ * the block behind the new ones are left as they were (and have no meaning under the new
+ * scale).  "Earlier" goes by kv_lens: after a rollback, later rows are simply written
+ * again; a scale never falls while its block holds earlier rows.
+ * A block that receives rows belongs to one sequence: another whose context shares it
+ * would see its earlier rows rounded again (copy the page first: gdn_copy_slots), and two
+ * sequences of one call must not write to the same block. */
+typedef struct gdn_attn8_prepare_args {
+  gdn_attn_prepare_args base;   /* base.cache NULL */
+  const gdn_attn_cache8* cache;
+} gdn_attn8_prepare_args;
+
+int gdn_attn8_prepare(const gdn_attn8_prepare_args* args, void* stream);
+
+/* gdn_attn8_paged -- gdn_attn_paged over a cache in 8 bits, of any finite scales (a key or
+ * value of another one is what code times scale gives).  Statistics and sums are f32.
+ * Roundings beside the last one: with many rows per kv head (max_q_len * Hq / Hkv) and
+ * bf16, the values are widened to bf16 (exact for scales that are powers of two from
+ * 2^-110 on) and then used as in gdn_attn_paged.  The workspace depends on the
+ * table's width then: it holds the widened contexts of some sequences at a time. */
+typedef struct gdn_attn8_paged_args {
+  gdn_attn_paged_args base;     /* base.cache NULL */
+  const gdn_attn_cache8* cache;
+} gdn_attn8_paged_args;
+
+int gdn_attn8_paged(const gdn_attn8_paged_args* args, void* stream);
+
+/* Workspace bytes gdn_attn8_paged needs for these sizes (0 for sizes the call would
+ * refuse). */
+size_t gdn_attn8_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
+                                       int64_t max_q_len, int32_t act_dtype, int64_t max_pages,
+                                       int64_t page_size);
+
 /* Scratch bytes gdn_prefill_varlen needs for these sizes and algorithm (0 for
  * the recurrent algorithm; for the fused one the bytes of its optional
  * workspace).  With GDN_PREFILL_AUTO it depends on
