@@ -196,6 +196,27 @@ class gdn_attn8_paged_args(ctypes.Structure):
     _fields_ = [("base", gdn_attn_paged_args), ("cache", ctypes.POINTER(gdn_attn_cache8))]
 
 
+class gdn_beam_select_args(ctypes.Structure):
+    _fields_ = [("B", _i64), ("W", _i64), ("V", _i64), ("K", _i64), ("dtype", _i32),
+                ("logits", _vp), ("logits_len", _i64), ("batch_stride", _i64),
+                ("beam_stride", _i64), ("scores", _vp), ("scores_len", _i64),
+                ("finished", _vp), ("finished_len", _i64), ("pad_token", _i64),
+                ("parents", _vp), ("parents_len", _i64), ("tokens", _vp), ("tokens_len", _i64),
+                ("out_scores", _vp), ("out_scores_len", _i64), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class gdn_slot_pool(ctypes.Structure):
+    _fields_ = [("data", _vp), ("len", _i64), ("slots", _i64), ("slot_bytes", _i64),
+                ("slot_stride", _i64)]
+
+
+class gdn_copy_slots_args(ctypes.Structure):
+    _fields_ = [("pools", ctypes.POINTER(gdn_slot_pool)), ("num_pools", _i64), ("n", _i64),
+                ("group", _i64), ("dst", _vp), ("src", _vp), ("dst_host", _vp),
+                ("src_host", _vp)]
+
+
 EXPORTED = ("gdn_prepare", "gdn_decode", "gdn_prefill_varlen", "gdn_kda_varlen",
             "gdn_spec_prepare", "gdn_spec_decode", "gdn_packed_decode", "gdn_gated_rmsnorm",
             "gdn_prefill_workspace_bytes",
@@ -204,7 +225,8 @@ EXPORTED = ("gdn_prepare", "gdn_decode", "gdn_prefill_varlen", "gdn_kda_varlen",
             "gdn_read_device_status", "gdn_version", "gdn_launch_count", "gdn_validate_mixed",
             "gdn_check_wait_timeout", "gdn_attn_prepare", "gdn_attn_varlen", "gdn_attn_paged",
             "gdn_attn_paged_workspace_bytes", "gdn_attn8_prepare", "gdn_attn8_paged",
-            "gdn_attn8_paged_workspace_bytes")
+            "gdn_attn8_paged_workspace_bytes", "gdn_beam_select",
+            "gdn_beam_select_workspace_bytes", "gdn_copy_slots")
 
 
 class GdnError(RuntimeError):
@@ -250,13 +272,16 @@ def lib() -> ctypes.CDLL:
             L.gdn_kda_workspace_bytes.restype = ctypes.c_size_t
             L.gdn_kda_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i64, _i32, _i32]
             for name in ("gdn_attn_prepare", "gdn_attn_varlen", "gdn_attn_paged",
-                         "gdn_attn8_prepare", "gdn_attn8_paged"):
+                         "gdn_attn8_prepare", "gdn_attn8_paged", "gdn_beam_select",
+                         "gdn_copy_slots"):
                 getattr(L, name).restype = ctypes.c_int
                 getattr(L, name).argtypes = [_vp, _vp]  # an address of, or a reference to, args
             L.gdn_attn_paged_workspace_bytes.restype = ctypes.c_size_t
             L.gdn_attn_paged_workspace_bytes.argtypes = [_i64] * 6 + [_i32]
             L.gdn_attn8_paged_workspace_bytes.restype = ctypes.c_size_t
             L.gdn_attn8_paged_workspace_bytes.argtypes = [_i64] * 6 + [_i32] + [_i64] * 2
+            L.gdn_beam_select_workspace_bytes.restype = ctypes.c_size_t
+            L.gdn_beam_select_workspace_bytes.argtypes = [_i64] * 4
             L.gdn_status_string.restype = ctypes.c_char_p
             L.gdn_status_string.argtypes = [ctypes.c_int]
             L.gdn_last_error_message.restype = ctypes.c_char_p
@@ -892,6 +917,118 @@ def gdn_attn8_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens,
     _attn_paged(_PAGED8, (_lib or lib()).gdn_attn8_paged, q, k_cache, v_cache, (k_scale, v_scale),
                 block_table, kv_lens, cu_seqlens, out, max_q_len, scale, gate, lse, workspace,
                 cu_seqlens_host, kv_lens_host, block_table_host, stream)
+
+
+# ---- searches over several continuations ---------------------------------------------
+
+_BEAM = _packer(gdn_beam_select_args)
+_SLOTS = _packer(gdn_copy_slots_args)
+
+
+def _on_device(name, what, t, shape, dtype, dev):
+    """A contiguous tensor of this shape, type and device: its address and length."""
+    if t.shape != shape:
+        raise _bad_shape(f"{what} {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise GdnError(GDN_ERR_DTYPE, "GDN_ERR_DTYPE", f"{what} {name} is {t.dtype}, not {dtype}")
+    if t.device != dev:
+        raise _bad(f"{what} {name} is on {t.device}, not {dev}")
+    if not t.is_contiguous():
+        raise _bad(f"{what} {name} must be contiguous")
+    return t.data_ptr(), t.numel()
+
+
+def gdn_beam_select_workspace_bytes(B, W, V, K) -> int:
+    return int(lib().gdn_beam_select_workspace_bytes(B, W, V, K))
+
+
+def gdn_beam_select(logits, scores, parents, tokens, out_scores, *, finished=None, pad_token=0,
+                    workspace=None, stream=None) -> None:
+    """include/gdn.h gdn_beam_select.  logits [B, W, V] (bf16 or f32, the vocabulary
+    contiguous, any other strides), scores [B, W] f32, finished [B, W] uint8 or bool;
+    parents, tokens [B, K] int32 and out_scores [B, K] f32 are written.  `workspace`: a
+    uint8 device tensor of at least gdn_beam_select_workspace_bytes() bytes; when None it
+    is allocated here for the call."""
+    if logits.dim() != 3 or parents.dim() != 2:
+        raise _bad_shape("beam_select logits must be [B, W, V] and parents [B, K]")
+    (n, W, V), K, dev = logits.shape, parents.shape[1], logits.device
+    bs, ws, vs = logits.stride()
+    if V > 1 and vs != 1:
+        raise _bad("beam_select logits' last dimension must be contiguous")
+    if (n > 1 and bs == 0) or (W > 1 and ws == 0):
+        raise _bad("beam_select logits is a broadcast view; pass real rows")
+    bs, ws = (bs if n > 1 else 0), (ws if W > 1 else 0)
+    if bs < 0 or ws < 0:
+        raise _bad_shape("beam_select logits strides out of range")
+    beams = (n, W)
+    fin = (0, 0)
+    if finished is not None:
+        if finished.dtype is torch.bool:
+            finished = finished.view(torch.uint8)
+        fin = _on_device("finished", "beam_select", finished, beams, torch.uint8, dev)
+    sc = _on_device("scores", "beam_select", scores, beams, torch.float32, dev)
+    outs = (n, K)
+    par = _on_device("parents", "beam_select", parents, outs, torch.int32, dev)
+    tok = _on_device("tokens", "beam_select", tokens, outs, torch.int32, dev)
+    best = _on_device("out_scores", "beam_select", out_scores, outs, torch.float32, dev)
+    if best[0] == sc[0] and K != W:
+        raise _bad("beam_select out_scores may be scores only where K = W")
+    dt = _dt(logits)
+    if not logits.is_cuda:
+        raise _bad(f"beam_select tensors must be on a CUDA device, got {dev}")
+    if workspace is None:
+        workspace = _scratch(gdn_beam_select_workspace_bytes(n, W, V, K), dev, stream)
+    elif workspace.device != dev:
+        raise _bad(f"beam_select workspace is on {workspace.device}, not {dev}")
+    length = (n - 1) * bs + (W - 1) * ws + V if n > 0 and W > 0 else 0
+    # A group stride of 0 stands for whole groups of beams: one group has no step of its own.
+    _BEAM.pack_into(_args.buf, 0, n, W, V, K, dt, logits.data_ptr(), length, bs, ws, *sc, *fin,
+                    int(pad_token), *par, *tok, *best, workspace.data_ptr(),
+                    workspace.numel() * workspace.element_size())
+    _attn_call((_lib or lib()).gdn_beam_select, logits, stream)
+
+
+def gdn_copy_slots(pools, dst, src, *, groups=False, dst_host=None, src_host=None,
+                   stream=None) -> None:
+    """include/gdn.h gdn_copy_slots: pool[dst] = pool[src] for every tensor of `pools`
+    (slots first, a slot's values contiguous), updated in place.  groups False: dst, src
+    [n] int32 slots; True: dst [groups, W] the groups' slots, src [groups, W] places in the
+    group (a search's parents)."""
+    if not pools:
+        raise _bad_shape("copy_slots needs at least one pool")
+    dev = pools[0].device
+    if dst.dim() != (2 if groups else 1):
+        raise _bad_shape(f"copy_slots dst has shape {tuple(dst.shape)}, not "
+                         f"{'[groups, W]' if groups else '[n]'}")
+    d = _on_device("dst", "copy_slots", dst, dst.shape, torch.int32, dev)
+    s = _on_device("src", "copy_slots", src, dst.shape, torch.int32, dev)
+    rows = []
+    for i, t in enumerate(pools):
+        if t.device != dev:
+            raise _bad(f"copy_slots pool {i} is on {t.device}, not {dev}")
+        if t.dim() == 0 or t.numel() == 0:
+            raise _bad_shape(f"copy_slots pool {i} has shape {tuple(t.shape)}")
+        if not t[0].is_contiguous():
+            raise _bad(f"copy_slots pool {i}: a slot's values must be contiguous")
+        es, n = t.element_size(), t.shape[0]
+        size = t.numel() // n * es
+        stride = t.stride(0) * es if n > 1 else size
+        if stride == 0:
+            raise _bad(f"copy_slots pool {i} is a broadcast view; pass a real pool")
+        rows += (t.data_ptr(), (n - 1) * stride + size, n, size, stride)
+    if not pools[0].is_cuda:
+        raise _bad(f"copy_slots tensors must be on a CUDA device, got {dev}")
+    table = struct.pack(f"@{len(rows)}q", *rows)
+    keep = ctypes.create_string_buffer(table, len(table))
+    mirrors = []
+    for name, t in (("dst_host", dst_host), ("src_host", src_host)):
+        h, p = _host_i32(t)
+        if h is not None and h.numel() != d[1]:
+            raise _bad_shape(f"copy_slots {name} holds {h.numel()} entries, not {d[1]}")
+        mirrors.append((h, p or 0))
+    _SLOTS.pack_into(_args.buf, 0, ctypes.addressof(keep), len(pools), d[1],
+                     dst.shape[1] if groups else 0, d[0], s[0], mirrors[0][1], mirrors[1][1])
+    _attn_call((_lib or lib()).gdn_copy_slots, pools[0], stream)
 
 
 def _host_u8(t: Optional[torch.Tensor]):

@@ -1540,3 +1540,183 @@ size_t gdn_attn_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t 
 }
 
 }  // extern "C"
+
+// ---- searches over several continuations --------------------------------------------
+
+namespace {
+
+int check_beam_dims(int64_t B, int64_t W, int64_t V, int64_t K, int32_t dt) {
+  if (int rc = check_act_dtype(dt)) return rc;
+  if (B <= 0 || W <= 0 || V <= 0 || K <= 0)
+    return fail(GDN_ERR_SHAPE, "beam_select shape must be positive, got batch=" + S(B) + " beams=" +
+                                   S(W) + " vocabulary=" + S(V) + " best=" + S(K));
+  if (W > gdn::kBeamMaxW || K > gdn::kBeamMaxK)
+    return fail(GDN_ERR_UNSUPPORTED, "beam_select supports at most " + S(gdn::kBeamMaxW) + " beams and " +
+                                         S(gdn::kBeamMaxK) + " continuations of a group");
+  if (V > INT32_MAX / W || B > (int64_t)1 << 20)
+    return fail(GDN_ERR_UNSUPPORTED, "beam_select sizes exceed 32-bit indexing");
+  return GDN_OK;
+}
+
+int beam_select(const gdn_beam_select_args* a, void* stream) {
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+  const int64_t B = a->B, W = a->W, V = a->V, K = a->K;
+  if (int rc = check_beam_dims(B, W, V, K, a->dtype)) return rc;
+  const int64_t beam = a->beam_stride != 0 ? a->beam_stride : V;
+  const int64_t batch = a->batch_stride != 0 ? a->batch_stride : W * beam;
+  if (beam < 0 || batch < 0 || beam > INT64_MAX / 4 / W || batch > INT64_MAX / 4 / B)
+    return fail(GDN_ERR_SHAPE, "beam_select logits strides out of range");
+  const LenRule rules[] = {
+      {"logits", a->logits_len, (B - 1) * batch + (W - 1) * beam + V},
+      {"scores", a->scores_len, B * W},
+      {"finished", a->finished != nullptr ? a->finished_len : B * W, B * W},
+      {"parents", a->parents_len, B * K},
+      {"tokens", a->tokens_len, B * K},
+      {"out_scores", a->out_scores_len, B * K},
+  };
+  if (int rc = check_lengths("beam_select", rules)) return rc;
+  for (auto pr : {std::make_pair(a->logits, "logits"), std::make_pair((const void*)a->scores, "scores"),
+                  std::make_pair((const void*)a->parents, "parents"),
+                  std::make_pair((const void*)a->tokens, "tokens"),
+                  std::make_pair((const void*)a->out_scores, "out_scores")})
+    if (int rc = require_ptr(pr.first, pr.second)) return rc;
+  const uintptr_t es = (uintptr_t)elem_size(a->dtype);
+  if (reinterpret_cast<uintptr_t>(a->logits) % es != 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "logits must be aligned to their type");
+  if (a->finished != nullptr && (a->pad_token < 0 || a->pad_token >= V))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "beam_select pad_token " + S(a->pad_token) + " is outside the vocabulary");
+  const size_t need = gdn::beam_workspace_bytes(B, W, V, K);
+  if (a->workspace == nullptr || a->workspace_bytes < need)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_beam_select workspace needs " + S((int64_t)need) +
+                                              " bytes, got " + S((int64_t)a->workspace_bytes));
+  if ((reinterpret_cast<uintptr_t>(a->workspace) & 255u) != 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  gdn::BeamLaunch p{};
+  p.B = (int)B;
+  p.W = (int)W;
+  p.V = (int)V;
+  p.K = (int)K;
+  p.pad = (int)a->pad_token;
+  p.bf16 = a->dtype == GDN_DTYPE_BF16;
+  p.logits = a->logits;
+  p.batch_stride = batch;
+  p.beam_stride = beam;
+  p.scores = a->scores;
+  p.finished = a->finished;
+  p.parents = a->parents;
+  p.tokens = a->tokens;
+  p.out_scores = a->out_scores;
+  p.ws = a->workspace;
+  return launch_result(gdn::launch_beam(p, static_cast<cudaStream_t>(stream)), "gdn_beam_select");
+}
+
+// What a host copy of the lists can show wrong; `slots`: of the smallest pool.
+int check_slots_host(const int32_t* dst, const int32_t* src, int64_t n, int64_t W, int64_t slots,
+                     int64_t most) {
+  if (dst == nullptr || src == nullptr) return GDN_OK;
+  std::vector<uint8_t> seen((size_t)most, 0);
+  for (int64_t i = 0; i < n; ++i) {
+    if (dst[i] >= slots || src[i] >= (W > 0 ? W : slots))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "copy_slots entry " + S(i) + " names " + S(dst[i]) + " from " +
+                                                S(src[i]) + ", of " + S(slots) + " slots" +
+                                                (W > 0 ? " and groups of " + S(W) : std::string()));
+    if (dst[i] < 0 || (W == 0 && src[i] < 0)) continue;
+    if (seen[(size_t)dst[i]])
+      return fail(GDN_ERR_INVALID_ARGUMENT, "copy_slots slot " + S(dst[i]) + " is a destination twice");
+    seen[(size_t)dst[i]] = 1;
+  }
+  if (W == 0)
+    for (int64_t i = 0; i < n; ++i)
+      if (dst[i] >= 0 && src[i] >= 0 && src[i] != dst[i] && seen[(size_t)src[i]])
+        return fail(GDN_ERR_INVALID_ARGUMENT, "copy_slots slot " + S(src[i]) +
+                                                  " is both a source and a destination");
+  return GDN_OK;
+}
+
+int copy_slots(const gdn_copy_slots_args* a, void* stream) {
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, "args is NULL");
+  if (a->n < 0 || a->num_pools <= 0 || a->group < 0)
+    return fail(GDN_ERR_SHAPE, "copy_slots shape must not be negative, got entries=" + S(a->n) + " pools=" +
+                                   S(a->num_pools) + " group=" + S(a->group));
+  if (a->group > 128) return fail(GDN_ERR_UNSUPPORTED, "copy_slots supports groups of at most 128");
+  if (a->group > 0 && a->n % a->group != 0)
+    return fail(GDN_ERR_SHAPE, "copy_slots entries " + S(a->n) + " must be whole groups of " + S(a->group));
+  if (a->n > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "copy_slots entries exceed 32 bits");
+  if (int rc = require_ptr(a->pools, "pools")) return rc;
+  if (a->n == 0) return succeed();
+  if (int rc = require_ptr(a->dst, "dst")) return rc;
+  if (int rc = require_ptr(a->src, "src")) return rc;
+  int64_t least = INT64_MAX, most = 0;
+  std::vector<gdn::SlotPool> pools;
+  for (int64_t i = 0; i < a->num_pools; ++i) {
+    const gdn_slot_pool& c = a->pools[i];
+    const std::string who = "copy_slots pool " + S(i);
+    if (c.slots <= 0 || c.slots > INT32_MAX || c.slot_bytes <= 0 || c.slot_bytes > (int64_t)1 << 40)
+      return fail(GDN_ERR_SHAPE, who + " has " + S(c.slots) + " slots of " + S(c.slot_bytes) + " bytes");
+    const int64_t stride = c.slot_stride != 0 ? c.slot_stride : c.slot_bytes;
+    if (stride < c.slot_bytes || stride > INT64_MAX / 4 / c.slots)
+      return fail(GDN_ERR_SHAPE, who + " slot stride shorter than a slot or out of range");
+    if (c.len < (c.slots - 1) * stride + c.slot_bytes)
+      return fail(GDN_ERR_SHAPE, who + " length " + S(c.len) + " < expected " +
+                                     S((c.slots - 1) * stride + c.slot_bytes));
+    if (c.data == nullptr) return fail(GDN_ERR_INVALID_ARGUMENT, who + " is NULL");
+    const uint64_t units = reinterpret_cast<uintptr_t>(c.data) | (uint64_t)c.slot_bytes | (uint64_t)stride;
+    if (units % 4 != 0)
+      return fail(GDN_ERR_INVALID_ARGUMENT, who + " address, slot and stride must be multiples of 4 bytes");
+    for (const gdn::SlotPool& o : pools)
+      if (o.data == c.data) return fail(GDN_ERR_INVALID_ARGUMENT, who + " is given twice");
+    gdn::SlotPool q{};
+    q.data = c.data;
+    q.stride = stride;
+    q.bytes = c.slot_bytes;
+    q.slots = c.slots;
+    q.words = units % 16 != 0;
+    pools.push_back(q);
+    least = std::min(least, c.slots);
+    most = std::max(most, c.slots);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::vector<int32_t> dst_buf, src_buf;
+  const int32_t *dst = nullptr, *src = nullptr;
+  if (int rc = host_view(a->dst_host, a->dst, a->n, st, dst_buf, dst)) return rc;
+  if (int rc = host_view(a->src_host, a->src, a->n, st, src_buf, src)) return rc;
+  if (int rc = check_slots_host(dst, src, a->n, a->group, least, most)) return rc;
+  gdn::SlotsLaunch p{};
+  p.W = (int)a->group;
+  p.n = a->n;
+  p.most_slots = most;
+  p.dst = a->dst;
+  p.src = a->src;
+  p.status = gdn::status_word();
+  if (p.status == nullptr) return fail(GDN_ERR_CUDA, "device status word unavailable");
+  for (size_t i = 0; i < pools.size(); i += gdn::kMaxSlotPools) {
+    p.pools = (int)std::min(pools.size() - i, (size_t)gdn::kMaxSlotPools);
+    std::copy_n(pools.begin() + (long)i, p.pools, p.pool);
+    if (int rc = launch_result(gdn::launch_slots(p, st), "gdn_copy_slots")) return rc;
+  }
+  return succeed();
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_beam_select(const gdn_beam_select_args* a, void* stream) {
+  return no_throw([&] { return beam_select(a, stream); });
+}
+
+size_t gdn_beam_select_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t K) {
+  size_t n = 0;
+  no_throw([&] {
+    if (int rc = check_beam_dims(B, W, V, K, GDN_DTYPE_F32)) return rc;
+    n = gdn::beam_workspace_bytes(B, W, V, K);
+    return succeed();
+  });
+  return n;
+}
+
+int gdn_copy_slots(const gdn_copy_slots_args* a, void* stream) {
+  return no_throw([&] { return copy_slots(a, stream); });
+}
+
+}  // extern "C"

@@ -260,4 +260,44 @@ cudaError_t launch_attn8_wide(const AttnLaunch& p, cudaStream_t s);
 size_t attn8_wide_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D,
                                   int64_t max_q, bool bf16, int64_t max_pages, int64_t page_size);
 
+// ---- searches over several continuations ----------------------------------------------
+
+constexpr int kBeamMaxW = 64, kBeamMaxK = 128;
+
+// The K best (beam, token) of each of B groups of W beams.
+struct BeamLaunch {
+  int B, W, V, K, pad;
+  bool bf16;
+  const void* logits;  // rows of V, strides in elements
+  int64_t batch_stride, beam_stride;
+  const float* scores;      // [B, W]
+  const uint8_t* finished;  // [B, W] or null
+  int32_t* parents;         // [B, K]
+  int32_t* tokens;
+  float* out_scores;
+  void* ws;
+};
+size_t beam_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t K);
+cudaError_t launch_beam(const BeamLaunch& p, cudaStream_t s);
+
+// Slots copied (W = 0) or reordered within groups of W.
+struct SlotPool {
+  void* data;
+  int64_t stride, bytes, slots;  // of a slot
+  bool words;                    // in units of 4 bytes, not 16
+  // set by the launch
+  int pairs;                     // of an item
+  int64_t piece, pieces, items;
+};
+constexpr int kMaxSlotPools = 48;
+struct SlotsLaunch {
+  int pools, W;
+  int64_t n, most_slots;
+  const int32_t* dst;
+  const int32_t* src;
+  unsigned* status;
+  SlotPool pool[kMaxSlotPools];
+};
+cudaError_t launch_slots(SlotsLaunch& p, cudaStream_t s);
+
 }  // namespace gdn

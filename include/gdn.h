@@ -856,6 +856,87 @@ size_t gdn_attn8_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t
                                        int64_t max_q_len, int32_t act_dtype, int64_t max_pages,
                                        int64_t page_size);
 
+/* ---------------------------------------------------------------------------
+ * Searches over several continuations of a prompt: each step picks the best
+ * continuations of a group's beams, and the chosen beams' states and cache pages
+ * follow.
+ * ------------------------------------------------------------------------- */
+
+/* gdn_beam_select -- for each group b of W beams, of the continuations (w, v) with
+ *   s[w, v] = scores[b, w] + logits[b, w, v] - ln sum_u e^{logits[b, w, u]}
+ * the K best, in falling order of s, at equal s by the lower w * V + v: parents[b, k] =
+ * w, tokens[b, k] = v, out_scores[b, k] = s.  A beam with finished[b, w] != 0 has one
+ * continuation, (w, pad_token) with s = scores[b, w]; its logits are not read.  Only a
+ * finite s is chosen: a logit of -inf is a token that may not come, a score of -inf a
+ * beam without a life, and a row that holds a NaN or +inf, or nothing but -inf, offers
+ * nothing.  Places left over get parent -1, token -1, s = -inf.
+ * Exponentials and a thread's sums are f32, sums between threads, the logarithm and s
+ * are f64; s is rounded to f32 where it is stored.  (Logits so small that s does not
+ * show their difference in f64 are ordered by the logit, not the index.)
+ * out_scores may be scores itself where K = W; otherwise outputs overlap nothing.
+ * K <= 128, W <= 64, W * V < 2^31.  The workspace is 256-byte aligned, of any contents. */
+typedef struct gdn_beam_select_args {
+  int64_t B, W, V, K;
+  int32_t dtype;             /* gdn_dtype of the logits */
+  const void* logits;        /* [B, W, V], V contiguous, rows at any element */
+  int64_t logits_len;
+  int64_t batch_stride;      /* elements; 0 = W * beam_stride */
+  int64_t beam_stride;       /* elements; 0 = V */
+  const float* scores;       /* [B, W] */
+  int64_t scores_len;
+  const uint8_t* finished;   /* [B, W] or NULL */
+  int64_t finished_len;
+  int64_t pad_token;
+  int32_t* parents;          /* [B, K] */
+  int64_t parents_len;
+  int32_t* tokens;           /* [B, K] */
+  int64_t tokens_len;
+  float* out_scores;         /* [B, K] */
+  int64_t out_scores_len;
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_beam_select_args;
+
+int gdn_beam_select(const gdn_beam_select_args* args, void* stream);
+
+size_t gdn_beam_select_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t K);
+
+/* gdn_copy_slots -- whole slots of any pools (recurrence states, conv tails, pages of a
+ * cache and their scales, rows of a block table), the same move in every pool:
+ *   group = 0:  pool[dst[i]] = pool[src[i]], i < n (a fork, a compaction).  A destination
+ *               is nobody's source.
+ *   group = W:  dst [n / W, W] are the slots of groups, src places in the group, as
+ *               gdn_beam_select's parents: pool[dst[g, j]] = what pool[dst[g, src[g, j]]]
+ *               held before the call, in place, whatever the cycles.
+ * A negative dst or src entry moves nothing (nor does a place whose slot is negative);
+ * nor does a slot onto itself.  No slot is a destination twice.  Pools do not overlap.
+ * What only the device can see wrong (an entry out of range, a slot that is a destination
+ * twice, or a source and a destination of lists) raises the status word
+ * (GDN_ERR_DEVICE_CHECK); an entry out of range moves nothing, and what the slots named
+ * twice then hold is unspecified.
+ * n = 0 is a call that does nothing.  A slot is slot_bytes contiguous bytes; addresses, slot_bytes and strides are multiples
+ * of 4 (of 16: copied in bulk).  group <= 128. */
+typedef struct gdn_slot_pool {
+  void* data;
+  int64_t len;          /* bytes reachable from data */
+  int64_t slots;
+  int64_t slot_bytes;
+  int64_t slot_stride;  /* bytes; 0 = slot_bytes */
+} gdn_slot_pool;
+
+typedef struct gdn_copy_slots_args {
+  const gdn_slot_pool* pools;  /* [num_pools], host */
+  int64_t num_pools;
+  int64_t n;
+  int64_t group;
+  const int32_t* dst;          /* [n], device */
+  const int32_t* src;          /* [n], device */
+  const int32_t* dst_host;     /* optional host copies (both, to be checked) */
+  const int32_t* src_host;
+} gdn_copy_slots_args;
+
+int gdn_copy_slots(const gdn_copy_slots_args* args, void* stream);
+
 /* Scratch bytes gdn_prefill_varlen needs for these sizes and algorithm (0 for
  * the recurrent algorithm; for the fused one the bytes of its optional
  * workspace).  With GDN_PREFILL_AUTO it depends on
