@@ -22,7 +22,7 @@ LIB = os.path.join(BUILD, "libgdn.so")
 SOURCES = ["gdn_api.cpp", "gdn_status.cu", "gdn_prepare.cu", "gdn_recurrent.cu", "gdn_fused.cu",
            "gdn_chunked.cu", "gdn_kda_chunked.cu", "gdn_noalloc.cu", "gdn_norm.cu", "gdn_packed.cu",
            "gdn_attn_prepare.cu", "gdn_attn_simt.cu",
-           "gdn_attn_tc.cu", "gdn_attn8_prepare.cu", "gdn_attn8_wide.cu",
+           "gdn_attn_tc.cu", "gdn_attn8_prepare.cu", "gdn_attn8_wide.cu", "gdn_attn8_tc.cu",
            "gdn_beam.cu", "gdn_slots.cu"]
 HEADERS = ["gdn_internal.h", "tcgen05.cuh", "gdn_math.cuh", "gdn_rowstep.cuh", "gdn_chunk_common.cuh",
            "gdn_attn_common.cuh", "gdn_attn_stream.cuh", "gdn_attn_prepare.cuh"]

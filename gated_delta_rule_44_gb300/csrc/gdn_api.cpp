@@ -1443,16 +1443,18 @@ int attn_paged(const gdn_attn_paged_args* a, void* stream) {
 }
 
 // Which form serves a cache in 8 bits: by the sizes and the type alone.
-enum class Attn8Form { rows, wide };
+enum class Attn8Form { tc, rows, wide };
 Attn8Form attn8_form(int64_t rows, int64_t D, int32_t act_dtype) {
-  (void)act_dtype;
+  if (gdn::attn8_tc_supported(rows, D, act_dtype == GDN_DTYPE_BF16)) return Attn8Form::tc;
   return gdn::attn8_rows_supported(rows, D) ? Attn8Form::rows : Attn8Form::wide;
 }
 
 size_t paged8_need(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q,
                    int32_t act_dtype, int64_t max_pages, int64_t page_size) {
-  if (attn8_form(max_q * (Hq / Hkv), D, act_dtype) == Attn8Form::rows)
-    return gdn::attn_simt_workspace_bytes(T, N, Hq, Hkv, D, max_q);
+  const int64_t rows = max_q * (Hq / Hkv);
+  const Attn8Form form = attn8_form(rows, D, act_dtype);
+  if (form == Attn8Form::tc) return gdn::attn8_tc_workspace_bytes(rows, D);
+  if (form == Attn8Form::rows) return gdn::attn_simt_workspace_bytes(T, N, Hq, Hkv, D, max_q);
   return gdn::attn8_wide_workspace_bytes(T, N, Hq, Hkv, D, max_q, act_dtype == GDN_DTYPE_BF16,
                                          max_pages, page_size);
 }
@@ -1487,6 +1489,7 @@ int attn8_paged(const gdn_attn8_paged_args* a, void* stream) {
   if (int rc = attn_paged_checks(&b, a->cache, "gdn_attn8_paged", need, st, p)) return rc;
   cudaError_t e;
   switch (attn8_form((int64_t)p.max_q * (p.Hq / p.Hkv), p.D, b.act_dtype)) {
+    case Attn8Form::tc: e = gdn::launch_attn8_tc(p, st); break;
     case Attn8Form::rows: e = gdn::launch_attn8_rows(p, st); break;
     default: e = gdn::launch_attn8_wide(p, st);
   }

@@ -1,0 +1,769 @@
+// gdn_attn8_tc.cu -- attention of few rows per kv head (decode, drafts) over a cache in 8
+// bits, on tcgen05 tensor cores, without widening a code.
+//
+// The codes go from the cache to the tensor cores as they are; what is multiplied with
+// them comes in two e4m3 parts, x ~ hi + lo / 32 with hi = e4m3(x), lo = e4m3(32 (x - hi)):
+// q, scaled by a power of two per row, which hi and lo hold exactly down to 2^-10 of the
+// row's largest value (a bf16 has 8 significant bits, the parts 4 and a sign each), and
+// the weights, to 2^-8 relative, as a weight rounded to bf16 would be.  The products are
+// transposed, so that the 128 rows of an MMA are keys or dims, all in use, and the few rows
+// of q are its columns, twice, for hi and lo:
+//   S^T [128 keys x 2R] = K q^T          A = K as it lies in the cache, B = q
+//   O^T [128 dims x 2R] += V^T p^T       A = V^T (keys outermost), B = p
+// with  s = (S_hi + S_lo / 32) kscale qscale log2(e),
+//       p = 2^(s - m) vscale,  l += 2^(s - m),  out = (O_hi + O_lo / 32) / l.
+// m is a reference for p, which has to stay within e4m3's range: the maximum of s +
+// log2(vscale) so far, raised (and O and l scaled) once a tile's maximum is 2^4 above it.
+// So blocks of small values keep their precision beside blocks of large ones.
+//
+// Warps:  0       TMA loads of K and V, a ring of tiles of 128 keys each
+//         1       the MMAs
+//         2       the ranges of key tiles, handed to the other roles
+//         3       TMEM; the stream form's bookkeeping
+//         4 ..    softmax and output: a group of 4 warps for each 16 rows of q.  A thread has
+//                 one key of the tile, so that a row's maximum is one transposing butterfly
+//                 over the lanes and one exchange between the four warps.
+// Two S and two P buffers: the scores of a tile are computed during the softmax of the one
+// before.  Two CTAs share an SM where their memory allows it, and hide each other's chains.
+// The work is that of the stream form (gdn_attn_stream.cuh).
+//
+// A row whose result is not finite, or whose l is too small to be trusted (blocks whose
+// scales differ by 2^90), is evaluated again key by key (exact_row).  Every wait is bounded.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "gdn_attn_common.cuh"
+#include "gdn_attn_stream.cuh"
+#include "gdn_chunk_common.cuh"
+#include "gdn_internal.h"
+#include "tcgen05.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace attn;
+using bf16 = __nv_bfloat16;
+
+constexpr int kMaxRing = 8, kSegs = 4, kMaxGroups = 4;
+constexpr float kHeadroom = 4.0f;       // log2: p reaches 2^4 before the reference follows
+constexpr float kPScale = 16.0f;        // p 2^4 in the parts' units: at most 256 of 448
+constexpr float kLoScale = 32.0f;
+constexpr float kLeastSum = 8.0e-28f;   // 2^-90
+
+struct Shared {
+  uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
+  uint64_t q_full, s_full[2], p_full[2], pv[2], o_full, o_empty, end;
+  uint64_t meet[kMaxGroups];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  Seg seg[kSegs];
+  uint32_t tmem;
+  int abort;
+  int redone;  // rows evaluated again so far, and parts of them
+  uint32_t k_loads[kMaxRing], v_loads[kMaxRing];  // issued so far
+  int start_s, start_hkv, start_u;
+  long long left;
+  long long scan[20];
+  uint32_t redo[kMaxGroups][2];                      // rows to evaluate again, by range parity
+  alignas(16) float qscale[kMaxGroups][16];
+  alignas(16) int last[kMaxGroups][16];              // a row's last visible key
+  alignas(16) float top[kMaxGroups][2][4][16];       // the warps' maxima (sums at the end)
+  alignas(16) float own[kMaxGroups][4][2][16];       // a warp's references and factors
+};
+
+template <int D, int R>
+struct Cfg {
+  static constexpr int N = 2 * R;                      // columns: hi and lo of each row
+  static constexpr int kRowBytes = D < 128 ? D : 128;  // of a swizzled row of K, V and q
+  static constexpr int NB = D / kRowBytes;             // blocks of them
+  static constexpr uint32_t kTile = 128 * D;           // of K, of V
+  static constexpr uint32_t kQ = N * D, kP = 128 * N;
+  static constexpr int kCtas = D <= 128 && R == 16 ? 2 : 1;  // per SM
+  static constexpr uint32_t kRoom = kCtas == 2 ? 115712 : 232448;
+  static constexpr int kFit = (int)((kRoom - sizeof(Shared) - kQ - 2 * kP) / (2 * kTile));
+  static constexpr int ST = kFit > kMaxRing ? kMaxRing : kFit;
+  static constexpr uint32_t kV = ST * kTile, kQAt = 2 * ST * kTile, kPAt = kQAt + kQ, kBars = kPAt + 2 * kP;
+  static constexpr uint32_t kBytes = kBars + sizeof(Shared);
+  static constexpr int kGroups = R / 16;
+  static constexpr int kThreads = 128 + 128 * kGroups;
+  static constexpr int OB = D == 256 ? 2 : 1;          // blocks of 128 dims of O^T
+  static constexpr uint32_t kTO = 2 * N;               // TMEM column of O^T
+  static constexpr uint32_t kCols = kTO + OB * N <= 128 ? 128 : kTO + OB * N <= 256 ? 256 : 512;
+  static_assert(ST >= 2, "tiles in flight");
+  static_assert(kBars % 16 == 0 && kBytes <= kRoom, "shared memory");
+};
+
+struct Tc8Args {
+  int pb;      // rows of a load: a tile's keys, or a divisor of the page
+  int ctas;    // the grid
+  int rows;    // rows of a workspace block
+  int4* info;  // per CTA, see stream_info
+  float* ws;   // the sums
+};
+
+// Operand descriptor for rows (or keys) of 32, 64 or 128 swizzled bytes.
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t lbo, uint32_t sbo, int row_bytes) {
+  const uint64_t mode = row_bytes == 128 ? 2u : row_bytes == 64 ? 4u : 6u;
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46 | mode << 61;
+}
+// The 16-byte chunk at which chunk c of row r lies.
+template <int ROW>
+__device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) {
+  return c ^ (ROW == 128 ? r & 7u : ROW == 64 ? (r >> 1) & 3u : (r >> 2) & 1u);
+}
+// kind::f8f6f4 with e4m3 operands and f32 accumulation, M = 128.
+constexpr uint32_t idesc_e4m3(int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// Maximum or sum over the warp of each of 16 values: lane i is left with that of value
+// i % 16.  Each step halves the values a lane keeps.
+template <bool SUM>
+__device__ __forceinline__ float across(float (&v)[16], int lane) {
+#pragma unroll
+  for (int w = 8; w > 0; w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float send = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
+      const float got = __shfl_xor_sync(0xffffffffu, send, w);
+      v[i] = SUM ? keep + got : fmaxf(keep, got);
+    }
+  }
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+  return SUM ? v[0] + got : fmaxf(v[0], got);
+}
+__device__ __forceinline__ void read16(const float* from, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(from)[i];
+    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+  }
+}
+// The parts of a pair of values.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = f_to_e4x2(a, b);
+  const float2 h = e4x2_to_f(hi);
+  lo = f_to_e4x2((a - h.x) * kLoScale, (b - h.y) * kLoScale);
+}
+
+#define WAIT(bar, parity) \
+  if (!warp_wait(&(bar), (parity), sh, p.status)) return
+
+template <int D, int R>
+__global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
+    attn8_tc_kernel(const __grid_constant__ AttnLaunch p, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ Tc8Args a) {
+  using C = Cfg<D, R>;
+  constexpr int N = C::N, ST = C::ST, ROW = C::kRowBytes, NB = C::NB;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Shared* sh = reinterpret_cast<Shared*>(smem + C::kBars);
+  const uint32_t sk = smem_u32(smem), sv = sk + C::kV, sq = sk + C::kQAt, sp = sk + C::kPAt;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.Hq / p.Hkv;
+
+  start_next_kernel();
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < ST; ++i) {
+        mbar_init(smem_u32(&sh->k_full[i]), 1);
+        mbar_init(smem_u32(&sh->k_empty[i]), 1);
+        mbar_init(smem_u32(&sh->v_full[i]), 1);
+        mbar_init(smem_u32(&sh->v_empty[i]), 1);
+        sh->k_loads[i] = sh->v_loads[i] = 0;
+      }
+      mbar_init(smem_u32(&sh->q_full), 4 * C::kGroups);
+      mbar_init(smem_u32(&sh->o_full), 1);
+      mbar_init(smem_u32(&sh->o_empty), 4 * C::kGroups);
+      mbar_init(smem_u32(&sh->end), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&sh->s_full[i]), 1);
+        mbar_init(smem_u32(&sh->p_full[i]), 4 * C::kGroups);
+        mbar_init(smem_u32(&sh->pv[i]), 1);
+      }
+      for (int i = 0; i < C::kGroups; ++i) {
+        mbar_init(smem_u32(&sh->meet[i]), 4);
+        sh->redo[i][0] = sh->redo[i][1] = 0;
+      }
+      for (int i = 0; i < kSegs; ++i) {
+        mbar_init(smem_u32(&sh->seg_full[i]), 1);
+        mbar_init(smem_u32(&sh->seg_empty[i]), 2 + 4 * C::kGroups);
+      }
+      sh->abort = sh->redone = 0;
+      fence_mbar_init();
+    }
+  } else if (warp == 3) {
+    tmem_alloc(smem_u32(&sh->tmem), C::kCols);
+  }
+  stream_start<C::kThreads>(p, a.ctas, sh);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+
+  int seg_in = 0;
+  auto next_seg = [&](Seg& g) -> bool {
+    const int i = seg_in % kSegs;
+    if (!warp_wait(&sh->seg_full[i], (seg_in / kSegs) & 1, sh, p.status)) return false;
+    g = sh->seg[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh->seg_empty[i]));
+    ++seg_in;
+    return g.s >= 0;
+  };
+  // A ring's position: place and parity of its round.
+  struct Ring {
+    uint32_t st = 0, round = 0;
+    __device__ void step() {
+      if (++st == ST) {
+        st = 0;
+        round ^= 1;
+      }
+    }
+  };
+  if (warp == 0) {
+    // ---- loads ----
+    auto role = [&] {
+      Ring ring;
+      uint32_t filled = 0;
+      Seg g;
+      while (next_seg(g)) {
+        const int kt0 = uni(g.kt0), n = uni(g.kt1) - kt0, hi = uni(g.hi), hkv = uni(g.hkv);
+        const int per_tile = BK / a.pb;
+        // Lane i looks up the page of, and issues, the tile's i-th group of pb keys.
+        auto find_page = [&](int kt) -> int {
+          const int jb = kt * BK + lane * a.pb;
+          if (lane >= per_tile || kt >= kt0 + n || jb >= hi) return 0;
+          const int64_t pg = page_of(p, g.s, jb / p.page_size);
+          if (pg < 0) atomicOr(p.status, kStatusBadIndex);
+          return pg < 0 ? (int)p.num_pages : (int)pg;  // past the end: reads as zeros
+        };
+        int next_page = find_page(kt0);
+        for (int j = 0; j < n; ++j, ring.step(), ++filled) {
+          const int j0 = (kt0 + j) * BK, page = next_page;
+          next_page = find_page(kt0 + j + 1);
+          const int groups = min(per_tile, (hi - j0 + a.pb - 1) / a.pb);
+          const int row = (j0 + lane * a.pb) % p.page_size;
+          auto load = [&](uint32_t to, const CUtensorMap* map, uint64_t* full, uint64_t* empty,
+                          uint32_t* loads) -> bool {
+            if (filled >= ST)
+              if (!warp_wait(&empty[ring.st], ring.round ^ 1, sh, p.status)) return false;
+            const uint32_t bar = smem_u32(&full[ring.st]);
+            if (elect_one()) {
+              ++loads[ring.st];
+              mbar_expect_tx(bar, groups * a.pb * (uint32_t)D);
+            }
+            __syncwarp();
+            if (lane < groups)
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                tma_load_4d(to + ring.st * C::kTile + b * 128 * ROW + lane * a.pb * ROW, map, bar, b * ROW,
+                            row, hkv, page);
+            __syncwarp();
+            return true;
+          };
+          if (!load(sk, &mk, sh->k_full, sh->k_empty, sh->k_loads)) return;
+          if (!load(sv, &mv, sh->v_full, sh->v_empty, sh->v_loads)) return;
+        }
+      }
+    };
+    role();
+  } else if (warp == 1) {
+    // ---- MMAs ----
+    auto role = [&] {
+      constexpr uint32_t kIdQK = idesc_e4m3(N, false, false), kIdPV = idesc_e4m3(N, true, true);
+      Ring kr, vr;
+      uint32_t nk = 0;  // tiles whose P V has been issued
+      int nseg = 0;
+      auto scores = [&](uint32_t n) -> bool {  // of tile n, into S[n & 1]
+        if (!warp_wait(&sh->k_full[kr.st], kr.round, sh, p.status)) return false;
+        fence_after_sync();
+        if (elect_one()) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint64_t kd = desc_of(sk + kr.st * C::kTile + b * 128 * ROW, 16, 8 * ROW, ROW);
+            const uint64_t qd = desc_of(sq + b * N * ROW, 16, 8 * ROW, ROW);
+#pragma unroll
+            for (int k = 0; k < ROW / 32; ++k)
+              mma_e4m3(tmem + (n & 1) * N, kd + k * 2, qd + k * 2, kIdQK, b + k > 0);
+          }
+          mma_commit(smem_u32(&sh->k_empty[kr.st]));
+          mma_commit(smem_u32(&sh->s_full[n & 1]));
+        }
+        kr.step();
+        return true;
+      };
+      Seg g;
+      while (next_seg(g)) {
+        const int n = uni(g.kt1 - g.kt0);
+        WAIT(sh->q_full, nseg & 1);
+        fence_after_sync();
+        if (!scores(nk)) return;
+        for (int j = 0; j < n; ++j, ++nk) {
+          if (j + 1 < n)
+            if (!scores(nk + 1)) return;
+          WAIT(sh->v_full[vr.st], vr.round);
+          WAIT(sh->p_full[nk & 1], (nk >> 1) & 1);
+          if (j == 0 && nseg > 0) WAIT(sh->o_empty, (nseg - 1) & 1);
+          fence_after_sync();
+          if (elect_one()) {
+            const uint64_t pd = desc_of(sp + (nk & 1) * C::kP, 16, 8 * N, N);
+#pragma unroll
+            for (int b = 0; b < C::OB; ++b) {
+              // (D = 64: dims 64 .. 127 of the product are not used; they read the tile's
+              // second half.)
+              const uint64_t vd = desc_of(sv + vr.st * C::kTile + b * 128 * ROW, 64 * ROW, 8 * ROW, ROW);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_e4m3(tmem + C::kTO + b * N, vd + ((k * 32 * ROW) >> 4), pd + ((k * 32 * N) >> 4), kIdPV,
+                         j + k > 0);
+            }
+            mma_commit(smem_u32(&sh->v_empty[vr.st]));
+            mma_commit(smem_u32(&sh->pv[nk & 1]));
+            if (j == n - 1) mma_commit(smem_u32(&sh->o_full));
+          }
+          vr.step();
+        }
+        ++nseg;
+      }
+    };
+    role();
+    __syncwarp();
+    if (elect_one()) mma_commit(smem_u32(&sh->end));
+    mbar_wait(smem_u32(&sh->end), 0, kWaitBudget);
+  } else if (warp == 2) {
+    // ---- ranges ----
+    auto role = [&] {
+      SegIter iter{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
+      for (int n = 0;; ++n) {
+        Seg g;
+        if (!iter.next(p, g)) g.s = -1;
+        const int i = n % kSegs;
+        if (n >= kSegs) WAIT(sh->seg_empty[i], (n / kSegs - 1) & 1);
+        if (lane == 0) {
+          sh->seg[i] = g;
+          mbar_arrive(smem_u32(&sh->seg_full[i]));
+        }
+        __syncwarp();
+        if (g.s < 0) return;
+      }
+    };
+    role();
+  } else if (warp == 3) {
+    if (lane == 0) a.info[blockIdx.x] = stream_info(p, sh);
+    // Sequences without a key.
+    for (int s = blockIdx.x; s < p.N; s += a.ctas) {
+      const SeqRange q = seq_range(p, s);
+      if (key_tiles(q) > 0) continue;
+      const float zero[D / 32] = {};
+      for (int t = q.a; t < q.b; ++t)
+        for (int h = 0; h < p.Hq; ++h) finish_row<bf16, D>(p, t, h, lane, zero, -INFINITY, 0.0f);
+    }
+  } else {
+    // ---- softmax, output ----
+    const int gr = (warp - 4) >> 2, w4 = warp & 3;
+    const int r = tid & 127;                       // key of the tile, dim of O, lane of TMEM
+    const uint32_t lanes = (uint32_t)w4 << 21;     // (32 * w4) << 16
+    const uint32_t ts = tmem + lanes + 32 * gr;
+    auto role = [&] {
+      uint32_t nk = 0, met = 0;
+      int seg_n = 0;
+      Ring vr;
+      // Meeting the group's other warps (bounded).
+      auto meet = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->meet[gr]));
+        return warp_wait(&sh->meet[gr], met++ & 1, sh, p.status);
+      };
+      float* own = &sh->own[gr][w4][0][0];
+      Seg g;
+      while (next_seg(g)) {
+        const int rows = g.nt * G;  // of q
+        // The pages and scales of this thread's key, two and one tile ahead.
+        auto page_at = [&](int kt) -> int64_t {
+          const int j = kt * BK + r;
+          return kt < g.kt1 && j < g.hi ? page_of(p, g.s, j / p.page_size) : -1;
+        };
+        auto scales_at = [&](int kt, int64_t pg, float& k, float& v) {
+          k = v = 0.0f;
+          if (pg < 0) return;
+          const int64_t at = scale_at(p.Hkv, p.page_size, p.block, pg, g.hkv, (kt * BK + r) % p.page_size);
+          k = p.ks[at];
+          v = p.vs[at];
+        };
+        float next_k, next_v;
+        scales_at(g.kt0, page_at(g.kt0), next_k, next_v);
+        int64_t next_page = page_at(g.kt0 + 1);
+        {
+          // q of the group's rows: 8 threads each.  All its products with the range before
+          // are done: their scores have been read.
+          const int i = r >> 3, part = r & 7, row = gr * 16 + i;
+          constexpr int E = D / 8;  // dims of a thread
+          float x[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = 0.0f;
+          if (row < rows) {
+            const bf16* from = static_cast<const bf16*>(p.q.p) + (int64_t)(g.t0 + row / G) * p.q.ts +
+                               (int64_t)(g.hkv * G + row % G) * p.q.hs + part * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 8) {
+              const uint4 v = *reinterpret_cast<const uint4*>(from + e);
+              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                x[e + 2 * k] = __uint_as_float(u[k] << 16);
+                x[e + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+              }
+            }
+          }
+          float big = 0.0f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(x[e]));
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+          // 2^e that brings the largest into [128, 256).
+          const int ex = max(-126, min(126, 134 - (int)(__float_as_uint(big) >> 23)));
+          const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+          if (part == 0) {
+            sh->qscale[gr][i] = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - ex) << 23);
+            sh->last[gr][i] = row < rows ? g.pos0 + row / G : -1;
+          }
+          uint32_t hi[E / 4], lo[E / 4];
+#pragma unroll
+          for (int e = 0; e < E; e += 4) {
+            uint32_t h0, l0, h1, l1;
+            // (x - x: what is not finite becomes NaN)
+            split2(fmaf(x[e], up, x[e] - x[e]), fmaf(x[e + 1], up, x[e + 1] - x[e + 1]), h0, l0);
+            split2(fmaf(x[e + 2], up, x[e + 2] - x[e + 2]), fmaf(x[e + 3], up, x[e + 3] - x[e + 3]), h1, l1);
+            hi[e / 4] = h0 | h1 << 16;
+            lo[e / 4] = l0 | l1 << 16;
+          }
+          auto put = [&](uint32_t n, const uint32_t(&c)[E / 4]) {
+#pragma unroll
+            for (int e = 0; e < E; e += 16) {
+              const int d = part * E + e, b = d / ROW, in = d % ROW;
+              unsigned char* to = smem + C::kQAt + b * N * ROW + n * ROW + swz<ROW>(n, in >> 4) * 16 + (in & 15);
+              if constexpr (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
+              else
+                *reinterpret_cast<uint4*>(to) = make_uint4(c[e / 4], c[e / 4 + 1], c[e / 4 + 2], c[e / 4 + 3]);
+            }
+          };
+          put(32 * gr + i, hi);
+          put(32 * gr + 16 + i, lo);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
+        }
+        if (!meet()) return;  // qscale, last
+        float l[16], m = -INFINITY;  // l of this thread's keys; m of row lane % 16
+#pragma unroll
+        for (int i = 0; i < 16; ++i) l[i] = 0.0f;
+        for (int kt = g.kt0; kt < g.kt1; ++kt, ++nk, vr.step()) {
+          const uint32_t buf = nk & 1;
+          const float ksc = next_k, vsc = next_v;
+          scales_at(kt + 1, next_page, next_k, next_v);
+          next_page = page_at(kt + 2);
+          // (a scale of nothing, 0, has no logarithm: 2^-64 stands for smaller ones)
+          const float lv = fmaxf(__log2f(fabsf(vsc)), -64.0f);
+          const int j = kt * BK + r;
+          const bool masked = kt * BK + BK - 1 > g.pos0;
+          float s[16];
+          {
+            float qs[16];
+            read16(sh->qscale[gr], qs);
+            WAIT(sh->s_full[buf], (nk >> 1) & 1);
+            fence_after_sync();
+            float y[32];
+            tmem_ld32(ts + buf * N, y);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = fmaf(y[16 + i], 1.0f / kLoScale, y[i]) * (ksc * qs[i]);
+          }
+          if (masked) {
+            const int4* last = reinterpret_cast<const int4*>(sh->last[gr]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int4 v = last[i];
+              s[4 * i] = j <= v.x ? s[4 * i] : -INFINITY;
+              s[4 * i + 1] = j <= v.y ? s[4 * i + 1] : -INFINITY;
+              s[4 * i + 2] = j <= v.z ? s[4 * i + 2] : -INFINITY;
+              s[4 * i + 3] = j <= v.w ? s[4 * i + 3] : -INFINITY;
+            }
+          }
+          {
+            float t[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t[i] = s[i] + lv;
+            const float mine = across<false>(t, lane);
+            if (lane < 16) sh->top[gr][buf][w4][lane] = mine;
+          }
+          if (!meet()) return;
+          bool raise = false;
+          {
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) top = fmaxf(top, sh->top[gr][buf][w][lane & 15]);
+            float f = 1.0f;
+            if (top > m + kHeadroom) {  // the same in the group's warps
+              raise = true;
+              f = ex2(m - top);
+              m = top;
+            }
+            if (lane < 16) {
+              own[lane] = m == -INFINITY ? 0.0f : m;
+              own[16 + lane] = f;
+            }
+            __syncwarp();
+          }
+          if (__any_sync(0xffffffffu, raise)) {
+            float f[16];
+            read16(own + 16, f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) l[i] *= f[i];
+            if (kt > g.kt0) {
+              WAIT(sh->pv[buf ^ 1], ((nk - 1) >> 1) & 1);
+              fence_after_sync();
+#pragma unroll 1
+              for (int b = 0; b < 2 * C::OB; ++b) {  // hi, lo of each block of dims
+                float o[16];
+                tmem_ld16(ts + C::kTO + (b >> 1) * N + (b & 1) * 16, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= f[i];
+                tmem_st16(ts + C::kTO + (b >> 1) * N + (b & 1) * 16, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          if (nk >= 2) WAIT(sh->pv[buf], ((nk >> 1) - 1) & 1);  // P[buf] has been read
+          {
+            float ref[16];
+            read16(own, ref);
+            const float vs = vsc * kPScale;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              float w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                w[e] = ex2(s[i + e] - ref[i + e]);
+                l[i + e] += w[e];
+                w[e] *= vs;
+              }
+              uint32_t h0, l0, h1, l1;
+              split2(w[0], w[1], h0, l0);
+              split2(w[2], w[3], h1, l1);
+              hi[i / 4] = h0 | h1 << 16;
+              lo[i / 4] = l0 | l1 << 16;
+            }
+            unsigned char* to = smem + C::kPAt + buf * C::kP + r * N;
+            *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr + 1) * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          if (gr == 0 && (kt + 1) * BK > g.hi) {
+            // Rows of V past the context's end: a stale NaN there would survive a weight of 0.
+            WAIT(sh->v_full[vr.st], vr.round);
+            if (j >= g.hi) {
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                uint4* to = reinterpret_cast<uint4*>(smem + C::kV + vr.st * C::kTile + b * 128 * ROW + r * ROW);
+#pragma unroll
+                for (int e = 0; e < ROW / 16; ++e) to[e] = make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+          }
+          fence_proxy_async();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
+        }
+        // ---- the rows' sums out ----
+        const float part_l = across<true>(l, lane);
+        if (lane < 16) sh->top[gr][nk & 1][w4][lane] = part_l;
+        if (!meet()) return;
+        if (r == 0) sh->redo[gr][(seg_n & 1) ^ 1] = 0;  // (the last range's has been read)
+        float L = 0.0f;  // of row lane % 16, the same in every warp
+#pragma unroll
+        for (int w = 0; w < 4; ++w) L += sh->top[gr][nk & 1][w][lane & 15];
+        const int live = min(16, rows - gr * 16);  // rows of this group
+        if (lane < 16) own[lane] = g.slot >= 0 ? 1.0f / kPScale : L == 0.0f ? 0.0f : 1.0f / (L * kPScale);
+        __syncwarp();
+        const bool fine = (L - L == 0.0f && L >= kLeastSum) || (m == -INFINITY && L == 0.0f);
+        uint32_t bad = __ballot_sync(0xffffffffu, !fine) & 0xffffu;
+        const Partials part(a.ws, 2 * (int64_t)a.ctas, a.rows, D);
+        WAIT(sh->o_full, seg_n & 1);
+        fence_after_sync();
+#pragma unroll 1
+        for (int b = 0; b < C::OB; ++b) {
+          float o[16];
+          {
+            float y[32];
+            tmem_ld32(ts + C::kTO + b * N, y);
+            tmem_ld_wait();
+            float f[16];
+            read16(own, f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = fmaf(y[16 + i], 1.0f / kLoScale, y[i]) * f[i];
+          }
+          const int dim = b * 128 + r;
+          if (D >= 128 || r < D) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (i >= live) continue;
+              const int row = gr * 16 + i;
+              if (!(o[i] - o[i] == 0.0f)) bad |= 1u << i;
+              if (g.slot >= 0) {
+                part.o[(g.slot * a.rows + row) * D + dim] = o[i];
+              } else {
+                const int t = g.t0 + row / G, h = g.hkv * G + row % G;
+                float x = o[i];
+                if (p.gate.p != nullptr)
+                  x *= sigmoid_gate(to_f(static_cast<const bf16*>(
+                      p.gate.p)[(int64_t)t * p.gate.ts + (int64_t)h * p.gate.hs + dim]));
+                static_cast<bf16*>(p.out)[((int64_t)t * p.Hq + h) * D + dim] = __float2bfloat16_rn(x);
+              }
+            }
+          }
+        }
+        fence_before_sync();
+        if (w4 == 0 && lane < live) {
+          const int row = gr * 16 + lane;
+          if (g.slot >= 0)
+            part.ml[g.slot * a.rows + row] = make_float2(L == 0.0f ? -INFINITY : m, L);
+          else if (p.lse != nullptr)
+            p.lse[(int64_t)(g.t0 + row / G) * p.Hq + g.hkv * G + row % G] =
+                L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
+        }
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        if (live < 16) bad &= live > 0 ? (1u << live) - 1u : 0u;
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sh->o_empty));
+          if (bad) atomicOr(&sh->redo[gr][seg_n & 1], bad);
+        }
+        if (!meet()) return;
+        uint32_t redo = *(volatile uint32_t*)&sh->redo[gr][seg_n & 1] & (0x1111u << w4);
+        while (redo) {
+          const int i = __ffs(redo) - 1, row = gr * 16 + i;
+          redo &= redo - 1;
+          const int t = g.t0 + row / G, h = g.hkv * G + row % G;
+          float acc[D / 32], em, el;
+          exact_row<bf16, D, E4>(p, g.s, cu_at(p.cu, g.s), t, h, g.kt0 * BK,
+                                 min(g.kt1 * BK, g.pos0 + row / G + 1), acc, em, el, &sh->redone);
+          if (g.slot >= 0) part.put<D / 32>(g.slot, row, lane, acc, em, el);
+          else finish_row<bf16, D>(p, t, h, lane, acc, em, el);
+          if (lane == 0) atomicAdd(&sh->redone, 1);
+        }
+        ++seg_n;
+      }
+    };
+    role();
+  }
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (sh->abort) {
+    // A wait gave up: copies may still be in flight (otherwise the MMA role has waited for
+    // each).  They land before the CTA's memory is given up.
+    if (tid == 0)
+      for (int i = 0; i < ST; ++i) {
+        if (sh->k_loads[i]) mbar_wait(smem_u32(&sh->k_full[i]), (sh->k_loads[i] - 1) & 1, kWaitBudget);
+        if (sh->v_loads[i]) mbar_wait(smem_u32(&sh->v_full[i]), (sh->v_loads[i] - 1) & 1, kWaitBudget);
+      }
+    __syncthreads();
+  }
+  if (warp == 3) tmem_dealloc(tmem, C::kCols);
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) attn8_join_kernel(const __grid_constant__ AttnLaunch p,
+                                                         const __grid_constant__ Tc8Args a) {
+  stream_join<bf16, D>(p, a);
+}
+
+// ---- host ------------------------------------------------------------------------
+
+template <int D, int R>
+bool codes_map(CUtensorMap* m, const AttnPages& c, const AttnLaunch& p, int pb) {
+  auto enc = chunk::encode_fn();
+  if (enc == nullptr) return false;
+  constexpr int ROW = Cfg<D, R>::kRowBytes;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)p.page_size, (cuuint64_t)p.Hkv,
+                              (cuuint64_t)p.num_pages};
+  const cuuint64_t st[3] = {(cuuint64_t)c.ts, (cuuint64_t)c.hs, (cuuint64_t)c.ps};
+  const cuuint32_t box[4] = {ROW, (cuuint32_t)pb, 1, 1}, es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.p, dims, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             ROW == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int row_class(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+template <int D, int R>
+cudaError_t run(const AttnLaunch& p, cudaStream_t st) {
+  using C = Cfg<D, R>;
+  Tc8Args a{};
+  a.pb = BK;
+  while (p.page_size % a.pb != 0) a.pb >>= 1;
+  a.ctas = C::kCtas * chunk::sm_count();
+  a.rows = p.max_q * (p.Hq / p.Hkv);
+  a.info = static_cast<int4*>(p.ws);
+  a.ws = reinterpret_cast<float*>(static_cast<char*>(p.ws) + info_bytes(a.ctas));
+  CUtensorMap mk, mv;
+  if (!codes_map<D, R>(&mk, p.kc, p, a.pb) || !codes_map<D, R>(&mv, p.vc, p, a.pb))
+    return cudaErrorInvalidValue;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      attn8_tc_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
+  if (attr != cudaSuccess) return attr;
+  attn8_tc_kernel<D, R><<<a.ctas, C::kThreads, C::kBytes, st>>>(p, mk, mv, a);
+  note_launch();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(attn8_join_kernel<D>, dim3(a.ctas, std::min(a.rows, 16)), 256, st, p, a);
+}
+
+template <int D>
+cudaError_t by_rows(const AttnLaunch& p, cudaStream_t st) {
+  switch (row_class((int64_t)p.max_q * (p.Hq / p.Hkv))) {
+    case 16: return run<D, 16>(p, st);
+    case 32: return run<D, 32>(p, st);
+    default: return run<D, 64>(p, st);
+  }
+}
+
+template <int D>
+int ctas_per_sm(int64_t rows) {
+  return row_class(rows) == 16 ? Cfg<D, 16>::kCtas : 1;
+}
+
+}  // namespace
+
+bool attn8_tc_supported(int64_t rows, int64_t D, bool bf16) { return bf16 && D >= 64 && rows <= 64; }
+
+size_t attn8_tc_workspace_bytes(int64_t rows, int64_t D) {
+  const int per = D == 64 ? ctas_per_sm<64>(rows) : D == 128 ? ctas_per_sm<128>(rows) : ctas_per_sm<256>(rows);
+  const int ctas = per * chunk::sm_count();
+  return info_bytes(ctas) + Partials::bytes(2 * (int64_t)ctas, (int)rows, D);
+}
+
+cudaError_t launch_attn8_tc(const AttnLaunch& p, cudaStream_t st) {
+  switch (p.D) {
+    case 64: return by_rows<64>(p, st);
+    case 128: return by_rows<128>(p, st);
+    default: return by_rows<256>(p, st);
+  }
+}
+
+}  // namespace gdn

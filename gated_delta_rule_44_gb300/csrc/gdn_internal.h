@@ -251,7 +251,10 @@ size_t attn_tc_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, in
                                int64_t max_q);
 
 // The same attention over a cache in 8 bits (p.ks, p.vs, p.block).
-// Few rows per kv head on CUDA cores: attn8_rows_supported() sizes.
+// Few rows per kv head on tensor cores, and on CUDA cores (attn8_..._supported() sizes).
+bool attn8_tc_supported(int64_t rows, int64_t D, bool bf16);
+cudaError_t launch_attn8_tc(const AttnLaunch& p, cudaStream_t s);
+size_t attn8_tc_workspace_bytes(int64_t rows, int64_t D);
 bool attn8_rows_supported(int64_t rows, int64_t D);
 cudaError_t launch_attn8_rows(const AttnLaunch& p, cudaStream_t s);
 // Any sizes: the contexts of some sequences at a time are widened into the workspace, and
