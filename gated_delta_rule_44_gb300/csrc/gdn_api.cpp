@@ -1556,7 +1556,7 @@ int check_beam_dims(int64_t B, int64_t W, int64_t V, int64_t K, int32_t dt) {
   if (W > gdn::kBeamMaxW || K > gdn::kBeamMaxK)
     return fail(GDN_ERR_UNSUPPORTED, "beam_select supports at most " + S(gdn::kBeamMaxW) + " beams and " +
                                          S(gdn::kBeamMaxK) + " continuations of a group");
-  if (V > INT32_MAX / W || B > (int64_t)1 << 20)
+  if (V > INT32_MAX / W || B > 65535)
     return fail(GDN_ERR_UNSUPPORTED, "beam_select sizes exceed 32-bit indexing");
   return GDN_OK;
 }

@@ -3,14 +3,19 @@
 //   s[w, v] = score[w] + x[w, v] - ln sum_u e^{x[w, u]},
 // in one pass over the logits.
 //
-// Row kernel.  A CTA has a segment of a row.  Each thread keeps a running maximum and sum of
-// exponentials (f32; the threads' sums are joined in f64), and the segment's K largest
-// logits are collected on the way: in the first chunk every warp sorts its lanes' maxima,
-// and the smallest of the warps' ceil(K / 8)-th ones is a value that at least K logits of
-// the segment reach; from then on only logits that reach it are put aside (some K to 10 K
-// of them), and the segment's list is the K first of them, sorted.  A segment in which more
-// reach it than there is room for (rows of equal logits) is read again, once for each of
-// the K places.
+// Row kernel.  A CTA has a segment of a row.  Each thread keeps a running sum of
+// 2^(H x - ref) (f32), H = log2(e) rounded to f32 and ref a whole number: H x - ref is one
+// rounding (an fma), changes of ref and joins are exact, and ln sum e^x = ref / H + ln(sum) to
+// within the 1.3e-8 (largest x - x) that H's rounding leaves, where x has its weight.  So
+// an element costs an fma, an exponential and an add.  The threads' sums are joined in f64.
+// The segment's K largest logits are collected on the way: the K-th largest of the threads'
+// maxima so far (found by one warp, two of the upper 16 bits of its order at a time) is a value
+// that at least K logits reach, and only 16-byte vectors with a logit that reaches it are put
+// aside, whole.  It is taken after the first chunk and again after 8, 64, ... (each time the
+// other warps wait for the one; from chunk to chunk some K more vectors reach it), and at the
+// end (ranking four chunks' worth by counting took three times as long).  The logits put aside that reach the last one are ranked by
+// counting.  A segment in which more are put aside, or reach it, than there
+// is room for (rows of equal logits) is read again, once for each of the K places.
 //
 // Join kernel.  A CTA per group joins the segments' sums into f64 log-sums, turns list
 // entries into 64-bit scores (beams are compared at 2^-53: two f32 roundings of a score of
@@ -18,7 +23,8 @@
 // head of a list.  Order: score, then the lower w V + v; keys are integers, since f64
 // comparisons are a sixty-fourth of their rate.
 //
-// Bound by the read of the logits; 64 x 8 rows of 131072 bf16 are 134 MB, 20 us.
+// Bound by the read of the logits in the end; now by instructions: 64 x 8 rows of 131072 bf16
+// (134 MB, 20 us) take 43 us in the row kernel, at 62 % of the issue rate, and 55 a call.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,13 +39,16 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;      // 16-byte vectors of a thread per chunk
-constexpr int kRoom = 2048;     // logits put aside
-constexpr int kMaxSegs = 32;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kAside = 768;     // vectors put aside
+constexpr int kRanked = 1024;    // logits of them, ranked by counting
+constexpr int kRoom = 2048;     // entries of the join's sorts
+constexpr int kMaxSegs = 32;    // a lane each
+constexpr float kH = 1.4426950408889634f;  // log2(e) in f32
 
-// What a segment leaves: count entries of its list (value key, ~index), its maximum and sum.
+// What a segment leaves: the count of its list's entries (value key, ~index), and its sum of
+// 2^(H x - ref) (ref -inf: nothing is above that).
 struct SegSum {
-  float m;
+  float ref;
   int count;
   double sum;
 };
@@ -95,6 +104,13 @@ struct Vec<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  __device__ uint4 bits() const { return r; }
+  __device__ void from(const uint4& b) { r = b; }
+  __device__ float top() const {  // (a NaN counts only beside another)
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&r);
+    const __nv_bfloat162 m = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
 };
 template <>
 struct Vec<float> {
@@ -104,163 +120,203 @@ struct Vec<float> {
   __device__ void get(float (&x)[4]) const {
     x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
   }
+  __device__ uint4 bits() const { return *reinterpret_cast<const uint4*>(&r); }
+  __device__ void from(const uint4& b) { r = *reinterpret_cast<const float4*>(&b); }
+  __device__ float top() const { return fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)); }
 };
 
-// Sorts the first n entries (padded with 0 up to a power of two; `size` of them have room)
-// in falling order, by the whole CTA.
-__device__ __forceinline__ void sort_falling(unsigned long long* a, int n) {
-  int size = 2;
-  while (size < n) size <<= 1;
-  for (int i = n + threadIdx.x; i < size; i += kThreads) a[i] = 0;
+// A value that at least K of the threads' values reach, near the K-th largest: by the whole
+// CTA (two barriers).
+__device__ __forceinline__ float common_floor(float t, int K, uint32_t* shared) {
+  shared[threadIdx.x] = order_of(t);
   __syncthreads();
-  for (int k = 2; k <= size; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-        const int lo = 2 * j * (i / j) + i % j, hi = lo + j;
-        const unsigned long long x = a[lo], y = a[hi];
-        if ((x < y) == ((lo & k) == 0)) {
-          a[lo] = y;
-          a[hi] = x;
-        }
+  if (threadIdx.x < 32) {
+    const uint4 a = reinterpret_cast<const uint4*>(shared)[threadIdx.x];
+    const uint4 b = reinterpret_cast<const uint4*>(shared)[threadIdx.x + 32];
+    uint32_t bound = 0;
+#pragma unroll
+    for (int bit = 30; bit >= 16; bit -= 2) {
+      uint32_t step = 0;  // the largest of three that K values still reach
+#pragma unroll
+      for (uint32_t q = 1; q <= 3; ++q) {
+        const uint32_t x = bound | q << bit;
+        const int n = (a.x >= x) + (a.y >= x) + (a.z >= x) + (a.w >= x) + (b.x >= x) + (b.y >= x) +
+                      (b.z >= x) + (b.w >= x);
+        if (__reduce_add_sync(0xffffffffu, n) >= K) step = q;
       }
-      __syncthreads();
+      bound |= step << bit;
     }
+    __syncwarp();
+    if (threadIdx.x == 0) shared[0] = bound;
+  }
+  __syncthreads();
+  // (below the order of -inf there is no number: nothing is known yet)
+  const uint32_t bound = shared[0];
+  return bound < 0x007fffffu ? -INFINITY : value_of(bound);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 6) beam_rows_kernel(const __grid_constant__ BeamLaunch p,
-                                                                int segs, int seg_len) {
+__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_constant__ BeamLaunch p,
+                                                                int seg_len) {
   attn::start_next_kernel();
-  __shared__ unsigned long long aside[kRoom];
-  __shared__ float bound[kWarps];
-  __shared__ float wm[kWarps];
+  attn::wait_for_previous_kernel();
+  __shared__ uint4 aside[kAside];
+  __shared__ int aside_at[kAside];
+  __shared__ unsigned long long few[kRanked];
+  __shared__ __align__(16) uint32_t tops_of[kThreads];
+  __shared__ float wref[kWarps];
   __shared__ double wsum[kWarps];
   __shared__ unsigned long long best[kWarps];
-  __shared__ int count;
+  __shared__ int count, few_count;
   using V = Vec<T>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x / segs, seg = blockIdx.x % segs;
-  const int K = p.K;
+  const int seg = blockIdx.x, segs = gridDim.x, K = p.K;
+  const int row = blockIdx.z * p.W + blockIdx.y;
   const Ws ws = carve(p.ws, (int64_t)p.B * p.W * segs);
-  SegSum* sum_out = ws.sums + blockIdx.x;
-  unsigned long long* list = ws.list + (int64_t)blockIdx.x * K;
+  SegSum* sum_out = ws.sums + (int64_t)row * segs + seg;
+  unsigned long long* list = ws.list + ((int64_t)row * segs + seg) * K;
   const float score = p.scores[row];
   if (!(fabsf(score) <= 3.402823466e38f) || (p.finished != nullptr && p.finished[row] != 0)) {
     if (tid == 0) *sum_out = SegSum{-INFINITY, 0, 0.0};
     return;
   }
-  const T* x = static_cast<const T*>(p.logits) + (int64_t)(row / p.W) * p.batch_stride +
-               (int64_t)(row % p.W) * p.beam_stride;
+  const T* x = static_cast<const T*>(p.logits) + blockIdx.z * p.batch_stride + blockIdx.y * p.beam_stride;
   const int v0 = min((int64_t)p.V, (int64_t)seg * seg_len), v1 = (int)min((int64_t)p.V, (int64_t)v0 + seg_len);
-  if (tid == 0) count = 0;
+  if (tid == 0) count = few_count = 0;
   // The row's 16-byte boundaries: logits before the first and behind the last go one by one.
   const int mis = (int)((reinterpret_cast<uintptr_t>(x + v0) & 15u) / sizeof(T));
   const int head = min(v1 - v0, mis ? V::N - mis : 0);
   const int vecs = (v1 - v0 - head) / V::N;
   const int tail0 = v0 + head + vecs * V::N;
   const T* body = x + v0 + head;
-  float m = -INFINITY, sum = 0.0f, ref = 0.0f;  // ref = m log2(e), 0 while m is -inf
-  float floor_ = -INFINITY;                     // logits below it are not among the segment's K
-  auto add = [&](float y) { sum += ex2(fmaf(y, kLog2e, -ref)); };
-  auto raise = [&](float top) {
-    if (top > m) {
-      const float r = top * kLog2e;
-      sum *= m == -INFINITY ? 1.0f : ex2(ref - r);  // (a sum of NaN stays one)
-      m = top;
-      ref = r;
+  float top = -INFINITY;               // this thread's largest logit
+  float ref = -INFINITY, sum = 0.0f;   // its sum of 2^(H x - ref)
+  float use = 0.0f;                    // ref, or 0 while that is -inf
+  float floor_ = -INFINITY;            // logits below it are not among the segment's K
+  auto add = [&](float y) { sum += ex2(fmaf(y, kH, -use)); };
+  auto raise = [&](float y) {
+    if (y > top) {
+      top = y;
+      const float r = ceilf(y * kH);
+      if (r > ref) {
+        if (ref != -INFINITY) sum *= ex2(ref - r);  // (a sum of NaN stays one)
+        ref = use = r;
+      }
     }
   };
+  // A logit that reaches the floor, to be ranked.
   auto put = [&](float y, int v) {
     if (y >= floor_ && y > -INFINITY) {
-      const int at = atomicAdd(&count, 1);
-      if (at < kRoom) aside[at] = entry(y, (uint32_t)v);
+      const int at = atomicAdd(&few_count, 1);
+      if (at < kRanked) few[at] = entry(y, (uint32_t)v);
     }
   };
   __syncthreads();
-  for (int base = 0; base < vecs; base += kThreads * kUnroll) {
-    V r[kUnroll];
+  int next_floor = 1, since = 0;  // chunks after which the floor is taken, and since it was
+  constexpr int kChunk = kThreads * kUnroll;
+  V r[kUnroll], ahead[kUnroll];
+  auto load = [&](int base, bool whole) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = base + u * kThreads + tid;
-      if (i < vecs) r[u].load(body + (int64_t)i * V::N);
+      if (whole || i < vecs) ahead[u].load(body + (int64_t)i * V::N);
     }
-    float tops[kUnroll];
+  };
+  int chunk = 1;
+  auto work = [&](int base, bool whole) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) r[u] = ahead[u];
+    if (base + 2 * kChunk <= vecs) load(base + kChunk, true);
+    else load(base + kChunk, false);
+    float tops[kUnroll], most = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      tops[u] = -INFINITY;
-      if (base + u * kThreads + tid >= vecs) continue;
+      tops[u] = whole || base + u * kThreads + tid < vecs ? r[u].top() : -INFINITY;
+      most = fmaxf(most, tops[u]);
+    }
+    raise(most);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (!whole && base + u * kThreads + tid >= vecs) continue;
       float y[V::N];
       r[u].get(y);
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) tops[u] = fmaxf(tops[u], y[e]);
-      raise(tops[u]);
 #pragma unroll
       for (int e = 0; e < V::N; ++e) add(y[e]);
     }
-    if (floor_ == -INFINITY) {  // the same in all threads
-      float t = -INFINITY;
+    if (chunk == next_floor || floor_ == -INFINITY) {  // the same in all threads
+      floor_ = common_floor(top, K, tops_of);
+      if (chunk == next_floor) next_floor *= 8;
+      since = 0;
+    }
+    if (most >= floor_ && most > -INFINITY) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) t = fmaxf(t, tops[u]);
-      // The warp's maxima in falling order over the lanes.
-#pragma unroll
-      for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j > 0; j >>= 1) {
-          const float o = __shfl_xor_sync(0xffffffffu, t, j);
-          const bool larger = ((lane & k) == 0) == ((lane & j) == 0);
-          t = larger ? fmaxf(t, o) : fminf(t, o);
+      for (int u = 0; u < kUnroll; ++u)
+        if (tops[u] >= floor_ && tops[u] > -INFINITY) {
+          const int at = atomicAdd(&count, 1);
+          if (at < kAside) {
+            aside[at] = r[u].bits();
+            aside_at[at] = base + u * kThreads + tid;
+          }
         }
-      t = __shfl_sync(0xffffffffu, t, (K + kWarps - 1) / kWarps - 1);
-      if (lane == 0) bound[warp] = t;
-      __syncthreads();
-      t = bound[0];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) t = fminf(t, bound[w]);
-      floor_ = t;
-      __syncthreads();  // `bound` may be written again
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * kThreads + tid;
-      if (i >= vecs || tops[u] < floor_ || tops[u] == -INFINITY) continue;
-      float y[V::N];
-      r[u].get(y);
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) put(y[e], v0 + head + i * V::N + e);
-    }
-  }
-  if (tid < head + (v1 - tail0)) {  // fewer than 16 of them
-    const int v = tid < head ? v0 + tid : tail0 + tid - head;
-    const float y = attn::to_f(x[v]);
-    raise(y);
-    add(y);
-    put(y, v);
+    ++chunk;
+    ++since;
+  };
+  load(0, false);
+  int base = 0;
+  for (; base + kChunk <= vecs; base += kChunk) work(base, true);
+  if (base < vecs) work(base, false);
+  const bool ragged = tid < head + (v1 - tail0);  // fewer than 16 of them
+  const int ragged_v = tid < head ? v0 + tid : tail0 + tid - head;
+  const float ragged_y = ragged ? attn::to_f(x[ragged_v]) : -INFINITY;
+  if (ragged) {
+    raise(ragged_y);
+    add(ragged_y);
   }
   // The threads' sums.
-  float top = m;
+  float most = ref;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) wm[warp] = top;
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (lane == 0) wref[warp] = most;
+  if (since > 1) floor_ = common_floor(top, K, tops_of);
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, wm[w]);
-  double d = m == -INFINITY ? (double)sum : (double)(sum * ex2(ref - top * kLog2e));
+  for (int w = 0; w < kWarps; ++w) most = fmaxf(most, wref[w]);
+  double d = (double)(ref == -INFINITY ? sum : sum * ex2(ref - most));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   if (lane == 0) wsum[warp] = d;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) d += wsum[w];
-    *sum_out = SegSum{top, min(count, K), d};
+  const int n = count;
+  for (int i = tid; i < min(n, kAside); i += kThreads) {
+    V v;
+    v.from(aside[i]);
+    if (v.top() < floor_) continue;
+    float y[V::N];
+    v.get(y);
+#pragma unroll
+    for (int e = 0; e < V::N; ++e) put(y[e], v0 + head + aside_at[i] * V::N + e);
   }
-  if (count <= kRoom) {
-    sort_falling(aside, count);
-    for (int i = tid; i < min(count, K); i += kThreads) list[i] = aside[i];
+  if (ragged) put(ragged_y, ragged_v);
+  __syncthreads();
+  const int c = few_count;
+  const bool all_there = n <= kAside && c <= kRanked;  // then at least K, or all above -inf
+  if (tid == 0)
+    for (int w = 1; w < kWarps; ++w) d += wsum[w];
+  if (all_there) {
+    if (tid == 0) *sum_out = SegSum{most, min(c, K), d};
+    for (int k = tid; k < c; k += kThreads) {
+      const unsigned long long mine = few[k];
+      int rank = 0;
+#pragma unroll 4
+      for (int i = 0; i < c; ++i) rank += few[i] > mine;
+      if (rank < K) list[rank] = mine;
+    }
     return;
   }
   // Too many: place after place, the largest entry below the last one.
   unsigned long long last = ~0ull;
-  for (int k = 0; k < K; ++k) {
+  int places = 0;
+  for (; places < K; ++places) {
     unsigned long long mine = 0;
     for (int v = v0 + tid; v < v1; v += kThreads) {
       const float y = attn::to_f(x[v]);
@@ -277,10 +333,12 @@ __global__ void __launch_bounds__(kThreads, 6) beam_rows_kernel(const __grid_con
     if (lane == 0) best[warp] = mine;
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) mine = best[w] > mine ? best[w] : mine;
+    if (mine == 0) break;  // no more
     last = mine;
-    if (tid == 0) list[k] = mine;
+    if (tid == 0) list[places] = mine;
     __syncthreads();
   }
+  if (tid == 0) *sum_out = SegSum{most, places, d};
 }
 
 // Sorts scores and their indices in falling order of score, rising of index.
@@ -314,46 +372,101 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
   __shared__ unsigned long long key[kRoom];
   __shared__ uint32_t index[kRoom];
   __shared__ double base[kBeamMaxW];  // score - log sum of each beam; NaN: takes no part
+  __shared__ float base_f[kBeamMaxW];
+  __shared__ int counts[kBeamMaxW * kMaxSegs];
+  __shared__ float least;
   __shared__ int count;
-  const int tid = threadIdx.x, b = blockIdx.x, K = p.K;
+  const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x, K = p.K;
   const int lists = p.W * segs;  // at most kRoom
+  attn::start_next_kernel();
   attn::wait_for_previous_kernel();
   const Ws ws = carve(p.ws, (int64_t)p.B * lists);
   const SegSum* sums = ws.sums + (int64_t)b * lists;
   const unsigned long long* list = ws.list + (int64_t)b * lists * K;
-  for (int w = tid; w < p.W; w += kThreads) {
-    const double score = p.scores[(int64_t)b * p.W + w];
-    float top = -INFINITY;
-    for (int s = 0; s < segs; ++s) top = fmaxf(top, sums[w * segs + s].m);
-    double total = 0.0;
-    for (int s = 0; s < segs; ++s) {
-      const SegSum x = sums[w * segs + s];
-      total += x.m == -INFINITY ? x.sum : x.sum * exp((double)x.m - (double)top);
+  if (tid == 0) count = 0;
+  // Few entries are on their way while the sums are joined: a warp's lists, a lane per entry
+  // (no division in the way; each would be a sixth of the time of all else).
+  const int all = lists * K, warp = tid >> 5;
+  constexpr int kAhead = 4;
+  const bool ahead = lists <= kAhead * kWarps && K <= 32;
+  unsigned long long entries[kAhead];
+  if (ahead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int l = warp * kAhead + u;
+      entries[u] = l < lists && lane < K ? list[l * K + lane] : 0;
     }
-    // Nothing in the row, an infinity or a NaN: no score of it is finite.
-    base[w] = score - ((double)top + log(total));
+  }
+  for (int w = tid >> 5; w < p.W; w += kWarps) {  // a warp per beam, a lane per segment
+    SegSum x{-INFINITY, 0, 0.0};
+    if (lane < segs) {
+      x = sums[w * segs + lane];
+      counts[w * segs + lane] = x.count;
+    }
+    float most = x.ref;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    // 2^(ref - most) from its bits; 0 from 2^-1023 on.
+    const float e = x.ref - most + 1023.0f;
+    double total = x.ref == -INFINITY ? x.sum : x.sum * __longlong_as_double(e > 0.0f ? (long long)e << 52 : 0);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) {
+      base[w] = total;
+      base_f[w] = most;
+    }
   }
   __syncthreads();
-  auto score_of = [&](int l, unsigned long long e) -> unsigned long long {
-    const double s = base[l / segs] + (double)value_of((uint32_t)(e >> 32));
+  // A lane per beam: f64 instructions of a warp take as long for one lane as for 32.
+  if (tid < p.W) {
+    // Nothing in the row, an infinity or a NaN: no score of it is finite.
+    const double x = (double)p.scores[(int64_t)b * p.W + tid] -
+                     ((double)base_f[tid] * (1.0 / (double)kH) + log(base[tid]));
+    base[tid] = x;
+    base_f[tid] = (float)x;
+  }
+  __syncthreads();
+  auto score_of = [&](int w, unsigned long long e) -> unsigned long long {
+    const double s = base[w] + (double)value_of((uint32_t)(e >> 32));
     return s - s == 0.0 ? order_of(s) : 0ull;
   };
-  // The K-th best head of a list is a score that K entries reach.
-  unsigned long long floor_ = 0;
-  if (lists >= K) {
-    for (int l = tid; l < lists; l += kThreads) {
-      key[l] = sums[l].count > 0 ? score_of(l, list[(int64_t)l * K]) : 0ull;
-      index[l] = (uint32_t)l;
+  // In f32, to within 2^-22 (|base| + |s|); NaN: none.
+  auto near_score = [&](int w, unsigned long long e) {
+    const float s = base_f[w] + value_of((uint32_t)(e >> 32));
+    return s - s == 0.0f ? s : __int_as_float(0x7fffffff);
+  };
+  // The K-th best head of a list is a score that K entries reach.  It is found in f32, and
+  // entries that do not come near it are left out before any f64 arithmetic.
+  float floor_ = -INFINITY;
+  if (lists >= K && lists <= kThreads) {
+    float* heads = reinterpret_cast<float*>(key);
+    const float none = __int_as_float(0x7fffffff);
+    if (ahead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int l = warp * kAhead + u;
+        if (lane == 0 && l < lists) heads[l] = counts[l] > 0 ? near_score(l / segs, entries[u]) : none;
+      }
+    } else if (tid < lists) {
+      heads[tid] = counts[tid] > 0 ? near_score(tid / segs, list[(int64_t)tid * K]) : none;
     }
-    sort_scores(key, index, lists);
-    floor_ = key[K - 1];
+    if (tid == 0) least = -INFINITY;
+    __syncthreads();
+    if (tid < lists) {
+      const float mine = heads[tid];
+      int rank = 0;  // equal heads by their number
+#pragma unroll 8
+      for (int i = 0; i < lists; ++i) rank += heads[i] > mine || (heads[i] == mine && i < tid);
+      if (rank == K - 1 && mine == mine) least = mine;
+    }
+    __syncthreads();
+    floor_ = least;
+    float big = fabsf(floor_);
+    for (int w = 0; w < p.W; ++w) big = fmaxf(big, fabsf(base_f[w]));  // (a NaN is passed over)
+    floor_ -= big * 0x1p-20f;  // -inf stays
+    __syncthreads();  // `key` is written again
   }
-  __syncthreads();
-  int kept = 0;
-  const int64_t all = (int64_t)lists * K;
   // Beams that ended come first: one entry each.
-  if (tid == 0) count = 0;
-  __syncthreads();
   for (int w = tid; w < p.W; w += kThreads) {
     const float s = p.scores[(int64_t)b * p.W + w];
     if (p.finished != nullptr && p.finished[(int64_t)b * p.W + w] != 0 && fabsf(s) <= 3.402823466e38f) {
@@ -362,44 +475,77 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
       index[at] = (uint32_t)(w * p.V + p.pad);
     }
   }
-  __syncthreads();
-  kept = count;
-  const int room = kRoom - kBeamMaxK;  // new ones of a pass; W <= kBeamMaxW <= kBeamMaxK
-  for (int64_t at0 = 0; at0 < all; at0 += room) {
-    for (int64_t i = at0 + tid; i < min(all, at0 + room); i += kThreads) {
-      const int l = (int)(i / K), k = (int)(i % K);
-      if (k >= sums[l].count) continue;
-      const unsigned long long e = list[i], s = score_of(l, e);
-      if (s != 0 && s >= floor_) {
-        const int at = atomicAdd(&count, 1);
-        key[at] = s;
-        index[at] = (uint32_t)(l / segs * p.V) + ~(uint32_t)e;
-      }
+  auto take = [&](int w, unsigned long long e) {
+    if (!(near_score(w, e) >= floor_)) return;
+    const unsigned long long s = score_of(w, e);
+    if (s != 0) {
+      const int at = atomicAdd(&count, 1);
+      key[at] = s;
+      index[at] = (uint32_t)(w * p.V) + ~(uint32_t)e;
+    }
+  };
+  auto write = [&](int k, unsigned long long s, uint32_t at) {
+    const int64_t to = (int64_t)b * K + k;
+    p.parents[to] = (int32_t)(at / (uint32_t)p.V);
+    p.tokens[to] = (int32_t)(at % (uint32_t)p.V);
+    p.out_scores[to] = (float)value_of(s);
+  };
+  int kept;
+  if (ahead) {  // at most 32 x 32 + W entries
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int l = warp * kAhead + u;
+      if (l < lists && lane < counts[l]) take(l / segs, entries[u]);
     }
     __syncthreads();
     const int n = count;
-    if (n > kept || at0 == 0) {
+    kept = min(n, K);
+    if (n <= kThreads) {  // by counting
+      if (tid < n) {
+        const unsigned long long mine = key[tid];
+        const uint32_t at = index[tid];
+        int rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) rank += key[i] > mine || (key[i] == mine && index[i] < at);
+        if (rank < K) write(rank, mine, at);
+      }
+    } else {
       sort_scores(key, index, n);
-      kept = min(n, K);
+      for (int k = tid; k < kept; k += kThreads) write(k, key[k], index[k]);
     }
+  } else {
     __syncthreads();
-    if (tid == 0) count = kept;
-    __syncthreads();
+    kept = count;
+    const int room = kRoom - kBeamMaxK;  // new ones of a pass; W <= kBeamMaxW <= kBeamMaxK
+    for (int at0 = 0; at0 < all; at0 += room) {
+      for (int i = at0 + tid; i < min(all, at0 + room); i += kThreads) {
+        const int l = i / K;
+        if (i - l * K < counts[l]) take(l / segs, list[i]);
+      }
+      __syncthreads();
+      const int n = count;
+      if (n > kept || at0 == 0) {
+        sort_scores(key, index, n);
+        kept = min(n, K);
+      }
+      __syncthreads();
+      if (tid == 0) count = kept;
+      __syncthreads();
+    }
+    for (int k = tid; k < kept; k += kThreads) write(k, key[k], index[k]);
   }
-  for (int k = tid; k < K; k += kThreads) {
-    const bool some = k < kept;
+  for (int k = kept + tid; k < K; k += kThreads) {
     const int64_t to = (int64_t)b * K + k;
-    p.parents[to] = some ? (int32_t)(index[k] / (uint32_t)p.V) : -1;
-    p.tokens[to] = some ? (int32_t)(index[k] % (uint32_t)p.V) : -1;
-    p.out_scores[to] = some ? (float)value_of(key[k]) : -INFINITY;
+    p.parents[to] = p.tokens[to] = -1;
+    p.out_scores[to] = -INFINITY;
   }
 }
 
-// Segments of a row.  Twenty-four CTAs for each SM (six at a time) even out, while a
-// segment of fewer than 4096 logits spends its time on the sorts; the sums depend on the
-// sizes alone.
+// Segments of a row.  Twelve CTAs for each SM (four at a time) even out, while a segment of
+// fewer than 4096 logits spends its time on the selection; the sums depend on the sizes
+// alone.
 int segments(int64_t rows, int64_t V) {
-  const int64_t want = (24 * 152 + rows - 1) / rows, most = (V + 4095) / 4096;
+  const int64_t want = (12 * 152 + rows - 1) / rows, most = (V + 4095) / 4096;
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, kMaxSegs}));
 }
 
@@ -415,13 +561,11 @@ cudaError_t launch_beam(const BeamLaunch& p, cudaStream_t st) {
   const int segs = segments(rows, p.V);
   // Whole vectors, so that only a row's own ends are ragged.
   const int seg_len = ((p.V + segs - 1) / segs + 7) & ~7;
-  const unsigned grid = (unsigned)(rows * segs);
-  if (p.bf16)
-    beam_rows_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p, segs, seg_len);
-  else
-    beam_rows_kernel<float><<<grid, kThreads, 0, st>>>(p, segs, seg_len);
-  note_launch();
-  cudaError_t e = cudaGetLastError();
+  const dim3 grid((unsigned)segs, (unsigned)p.W, (unsigned)p.B);
+  // (Both launches are prepared while the kernel before them still runs.)
+  const cudaError_t e =
+      p.bf16 ? attn::launch_after(beam_rows_kernel<__nv_bfloat16>, grid, kThreads, st, p, seg_len)
+             : attn::launch_after(beam_rows_kernel<float>, grid, kThreads, st, p, seg_len);
   if (e != cudaSuccess) return e;
   return attn::launch_after(beam_join_kernel, dim3((unsigned)p.B), kThreads, st, p, segs);
 }

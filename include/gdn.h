@@ -869,12 +869,13 @@ size_t gdn_attn8_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t
  * continuation, (w, pad_token) with s = scores[b, w]; its logits are not read.  Only a
  * finite s is chosen: a logit of -inf is a token that may not come, a score of -inf a
  * beam without a life, and a row that holds a NaN or +inf, or nothing but -inf, offers
- * nothing.  Places left over get parent -1, token -1, s = -inf.
+ * nothing (a logit of 2^127 or more counts as +inf).  Places left over get parent -1,
+ * token -1, s = -inf.
  * Exponentials and a thread's sums are f32, sums between threads, the logarithm and s
  * are f64; s is rounded to f32 where it is stored.  (Logits so small that s does not
  * show their difference in f64 are ordered by the logit, not the index.)
  * out_scores may be scores itself where K = W; otherwise outputs overlap nothing.
- * K <= 128, W <= 64, W * V < 2^31.  The workspace is 256-byte aligned, of any contents. */
+ * K <= 128, W <= 64, B <= 65535, W * V < 2^31.  The workspace is 256-byte aligned, of any contents. */
 typedef struct gdn_beam_select_args {
   int64_t B, W, V, K;
   int32_t dtype;             /* gdn_dtype of the logits */
