@@ -19,8 +19,10 @@
 // Warps:  0       TMA loads of K and V, a ring of tiles of 128 keys each
 //         1       the MMAs
 //         2       the ranges of key tiles, handed to the other roles
-//         3       TMEM; the stream form's bookkeeping
-//         4 ..    softmax and output: a group of 4 warps for each 16 rows of q.  A thread has
+//         3       TMEM; the scales, four tiles at a time, a ring of eight; the stream form's
+//                 bookkeeping
+//         4 ..    softmax and output: a group of 4 warps for each 16 rows of q (or
+//                 the 8 of a kernel of its own).  A thread has
 //                 one key of the tile, so that a row's maximum is one transposing butterfly
 //                 over the lanes and one exchange between the four warps.
 // Two S and two P buffers: the scores of a tile are computed during the softmax of the one
@@ -48,7 +50,7 @@ namespace {
 using namespace attn;
 using bf16 = __nv_bfloat16;
 
-constexpr int kMaxRing = 8, kSegs = 4, kMaxGroups = 4;
+constexpr int kMaxRing = 8, kSegs = 4, kMaxGroups = 4, kScaleRing = 8;
 constexpr float kHeadroom = 4.0f;       // log2: p reaches 2^4 before the reference follows
 constexpr float kPScale = 16.0f;        // p 2^4 in the parts' units: at most 256 of 448
 constexpr float kLoScale = 32.0f;
@@ -58,6 +60,7 @@ struct Shared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t q_full, s_full[2], p_full[2], pv[2], o_full, o_empty, end;
   uint64_t meet[kMaxGroups];
+  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Seg seg[kSegs];
   uint32_t tmem;
@@ -65,9 +68,10 @@ struct Shared {
   int redone;  // rows evaluated again so far, and parts of them
   uint32_t k_loads[kMaxRing], v_loads[kMaxRing];  // issued so far
   int start_s, start_hkv, start_u;
-  long long left;
+  long long left, total;
   long long scan[20];
   uint32_t redo[kMaxGroups][2];                      // rows to evaluate again, by range parity
+  float2 scales[kScaleRing][8];                      // of K and V, for each 16 keys of a tile
   alignas(16) float qscale[kMaxGroups][16];
   alignas(16) int last[kMaxGroups][16];              // a row's last visible key
   alignas(16) float top[kMaxGroups][2][4][16];       // the warps' maxima (sums at the end)
@@ -76,18 +80,20 @@ struct Shared {
 
 template <int D, int R>
 struct Cfg {
-  static constexpr int N = 2 * R;                      // columns: hi and lo of each row
+  static constexpr int RG = R < 16 ? R : 16;           // rows of a softmax group
+  static constexpr int N = R < 16 ? 32 : 2 * R;        // columns: hi and lo of each row (R = 8:
+                                                       // 16 more that nothing looks at)
   static constexpr int kRowBytes = D < 128 ? D : 128;  // of a swizzled row of K, V and q
   static constexpr int NB = D / kRowBytes;             // blocks of them
   static constexpr uint32_t kTile = 128 * D;           // of K, of V
   static constexpr uint32_t kQ = N * D, kP = 128 * N;
-  static constexpr int kCtas = D <= 128 && R == 16 ? 2 : 1;  // per SM
+  static constexpr int kCtas = D <= 128 && R <= 16 ? 2 : 1;  // per SM
   static constexpr uint32_t kRoom = kCtas == 2 ? 115712 : 232448;
   static constexpr int kFit = (int)((kRoom - sizeof(Shared) - kQ - 2 * kP) / (2 * kTile));
   static constexpr int ST = kFit > kMaxRing ? kMaxRing : kFit;
   static constexpr uint32_t kV = ST * kTile, kQAt = 2 * ST * kTile, kPAt = kQAt + kQ, kBars = kPAt + 2 * kP;
   static constexpr uint32_t kBytes = kBars + sizeof(Shared);
-  static constexpr int kGroups = R / 16;
+  static constexpr int kGroups = R / RG;
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int OB = D == 256 ? 2 : 1;          // blocks of 128 dims of O^T
   static constexpr uint32_t kTO = 2 * N;               // TMEM column of O^T
@@ -129,12 +135,12 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// Maximum or sum over the warp of each of 16 values: lane i is left with that of value
-// i % 16.  Each step halves the values a lane keeps.
-template <bool SUM>
-__device__ __forceinline__ float across(float (&v)[16], int lane) {
+// Maximum or sum over the warp of each of RG values: lane i is left with that of value
+// i % RG.  Each step halves the values a lane keeps.
+template <bool SUM, int RG>
+__device__ __forceinline__ float across(float (&v)[RG], int lane) {
 #pragma unroll
-  for (int w = 8; w > 0; w >>= 1) {
+  for (int w = RG / 2; w > 0; w >>= 1) {
     const bool up = lane & w;
 #pragma unroll
     for (int i = 0; i < w; ++i) {
@@ -143,21 +149,46 @@ __device__ __forceinline__ float across(float (&v)[16], int lane) {
       v[i] = SUM ? keep + got : fmaxf(keep, got);
     }
   }
-  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
-  return SUM ? v[0] + got : fmaxf(v[0], got);
-}
-__device__ __forceinline__ void read16(const float* from, float (&x)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int w = RG; w < 32; w <<= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, v[0], w);
+    v[0] = SUM ? v[0] + got : fmaxf(v[0], got);
+  }
+  return v[0];
+}
+template <int RG>
+__device__ __forceinline__ void read_rows(const float* from, float (&x)[RG]) {
+#pragma unroll
+  for (int i = 0; i < RG / 4; ++i) {
     const float4 v = reinterpret_cast<const float4*>(from)[i];
     x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
   }
 }
-// The parts of a pair of values.
+// 2 RG columns of a lane: hi, then lo of each row.
+template <int RG>
+__device__ __forceinline__ void load_parts(uint32_t from, float (&y)[2 * RG]) {
+  if constexpr (RG == 16) tmem_ld32(from, y);
+  else tmem_ld16(from, y);
+  tmem_ld_wait();
+}
+// The parts of a pair of values.  Between them in f16, whose 11 bits hold the two parts' 8
+// (and all of a bf16's): six instructions, where f32 takes nine.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = f_to_e4x2(a, b);
-  const float2 h = e4x2_to_f(hi);
-  lo = f_to_e4x2((a - h.x) * kLoScale, (b - h.y) * kLoScale);
+  const __half2 x = __floats2half2_rn(a, b);
+  uint32_t back;
+  asm("{\n\t.reg .b16 c;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 c, %2;\n\t"
+      "cvt.u32.u16 %0, c;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, c;\n\t}\n"
+      : "=r"(hi), "=r"(back)
+      : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  const __half2 rest =
+      __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(kLoScale));
+  asm("{\n\t.reg .b16 c;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 c, %1;\n\t"
+      "cvt.u32.u16 %0, c;\n\t}\n"
+      : "=r"(lo)
+      : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
 }
 
 #define WAIT(bar, parity) \
@@ -168,7 +199,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     attn8_tc_kernel(const __grid_constant__ AttnLaunch p, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ Tc8Args a) {
   using C = Cfg<D, R>;
-  constexpr int N = C::N, ST = C::ST, ROW = C::kRowBytes, NB = C::NB;
+  constexpr int N = C::N, ST = C::ST, ROW = C::kRowBytes, NB = C::NB, RG = C::RG;
   extern __shared__ __align__(1024) unsigned char smem[];
   Shared* sh = reinterpret_cast<Shared*>(smem + C::kBars);
   const uint32_t sk = smem_u32(smem), sv = sk + C::kV, sq = sk + C::kQAt, sp = sk + C::kPAt;
@@ -200,7 +231,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       }
       for (int i = 0; i < kSegs; ++i) {
         mbar_init(smem_u32(&sh->seg_full[i]), 1);
-        mbar_init(smem_u32(&sh->seg_empty[i]), 2 + 4 * C::kGroups);
+        mbar_init(smem_u32(&sh->seg_empty[i]), 3 + 4 * C::kGroups);
+      }
+      for (int i = 0; i < kScaleRing; ++i) {
+        mbar_init(smem_u32(&sh->sc_full[i]), 1);
+        mbar_init(smem_u32(&sh->sc_empty[i]), 4 * C::kGroups);
       }
       sh->abort = sh->redone = 0;
       fence_mbar_init();
@@ -363,7 +398,38 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     };
     role();
   } else if (warp == 3) {
-    if (lane == 0) a.info[blockIdx.x] = stream_info(p, sh);
+    // ---- scales ----
+    // Lane 8 t + i: of keys 16 i .. 16 i + 15 of the t-th of four tiles.  Loaded by the
+    // threads that use them, a tile ahead, they came too late under load (decode of 256
+    // sequences: 371 us) and cost each thread their addresses.
+    auto role = [&] {
+      uint32_t nk = 0;  // tiles before these
+      Seg g;
+      while (next_seg(g)) {
+        for (int kt = g.kt0; kt < g.kt1; kt += 4) {
+          const int tiles = min(4, g.kt1 - kt), t = lane >> 3, j = (kt + t) * BK + (lane & 7) * 16;
+          float2 x = make_float2(0.0f, 0.0f);
+          if (t < tiles && j < g.hi) {
+            const int pi = j / p.page_size;
+            const int64_t pg = page_of(p, g.s, pi);  // (raised by the loads)
+            if (pg >= 0) {
+              const int64_t at = scale_at(p.Hkv, p.page_size, p.block, pg, g.hkv, j - pi * p.page_size);
+              x = make_float2(p.ks[at], p.vs[at]);
+            }
+          }
+          for (int i = 0; i < tiles; ++i) {
+            const uint32_t n = nk + i, at = n % kScaleRing;
+            if (n >= kScaleRing) WAIT(sh->sc_empty[at], (n / kScaleRing - 1) & 1);
+            if (t == i) sh->scales[at][lane & 7] = x;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh->sc_full[at]));
+          }
+          nk += tiles;
+        }
+      }
+    };
+    role();
+    if (lane == 0) a.info[blockIdx.x] = stream_info(p, a.ctas, sh);
     // Sequences without a key.
     for (int s = blockIdx.x; s < p.N; s += a.ctas) {
       const SeqRange q = seq_range(p, s);
@@ -377,7 +443,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     const int gr = (warp - 4) >> 2, w4 = warp & 3;
     const int r = tid & 127;                       // key of the tile, dim of O, lane of TMEM
     const uint32_t lanes = (uint32_t)w4 << 21;     // (32 * w4) << 16
-    const uint32_t ts = tmem + lanes + 32 * gr;
+    const uint32_t ts = tmem + lanes + 2 * RG * gr;
     auto role = [&] {
       uint32_t nk = 0, met = 0;
       int seg_n = 0;
@@ -392,26 +458,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       Seg g;
       while (next_seg(g)) {
         const int rows = g.nt * G;  // of q
-        // The pages and scales of this thread's key, two and one tile ahead.
-        auto page_at = [&](int kt) -> int64_t {
-          const int j = kt * BK + r;
-          return kt < g.kt1 && j < g.hi ? page_of(p, g.s, j / p.page_size) : -1;
-        };
-        auto scales_at = [&](int kt, int64_t pg, float& k, float& v) {
-          k = v = 0.0f;
-          if (pg < 0) return;
-          const int64_t at = scale_at(p.Hkv, p.page_size, p.block, pg, g.hkv, (kt * BK + r) % p.page_size);
-          k = p.ks[at];
-          v = p.vs[at];
-        };
-        float next_k, next_v;
-        scales_at(g.kt0, page_at(g.kt0), next_k, next_v);
-        int64_t next_page = page_at(g.kt0 + 1);
         {
-          // q of the group's rows: 8 threads each.  All its products with the range before
-          // are done: their scores have been read.
-          const int i = r >> 3, part = r & 7, row = gr * 16 + i;
-          constexpr int E = D / 8;  // dims of a thread
+          // q of the group's rows.  All its products with the range before are done: their
+          // scores have been read.
+          constexpr int kPer = 128 / RG, E = D / kPer;  // threads of a row, dims of a thread
+          const int i = r / kPer, part = r % kPer, row = gr * RG + i;
           float x[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) x[e] = 0.0f;
@@ -419,21 +470,19 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             const bf16* from = static_cast<const bf16*>(p.q.p) + (int64_t)(g.t0 + row / G) * p.q.ts +
                                (int64_t)(g.hkv * G + row % G) * p.q.hs + part * E;
 #pragma unroll
-            for (int e = 0; e < E; e += 8) {
-              const uint4 v = *reinterpret_cast<const uint4*>(from + e);
-              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                x[e + 2 * k] = __uint_as_float(u[k] << 16);
-                x[e + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-              }
+            for (int e = 0; e < E; e += 4) {
+              const uint2 v = *reinterpret_cast<const uint2*>(from + e);
+              x[e] = __uint_as_float(v.x << 16);
+              x[e + 1] = __uint_as_float(v.x & 0xffff0000u);
+              x[e + 2] = __uint_as_float(v.y << 16);
+              x[e + 3] = __uint_as_float(v.y & 0xffff0000u);
             }
           }
           float big = 0.0f;
 #pragma unroll
           for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(x[e]));
 #pragma unroll
-          for (int o = 4; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+          for (int o = kPer / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
           // 2^e that brings the largest into [128, 256).
           const int ex = max(-126, min(126, 134 - (int)(__float_as_uint(big) >> 23)));
           const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
@@ -453,49 +502,47 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           }
           auto put = [&](uint32_t n, const uint32_t(&c)[E / 4]) {
 #pragma unroll
-            for (int e = 0; e < E; e += 16) {
+            for (int e = 0; e < E; e += 4) {
               const int d = part * E + e, b = d / ROW, in = d % ROW;
-              unsigned char* to = smem + C::kQAt + b * N * ROW + n * ROW + swz<ROW>(n, in >> 4) * 16 + (in & 15);
-              if constexpr (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
-              else
-                *reinterpret_cast<uint4*>(to) = make_uint4(c[e / 4], c[e / 4 + 1], c[e / 4 + 2], c[e / 4 + 3]);
+              *reinterpret_cast<uint32_t*>(smem + C::kQAt + b * N * ROW + n * ROW + swz<ROW>(n, in >> 4) * 16 +
+                                           (in & 15)) = c[e / 4];
             }
           };
-          put(32 * gr + i, hi);
-          put(32 * gr + 16 + i, lo);
+          put(2 * RG * gr + i, hi);
+          put(2 * RG * gr + RG + i, lo);
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
         }
         if (!meet()) return;  // qscale, last
-        float l[16], m = -INFINITY;  // l of this thread's keys; m of row lane % 16
+        float l[RG], m = -INFINITY;  // l of this thread's keys; m of row lane % RG
 #pragma unroll
-        for (int i = 0; i < 16; ++i) l[i] = 0.0f;
+        for (int i = 0; i < RG; ++i) l[i] = 0.0f;
         for (int kt = g.kt0; kt < g.kt1; ++kt, ++nk, vr.step()) {
           const uint32_t buf = nk & 1;
-          const float ksc = next_k, vsc = next_v;
-          scales_at(kt + 1, next_page, next_k, next_v);
-          next_page = page_at(kt + 2);
+          const uint32_t sc = nk % kScaleRing;
+          WAIT(sh->sc_full[sc], (nk / kScaleRing) & 1);
+          const float2 scale = sh->scales[sc][r >> 4];
+          const float ksc = scale.x, vsc = scale.y;
           // (a scale of nothing, 0, has no logarithm: 2^-64 stands for smaller ones)
           const float lv = fmaxf(__log2f(fabsf(vsc)), -64.0f);
           const int j = kt * BK + r;
           const bool masked = kt * BK + BK - 1 > g.pos0;
-          float s[16];
+          float s[RG];
           {
-            float qs[16];
-            read16(sh->qscale[gr], qs);
+            float qs[RG];
+            read_rows<RG>(sh->qscale[gr], qs);
             WAIT(sh->s_full[buf], (nk >> 1) & 1);
             fence_after_sync();
-            float y[32];
-            tmem_ld32(ts + buf * N, y);
-            tmem_ld_wait();
+            float y[2 * RG];
+            load_parts<RG>(ts + buf * N, y);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = fmaf(y[16 + i], 1.0f / kLoScale, y[i]) * (ksc * qs[i]);
+            for (int i = 0; i < RG; ++i) s[i] = fmaf(y[RG + i], 1.0f / kLoScale, y[i]) * (ksc * qs[i]);
           }
           if (masked) {
             const int4* last = reinterpret_cast<const int4*>(sh->last[gr]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RG / 4; ++i) {
               const int4 v = last[i];
               s[4 * i] = j <= v.x ? s[4 * i] : -INFINITY;
               s[4 * i + 1] = j <= v.y ? s[4 * i + 1] : -INFINITY;
@@ -504,58 +551,59 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             }
           }
           {
-            float t[16];
+            float t[RG];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) t[i] = s[i] + lv;
-            const float mine = across<false>(t, lane);
-            if (lane < 16) sh->top[gr][buf][w4][lane] = mine;
+            for (int i = 0; i < RG; ++i) t[i] = s[i] + lv;
+            const float mine = across<false, RG>(t, lane);
+            if (lane < RG) sh->top[gr][buf][w4][lane] = mine;
           }
           if (!meet()) return;
           bool raise = false;
           {
             float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) top = fmaxf(top, sh->top[gr][buf][w][lane & 15]);
+            for (int w = 0; w < 4; ++w) top = fmaxf(top, sh->top[gr][buf][w][lane & (RG - 1)]);
             float f = 1.0f;
             if (top > m + kHeadroom) {  // the same in the group's warps
               raise = true;
               f = ex2(m - top);
               m = top;
             }
-            if (lane < 16) {
+            if (lane < RG) {
               own[lane] = m == -INFINITY ? 0.0f : m;
               own[16 + lane] = f;
             }
             __syncwarp();
           }
           if (__any_sync(0xffffffffu, raise)) {
-            float f[16];
-            read16(own + 16, f);
+            float f[RG];
+            read_rows<RG>(own + 16, f);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) l[i] *= f[i];
+            for (int i = 0; i < RG; ++i) l[i] *= f[i];
             if (kt > g.kt0) {
               WAIT(sh->pv[buf ^ 1], ((nk - 1) >> 1) & 1);
               fence_after_sync();
 #pragma unroll 1
-              for (int b = 0; b < 2 * C::OB; ++b) {  // hi, lo of each block of dims
+              for (int b = 0; b < (RG == 16 ? 2 : 1) * C::OB; ++b) {  // 16 columns at a time
+                const uint32_t at = ts + C::kTO + (RG == 16 ? (b >> 1) * N + (b & 1) * 16 : b * N);
                 float o[16];
-                tmem_ld16(ts + C::kTO + (b >> 1) * N + (b & 1) * 16, o);
+                tmem_ld16(at, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= f[i];
-                tmem_st16(ts + C::kTO + (b >> 1) * N + (b & 1) * 16, o);
+                for (int i = 0; i < 16; ++i) o[i] *= f[i % RG];
+                tmem_st16(at, o);
               }
               tmem_st_wait();
             }
           }
           if (nk >= 2) WAIT(sh->pv[buf], ((nk >> 1) - 1) & 1);  // P[buf] has been read
           {
-            float ref[16];
-            read16(own, ref);
+            float ref[RG];
+            read_rows<RG>(own, ref);
             const float vs = vsc * kPScale;
-            uint32_t hi[4], lo[4];
+            uint32_t hi[RG / 4], lo[RG / 4];
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
+            for (int i = 0; i < RG; i += 4) {
               float w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -570,8 +618,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
               lo[i / 4] = l0 | l1 << 16;
             }
             unsigned char* to = smem + C::kPAt + buf * C::kP + r * N;
-            *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr + 1) * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if constexpr (RG == 16) {
+              *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr + 1) * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+              *reinterpret_cast<uint4*>(to + swz<N>(r, 0) * 16) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+            }
           }
           if (gr == 0 && (kt + 1) * BK > g.hi) {
             // Rows of V past the context's end: a stale NaN there would survive a weight of 0.
@@ -588,42 +640,44 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           fence_proxy_async();
           fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sh->p_full[buf]));
+            mbar_arrive(smem_u32(&sh->sc_empty[sc]));
+          }
         }
         // ---- the rows' sums out ----
-        const float part_l = across<true>(l, lane);
-        if (lane < 16) sh->top[gr][nk & 1][w4][lane] = part_l;
+        const float part_l = across<true, RG>(l, lane);
+        if (lane < RG) sh->top[gr][nk & 1][w4][lane] = part_l;
         if (!meet()) return;
         if (r == 0) sh->redo[gr][(seg_n & 1) ^ 1] = 0;  // (the last range's has been read)
-        float L = 0.0f;  // of row lane % 16, the same in every warp
+        float L = 0.0f;  // of row lane % RG, the same in every warp
 #pragma unroll
-        for (int w = 0; w < 4; ++w) L += sh->top[gr][nk & 1][w][lane & 15];
-        const int live = min(16, rows - gr * 16);  // rows of this group
-        if (lane < 16) own[lane] = g.slot >= 0 ? 1.0f / kPScale : L == 0.0f ? 0.0f : 1.0f / (L * kPScale);
+        for (int w = 0; w < 4; ++w) L += sh->top[gr][nk & 1][w][lane & (RG - 1)];
+        const int live = min(RG, rows - gr * RG);  // rows of this group
+        if (lane < RG) own[lane] = g.slot >= 0 ? 1.0f / kPScale : L == 0.0f ? 0.0f : 1.0f / (L * kPScale);
         __syncwarp();
         const bool fine = (L - L == 0.0f && L >= kLeastSum) || (m == -INFINITY && L == 0.0f);
-        uint32_t bad = __ballot_sync(0xffffffffu, !fine) & 0xffffu;
+        uint32_t bad = __ballot_sync(0xffffffffu, !fine) & ((1u << RG) - 1u);
         const Partials part(a.ws, 2 * (int64_t)a.ctas, a.rows, D);
         WAIT(sh->o_full, seg_n & 1);
         fence_after_sync();
 #pragma unroll 1
         for (int b = 0; b < C::OB; ++b) {
-          float o[16];
+          float o[RG];
           {
-            float y[32];
-            tmem_ld32(ts + C::kTO + b * N, y);
-            tmem_ld_wait();
-            float f[16];
-            read16(own, f);
+            float y[2 * RG];
+            load_parts<RG>(ts + C::kTO + b * N, y);
+            float f[RG];
+            read_rows<RG>(own, f);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = fmaf(y[16 + i], 1.0f / kLoScale, y[i]) * f[i];
+            for (int i = 0; i < RG; ++i) o[i] = fmaf(y[RG + i], 1.0f / kLoScale, y[i]) * f[i];
           }
           const int dim = b * 128 + r;
           if (D >= 128 || r < D) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < RG; ++i) {
               if (i >= live) continue;
-              const int row = gr * 16 + i;
+              const int row = gr * RG + i;
               if (!(o[i] - o[i] == 0.0f)) bad |= 1u << i;
               if (g.slot >= 0) {
                 part.o[(g.slot * a.rows + row) * D + dim] = o[i];
@@ -640,7 +694,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         }
         fence_before_sync();
         if (w4 == 0 && lane < live) {
-          const int row = gr * 16 + lane;
+          const int row = gr * RG + lane;
           if (g.slot >= 0)
             part.ml[g.slot * a.rows + row] = make_float2(L == 0.0f ? -INFINITY : m, L);
           else if (p.lse != nullptr)
@@ -648,7 +702,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
                 L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
         }
         bad = __reduce_or_sync(0xffffffffu, bad);
-        if (live < 16) bad &= live > 0 ? (1u << live) - 1u : 0u;
+        if (live < RG) bad &= live > 0 ? (1u << live) - 1u : 0u;
         if (lane == 0) {
           mbar_arrive(smem_u32(&sh->o_empty));
           if (bad) atomicOr(&sh->redo[gr][seg_n & 1], bad);
@@ -656,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         if (!meet()) return;
         uint32_t redo = *(volatile uint32_t*)&sh->redo[gr][seg_n & 1] & (0x1111u << w4);
         while (redo) {
-          const int i = __ffs(redo) - 1, row = gr * 16 + i;
+          const int i = __ffs(redo) - 1, row = gr * RG + i;
           redo &= redo - 1;
           const int t = g.t0 + row / G, h = g.hkv * G + row % G;
           float acc[D / 32], em, el;
@@ -709,7 +763,7 @@ bool codes_map(CUtensorMap* m, const AttnPages& c, const AttnLaunch& p, int pb) 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int row_class(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+constexpr int row_class(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 template <int D, int R>
 cudaError_t run(const AttnLaunch& p, cudaStream_t st) {
@@ -737,6 +791,7 @@ cudaError_t run(const AttnLaunch& p, cudaStream_t st) {
 template <int D>
 cudaError_t by_rows(const AttnLaunch& p, cudaStream_t st) {
   switch (row_class((int64_t)p.max_q * (p.Hq / p.Hkv))) {
+    case 8: return run<D, 8>(p, st);
     case 16: return run<D, 16>(p, st);
     case 32: return run<D, 32>(p, st);
     default: return run<D, 64>(p, st);
@@ -745,7 +800,7 @@ cudaError_t by_rows(const AttnLaunch& p, cudaStream_t st) {
 
 template <int D>
 int ctas_per_sm(int64_t rows) {
-  return row_class(rows) == 16 ? Cfg<D, 16>::kCtas : 1;
+  return row_class(rows) <= 16 ? Cfg<D, 16>::kCtas : 1;
 }
 
 }  // namespace

@@ -185,7 +185,10 @@ __device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, Sh* 
   }
   total *= p.Hkv;
   const long long w0 = total * blockIdx.x / ctas, w1 = total * (blockIdx.x + 1) / ctas;
-  if (tid == 0) sh->left = w1 - w0;
+  if (tid == 0) {
+    sh->left = w1 - w0;
+    sh->total = total;
+  }
   if (w1 > w0 && before * p.Hkv <= w0 && w0 < (before + mine) * p.Hkv) {
     long long at = before * p.Hkv;
     for (int s = s0; s < s1; ++s) {
@@ -203,11 +206,12 @@ __device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, Sh* 
 
 // What the joining kernel needs of CTA blockIdx.x's ranges, by one thread:
 // {s, kv head of the pair it began and left open (s = -1: none), how its first range ends:
-// 0 open, 1 the pair's end, 2 no range at all}.
+// 0 open, 1 the pair's end, 2 no range at all; the CTA that ends the pair it left open}.
 template <typename Sh>
-__device__ __forceinline__ int4 stream_info(const AttnLaunch& p, const Sh* sh) {
+__device__ __forceinline__ int4 stream_info(const AttnLaunch& p, int ctas, const Sh* sh) {
   int4 r = make_int4(-1, 0, 2, 0);
   SegIter every{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
+  long long at = sh->total * blockIdx.x / ctas;  // tiles before the range
   Seg g;
   for (bool first = true; every.next(p, g); first = false) {
     const int n = key_tiles(seq_range(p, g.s));
@@ -215,7 +219,13 @@ __device__ __forceinline__ int4 stream_info(const AttnLaunch& p, const Sh* sh) {
     if (g.kt0 == 0 && g.kt1 < n) {
       r.x = g.s;
       r.y = g.hkv;
+      // The CTA with the pair's last tile, total c / ctas <= last < total (c + 1) / ctas.
+      const long long last = at + n - 1;
+      long long c = last * ctas / sh->total;
+      while (sh->total * (c + 1) / ctas <= last) ++c;
+      r.w = (int)c;
     }
+    at += g.kt1 - g.kt0;
   }
   return r;
 }
@@ -229,19 +239,14 @@ __device__ __forceinline__ int4 stream_info(const AttnLaunch& p, const Sh* sh) {
 template <typename T, int D, typename Args>
 __device__ __forceinline__ void stream_join(const AttnLaunch& p, const Args& a) {
   wait_for_previous_kernel();
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x;
   const int4 mine = a.info[c0];
   if (mine.x < 0) return;
   const int G = p.Hq / p.Hkv;
   const SeqRange q = seq_range(p, mine.x);
   const int rows = min(q.b - q.a, p.max_q) * G;
   if ((int)blockIdx.y >= rows) return;
-  // The last range: the first after c0 that ends the pair.
-  int c1 = c0;
-  for (int c = c0 + 1; c1 == c0 && c < a.ctas; c += 32) {
-    const unsigned ends = __ballot_sync(0xffffffffu, c + lane < a.ctas && a.info[c + lane].z == 1);
-    c1 = ends ? c + __ffs(ends) - 1 : (c + 32 >= a.ctas ? a.ctas - 1 : c0);
-  }
+  const int c1 = mine.w;  // the last range's CTA
   const Partials part(a.ws, 2 * (int64_t)a.ctas, a.rows, D);
   // Block 2 c0 + 1 for the first range, 2 c for the rest; none for a CTA without one.
   auto slot_of = [&](int z) -> int64_t {

@@ -108,7 +108,7 @@ struct Shared {
   int redone;  // rows evaluated again so far, and parts of them
   uint32_t k_loads[kMaxRing], v_loads[kMaxRing], v_lands[kMaxRing], q_loads, clc_asked;  // issued so far
   int start_s, start_hkv, start_u;
-  long long left;
+  long long left, total;
   long long scan[20];
   // What the two warps of 32 rows exchange, 256 bytes twice for each of the four
   // pairs of the one-tile form, once for each of the eight of the other.
@@ -142,8 +142,7 @@ struct TcArgs {
   int pbk, pbv; // rows of a load of K, of V: a unit's keys, or a divisor of the page
   int ctas;     // stream form: the grid
   int rows;     // rows of a workspace block
-  int4* info;   // stream form, per CTA: {s, kv head of the pair it began and left open (s = -1:
-                // none), how its first range ends: 0 open, 1 the pair's end, 2 no range at all}
+  int4* info;   // stream form, per CTA: see stream_info
   float* ws;    // the sums
 };
 
@@ -619,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       // What the joining kernel needs of this CTA's ranges; the outputs of
       // sequences without a key.
       if (lane == 0) {
-        a.info[blockIdx.x] = stream_info(p, sh);
+        a.info[blockIdx.x] = stream_info(p, a.ctas, sh);
       }
       for (int s = blockIdx.x; s < p.N; s += a.ctas) {
         const SeqRange q = seq_range(p, s);
