@@ -16,15 +16,19 @@
 // log2(vscale) so far, raised (and O and l scaled) once a tile's maximum is 2^4 above it.
 // So blocks of small values keep their precision beside blocks of large ones.
 //
-// Warps:  0       TMA loads of K and V, a ring of tiles of 128 keys each
+// Warps:  0       hands out the ranges of key tiles; TMA loads of K, a ring of tiles of 128 keys
 //         1       the MMAs
-//         2       the ranges of key tiles, handed to the other roles
-//         3       TMEM; the scales, four tiles at a time, a ring of eight; the stream form's
-//                 bookkeeping
-//         4 ..    softmax and output: a group of 4 warps for each 16 rows of q (or
-//                 the 8 of a kernel of its own).  A thread has
-//                 one key of the tile, so that a row's maximum is one transposing butterfly
-//                 over the lanes and one exchange between the four warps.
+//         2       TMA loads of V; the scales.  (One warp for both loads issued one of a 16-row
+//                 page every 40 cycles.)
+//         3       TMEM; the stream form's bookkeeping
+//         4 ..    softmax and output: a group of 4 warps for each 16 rows of q (or the 8 of a
+//                 kernel of its own).  A thread has one key of the tile, so that a row's
+//                 maximum is one reduction over the warp and one exchange between the four.
+// What a tile costs is the chain of its softmax, 2600 cycles for 16 rows at first and 1400
+// now; a wait alone takes 150 to 250 even for what is there.  So there are three: for the
+// scores (whose barrier says also that the scales are there, and, the MMAs being one warp's in
+// order, that P's buffer is free again), for the maxima, and for the P V of the tile before
+// where O is scaled.  More groups that took the tiles in turns were no faster (spills).
 // Two S and two P buffers: the scores of a tile are computed during the softmax of the one
 // before.  Two CTAs share an SM where their memory allows it, and hide each other's chains.
 // The work is that of the stream form (gdn_attn_stream.cuh).
@@ -50,7 +54,7 @@ namespace {
 using namespace attn;
 using bf16 = __nv_bfloat16;
 
-constexpr int kMaxRing = 8, kSegs = 4, kMaxGroups = 4, kScaleRing = 8;
+constexpr int kMaxRing = 8, kSegs = 4, kMaxGroups = 4;
 constexpr float kHeadroom = 4.0f;       // log2: p reaches 2^4 before the reference follows
 constexpr float kPScale = 16.0f;        // p 2^4 in the parts' units: at most 256 of 448
 constexpr float kLoScale = 32.0f;
@@ -60,7 +64,6 @@ struct Shared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t q_full, s_full[2], p_full[2], pv[2], o_full, o_empty, end;
   uint64_t meet[kMaxGroups];
-  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Seg seg[kSegs];
   uint32_t tmem;
@@ -71,7 +74,7 @@ struct Shared {
   long long left, total;
   long long scan[20];
   uint32_t redo[kMaxGroups][2];                      // rows to evaluate again, by range parity
-  float2 scales[kScaleRing][8];                      // of K and V, for each 16 keys of a tile
+  float2 scales[2][8];                               // of K and V, for each 16 keys of a tile
   alignas(16) float qscale[kMaxGroups][16];
   alignas(16) int last[kMaxGroups][16];              // a row's last visible key
   alignas(16) float top[kMaxGroups][2][4][16];       // the warps' maxima (sums at the end)
@@ -135,26 +138,37 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// Maximum or sum over the warp of each of RG values: lane i is left with that of value
-// i % RG.  Each step halves the values a lane keeps.
-template <bool SUM, int RG>
-__device__ __forceinline__ float across(float (&v)[RG], int lane) {
+// The sum over the warp of each of RG values: lane i is left with that of value i % RG.
+// Each step halves the values a lane keeps.
+template <int RG>
+__device__ __forceinline__ float sum_across(float (&v)[RG], int lane) {
 #pragma unroll
   for (int w = RG / 2; w > 0; w >>= 1) {
     const bool up = lane & w;
 #pragma unroll
     for (int i = 0; i < w; ++i) {
       const float send = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, w);
-      v[i] = SUM ? keep + got : fmaxf(keep, got);
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
     }
   }
 #pragma unroll
-  for (int w = RG; w < 32; w <<= 1) {
-    const float got = __shfl_xor_sync(0xffffffffu, v[0], w);
-    v[0] = SUM ? v[0] + got : fmaxf(v[0], got);
-  }
+  for (int w = RG; w < 32; w <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
   return v[0];
+}
+// The maximum over the warp, of numbers only.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int RG>
+__device__ __forceinline__ void read_rows(const float* from, float2 (&x)[RG / 2]) {
+#pragma unroll
+  for (int i = 0; i < RG / 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(from)[i];
+    x[2 * i] = make_float2(v.x, v.y);
+    x[2 * i + 1] = make_float2(v.z, v.w);
+  }
 }
 template <int RG>
 __device__ __forceinline__ void read_rows(const float* from, float (&x)[RG]) {
@@ -221,7 +235,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       mbar_init(smem_u32(&sh->o_empty), 4 * C::kGroups);
       mbar_init(smem_u32(&sh->end), 1);
       for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_u32(&sh->s_full[i]), 1);
+        mbar_init(smem_u32(&sh->s_full[i]), 2);  // the scores, the scales
         mbar_init(smem_u32(&sh->p_full[i]), 4 * C::kGroups);
         mbar_init(smem_u32(&sh->pv[i]), 1);
       }
@@ -231,11 +245,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       }
       for (int i = 0; i < kSegs; ++i) {
         mbar_init(smem_u32(&sh->seg_full[i]), 1);
-        mbar_init(smem_u32(&sh->seg_empty[i]), 3 + 4 * C::kGroups);
-      }
-      for (int i = 0; i < kScaleRing; ++i) {
-        mbar_init(smem_u32(&sh->sc_full[i]), 1);
-        mbar_init(smem_u32(&sh->sc_empty[i]), 4 * C::kGroups);
+        mbar_init(smem_u32(&sh->seg_empty[i]), 2 + 4 * C::kGroups);
       }
       sh->abort = sh->redone = 0;
       fence_mbar_init();
@@ -269,50 +279,67 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       }
     }
   };
-  if (warp == 0) {
-    // ---- loads ----
-    auto role = [&] {
-      Ring ring;
-      uint32_t filled = 0;
-      Seg g;
-      while (next_seg(g)) {
-        const int kt0 = uni(g.kt0), n = uni(g.kt1) - kt0, hi = uni(g.hi), hkv = uni(g.hkv);
-        const int per_tile = BK / a.pb;
-        // Lane i looks up the page of, and issues, the tile's i-th group of pb keys.
-        auto find_page = [&](int kt) -> int {
-          const int jb = kt * BK + lane * a.pb;
-          if (lane >= per_tile || kt >= kt0 + n || jb >= hi) return 0;
-          const int64_t pg = page_of(p, g.s, jb / p.page_size);
-          if (pg < 0) atomicOr(p.status, kStatusBadIndex);
-          return pg < 0 ? (int)p.num_pages : (int)pg;  // past the end: reads as zeros
-        };
-        int next_page = find_page(kt0);
-        for (int j = 0; j < n; ++j, ring.step(), ++filled) {
-          const int j0 = (kt0 + j) * BK, page = next_page;
-          next_page = find_page(kt0 + j + 1);
-          const int groups = min(per_tile, (hi - j0 + a.pb - 1) / a.pb);
-          const int row = (j0 + lane * a.pb) % p.page_size;
-          auto load = [&](uint32_t to, const CUtensorMap* map, uint64_t* full, uint64_t* empty,
-                          uint32_t* loads) -> bool {
-            if (filled >= ST)
-              if (!warp_wait(&empty[ring.st], ring.round ^ 1, sh, p.status)) return false;
-            const uint32_t bar = smem_u32(&full[ring.st]);
-            if (elect_one()) {
-              ++loads[ring.st];
-              mbar_expect_tx(bar, groups * a.pb * (uint32_t)D);
-            }
-            __syncwarp();
-            if (lane < groups)
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-                tma_load_4d(to + ring.st * C::kTile + b * 128 * ROW + lane * a.pb * ROW, map, bar, b * ROW,
-                            row, hkv, page);
-            __syncwarp();
-            return true;
-          };
-          if (!load(sk, &mk, sh->k_full, sh->k_empty, sh->k_loads)) return;
-          if (!load(sv, &mv, sh->v_full, sh->v_empty, sh->v_loads)) return;
+  // The loads of a range's tiles, of K or V.  Pages are looked up four tiles at a time, a
+  // batch ahead: lane 8 t + i has that of the i-th group of pb keys of the t-th tile.
+  uint32_t loaded = 0;  // tiles before this range
+  auto load_range = [&](const Seg& g, uint32_t to, const CUtensorMap* map, uint64_t* full, uint64_t* empty,
+                        uint32_t* loads, bool raise, auto batch, auto after) -> bool {
+    const int kt0 = uni(g.kt0), kt1 = uni(g.kt1), hi = uni(g.hi), hkv = uni(g.hkv);
+    const int per_tile = BK / a.pb;
+    auto find_pages = [&](int kt) -> int {
+      const int i = lane & 7, jb = (kt + (lane >> 3)) * BK + i * a.pb;
+      if (i >= per_tile || kt + (lane >> 3) >= kt1 || jb >= hi) return 0;
+      const int64_t pg = page_of(p, g.s, jb / p.page_size);
+      if (pg < 0 && raise) atomicOr(p.status, kStatusBadIndex);
+      return pg < 0 ? (int)p.num_pages : (int)pg;  // past the end: reads as zeros
+    };
+    int next_pages = find_pages(kt0);
+    for (int kt = kt0; kt < kt1; kt += 4) {
+      const int pages = next_pages;
+      next_pages = find_pages(kt + 4);
+      batch(kt);
+      for (int t = 0; t < 4 && kt + t < kt1; ++t, ++loaded) {
+        const int j0 = (kt + t) * BK, page = __shfl_sync(0xffffffffu, pages, t * 8 + (lane & 7));
+        const int groups = min(per_tile, (hi - j0 + a.pb - 1) / a.pb);
+        const int row = (j0 + lane * a.pb) % p.page_size;
+        const uint32_t at = loaded % ST, round = loaded / ST;
+        if (round > 0)
+          if (!warp_wait(&empty[at], (round - 1) & 1, sh, p.status)) return false;
+        const uint32_t bar = smem_u32(&full[at]);
+        if (elect_one()) {
+          ++loads[at];
+          mbar_expect_tx(bar, groups * a.pb * (uint32_t)D);
         }
+        __syncwarp();
+        if (lane < groups)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            tma_load_4d(to + at * C::kTile + b * 128 * ROW + lane * a.pb * ROW, map, bar, b * ROW, row, hkv,
+                        page);
+        __syncwarp();
+        if (!after(t)) return false;
+      }
+    }
+    return true;
+  };
+  if (warp == 0) {
+    // ---- ranges, loads of K ----
+    auto role = [&] {
+      SegIter iter{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
+      for (int n = 0;; ++n) {
+        Seg g;
+        if (!iter.next(p, g)) g.s = -1;
+        const int i = n % kSegs;
+        if (n >= kSegs) WAIT(sh->seg_empty[i], (n / kSegs - 1) & 1);
+        if (lane == 0) {
+          sh->seg[i] = g;
+          mbar_arrive(smem_u32(&sh->seg_full[i]));
+        }
+        __syncwarp();
+        if (g.s < 0) return;
+        if (!load_range(g, sk, &mk, sh->k_full, sh->k_empty, sh->k_loads, true, [](int) {},
+                        [](int) { return true; }))
+          return;
       }
     };
     role();
@@ -380,55 +407,46 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     if (elect_one()) mma_commit(smem_u32(&sh->end));
     mbar_wait(smem_u32(&sh->end), 0, kWaitBudget);
   } else if (warp == 2) {
-    // ---- ranges ----
+    // ---- loads of V, scales ----
+    // Lane 8 t + i has the scales of keys 16 i .. 16 i + 15 of the t-th of four tiles.  Loaded
+    // by the threads that use them, a tile ahead, they came too late under load and cost each
+    // thread their addresses (decode of 256 sequences: 371 for 361 us).
     auto role = [&] {
-      SegIter iter{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
-      for (int n = 0;; ++n) {
-        Seg g;
-        if (!iter.next(p, g)) g.s = -1;
-        const int i = n % kSegs;
-        if (n >= kSegs) WAIT(sh->seg_empty[i], (n / kSegs - 1) & 1);
-        if (lane == 0) {
-          sh->seg[i] = g;
-          mbar_arrive(smem_u32(&sh->seg_full[i]));
-        }
-        __syncwarp();
-        if (g.s < 0) return;
+      Seg g;
+      float2 x, next;
+      while (next_seg(g)) {
+        auto find_scales = [&](int kt) -> float2 {
+          const int t = kt + (lane >> 3), j = t * BK + (lane & 7) * 16;
+          float2 s = make_float2(0.0f, 0.0f);
+          if (t < g.kt1 && j < g.hi) {
+            const int pi = j / p.page_size;
+            const int64_t pg = page_of(p, g.s, pi);
+            if (pg >= 0) {
+              const int64_t at = scale_at(p.Hkv, p.page_size, p.block, pg, g.hkv, j - pi * p.page_size);
+              s = make_float2(p.ks[at], p.vs[at]);
+            }
+          }
+          return s;
+        };
+        next = find_scales(g.kt0);
+        auto batch = [&](int kt) {
+          x = next;
+          next = find_scales(kt + 4);
+        };
+        auto after = [&](int t) -> bool {  // tile `loaded`'s V is on its way
+          // The tile two before has used its scales.
+          if (loaded >= 2)
+            if (!warp_wait(&sh->p_full[loaded & 1], ((loaded >> 1) - 1) & 1, sh, p.status)) return false;
+          if ((lane >> 3) == t) sh->scales[loaded & 1][lane & 7] = x;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->s_full[loaded & 1]));
+          return true;
+        };
+        if (!load_range(g, sv, &mv, sh->v_full, sh->v_empty, sh->v_loads, false, batch, after)) return;
       }
     };
     role();
   } else if (warp == 3) {
-    // ---- scales ----
-    // Lane 8 t + i: of keys 16 i .. 16 i + 15 of the t-th of four tiles.  Loaded by the
-    // threads that use them, a tile ahead, they came too late under load (decode of 256
-    // sequences: 371 us) and cost each thread their addresses.
-    auto role = [&] {
-      uint32_t nk = 0;  // tiles before these
-      Seg g;
-      while (next_seg(g)) {
-        for (int kt = g.kt0; kt < g.kt1; kt += 4) {
-          const int tiles = min(4, g.kt1 - kt), t = lane >> 3, j = (kt + t) * BK + (lane & 7) * 16;
-          float2 x = make_float2(0.0f, 0.0f);
-          if (t < tiles && j < g.hi) {
-            const int pi = j / p.page_size;
-            const int64_t pg = page_of(p, g.s, pi);  // (raised by the loads)
-            if (pg >= 0) {
-              const int64_t at = scale_at(p.Hkv, p.page_size, p.block, pg, g.hkv, j - pi * p.page_size);
-              x = make_float2(p.ks[at], p.vs[at]);
-            }
-          }
-          for (int i = 0; i < tiles; ++i) {
-            const uint32_t n = nk + i, at = n % kScaleRing;
-            if (n >= kScaleRing) WAIT(sh->sc_empty[at], (n / kScaleRing - 1) & 1);
-            if (t == i) sh->scales[at][lane & 7] = x;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh->sc_full[at]));
-          }
-          nk += tiles;
-        }
-      }
-    };
-    role();
     if (lane == 0) a.info[blockIdx.x] = stream_info(p, a.ctas, sh);
     // Sequences without a key.
     for (int s = blockIdx.x; s < p.N; s += a.ctas) {
@@ -515,47 +533,61 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
         }
         if (!meet()) return;  // qscale, last
-        float l[RG], m = -INFINITY;  // l of this thread's keys; m of row lane % RG
+        float2 l[RG / 2];     // of this thread's keys
+        float m = -INFINITY;  // of row lane % RG
 #pragma unroll
-        for (int i = 0; i < RG; ++i) l[i] = 0.0f;
+        for (int i = 0; i < RG / 2; ++i) l[i] = make_float2(0.0f, 0.0f);
         for (int kt = g.kt0; kt < g.kt1; ++kt, ++nk, vr.step()) {
           const uint32_t buf = nk & 1;
-          const uint32_t sc = nk % kScaleRing;
-          WAIT(sh->sc_full[sc], (nk / kScaleRing) & 1);
-          const float2 scale = sh->scales[sc][r >> 4];
-          const float ksc = scale.x, vsc = scale.y;
-          // (a scale of nothing, 0, has no logarithm: 2^-64 stands for smaller ones)
-          const float lv = fmaxf(__log2f(fabsf(vsc)), -64.0f);
           const int j = kt * BK + r;
           const bool masked = kt * BK + BK - 1 > g.pos0;
-          float s[RG];
+          float2 s[RG / 2];  // of rows 2 i, 2 i + 1: f32 instructions take pairs
+          float vsc, lv;
           {
-            float qs[RG];
+            float2 qs[RG / 2];
             read_rows<RG>(sh->qscale[gr], qs);
             WAIT(sh->s_full[buf], (nk >> 1) & 1);
             fence_after_sync();
+            const float2 scale = sh->scales[buf][r >> 4];
+            vsc = scale.y;
+            // (a scale of nothing, 0, has no logarithm: 2^-64 stands for smaller ones)
+            lv = fmaxf(__log2f(fabsf(vsc)), -64.0f);
             float y[2 * RG];
             load_parts<RG>(ts + buf * N, y);
+            const float2 ksc = make_float2(scale.x, scale.x);
+            const float2 part = make_float2(1.0f / kLoScale, 1.0f / kLoScale);
 #pragma unroll
-            for (int i = 0; i < RG; ++i) s[i] = fmaf(y[RG + i], 1.0f / kLoScale, y[i]) * (ksc * qs[i]);
+            for (int i = 0; i < RG / 2; ++i)
+              s[i] = __fmul2_rn(__ffma2_rn(make_float2(y[RG + 2 * i], y[RG + 2 * i + 1]), part,
+                                           make_float2(y[2 * i], y[2 * i + 1])),
+                                __fmul2_rn(ksc, qs[i]));
           }
           if (masked) {
             const int4* last = reinterpret_cast<const int4*>(sh->last[gr]);
 #pragma unroll
             for (int i = 0; i < RG / 4; ++i) {
               const int4 v = last[i];
-              s[4 * i] = j <= v.x ? s[4 * i] : -INFINITY;
-              s[4 * i + 1] = j <= v.y ? s[4 * i + 1] : -INFINITY;
-              s[4 * i + 2] = j <= v.z ? s[4 * i + 2] : -INFINITY;
-              s[4 * i + 3] = j <= v.w ? s[4 * i + 3] : -INFINITY;
+              s[2 * i].x = j <= v.x ? s[2 * i].x : -INFINITY;
+              s[2 * i].y = j <= v.y ? s[2 * i].y : -INFINITY;
+              s[2 * i + 1].x = j <= v.z ? s[2 * i + 1].x : -INFINITY;
+              s[2 * i + 1].y = j <= v.w ? s[2 * i + 1].y : -INFINITY;
             }
           }
           {
+            const float2 lv2 = make_float2(lv, lv);
             float t[RG];
 #pragma unroll
-            for (int i = 0; i < RG; ++i) t[i] = s[i] + lv;
-            const float mine = across<false, RG>(t, lane);
-            if (lane < RG) sh->top[gr][buf][w4][lane] = mine;
+            for (int i = 0; i < RG / 2; ++i) {
+              const float2 x = __fadd2_rn(s[i], lv2);
+              t[2 * i] = warp_max(x.x);
+              t[2 * i + 1] = warp_max(x.y);
+            }
+            if (lane == 0) {
+#pragma unroll
+              for (int i = 0; i < RG / 4; ++i)
+                reinterpret_cast<float4*>(sh->top[gr][buf][w4])[i] =
+                    make_float4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
+            }
           }
           if (!meet()) return;
           bool raise = false;
@@ -570,16 +602,16 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
               m = top;
             }
             if (lane < RG) {
-              own[lane] = m == -INFINITY ? 0.0f : m;
+              own[lane] = m == -INFINITY ? 0.0f : -m;
               own[16 + lane] = f;
             }
             __syncwarp();
           }
           if (__any_sync(0xffffffffu, raise)) {
-            float f[RG];
+            float2 f[RG / 2];
             read_rows<RG>(own + 16, f);
 #pragma unroll
-            for (int i = 0; i < RG; ++i) l[i] *= f[i];
+            for (int i = 0; i < RG / 2; ++i) l[i] = __fmul2_rn(l[i], f[i]);
             if (kt > g.kt0) {
               WAIT(sh->pv[buf ^ 1], ((nk - 1) >> 1) & 1);
               fence_after_sync();
@@ -590,33 +622,34 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
                 tmem_ld16(at, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= f[i % RG];
+                for (int i = 0; i < 16; ++i) o[i] *= i % 2 ? f[i % RG / 2].y : f[i % RG / 2].x;
                 tmem_st16(at, o);
               }
               tmem_st_wait();
             }
           }
-          if (nk >= 2) WAIT(sh->pv[buf], ((nk >> 1) - 1) & 1);  // P[buf] has been read
           {
-            float ref[RG];
+            float2 ref[RG / 2];
             read_rows<RG>(own, ref);
-            const float vs = vsc * kPScale;
+            const float2 vs = make_float2(vsc * kPScale, vsc * kPScale);
             uint32_t hi[RG / 4], lo[RG / 4];
 #pragma unroll
-            for (int i = 0; i < RG; i += 4) {
-              float w[4];
+            for (int i = 0; i < RG / 4; ++i) {
+              uint32_t h[2], o[2];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                w[e] = ex2(s[i + e] - ref[i + e]);
-                l[i + e] += w[e];
-                w[e] *= vs;
+              for (int e = 0; e < 2; ++e) {
+                const int k = 2 * i + e;
+                float2 w = __fadd2_rn(s[k], ref[k]);  // (minus the reference)
+                w.x = ex2(w.x);
+                w.y = ex2(w.y);
+                l[k] = __fadd2_rn(l[k], w);
+                w = __fmul2_rn(w, vs);
+                split2(w.x, w.y, h[e], o[e]);
               }
-              uint32_t h0, l0, h1, l1;
-              split2(w[0], w[1], h0, l0);
-              split2(w[2], w[3], h1, l1);
-              hi[i / 4] = h0 | h1 << 16;
-              lo[i / 4] = l0 | l1 << 16;
+              hi[i] = h[0] | h[1] << 16;
+              lo[i] = o[0] | o[1] << 16;
             }
+            // (P[buf] has been read: the scores' MMAs followed that product.)
             unsigned char* to = smem + C::kPAt + buf * C::kP + r * N;
             if constexpr (RG == 16) {
               *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -640,13 +673,16 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           fence_proxy_async();
           fence_before_sync();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_u32(&sh->p_full[buf]));
-            mbar_arrive(smem_u32(&sh->sc_empty[sc]));
-          }
+          if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
         }
         // ---- the rows' sums out ----
-        const float part_l = across<true, RG>(l, lane);
+        float ls[RG];
+#pragma unroll
+        for (int i = 0; i < RG / 2; ++i) {
+          ls[2 * i] = l[i].x;
+          ls[2 * i + 1] = l[i].y;
+        }
+        const float part_l = sum_across<RG>(ls, lane);
         if (lane < RG) sh->top[gr][nk & 1][w4][lane] = part_l;
         if (!meet()) return;
         if (r == 0) sh->redo[gr][(seg_n & 1) ^ 1] = 0;  // (the last range's has been read)
