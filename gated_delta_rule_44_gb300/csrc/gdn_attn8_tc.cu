@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.Hq / p.Hkv;
 
-  start_next_kernel();
+  // (Launched with programmatic dependence: up to the wait, beside the kernel before.)
   if (warp == 0) {
     if (lane == 0) {
       for (int i = 0; i < ST; ++i) {
@@ -253,6 +253,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   } else if (warp == 3) {
     tmem_alloc(smem_u32(&sh->tmem), C::kCols);
   }
+  wait_for_previous_kernel();
+  start_next_kernel();
   stream_start<C::kThreads>(p, a.ctas, sh);
   fence_before_sync();
   __syncthreads();
@@ -710,20 +712,36 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           }
           const int dim = b * 128 + r;
           if (D >= 128 || r < D) {
+            if (g.slot >= 0) {
+              float* to = part.o + (g.slot * a.rows + gr * RG) * D + dim;
 #pragma unroll
-            for (int i = 0; i < RG; ++i) {
-              if (i >= live) continue;
-              const int row = gr * RG + i;
-              if (!(o[i] - o[i] == 0.0f)) bad |= 1u << i;
-              if (g.slot >= 0) {
-                part.o[(g.slot * a.rows + row) * D + dim] = o[i];
-              } else {
-                const int t = g.t0 + row / G, h = g.hkv * G + row % G;
+              for (int i = 0; i < RG; ++i) {
+                if (i >= live) continue;
+                if (!(o[i] - o[i] == 0.0f)) bad |= 1u << i;
+                to[i * D] = o[i];
+              }
+            } else {
+              // Row after row: the next head, or the next token's first of the group.
+              int h = gr * RG % G;
+              const int t = g.t0 + gr * RG / G;
+              bf16* to = static_cast<bf16*>(p.out) + ((int64_t)t * p.Hq + g.hkv * G + h) * D + dim;
+              const bf16* gate = static_cast<const bf16*>(p.gate.p) + (int64_t)t * p.gate.ts +
+                                 (int64_t)(g.hkv * G + h) * p.gate.hs + dim;
+              const int64_t out_wrap = (int64_t)(p.Hq - G) * D, gate_wrap = p.gate.ts - G * p.gate.hs;
+#pragma unroll
+              for (int i = 0; i < RG; ++i) {
+                if (i >= live) continue;
+                if (!(o[i] - o[i] == 0.0f)) bad |= 1u << i;
                 float x = o[i];
-                if (p.gate.p != nullptr)
-                  x *= sigmoid_gate(to_f(static_cast<const bf16*>(
-                      p.gate.p)[(int64_t)t * p.gate.ts + (int64_t)h * p.gate.hs + dim]));
-                static_cast<bf16*>(p.out)[((int64_t)t * p.Hq + h) * D + dim] = __float2bfloat16_rn(x);
+                if (p.gate.p != nullptr) x *= sigmoid_gate(to_f(*gate));
+                *to = __float2bfloat16_rn(x);
+                to += D;
+                gate += p.gate.hs;
+                if (++h == G) {
+                  h = 0;
+                  to += out_wrap;
+                  gate += gate_wrap;
+                }
               }
             }
           }
@@ -780,7 +798,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 template <int D>
 __global__ void __launch_bounds__(256) attn8_join_kernel(const __grid_constant__ AttnLaunch p,
                                                          const __grid_constant__ Tc8Args a) {
-  stream_join<bf16, D>(p, a);
+  stream_join<bf16, D, true>(p, a);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -817,11 +835,9 @@ cudaError_t run(const AttnLaunch& p, cudaStream_t st) {
   static const cudaError_t attr = cudaFuncSetAttribute(
       attn8_tc_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
   if (attr != cudaSuccess) return attr;
-  attn8_tc_kernel<D, R><<<a.ctas, C::kThreads, C::kBytes, st>>>(p, mk, mv, a);
-  note_launch();
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(attn8_tc_kernel<D, R>, dim3(a.ctas), C::kThreads, st, C::kBytes, p, mk, mv, a);
   if (e != cudaSuccess) return e;
-  return launch_after(attn8_join_kernel<D>, dim3(a.ctas, std::min(a.rows, 16)), 256, st, p, a);
+  return launch_after(attn8_join_kernel<D>, dim3(a.ctas, std::min(a.rows, 16)), 256, st, 0, p, a);
 }
 
 template <int D>

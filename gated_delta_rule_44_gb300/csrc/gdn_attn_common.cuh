@@ -220,13 +220,15 @@ __device__ __forceinline__ void wait_for_previous_kernel() {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 template <typename... K, typename... A>
-cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, cudaStream_t st, const A&... a) {
+cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, cudaStream_t st, size_t shared,
+                         const A&... a) {
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
@@ -239,7 +241,7 @@ cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, cudaStrea
 //   out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z,
 // whose sums are in the blocks slot_of(z) (negative: none), by RW warps of a CTA
 // of 8: warp w takes z = w, w + RW, ...: the (m, l) of 32 ranges first, a lane
-// each, then their weighted O, four loads in flight.  The order of the sums
+// each, then their weighted O, eight loads in flight.  The order of the sums
 // depends on n alone.
 template <typename T, int D, int RW, typename SlotOf>
 __device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& part, int n,
@@ -267,9 +269,9 @@ __device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& pa
     for (int e = 0; e < E; ++e) acc[e] *= f;
     unsigned todo = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
     while (todo) {
-      float x[4][E], wk[4];
+      float x[8][E], wk[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         wk[k] = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) x[k][e] = 0.0f;
@@ -284,7 +286,7 @@ __device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& pa
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 8; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(wk[k], x[k][e], acc[e]);
     }

@@ -593,9 +593,9 @@ cudaError_t join(const AttnLaunch& p, int splits, int bm, int TT, cudaStream_t s
   // Eight warps to a row when there is a range for each (5 instead of 16 us for 16
   // ranges of 8 rows), else a warp.
   if (splits >= 8)
-    return launch_after(attn_join_kernel<T, D, 8>, dim3((unsigned)ctas, rows), kThreads, st, p, splits,
+    return launch_after(attn_join_kernel<T, D, 8>, dim3((unsigned)ctas, rows), kThreads, st, 0, p, splits,
                         bm, TT);
-  return launch_after(attn_join_kernel<T, D, 1>, dim3((unsigned)ctas, (rows + 7) / 8), kThreads, st, p,
+  return launch_after(attn_join_kernel<T, D, 1>, dim3((unsigned)ctas, (rows + 7) / 8), kThreads, st, 0, p,
                       splits, bm, TT);
 }
 

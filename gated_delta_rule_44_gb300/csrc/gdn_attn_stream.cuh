@@ -236,8 +236,12 @@ __device__ __forceinline__ int4 stream_info(const AttnLaunch& p, int ctas, const
 // keys.
 // `a` has the grid of the streaming kernel (ctas), its int4 info per CTA, the sums (ws) and
 // the rows of a block of them.
-template <typename T, int D, typename Args>
+// FEW: pairs in few ranges are joined by a warp a row, eight rows to a CTA.  (Drafts of 128
+// sequences, every one of 304 CTAs leaving a pair of 16 rows open: 15 us of 208 went into
+// 4900 CTAs of eight warps for two ranges.)
+template <typename T, int D, bool FEW, typename Args>
 __device__ __forceinline__ void stream_join(const AttnLaunch& p, const Args& a) {
+  start_next_kernel();
   wait_for_previous_kernel();
   const int c0 = blockIdx.x;
   const int4 mine = a.info[c0];
@@ -252,6 +256,13 @@ __device__ __forceinline__ void stream_join(const AttnLaunch& p, const Args& a) 
   auto slot_of = [&](int z) -> int64_t {
     return z == 0 ? 2 * (int64_t)c0 + 1 : a.info[c0 + z].z == 2 ? -1 : 2 * (int64_t)(c0 + z);
   };
+  if (FEW && c1 - c0 < 8) {
+    for (int r0 = 8 * blockIdx.y; r0 < rows; r0 += 8 * gridDim.y) {
+      const int r = r0 + (threadIdx.x >> 5);
+      join_row<T, D, 1>(p, part, c1 - c0 + 1, slot_of, r, r < rows, q.a + r / G, mine.y * G + r % G);
+    }
+    return;
+  }
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
     join_row<T, D, 8>(p, part, c1 - c0 + 1, slot_of, r, true, q.a + r / G, mine.y * G + r % G);
     __syncthreads();

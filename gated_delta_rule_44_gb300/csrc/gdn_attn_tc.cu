@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(256) attn_stream_join_kernel(const __grid_constant__ AttnLaunch p,
                                                                const __grid_constant__ TcArgs a) {
-  stream_join<bf16, D>(p, a);
+  stream_join<bf16, D, false>(p, a);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -1034,7 +1034,7 @@ cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
     a.ws = reinterpret_cast<float*>(static_cast<char*>(p.ws) + info_bytes(sms));
     cudaError_t e = run<D, 1, true, true>(p, a, dim3(sms), st);
     if (e != cudaSuccess) return e;
-    return launch_after(attn_stream_join_kernel<D>, dim3(sms, std::min(a.rows, 16)), 256, st, p, a);
+    return launch_after(attn_stream_join_kernel<D>, dim3(sms, std::min(a.rows, 16)), 256, st, 0, p, a);
   }
   a.q_box = a.TQ;
   const int TT = NQ * a.TQ;

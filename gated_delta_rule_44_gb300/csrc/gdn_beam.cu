@@ -564,10 +564,10 @@ cudaError_t launch_beam(const BeamLaunch& p, cudaStream_t st) {
   const dim3 grid((unsigned)segs, (unsigned)p.W, (unsigned)p.B);
   // (Both launches are prepared while the kernel before them still runs.)
   const cudaError_t e =
-      p.bf16 ? attn::launch_after(beam_rows_kernel<__nv_bfloat16>, grid, kThreads, st, p, seg_len)
-             : attn::launch_after(beam_rows_kernel<float>, grid, kThreads, st, p, seg_len);
+      p.bf16 ? attn::launch_after(beam_rows_kernel<__nv_bfloat16>, grid, kThreads, st, 0, p, seg_len)
+             : attn::launch_after(beam_rows_kernel<float>, grid, kThreads, st, 0, p, seg_len);
   if (e != cudaSuccess) return e;
-  return attn::launch_after(beam_join_kernel, dim3((unsigned)p.B), kThreads, st, p, segs);
+  return attn::launch_after(beam_join_kernel, dim3((unsigned)p.B), kThreads, st, 0, p, segs);
 }
 
 }  // namespace gdn
