@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "gdn_attn_common.cuh"
 #include "gdn_internal.h"
 #include "tcgen05.cuh"
 
@@ -91,6 +92,8 @@ __device__ void check_lists(const SlotsLaunch& p, uint32_t* seen) {
 __global__ void __launch_bounds__(kThreads) slots_kernel(const __grid_constant__ SlotsLaunch p) {
   extern __shared__ __align__(128) unsigned char stage[];
   __shared__ uint64_t landed;
+  attn::start_next_kernel();
+  attn::wait_for_previous_kernel();
   const int tid = threadIdx.x, lane = tid & 31;
   // The pool whose items hold this number.
   int64_t item = blockIdx.x;
@@ -174,9 +177,7 @@ cudaError_t launch_slots(SlotsLaunch& p, cudaStream_t st) {
   static const cudaError_t attr =
       cudaFuncSetAttribute(slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStage);
   if (attr != cudaSuccess) return attr;
-  slots_kernel<<<(unsigned)items + 1, kThreads, kStage, st>>>(p);
-  note_launch();
-  return cudaGetLastError();
+  return attn::launch_after(slots_kernel, dim3((unsigned)items + 1), kThreads, st, kStage, p);
 }
 
 }  // namespace gdn

@@ -212,6 +212,50 @@ def test_write_norm_and_rotary(q_lens, kv_lens, Hq, Hkv, D, rot, page, block, dt
         a += n
 
 
+@pytest.mark.parametrize("T,Hkv,D,rot,dtype", [(2000, 2, 128, 128, BF), (700, 1, 256, 64, BF), (900, 3, 64, 64, F32),
+                                               (1500, 2, 32, 32, BF), (400, 2, 128, 64, F32)])
+@pytest.mark.parametrize("single", [False, True])
+def test_write_codes_of_the_exact_values(T, Hkv, D, rot, dtype, single, cuda_device):
+    """A key's codes are those of its exact value, in one prompt and token by token: equal to
+    the 64-bit value's, which itself is off by 2^-44 of the row's magnitude at most."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(T + D)
+    page = block = 16
+    n = -(-T // page)
+    N = T if single else 1
+    if single:      # one token per sequence, a page each
+        n = T
+    table = torch.arange(n, dtype=torch.int32).view(N, -1).to(dev)
+    kc = torch.zeros(n, Hkv, page, D, dtype=torch.uint8, device=dev).view(E4M3)
+    vc = torch.zeros_like(kc.view(torch.uint8)).view(E4M3)
+    ks, vs = torch.zeros(n, Hkv, 1, device=dev), torch.zeros(n, Hkv, 1, device=dev)
+    k = randn(g, T, Hkv, D, dtype=dtype)
+    kw = (torch.rand(D, generator=g) + 0.5).to(dtype)
+    ang = torch.rand(T, rot // 2, generator=g, dtype=torch.float64) * 6.28
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    pos = torch.arange(T, dtype=torch.int32, device=dev)
+    B.gdn_attn8_prepare(k.to(dev), k.to(dev), k.to(dev), None if single else cu_of([T], dev),
+                        torch.empty(T, Hkv, D, dtype=dtype, device=dev),
+                        kv_lens=torch.full((N,), 1 if single else T, dtype=torch.int32, device=dev),
+                        k_cache=kc, v_cache=vc, k_scale=ks, v_scale=vs, block_table=table, positions=pos,
+                        k_norm_weight=kw.to(dev), cos_sin=cs.to(dev))
+    B.gdn_read_device_status()
+    y, mag = R.norm_rotate(R.f64(k), R.f64(kw), float(np.float32(1e-6)), R.f64(cs)[:, :rot // 2], R.f64(cs)[:, rot // 2:])
+    S = R.f64(ks)[:, :, 0] if single else np.repeat(R.f64(ks)[:, :, 0], page, 0)[:T]
+    got = R.f64(kc.cpu().float())
+    got = got[:, :, 0] if single else got.transpose(0, 2, 1, 3).reshape(-1, Hkv, D)[:T]
+    for t in range(0, T, page if not single else 1):       # the scales, from the exact maxima
+        rows = slice(t, min(t + (1 if single else page), T))
+        for h in range(Hkv):
+            top = np.abs(y[rows, h]).max()
+            if Q.need(top * (1 - 1e-6)) == Q.need(top * (1 + 1e-6)):
+                assert S[t, h] == Q.need(top)
+    z = y / S[..., None]
+    half = Q.half_code(z)
+    slack = 2.0 ** -44 * mag / S[..., None]
+    assert (np.abs(got - z) <= half + slack).all()
+
+
 def test_write_bad_metadata(cuda_device):
     """Pages, lengths and positions that cannot be right: raised, nothing written for them."""
     dev = cuda_device
