@@ -8,6 +8,7 @@ if the library cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 import threading
 from typing import Optional
@@ -611,6 +612,14 @@ class _Args(threading.local):
 
 _args = _Args()
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_need(device, name, *sizes) -> int:
+    """Workspace bytes of a call of these sizes on this device (a decode step asks for the
+    same ones again and again)."""
+    return int(getattr(lib(), name)(*sizes))
 
 
 def _bad(msg: str):
@@ -755,7 +764,7 @@ def _attn_call(fn, q, stream) -> None:
         s = _raw_stream(q.device.index)
     else:
         s = torch.cuda.current_stream(q.device).cuda_stream
-    if q.device.index != torch.cuda.current_device():  # the library launches on the current device
+    if q.device.index != _current_device():  # the library launches on the current device
         with torch.cuda.device(q.device):
             _check(fn(_args.at, s))
     else:
@@ -866,8 +875,8 @@ def _attn_paged(packer, fn, q, k_cache, v_cache, scales, block_table, kv_lens, c
         # Without offsets a call has one token per sequence, whatever max_q_len says.
         most = max_q_len if cu_seqlens is not None or scales is None else 1
         nbytes = (gdn_attn_paged_workspace_bytes(T, N, Hq, Hkv, D, most, _dt(q)) if scales is None else
-                  gdn_attn8_paged_workspace_bytes(T, N, Hq, Hkv, D, most, _dt(q),
-                                                  block_table.shape[1], k_cache.shape[2]))
+                  _workspace_need(dev.index, "gdn_attn8_paged_workspace_bytes", T, N, Hq, Hkv, D,
+                                  most, _dt(q), block_table.shape[1], k_cache.shape[2]))
         if nbytes:
             workspace = _scratch(nbytes, dev, stream)
     elif workspace.device != dev:
@@ -977,7 +986,8 @@ def gdn_beam_select(logits, scores, parents, tokens, out_scores, *, finished=Non
     if not logits.is_cuda:
         raise _bad(f"beam_select tensors must be on a CUDA device, got {dev}")
     if workspace is None:
-        workspace = _scratch(gdn_beam_select_workspace_bytes(n, W, V, K), dev, stream)
+        workspace = _scratch(_workspace_need(dev.index, "gdn_beam_select_workspace_bytes", n, W, V, K),
+                             dev, stream)
     elif workspace.device != dev:
         raise _bad(f"beam_select workspace is on {workspace.device}, not {dev}")
     length = (n - 1) * bs + (W - 1) * ws + V if n > 0 and W > 0 else 0
@@ -1006,15 +1016,18 @@ def gdn_copy_slots(pools, dst, src, *, groups=False, dst_host=None, src_host=Non
     for i, t in enumerate(pools):
         if t.device != dev:
             raise _bad(f"copy_slots pool {i} is on {t.device}, not {dev}")
-        if t.dim() == 0 or t.numel() == 0:
+        n = t.shape[0] if t.dim() else 0
+        size = t.nbytes // n if n else 0
+        if size == 0:
             raise _bad_shape(f"copy_slots pool {i} has shape {tuple(t.shape)}")
-        if not t[0].is_contiguous():
-            raise _bad(f"copy_slots pool {i}: a slot's values must be contiguous")
-        es, n = t.element_size(), t.shape[0]
-        size = t.numel() // n * es
-        stride = t.stride(0) * es if n > 1 else size
-        if stride == 0:
-            raise _bad(f"copy_slots pool {i} is a broadcast view; pass a real pool")
+        stride = size
+        if not t.is_contiguous():
+            if not t[0].is_contiguous():
+                raise _bad(f"copy_slots pool {i}: a slot's values must be contiguous")
+            if n > 1:
+                stride = t.stride(0) * t.element_size()
+                if stride == 0:
+                    raise _bad(f"copy_slots pool {i} is a broadcast view; pass a real pool")
         rows += (t.data_ptr(), (n - 1) * stride + size, n, size, stride)
     if not pools[0].is_cuda:
         raise _bad(f"copy_slots tensors must be on a CUDA device, got {dev}")

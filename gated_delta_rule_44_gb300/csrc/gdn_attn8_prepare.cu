@@ -174,7 +174,7 @@ __device__ __noinline__ uint2 exact_codes(const T* row, const T* weight, const f
 template <typename T, int D, int TEAM>
 __device__ __forceinline__ void block_item(const AttnPrepareLaunch& p, int64_t id, int h2) {
   constexpr int LG = D / 8, RG = TEAM / LG;  // lanes of a row, rows of a pass
-  constexpr int kKeep = TEAM > 32 ? 4 : 1;
+  constexpr int kKeep = TEAM > 32 ? 2 : 1;
   const int in_team = threadIdx.x % TEAM, lane = in_team % LG, row_of = in_team / LG;
   const int B = p.block;
   const unsigned mask =  // the row's lanes
@@ -249,17 +249,9 @@ __device__ __forceinline__ void block_item(const AttnPrepareLaunch& p, int64_t i
 #pragma unroll
       for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
       const float inv = math::rms_inv(ss, 1.0f / D, p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= inv * w[e];
+      scale_pairs(x, inv, w);
     }
-    if (live && rotates) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float u = x[e], v = x[e + 4];
-        x[e] = fmaf(u, c4[e], -v * s4[e]);
-        x[e + 4] = fmaf(v, c4[e], u * s4[e]);
-      }
-    }
+    if (live && rotates) rotate_pairs(x, c4, s4);
     return live;
   };
   float amax = 0.0f;
@@ -365,7 +357,7 @@ __device__ __forceinline__ void block_item(const AttnPrepareLaunch& p, int64_t i
 }
 
 template <typename T, int D, int TEAM>
-__global__ void __launch_bounds__(kThreads, TEAM > 32 ? 3 : 4) attn8_prepare_kernel(
+__global__ void __launch_bounds__(kThreads, 4) attn8_prepare_kernel(
     const __grid_constant__ AttnPrepareLaunch p, const __grid_constant__ AttnPrepareLaunch q_rows,
     int64_t items, int item_ctas, int heads, int heads_per_group, int token_ctas, int gx) {
   attn::start_next_kernel();

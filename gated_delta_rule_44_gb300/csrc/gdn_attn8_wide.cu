@@ -51,36 +51,52 @@ __device__ __forceinline__ void widen16(const uint4& c, float f, float* to) {
   }
 }
 
-// Page blockIdx.x of sequence s0 + blockIdx.y, all heads, K and V, into page
+// A head's page blockIdx.x of sequence s0 + blockIdx.y, of K or V (blockIdx.z), into page
 // blockIdx.y * max_pages + blockIdx.x of the workspace; its entry of the table there.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ AttnLaunch p, int s0,
                                                          int32_t* table, T* k, T* v) {
+  start_next_kernel();
+  wait_for_previous_kernel();
   const int s = s0 + blockIdx.y, pi = blockIdx.x;
   const SeqRange q = seq_range(p, s);
   if (q.bad && pi == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
   const int64_t to = (int64_t)blockIdx.y * p.max_pages + pi;
-  if (threadIdx.x == 0) table[to] = (int32_t)to;
+  if (threadIdx.x == 0 && blockIdx.z == 0) table[to] = (int32_t)to;
   const int rows = min(p.page_size, q.kv - pi * p.page_size);
   if (q.b <= q.a || rows <= 0) return;
   const int64_t pg = page_of(p, s, pi);
   if (pg < 0 && threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
   const int vecs = p.D / 16, n = rows * vecs;  // 16-code pieces of a head's rows
-  int hv = 0;  // head of K, or Hkv + head of V
-  for (int i = threadIdx.x;; i += kThreads) {
-    for (; i >= n; i -= n) ++hv;
-    if (hv >= 2 * p.Hkv) break;
-    const bool of_v = hv >= p.Hkv;
-    const int h = of_v ? hv - p.Hkv : hv, d = i % vecs * 16, r = i / vecs;
-    uint4 c = make_uint4(0u, 0u, 0u, 0u);
-    float f = 0.0f;
-    if (pg >= 0) {  // a bad page reads as zeros
-      const AttnPages& src = of_v ? p.vc : p.kc;
-      c = *reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(src.p) + pg * src.ps +
-                                          (int64_t)h * src.hs + (int64_t)r * src.ts + d);
-      f = (of_v ? p.vs : p.ks)[scale_at(p.Hkv, p.page_size, p.block, pg, h, r)];
+  // Head blockIdx.z of K, or Hkv + head of V.  Loads four at a time: one at a time, all heads
+  // of a page by a CTA, took 37 us where HBM takes 17 (a chunk of 2048 over 32768 tokens).
+  for (int z = blockIdx.z; z < 2 * p.Hkv; z += gridDim.z) {
+    const bool of_v = z >= p.Hkv;
+    const int h = of_v ? z - p.Hkv : z;
+    const AttnPages& src = of_v ? p.vc : p.kc;
+    const unsigned char* from = static_cast<const unsigned char*>(src.p) + pg * src.ps + (int64_t)h * src.hs;
+    const float* scales = (of_v ? p.vs : p.ks) + scale_at(p.Hkv, p.page_size, p.block, max(pg, (int64_t)0), h, 0);
+    T* out = (of_v ? v : k) + (to * p.Hkv + h) * p.page_size * p.D;
+    constexpr int kAhead = 4;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * kThreads) {
+      uint4 c[kAhead];
+      float f[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kThreads, r = i / vecs;
+        c[u] = make_uint4(0u, 0u, 0u, 0u);
+        f[u] = 0.0f;
+        if (i < n && pg >= 0) {  // a bad page reads as zeros
+          c[u] = *reinterpret_cast<const uint4*>(from + (int64_t)r * src.ts + (i - r * vecs) * 16);
+          f[u] = scales[r / p.block];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kThreads;
+        if (i < n) widen16(c[u], f[u], out + (int64_t)i * 16);
+      }
     }
-    widen16(c, f, (of_v ? v : k) + ((to * p.Hkv + h) * p.page_size + r) * p.D + d);
   }
 }
 
@@ -107,9 +123,8 @@ cudaError_t run(const AttnLaunch& p, cudaStream_t st) {
   T* v = reinterpret_cast<T*>(reinterpret_cast<char*>(k) + half);
   for (int64_t s0 = 0; s0 < p.N; s0 += group) {
     const int ns = (int)std::min<int64_t>(group, p.N - s0);
-    widen_kernel<T><<<dim3((unsigned)p.max_pages, (unsigned)ns), kThreads, 0, st>>>(p, (int)s0, table, k, v);
-    note_launch();
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_after(widen_kernel<T>, dim3((unsigned)p.max_pages, (unsigned)ns, (unsigned)std::min(2 * p.Hkv, 65535)), kThreads, st,
+                                 0, p, (int)s0, table, k, v);
     if (e != cudaSuccess) return e;
     AttnLaunch w = p;
     w.N = ns;

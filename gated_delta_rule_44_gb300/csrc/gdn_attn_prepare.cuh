@@ -66,6 +66,31 @@ struct Vec8<float> {
   }
 };
 
+// x *= inv * w and the rotation of (x[e], x[e + 4]), two f32 to an instruction, rounded as
+// one by one.
+__device__ __forceinline__ void scale_pairs(float (&x)[8], float inv, const float (&w)[8]) {
+  const float2 i2 = make_float2(inv, inv);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 y = __fmul2_rn(make_float2(x[e], x[e + 1]), __fmul2_rn(i2, make_float2(w[e], w[e + 1])));
+    x[e] = y.x;
+    x[e + 1] = y.y;
+  }
+}
+__device__ __forceinline__ void rotate_pairs(float (&x)[8], const float (&c)[4], const float (&s)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const float2 u = make_float2(x[e], x[e + 1]), v = make_float2(x[e + 4], x[e + 5]);
+    const float2 c2 = make_float2(c[e], c[e + 1]), s2 = make_float2(s[e], s[e + 1]);
+    const float2 a = __ffma2_rn(u, c2, __fmul2_rn(make_float2(-v.x, -v.y), s2));
+    const float2 b = __ffma2_rn(v, c2, __fmul2_rn(u, s2));
+    x[e] = a.x;
+    x[e + 1] = a.y;
+    x[e + 4] = b.x;
+    x[e + 5] = b.y;
+  }
+}
+
 // The last sequence s with cu[s] <= t, for the warp's first token t: 32 probes at
 // a time, a lane each, so that the chain of dependent loads is log32 N long.  A
 // decode batch's answer, s = t, is tried beside the first probes.
@@ -210,17 +235,9 @@ __device__ __forceinline__ void prepare_rows(const AttnPrepareLaunch& p, int hea
 #pragma unroll
           for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(grp, ss, o);
           const float inv = math::rms_inv(ss, 1.0f / D, p.eps);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= inv * w[e];
+          scale_pairs(x, inv, w);
         }
-        if (rotates) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float u = x[e], v = x[e + 4];
-            x[e] = fmaf(u, c4[e], -v * s4[e]);
-            x[e + 4] = fmaf(v, c4[e], u * s4[e]);
-          }
-        }
+        if (rotates) rotate_pairs(x, c4, s4);
         if (!shown) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = 0.0f;

@@ -366,29 +366,55 @@ __global__ void __launch_bounds__(kThreads, RB * D <= 512 ? 2 : 1) attn_rows_ker
       if (next_k < 0) atomicOr(p.status, kStatusBadIndex);
     }
   };
+  // Of codes, a step's are on their way during the step before: they take a quarter of the
+  // registers of f32, and a chain of page, scale and row per step was most of the time.
+  using Raw = std::conditional_t<E == 8, uint2, std::conditional_t<E == 4, uint32_t,
+              std::conditional_t<E == 2, uint16_t, uint8_t>>>;
+  Raw raw_k[kScaled ? kKeys : 1], raw_v[kScaled ? kKeys : 1];
+  float raw_ks = 0.0f, raw_vs = 0.0f;
+  auto fetch = [&] {  // the step that find() found
+    raw_ks = next_ks;
+    raw_vs = next_vs;
+#pragma unroll
+    for (int i = 0; i < (kScaled ? kKeys : 0); ++i) {
+      const int64_t a = __shfl_sync(0xffffffffu, next_k, i), b = __shfl_sync(0xffffffffu, next_v, i);
+      raw_k[i] = raw_v[i] = Raw{};
+      if (a >= 0) raw_k[i] = reinterpret_cast<const Raw*>(static_cast<const E4*>(key_base(p, false)) + a)[lane];
+      if (b >= 0) raw_v[i] = reinterpret_cast<const Raw*>(static_cast<const E4*>(key_base(p, true)) + b)[lane];
+    }
+  };
   find(k0 + warp * kKeys + lane);
+  if constexpr (kScaled) {
+    fetch();
+    find(k0 + (W + warp) * kKeys + lane);
+  }
 #pragma unroll 1
   for (int j0 = k0 + warp * kKeys; j0 < k1; j0 += W * kKeys) {
-    float k[kKeys][E], v[kKeys][E];
-    const int64_t ko = next_k, vo = next_v;
-    const float ks = next_ks, vs = next_vs;
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const int64_t a = __shfl_sync(0xffffffffu, ko, i), b = __shfl_sync(0xffffffffu, vo, i);
-#pragma unroll
-      for (int e = 0; e < E; ++e) k[i][e] = v[i][e] = 0.0f;
-      if (a >= 0) load_lane(lane, static_cast<const C*>(key_base(p, false)) + a, k[i]);
-      if (b >= 0) load_lane(lane, static_cast<const C*>(key_base(p, true)) + b, v[i]);
-    }
+    float k[kKeys][E], v[kKeys][E], ks = 0.0f;
     if constexpr (kScaled) {
+      ks = raw_ks;
 #pragma unroll
       for (int i = 0; i < kKeys; ++i) {
-        const float f = __shfl_sync(0xffffffffu, vs, i);
+        load_lane(0, reinterpret_cast<const E4*>(&raw_k[i]), k[i]);
+        load_lane(0, reinterpret_cast<const E4*>(&raw_v[i]), v[i]);
+        const float f = __shfl_sync(0xffffffffu, raw_vs, i);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[i][e] *= f;
       }
+      fetch();
+      find(j0 + 2 * W * kKeys + lane);
+    } else {
+      const int64_t ko = next_k, vo = next_v;
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) {
+        const int64_t a = __shfl_sync(0xffffffffu, ko, i), b = __shfl_sync(0xffffffffu, vo, i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) k[i][e] = v[i][e] = 0.0f;
+        if (a >= 0) load_lane(lane, static_cast<const C*>(key_base(p, false)) + a, k[i]);
+        if (b >= 0) load_lane(lane, static_cast<const C*>(key_base(p, true)) + b, v[i]);
+      }
+      find(j0 + W * kKeys + lane);
     }
-    find(j0 + W * kKeys + lane);
     // Dot products: value rr * kKeys + i of a butterfly is row rr, key i.
     float s[NB];  // this lane's row and key of each butterfly
 #pragma unroll
