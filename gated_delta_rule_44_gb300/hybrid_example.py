@@ -9,6 +9,10 @@ the projection, and projects back; a residual joins them.  The prompts go throug
 batch over the state pool, the conv pool and the paged cache that the prompts
 left.  ``generate`` returns every hidden row, so that serving in steps can be
 compared with the whole sequences in one batch.
+
+``beam_search`` keeps several continuations of each prompt: a prompt is computed once
+and forked, and every step's best continuations take the states and cache pages of the
+beams that they continue.  With ``cache_bits=8`` keys and values are cached in 8 bits.
 """
 from __future__ import annotations
 
@@ -16,6 +20,7 @@ from typing import List
 
 import torch
 
+from . import binding as B
 from .layer import AttnStep, GdnStep
 
 
@@ -26,7 +31,7 @@ class HybridStack:
     HQ, HKV, D, ROT, PAGE = 8, 2, 128, 64, 16           # attention layer
 
     def __init__(self, slots: int, max_tokens: int, device, seed: int = 0,
-                 dtype: torch.dtype = torch.bfloat16):
+                 dtype: torch.dtype = torch.bfloat16, cache_bits: int = 16):
         g = torch.Generator().manual_seed(seed)
         self.dev, self.dt, self.slots = torch.device(device), dtype, slots
 
@@ -49,22 +54,29 @@ class HybridStack:
                          q_norm=(1 + w(self.D, std=0.1)).to(dtype),
                          k_norm=(1 + w(self.D, std=0.1)).to(dtype))
         width = -(-max_tokens // self.PAGE)
-        self.k_cache = torch.zeros(slots * width, self.HKV, self.PAGE, self.D, dtype=dtype,
-                                   device=self.dev)
-        self.v_cache = torch.zeros_like(self.k_cache)
+        shape = (slots * width, self.HKV, self.PAGE, self.D)
+        kind = torch.uint8 if cache_bits == 8 else dtype
+        self.k_cache, self.v_cache = (torch.zeros(shape, dtype=kind, device=self.dev) for _ in range(2))
+        self.scales = {}
+        if cache_bits == 8:        # a scale for each page and head
+            self.k_cache, self.v_cache = (t.view(torch.float8_e4m3fn) for t in (self.k_cache, self.v_cache))
+            self.scales = {n: torch.zeros(slots * width, self.HKV, 1, device=self.dev)
+                           for n in ("k_scale", "v_scale")}
         self.table = torch.randperm(slots * width, generator=g).to(torch.int32).view(slots, width).to(self.dev)
         inv = 1e4 ** (-torch.arange(0, self.ROT, 2, dtype=torch.float64) / self.ROT)
         ang = torch.arange(max_tokens, dtype=torch.float64)[:, None] * inv
         self.cos_sin = torch.cat([ang.cos(), ang.sin()], 1).float().to(self.dev)
 
-    def step(self, x, lens: List[int], kv_lens: List[int], new: bool):
-        """Hidden rows x [T, HID] of sequences 0 .. N-1 with `lens` new tokens each,
-        their contexts `kv_lens` long afterwards; new: they start here."""
+    def step(self, x, lens: List[int], kv_lens: List[int], new: bool, slots=None):
+        """Hidden rows x [T, HID] of sequences with `lens` new tokens each, in `slots`
+        (int32, default 0 .. N-1), their contexts `kv_lens` long afterwards; new: they
+        start here."""
         T, N = x.shape[0], len(lens)
         nd = 0 if new else N
         cu = torch.tensor([0] + lens, dtype=torch.int64).cumsum(0).to(torch.int32).to(self.dev)
         kv = torch.tensor(kv_lens, dtype=torch.int32, device=self.dev)
-        slots = torch.arange(N, dtype=torch.int32, device=self.dev)
+        if slots is None:
+            slots = torch.arange(N, dtype=torch.int32, device=self.dev)
         begun = torch.full((N,), 0 if new else 1, dtype=torch.uint8, device=self.dev)
         C = 2 * self.HK * self.DK + self.HV * self.DV
         gdn = GdnStep(T, N, nd, self.HK, self.HV, self.DK, self.DV, self.K, self.dt, self.dev)
@@ -79,11 +91,34 @@ class HybridStack:
                 q = row[:, :2 * self.HQ * self.D].view(T, self.HQ, 2 * self.D)
                 kvr = row[:, 2 * self.HQ * self.D:].view(T, 2 * self.HKV, self.D)
                 y = attn.run(q[..., :self.D], kvr[:, :self.HKV], kvr[:, self.HKV:], cu, kv,
-                             self.table[:N], self.k_cache, self.v_cache, cu_seqlens_prefill=cu,
-                             gate=q[..., self.D:], q_norm_weight=L["q_norm"],
-                             k_norm_weight=L["k_norm"], cos_sin=self.cos_sin)
+                             self.table[slots.long()], self.k_cache, self.v_cache,
+                             cu_seqlens_prefill=cu, gate=q[..., self.D:], q_norm_weight=L["q_norm"],
+                             k_norm_weight=L["k_norm"], cos_sin=self.cos_sin, **self.scales)
             x = x + y.reshape(T, -1) @ L["w_out"]
         return x
+
+    def _states(self):
+        return [p for L in self.linear for p in (L["state"], L["tail"])]
+
+    def _pages(self):
+        return [self.k_cache, self.v_cache, *self.scales.values()]
+
+    def fork(self, src, dst):
+        """Slots dst become copies of slots src (int32, equal lengths)."""
+        B.gdn_copy_slots(self._states(), dst, src)
+        B.gdn_copy_slots(self._pages(), self.table[dst.long()].reshape(-1),
+                         self.table[src.long()].reshape(-1))
+
+    def reorder(self, parents, first: int, tokens: int):
+        """Slots in groups of W: place j of a group continues its place parents[g, j]
+        (int32 [groups, W]).  Contexts are the same before position `first` and `tokens`
+        long."""
+        groups, W = parents.shape
+        slots = torch.arange(groups * W, dtype=torch.int32, device=self.dev).view(groups, W)
+        B.gdn_copy_slots(self._states(), slots, parents, groups=True)
+        p0, p1 = first // self.PAGE, -(-tokens // self.PAGE)
+        pages = self.table[:groups * W, p0:p1].t().contiguous().view(-1, W)    # [pages * groups, W]
+        B.gdn_copy_slots(self._pages(), pages, parents.repeat(p1 - p0, 1), groups=True)
 
 
 def generate(stack: HybridStack, x, prompt_lens: List[int], total_lens: List[int]):
@@ -110,6 +145,37 @@ def generate(stack: HybridStack, x, prompt_lens: List[int], total_lens: List[int
     return out
 
 
+def beam_search(stack: HybridStack, vocab, prompts, beams: int, steps: int, end: int = -1):
+    """The `beams` best continuations of `steps` tokens for each prompt (token tensors).
+    vocab [V, HID]: a token's row, and the projection to the logits; end: the token that
+    ends a continuation.  Returns tokens [prompts, beams, steps], their log-probabilities
+    [prompts, beams], and each one's last hidden row [prompts, beams, HID]."""
+    dev, n, W = stack.dev, len(prompts), beams
+    lens = [len(p) for p in prompts]
+    slots = torch.arange(n * W, dtype=torch.int32, device=dev).view(n, W)
+    rows = stack.step(vocab[torch.cat(list(prompts)).to(dev)], lens, lens, True,
+                      slots=slots[:, 0].contiguous())
+    rows = rows[torch.tensor(lens).cumsum(0).to(dev) - 1]
+    if W > 1:
+        stack.fork(slots[:, :1].repeat(1, W - 1).view(-1), slots[:, 1:].contiguous().view(-1))
+    rows = rows[:, None].repeat(1, W, 1)
+    scores = torch.full((n, W), float("-inf"), device=dev)
+    scores[:, 0] = 0.0                                   # one beam is alive at first
+    ended = torch.zeros((n, W), dtype=torch.bool, device=dev)
+    tokens = torch.zeros((n, W, 0), dtype=torch.int32, device=dev)
+    for i in range(steps):
+        parents, new = (torch.empty((n, W), dtype=torch.int32, device=dev) for _ in range(2))
+        B.gdn_beam_select(rows.reshape(n * W, -1).matmul(vocab.t()).view(n, W, -1), scores, parents,
+                          new, scores, finished=ended, pad_token=max(end, 0))
+        at = parents.clamp(min=0).long()                 # (-1: fewer continuations than beams)
+        ended = torch.gather(ended, 1, at) | (new == end)
+        tokens = torch.cat([torch.gather(tokens, 1, at[..., None].expand(-1, -1, i)), new[..., None]], 2)
+        kv = [m + i + 1 for m in lens for _ in range(W)]
+        stack.reorder(parents, min(lens), max(kv) - 1)
+        rows = stack.step(vocab[new.clamp(min=0).view(-1).long()], [1] * (n * W), kv, False).view(n, W, -1)
+    return tokens, scores, rows
+
+
 def main() -> None:
     dev = torch.device("cuda:0")
     prompts, more = [37, 130, 1], 9
@@ -122,6 +188,13 @@ def main() -> None:
     print(f"{len(total)} sequences, {sum(total)} tokens: prompts and {more} single tokens each, "
           f"against whole sequences: max difference {diff:.3f} of rows of rms "
           f"{whole.float().square().mean().sqrt().item():.2f}")
+    vocab = (torch.randn(500, HybridStack.HID, generator=g) * 0.3).to(torch.bfloat16).to(dev)
+    asked = [torch.randint(0, 500, (n,), generator=g) for n in (19, 40)]
+    for bits in (16, 8):
+        stack = HybridStack(8, 60, dev, cache_bits=bits)
+        tokens, scores, _ = beam_search(stack, vocab, asked, beams=4, steps=8)
+        print(f"cache in {bits} bits, best of 4 beams: "
+              + "; ".join(f"{t.tolist()} ({s:.2f})" for t, s in zip(tokens[:, 0], scores[:, 0])))
 
 
 if __name__ == "__main__":

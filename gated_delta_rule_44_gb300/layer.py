@@ -148,38 +148,66 @@ class AttnStep:
             ws = max(ws, B.gdn_attn_paged_workspace_bytes(Tp, Np, Hq, Hkv, D, self.max_q_len, dt))
         # One after the other on one stream: the two calls share it.
         self.workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
+        self.dt = dt
+        self.widths = {}  # table width and page size: workspace bytes of the calls on a cache in 8 bits
 
     def run(self, q, k, v, cu_seqlens, kv_lens, block_table, k_cache, v_cache, *,
             cu_seqlens_prefill=None, gate=None, q_norm_weight=None, k_norm_weight=None,
-            norm_eps=1e-6, cos_sin=None, positions=None,
+            norm_eps=1e-6, cos_sin=None, positions=None, k_scale=None, v_scale=None,
             stream: Optional[torch.cuda.Stream] = None,
             out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """One step over the raw projections q, gate [T, Hq, D], k, v [T, Hkv, D]
         (views of any row stride).  Writes the new keys and values into the cache
         pages of block_table [N, max_pages], and the output to ``out`` (default:
         this object's own buffer), which it returns.  cu_seqlens_prefill: the
-        offsets of the sequences after the decode rows, rebased to 0."""
+        offsets of the sequences after the decode rows, rebased to 0.  With
+        k_scale and v_scale the cache is one in 8 bits (its workspace grows with
+        the first step over a wider table)."""
         nd = self.n_decode
         out = self.out if out is None else out
-        B.gdn_attn_prepare(q, k, v, cu_seqlens, self.q, kv_lens=kv_lens, block_table=block_table,
-                           k_cache=k_cache, v_cache=v_cache, k_out=self.k,
-                           q_norm_weight=q_norm_weight, k_norm_weight=k_norm_weight,
-                           norm_eps=norm_eps, cos_sin=cos_sin, positions=positions, stream=stream)
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("a cache in 8 bits has k_scale and v_scale")
+        eight = k_scale is not None
+        if eight:
+            self._grow8(block_table.shape[1], k_cache.shape[2])
+        scales = (k_scale, v_scale) if eight else ()
+        prepare, paged = ((B.gdn_attn8_prepare, B.gdn_attn8_paged) if eight
+                          else (B.gdn_attn_prepare, B.gdn_attn_paged))
+        prepare(q, k, v, cu_seqlens, self.q, kv_lens=kv_lens, block_table=block_table,
+                k_cache=k_cache, v_cache=v_cache, k_out=self.k, q_norm_weight=q_norm_weight,
+                k_norm_weight=k_norm_weight, norm_eps=norm_eps, cos_sin=cos_sin,
+                positions=positions, stream=stream,
+                **(dict(k_scale=k_scale, v_scale=v_scale) if eight else {}))
         if nd > 0:
-            B.gdn_attn_paged(self.q[:nd], k_cache, v_cache, block_table[:nd], kv_lens[:nd], None,
-                             out[:nd], max_q_len=1, scale=self.scale,
-                             gate=None if gate is None else gate[:nd], workspace=self.workspace,
-                             stream=stream)
+            paged(self.q[:nd], k_cache, v_cache, *scales, block_table[:nd], kv_lens[:nd], None,
+                  out[:nd], max_q_len=1, scale=self.scale, gate=None if gate is None else gate[:nd],
+                  workspace=self.workspace, stream=stream)
         if self.N > nd:
             g = None if gate is None else gate[nd:]
             if self.new_prompts:
                 B.gdn_attn_varlen(self.q[nd:], self.k[nd:], v[nd:], cu_seqlens_prefill, out[nd:],
                                   scale=self.scale, gate=g, stream=stream)
             else:
-                B.gdn_attn_paged(self.q[nd:], k_cache, v_cache, block_table[nd:], kv_lens[nd:],
-                                 cu_seqlens_prefill, out[nd:], max_q_len=self.max_q_len,
-                                 scale=self.scale, gate=g, workspace=self.workspace, stream=stream)
+                paged(self.q[nd:], k_cache, v_cache, *scales, block_table[nd:], kv_lens[nd:],
+                      cu_seqlens_prefill, out[nd:], max_q_len=self.max_q_len, scale=self.scale,
+                      gate=g, workspace=self.workspace, stream=stream)
         return out
+
+    def _grow8(self, width: int, page: int) -> None:
+        """Room for the calls on a cache in 8 bits with tables of this width."""
+        if (width, page) in self.widths:
+            return
+        nd, Tp, Np = self.n_decode, self.T - self.n_decode, self.N - self.n_decode
+        need = 0
+        if nd > 0:
+            need = B.gdn_attn8_paged_workspace_bytes(nd, nd, self.Hq, self.Hkv, self.D, 1, self.dt,
+                                                     width, page)
+        if Np > 0 and not self.new_prompts:
+            need = max(need, B.gdn_attn8_paged_workspace_bytes(Tp, Np, self.Hq, self.Hkv, self.D,
+                                                               self.max_q_len, self.dt, width, page))
+        if need > self.workspace.numel():
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.workspace.device)
+        self.widths[(width, page)] = need
 
 
 class GdnHostPipeline:

@@ -1,0 +1,107 @@
+"""GPU: the selection, the forks and reorders, and the cache in either width together, as a
+beam search over the hybrid stack runs them; the step helper on a cache in 8 bits."""
+import pytest
+import torch
+
+import attn8_reference as Q
+import attn_reference as R
+from gated_delta_rule_44_gb300 import binding as B
+from gated_delta_rule_44_gb300 import hybrid_example as E
+from gated_delta_rule_44_gb300.layer import AttnStep
+from test_gpu_attn8 import E4M3, bounds, make_cache8
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("lens,beams,steps", [([19, 40], 4, 7), ([5], 3, 20), ([17, 16, 1], 2, 4)])
+def test_beams_have_their_own_histories(bits, lens, beams, steps, cuda_device):
+    """Every beam's last row is that of its tokens served by themselves: states, conv tails and
+    pages followed the selection.  (The batches differ, so that sums are split elsewhere: rows
+    may differ by a few 2^-8 after eight stored projections.)  Its score is the sum of its
+    tokens' log-probabilities there."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(sum(lens) + bits)
+    V = 300
+    vocab = (torch.randn(V, E.HybridStack.HID, generator=g) * 0.3).to(BF).to(dev)
+    prompts = [torch.randint(0, V, (n,), generator=g) for n in lens]
+    n, top = len(lens), max(lens) + steps
+    tokens, scores, rows = E.beam_search(E.HybridStack(n * beams, top, dev, cache_bits=bits), vocab, prompts,
+                                         beams, steps)
+    B.gdn_read_device_status()
+    assert tokens.shape == (n, beams, steps) and (tokens >= 0).all()
+    assert (scores[:, :-1] >= scores[:, 1:]).all()
+    for b in range(n):        # beams of a search differ
+        assert len({tuple(t) for t in tokens[b].tolist()}) == beams
+    seqs = [torch.cat([prompts[b].to(dev), tokens[b, w].long()]) for b in range(n) for w in range(beams)]
+    own = E.generate(E.HybridStack(n * beams, top, dev, cache_bits=bits), vocab[torch.cat(seqs)],
+                     [m for m in lens for _ in range(beams)], [m + steps for m in lens for _ in range(beams)])
+    B.gdn_read_device_status()
+    at = 0
+    rms = rows.float().square().mean().sqrt().item()
+    for b in range(n):
+        for w in range(beams):
+            mine = own[at:at + lens[b] + steps].float()
+            at += lens[b] + steps
+            err = (mine[-1] - rows[b, w].float()).square().mean().sqrt().item()
+            assert err <= 16 * 2.0 ** -8 * rms, (b, w, err, rms)
+            logp = torch.log_softmax(mine[lens[b] - 1:-1] @ vocab.float().t(), -1)
+            total = logp.gather(1, tokens[b, w].long()[:, None]).sum().item()
+            # a row off by e moves a logit by |vocab row| e sqrt(HID) / sqrt(HID) at the most
+            slack = steps * 2 * 16 * 2.0 ** -8 * rms * vocab.float().norm(dim=1).max().item()
+            assert abs(total - scores[b, w].item()) <= slack
+
+
+def test_ended_beams_stay(cuda_device):
+    """A beam that ends goes on as padding with its score; the search's best stays sorted."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(3)
+    V, W, steps = 40, 4, 6
+    vocab = (torch.randn(V, E.HybridStack.HID, generator=g) * 0.2).to(BF).to(dev)
+    prompts = [torch.randint(0, V, (n,), generator=g) for n in (9, 21)]
+    for end in (0, 3, 7):
+        tokens, scores, _ = E.beam_search(E.HybridStack(2 * W, 40, dev), vocab, prompts, W, steps, end=end)
+        B.gdn_read_device_status()
+        assert (scores[:, :-1] >= scores[:, 1:]).all()
+        for seq in tokens.view(-1, steps).tolist():
+            if end in seq:
+                assert all(t == end for t in seq[seq.index(end):])
+
+
+@pytest.mark.parametrize("new_prompts", [True, False])
+def test_step_on_a_cache_in_8_bits(new_prompts, cuda_device):
+    """Three decode rows and two prompts (or chunks over an earlier context) in one batch,
+    against the 64-bit forms on the rows and codes that the step stored."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(3)
+    Hq, Hkv, D, page, block = 8, 2, 128, 32, 16
+    ql = [1, 1, 1, 40, 150]
+    before = [4, 299, 0, 0, 0] if new_prompts else [4, 299, 0, 50, 20]
+    kl = [a + b for a, b in zip(before, ql)]
+    T, N, nd = sum(ql), 5, 3
+    c, _ = make_cache8(g, kl, Hkv, D, page, block, dev)
+    row = torch.randn(T, (2 * Hq + 2 * Hkv) * D, generator=g).to(BF).to(dev)
+    qg = row[:, :2 * Hq * D].view(T, Hq, 2 * D)
+    kv = row[:, 2 * Hq * D:].view(T, 2 * Hkv, D)
+    cs = torch.randn(320, 64, generator=g).to(dev)
+    cu = torch.tensor([0] + ql).cumsum(0).to(torch.int32).to(dev)
+    step = AttnStep(T, N, nd, Hq, Hkv, D, BF, dev, max_q_len=150, new_prompts=new_prompts)
+    out = step.run(qg[..., :D], kv[:, :Hkv], kv[:, Hkv:], cu, torch.tensor(kl, dtype=torch.int32, device=dev),
+                   c["block_table"], c["k_cache"], c["v_cache"], cu_seqlens_prefill=(cu[nd:] - nd).contiguous(),
+                   gate=qg[..., D:], cos_sin=cs, k_scale=c["k_scale"], v_scale=c["v_scale"])
+    B.gdn_read_device_status()
+    cpu = [c[n].cpu() for n in ("k_cache", "k_scale", "v_cache", "v_scale", "block_table")]
+    ro, _, pieces = Q.paged(step.q, *cpu, kl, ql, D ** -0.5, qg[..., D:])
+    got, tol = R.f64(out), bounds(pieces, ro, BF)
+    R.check(got[:nd], ro[:nd], tol[:nd], "decode")
+    if new_prompts:        # prompts attend to their keys as they are
+        kk, vv = R.f64(step.k)[nd:], R.f64(kv[nd:, Hkv:])
+        rp, _, pp = R._packed(R.f64(step.q)[nd:], [(kk[:40], vv[:40], 0), (kk[40:], vv[40:], 0)], ql[nd:],
+                              D ** -0.5, R.f64(qg[nd:, :, D:]))
+        R.check(got[nd:], rp, R.bound(rp, pp, BF, True), "prompts")
+    else:
+        R.check(got[nd:], ro[nd:], tol[nd:], "chunks")
+    with pytest.raises(ValueError):
+        step.run(qg[..., :D], kv[:, :Hkv], kv[:, Hkv:], cu, None, c["block_table"], c["k_cache"], c["v_cache"],
+                 k_scale=c["k_scale"])
