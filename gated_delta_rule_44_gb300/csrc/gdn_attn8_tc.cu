@@ -70,7 +70,7 @@ struct Shared {
   int abort;
   int redone;  // rows evaluated again so far, and parts of them
   uint32_t k_loads[kMaxRing], v_loads[kMaxRing];  // issued so far
-  int start_s, start_hkv, start_u;
+  int start_s, start_hkv, start_rt, start_u;
   long long left, total;
   long long scan[20];
   uint32_t redo[kMaxGroups][2];                      // rows to evaluate again, by range parity
@@ -109,6 +109,7 @@ struct Tc8Args {
   int pb;      // rows of a load: a tile's keys, or a divisor of the page
   int ctas;    // the grid
   int rows;    // rows of a workspace block
+  int tq;      // tokens of a pair's row tile
   int4* info;  // per CTA, see stream_info
   float* ws;   // the sums
 };
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   }
   wait_for_previous_kernel();
   start_next_kernel();
-  stream_start<C::kThreads>(p, a.ctas, sh);
+  stream_start<C::kThreads>(p, a.ctas, a.tq, sh);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   if (warp == 0) {
     // ---- ranges, loads of K ----
     auto role = [&] {
-      SegIter iter{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
+      SegIter iter{sh->start_s, sh->start_hkv, sh->start_rt, sh->start_u, (int)blockIdx.x, a.tq, sh->left};
       for (int n = 0;; ++n) {
         Seg g;
         if (!iter.next(p, g)) g.s = -1;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     };
     role();
   } else if (warp == 3) {
-    if (lane == 0) a.info[blockIdx.x] = stream_info(p, a.ctas, sh);
+    if (lane == 0) a.info[blockIdx.x] = stream_info(p, a.ctas, a.tq, sh);
     // Sequences without a key.
     for (int s = blockIdx.x; s < p.N; s += a.ctas) {
       const SeqRange q = seq_range(p, s);
@@ -817,6 +818,7 @@ bool codes_map(CUtensorMap* m, const AttnPages& c, const AttnLaunch& p, int pb) 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kMostRows = 256;
 constexpr int row_class(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 template <int D, int R>
@@ -826,7 +828,9 @@ cudaError_t run(const AttnLaunch& p, cudaStream_t st) {
   a.pb = BK;
   while (p.page_size % a.pb != 0) a.pb >>= 1;
   a.ctas = C::kCtas * chunk::sm_count();
-  a.rows = p.max_q * (p.Hq / p.Hkv);
+  const int G = p.Hq / p.Hkv;
+  a.tq = std::min(p.max_q, R / G);  // (G <= R)
+  a.rows = a.tq * G;
   a.info = static_cast<int4*>(p.ws);
   a.ws = reinterpret_cast<float*>(static_cast<char*>(p.ws) + info_bytes(a.ctas));
   CUtensorMap mk, mv;
@@ -857,12 +861,15 @@ int ctas_per_sm(int64_t rows) {
 
 }  // namespace
 
-bool attn8_tc_supported(int64_t rows, int64_t D, bool bf16) { return bf16 && D >= 64 && rows <= 64; }
+// More than 64 rows read their keys again for every 64; against widening first, 128 rows
+// take 320 and 600 us (128 sequences of 4096 keys, 4 kv heads of 128), 40 and 66 (one of
+// 32768), 256 rows 619 and 555, 59 and 68, 512 rows 84 and 84 (one).
+bool attn8_tc_supported(int64_t rows, int64_t D, bool bf16) { return bf16 && D >= 64 && rows <= kMostRows; }
 
 size_t attn8_tc_workspace_bytes(int64_t rows, int64_t D) {
   const int per = D == 64 ? ctas_per_sm<64>(rows) : D == 128 ? ctas_per_sm<128>(rows) : ctas_per_sm<256>(rows);
   const int ctas = per * chunk::sm_count();
-  return info_bytes(ctas) + Partials::bytes(2 * (int64_t)ctas, (int)rows, D);
+  return info_bytes(ctas) + Partials::bytes(2 * (int64_t)ctas, (int)std::min<int64_t>(rows, 64), D);
 }
 
 cudaError_t launch_attn8_tc(const AttnLaunch& p, cudaStream_t st) {

@@ -2,7 +2,8 @@
 // whole warps, elected issue, and the stream form's work, in which the key tiles of all
 // (sequence, kv head) pairs, in order, are cut into equal consecutive ranges, one per CTA,
 // whatever the lengths.  A pair cut between CTAs leaves its sums in a workspace, and a
-// second kernel joins them in the order of their keys.
+// second kernel joins them in the order of their keys.  A sequence with more than tq new
+// tokens makes a pair of its own for every tq of them.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -29,10 +30,13 @@ struct Seg {
 __device__ __forceinline__ int key_tiles(const SeqRange& q) {
   return q.b > q.a ? (q.kv + BK - 1) / BK : 0;
 }
+__device__ __forceinline__ int row_tiles(const AttnLaunch& p, const SeqRange& q, int tq) {
+  return (min(q.b - q.a, p.max_q) + tq - 1) / tq;
+}
 
 // The ranges of one CTA of the stream form.
 struct SegIter {
-  int s, hkv, u, cta;
+  int s, hkv, rt, u, cta, tq;
   int64_t left;
   __device__ bool next(const AttnLaunch& p, Seg& g) {
     if (left <= 0) return false;
@@ -47,9 +51,9 @@ struct SegIter {
     const int take = (int)min((int64_t)(n - u), left);
     g.s = s;
     g.hkv = hkv;
-    g.t0 = q.a;
-    g.nt = min(q.b - q.a, p.max_q);
-    g.pos0 = q.kv - (q.b - q.a);
+    g.t0 = q.a + rt * tq;
+    g.nt = min(tq, min(q.b - q.a, p.max_q) - rt * tq);
+    g.pos0 = q.kv - (q.b - q.a) + rt * tq;
     g.hi = q.kv;
     g.kt0 = u;
     g.kt1 = u + take;
@@ -58,9 +62,12 @@ struct SegIter {
     u += take;
     if (u == n) {
       u = 0;
-      if (++hkv == p.Hkv) {
-        hkv = 0;
-        ++s;
+      if (++rt == row_tiles(p, q, tq)) {
+        rt = 0;
+        if (++hkv == p.Hkv) {
+          hkv = 0;
+          ++s;
+        }
       }
     }
     return true;
@@ -152,10 +159,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Where CTA blockIdx.x of `ctas` begins, into sh->start_s, start_hkv, start_u, and how many
+// Where CTA blockIdx.x of `ctas` begins, into sh->start_s, start_hkv, start_rt, start_u, and how many
 // key tiles it has (sh->left); by the whole CTA, which synchronises before it reads them.
 template <int kThreads, typename Sh>
-__device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, Sh* sh) {
+__device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, int tq, Sh* sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // Prefix sum of the key tiles over the sequences, a run of them per thread.
   const int per = (p.N + kThreads - 1) / kThreads;
@@ -164,7 +171,7 @@ __device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, Sh* 
   unsigned bad = 0;
   for (int s = s0; s < s1; ++s) {
     const SeqRange q = seq_range(p, s);
-    mine += key_tiles(q);
+    mine += (long long)key_tiles(q) * row_tiles(p, q, tq);
     bad |= q.bad;
   }
   if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
@@ -192,33 +199,37 @@ __device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, Sh* 
   if (w1 > w0 && before * p.Hkv <= w0 && w0 < (before + mine) * p.Hkv) {
     long long at = before * p.Hkv;
     for (int s = s0; s < s1; ++s) {
-      const int n = key_tiles(seq_range(p, s));
-      if (w0 < at + (long long)n * p.Hkv) {
+      const SeqRange q = seq_range(p, s);
+      const int n = key_tiles(q);
+      const long long all = (long long)n * row_tiles(p, q, tq);  // of a kv head
+      if (w0 < at + all * p.Hkv) {
         sh->start_s = s;
-        sh->start_hkv = (int)((w0 - at) / n);
-        sh->start_u = (int)((w0 - at) % n);
+        sh->start_hkv = (int)((w0 - at) / all);
+        sh->start_rt = (int)((w0 - at) % all / n);
+        sh->start_u = (int)((w0 - at) % all % n);
         break;
       }
-      at += (long long)n * p.Hkv;
+      at += all * p.Hkv;
     }
   }
 }
 
 // What the joining kernel needs of CTA blockIdx.x's ranges, by one thread:
-// {s, kv head of the pair it began and left open (s = -1: none), how its first range ends:
-// 0 open, 1 the pair's end, 2 no range at all; the CTA that ends the pair it left open}.
+// {s, kv head + 2^16 row tile of the pair it began and left open (s = -1: none), how its first
+// range ends: 0 open, 1 the pair's end, 2 no range at all; the CTA that ends the pair it left open}.
 template <typename Sh>
-__device__ __forceinline__ int4 stream_info(const AttnLaunch& p, int ctas, const Sh* sh) {
+__device__ __forceinline__ int4 stream_info(const AttnLaunch& p, int ctas, int tq, const Sh* sh) {
   int4 r = make_int4(-1, 0, 2, 0);
-  SegIter every{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
+  SegIter every{sh->start_s, sh->start_hkv, sh->start_rt, sh->start_u, (int)blockIdx.x, tq, sh->left};
   long long at = sh->total * blockIdx.x / ctas;  // tiles before the range
   Seg g;
   for (bool first = true; every.next(p, g); first = false) {
-    const int n = key_tiles(seq_range(p, g.s));
+    const SeqRange q = seq_range(p, g.s);
+    const int n = key_tiles(q);
     if (first) r.z = g.kt1 == n ? 1 : 0;
     if (g.kt0 == 0 && g.kt1 < n) {
       r.x = g.s;
-      r.y = g.hkv;
+      r.y = g.hkv + ((g.t0 - q.a) / tq << 16);
       // The CTA with the pair's last tile, total c / ctas <= last < total (c + 1) / ctas.
       const long long last = at + n - 1;
       long long c = last * ctas / sh->total;
@@ -234,8 +245,8 @@ __device__ __forceinline__ int4 stream_info(const AttnLaunch& p, int ctas, const
 // that range c began and left open, a row of it per blockIdx.y and its multiples;
 // its further sums are in the blocks of the CTAs after it, in the order of their
 // keys.
-// `a` has the grid of the streaming kernel (ctas), its int4 info per CTA, the sums (ws) and
-// the rows of a block of them.
+// `a` has the grid of the streaming kernel (ctas), its int4 info per CTA, the sums (ws), the
+// rows of a block of them and tq.
 // FEW: pairs in few ranges are joined by a warp a row, eight rows to a CTA.  (Drafts of 128
 // sequences, every one of 304 CTAs leaving a pair of 16 rows open: 15 us of 208 went into
 // 4900 CTAs of eight warps for two ranges.)
@@ -248,7 +259,8 @@ __device__ __forceinline__ void stream_join(const AttnLaunch& p, const Args& a) 
   if (mine.x < 0) return;
   const int G = p.Hq / p.Hkv;
   const SeqRange q = seq_range(p, mine.x);
-  const int rows = min(q.b - q.a, p.max_q) * G;
+  const int hkv = mine.y & 0xffff, first = (mine.y >> 16) * a.tq;  // tokens before the row tile's
+  const int rows = min(a.tq, min(q.b - q.a, p.max_q) - first) * G;
   if ((int)blockIdx.y >= rows) return;
   const int c1 = mine.w;  // the last range's CTA
   const Partials part(a.ws, 2 * (int64_t)a.ctas, a.rows, D);
@@ -259,12 +271,12 @@ __device__ __forceinline__ void stream_join(const AttnLaunch& p, const Args& a) 
   if (FEW && c1 - c0 < 8) {
     for (int r0 = 8 * blockIdx.y; r0 < rows; r0 += 8 * gridDim.y) {
       const int r = r0 + (threadIdx.x >> 5);
-      join_row<T, D, 1>(p, part, c1 - c0 + 1, slot_of, r, r < rows, q.a + r / G, mine.y * G + r % G);
+      join_row<T, D, 1>(p, part, c1 - c0 + 1, slot_of, r, r < rows, q.a + first + r / G, hkv * G + r % G);
     }
     return;
   }
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    join_row<T, D, 8>(p, part, c1 - c0 + 1, slot_of, r, true, q.a + r / G, mine.y * G + r % G);
+    join_row<T, D, 8>(p, part, c1 - c0 + 1, slot_of, r, true, q.a + first + r / G, hkv * G + r % G);
     __syncthreads();
   }
 }

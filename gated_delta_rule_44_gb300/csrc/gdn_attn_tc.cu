@@ -107,7 +107,7 @@ struct Shared {
   int abort;
   int redone;  // rows evaluated again so far, and parts of them
   uint32_t k_loads[kMaxRing], v_loads[kMaxRing], v_lands[kMaxRing], q_loads, clc_asked;  // issued so far
-  int start_s, start_hkv, start_u;
+  int start_s, start_hkv, start_rt, start_u;
   long long left, total;
   long long scan[20];
   // What the two warps of 32 rows exchange, 256 bytes twice for each of the four
@@ -142,6 +142,7 @@ struct TcArgs {
   int pbk, pbv; // rows of a load of K, of V: a unit's keys, or a divisor of the page
   int ctas;     // stream form: the grid
   int rows;     // rows of a workspace block
+  int tq;       // stream form: tokens of a pair (all of a sequence's)
   int4* info;   // stream form, per CTA: see stream_info
   float* ws;    // the sums
 };
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   } else if (warp == 2) {
     tmem_alloc(smem_u32(&sh->tmem), 512);
   }
-  if constexpr (STREAM) stream_start<C::kThreads>(p, a.ctas, sh);
+  if constexpr (STREAM) stream_start<C::kThreads>(p, a.ctas, a.tq, sh);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     // ---- work; loads of Q and K ----
     SegIter iter{};
     if constexpr (STREAM)
-      iter = SegIter{sh->start_s, sh->start_hkv, sh->start_u, (int)blockIdx.x, sh->left};
+      iter = SegIter{sh->start_s, sh->start_hkv, sh->start_rt, sh->start_u, (int)blockIdx.x, a.tq, sh->left};
     auto role = [&] {
       Ring ring;
       uint32_t filled = 0;  // units so far
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       // What the joining kernel needs of this CTA's ranges; the outputs of
       // sequences without a key.
       if (lane == 0) {
-        a.info[blockIdx.x] = stream_info(p, a.ctas, sh);
+        a.info[blockIdx.x] = stream_info(p, a.ctas, a.tq, sh);
       }
       for (int s = blockIdx.x; s < p.N; s += a.ctas) {
         const SeqRange q = seq_range(p, s);
@@ -1030,6 +1031,7 @@ cudaError_t launch(const AttnLaunch& p, cudaStream_t st) {
     a.q_box = std::min(a.TQ, p.max_q);
     a.ctas = sms;
     a.rows = p.max_q * G;
+    a.tq = p.max_q;
     a.info = static_cast<int4*>(p.ws);
     a.ws = reinterpret_cast<float*>(static_cast<char*>(p.ws) + info_bytes(sms));
     cudaError_t e = run<D, 1, true, true>(p, a, dim3(sms), st);

@@ -304,7 +304,11 @@ PAGED = [
     ([3, 2], [260, 140], 16, 1, 256, 128, 128, BF, False, "head"),
     ([1, 2], [70, 300], 64, 1, 128, 32, 32, BF, False, "head"),       # the widest group
     ([4, 6], [2, 40], 5, 1, 64, 16, 16, BF, False, "head"),            # tokens without a key
-    ([40, 7], [300, 7], 8, 2, 128, 64, 32, BF, True, "head"),          # many rows: widened
+    ([40, 7], [300, 7], 8, 2, 128, 64, 32, BF, True, "head"),          # several tiles of rows
+    ([20, 1, 0, 40], [500, 300, 9, 41], 12, 2, 128, 32, 16, BF, False, "token"),
+    ([4, 3], [700, 2], 64, 1, 64, 64, 32, BF, True, "head"),
+    ([9, 16, 5], [129, 1100, 260], 15, 1, 256, 48, 16, BF, False, "head"),
+    ([90, 7], [300, 7], 8, 2, 128, 64, 32, BF, True, "head"),          # many rows: widened
     ([130], [200], 4, 1, 256, 16, 16, BF, False, "token"),
     ([17, 100], [400, 100], 6, 2, 64, 112, 16, BF, False, "head"),
     ([1, 3, 0], [90, 40, 9], 4, 2, 32, 32, 16, BF, False, "head"),
@@ -442,7 +446,7 @@ def test_paged8_bad_pages(cuda_device):
         torch.testing.assert_close(outs[0], outs[1], rtol=2.0 ** -7, atol=1e-3)
 
 
-@pytest.mark.parametrize("dtype,q_len", [(BF, 1), (BF, 3), (BF, 40), (F32, 1)])
+@pytest.mark.parametrize("dtype,q_len", [(BF, 1), (BF, 3), (BF, 40), (BF, 70), (F32, 1)])
 def test_paged8_repeats_streams_and_graphs(dtype, q_len, cuda_device):
     """Bit for bit the same on another stream, in a graph replayed over changed inputs, and
     beside another call in flight."""
