@@ -96,13 +96,10 @@ struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
   uint4 r;
   __device__ void load(const __nv_bfloat16* p) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ void get(float (&x)[8]) const {
+  __device__ void get(float2 (&x)[4]) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
   }
   __device__ uint4 bits() const { return r; }
   __device__ void from(const uint4& b) { r = b; }
@@ -117,42 +114,33 @@ struct Vec<float> {
   static constexpr int N = 4;
   float4 r;
   __device__ void load(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
-  __device__ void get(float (&x)[4]) const {
-    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
+  __device__ void get(float2 (&x)[2]) const {
+    x[0] = {r.x, r.y};
+    x[1] = {r.z, r.w};
   }
   __device__ uint4 bits() const { return *reinterpret_cast<const uint4*>(&r); }
   __device__ void from(const uint4& b) { r = *reinterpret_cast<const float4*>(&b); }
   __device__ float top() const { return fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)); }
 };
 
-// A value that at least K of the threads' values reach, near the K-th largest: by the whole
-// CTA (two barriers).
-__device__ __forceinline__ float common_floor(float t, int K, uint32_t* shared) {
-  shared[threadIdx.x] = order_of(t);
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const uint4 a = reinterpret_cast<const uint4*>(shared)[threadIdx.x];
-    const uint4 b = reinterpret_cast<const uint4*>(shared)[threadIdx.x + 32];
-    uint32_t bound = 0;
-#pragma unroll
-    for (int bit = 30; bit >= 16; bit -= 2) {
-      uint32_t step = 0;  // the largest of three that K values still reach
-#pragma unroll
-      for (uint32_t q = 1; q <= 3; ++q) {
-        const uint32_t x = bound | q << bit;
-        const int n = (a.x >= x) + (a.y >= x) + (a.z >= x) + (a.w >= x) + (b.x >= x) + (b.y >= x) +
-                      (b.z >= x) + (b.w >= x);
-        if (__reduce_add_sync(0xffffffffu, n) >= K) step = q;
-      }
-      bound |= step << bit;
-    }
-    __syncwarp();
-    if (threadIdx.x == 0) shared[0] = bound;
+// The warp's largest value; a NaN is passed over.
+__device__ __forceinline__ float warp_top(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A value that at least `n` of the warp's values reach, -inf if fewer are above that: its
+// n-th largest.
+__device__ __forceinline__ float nth_top(float x, int n) {
+  float y = warp_top(x);
+  for (;;) {
+    const unsigned equal = __ballot_sync(0xffffffffu, x == y);
+    n -= __popc(equal);
+    if (n <= 0 || y == -INFINITY) return y;
+    if (x == y) x = -INFINITY;
+    y = warp_top(x);
   }
-  __syncthreads();
-  // (below the order of -inf there is no number: nothing is known yet)
-  const uint32_t bound = shared[0];
-  return bound < 0x007fffffu ? -INFINITY : value_of(bound);
 }
 
 template <typename T>
@@ -163,9 +151,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
   __shared__ uint4 aside[kAside];
   __shared__ int aside_at[kAside];
   __shared__ unsigned long long few[kRanked];
-  __shared__ __align__(16) uint32_t tops_of[kThreads];
-  __shared__ float wref[kWarps];
-  __shared__ double wsum[kWarps];
+  __shared__ volatile float floors[kWarps];  // values that K / kWarps of a warp's threads have reached
+  __shared__ float refs[kThreads], parts[kThreads];
   __shared__ unsigned long long best[kWarps];
   __shared__ int count, few_count;
   using V = Vec<T>;
@@ -183,24 +170,30 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
   const T* x = static_cast<const T*>(p.logits) + blockIdx.z * p.batch_stride + blockIdx.y * p.beam_stride;
   const int v0 = min((int64_t)p.V, (int64_t)seg * seg_len), v1 = (int)min((int64_t)p.V, (int64_t)v0 + seg_len);
   if (tid == 0) count = few_count = 0;
+  if (lane == 0) floors[warp] = -INFINITY;
   // The row's 16-byte boundaries: logits before the first and behind the last go one by one.
   const int mis = (int)((reinterpret_cast<uintptr_t>(x + v0) & 15u) / sizeof(T));
   const int head = min(v1 - v0, mis ? V::N - mis : 0);
   const int vecs = (v1 - v0 - head) / V::N;
   const int tail0 = v0 + head + vecs * V::N;
   const T* body = x + v0 + head;
-  float top = -INFINITY;               // this thread's largest logit
-  float ref = -INFINITY, sum = 0.0f;   // its sum of 2^(H x - ref)
-  float use = 0.0f;                    // ref, or 0 while that is -inf
-  float floor_ = -INFINITY;            // logits below it are not among the segment's K
-  auto add = [&](float y) { sum += ex2(fmaf(y, kH, -use)); };
+  float top = -INFINITY;  // this thread's largest logit
+  float ref = -INFINITY;  // its sum of 2^(H x - ref), in two parts
+  float2 sum = {0.0f, 0.0f};
+  float use = 0.0f;          // -ref, or 0 while that is -inf
+  float floor_ = -INFINITY;  // logits below it are not among the segment's K
   auto raise = [&](float y) {
     if (y > top) {
       top = y;
       const float r = ceilf(y * kH);
       if (r > ref) {
-        if (ref != -INFINITY) sum *= ex2(ref - r);  // (a sum of NaN stays one)
-        ref = use = r;
+        if (ref != -INFINITY) {  // (a sum of NaN stays one)
+          const float f = ex2(ref - r);
+          sum.x *= f;
+          sum.y *= f;
+        }
+        ref = r;
+        use = -r;
       }
     }
   };
@@ -212,7 +205,6 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
     }
   };
   __syncthreads();
-  int next_floor = 1, since = 0;  // chunks after which the floor is taken, and since it was
   constexpr int kChunk = kThreads * kUnroll;
   V r[kUnroll], ahead[kUnroll];
   auto load = [&](int base, bool whole) {
@@ -222,7 +214,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
       if (whole || i < vecs) ahead[u].load(body + (int64_t)i * V::N);
     }
   };
-  int chunk = 1;
+  // The least of the warps' floors: a value that at least K logits have reached.
+  auto read_floor = [&] {
+    float f = floors[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) f = fminf(f, floors[w]);
+    floor_ = f;
+  };
+  const int share = (K + kWarps - 1) / kWarps;
   auto work = [&](int base, bool whole) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) r[u] = ahead[u];
@@ -235,32 +234,38 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
       most = fmaxf(most, tops[u]);
     }
     raise(most);
+    const float2 h2 = {kH, kH}, use2 = {use, use};
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (!whole && base + u * kThreads + tid >= vecs) continue;
-      float y[V::N];
+      float2 y[V::N / 2];
       r[u].get(y);
 #pragma unroll
-      for (int e = 0; e < V::N; ++e) add(y[e]);
+      for (int e = 0; e < V::N / 2; ++e) {
+        const float2 t = __ffma2_rn(y[e], h2, use2);
+        sum = __fadd2_rn(sum, float2{ex2(t.x), ex2(t.y)});
+      }
     }
-    if (chunk == next_floor || floor_ == -INFINITY) {  // the same in all threads
-      floor_ = common_floor(top, K, tops_of);
-      if (chunk == next_floor) next_floor *= 8;
-      since = 0;
-    }
-    if (most >= floor_ && most > -INFINITY) {
+    // Only a warp with a logit that reaches the floor that it knows looks for a newer one.
+    // (floors only rise: an old one lets more pass.)
+    if (__any_sync(0xffffffffu, base == 0 || most >= floor_)) {
+      const float mine = nth_top(top, share);
+      if (lane == 0) floors[warp] = mine;
+      if (base == 0) __syncthreads();  // (every warp is here, with nothing known yet)
+      else __syncwarp();
+      read_floor();
+      if (most >= floor_ && most > -INFINITY) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        if (tops[u] >= floor_ && tops[u] > -INFINITY) {
-          const int at = atomicAdd(&count, 1);
-          if (at < kAside) {
-            aside[at] = r[u].bits();
-            aside_at[at] = base + u * kThreads + tid;
+        for (int u = 0; u < kUnroll; ++u)
+          if (tops[u] >= floor_ && tops[u] > -INFINITY) {
+            const int at = atomicAdd(&count, 1);
+            if (at < kAside) {
+              aside[at] = r[u].bits();
+              aside_at[at] = base + u * kThreads + tid;
+            }
           }
-        }
+      }
     }
-    ++chunk;
-    ++since;
   };
   load(0, false);
   int base = 0;
@@ -271,39 +276,52 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
   const float ragged_y = ragged ? attn::to_f(x[ragged_v]) : -INFINITY;
   if (ragged) {
     raise(ragged_y);
-    add(ragged_y);
+    sum.x += ex2(fmaf(ragged_y, kH, use));
   }
-  // The threads' sums.
-  float most = ref;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (lane == 0) wref[warp] = most;
-  if (since > 1) floor_ = common_floor(top, K, tops_of);
+  refs[tid] = ref;
+  parts[tid] = sum.x + sum.y;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) most = fmaxf(most, wref[w]);
-  double d = (double)(ref == -INFINITY ? sum : sum * ex2(ref - most));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if (lane == 0) wsum[warp] = d;
+  read_floor();
   const int n = count;
   for (int i = tid; i < min(n, kAside); i += kThreads) {
     V v;
     v.from(aside[i]);
     if (v.top() < floor_) continue;
-    float y[V::N];
+    float2 y[V::N / 2];
     v.get(y);
 #pragma unroll
-    for (int e = 0; e < V::N; ++e) put(y[e], v0 + head + aside_at[i] * V::N + e);
+    for (int e = 0; e < V::N / 2; ++e) {
+      put(y[e].x, v0 + head + aside_at[i] * V::N + 2 * e);
+      put(y[e].y, v0 + head + aside_at[i] * V::N + 2 * e + 1);
+    }
   }
   if (ragged) put(ragged_y, ragged_v);
+  // The threads' sums, by the last warp (f64 is slow: thirteen additions instead of a
+  // tree in every warp).
+  float most = -INFINITY;
+  double d = 0.0;
+  if (warp == kWarps - 1) {
+    float rs[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      rs[w] = refs[32 * w + lane];
+      most = fmaxf(most, rs[w]);
+    }
+    most = warp_top(most);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float s = parts[32 * w + lane];
+      d += (double)(rs[w] == -INFINITY ? s : s * ex2(rs[w] - most));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  }
+  const bool writer = tid == kThreads - 32;
   __syncthreads();
   const int c = few_count;
   const bool all_there = n <= kAside && c <= kRanked;  // then at least K, or all above -inf
-  if (tid == 0)
-    for (int w = 1; w < kWarps; ++w) d += wsum[w];
   if (all_there) {
-    if (tid == 0) *sum_out = SegSum{most, min(c, K), d};
+    if (writer) *sum_out = SegSum{most, min(c, K), d};
     for (int k = tid; k < c; k += kThreads) {
       const unsigned long long mine = few[k];
       int rank = 0;
@@ -338,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
     if (tid == 0) list[places] = mine;
     __syncthreads();
   }
-  if (tid == 0) *sum_out = SegSum{most, places, d};
+  if (writer) *sum_out = SegSum{most, places, d};
 }
 
 // Sorts scores and their indices in falling order of score, rising of index.
