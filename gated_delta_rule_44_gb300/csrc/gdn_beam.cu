@@ -3,28 +3,33 @@
 //   s[w, v] = score[w] + x[w, v] - ln sum_u e^{x[w, u]},
 // in one pass over the logits.
 //
-// Row kernel.  A CTA has a segment of a row.  Each thread keeps a running sum of
-// 2^(H x - ref) (f32), H = log2(e) rounded to f32 and ref a whole number: H x - ref is one
-// rounding (an fma), changes of ref and joins are exact, and ln sum e^x = ref / H + ln(sum) to
-// within the 1.3e-8 (largest x - x) that H's rounding leaves, where x has its weight.  So
-// an element costs an fma, an exponential and an add.  The threads' sums are joined in f64.
-// The segment's K largest logits are collected on the way: the K-th largest of the threads'
-// maxima so far (found by one warp, two of the upper 16 bits of its order at a time) is a value
-// that at least K logits reach, and only 16-byte vectors with a logit that reaches it are put
-// aside, whole.  It is taken after the first chunk and again after 8, 64, ... (each time the
-// other warps wait for the one; from chunk to chunk some K more vectors reach it), and at the
-// end (ranking four chunks' worth by counting took three times as long).  The logits put aside that reach the last one are ranked by
-// counting.  A segment in which more are put aside, or reach it, than there
-// is room for (rows of equal logits) is read again, once for each of the K places.
+// Row kernel.  The rows' chunks of 1024 vectors of 16 bytes, one row after another, are
+// divided equally among two CTAs per SM, and a CTA's part of a row is a segment of it.  Each
+// thread copies its vectors three chunks ahead into shared memory (asynchronously, past
+// segments' ends, so that reading goes on while a segment is finished; rows that take no part
+// are not read), and keeps a running sum of 2^(H x - ref) (f32), H = log2(e) rounded to f32 and
+// ref a whole number: H x - ref is one rounding (an fma), changes of ref and joins are exact,
+// and ln sum e^x = ref / H + ln(sum) to within the 1.3e-8 (largest x - x) that H's rounding
+// leaves, where x has its weight.  So an element costs half of an fma, an exponential and
+// half of an add.  The threads' sums are joined in f64.
+// The segment's K largest logits: while it reads, a thread notes only its largest logit of each
+// chunk.  Then every warp gives the n-th largest of its threads' maxima, n warps' shares of
+// K, and the least of these is a value that at least K logits reach; the some 3 K chunks of
+// a thread that reach it are read again, and their logits that do are ranked by counting.
+// (Putting vectors aside on the way took 13 us of 42 for K = 16: each time the warp waits.)
+// A segment in which more reach it than there is room for (rows of equal logits) is read again,
+// once for each of the K places.
 //
 // Join kernel.  A CTA per group joins the segments' sums into f64 log-sums, turns list
 // entries into 64-bit scores (beams are compared at 2^-53: two f32 roundings of a score of
-// -12 already span what separates neighbours), and sorts those that reach the K-th best
-// head of a list.  Order: score, then the lower w V + v; keys are integers, since f64
-// comparisons are a sixty-fourth of their rate.
+// -12 already span what separates neighbours), those that can be among the K, and ranks
+// them.  Order: score, then the lower w V + v; keys are integers, since f64 comparisons
+// are a sixty-fourth of their rate.
 //
-// Bound by the read of the logits in the end; now by instructions: 64 x 8 rows of 131072 bf16
-// (134 MB, 20 us) take 43 us in the row kernel, at 62 % of the issue rate, and 55 a call.
+// Bound by the read of the logits in the end; now by the instructions and their latency: 64 x 8
+// rows of 131072 bf16 (134 MB, 20 us) take 38 us with K = 16, 10 of them the join's and
+// what goes on around it, and 35 with K = 2; f32 (268 MB, 40 us) 53.  One CTA more per SM,
+// one stage more or less, or chunks of 2048 vectors are within 2 %; chunks of 512 took 46.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -39,10 +44,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;      // 16-byte vectors of a thread per chunk
-constexpr int kAside = 768;     // vectors put aside
-constexpr int kRanked = 1024;    // logits of them, ranked by counting
+constexpr int kCells = 16;      // chunks between two looks at their maxima
+constexpr int kRanked = 1024;   // logits ranked by counting
+constexpr int kFound = 512;     // cells read again
 constexpr int kRoom = 2048;     // entries of the join's sorts
 constexpr int kMaxSegs = 32;    // a lane each
+constexpr int kStages = 3;      // chunks of a CTA on their way
+constexpr int kChunk = kThreads * kUnroll;  // vectors
+constexpr int kCtasPerSm = 2;
 constexpr float kH = 1.4426950408889634f;  // log2(e) in f32
 
 // What a segment leaves: the count of its list's entries (value key, ~index), and its sum of
@@ -56,6 +65,18 @@ struct Ws {
   SegSum* sums;               // [rows][segs]
   unsigned long long* list;   // [rows][segs][K]
 };
+// The rows' chunks, one row after another, in equal ranges for the CTAs.
+struct Split {
+  int64_t chunks;  // of all rows
+  int per_row, ctas, segs;  // segs: a row's segments at most
+};
+__device__ __forceinline__ int64_t range_begin(const Split& s, int cta) {
+  return (int64_t)((uint64_t)s.chunks * (uint32_t)cta / (uint32_t)s.ctas);
+}
+// The CTA whose range holds a chunk: the last one that begins at or before it.
+__device__ __forceinline__ int cta_of(const Split& s, int64_t chunk) {
+  return (int)(((uint64_t)(chunk + 1) * (uint32_t)s.ctas - 1) / (uint64_t)s.chunks);
+}
 __host__ __device__ inline Ws carve(void* ws, int64_t lists) {
   Ws w;
   w.sums = static_cast<SegSum*>(ws);
@@ -101,13 +122,17 @@ struct Vec<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
   }
-  __device__ uint4 bits() const { return r; }
   __device__ void from(const uint4& b) { r = b; }
-  __device__ float top() const {  // (a NaN counts only beside another)
+  __device__ void fill() { r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }  // -inf
+  __device__ __nv_bfloat162 tops() const {  // (a NaN counts only beside another)
     const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&r);
-    const __nv_bfloat162 m = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
-    return fmaxf(__low2float(m), __high2float(m));
+    return __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
   }
+  static __device__ __nv_bfloat162 larger(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2(a, b); }
+  static __device__ float top_of(__nv_bfloat162 m) {
+    return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);  // (-inf of NaN)
+  }
+  __device__ float top() const { return top_of(tops()); }
 };
 template <>
 struct Vec<float> {
@@ -118,10 +143,21 @@ struct Vec<float> {
     x[0] = {r.x, r.y};
     x[1] = {r.z, r.w};
   }
-  __device__ uint4 bits() const { return *reinterpret_cast<const uint4*>(&r); }
   __device__ void from(const uint4& b) { r = *reinterpret_cast<const float4*>(&b); }
-  __device__ float top() const { return fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)); }
+  __device__ void fill() { r = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
+  __device__ float tops() const { return fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)); }
+  static __device__ float larger(float a, float b) { return fmaxf(a, b); }
+  static __device__ float top_of(float m) { return fmaxf(m, -INFINITY); }
+  __device__ float top() const { return top_of(tops()); }
 };
+// The largest logit of vectors; -inf of NaN alone.
+template <typename V, int N>
+__device__ __forceinline__ float top_of(const V (&v)[N]) {
+  auto m = v[0].tops();
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = V::larger(m, v[i].tops());
+  return V::top_of(m);
+}
 
 // The warp's largest value; a NaN is passed over.
 __device__ __forceinline__ float warp_top(float x) {
@@ -144,219 +180,304 @@ __device__ __forceinline__ float nth_top(float x, int n) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_constant__ BeamLaunch p,
-                                                                int seg_len) {
+struct RowShared {
+  uint4 ring[kStages][kUnroll][kThreads];
+  unsigned long long few[kRanked];
+  unsigned long long best[kWarps];
+  float refs[kThreads], parts[kThreads];
+  float cells[kCells][kThreads];  // each thread's largest logit of a chunk
+  float floors[kWarps];           // values that a warp's share of K logits has reached
+  int few_count, found_count;
+  uint16_t found[kFound];  // cells that reach the floor
+};
+
+// A row as both cursors see it.
+template <typename T>
+struct Row {
+  const T* x;
+  int head, vecs;  // logits before the first 16-byte boundary, whole vectors behind it
+  bool takes_part;
+  __device__ void set(const BeamLaunch& p, int64_t row, float score, bool ended) {
+    const int64_t b = row / p.W, w = row - b * p.W;
+    x = static_cast<const T*>(p.logits) + b * p.batch_stride + w * p.beam_stride;
+    const int mis = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    head = min(p.V, mis ? Vec<T>::N - mis : 0);
+    vecs = (p.V - head) / Vec<T>::N;
+    takes_part = fabsf(score) <= 3.402823466e38f && !ended;
+  }
+};
+
+// 16 bytes that are read once: they leave L2 before others.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n" ::"r"(to), "l"(from), "l"(policy)
+               : "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ Split split) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  RowShared<T>& sh = *reinterpret_cast<RowShared<T>*>(smem);
   attn::start_next_kernel();
   attn::wait_for_previous_kernel();
-  __shared__ uint4 aside[kAside];
-  __shared__ int aside_at[kAside];
-  __shared__ unsigned long long few[kRanked];
-  __shared__ volatile float floors[kWarps];  // values that K / kWarps of a warp's threads have reached
-  __shared__ float refs[kThreads], parts[kThreads];
-  __shared__ unsigned long long best[kWarps];
-  __shared__ int count, few_count;
   using V = Vec<T>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int seg = blockIdx.x, segs = gridDim.x, K = p.K;
-  const int row = blockIdx.z * p.W + blockIdx.y;
-  const Ws ws = carve(p.ws, (int64_t)p.B * p.W * segs);
-  SegSum* sum_out = ws.sums + (int64_t)row * segs + seg;
-  unsigned long long* list = ws.list + ((int64_t)row * segs + seg) * K;
-  const float score = p.scores[row];
-  if (!(fabsf(score) <= 3.402823466e38f) || (p.finished != nullptr && p.finished[row] != 0)) {
-    if (tid == 0) *sum_out = SegSum{-INFINITY, 0, 0.0};
-    return;
-  }
-  const T* x = static_cast<const T*>(p.logits) + blockIdx.z * p.batch_stride + blockIdx.y * p.beam_stride;
-  const int v0 = min((int64_t)p.V, (int64_t)seg * seg_len), v1 = (int)min((int64_t)p.V, (int64_t)v0 + seg_len);
-  if (tid == 0) count = few_count = 0;
-  if (lane == 0) floors[warp] = -INFINITY;
-  // The row's 16-byte boundaries: logits before the first and behind the last go one by one.
-  const int mis = (int)((reinterpret_cast<uintptr_t>(x + v0) & 15u) / sizeof(T));
-  const int head = min(v1 - v0, mis ? V::N - mis : 0);
-  const int vecs = (v1 - v0 - head) / V::N;
-  const int tail0 = v0 + head + vecs * V::N;
-  const T* body = x + v0 + head;
-  float top = -INFINITY;  // this thread's largest logit
-  float ref = -INFINITY;  // its sum of 2^(H x - ref), in two parts
-  float2 sum = {0.0f, 0.0f};
-  float use = 0.0f;          // -ref, or 0 while that is -inf
-  float floor_ = -INFINITY;  // logits below it are not among the segment's K
-  auto raise = [&](float y) {
-    if (y > top) {
-      top = y;
-      const float r = ceilf(y * kH);
-      if (r > ref) {
-        if (ref != -INFINITY) {  // (a sum of NaN stays one)
-          const float f = ex2(ref - r);
-          sum.x *= f;
-          sum.y *= f;
+  const int K = p.K, U = split.per_row;
+  const int64_t rows = (int64_t)p.B * p.W;
+  const Ws ws = carve(p.ws, rows * split.segs);
+  const int64_t first = range_begin(split, blockIdx.x);
+  int left = (int)(range_begin(split, blockIdx.x + 1) - first);  // chunks to work on
+  int64_t row = first / U;
+  int u0 = (int)(first - row * U);  // and where in the row
+
+  // The copies run kStages chunks ahead, through the rows' ends: every thread copies the
+  // vectors that it will read itself, so that they need no barrier.
+  auto ended = [&](int64_t r) { return p.finished != nullptr && p.finished[r] != 0; };
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sh.ring[0][0][tid]);
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  int64_t copy_row = row;
+  int copy_u = u0, copy_left = left;
+  Row<T> from;
+  from.set(p, row, p.scores[row], ended(row));
+  float next_score = row + 1 < rows ? p.scores[row + 1] : 0.0f;
+  bool next_ended = row + 1 < rows && ended(row + 1);
+  auto copy = [&](int stage) {
+    if (copy_left > 0) {
+      if (from.takes_part) {
+        const int i = copy_u * kChunk + tid;
+        const T* src = from.x + from.head + (int64_t)i * V::N;
+        const uint32_t to = ring + stage * (kUnroll * kThreads * 16);
+        if ((copy_u + 1) * kChunk <= from.vecs) {
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) copy_async(to + u * kThreads * 16, src + u * kThreads * V::N, policy);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u)
+            if (i + u * kThreads < from.vecs) copy_async(to + u * kThreads * 16, src + u * kThreads * V::N, policy);
         }
-        ref = r;
-        use = -r;
+      }
+      --copy_left;
+      if (++copy_u == U && copy_left > 0) {
+        copy_u = 0;
+        ++copy_row;
+        from.set(p, copy_row, next_score, next_ended);
+        if (copy_row + 1 < rows) {
+          next_score = p.scores[copy_row + 1];
+          next_ended = ended(copy_row + 1);
+        }
       }
     }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
   };
-  // A logit that reaches the floor, to be ranked.
-  auto put = [&](float y, int v) {
-    if (y >= floor_ && y > -INFINITY) {
-      const int at = atomicAdd(&few_count, 1);
-      if (at < kRanked) few[at] = entry(y, (uint32_t)v);
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) copy(i);
+  int stage = 0;
+
+  for (; left > 0; ++row, u0 = 0) {
+    const int u1 = min(U, u0 + left);
+    left -= u1 - u0;
+    Row<T> r;
+    r.set(p, row, p.scores[row], ended(row));
+    const int64_t at = row * split.segs + (u0 == 0 ? 0 : (int)blockIdx.x - cta_of(split, row * U));
+    SegSum* sum_out = ws.sums + at;
+    unsigned long long* list = ws.list + at * K;
+    // A row's last segment also leaves the places behind it empty.
+    if (u1 == U) {
+      const int64_t end = (row + 1) * split.segs;
+      for (int64_t i = at + 1 + tid; i < end; i += kThreads) ws.sums[i] = SegSum{-INFINITY, 0, 0.0};
     }
-  };
-  __syncthreads();
-  constexpr int kChunk = kThreads * kUnroll;
-  V r[kUnroll], ahead[kUnroll];
-  auto load = [&](int base, bool whole) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * kThreads + tid;
-      if (whole || i < vecs) ahead[u].load(body + (int64_t)i * V::N);
-    }
-  };
-  // The least of the warps' floors: a value that at least K logits have reached.
-  auto read_floor = [&] {
-    float f = floors[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) f = fminf(f, floors[w]);
-    floor_ = f;
-  };
-  const int share = (K + kWarps - 1) / kWarps;
-  auto work = [&](int base, bool whole) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) r[u] = ahead[u];
-    if (base + 2 * kChunk <= vecs) load(base + kChunk, true);
-    else load(base + kChunk, false);
-    float tops[kUnroll], most = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      tops[u] = whole || base + u * kThreads + tid < vecs ? r[u].top() : -INFINITY;
-      most = fmaxf(most, tops[u]);
-    }
-    raise(most);
-    const float2 h2 = {kH, kH}, use2 = {use, use};
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (!whole && base + u * kThreads + tid >= vecs) continue;
-      float2 y[V::N / 2];
-      r[u].get(y);
-#pragma unroll
-      for (int e = 0; e < V::N / 2; ++e) {
-        const float2 t = __ffma2_rn(y[e], h2, use2);
-        sum = __fadd2_rn(sum, float2{ex2(t.x), ex2(t.y)});
+    if (!r.takes_part) {
+      if (tid == 0) *sum_out = SegSum{-INFINITY, 0, 0.0};
+      for (int u = u0; u < u1; ++u) {
+        copy(stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
       }
+      continue;
     }
-    // Only a warp with a logit that reaches the floor that it knows looks for a newer one.
-    // (floors only rise: an old one lets more pass.)
-    if (__any_sync(0xffffffffu, base == 0 || most >= floor_)) {
-      const float mine = nth_top(top, share);
-      if (lane == 0) floors[warp] = mine;
-      if (base == 0) __syncthreads();  // (every warp is here, with nothing known yet)
-      else __syncwarp();
-      read_floor();
-      if (most >= floor_ && most > -INFINITY) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-          if (tops[u] >= floor_ && tops[u] > -INFINITY) {
-            const int at = atomicAdd(&count, 1);
-            if (at < kAside) {
-              aside[at] = r[u].bits();
-              aside_at[at] = base + u * kThreads + tid;
-            }
+    if (tid == 0) sh.few_count = sh.found_count = 0;  // (counted behind the next barrier)
+    bool crowded = false;   // more found than there is room for
+    float top = -INFINITY;  // this thread's largest logit
+    float ref = -INFINITY;  // its sum of 2^(H x - ref), in two parts
+    float2 sum = {0.0f, 0.0f};
+    float use = 0.0f;          // -ref, or 0 while that is -inf
+    float floor_ = -INFINITY;  // logits below it are not among the segment's K
+    auto raise = [&](float y) {
+      if (y > top) {
+        top = y;
+        const float up = ceilf(y * kH);
+        if (up > ref) {
+          if (ref != -INFINITY) {  // (a sum of NaN stays one)
+            const float f = ex2(ref - up);
+            sum.x *= f;
+            sum.y *= f;
           }
+          ref = up;
+          use = -up;
+        }
       }
-    }
-  };
-  load(0, false);
-  int base = 0;
-  for (; base + kChunk <= vecs; base += kChunk) work(base, true);
-  if (base < vecs) work(base, false);
-  const bool ragged = tid < head + (v1 - tail0);  // fewer than 16 of them
-  const int ragged_v = tid < head ? v0 + tid : tail0 + tid - head;
-  const float ragged_y = ragged ? attn::to_f(x[ragged_v]) : -INFINITY;
-  if (ragged) {
-    raise(ragged_y);
-    sum.x += ex2(fmaf(ragged_y, kH, use));
-  }
-  refs[tid] = ref;
-  parts[tid] = sum.x + sum.y;
-  __syncthreads();
-  read_floor();
-  const int n = count;
-  for (int i = tid; i < min(n, kAside); i += kThreads) {
-    V v;
-    v.from(aside[i]);
-    if (v.top() < floor_) continue;
-    float2 y[V::N / 2];
-    v.get(y);
+    };
+    auto work = [&](int u, bool whole) {
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
+      const int i = u * kChunk + tid;
+      V v[kUnroll];
 #pragma unroll
-    for (int e = 0; e < V::N / 2; ++e) {
-      put(y[e].x, v0 + head + aside_at[i] * V::N + 2 * e);
-      put(y[e].y, v0 + head + aside_at[i] * V::N + 2 * e + 1);
-    }
-  }
-  if (ragged) put(ragged_y, ragged_v);
-  // The threads' sums, by the last warp (f64 is slow: thirteen additions instead of a
-  // tree in every warp).
-  float most = -INFINITY;
-  double d = 0.0;
-  if (warp == kWarps - 1) {
-    float rs[kWarps];
+      for (int e = 0; e < kUnroll; ++e) {
+        v[e].from(sh.ring[stage][e][tid]);
+        if (!whole && i + e * kThreads >= r.vecs) v[e].fill();
+      }
+      const float most = top_of(v);
+      sh.cells[(u - u0) % kCells][tid] = most;
+      raise(most);
+      copy(stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      const float2 h2 = {kH, kH}, use2 = {use, use};
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      rs[w] = refs[32 * w + lane];
-      most = fmaxf(most, rs[w]);
-    }
-    most = warp_top(most);
+      for (int e = 0; e < kUnroll; ++e) {
+        float2 y[V::N / 2];
+        v[e].get(y);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float s = parts[32 * w + lane];
-      d += (double)(rs[w] == -INFINITY ? s : s * ex2(rs[w] - most));
-    }
+        for (int k = 0; k < V::N / 2; ++k) {
+          const float2 t = __ffma2_rn(y[k], h2, use2);
+          sum = __fadd2_rn(sum, float2{ex2(t.x), ex2(t.y)});
+        }
+      }
+    };
+    // A logit that reaches the floor, to be ranked.
+    auto put = [&](float y, int v) {
+      if (y >= floor_ && y > -INFINITY) {
+        const int to = atomicAdd(&sh.few_count, 1);
+        if (to < kRanked) sh.few[to] = entry(y, (uint32_t)v);
+      }
+    };
+    // The warps with a vector for every thread of theirs (one at least) take their shares of K.
+    const int warps = max(1, min(kWarps, (min(r.vecs, u1 * kChunk) - u0 * kChunk) / 32));
+    const int share = (K + warps - 1) / warps;
+    // What the row has before its first vector and behind its last: fewer than 16 logits.
+    const int heads = u0 == 0 ? r.head : 0, tail0 = r.head + r.vecs * V::N;
+    const bool ragged = tid < heads + (u1 == U ? p.V - tail0 : 0);
+    const int ragged_v = tid < heads ? tid : tail0 + tid - heads;
+    const float ragged_y = ragged ? attn::to_f(r.x[ragged_v]) : -INFINITY;
+    for (int u = u0; u < u1;) {
+      const int c0 = u, c1 = min(u1, u + kCells);
+      for (; u < c1; ++u) {
+        if ((u + 1) * kChunk <= r.vecs) work(u, true);
+        else work(u, false);
+      }
+      const bool end = u == u1;
+      if (end) {
+        if (ragged) {
+          raise(ragged_y);
+          sum.x += ex2(fmaf(ragged_y, kH, use));
+        }
+        sh.refs[tid] = ref;
+        sh.parts[tid] = sum.x + sum.y;
+      }
+      const float mine = warp < warps ? nth_top(top, share) : INFINITY;
+      if (lane == 0) sh.floors[warp] = mine;
+      __syncthreads();
+      floor_ = sh.floors[0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  }
-  const bool writer = tid == kThreads - 32;
-  __syncthreads();
-  const int c = few_count;
-  const bool all_there = n <= kAside && c <= kRanked;  // then at least K, or all above -inf
-  if (all_there) {
-    if (writer) *sum_out = SegSum{most, min(c, K), d};
-    for (int k = tid; k < c; k += kThreads) {
-      const unsigned long long mine = few[k];
-      int rank = 0;
+      for (int w = 1; w < kWarps; ++w) floor_ = fminf(floor_, sh.floors[w]);
+      if (end && ragged) put(ragged_y, ragged_v);
+      // The chunks' vectors with a logit that reaches the floor are listed, and come again from
+      // L2, one to a thread.
+      if (top >= floor_ && top > -INFINITY) {
 #pragma unroll 4
-      for (int i = 0; i < c; ++i) rank += few[i] > mine;
-      if (rank < K) list[rank] = mine;
-    }
-    return;
-  }
-  // Too many: place after place, the largest entry below the last one.
-  unsigned long long last = ~0ull;
-  int places = 0;
-  for (; places < K; ++places) {
-    unsigned long long mine = 0;
-    for (int v = v0 + tid; v < v1; v += kThreads) {
-      const float y = attn::to_f(x[v]);
-      if (y > -INFINITY) {
-        const unsigned long long e = entry(y, (uint32_t)v);
-        if (e < last && e > mine) mine = e;
+        for (int c = 0; c < c1 - c0; ++c) {
+          const float most = sh.cells[c][tid];
+          if (most >= floor_ && most > -INFINITY) {
+            const int to = atomicAdd(&sh.found_count, 1);
+            if (to < kFound) sh.found[to] = (uint16_t)(c * kThreads + tid);
+          }
+        }
+      }
+      __syncthreads();
+      const int found = sh.found_count;
+      crowded |= found > kFound;
+      for (int j = tid; j < min(found, kFound) * kUnroll; j += kThreads) {
+        const int cell = sh.found[j / kUnroll];
+        const int i = (c0 + cell / kThreads) * kChunk + j % kUnroll * kThreads + cell % kThreads;
+        if (i >= r.vecs) continue;
+        V v;
+        v.load(r.x + r.head + (int64_t)i * V::N);
+        if (!(v.top() >= floor_)) continue;
+        float2 y[V::N / 2];
+        v.get(y);
+#pragma unroll
+        for (int k = 0; k < V::N / 2; ++k) {
+          put(y[k].x, r.head + i * V::N + 2 * k);
+          put(y[k].y, r.head + i * V::N + 2 * k + 1);
+        }
+      }
+      if (!end) {
+        __syncthreads();
+        if (tid == 0) sh.found_count = 0;  // (counted behind the next floors' barrier)
       }
     }
+    // The threads' sums, by the last warp (f64 is slow: thirteen additions instead of a
+    // tree in every warp).
+    float most = -INFINITY;
+    double d = 0.0;
+    if (warp == kWarps - 1) {
+      float rs[kWarps];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xffffffffu, mine, o);
-      mine = other > mine ? other : mine;
+      for (int w = 0; w < kWarps; ++w) {
+        rs[w] = sh.refs[32 * w + lane];
+        most = fmaxf(most, rs[w]);
+      }
+      most = warp_top(most);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float s = sh.parts[32 * w + lane];
+        d += (double)(rs[w] == -INFINITY ? s : s * ex2(rs[w] - most));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     }
-    if (lane == 0) best[warp] = mine;
+    const bool writer = tid == kThreads - 32;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) mine = best[w] > mine ? best[w] : mine;
-    if (mine == 0) break;  // no more
-    last = mine;
-    if (tid == 0) list[places] = mine;
-    __syncthreads();
+    const int c = sh.few_count;
+    int places = min(c, K);
+    if (!crowded && c <= kRanked) {  // at least K, or all above -inf
+      for (int k = tid; k < c; k += kThreads) {
+        const unsigned long long mine = sh.few[k];
+        int rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < c; ++i) rank += sh.few[i] > mine;
+        if (rank < K) list[rank] = mine;
+      }
+    } else {
+      // Too many: place after place, the largest entry below the last one.
+      const int v0 = u0 == 0 ? 0 : r.head + u0 * kChunk * V::N;
+      const uint32_t v1 = u1 == U ? p.V : r.head + u1 * kChunk * V::N;
+      unsigned long long last = ~0ull;
+      for (places = 0; places < K; ++places) {
+        unsigned long long mine = 0;
+        for (uint32_t v = v0 + tid; v < v1; v += kThreads) {
+          const float y = attn::to_f(r.x[v]);
+          if (y > -INFINITY) {
+            const unsigned long long e = entry(y, v);
+            if (e < last && e > mine) mine = e;
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const unsigned long long other = __shfl_xor_sync(0xffffffffu, mine, o);
+          mine = other > mine ? other : mine;
+        }
+        if (lane == 0) sh.best[warp] = mine;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) mine = sh.best[w] > mine ? sh.best[w] : mine;
+        if (mine == 0) break;  // no more
+        last = mine;
+        if (tid == 0) list[places] = mine;
+        __syncthreads();
+      }
+    }
+    if (writer) *sum_out = SegSum{most, places, d};
+    __syncthreads();  // the shared lists are filled anew
   }
-  if (writer) *sum_out = SegSum{most, places, d};
 }
 
 // Sorts scores and their indices in falling order of score, rising of index.
@@ -386,206 +507,227 @@ __device__ __forceinline__ void sort_scores(unsigned long long* key, uint32_t* i
     }
 }
 
-__global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_constant__ BeamLaunch p, int segs) {
-  __shared__ unsigned long long key[kRoom];
-  __shared__ uint32_t index[kRoom];
-  __shared__ double base[kBeamMaxW];  // score - log sum of each beam; NaN: takes no part
-  __shared__ float base_f[kBeamMaxW];
-  __shared__ int counts[kBeamMaxW * kMaxSegs];
-  __shared__ float least;
-  __shared__ int count;
-  const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x, K = p.K;
-  const int lists = p.W * segs;  // at most kRoom
+// What limits the join is fetching its own instructions, so loops are not unrolled.
+struct JoinShared {
+  unsigned long long list[kRoom];
+  unsigned long long key[kRoom];
+  uint32_t index[kRoom];
+  float heads[8 * kThreads];  // [level][list]
+  double base[kBeamMaxW];     // score - log sum of each beam; NaN: takes no part
+  float base_f[kBeamMaxW];
+  int counts[kBeamMaxW * kMaxSegs];
+  uint32_t least;
+  int count;
+};
+__global__ void __launch_bounds__(kThreads)
+beam_join_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ Split split) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  JoinShared& sh = *reinterpret_cast<JoinShared*>(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x, K = p.K, segs = split.segs;
+  const int lists = p.W * segs, all = lists * K;  // at most kRoom lists
   attn::start_next_kernel();
   attn::wait_for_previous_kernel();
   const Ws ws = carve(p.ws, (int64_t)p.B * lists);
   const SegSum* sums = ws.sums + (int64_t)b * lists;
-  const unsigned long long* list = ws.list + (int64_t)b * lists * K;
-  if (tid == 0) count = 0;
-  // Few entries are on their way while the sums are joined: a warp's lists, a lane per entry
-  // (no division in the way; each would be a sixth of the time of all else).
-  const int all = lists * K, warp = tid >> 5;
-  constexpr int kAhead = 4;
-  const bool ahead = lists <= kAhead * kWarps && K <= 32;
-  unsigned long long entries[kAhead];
-  if (ahead) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int l = warp * kAhead + u;
-      entries[u] = l < lists && lane < K ? list[l * K + lane] : 0;
-    }
+  const unsigned long long* list = ws.list + (int64_t)b * all;
+  // The entries come while the sums are joined, if there is room for them.
+  const bool here = all <= kRoom;
+  if (here) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(sh.list);
+#pragma unroll 1
+    for (int i = tid; i < all; i += kThreads)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to + i * 8), "l"(list + i) : "memory");
+    list = sh.list;
   }
-  for (int w = tid >> 5; w < p.W; w += kWarps) {  // a warp per beam, a lane per segment
+  float score = 0.0f;
+  bool ended = false;
+  if (tid < p.W) {
+    score = p.scores[(int64_t)b * p.W + tid];
+    ended = p.finished != nullptr && p.finished[(int64_t)b * p.W + tid] != 0;
+  }
+  if (tid == 0) {
+    sh.count = 0;
+    sh.least = 0;
+  }
+#pragma unroll 1
+  for (int w = warp; w < p.W; w += kWarps) {  // a warp per beam, a lane per segment
     SegSum x{-INFINITY, 0, 0.0};
     if (lane < segs) {
       x = sums[w * segs + lane];
-      counts[w * segs + lane] = x.count;
+      sh.counts[w * segs + lane] = x.count;
     }
-    float most = x.ref;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float most = warp_top(x.ref);
     // 2^(ref - most) from its bits; 0 from 2^-1023 on.
     const float e = x.ref - most + 1023.0f;
     double total = x.ref == -INFINITY ? x.sum : x.sum * __longlong_as_double(e > 0.0f ? (long long)e << 52 : 0);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+#pragma unroll 1
+    for (int o = segs > 1 ? 1 << (31 - __clz(segs - 1)) : 0; o > 0; o >>= 1)
+      total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane == 0) {
-      base[w] = total;
-      base_f[w] = most;
+      sh.base[w] = total;
+      sh.base_f[w] = most;
     }
   }
   __syncthreads();
   // A lane per beam: f64 instructions of a warp take as long for one lane as for 32.
   if (tid < p.W) {
     // Nothing in the row, an infinity or a NaN: no score of it is finite.
-    const double x = (double)p.scores[(int64_t)b * p.W + tid] -
-                     ((double)base_f[tid] * (1.0 / (double)kH) + log(base[tid]));
-    base[tid] = x;
-    base_f[tid] = (float)x;
+    const double x = (double)score - ((double)sh.base_f[tid] * (1.0 / (double)kH) + log(sh.base[tid]));
+    sh.base[tid] = x;
+    sh.base_f[tid] = (float)x;
   }
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
   __syncthreads();
-  auto score_of = [&](int w, unsigned long long e) -> unsigned long long {
-    const double s = base[w] + (double)value_of((uint32_t)(e >> 32));
-    return s - s == 0.0 ? order_of(s) : 0ull;
+  // In f32, to within 2^-22 (|base| + |s|); NaN or an infinity: none.
+  auto near_score = [&](int l, unsigned long long e) {
+    return sh.base_f[l / segs] + value_of((uint32_t)(e >> 32));
   };
-  // In f32, to within 2^-22 (|base| + |s|); NaN: none.
-  auto near_score = [&](int w, unsigned long long e) {
-    const float s = base_f[w] + value_of((uint32_t)(e >> 32));
-    return s - s == 0.0f ? s : __int_as_float(0x7fffffff);
-  };
-  // The K-th best head of a list is a score that K entries reach.  It is found in f32, and
-  // entries that do not come near it are left out before any f64 arithmetic.
-  float floor_ = -INFINITY;
-  if (lists >= K && lists <= kThreads) {
-    float* heads = reinterpret_cast<float*>(key);
-    const float none = __int_as_float(0x7fffffff);
-    if (ahead) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int l = warp * kAhead + u;
-        if (lane == 0 && l < lists) heads[l] = counts[l] > 0 ? near_score(l / segs, entries[u]) : none;
+  // If j entries of each of r lists reach a score, K = r j do: for j = 1, 2, 4, ..., the r-th
+  // best of the lists' j-th entries is a floor, and the highest of these floors is taken.
+  // It is found in f32, and entries that do not come near it are left out before any f64
+  // arithmetic.
+  float floor_ = -3.402823466e38f;
+  if (lists <= kThreads) {
+    const int heads = (32 - __clz(K)) * lists;  // 8 levels at most
+#pragma unroll 1
+    for (int i = tid; i < heads; i += kThreads) {
+      const int level = i / lists, l = i - level * lists, k = (1 << level) - 1;
+      sh.heads[i] = k < sh.counts[l] ? near_score(l, list[(int64_t)l * K + k]) : -INFINITY;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < heads; i += kThreads) {
+      const int level = i / lists;
+      const float mine = sh.heads[i];
+      int reach = 0;
+#pragma unroll 4
+      for (int l = 0; l < lists; ++l) reach += sh.heads[level * lists + l] >= mine;
+      if (fabsf(mine) <= 3.402823466e38f && reach << level >= K) atomicMax(&sh.least, order_of(mine));
+    }
+    __syncthreads();
+    if (sh.least != 0) {
+      floor_ = value_of(sh.least);
+      float big = fabsf(floor_);
+#pragma unroll 1
+      for (int w = 0; w < p.W; ++w) {  // (a NaN is passed over; infinite ones have no entries)
+        const float f = fabsf(sh.base_f[w]);
+        if (f <= 3.402823466e38f) big = fmaxf(big, f);
       }
-    } else if (tid < lists) {
-      heads[tid] = counts[tid] > 0 ? near_score(tid / segs, list[(int64_t)tid * K]) : none;
+      floor_ -= big * 0x1p-20f;
     }
-    if (tid == 0) least = -INFINITY;
-    __syncthreads();
-    if (tid < lists) {
-      const float mine = heads[tid];
-      int rank = 0;  // equal heads by their number
-#pragma unroll 8
-      for (int i = 0; i < lists; ++i) rank += heads[i] > mine || (heads[i] == mine && i < tid);
-      if (rank == K - 1 && mine == mine) least = mine;
-    }
-    __syncthreads();
-    floor_ = least;
-    float big = fabsf(floor_);
-    for (int w = 0; w < p.W; ++w) big = fmaxf(big, fabsf(base_f[w]));  // (a NaN is passed over)
-    floor_ -= big * 0x1p-20f;  // -inf stays
-    __syncthreads();  // `key` is written again
   }
   // Beams that ended come first: one entry each.
-  for (int w = tid; w < p.W; w += kThreads) {
-    const float s = p.scores[(int64_t)b * p.W + w];
-    if (p.finished != nullptr && p.finished[(int64_t)b * p.W + w] != 0 && fabsf(s) <= 3.402823466e38f) {
-      const int at = atomicAdd(&count, 1);
-      key[at] = order_of((double)s);
-      index[at] = (uint32_t)(w * p.V + p.pad);
-    }
+  if (ended && fabsf(score) <= 3.402823466e38f) {
+    const int at = atomicAdd(&sh.count, 1);
+    sh.key[at] = order_of((double)score);
+    sh.index[at] = (uint32_t)(tid * p.V + p.pad);
   }
-  auto take = [&](int w, unsigned long long e) {
-    if (!(near_score(w, e) >= floor_)) return;
-    const unsigned long long s = score_of(w, e);
-    if (s != 0) {
-      const int at = atomicAdd(&count, 1);
-      key[at] = s;
-      index[at] = (uint32_t)(w * p.V) + ~(uint32_t)e;
+  __syncthreads();
+  int kept = sh.count;  // scored entries in front
+  // Entries are put behind those with their beam in `index`, and then scored, a thread each.
+  // A list holds at most K, and `key` the K best of what came before and kRoom / 2 more.
+  int l0 = 0;
+  do {
+    __syncthreads();  // `count` is `kept`
+    const int step = here ? lists : max(1, kRoom / 2 / K);
+#pragma unroll 1
+    for (int l = l0 + warp; l < min(lists, l0 + step); l += kWarps) {
+#pragma unroll 1
+      for (int k = lane; k < sh.counts[l]; k += 32) {
+        const unsigned long long e = list[(int64_t)l * K + k];
+        const float s = near_score(l, e);
+        if (s >= floor_ && s <= 3.402823466e38f) {
+          const int at = atomicAdd(&sh.count, 1);
+          sh.key[at] = e;
+          sh.index[at] = l / segs;
+        }
+      }
     }
-  };
+    l0 += step;
+    __syncthreads();
+    const int n = sh.count;
+#pragma unroll 1
+    for (int i = kept + tid; i < n; i += kThreads) {
+      const unsigned long long e = sh.key[i];
+      const uint32_t w = sh.index[i];
+      sh.key[i] = order_of(sh.base[w] + (double)value_of((uint32_t)(e >> 32)));
+      sh.index[i] = w * p.V + ~(uint32_t)e;
+    }
+    __syncthreads();
+    if (n > kThreads || l0 < lists) {
+      if (n > kept || kept > K) sort_scores(sh.key, sh.index, n);
+      kept = min(n, K);
+      if (tid == 0) sh.count = kept;
+    } else {
+      kept = n;
+    }
+  } while (l0 < lists);
+  __syncthreads();
+  // (few are ranked by counting, more have been sorted)
+  const int n = sh.count;
   auto write = [&](int k, unsigned long long s, uint32_t at) {
     const int64_t to = (int64_t)b * K + k;
-    p.parents[to] = (int32_t)(at / (uint32_t)p.V);
-    p.tokens[to] = (int32_t)(at % (uint32_t)p.V);
+    const uint32_t w = at / (uint32_t)p.V;
+    p.parents[to] = (int32_t)w;
+    p.tokens[to] = (int32_t)(at - w * (uint32_t)p.V);
     p.out_scores[to] = (float)value_of(s);
   };
-  int kept;
-  if (ahead) {  // at most 32 x 32 + W entries
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int l = warp * kAhead + u;
-      if (l < lists && lane < counts[l]) take(l / segs, entries[u]);
-    }
-    __syncthreads();
-    const int n = count;
-    kept = min(n, K);
-    if (n <= kThreads) {  // by counting
-      if (tid < n) {
-        const unsigned long long mine = key[tid];
-        const uint32_t at = index[tid];
-        int rank = 0;
+  if (tid < n && n <= kThreads) {
+    const unsigned long long mine = sh.key[tid];
+    const uint32_t at = sh.index[tid];
+    int rank = 0;
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) rank += key[i] > mine || (key[i] == mine && index[i] < at);
-        if (rank < K) write(rank, mine, at);
-      }
-    } else {
-      sort_scores(key, index, n);
-      for (int k = tid; k < kept; k += kThreads) write(k, key[k], index[k]);
-    }
-  } else {
-    __syncthreads();
-    kept = count;
-    const int room = kRoom - kBeamMaxK;  // new ones of a pass; W <= kBeamMaxW <= kBeamMaxK
-    for (int at0 = 0; at0 < all; at0 += room) {
-      for (int i = at0 + tid; i < min(all, at0 + room); i += kThreads) {
-        const int l = i / K;
-        if (i - l * K < counts[l]) take(l / segs, list[i]);
-      }
-      __syncthreads();
-      const int n = count;
-      if (n > kept || at0 == 0) {
-        sort_scores(key, index, n);
-        kept = min(n, K);
-      }
-      __syncthreads();
-      if (tid == 0) count = kept;
-      __syncthreads();
-    }
-    for (int k = tid; k < kept; k += kThreads) write(k, key[k], index[k]);
+    for (int i = 0; i < n; ++i) rank += sh.key[i] > mine || (sh.key[i] == mine && sh.index[i] < at);
+    if (rank < K) write(rank, mine, at);
   }
-  for (int k = kept + tid; k < K; k += kThreads) {
+  for (int k = min(n, K) + tid; k < K; k += kThreads) {
     const int64_t to = (int64_t)b * K + k;
     p.parents[to] = p.tokens[to] = -1;
     p.out_scores[to] = -INFINITY;
   }
 }
 
-// Segments of a row.  Twelve CTAs for each SM (four at a time) even out, while a segment of
-// fewer than 4096 logits spends its time on the selection; the sums depend on the sizes
-// alone.
-int segments(int64_t rows, int64_t V) {
-  const int64_t want = (12 * 152 + rows - 1) / rows, most = (V + 4095) / 4096;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, kMaxSegs}));
+// The CTAs share the chunks equally, but a row has at most 30 of them (a lane each in the
+// join).
+Split split_rows(int64_t rows, int64_t V, bool bf16) {
+  const int64_t chunk = kChunk * (bf16 ? 8 : 4);
+  Split s;
+  s.per_row = (int)((V + chunk - 1) / chunk);
+  s.chunks = rows * s.per_row;
+  s.ctas = (int)std::min<int64_t>({kCtasPerSm * 152, s.chunks, (kMaxSegs - 2) * rows});
+  s.segs = (int)(s.ctas / rows + (s.ctas % rows ? 2 : 0));
+  return s;
+}
+
+template <typename T>
+cudaError_t launch_rows(const BeamLaunch& p, const Split& s, cudaStream_t st) {
+  constexpr size_t smem = sizeof(RowShared<T>);
+  static_assert(kCtasPerSm * (smem + 1024) <= 228 * 1024, "CTAs of an SM");
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(beam_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (attr != cudaSuccess) return attr;
+  return attn::launch_after(beam_rows_kernel<T>, dim3((unsigned)s.ctas), kThreads, st, smem, p, s);
 }
 
 }  // namespace
 
 size_t beam_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t K) {
-  const int64_t lists = B * W * segments(B * W, V);
-  return (size_t)(lists * ((int64_t)sizeof(SegSum) + 8 * K));
+  // (of two types, the one with more lists)
+  const int64_t segs = std::max(split_rows(B * W, V, true).segs, split_rows(B * W, V, false).segs);
+  return (size_t)(B * W * segs * ((int64_t)sizeof(SegSum) + 8 * K));
 }
 
 cudaError_t launch_beam(const BeamLaunch& p, cudaStream_t st) {
-  const int64_t rows = (int64_t)p.B * p.W;
-  const int segs = segments(rows, p.V);
-  // Whole vectors, so that only a row's own ends are ragged.
-  const int seg_len = ((p.V + segs - 1) / segs + 7) & ~7;
-  const dim3 grid((unsigned)segs, (unsigned)p.W, (unsigned)p.B);
+  const Split s = split_rows((int64_t)p.B * p.W, p.V, p.bf16);
   // (Both launches are prepared while the kernel before them still runs.)
   const cudaError_t e =
-      p.bf16 ? attn::launch_after(beam_rows_kernel<__nv_bfloat16>, grid, kThreads, st, 0, p, seg_len)
-             : attn::launch_after(beam_rows_kernel<float>, grid, kThreads, st, 0, p, seg_len);
+      p.bf16 ? launch_rows<__nv_bfloat16>(p, s, st) : launch_rows<float>(p, s, st);
   if (e != cudaSuccess) return e;
-  return attn::launch_after(beam_join_kernel, dim3((unsigned)p.B), kThreads, st, 0, p, segs);
+  constexpr size_t smem = sizeof(JoinShared);
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(beam_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (attr != cudaSuccess) return attr;
+  return attn::launch_after(beam_join_kernel, dim3((unsigned)p.B), kThreads, st, smem, p, s);
 }
 
 }  // namespace gdn

@@ -108,6 +108,21 @@ def test_ended_dead_and_masked(dtype, cuda_device):
     assert (got[0].cpu()[3, 3:] == -1).all()
 
 
+@pytest.mark.parametrize("n,W,V,K,dtype", [(200, 4, 9001, 8, F32), (9, 3, 70001, 5, BF), (1, 7, 130001, 7, F32),
+                                           (150, 8, 301, 16, F32)])
+def test_many_rows_with_some_that_take_no_part(n, W, V, K, dtype, cuda_device):
+    """Rows that end inside a block's share, next to ended and dead ones."""
+    g = torch.Generator().manual_seed(n + V)
+    x = (torch.randn(n, W, V, generator=g) * 3).to(dtype)
+    s = -torch.rand(n, W, generator=g) * 6
+    fin = torch.rand(n, W, generator=g) < 0.3
+    dead = torch.rand(n, W, generator=g) < 0.2
+    s[dead & ~fin] = float("-inf")
+    x[fin] = float("nan")
+    got = select(x.to(cuda_device), s.to(cuda_device), K, cuda_device, finished=fin.to(cuda_device), pad=3)
+    check(got, definition(x, s, K, fin.numpy(), 3))
+
+
 @pytest.mark.parametrize("dtype,V", [(BF, 50001), (F32, 9000), (BF, 1500)])
 def test_equal_logits(dtype, V, cuda_device):
     """Rows of one value, of two, of zeros of either sign: the lowest indices, though more
