@@ -170,3 +170,38 @@ def test_many_pools_stream_and_graph(cuda_device):
     B.gdn_read_device_status()
     for p, b in zip(pools, before):
         assert torch.equal(p, b)
+
+
+@pytest.mark.parametrize("groups", [False, True])
+def test_many_pairs_and_offsets_past_32_bits(groups, cuda_device):
+    """A pool of more than 2^32 bytes next to one of many small slots; lists of 60000, right, and
+    wrong in their last pair."""
+    dev, n, slots = cuda_device, 60000, 1_100_000
+    g = torch.Generator().manual_seed(7)
+    big = torch.empty(slots, 1024, dtype=torch.int32, device=dev)
+    small = torch.arange(slots, dtype=torch.int32, device=dev).view(-1, 1).clone()
+    order = torch.randperm(slots, generator=g)
+    last = int((order == slots - 1).nonzero()[0, 0])
+    order[last] = order[0]
+    order[0] = slots - 1
+    dst = order[:n].to(torch.int32)
+    if groups:
+        dst = dst.view(-1, 5)
+        src = torch.randint(0, 5, dst.shape, generator=g).to(torch.int32)
+        want = torch.gather(dst, 1, src.long())
+    else:
+        src = want = order[n:2 * n].to(torch.int32)
+    big[:, 0] = small[:, 0]
+    big[:, 1023] = small[:, 0]
+    B.gdn_copy_slots([big, small], dst.to(dev), src.to(dev), groups=groups)
+    B.gdn_read_device_status()
+    d = dst.view(-1).long().to(dev)
+    w = want.reshape(-1).to(dev)
+    assert torch.equal(small[d, 0], w) and torch.equal(big[d, 0], w) and torch.equal(big[d, 1023], w)
+    wrong = dst.clone()
+    wrong.view(-1)[-1] = wrong.view(-1)[3]
+    B.gdn_copy_slots([small], wrong.to(dev), src.to(dev), groups=groups)
+    with pytest.raises(B.GdnError):
+        B.gdn_read_device_status()
+    del big
+    torch.cuda.empty_cache()
