@@ -1,5 +1,5 @@
-// gdn_attn8_tc.cu -- attention of few rows per kv head (decode, drafts) over a cache in 8
-// bits, on tcgen05 tensor cores, without widening a code.
+// gdn_attn8_tc.cu -- attention of up to 256 rows per kv head (decode, drafts, short chunks)
+// over a cache in 8 bits, on tcgen05 tensor cores, without widening a code.
 //
 // The codes go from the cache to the tensor cores as they are; what is multiplied with
 // them comes in two e4m3 parts, x ~ hi + lo / 32 with hi = e4m3(x), lo = e4m3(32 (x - hi)):
@@ -32,6 +32,12 @@
 // Two S and two P buffers: the scores of a tile are computed during the softmax of the one
 // before.  Two CTAs share an SM where their memory allows it, and hide each other's chains.
 // The work is that of the stream form (gdn_attn_stream.cuh).
+//
+// Bound by HBM where many sequences keep every SM's rings full: 256 single tokens over 1 to
+// 16384 keys, 32 + 4 heads of 128, take 338 us (2.2 GB at 6.6 TB/s, 98 % of the copy rate); 128
+// sequences with 1 to 4 drafts over up to 8192 keys, 32 + 8 heads, 16-row pages, 195 (1.06 GB
+// at 5.4 TB/s: TMA loads of 2 KB, and the ranges' ends); one token over 200003 keys 48 (205 MB, 33 to 41 of it the main
+// kernel, then the join of 76 ranges).
 //
 // A row whose result is not finite, or whose l is too small to be trusted (blocks whose
 // scales differ by 2^90), is evaluated again key by key (exact_row).  Every wait is bounded.
@@ -836,10 +842,10 @@ cudaError_t run(const AttnLaunch& p, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!codes_map<D, R>(&mk, p.kc, p, a.pb) || !codes_map<D, R>(&mv, p.vc, p, a.pb))
     return cudaErrorInvalidValue;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      attn8_tc_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
-  if (attr != cudaSuccess) return attr;
-  const cudaError_t e = launch_after(attn8_tc_kernel<D, R>, dim3(a.ctas), C::kThreads, st, C::kBytes, p, mk, mv, a);
+  static std::atomic<uint64_t> devices{0};
+  cudaError_t e = allow_shared(attn8_tc_kernel<D, R>, C::kBytes, devices);
+  if (e != cudaSuccess) return e;
+  e = launch_after(attn8_tc_kernel<D, R>, dim3(a.ctas), C::kThreads, st, C::kBytes, p, mk, mv, a);
   if (e != cudaSuccess) return e;
   return launch_after(attn8_join_kernel<D>, dim3(a.ctas, std::min(a.rows, 16)), 256, st, 0, p, a);
 }

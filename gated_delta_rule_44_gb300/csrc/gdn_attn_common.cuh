@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "gdn_internal.h"
@@ -234,6 +235,19 @@ cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, cudaStrea
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
   note_launch();
+  return e;
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device: every device has
+// attributes of its own.  `done`: the kernel's, a bit for each of the first 64 devices.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & bit) != 0) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
 

@@ -540,9 +540,8 @@ cudaError_t launch_rows(const AttnLaunch& p, cudaStream_t st) {
 
 template <typename T, int D, bool PAGED>
 cudaError_t launch_tiles(const AttnLaunch& p, int64_t items, int ranks, cudaStream_t st) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(attn_simt_kernel<T, D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sizeof(Smem<D>));
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t attr = allow_shared(attn_simt_kernel<T, D, PAGED>, sizeof(Smem<D>), devices);
   if (attr != cudaSuccess) return attr;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;

@@ -1007,9 +1007,8 @@ cudaError_t run(const AttnLaunch& p, TcArgs a, dim3 grid, cudaStream_t st) {
   if (!q_map(&mq, p, a.q_box) || !(PAGED ? pages_map(&mk, p.kc, p, a.pbk) : rows_map(&mk, p.k, p, a.pbk)) ||
       !(PAGED ? pages_map(&mv, p.vc, p, a.pbv) : rows_map(&mv, p.v, p, a.pbv)))
     return cudaErrorInvalidValue;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(attn_tc_kernel<D, NQ, PAGED, STREAM>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t attr = allow_shared(attn_tc_kernel<D, NQ, PAGED, STREAM>, C::kBytes, devices);
   if (attr != cudaSuccess) return attr;
   attn_tc_kernel<D, NQ, PAGED, STREAM><<<grid, C::kThreads, C::kBytes, st>>>(p, mq, mk, mv, a);
   note_launch();

@@ -703,9 +703,9 @@ template <typename T>
 cudaError_t launch_rows(const BeamLaunch& p, const Split& s, cudaStream_t st) {
   constexpr size_t smem = sizeof(RowShared<T>);
   static_assert(kCtasPerSm * (smem + 1024) <= 228 * 1024, "CTAs of an SM");
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(beam_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t e = attn::allow_shared(beam_rows_kernel<T>, smem, devices);
+  if (e != cudaSuccess) return e;
   return attn::launch_after(beam_rows_kernel<T>, dim3((unsigned)s.ctas), kThreads, st, smem, p, s);
 }
 
@@ -720,13 +720,13 @@ size_t beam_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t K) {
 cudaError_t launch_beam(const BeamLaunch& p, cudaStream_t st) {
   const Split s = split_rows((int64_t)p.B * p.W, p.V, p.bf16);
   // (Both launches are prepared while the kernel before them still runs.)
-  const cudaError_t e =
+  cudaError_t e =
       p.bf16 ? launch_rows<__nv_bfloat16>(p, s, st) : launch_rows<float>(p, s, st);
   if (e != cudaSuccess) return e;
   constexpr size_t smem = sizeof(JoinShared);
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(beam_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> devices{0};
+  e = attn::allow_shared(beam_join_kernel, smem, devices);
+  if (e != cudaSuccess) return e;
   return attn::launch_after(beam_join_kernel, dim3((unsigned)p.B), kThreads, st, smem, p, s);
 }
 
