@@ -195,3 +195,19 @@ def test_in_place_streams_and_graphs(cuda_device):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(par, w[0]) and torch.equal(tok, w[1]) and torch.equal(best, w[2])
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """Rows more than 2^32 elements apart."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(6)
+    n, W, V, K = 3, 2, 2001, 4
+    x = (torch.randn(n, W, V, generator=g) * 2).to(BF)
+    far = torch.empty(2 ** 32 + 100 + 3 * V, dtype=BF, device=dev)
+    step = 2 ** 31 + 7
+    rows = far.as_strided((n, W, V), (step, V + 5, 1))
+    rows.copy_(x)
+    s = -torch.rand(n, W, generator=g)
+    check(select(rows, s.to(dev), K, dev), definition(x, s, K))
+    del far, rows
+    torch.cuda.empty_cache()
