@@ -11,8 +11,9 @@
 //
 // The code is that of the exact x: it is taken from an f32 evaluation, and where a change by
 // what that may be off would change it (2^-19 of x and its partner; some one row of 256
-// values in 50), the row is evaluated again in pairs of f32, hi + lo, and rounded from those.  What is kept of a key for the whole
-// sequence then does not hang on the order of a sum.
+// values in 50), the row is evaluated again in pairs of f32, hi + lo, and rounded from
+// those.  What is kept of a key for the whole sequence then does not hang on the order of a
+// sum.
 //
 // Work.  Items of (block of a sequence's positions, kv head, k or v), each one team's: the
 // team reads its new rows, keeps the rotated values in registers (the first few rows of a

@@ -839,10 +839,14 @@ int gdn_attn8_prepare(const gdn_attn8_prepare_args* args, void* stream);
 
 /* gdn_attn8_paged -- gdn_attn_paged over a cache in 8 bits, of any finite scales (a key or
  * value of another one is what code times scale gives).  Statistics and sums are f32.
- * Roundings beside the last one: with many rows per kv head (max_q_len * Hq / Hkv) and
- * bf16, the values are widened to bf16 (exact for scales that are powers of two from
- * 2^-110 on) and then used as in gdn_attn_paged.  The workspace depends on the
- * table's width then: it holds the widened contexts of some sequences at a time. */
+ * Roundings beside the last one, by rows per kv head (max_q_len * Hq / Hkv), in bf16:
+ *   up to 256, D >= 64: the codes are used as they are; q in two e4m3 parts, exact down to
+ *   2^-10 of its row's largest value, and the softmax weights to 2^-8 of each.
+ *   more: the values are widened to bf16 (exact for scales that are powers of two from
+ *   2^-110 on) and then used as in gdn_attn_paged.
+ * f32, and bf16 with D = 32 and few rows, round nothing but the result.  The widened form (of
+ * f32 too) needs a workspace that depends on the table's width: it holds the contexts of some
+ * sequences at a time. */
 typedef struct gdn_attn8_paged_args {
   gdn_attn_paged_args base;     /* base.cache NULL */
   const gdn_attn_cache8* cache;
