@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   }
   wait_for_previous_kernel();
   start_next_kernel();
-  stream_start<C::kThreads>(p, a.ctas, a.tq, sh);
+  stream_start<C::kThreads, true>(p, a.ctas, a.tq, sh);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   if (warp == 0) {
     // ---- ranges, loads of K ----
     auto role = [&] {
-      SegIter iter{sh->start_s, sh->start_hkv, sh->start_rt, sh->start_u, (int)blockIdx.x, a.tq, sh->left};
+      SegIter<true> iter{sh->start_s, sh->start_hkv, sh->start_rt, sh->start_u, (int)blockIdx.x, a.tq, sh->left};
       for (int n = 0;; ++n) {
         Seg g;
         if (!iter.next(p, g)) g.s = -1;
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     };
     role();
   } else if (warp == 3) {
-    if (lane == 0) a.info[blockIdx.x] = stream_info(p, a.ctas, a.tq, sh);
+    if (lane == 0) a.info[blockIdx.x] = stream_info<true>(p, a.ctas, a.tq, sh);
     // Sequences without a key.
     for (int s = blockIdx.x; s < p.N; s += a.ctas) {
       const SeqRange q = seq_range(p, s);

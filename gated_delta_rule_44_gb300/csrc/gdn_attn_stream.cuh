@@ -30,11 +30,15 @@ struct Seg {
 __device__ __forceinline__ int key_tiles(const SeqRange& q) {
   return q.b > q.a ? (q.kv + BK - 1) / BK : 0;
 }
+// TILES: a sequence's tokens may be several tiles of tq; else they are one (and the rest is as it
+// was without them, for the wide cache: 128 sequences' drafts take 351 us, 355 with them).
+template <bool TILES>
 __device__ __forceinline__ int row_tiles(const AttnLaunch& p, const SeqRange& q, int tq) {
-  return (min(q.b - q.a, p.max_q) + tq - 1) / tq;
+  return !TILES ? 1 : (min(q.b - q.a, p.max_q) + tq - 1) / tq;
 }
 
 // The ranges of one CTA of the stream form.
+template <bool TILES>
 struct SegIter {
   int s, hkv, rt, u, cta, tq;
   int64_t left;
@@ -51,9 +55,11 @@ struct SegIter {
     const int take = (int)min((int64_t)(n - u), left);
     g.s = s;
     g.hkv = hkv;
-    g.t0 = q.a + rt * tq;
-    g.nt = min(tq, min(q.b - q.a, p.max_q) - rt * tq);
-    g.pos0 = q.kv - (q.b - q.a) + rt * tq;
+    const int t = TILES ? rt * tq : 0;
+    g.t0 = q.a + t;
+    g.nt = min(q.b - q.a, p.max_q) - t;
+    if (TILES) g.nt = min(g.nt, tq);
+    g.pos0 = q.kv - (q.b - q.a) + t;
     g.hi = q.kv;
     g.kt0 = u;
     g.kt1 = u + take;
@@ -62,7 +68,7 @@ struct SegIter {
     u += take;
     if (u == n) {
       u = 0;
-      if (++rt == row_tiles(p, q, tq)) {
+      if (!TILES || ++rt == row_tiles<TILES>(p, q, tq)) {
         rt = 0;
         if (++hkv == p.Hkv) {
           hkv = 0;
@@ -161,7 +167,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 // Where CTA blockIdx.x of `ctas` begins, into sh->start_s, start_hkv, start_rt, start_u, and how many
 // key tiles it has (sh->left); by the whole CTA, which synchronises before it reads them.
-template <int kThreads, typename Sh>
+template <int kThreads, bool TILES, typename Sh>
 __device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, int tq, Sh* sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // Prefix sum of the key tiles over the sequences, a run of them per thread.
@@ -171,7 +177,7 @@ __device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, int 
   unsigned bad = 0;
   for (int s = s0; s < s1; ++s) {
     const SeqRange q = seq_range(p, s);
-    mine += (long long)key_tiles(q) * row_tiles(p, q, tq);
+    mine += (long long)key_tiles(q) * row_tiles<TILES>(p, q, tq);
     bad |= q.bad;
   }
   if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
@@ -201,11 +207,11 @@ __device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, int 
     for (int s = s0; s < s1; ++s) {
       const SeqRange q = seq_range(p, s);
       const int n = key_tiles(q);
-      const long long all = (long long)n * row_tiles(p, q, tq);  // of a kv head
+      const long long all = (long long)n * row_tiles<TILES>(p, q, tq);  // of a kv head
       if (w0 < at + all * p.Hkv) {
         sh->start_s = s;
         sh->start_hkv = (int)((w0 - at) / all);
-        sh->start_rt = (int)((w0 - at) % all / n);
+        sh->start_rt = TILES ? (int)((w0 - at) % all / n) : 0;
         sh->start_u = (int)((w0 - at) % all % n);
         break;
       }
@@ -217,10 +223,10 @@ __device__ __forceinline__ void stream_start(const AttnLaunch& p, int ctas, int 
 // What the joining kernel needs of CTA blockIdx.x's ranges, by one thread:
 // {s, kv head + 2^16 row tile of the pair it began and left open (s = -1: none), how its first
 // range ends: 0 open, 1 the pair's end, 2 no range at all; the CTA that ends the pair it left open}.
-template <typename Sh>
+template <bool TILES, typename Sh>
 __device__ __forceinline__ int4 stream_info(const AttnLaunch& p, int ctas, int tq, const Sh* sh) {
   int4 r = make_int4(-1, 0, 2, 0);
-  SegIter every{sh->start_s, sh->start_hkv, sh->start_rt, sh->start_u, (int)blockIdx.x, tq, sh->left};
+  SegIter<TILES> every{sh->start_s, sh->start_hkv, sh->start_rt, sh->start_u, (int)blockIdx.x, tq, sh->left};
   long long at = sh->total * blockIdx.x / ctas;  // tiles before the range
   Seg g;
   for (bool first = true; every.next(p, g); first = false) {
@@ -229,7 +235,7 @@ __device__ __forceinline__ int4 stream_info(const AttnLaunch& p, int ctas, int t
     if (first) r.z = g.kt1 == n ? 1 : 0;
     if (g.kt0 == 0 && g.kt1 < n) {
       r.x = g.s;
-      r.y = g.hkv + ((g.t0 - q.a) / tq << 16);
+      r.y = g.hkv + (TILES ? (g.t0 - q.a) / tq << 16 : 0);
       // The CTA with the pair's last tile, total c / ctas <= last < total (c + 1) / ctas.
       const long long last = at + n - 1;
       long long c = last * ctas / sh->total;

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   } else if (warp == 2) {
     tmem_alloc(smem_u32(&sh->tmem), 512);
   }
-  if constexpr (STREAM) stream_start<C::kThreads>(p, a.ctas, a.tq, sh);
+  if constexpr (STREAM) stream_start<C::kThreads, false>(p, a.ctas, a.tq, sh);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   };
   if (warp == 0) {
     // ---- work; loads of Q and K ----
-    SegIter iter{};
+    SegIter<false> iter{};
     if constexpr (STREAM)
-      iter = SegIter{sh->start_s, sh->start_hkv, sh->start_rt, sh->start_u, (int)blockIdx.x, a.tq, sh->left};
+      iter = SegIter<false>{sh->start_s, sh->start_hkv, sh->start_rt, sh->start_u, (int)blockIdx.x, a.tq, sh->left};
     auto role = [&] {
       Ring ring;
       uint32_t filled = 0;  // units so far
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       // What the joining kernel needs of this CTA's ranges; the outputs of
       // sequences without a key.
       if (lane == 0) {
-        a.info[blockIdx.x] = stream_info(p, a.ctas, a.tq, sh);
+        a.info[blockIdx.x] = stream_info<false>(p, a.ctas, a.tq, sh);
       }
       for (int s = blockIdx.x; s < p.N; s += a.ctas) {
         const SeqRange q = seq_range(p, s);
