@@ -255,9 +255,10 @@ cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<uint64_t>& don
 //   out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z,
 // whose sums are in the blocks slot_of(z) (negative: none), by RW warps of a CTA
 // of 8: warp w takes z = w, w + RW, ...: the (m, l) of 32 ranges first, a lane
-// each, then their weighted O, eight loads in flight.  The order of the sums
+// each, then their weighted O, AHEAD loads in flight (8 for 76 ranges of a row; for two or
+// three the wide cache's drafts take 353 us with 8, 350.5 with 4).  The order of the sums
 // depends on n alone.
-template <typename T, int D, int RW, typename SlotOf>
+template <typename T, int D, int RW, int AHEAD = 8, typename SlotOf>
 __device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& part, int n,
                                          SlotOf slot_of, int r, bool live, int t, int h) {
   constexpr int E = D / 32;
@@ -283,9 +284,9 @@ __device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& pa
     for (int e = 0; e < E; ++e) acc[e] *= f;
     unsigned todo = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
     while (todo) {
-      float x[8][E], wk[8];
+      float x[AHEAD][E], wk[AHEAD];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < AHEAD; ++k) {
         wk[k] = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) x[k][e] = 0.0f;
@@ -300,7 +301,7 @@ __device__ __forceinline__ void join_row(const AttnLaunch& p, const Partials& pa
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(wk[k], x[k][e], acc[e]);
     }

@@ -31,7 +31,7 @@ __device__ __forceinline__ int key_tiles(const SeqRange& q) {
   return q.b > q.a ? (q.kv + BK - 1) / BK : 0;
 }
 // TILES: a sequence's tokens may be several tiles of tq; else they are one (and the rest is as it
-// was without them, for the wide cache: 128 sequences' drafts take 351 us, 355 with them).
+// was without them, for the wide cache).
 template <bool TILES>
 __device__ __forceinline__ int row_tiles(const AttnLaunch& p, const SeqRange& q, int tq) {
   return !TILES ? 1 : (min(q.b - q.a, p.max_q) + tq - 1) / tq;
@@ -282,7 +282,7 @@ __device__ __forceinline__ void stream_join(const AttnLaunch& p, const Args& a) 
     return;
   }
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    join_row<T, D, 8>(p, part, c1 - c0 + 1, slot_of, r, true, q.a + first + r / G, hkv * G + r % G);
+    join_row<T, D, 8, FEW ? 8 : 4>(p, part, c1 - c0 + 1, slot_of, r, true, q.a + first + r / G, hkv * G + r % G);
     __syncthreads();
   }
 }
