@@ -27,9 +27,9 @@
 // are a sixty-fourth of their rate.
 //
 // Bound by the read of the logits in the end; now by the instructions and their latency: 64 x 8
-// rows of 131072 bf16 (134 MB, 20 us) take 38 us with K = 16, 10 of them the join's and
-// what goes on around it, and 35 with K = 2; f32 (268 MB, 40 us) 53.  One CTA more per SM,
-// one stage more or less, or chunks of 2048 vectors are within 2 %; chunks of 512 took 46.
+// rows of 131072 bf16 (134 MB, 20 us) take 37 us with K = 16, some 9 of them the join's and
+// what goes on around it, and 34 with K = 2; f32 (268 MB, 40 us) 53.  A stage more or less
+// and chunks of 2048 vectors are within 2 %; chunks of 512 took 46.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -182,12 +182,12 @@ __device__ __forceinline__ float nth_top(float x, int n) {
 template <typename T>
 struct RowShared {
   uint4 ring[kStages][kUnroll][kThreads];
-  unsigned long long few[kRanked];
+  unsigned long long few[2][kRanked];  // of every other segment
   unsigned long long best[kWarps];
   float refs[kThreads], parts[kThreads];
   float cells[kCells][kThreads];  // each thread's largest logit of a chunk
   float floors[kWarps];           // values that a warp's share of K logits has reached
-  int few_count, found_count;
+  int few_count[2], found_count;
   uint16_t found[kFound];  // cells that reach the floor
 };
 
@@ -274,6 +274,7 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
   for (int i = 0; i < kStages; ++i) copy(i);
   int stage = 0;
 
+  int side = 0;
   for (; left > 0; ++row, u0 = 0) {
     const int u1 = min(U, u0 + left);
     left -= u1 - u0;
@@ -295,7 +296,8 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
       }
       continue;
     }
-    if (tid == 0) sh.few_count = sh.found_count = 0;  // (counted behind the next barrier)
+    unsigned long long* few = sh.few[side];
+    if (tid == 0) sh.few_count[side] = sh.found_count = 0;  // (counted behind the next barrier)
     bool crowded = false;   // more found than there is room for
     float top = -INFINITY;  // this thread's largest logit
     float ref = -INFINITY;  // its sum of 2^(H x - ref), in two parts
@@ -346,8 +348,8 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
     // A logit that reaches the floor, to be ranked.
     auto put = [&](float y, int v) {
       if (y >= floor_ && y > -INFINITY) {
-        const int to = atomicAdd(&sh.few_count, 1);
-        if (to < kRanked) sh.few[to] = entry(y, (uint32_t)v);
+        const int to = atomicAdd(&sh.few_count[side], 1);
+        if (to < kRanked) few[to] = entry(y, (uint32_t)v);
       }
     };
     // The warps with a vector for every thread of theirs (one at least) take their shares of K.
@@ -437,14 +439,14 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
     }
     const bool writer = tid == kThreads - 32;
     __syncthreads();
-    const int c = sh.few_count;
+    const int c = sh.few_count[side];
     int places = min(c, K);
     if (!crowded && c <= kRanked) {  // at least K, or all above -inf
       for (int k = tid; k < c; k += kThreads) {
-        const unsigned long long mine = sh.few[k];
+        const unsigned long long mine = few[k];
         int rank = 0;
 #pragma unroll 4
-        for (int i = 0; i < c; ++i) rank += sh.few[i] > mine;
+        for (int i = 0; i < c; ++i) rank += few[i] > mine;
         if (rank < K) list[rank] = mine;
       }
     } else {
@@ -476,7 +478,9 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
       }
     }
     if (writer) *sum_out = SegSum{most, places, d};
-    __syncthreads();  // the shared lists are filled anew
+    // The warps that have none to rank go on: `few` is filled anew two segments on, and the rest
+    // behind the barriers above.
+    side ^= 1;
   }
 }
 
