@@ -257,10 +257,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       sh->abort = sh->redone = 0;
       fence_mbar_init();
     }
-  } else if (warp == 3) {
-    tmem_alloc(smem_u32(&sh->tmem), C::kCols);
   }
   wait_for_previous_kernel();
+  // Tensor memory is taken only now: had a CTA of this kernel taken it first, one of the kernel
+  // before, beside it on the SM, could wait for it, and this one for that kernel's end.
+  if (warp == 3) tmem_alloc(smem_u32(&sh->tmem), C::kCols);
   start_next_kernel();
   stream_start<C::kThreads, true>(p, a.ctas, a.tq, sh);
   fence_before_sync();

@@ -105,3 +105,75 @@ def test_step_on_a_cache_in_8_bits(new_prompts, cuda_device):
     with pytest.raises(ValueError):
         step.run(qg[..., :D], kv[:, :Hkv], kv[:, Hkv:], cu, None, c["block_table"], c["k_cache"], c["v_cache"],
                  k_scale=c["k_scale"])
+
+
+@pytest.mark.parametrize("dtype,q_len,Hq", [(torch.bfloat16, 1, 8), (torch.bfloat16, 70, 8), (torch.float32, 1, 2)])
+def test_captured_together(dtype, q_len, Hq, cuda_device):
+    """The calls of a step in one graph, on a side stream, between kernels of others: bit for bit
+    as one after another, each replay from changed inputs."""
+    dev, n, W, Hkv, D, page, V = cuda_device, 2, 2, 2, 128, 32, 5000
+    g = torch.Generator(device=dev).manual_seed(q_len + Hq)
+    N = n * W
+    lens = [300, 90, 128, 701][:N]
+    pages = N * 24
+    table = torch.randperm(pages, generator=g, device=dev).to(torch.int32).view(N, 24)
+    kv = torch.tensor(lens, dtype=torch.int32, device=dev)
+    cu = torch.arange(0, N * q_len + 1, q_len, dtype=torch.int32, device=dev)
+    T = N * q_len
+    start = dict(k_cache=torch.randn(pages, Hkv, page, D, generator=g, device=dev).to(torch.float8_e4m3fn),
+                 v_cache=torch.randn(pages, Hkv, page, D, generator=g, device=dev).to(torch.float8_e4m3fn),
+                 k_scale=torch.ones(pages, Hkv, 2, device=dev), v_scale=torch.ones(pages, Hkv, 2, device=dev))
+    inputs = [(torch.randn(T, Hq, D, generator=g, device=dev).to(dtype), torch.randn(T, Hkv, D, generator=g, device=dev).to(dtype),
+               torch.randn(n, W, V, generator=g, device=dev).to(dtype)) for _ in range(3)]
+    cos_sin = torch.randn(800, 64, generator=g, device=dev)
+    slots = torch.arange(N, dtype=torch.int32, device=dev).view(n, W)
+    q, k, logits = (t.clone() for t in inputs[0])
+    c = {m: t.clone() for m, t in start.items()}
+    q_out, out = torch.empty_like(q), torch.empty_like(q)
+    scores = torch.zeros(n, W, device=dev)
+    par, tok = (torch.empty(n, W, dtype=torch.int32, device=dev) for _ in range(2))
+    state = torch.zeros(N, T * Hq * D // N, dtype=dtype, device=dev)
+    need = B.gdn_attn8_paged_workspace_bytes(T, N, Hq, Hkv, D, q_len, B._dt(q), 24, page)
+    ws = [torch.empty(max(1, b), dtype=torch.uint8, device=dev)
+          for b in (need, B.gdn_beam_select_workspace_bytes(n, W, V, W))]
+
+    def step(stream):
+        B.gdn_attn8_prepare(q, k, k, cu, q_out, kv_lens=kv, block_table=table, cos_sin=cos_sin, stream=stream, **c)
+        B.gdn_attn8_paged(q_out, *c.values(), table, kv, cu, out, max_q_len=q_len, workspace=ws[0], stream=stream)
+        state.copy_(out.view(N, -1))
+        B.gdn_beam_select(logits, scores, par, tok, scores, workspace=ws[1], stream=stream)
+        B.gdn_copy_slots([state, c["k_scale"][:N], table], slots, par, groups=True, stream=stream)
+
+    tab0 = table.clone()
+
+    def reset(i):
+        for t, s in zip((q, k, logits), inputs[i]):
+            t.copy_(s)
+        for m, t in start.items():
+            c[m].copy_(t)
+        table.copy_(tab0)
+        scores.zero_()
+
+    def results():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (q_out, out, state, scores, par, tok, table, *(x.view(torch.uint8) for x in c.values()))]
+
+    want = []
+    for i in range(3):
+        reset(i)
+        torch.cuda.synchronize()
+        step(None)
+        want.append(results())
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(torch.cuda.current_stream())
+    for i in (1, 0, 2, 1):
+        reset(i)
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.default_stream())
+            graph.replay()
+        got = results()
+        for a, b in zip(got, want[i]):
+            assert torch.equal(a, b)
+    B.gdn_read_device_status()
