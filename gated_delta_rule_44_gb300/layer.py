@@ -150,6 +150,7 @@ class AttnStep:
         self.workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
         self.dt = dt
         self.widths = {}  # table width and page size: workspace bytes of the calls on a cache in 8 bits
+        self.outgrown = []  # smaller workspaces, which graphs captured earlier go on using
 
     def run(self, q, k, v, cu_seqlens, kv_lens, block_table, k_cache, v_cache, *,
             cu_seqlens_prefill=None, gate=None, q_norm_weight=None, k_norm_weight=None,
@@ -169,7 +170,7 @@ class AttnStep:
             raise ValueError("a cache in 8 bits has k_scale and v_scale")
         eight = k_scale is not None
         if eight:
-            self._grow8(block_table.shape[1], k_cache.shape[2])
+            self._grow8(block_table.shape[1], k_cache.shape[2], stream)
         scales = (k_scale, v_scale) if eight else ()
         prepare, paged = ((B.gdn_attn8_prepare, B.gdn_attn8_paged) if eight
                           else (B.gdn_attn_prepare, B.gdn_attn_paged))
@@ -193,7 +194,7 @@ class AttnStep:
                       gate=g, workspace=self.workspace, stream=stream)
         return out
 
-    def _grow8(self, width: int, page: int) -> None:
+    def _grow8(self, width: int, page: int, stream) -> None:
         """Room for the calls on a cache in 8 bits with tables of this width."""
         if (width, page) in self.widths:
             return
@@ -206,7 +207,8 @@ class AttnStep:
             need = max(need, B.gdn_attn8_paged_workspace_bytes(Tp, Np, self.Hq, self.Hkv, self.D,
                                                                self.max_q_len, self.dt, width, page))
         if need > self.workspace.numel():
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.workspace.device)
+            self.outgrown.append(self.workspace)
+            self.workspace = B._scratch(need, self.workspace.device, stream)
         self.widths[(width, page)] = need
 
 

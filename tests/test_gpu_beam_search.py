@@ -107,6 +107,43 @@ def test_step_on_a_cache_in_8_bits(new_prompts, cuda_device):
                  k_scale=c["k_scale"])
 
 
+def test_step_captured_before_a_wider_table(cuda_device):
+    """A graph keeps the workspace that it was captured with, after the step has grown another for
+    a wider table and the memory around it has been written."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(5)
+    T, Hq, Hkv, D = 300, 8, 2, 128            # 300 tokens of 4 heads each: contexts are widened
+    c, _ = make_cache8(g, [700], Hkv, D, 32, 16, dev)
+    q, k = (torch.randn(T, h, D, generator=g).to(BF).to(dev) for h in (Hq, Hkv))
+    cu = torch.tensor([0, T], dtype=torch.int32, device=dev)
+    kv = torch.tensor([700], dtype=torch.int32, device=dev)
+    step = AttnStep(T, 1, 0, Hq, Hkv, D, BF, dev, max_q_len=T)
+    wide = torch.cat([c["block_table"], torch.full((1, 500), -1, dtype=torch.int32, device=dev)], 1)
+
+    def run(table, stream=None):
+        return step.run(q, k, k, cu, kv, table, c["k_cache"], c["v_cache"], cu_seqlens_prefill=cu,
+                        k_scale=c["k_scale"], v_scale=c["v_scale"], stream=stream)
+
+    want = run(c["block_table"]).clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(c["block_table"], torch.cuda.current_stream())
+    size = step.workspace.numel()
+    # (The widened form cuts its keys by the table's width: other sums, within a rounding or two of
+    # the weights, 2^-8, and of the result.)
+    assert torch.allclose(run(wide).float(), want.float(), rtol=2.0 ** -7, atol=2.0 ** -7 * want.float().abs().max().item())
+    assert step.workspace.numel() > size
+    junk = [torch.full((size,), 0xFF, dtype=torch.uint8, device=dev) for _ in range(4)]
+    keep = [j.clone() for j in junk]
+    step.out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(step.out, want)
+    for a, b in zip(junk, keep):
+        assert torch.equal(a, b)
+    B.gdn_read_device_status()
+
+
 @pytest.mark.parametrize("dtype,q_len,Hq", [(torch.bfloat16, 1, 8), (torch.bfloat16, 70, 8), (torch.float32, 1, 2)])
 def test_captured_together(dtype, q_len, Hq, cuda_device):
     """The calls of a step in one graph, on a side stream, between kernels of others: bit for bit
