@@ -699,7 +699,7 @@ Split split_rows(int64_t rows, int64_t V, bool bf16) {
   s.per_row = (int)((V + chunk - 1) / chunk);
   s.chunks = rows * s.per_row;
   s.ctas = (int)std::min<int64_t>({kCtasPerSm * 152, s.chunks, (kMaxSegs - 2) * rows});
-  s.segs = (int)(s.ctas / rows + (s.ctas % rows ? 2 : 0));
+  s.segs = (int)std::min<int64_t>(s.per_row, s.ctas / rows + (s.ctas % rows ? 2 : 0));
   return s;
 }
 
