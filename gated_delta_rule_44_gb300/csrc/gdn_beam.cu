@@ -716,9 +716,11 @@ cudaError_t launch_rows(const BeamLaunch& p, const Split& s, cudaStream_t st) {
 }  // namespace
 
 size_t beam_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t K) {
-  // (of two types, the one with more lists)
-  const int64_t segs = std::max(split_rows(B * W, V, true).segs, split_rows(B * W, V, false).segs);
-  return (size_t)(B * W * segs * ((int64_t)sizeof(SegSum) + 8 * K));
+  // Of both types (f32 has more chunks), and as much for any smaller sizes: segs <= per_row, and
+  // rows * segs <= ctas + 2 rows.
+  const int64_t rows = B * W;
+  const int64_t lists = std::min<int64_t>(rows * split_rows(rows, V, false).per_row, kCtasPerSm * 152 + 2 * rows);
+  return (size_t)(lists * ((int64_t)sizeof(SegSum) + 8 * K));
 }
 
 cudaError_t launch_beam(const BeamLaunch& p, cudaStream_t st) {

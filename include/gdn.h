@@ -904,6 +904,8 @@ typedef struct gdn_beam_select_args {
 
 int gdn_beam_select(const gdn_beam_select_args* args, void* stream);
 
+/* Workspace bytes of a call of these sizes, which do for every smaller one, too (0 for sizes
+ * the call would refuse). */
 size_t gdn_beam_select_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t K);
 
 /* gdn_copy_slots -- whole slots of any pools (recurrence states, conv tails, pages of a

@@ -46,6 +46,16 @@ def test_beam():
     assert f(2, 4, 100, 4) > 0 and f(0, 4, 100, 4) == 0 and f(2, 65, 100, 4) == 0
 
 
+def test_beam_workspace_does_for_smaller_calls():
+    f = B.gdn_beam_select_workspace_bytes
+    for W, V, K in ((1, 131072, 1), (4, 32003, 8), (8, 131072, 16), (3, 200, 3), (64, 5000, 128)):
+        needs = [f(n, W, V, K) for n in range(1, 700)]
+        assert needs == sorted(needs)
+        assert f(50, W, V - 100, K) <= f(50, W, V, K) and f(50, W, V, K) <= f(50, W, V, K + 1 if K < 128 else K)
+        # a list for every chunk of 4096, or a row's two ends and what 304 blocks cut
+        assert needs[-1] <= (304 + 2 * 699 * W) * (16 + 8 * K)
+
+
 def pool(**over):
     a = dict(data=FAKE, len=10 * 64, slots=10, slot_bytes=64, slot_stride=0)
     a.update(over)
