@@ -21,6 +21,11 @@
 // A team is the D / 8 lanes of one row where the calls bring a few tokens a sequence, and a
 // CTA of 256 threads where they bring many.  Beside the items, further CTAs of the same
 // launch do the rows of q (and of k for k_out).
+//
+// Four prompts of 2048, 16 + 2 heads of 256 (161 MB, 24 us) take 40 us, bound by the instructions
+// of the rows of q as in gdn_attn_prepare.cu (57 % of the issue rate); with the values of k and v
+// kept in shared memory instead of computed twice, or three or five CTAs per SM, 40, 43.5
+// and 43.7.  512 single tokens take 10.5 us of kernel time, two chains of dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
