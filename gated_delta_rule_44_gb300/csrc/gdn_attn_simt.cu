@@ -24,7 +24,8 @@
 // (21 TFLOP/s, about 28 % of the FMA rate; the shared-memory loads of the 4 x 4
 // pieces and the barriers between a block's phases bind; packed two-lane FMAs
 // changed nothing).  8 single tokens over up to 4097 keys: 24 us a call, of which
-// the chains of loads of a few steps per warp and the join take most.
+// the chains of loads of a few steps per warp and the join take most; 27 over a cache in
+// 8 bits (33 before a step's codes were loaded during the step before).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
