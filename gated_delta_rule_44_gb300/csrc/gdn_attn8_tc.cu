@@ -2,19 +2,27 @@
 // over a cache in 8 bits, on tcgen05 tensor cores, without widening a code.
 //
 // The codes go from the cache to the tensor cores as they are; what is multiplied with
-// them comes in two e4m3 parts, x ~ hi + lo / 32 with hi = e4m3(x), lo = e4m3(32 (x - hi)):
-// q, scaled by a power of two per row, which hi and lo hold exactly down to 2^-10 of the
-// row's largest value (a bf16 has 8 significant bits, the parts 4 and a sign each), and
-// the weights, to 2^-8 relative, as a weight rounded to bf16 would be.  The products are
+// them comes in e4m3 parts.  q, scaled by a power of two per row, in two, x ~ hi + lo / 32 with
+// hi = e4m3(x), lo = e4m3(32 (x - hi)), which hold it exactly down to 2^-10 of the row's largest
+// value (a bf16 has 8 significant bits, the parts 4 and a sign each).  The products are
 // transposed, so that the 128 rows of an MMA are keys or dims, all in use, and the few rows
 // of q are its columns, twice, for hi and lo:
 //   S^T [128 keys x 2R] = K q^T          A = K as it lies in the cache, B = q
 //   O^T [128 dims x 2R] += V^T p^T       A = V^T (keys outermost), B = p
 // with  s = (S_hi + S_lo / 32) kscale qscale log2(e),
-//       p = 2^(s - m) vscale,  l += 2^(s - m),  out = (O_hi + O_lo / 32) / l.
+//       p = 2^(s - m) vscale,  l += 2^(s - m),  out = (O_1 + O_2 / 2^15) / l.
 // m is a reference for p, which has to stay within e4m3's range: the maximum of s +
 // log2(vscale) so far, raised (and O and l scaled) once a tile's maximum is 2^4 above it.
 // So blocks of small values keep their precision beside blocks of large ones.
+//
+// p in four parts, two for each of O's accumulators: x = 16 p, rounded to f16, is
+//   x ~ a + b + (c + d) / 2^15,  a = e4m3(x), b = e4m3(x - a), c = e4m3(y), d = e4m3(y - c),
+//   y = 2^15 (x - a - b),
+// a and c in one B operand of the MMAs, b and d in a second one that adds to the same two
+// accumulators.  Two parts alone (a and e4m3(32 (x - a))) end at 2^-14: where one key has
+// most of a row's weight, thousands of others are below that, and what they add up to was lost.
+// Four hold every f16 to 2^-9 of itself, so that a weight is off by 2^-8 of it at most down to
+// 2^-21 of the largest, and by 2^-29 of that below.
 //
 // Warps:  0       hands out the ranges of key tiles; TMA loads of K, a ring of tiles of 128 keys
 //         1       the MMAs
@@ -29,15 +37,17 @@
 // scores (whose barrier says also that the scales are there, and, the MMAs being one warp's in
 // order, that P's buffer is free again), for the maxima, and for the P V of the tile before
 // where O is scaled.  More groups that took the tiles in turns were no faster (spills).
-// Two S and two P buffers: the scores of a tile are computed during the softmax of the one
-// before.  Two CTAs share an SM where their memory allows it, and hide each other's chains.
+// Two S and two P buffers (one P for 64 rows of D = 256, where K and V leave room for no more): the
+// scores of a tile are computed during the softmax of the one before.  Two CTAs share an SM where their memory allows it, and hide each other's chains.
 // The work is that of the stream form (gdn_attn_stream.cuh).
 //
 // Bound by HBM where many sequences keep every SM's rings full: 256 single tokens over 1 to
-// 16384 keys, 32 + 4 heads of 128, take 338 us (2.2 GB at 6.6 TB/s, 98 % of the copy rate); 128
-// sequences with 1 to 4 drafts over up to 8192 keys, 32 + 8 heads, 16-row pages, 195 (1.06 GB
-// at 5.4 TB/s: TMA loads of 2 KB, and the ranges' ends); one token over 200003 keys 48 (205 MB, 33 to 41 of it the main
-// kernel, then the join of 76 ranges).
+// 16384 keys, 32 + 4 heads of 128, take 339 to 342 us (2.2 GB at 6.6 TB/s, 98 % of the copy rate); 128
+// sequences with 1 to 4 drafts over up to 8192 keys, 32 + 8 heads, 16-row pages, 198 to 200 (1.06 GB
+// at 5.3 TB/s: TMA loads of 2 KB, and the ranges' ends); one token over 200003 keys 48 (205 MB, 33 to 41 of it the main
+// kernel, then the join of 76 ranges).  32 and 64 rows of the 256 single tokens' contexts, 128 and 256
+// query heads, take 474 and 730 (bound by the chain of the softmax and, at 64, the MMAs).  Against two
+// parts of p, four cost 0.5 to 2 % with up to 16 rows, 5 and 12 % with 32 and 64.
 //
 // A row whose result is not finite, or whose l is too small to be trusted (blocks whose
 // scales differ by 2^90), is evaluated again key by key (exact_row).  Every wait is bounded.
@@ -63,7 +73,8 @@ using bf16 = __nv_bfloat16;
 constexpr int kMaxRing = 8, kSegs = 4, kMaxGroups = 4;
 constexpr float kHeadroom = 4.0f;       // log2: p reaches 2^4 before the reference follows
 constexpr float kPScale = 16.0f;        // p 2^4 in the parts' units: at most 256 of 448
-constexpr float kLoScale = 32.0f;
+constexpr float kLoScale = 32.0f;       // of q's second part
+constexpr float kLowScale = 32768.0f;   // 2^15: of p's third and fourth
 constexpr float kLeastSum = 8.0e-28f;   // 2^-90
 
 struct Shared {
@@ -95,12 +106,14 @@ struct Cfg {
   static constexpr int kRowBytes = D < 128 ? D : 128;  // of a swizzled row of K, V and q
   static constexpr int NB = D / kRowBytes;             // blocks of them
   static constexpr uint32_t kTile = 128 * D;           // of K, of V
-  static constexpr uint32_t kQ = N * D, kP = 128 * N;
+  static constexpr uint32_t kQ = N * D, kHalfP = 128 * N, kP = 2 * kHalfP;
   static constexpr int kCtas = D <= 128 && R <= 16 ? 2 : 1;  // per SM
   static constexpr uint32_t kRoom = kCtas == 2 ? 115712 : 232448;
-  static constexpr int kFit = (int)((kRoom - sizeof(Shared) - kQ - 2 * kP) / (2 * kTile));
+  // P buffers: two, but for the largest tiles, whose K and V would not be two each any more.
+  static constexpr int kPBufs = kRoom - sizeof(Shared) - kQ - 2 * kP >= 4 * kTile ? 2 : 1;
+  static constexpr int kFit = (int)((kRoom - sizeof(Shared) - kQ - kPBufs * kP) / (2 * kTile));
   static constexpr int ST = kFit > kMaxRing ? kMaxRing : kFit;
-  static constexpr uint32_t kV = ST * kTile, kQAt = 2 * ST * kTile, kPAt = kQAt + kQ, kBars = kPAt + 2 * kP;
+  static constexpr uint32_t kV = ST * kTile, kQAt = 2 * ST * kTile, kPAt = kQAt + kQ, kBars = kPAt + kPBufs * kP;
   static constexpr uint32_t kBytes = kBars + sizeof(Shared);
   static constexpr int kGroups = R / RG;
   static constexpr int kThreads = 128 + 128 * kGroups;
@@ -210,6 +223,23 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
       "cvt.u32.u16 %0, c;\n\t}\n"
       : "=r"(lo)
       : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
+}
+// The four parts of a pair of weights: a and b, and 2^15 times what they leave in c and d.  (What
+// is more than 448 becomes that: of weights that a and b hold to 2^-9 already.)
+__device__ __forceinline__ void split4(float a, float b, uint32_t (&part)[4]) {
+  __half2 x = __floats2half2_rn(a, b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i == 2) x = __hmul2(x, __float2half2_rn(kLowScale));
+    uint32_t back;
+    asm("{\n\t.reg .b16 c;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 c, %2;\n\t"
+        "cvt.u32.u16 %0, c;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, c;\n\t}\n"
+        : "=r"(part[i]), "=r"(back)
+        : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+    if (i < 3) x = __hsub2(x, *reinterpret_cast<const __half2*>(&back));
+  }
 }
 
 #define WAIT(bar, parity) \
@@ -392,16 +422,16 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           if (j == 0 && nseg > 0) WAIT(sh->o_empty, (nseg - 1) & 1);
           fence_after_sync();
           if (elect_one()) {
-            const uint64_t pd = desc_of(sp + (nk & 1) * C::kP, 16, 8 * N, N);
+            const uint64_t pd = desc_of(sp + (C::kPBufs == 2 ? (nk & 1) * C::kP : 0), 16, 8 * N, N);
 #pragma unroll
             for (int b = 0; b < C::OB; ++b) {
               // (D = 64: dims 64 .. 127 of the product are not used; they read the tile's
               // second half.)
               const uint64_t vd = desc_of(sv + vr.st * C::kTile + b * 128 * ROW, 64 * ROW, 8 * ROW, ROW);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_e4m3(tmem + C::kTO + b * N, vd + ((k * 32 * ROW) >> 4), pd + ((k * 32 * N) >> 4), kIdPV,
-                         j + k > 0);
+              for (int k = 0; k < 8; ++k)  // a and c, then b and d, of 32 keys
+                mma_e4m3(tmem + C::kTO + b * N, vd + ((k / 2 * 32 * ROW) >> 4),
+                         pd + ((k % 2 * C::kHalfP + k / 2 * 32 * N) >> 4), kIdPV, j + k > 0);
             }
             mma_commit(smem_u32(&sh->v_empty[vr.st]));
             mma_commit(smem_u32(&sh->pv[nk & 1]));
@@ -642,10 +672,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             float2 ref[RG / 2];
             read_rows<RG>(own, ref);
             const float2 vs = make_float2(vsc * kPScale, vsc * kPScale);
-            uint32_t hi[RG / 4], lo[RG / 4];
+            uint32_t parts[4][RG / 4];
 #pragma unroll
             for (int i = 0; i < RG / 4; ++i) {
-              uint32_t h[2], o[2];
+              uint32_t of[2][4];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int k = 2 * i + e;
@@ -654,18 +684,25 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
                 w.y = ex2(w.y);
                 l[k] = __fadd2_rn(l[k], w);
                 w = __fmul2_rn(w, vs);
-                split2(w.x, w.y, h[e], o[e]);
+                split4(w.x, w.y, of[e]);
               }
-              hi[i] = h[0] | h[1] << 16;
-              lo[i] = o[0] | o[1] << 16;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) parts[k][i] = of[0][k] | of[1][k] << 16;
             }
-            // (P[buf] has been read: the scores' MMAs followed that product.)
-            unsigned char* to = smem + C::kPAt + buf * C::kP + r * N;
-            if constexpr (RG == 16) {
-              *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr + 1) * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            } else {
-              *reinterpret_cast<uint4*>(to + swz<N>(r, 0) * 16) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+            // (P[buf] has been read: the scores' MMAs followed that product.  One buffer is read
+            // by the product of the tile before.)
+            if constexpr (C::kPBufs == 1)
+              if (kt > g.kt0) WAIT(sh->pv[buf ^ 1], ((nk - 1) >> 1) & 1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const auto &first = parts[k], &second = parts[k + 2];
+              unsigned char* to = smem + C::kPAt + (C::kPBufs == 2 ? buf * C::kP : 0) + k * C::kHalfP + r * N;
+              if constexpr (RG == 16) {
+                *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr) * 16) = make_uint4(first[0], first[1], first[2], first[3]);
+                *reinterpret_cast<uint4*>(to + swz<N>(r, 2 * gr + 1) * 16) = make_uint4(second[0], second[1], second[2], second[3]);
+              } else {
+                *reinterpret_cast<uint4*>(to + swz<N>(r, 0) * 16) = make_uint4(first[0], first[1], second[0], second[1]);
+              }
             }
           }
           if (gr == 0 && (kt + 1) * BK > g.hi) {
@@ -716,7 +753,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             float f[RG];
             read_rows<RG>(own, f);
 #pragma unroll
-            for (int i = 0; i < RG; ++i) o[i] = fmaf(y[RG + i], 1.0f / kLoScale, y[i]) * f[i];
+            for (int i = 0; i < RG; ++i) o[i] = fmaf(y[RG + i], 1.0f / kLowScale, y[i]) * f[i];
           }
           const int dim = b * 128 + r;
           if (D >= 128 || r < D) {
@@ -868,9 +905,14 @@ int ctas_per_sm(int64_t rows) {
 
 }  // namespace
 
-// More than 64 rows read their keys again for every 64; against widening first, 128 rows
-// take 320 and 600 us (128 sequences of 4096 keys, 4 kv heads of 128), 40 and 66 (one of
-// 32768), 256 rows 619 and 555, 59 and 68, 512 rows 84 and 84 (one).
+// More than 64 rows read their keys again for every 64.  Against widening first (4 kv heads; 128
+// sequences of 4096 keys, one of 32768), us:
+//   rows       64              128             192             256
+//   D = 64     188/374 32/45   354/397 40/56   520/422 52/44   688/429 61/54
+//   D = 128    191/541 32/55   357/570 42/68   524/547 53/55   693/556 63/68
+//   D = 256    249/1025 46/96  465/1127 54/117 682/1136 69/96  909/1157 81/109
+// Widening also takes a workspace as large as the contexts, so it begins where it gains in
+// every shape of D = 128 and more.
 bool attn8_tc_supported(int64_t rows, int64_t D, bool bf16) { return bf16 && D >= 64 && rows <= kMostRows; }
 
 size_t attn8_tc_workspace_bytes(int64_t rows, int64_t D) {
