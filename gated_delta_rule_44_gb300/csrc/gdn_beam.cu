@@ -12,6 +12,10 @@
 // and ln sum e^x = ref / H + ln(sum) to within the 1.3e-8 (largest x - x) that H's rounding
 // leaves, where x has its weight.  So an element costs half of an fma, an exponential and
 // half of an add.  The threads' sums are joined in f64.
+// Past 2^22 a whole number near H x is no longer near the product (from 2^32 on the fma's result may
+// be in the hundreds).  So ref is -2^22 at least, where what is further down (a mask) has no
+// weight beside anything else; and a segment whose largest logit itself is beyond 2^22 on
+// either side sums 2^(H (x - top)), top its largest logit, by reading it once more ("far").
 // The segment's K largest logits: while it reads, a thread notes only its largest logit of each
 // chunk.  Then every warp gives the n-th largest of its threads' maxima, n warps' shares of
 // K, and the least of these is a value that at least K logits reach; the some 3 K chunks of
@@ -27,9 +31,9 @@
 // are a sixty-fourth of their rate.
 //
 // Bound by the read of the logits in the end; now by the instructions and their latency: 64 x 8
-// rows of 131072 bf16 (134 MB, 20 us) take 37 us with K = 16, some 9 of them the join's and
-// what goes on around it, and 34 with K = 2; f32 (268 MB, 40 us) 53.  A stage more or less
-// and chunks of 2048 vectors are within 2 %; chunks of 512 took 46.
+// rows of 131072 bf16 (134 MB, 20 us) take 38 us with K = 16, some 9 of them the join's and
+// what goes on around it, and 34.5 with K = 2; f32 (268 MB, 40 us) 54.5.  A stage more or less
+// and chunks of 2048 vectors are within 2 %; chunks of 512 took 46.  (The care for far segments took 0.9 of the 38.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -53,9 +57,12 @@ constexpr int kStages = 3;      // chunks of a CTA on their way
 constexpr int kChunk = kThreads * kUnroll;  // vectors
 constexpr int kCtasPerSm = 2;
 constexpr float kH = 1.4426950408889634f;  // log2(e) in f32
+constexpr float kFarRef = 4194304.0f;
+constexpr int kFar = 1 << 30;
 
 // What a segment leaves: the count of its list's entries (value key, ~index), and its sum of
-// 2^(H x - ref) (ref -inf: nothing is above that).
+// 2^(H x - ref) (ref -inf: nothing is above that).  A far segment, kFar in `count`: of
+// 2^(H (x - ref)).
 struct SegSum {
   float ref;
   int count;
@@ -187,6 +194,8 @@ struct RowShared {
   float refs[kThreads], parts[kThreads];
   float cells[kCells][kThreads];  // each thread's largest logit of a chunk
   float floors[kWarps];           // values that a warp's share of K logits has reached
+  double far[kWarps];             // a far segment's sums
+  float most;                     // the segment's largest ref
   int few_count[2], found_count;
   uint16_t found[kFound];  // cells that reach the floor
 };
@@ -307,7 +316,7 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
     auto raise = [&](float y) {
       if (y > top) {
         top = y;
-        const float up = ceilf(y * kH);
+        const float up = fmaxf(ceilf(y * kH), -kFarRef);
         if (up > ref) {
           if (ref != -INFINITY) {  // (a sum of NaN stays one)
             const float f = ex2(ref - up);
@@ -438,7 +447,26 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
       for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     }
     const bool writer = tid == kThreads - 32;
+    if (writer) sh.most = most;
     __syncthreads();
+    const int v0 = u0 == 0 ? 0 : r.head + u0 * kChunk * V::N;
+    const uint32_t v1 = u1 == U ? p.V : r.head + u1 * kChunk * V::N;
+    const bool far = sh.most > kFarRef || sh.most == -kFarRef;
+    if (far) {
+      const float mine = warp_top(top);
+      if (lane == 0) sh.floors[warp] = mine;
+      __syncthreads();
+      most = sh.floors[0];
+      for (int w = 1; w < kWarps; ++w) most = fmaxf(most, sh.floors[w]);
+      d = 0.0;
+      for (uint32_t v = v0 + tid; v < v1; v += kThreads) d += (double)ex2((attn::to_f(r.x[v]) - most) * kH);
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if (lane == 0) sh.far[warp] = d;
+      __syncthreads();
+      d = 0.0;
+      for (int w = 0; w < kWarps; ++w) d += sh.far[w];
+    }
     const int c = sh.few_count[side];
     int places = min(c, K);
     if (!crowded && c <= kRanked) {  // at least K, or all above -inf
@@ -451,8 +479,6 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
       }
     } else {
       // Too many: place after place, the largest entry below the last one.
-      const int v0 = u0 == 0 ? 0 : r.head + u0 * kChunk * V::N;
-      const uint32_t v1 = u1 == U ? p.V : r.head + u1 * kChunk * V::N;
       unsigned long long last = ~0ull;
       for (places = 0; places < K; ++places) {
         unsigned long long mine = 0;
@@ -477,7 +503,7 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
         __syncthreads();
       }
     }
-    if (writer) *sum_out = SegSum{most, places, d};
+    if (writer) *sum_out = SegSum{most, places | (far ? kFar : 0), d};
     // The warps that have none to rank go on: `few` is filled anew two segments on, and the rest
     // behind the barriers above.
     side ^= 1;
@@ -511,14 +537,26 @@ __device__ __forceinline__ void sort_scores(unsigned long long* key, uint32_t* i
     }
 }
 
+// A beam's segments with a far one among them: the logit that their joined sum refers to.
+// By a warp, a lane per segment; `total`: the lane's part of the sum.
+__device__ __noinline__ double far_join(const SegSum& x, double& total) {
+  const double at = x.count & kFar ? (double)x.ref : (double)x.ref * (1.0 / (double)kH);
+  double most = at;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
+  total = at == -INFINITY ? x.sum : x.sum * exp2((at - most) * (double)kH);  // (NaN of an infinity)
+  return most;
+}
+
 // What limits the join is fetching its own instructions, so loops are not unrolled.
 struct JoinShared {
   unsigned long long list[kRoom];
   unsigned long long key[kRoom];
   uint32_t index[kRoom];
   float heads[8 * kThreads];  // [level][list]
-  double base[kBeamMaxW];     // score - log sum of each beam; NaN: takes no part
-  float base_f[kBeamMaxW];
+  double base[kBeamMaxW];     // score - log of the sum of each beam; NaN: takes no part
+  double at[kBeamMaxW];       // the logit that the sum refers to
+  float base_f[kBeamMaxW], at_f[kBeamMaxW];
   int counts[kBeamMaxW * kMaxSegs];
   uint32_t least;
   int count;
@@ -558,33 +596,41 @@ beam_join_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
     SegSum x{-INFINITY, 0, 0.0};
     if (lane < segs) {
       x = sums[w * segs + lane];
-      sh.counts[w * segs + lane] = x.count;
+      sh.counts[w * segs + lane] = x.count & ~kFar;
     }
-    const float most = warp_top(x.ref);
-    // 2^(ref - most) from its bits; 0 from 2^-1023 on.
-    const float e = x.ref - most + 1023.0f;
-    double total = x.ref == -INFINITY ? x.sum : x.sum * __longlong_as_double(e > 0.0f ? (long long)e << 52 : 0);
+    double total, at;
+    if (!__any_sync(0xffffffffu, x.count & kFar)) {
+      const float most = warp_top(x.ref);
+      // 2^(ref - most) from its bits; 0 from 2^-1023 on.
+      const float e = x.ref - most + 1023.0f;
+      total = x.ref == -INFINITY ? x.sum : x.sum * __longlong_as_double(e > 0.0f ? (long long)e << 52 : 0);
+      at = (double)most * (1.0 / (double)kH);
+    } else {
+      at = far_join(x, total);
+    }
 #pragma unroll 1
     for (int o = segs > 1 ? 1 << (31 - __clz(segs - 1)) : 0; o > 0; o >>= 1)
       total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane == 0) {
       sh.base[w] = total;
-      sh.base_f[w] = most;
+      sh.at[w] = at;
     }
   }
   __syncthreads();
   // A lane per beam: f64 instructions of a warp take as long for one lane as for 32.
   if (tid < p.W) {
     // Nothing in the row, an infinity or a NaN: no score of it is finite.
-    const double x = (double)score - ((double)sh.base_f[tid] * (1.0 / (double)kH) + log(sh.base[tid]));
+    const double x = (double)score - log(sh.base[tid]);
     sh.base[tid] = x;
     sh.base_f[tid] = (float)x;
+    sh.at_f[tid] = (float)sh.at[tid];
   }
   asm volatile("cp.async.wait_all;\n" ::: "memory");
   __syncthreads();
-  // In f32, to within 2^-22 (|base| + |s|); NaN or an infinity: none.
+  // base + (x - at) in f32, to within 2^-24 (|base| + |at| + |x - at| + |s|), of which the third is no
+  // more than the first and the last; NaN or an infinity: none.
   auto near_score = [&](int l, unsigned long long e) {
-    return sh.base_f[l / segs] + value_of((uint32_t)(e >> 32));
+    return sh.base_f[l / segs] + (value_of((uint32_t)(e >> 32)) - sh.at_f[l / segs]);
   };
   // If j entries of each of r lists reach a score, K = r j do: for j = 1, 2, 4, ..., the r-th
   // best of the lists' j-th entries is a floor, and the highest of these floors is taken.
@@ -614,10 +660,11 @@ beam_join_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
       float big = fabsf(floor_);
 #pragma unroll 1
       for (int w = 0; w < p.W; ++w) {  // (a NaN is passed over; infinite ones have no entries)
-        const float f = fabsf(sh.base_f[w]);
+        const float f = fabsf(sh.base_f[w]), at = fabsf(sh.at_f[w]);
         if (f <= 3.402823466e38f) big = fmaxf(big, f);
+        if (at <= kFarRef) big = fmaxf(big, at);  // (a far segment's is an f32)
       }
-      floor_ -= big * 0x1p-20f;
+      floor_ = fmaxf(floor_ - big * 0x1p-20f, -3.402823466e38f);
     }
   }
   // Beams that ended come first: one entry each.
@@ -654,7 +701,7 @@ beam_join_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
     for (int i = kept + tid; i < n; i += kThreads) {
       const unsigned long long e = sh.key[i];
       const uint32_t w = sh.index[i];
-      sh.key[i] = order_of(sh.base[w] + (double)value_of((uint32_t)(e >> 32)));
+      sh.key[i] = order_of(sh.base[w] + ((double)value_of((uint32_t)(e >> 32)) - sh.at[w]));
       sh.index[i] = w * p.V + ~(uint32_t)e;
     }
     __syncthreads();

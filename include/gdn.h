@@ -873,10 +873,10 @@ size_t gdn_attn8_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t
  * the K best, in falling order of s, at equal s by the lower w * V + v: parents[b, k] =
  * w, tokens[b, k] = v, out_scores[b, k] = s.  A beam with finished[b, w] != 0 has one
  * continuation, (w, pad_token) with s = scores[b, w]; its logits are not read.  Only a
- * finite s is chosen: a logit of -inf is a token that may not come, a score of -inf a
+ * finite s (in f32) is chosen: a logit of -inf is a token that may not come, a score of -inf a
  * beam without a life, and a row that holds a NaN or +inf, or nothing but -inf, offers
- * nothing (a logit of 2^127 or more counts as +inf).  Places left over get parent -1,
- * token -1, s = -inf.
+ * nothing.  Finite logits may be of any size; a finite mask makes a candidate, which takes a place
+ * that allowed tokens leave.  Places left over get parent -1, token -1, s = -inf.
  * Exponentials and a thread's sums are f32, sums between threads, the logarithm and s
  * are f64; s is rounded to f32 where it is stored.  (Logits so small that s does not
  * show their difference in f64 are ordered by the logit, not the index.)

@@ -1,0 +1,93 @@
+"""GPU: gdn_beam_select over logits of any finite size: masks of large finite values, rows that hold
+nothing else, logits far from zero.  Against the definition in 64 bits, as in test_gpu_beam.py."""
+import pytest
+import torch
+
+from test_gpu_beam import BF, F32, check, definition, select
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = {BF: torch.finfo(BF).min, F32: torch.finfo(F32).min}
+
+
+def value(mask, dtype):
+    return LOWEST[dtype] if mask == "lowest" else float(mask)
+
+
+def masked_but(n, W, V, keep, mask, dtype, g):
+    """Normal logits at `keep` tokens of each row, the rest masked."""
+    x = torch.full((n, W, V), value(mask, dtype))
+    for b in range(n):
+        for w in range(W):
+            at = torch.randperm(V, generator=g)[:keep]
+            x[b, w, at] = torch.randn(keep, generator=g) * 2
+    return x.to(dtype)
+
+
+MASKS = [-1e4, -1e9, -1e10, -1e12, -1e18, -1e20, -1e30, -1e32, "lowest"]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("mask", MASKS)
+def test_masks_of_large_finite_values(mask, dtype, cuda_device):
+    """A few tokens of each row are allowed; whole chunks and most threads see the mask only."""
+    g = torch.Generator().manual_seed(1)
+    n, W, V, K = 2, 3, 40011, 5
+    x = masked_but(n, W, V, 20, mask, dtype, g)
+    x[0, 0] = (torch.randn(V, generator=g) * 2).to(dtype)       # an ordinary row, its first chunks masked
+    x[0, 0, :17000] = value(mask, dtype)
+    s = -torch.rand(n, W, generator=g) * 4
+    check(select(x.to(cuda_device), s.to(cuda_device), K, cuda_device), definition(x, s, K))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("mask", [-1e9, -1e20, "lowest"])
+def test_fewer_allowed_tokens_than_places(mask, dtype, cuda_device):
+    """Masked tokens are finite candidates: they take the places that are left, lowest first."""
+    g = torch.Generator().manual_seed(2)
+    n, W, V, K = 2, 1, 9001, 12
+    x = masked_but(n, W, V, 4, mask, dtype, g)
+    s = -torch.rand(n, W, generator=g)
+    check(select(x.to(cuda_device), s.to(cuda_device), K, cuda_device), definition(x, s, K))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("level", [-1e7, -1e10, -1e20, -1e30, -1.6e38, "lowest", 2.8e6, 1e10, 1.5 * 2.0 ** 32, 1e20, 1.2e38,
+                                   3e38])
+@pytest.mark.parametrize("V", [5, 1000, 33001])
+def test_rows_far_from_zero(V, level, dtype, cuda_device):
+    """Rows of one value: each token's score is score - ln V, whatever the value.  Beside them a row
+    of several values near it, and an ordinary one."""
+    g = torch.Generator().manual_seed(3)
+    K = 4
+    x = torch.full((3, 2, V), value(level, dtype)).to(dtype)
+    step = float(x[0, 0, 0].abs()) * float(torch.finfo(dtype).eps)
+    x[1, 0] = (x[1, 0].double() + step * torch.randint(-3 if level != "lowest" else 0, 4, (V,), generator=g).double()).to(dtype)
+    x[2, 1] = (torch.randn(V, generator=g) * 2).to(dtype)
+    s = torch.tensor([[-1.0, -2.5], [-0.5, -40.0], [-30.0, -0.25]])
+    want = definition(x, s, K)
+    got = select(x.to(cuda_device), s.to(cuda_device), K, cuda_device)
+    check(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_low_and_high_parts_of_a_row(dtype, cuda_device):
+    """Rows whose parts lie far apart: only the highest has weight; NaN and infinities still take a
+    row out wherever they are."""
+    V, K = 70000, 24
+    x = torch.zeros(8, 1, V)
+    x[0, 0, :40000] = -1e12
+    x[1, 0, 40000:] = 1e12
+    x[2, 0, :40000], x[2, 0, 40000:] = -1e30, -1e31
+    x[3, 0, :40000], x[3, 0, 40000:] = 1e30, 1e31
+    x[4] = -1e20
+    x[4, 0, 69999] = float("nan")
+    x[5] = -1e20
+    x[5, 0, 7] = float("inf")
+    x[6] = 1e20
+    x[6, 0, 5] = float("nan")
+    x[7] = float("-inf")
+    x[7, 0, 69000:] = -1e25
+    x = x.to(dtype)
+    s = -torch.arange(1.0, 9.0)[:, None]
+    check(select(x.to(cuda_device), s.to(cuda_device), K, cuda_device), definition(x, s, K))
