@@ -11,7 +11,10 @@
 // ref a whole number: H x - ref is one rounding (an fma), changes of ref and joins are exact,
 // and ln sum e^x = ref / H + ln(sum) to within the 1.3e-8 (largest x - x) that H's rounding
 // leaves, where x has its weight.  So an element costs half of an fma, an exponential and
-// half of an add.  The threads' sums are joined in f64.
+// half of an add.  A chunk's terms are added as a tree, and the chunks' sums with what each addition
+// loses (Knuth's two-sum): one after another, 256 equal terms of a flat row of 131072 were off by
+// 2.4e-6 together.  The threads' sums are joined in f64.  (Where a row is cut, and where its first
+// 16-byte boundary lies, still decides which terms meet: equal rows may differ by some 2^-22.)
 // Past 2^22 a whole number near H x is no longer near the product (from 2^32 on the fma's result may
 // be in the hundreds).  So ref is -2^22 at least, where what is further down (a mask) has no
 // weight beside anything else; and a segment whose largest logit itself is beyond 2^22 on
@@ -31,9 +34,9 @@
 // are a sixty-fourth of their rate.
 //
 // Bound by the read of the logits in the end; now by the instructions and their latency: 64 x 8
-// rows of 131072 bf16 (134 MB, 20 us) take 38 us with K = 16, some 9 of them the join's and
-// what goes on around it, and 34.5 with K = 2; f32 (268 MB, 40 us) 54.5.  A stage more or less
-// and chunks of 2048 vectors are within 2 %; chunks of 512 took 46.  (The care for far segments took 0.9 of the 38.)
+// rows of 131072 bf16 (134 MB, 20 us) take 38.5 us with K = 16, some 9 of them the join's and
+// what goes on around it, and 35 with K = 2; f32 (268 MB, 40 us) 55.  A stage more or less
+// and chunks of 2048 vectors are within 2 %; chunks of 512 took 46.  (Far segments take 0.9 of the 38.5, sums that keep what they lose 0.5.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -309,8 +312,8 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
     if (tid == 0) sh.few_count[side] = sh.found_count = 0;  // (counted behind the next barrier)
     bool crowded = false;   // more found than there is room for
     float top = -INFINITY;  // this thread's largest logit
-    float ref = -INFINITY;  // its sum of 2^(H x - ref), in two parts
-    float2 sum = {0.0f, 0.0f};
+    float ref = -INFINITY;  // its sum of 2^(H x - ref), and what the sum's additions lost
+    float sum = 0.0f, lost = 0.0f;
     float use = 0.0f;          // -ref, or 0 while that is -inf
     float floor_ = -INFINITY;  // logits below it are not among the segment's K
     auto raise = [&](float y) {
@@ -320,13 +323,18 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
         if (up > ref) {
           if (ref != -INFINITY) {  // (a sum of NaN stays one)
             const float f = ex2(ref - up);
-            sum.x *= f;
-            sum.y *= f;
+            sum *= f;
+            lost *= f;
           }
           ref = up;
           use = -up;
         }
       }
+    };
+    auto add = [&](float x) {
+      const float s = sum + x, z = s - sum;
+      lost += (sum - (s - z)) + (x - z);
+      sum = s;
     };
     auto work = [&](int u, bool whole) {
       asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
@@ -343,6 +351,7 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
       copy(stage);
       stage = stage + 1 == kStages ? 0 : stage + 1;
       const float2 h2 = {kH, kH}, use2 = {use, use};
+      float2 of[kUnroll];
 #pragma unroll
       for (int e = 0; e < kUnroll; ++e) {
         float2 y[V::N / 2];
@@ -350,9 +359,16 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
 #pragma unroll
         for (int k = 0; k < V::N / 2; ++k) {
           const float2 t = __ffma2_rn(y[k], h2, use2);
-          sum = __fadd2_rn(sum, float2{ex2(t.x), ex2(t.y)});
+          y[k] = float2{ex2(t.x), ex2(t.y)};
         }
+#pragma unroll
+        for (int n = V::N / 4; n > 0; n /= 2)
+#pragma unroll
+          for (int k = 0; k < n; ++k) y[k] = __fadd2_rn(y[k], y[k + n]);
+        of[e] = y[0];
       }
+      const float2 all = __fadd2_rn(__fadd2_rn(of[0], of[1]), __fadd2_rn(of[2], of[3]));
+      add(all.x + all.y);
     };
     // A logit that reaches the floor, to be ranked.
     auto put = [&](float y, int v) {
@@ -379,10 +395,10 @@ beam_rows_kernel(const __grid_constant__ BeamLaunch p, const __grid_constant__ S
       if (end) {
         if (ragged) {
           raise(ragged_y);
-          sum.x += ex2(fmaf(ragged_y, kH, use));
+          add(ex2(fmaf(ragged_y, kH, use)));
         }
         sh.refs[tid] = ref;
-        sh.parts[tid] = sum.x + sum.y;
+        sh.parts[tid] = sum + lost;
       }
       const float mine = warp < warps ? nth_top(top, share) : INFINITY;
       if (lane == 0) sh.floors[warp] = mine;

@@ -877,8 +877,11 @@ size_t gdn_attn8_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t
  * beam without a life, and a row that holds a NaN or +inf, or nothing but -inf, offers
  * nothing.  Finite logits may be of any size; a finite mask makes a candidate, which takes a place
  * that allowed tokens leave.  Places left over get parent -1, token -1, s = -inf.
- * Exponentials and a thread's sums are f32, sums between threads, the logarithm and s
- * are f64; s is rounded to f32 where it is stored.  (Logits so small that s does not
+ * Exponentials and a thread's sums are f32 (kept so that what they lose does not grow with V), sums
+ * between threads, the logarithm and s are f64; s is rounded to f32 where it is stored.  The
+ * log-sum is within 2^-19, and its last bits hang on where a row lies and how it is divided: beams of
+ * equal logits and scores tie when their rows are divided alike, and may else come in either order.
+ * (Logits so small that s does not
  * show their difference in f64 are ordered by the logit, not the index.)
  * out_scores may be scores itself where K = W; otherwise outputs overlap nothing.
  * K <= 128, W <= 64, B <= 65535, W * V < 2^31.  The workspace is 256-byte aligned, of any contents. */

@@ -1,9 +1,12 @@
 """GPU: gdn_beam_select over logits of any finite size: masks of large finite values, rows that hold
-nothing else, logits far from zero.  Against the definition in 64 bits, as in test_gpu_beam.py."""
+nothing else, logits far from zero; and sums of many equal terms.  Against the definition in 64
+bits, as in test_gpu_beam.py."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_beam import BF, F32, check, definition, select
+from gated_delta_rule_44_gb300 import binding as B
+from test_gpu_beam import BF, F32, LSE, check, definition, select
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +94,25 @@ def test_low_and_high_parts_of_a_row(dtype, cuda_device):
     x = x.to(dtype)
     s = -torch.arange(1.0, 9.0)[:, None]
     check(select(x.to(cuda_device), s.to(cuda_device), K, cuda_device), definition(x, s, K))
+
+
+@pytest.mark.parametrize("n,W,V,dtype", [(152, 2, 131072, F32), (152, 2, 262144, F32), (160, 2, 131071, BF), (320, 1, 262147, BF),
+                                         (2, 2, 1 << 20, F32)])
+def test_sums_of_many_equal_terms(n, W, V, dtype, cuda_device):
+    """Flat rows: every term of a thread's sum is the same, and what an addition loses is lost at
+    each.  The score is score - ln V."""
+    dev = cuda_device
+    x = torch.empty(n, W, V, dtype=dtype, device=dev)
+    s = torch.zeros(n, W, device=dev)
+    for flat in (0.3, -1.1, 5.6, -17.3):
+        x.fill_(flat)
+        got = select(x, s, 1, dev)
+        err = (got[2].double() + np.log(V)).abs().max().item()
+        print(f"{flat}: log-sum off by {err:.2e}")
+        assert err <= LSE + 2.0 ** -24 * np.log(V)
+    g = torch.Generator(device=dev).manual_seed(V)
+    x.copy_(torch.randn(1, 1, V, generator=g, device=dev).to(dtype).expand(n, W, V))
+    got = select(x, s, 1, dev)
+    y = x[0, 0].double()
+    want = (y.max() - torch.logsumexp(y, 0)).item()
+    assert (got[2].double() - want).abs().max().item() <= LSE + 2.0 ** -24 * abs(want)
