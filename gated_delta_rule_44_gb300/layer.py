@@ -29,6 +29,16 @@ import torch
 from . import binding as B
 
 
+def _capturing(stream: Optional[torch.cuda.Stream]) -> bool:
+    """Whether work on this stream (None: the current one) goes into a graph."""
+    if not torch.cuda.is_initialized():
+        return False
+    if stream is None or stream == torch.cuda.current_stream(stream.device):
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class GdnStep:
     """Preallocated intermediates (q, k, v, g, beta, out, prefill workspace) for
     batches of a fixed token count, and the three calls of one step."""
@@ -150,6 +160,7 @@ class AttnStep:
         self.workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
         self.dt = dt
         self.widths = {}  # table width and page size: workspace bytes of the calls on a cache in 8 bits
+        self.captured = False  # whether a graph uses the present workspace
         self.outgrown = []  # smaller workspaces, which graphs captured earlier go on using
 
     def run(self, q, k, v, cu_seqlens, kv_lens, block_table, k_cache, v_cache, *,
@@ -163,7 +174,8 @@ class AttnStep:
         this object's own buffer), which it returns.  cu_seqlens_prefill: the
         offsets of the sequences after the decode rows, rebased to 0.  With
         k_scale and v_scale the cache is one in 8 bits (its workspace grows with
-        the first step over a wider table)."""
+        the first step over a wider table; only one that a graph was captured
+        with is kept beside it)."""
         nd = self.n_decode
         out = self.out if out is None else out
         if (k_scale is None) != (v_scale is None):
@@ -171,6 +183,7 @@ class AttnStep:
         eight = k_scale is not None
         if eight:
             self._grow8(block_table.shape[1], k_cache.shape[2], stream)
+        self.captured = self.captured or _capturing(stream)
         scales = (k_scale, v_scale) if eight else ()
         prepare, paged = ((B.gdn_attn8_prepare, B.gdn_attn8_paged) if eight
                           else (B.gdn_attn_prepare, B.gdn_attn_paged))
@@ -195,7 +208,9 @@ class AttnStep:
         return out
 
     def _grow8(self, width: int, page: int, stream) -> None:
-        """Room for the calls on a cache in 8 bits with tables of this width."""
+        """Room for the calls on a cache in 8 bits with tables of this width.  A workspace that a
+        graph was captured with is kept beside the new one, which is then twice as large at
+        least, so that what is kept is never more than what is in use."""
         if (width, page) in self.widths:
             return
         nd, Tp, Np = self.n_decode, self.T - self.n_decode, self.N - self.n_decode
@@ -207,8 +222,15 @@ class AttnStep:
             need = max(need, B.gdn_attn8_paged_workspace_bytes(Tp, Np, self.Hq, self.Hkv, self.D,
                                                                self.max_q_len, self.dt, width, page))
         if need > self.workspace.numel():
-            self.outgrown.append(self.workspace)
-            self.workspace = B._scratch(need, self.workspace.device, stream)
+            old, capturing = self.workspace, _capturing(stream)
+            if self.captured:
+                need = max(need, 2 * old.numel())
+            self.workspace = B._scratch(need, old.device, stream)
+            if self.captured or capturing:
+                self.outgrown.append(old)
+            elif old.is_cuda:  # an earlier step may have work pending on it on this stream
+                old.record_stream(stream or torch.cuda.current_stream(old.device))
+            self.captured = False
         self.widths[(width, page)] = need
 
 
