@@ -1216,6 +1216,23 @@ int check_attn_scales(const gdn_attn_cache8& c, const AttnCacheView& v, int64_t 
   return GDN_OK;
 }
 
+// Into a cache in 8 bits a block's rows of k and v are read, in part twice, while other blocks of
+// threads write q_out and k_out.
+int check_attn8_overlap(const gdn_attn_prepare_args& a, const gdn::AttnPrepareLaunch& p) {
+  const uintptr_t es = (uintptr_t)elem_size(a.act_dtype);
+  for (auto in : {std::make_pair(&p.k, "key"), std::make_pair(&p.v, "value")}) {
+    const uintptr_t i0 = reinterpret_cast<uintptr_t>(in.first->p);
+    const uintptr_t i1 = i0 + (uintptr_t)((a.T - 1) * in.first->ts + (a.Hkv - 1) * in.first->hs + a.D) * es;
+    for (auto out : {std::make_pair(a.q_out, a.Hq), std::make_pair(a.k_out, a.Hkv)}) {
+      const uintptr_t o0 = reinterpret_cast<uintptr_t>(out.first);
+      if (o0 != 0 && o0 < i1 && i0 < o0 + (uintptr_t)(a.T * out.second * a.D) * es)
+        return fail(GDN_ERR_INVALID_ARGUMENT,
+                    std::string("gdn_attn8_prepare q_out and k_out must not overlap the ") + in.second + " rows");
+    }
+  }
+  return GDN_OK;
+}
+
 // The checks of the prepare calls; fills p.  The cache is c8's where that is not NULL.
 int attn_prepare_checks(const gdn_attn_prepare_args* a, const gdn_attn_cache8* c8, cudaStream_t st,
                         gdn::AttnPrepareLaunch& p) {
@@ -1265,6 +1282,8 @@ int attn_prepare_checks(const gdn_attn_prepare_args* a, const gdn_attn_cache8* c
                                a->cu_seqlens_host, a->kv_lens, a->kv_lens_host, cache,
                                cv.table_stride, st))
     return rc;
+  if (c8 != nullptr)
+    if (int rc = check_attn8_overlap(*a, p)) return rc;
   p.T = (int)a->T;
   p.N = (int)a->N;
   p.Hq = (int)a->Hq;

@@ -817,7 +817,7 @@ typedef struct gdn_attn_cache8 {
 } gdn_attn_cache8;
 
 /* gdn_attn8_prepare -- gdn_attn_prepare into a cache in 8 bits.  q_out and k_out are as
- * there.  For each block that receives rows, kv head, and k or v:
+ * there, and overlap nothing between the first and the last value of k and v (refused).  For each block that receives rows, kv head, and k or v:
  *   need = the smallest 2^e, e >= -64, with max |x| <= 448 2^e over the block's finite new
  *          values (of k after norm and rotary, in f32)
  *   S = need, when no earlier row of the sequence is in the block; else the larger of need
