@@ -49,8 +49,8 @@
 // query heads, take 474 and 730 (bound by the chain of the softmax and, at 64, the MMAs).  Against two
 // parts of p, four cost 0.5 to 2 % with up to 16 rows, 5 and 12 % with 32 and 64.
 //
-// A row whose result is not finite, or whose l is too small to be trusted (blocks whose
-// scales differ by 2^90), is evaluated again key by key (exact_row).  Every wait is bounded.
+// A row whose result is not finite, or whose l is too small to be trusted (value scales of 2^60 and
+// more), is evaluated again key by key (exact_row).  Every wait is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -75,7 +75,10 @@ constexpr float kHeadroom = 4.0f;       // log2: p reaches 2^4 before the refere
 constexpr float kPScale = 16.0f;        // p 2^4 in the parts' units: at most 256 of 448
 constexpr float kLoScale = 32.0f;       // of q's second part
 constexpr float kLowScale = 32768.0f;   // 2^15: of p's third and fourth
-constexpr float kLeastSum = 8.0e-28f;   // 2^-90
+// A sum l below 2^-60 is not trusted.  m goes down to log2 of the least value scale, 2^-64, below a
+// row's scores and, where l may be that small, 60 above them: parts of a row are joined at 2^-124 at
+// the least, short of where f32 loses bits.
+constexpr float kLeastSum = 8.6e-19f;
 
 struct Shared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];

@@ -838,12 +838,13 @@ typedef struct gdn_attn8_prepare_args {
 int gdn_attn8_prepare(const gdn_attn8_prepare_args* args, void* stream);
 
 /* gdn_attn8_paged -- gdn_attn_paged over a cache in 8 bits, of any finite scales (a key or
- * value of another one is what code times scale gives).  Statistics and sums are f32.
+ * value of another one is what code times scale gives; where the codes are used as they are, rows
+ * that see value scales of 2^60 and more are evaluated key by key, and slowly).  Statistics and sums are f32.
  * Roundings beside the last one, by rows per kv head (max_q_len * Hq / Hkv), in bf16:
  *   up to 256, D >= 64: the codes are used as they are; q in two e4m3 parts, exact down to
  *   2^-10 of its row's largest value, and the softmax weights to 2^-8 of each, down to 2^-21
- *   of the row's largest (a weight counts here with the scale of its value's block), below
- *   that to 2^-29 of the largest.
+ *   of the row's largest (a weight counts here with the scale of its value's block, 2^-64 at
+ *   the least), below that to 2^-29 of the largest.
  *   more: the values are widened to bf16 (exact for scales that are powers of two from
  *   2^-110 on) and then used as in gdn_attn_paged.
  * f32, and bf16 with D = 32 and few rows, round nothing but the result.  The widened form (of
