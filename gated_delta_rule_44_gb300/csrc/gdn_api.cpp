@@ -1607,6 +1607,10 @@ int beam_select(const gdn_beam_select_args* a, void* stream) {
     return fail(GDN_ERR_INVALID_ARGUMENT, "logits must be aligned to their type");
   if (a->finished != nullptr && (a->pad_token < 0 || a->pad_token >= V))
     return fail(GDN_ERR_INVALID_ARGUMENT, "beam_select pad_token " + S(a->pad_token) + " is outside the vocabulary");
+  // A group's scores are read and replaced by its own block of threads alone.
+  const float *out0 = a->out_scores, *in0 = a->scores;
+  if (out0 < in0 + B * W && in0 < out0 + B * K && (out0 != in0 || K != W))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "beam_select out_scores may be scores only where K = W");
   const size_t need = gdn::beam_workspace_bytes(B, W, V, K);
   if (a->workspace == nullptr || a->workspace_bytes < need)
     return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_beam_select workspace needs " + S((int64_t)need) +

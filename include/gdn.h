@@ -884,7 +884,8 @@ size_t gdn_attn8_paged_workspace_bytes(int64_t T, int64_t N, int64_t Hq, int64_t
  * equal logits and scores tie when their rows are divided alike, and may else come in either order.
  * (Logits so small that s does not
  * show their difference in f64 are ordered by the logit, not the index.)
- * out_scores may be scores itself where K = W; otherwise outputs overlap nothing.
+ * out_scores may be scores itself where K = W (other overlaps of the two are refused); otherwise
+ * outputs overlap nothing.
  * K <= 128, W <= 64, B <= 65535, W * V < 2^31.  The workspace is 256-byte aligned, of any contents. */
 typedef struct gdn_beam_select_args {
   int64_t B, W, V, K;
