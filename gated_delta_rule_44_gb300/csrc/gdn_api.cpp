@@ -1099,6 +1099,9 @@ int check_attn_pages(const char* label, void* p, int64_t len, int64_t ps, int64_
   return GDN_OK;
 }
 
+// The kernels look some keys ahead of a context's end in 32 bits.
+constexpr int64_t kMostPositions = (int64_t)INT32_MAX + 1 - 65536;
+
 // es: bytes of a cache element.
 int check_attn_cache(const gdn_attn_cache* c, int64_t N, int64_t Hkv, int64_t D, int64_t es,
                      AttnCacheView* out) {
@@ -1106,7 +1109,7 @@ int check_attn_cache(const gdn_attn_cache* c, int64_t N, int64_t Hkv, int64_t D,
     return fail(GDN_ERR_SHAPE, "attention cache shape must be positive, got num_pages=" +
                                    S(c->num_pages) + " page_size=" + S(c->page_size) +
                                    " max_pages=" + S(c->max_pages));
-  if (c->num_pages > INT32_MAX || c->page_size > (1 << 20) || c->max_pages > INT32_MAX / c->page_size)
+  if (c->num_pages > INT32_MAX || c->page_size > (1 << 20) || c->max_pages > kMostPositions / c->page_size)
     return fail(GDN_ERR_UNSUPPORTED, "attention cache positions exceed 32 bits");
   out->table_stride = c->table_stride != 0 ? c->table_stride : c->max_pages;
   if (out->table_stride < c->max_pages || out->table_stride > INT64_MAX / 8 / N)
@@ -1479,7 +1482,7 @@ size_t paged8_need(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int
 }
 
 bool attn8_cache_dims(int64_t max_pages, int64_t page_size) {
-  return max_pages > 0 && page_size > 0 && page_size <= (1 << 20) && max_pages <= INT32_MAX / page_size;
+  return max_pages > 0 && page_size > 0 && page_size <= (1 << 20) && max_pages <= kMostPositions / page_size;
 }
 
 size_t attn8_paged_workspace(int64_t T, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q_len,

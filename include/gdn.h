@@ -702,7 +702,8 @@ typedef struct gdn_attn_cache {
   int64_t v_len, v_page_stride, v_head_stride, v_token_stride;
   int64_t num_pages, page_size;
   const int32_t* block_table;      /* [N, max_pages] */
-  int64_t max_pages, table_stride; /* table_stride 0 = max_pages */
+  int64_t max_pages, table_stride; /* max_pages * page_size <= 2^31 - 2^16;
+                                      table_stride 0 = max_pages */
   const int32_t* block_table_host; /* optional host copy (needs kv_lens_host): the pages
                                       of live positions are checked */
 } gdn_attn_cache;
