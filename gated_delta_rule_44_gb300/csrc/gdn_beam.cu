@@ -24,8 +24,9 @@
 // K, and the least of these is a value that at least K logits reach; the some 3 K chunks of
 // a thread that reach it are read again, and their logits that do are ranked by counting.
 // (Putting vectors aside on the way took 13 us of 42 for K = 16: each time the warp waits.)
-// A segment in which more reach it than there is room for (rows of equal logits) is read again,
-// once for each of the K places.
+// A segment in which more reach it than there is room for (rows of equal logits; a finite mask over
+// all but fewer than K tokens, the mask then being the floor) is read again, once for each of the K
+// places: 64 x 8 rows of 131072 with 20 tokens above a mask of -1e9 take 1050 us, with 1000 of them 66.
 //
 // Join kernel.  A CTA per group joins the segments' sums into f64 log-sums, turns list
 // entries into 64-bit scores (beams are compared at 2^-53: two f32 roundings of a score of

@@ -8,7 +8,8 @@
 // shared memory with bulk copies, waits for all of them, and only then sends them to their
 // destinations.  As every CTA handles the same bytes of all the slots of its groups, a
 // group is reordered in place whatever its cycles, without a second pool.  A source of
-// several places is read once; a slot that stays where it is is not touched.
+// several places is read once for every 32 pairs of an item (a warp's) that it is in; a slot that
+// stays where it is is not touched.
 //
 // Bound by HBM: each moved byte is read and written once.  The copies need no registers and
 // one thread per slot, so the number of bytes in flight is the shared memory's: 40 KB for
