@@ -16,8 +16,8 @@
 // The workspace holds the contexts of some sequences at a time, up to 1 GiB or one
 // sequence, whichever is more; each group of them is one pass of the two kernels.  The host knows
 // the table's width, not the lengths, so a wide table makes small groups: 64 chunks of 100 tokens
-// over 1000, 64 + 8 heads of 128, take 310 us with a table for 1024 positions, 440 with 8192 (four
-// groups more) and 3100 with 131072 (64 groups of one).
+// over 1000, 64 + 8 heads of 128, take 310 us with a table for 1024 positions, 440 with 8192 (two
+// groups) and 3100 with 131072 (64 groups of one).
 //
 // f32 comes here with more rows than the row kernel holds (gdn_attn_simt.cu), single tokens of wide
 // groups among them: 8 tokens over 4096 keys each, 2 kv heads of 128, take 200 us with 16 query
