@@ -37,15 +37,16 @@
 // scores (whose barrier says also that the scales are there, and, the MMAs being one warp's in
 // order, that P's buffer is free again), for the maxima, and for the P V of the tile before
 // where O is scaled.  More groups that took the tiles in turns were no faster (spills).
-// Two S and two P buffers (one P for 64 rows of D = 256, where K and V leave room for no more): the
-// scores of a tile are computed during the softmax of the one before.  Two CTAs share an SM where their memory allows it, and hide each other's chains.
+// Two S and two P buffers (one P for 64 rows of D = 256, where K and V leave room for no
+// more): the scores of a tile are computed during the softmax of the one before.  Two CTAs
+// share an SM where their memory allows it, and hide each other's chains.
 // The work is that of the stream form (gdn_attn_stream.cuh).
 //
 // Bound by HBM where many sequences keep every SM's rings full: 256 single tokens over 1 to
 // 16384 keys, 32 + 4 heads of 128, take 339 to 342 us (2.2 GB at 6.6 TB/s, 98 % of the copy rate); 128
 // sequences with 1 to 4 drafts over up to 8192 keys, 32 + 8 heads, 16-row pages, 198 to 200 (1.06 GB
-// at 5.3 TB/s: TMA loads of 2 KB, and the ranges' ends); one token over 200003 keys 48 (205 MB, 33 to 41 of it the main
-// kernel, then the join of 76 ranges).  32 and 64 rows of the 256 single tokens' contexts, 128 and 256
+// at 5.3 TB/s: TMA loads of 2 KB, and the ranges' ends); one token over 200003 keys 48 (205 MB,
+// 33 to 41 of it the main kernel, then the join of 76 ranges).  32 and 64 rows of the 256 single tokens' contexts, 128 and 256
 // query heads, take 474 and 730 (bound by the chain of the softmax and, at 64, the MMAs).  Against two
 // parts of p, four cost 0.5 to 2 % with up to 16 rows, 5 and 12 % with 32 and 64.
 //

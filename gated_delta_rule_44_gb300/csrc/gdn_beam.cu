@@ -37,7 +37,8 @@
 // Bound by the read of the logits in the end; now by the instructions and their latency: 64 x 8
 // rows of 131072 bf16 (134 MB, 20 us) take 38.5 us with K = 16, some 9 of them the join's and
 // what goes on around it, and 35 with K = 2; f32 (268 MB, 40 us) 55.  A stage more or less
-// and chunks of 2048 vectors are within 2 %; chunks of 512 took 46.  (Far segments take 0.9 of the 38.5, sums that keep what they lose 0.5.)
+// and chunks of 2048 vectors are within 2 %; chunks of 512 took 46.  (The care for far segments takes
+// 0.9 of the 38.5, sums that keep what they lose 0.5.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
