@@ -46,9 +46,10 @@
 // 16384 keys, 32 + 4 heads of 128, take 339 to 342 us (2.2 GB at 6.6 TB/s, 98 % of the copy rate); 128
 // sequences with 1 to 4 drafts over up to 8192 keys, 32 + 8 heads, 16-row pages, 198 to 200 (1.06 GB
 // at 5.3 TB/s: TMA loads of 2 KB, and the ranges' ends); one token over 200003 keys 48 (205 MB,
-// 33 to 41 of it the main kernel, then the join of 76 ranges).  32 and 64 rows of the 256 single tokens' contexts, 128 and 256
-// query heads, take 474 and 730 (bound by the chain of the softmax and, at 64, the MMAs).  Against two
-// parts of p, four cost 0.5 to 2 % with up to 16 rows, 5 and 12 % with 32 and 64.
+// 33 to 41 of it the main kernel, then the join of 76 ranges).  With 32 and 64 rows for each of the
+// 256 single tokens, 128 and 256 query heads, the first call takes 474 and 730 (bound by the chain of
+// the softmax and, at 64, the MMAs).  Against two parts of p, four cost 0.5 to 2 % with up to 16 rows,
+// 5 and 12 % with 32 and 64.
 //
 // A row whose result is not finite, or whose l is too small to be trusted (value scales of 2^60 and
 // more), is evaluated again key by key (exact_row).  Every wait is bounded.

@@ -116,3 +116,19 @@ def test_sums_of_many_equal_terms(n, W, V, dtype, cuda_device):
     y = x[0, 0].double()
     want = (y.max() - torch.logsumexp(y, 0)).item()
     assert (got[2].double() - want).abs().max().item() <= LSE + 2.0 ** -24 * abs(want)
+
+
+@pytest.mark.parametrize("n,W,V,dtype", [(1, 4, 40001, F32), (100, 4, 40003, BF), (3, 5, 131071, BF), (1, 64, 5001, F32)])
+def test_equal_beams_at_different_places(n, W, V, dtype, cuda_device):
+    """Equal rows that begin at different elements and are divided differently: each token comes
+    from every beam before the next best one, the beams' scores within the log-sums' 2^-19."""
+    dev = cuda_device
+    g = torch.Generator(device=dev).manual_seed(V)
+    row = torch.randn(V, generator=g, device=dev).to(dtype)
+    row[torch.tensor([7, V // 2], device=dev)] = torch.tensor([9.0, 8.0], device=dev).to(dtype)
+    x = row.expand(n, W, V).contiguous()
+    par, tok, best = select(x, torch.full((n, W), -2.0, device=dev), 2 * W, dev)
+    assert (par.view(n, 2, W).sort(-1).values == torch.arange(W, device=dev)).all()
+    assert torch.equal(tok, torch.tensor([7] * W + [V // 2] * W, dtype=torch.int32, device=dev).expand(n, -1))
+    want = -2.0 - torch.logsumexp(row.double(), 0) + torch.tensor([9.0, 8.0], dtype=torch.float64, device=dev)
+    assert ((best.view(n, 2, W).double() - want[:, None]).abs() <= 2 * LSE + 2.0 ** -24 * 20).all()
